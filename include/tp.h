@@ -261,6 +261,103 @@ TP_API tp_status tp_attn_core_dropout_bwd(tp_dtype dt, int64_t T, int64_t s, int
                                           void* workspace, size_t ws_bytes, void* stream);
 
 /* ------------------------------------------------------------------------ */
+/* Attention without stored probabilities, and a relative position bias      */
+/* ------------------------------------------------------------------------ */
+
+/* Sizes of the attention (host struct). */
+typedef struct {
+  int64_t T;          /* token rows of every buffer */
+  int64_t b;          /* sequences */
+  int64_t s;          /* tokens of every sequence without seq_starts (then T = b s); unused with them */
+  int32_t n_heads;    /* query heads */
+  int32_t n_kv_heads; /* key/value heads; query head j uses key/value head j / (n_heads / n_kv_heads) */
+  int32_t d;          /* head width, a multiple of 8, 8 <= d <= 128 */
+  int32_t N;          /* shards; n_heads, n_kv_heads multiples of N, n_heads of n_kv_heads */
+  int32_t causal;     /* a query sees the keys of its sequence up to its own position, else all of them */
+  float scale;        /* of the scores, finite and > 0; 0 = 1 / sqrt(d) */
+} tp_attn_config;
+
+/* Relative position bias by buckets (host struct).  With n the distance:
+ *   bidirectional = 0: n = max(query - key, 0), B = num_buckets buckets;
+ *   bidirectional = 1: n = |query - key|, B = num_buckets / 2 buckets, those of
+ *     keys ahead of the query (key > query) numbered from B on;
+ *   E = B / 2 (rounded down): distances n < E have bucket n; others
+ *   min(B - 1, E + floor((B - E) ln(n / E) / ln(max_distance / E))), the floor
+ *   taken of the exact value.
+ * E < max_distance <= 1024, B >= 2, num_buckets <= 256 (even if bidirectional). */
+typedef struct {
+  int32_t num_buckets;
+  int32_t max_distance;
+  int32_t bidirectional;
+} tp_relbias_config;
+
+/*
+ * tp_attn_recompute_fwd / _bwd -- softmax attention as tp_attn_core_fwd / _bwd
+ * ([TP notes] §Self-Attention层; [Walkthrough] §ParallelSelfAttention) that
+ * stores no (s x s) matrix: the forward leaves C and one log-sum-exp a row, and
+ * the backward computes the probabilities from them again.  Sequences may have
+ * unequal lengths, and query heads may share key/value heads.
+ *   x_ij = scale q_i . k_j,  lse_i = log sum_j exp(x_ij),
+ *   C_i = sum_j exp(x_ij - lse_i) v_j
+ *   P = exp(x - lse),  D_i = dC_i . C_i,  dS_ij = P_ij (dC_i . v_j - D_i),
+ *   dq_i = scale sum_j dS_ij k_j,  dk_j = scale sum_i dS_ij q_i,
+ *   dv_j = sum_i P_ij dC_i   (dk, dv: over the query heads that share the head)
+ * Arguments (bf16 only, TP_ERR_UNSUPPORTED for TP_F32):
+ *   seq_starts  device int64[b + 1]: sequence i is the rows seq_starts[i] ..
+ *               seq_starts[i + 1] - 1 (none, if they are equal); rows outside
+ *               every sequence are neither used nor written.  Or NULL: b
+ *               sequences of s rows each.
+ *   QKV         (T, (n_heads + 2 n_kv_heads) d) with row pitch ld_qkv, shard-major:
+ *               shard i holds [Q_i K_i V_i], its heads in order inside each.
+ *   C, dC       (T, n_heads d), head j in columns [j d, (j + 1) d), pitches ld_c, ld_dc
+ *   lse         (n_heads, T) fp32
+ *   dQKV        out, as QKV, pitch ld_dqkv; every column of a sequence's rows is written
+ *   workspace   tp_attn_recompute_workspace_size bytes, 256-byte aligned (backward)
+ * Scores, softmax and D are fp32; the probabilities and dS are rounded to bf16
+ * as operands of their products.  No (s x s) matrix is stored.  Sums have a
+ * fixed order: equal calls give equal bits.
+ * Rows of one sequence never depend on another sequence's values, whatever
+ * they are.  Inside a sequence a non-finite value may reach every row.
+ * Errors: TP_ERR_INVALID for sizes outside the ranges above, pitches narrower
+ * than a row, null pointers, T > 2^31 - 1; TP_ERR_ALIGN for a d or pitch that is
+ * no multiple of 8 or a QKV, C, dC, dQKV that is not 16-byte aligned (lse, table: 4-byte);
+ * all before anything is launched.  Sequence starts are on the device: if they
+ * decrease or leave [0, T], no access leaves the buffers, the results are
+ * unspecified and tp_get_status returns TP_ERR_INVALID.
+ */
+TP_API tp_status tp_attn_recompute_fwd(tp_dtype dt, const tp_attn_config* cfg, const int64_t* seq_starts,
+                                       const void* QKV, int64_t ld_qkv, void* C, int64_t ld_c, float* lse,
+                                       void* stream);
+TP_API tp_status tp_attn_recompute_bwd(tp_dtype dt, const tp_attn_config* cfg, const int64_t* seq_starts,
+                                       const void* QKV, int64_t ld_qkv, const void* C, int64_t ld_c,
+                                       const float* lse, const void* dC, int64_t ld_dc, void* dQKV,
+                                       int64_t ld_dqkv, void* workspace, size_t ws_bytes, void* stream);
+
+/*
+ * tp_attn_relbias_fwd / _bwd -- the same with a learned bias of the relative
+ * position: x_ij = scale q_i . k_j + table[bucket(j - i), head].
+ *   table   (num_buckets, n_heads) fp32, buckets as in tp_relbias_config
+ *   dtable  out, fp32, same shape: dtable[u, head] = sum of dS_ij over every pair
+ *           of bucket u in every sequence (fp32 dS, before its rounding; accumulate:
+ *           added to the old value), or NULL: not computed
+ * The bias is added inside the kernels and its gradient summed there, in a
+ * fixed order.
+ */
+TP_API tp_status tp_attn_relbias_fwd(tp_dtype dt, const tp_attn_config* cfg, const tp_relbias_config* bias,
+                                     const float* table, const int64_t* seq_starts, const void* QKV,
+                                     int64_t ld_qkv, void* C, int64_t ld_c, float* lse, void* stream);
+TP_API tp_status tp_attn_relbias_bwd(tp_dtype dt, const tp_attn_config* cfg, const tp_relbias_config* bias,
+                                     const float* table, const int64_t* seq_starts, const void* QKV,
+                                     int64_t ld_qkv, const void* C, int64_t ld_c, const float* lse,
+                                     const void* dC, int64_t ld_dc, void* dQKV, int64_t ld_dqkv,
+                                     float* dtable, int accumulate, void* workspace, size_t ws_bytes,
+                                     void* stream);
+
+/* Workspace bytes of the backward calls (bias: NULL for tp_attn_recompute_bwd,
+ * or if dtable is NULL); 0 for invalid sizes or T = 0. */
+TP_API size_t tp_attn_recompute_workspace_size(const tp_attn_config* cfg, const tp_relbias_config* bias);
+
+/* ------------------------------------------------------------------------ */
 /* One tensor-parallel transformer layer                                     */
 /* ------------------------------------------------------------------------ */
 
@@ -609,8 +706,9 @@ TP_API size_t tp_adam_step_workspace_size(void);
 /* ------------------------------------------------------------------------ */
 
 /* Synchronises `stream`, then reads and clears the device error word of the
- * current device: TP_OK, TP_ERR_TIMEOUT (a bounded wait expired), or
- * TP_ERR_CUDA (a CUDA error, sticky or not). */
+ * current device: TP_OK, TP_ERR_TIMEOUT (a bounded wait expired),
+ * TP_ERR_INVALID (sequence starts on the device that decrease or leave the
+ * buffers), or TP_ERR_CUDA (a CUDA error, sticky or not). */
 TP_API tp_status tp_get_status(void* stream);
 
 /* Human-readable name of a status code (static string). */
@@ -640,7 +738,7 @@ TP_API tp_status tp_gelu_eval(const float* z, float* y, float* dy, int64_t n, vo
 
 /* Fault injection for testing the bounded waits (host-controlled; never
  * faults the GPU).  kind 1: the TMA producer of the next tensor-core GEMM
- * launch skips its first stage, so the consumer's bounded wait expires and
+ * or attention launch skips its first stage, so the consumer's bounded wait expires and
  * the kernel returns early with TP_ERR_TIMEOUT recorded.  kind 0: off.
  * wait_limit_ms sets the bounded-wait limit (default 1000 ms). */
 TP_API void tp_debug_inject_fault(int kind);

@@ -31,7 +31,8 @@ __all__ = [
     "read_optimizer_state", "tp_attn_core_fwd", "tp_attn_core_bwd", "tp_attn_core_workspace_size",
     "tp_attn_core_dropout_fwd", "tp_attn_core_dropout_bwd", "tp_position_embed_dropout",
     "tp_transformer_layer_workspace_size", "tp_transformer_layer_fwd", "tp_transformer_layer_bwd",
-    "tp_layer_config", "layer_stream",
+    "tp_layer_config", "layer_stream", "tp_attn_config", "tp_relbias_config", "tp_attn_recompute_fwd",
+    "tp_attn_recompute_bwd", "tp_attn_relbias_fwd", "tp_attn_relbias_bwd", "tp_attn_recompute_workspace_size",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libtp.so")
@@ -89,6 +90,20 @@ class tp_layer_grads(ctypes.Structure):
                                                 "db2", "dW", "da", "dU", "db")]
 
 
+class tp_attn_config(ctypes.Structure):
+    """Sizes of the attention without stored probabilities (layout of the C struct)."""
+    _fields_ = [("T", ctypes.c_int64), ("b", ctypes.c_int64), ("s", ctypes.c_int64),
+                ("n_heads", ctypes.c_int32), ("n_kv_heads", ctypes.c_int32), ("d", ctypes.c_int32),
+                ("N", ctypes.c_int32), ("causal", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+
+class tp_relbias_config(ctypes.Structure):
+    _fields_ = [("num_buckets", ctypes.c_int32), ("max_distance", ctypes.c_int32),
+                ("bidirectional", ctypes.c_int32)]
+
+
+_PCFG, _PBIAS = ctypes.POINTER(tp_attn_config), ctypes.POINTER(tp_relbias_config)
+
 _SIGNATURES = {
     "tp_mlp_fwd": (_int, [_int, _i64, _i64, _i64, _int, _c_void_p, _PP, _PP, _PP, _c_void_p,
                           _c_void_p, _c_void_p, _c_void_p, _c_void_p]),
@@ -144,6 +159,16 @@ _SIGNATURES = {
                                         ctypes.c_uint64, ctypes.c_uint64, _c_void_p, _c_void_p,
                                         _c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_void_p, _size_t,
                                         _c_void_p]),
+    "tp_attn_recompute_fwd": (_int, [_int, _PCFG, _c_void_p, _c_void_p, _i64, _c_void_p, _i64, _c_void_p,
+                                     _c_void_p]),
+    "tp_attn_recompute_bwd": (_int, [_int, _PCFG, _c_void_p, _c_void_p, _i64, _c_void_p, _i64, _c_void_p,
+                                     _c_void_p, _i64, _c_void_p, _i64, _c_void_p, _size_t, _c_void_p]),
+    "tp_attn_relbias_fwd": (_int, [_int, _PCFG, _PBIAS, _c_void_p, _c_void_p, _c_void_p, _i64, _c_void_p, _i64,
+                                   _c_void_p, _c_void_p]),
+    "tp_attn_relbias_bwd": (_int, [_int, _PCFG, _PBIAS, _c_void_p, _c_void_p, _c_void_p, _i64, _c_void_p, _i64,
+                                   _c_void_p, _c_void_p, _i64, _c_void_p, _i64, _c_void_p, _int, _c_void_p,
+                                   _size_t, _c_void_p]),
+    "tp_attn_recompute_workspace_size": (_size_t, [_PCFG, _PBIAS]),
     "tp_position_embed_dropout": (_int, [_i64, _i64, _i64, _c_void_p, _c_void_p, _c_void_p,
                                          ctypes.c_float, ctypes.c_uint64, ctypes.c_uint64, _c_void_p,
                                          _c_void_p]),
@@ -480,6 +505,116 @@ def tp_attn_core_dropout_bwd(QKV, P, Pd, C, dC, s, n_heads, N, causal, p_attn, s
                                           _dev(dQKV, "dQKV"), _dev(workspace, "workspace"),
                                           _ws_bytes(workspace), _stream(stream)),
            "tp_attn_core_dropout_bwd")
+
+
+# ----------------------------------------------------------------------------
+# Attention without stored probabilities, and the relative position bias
+# ----------------------------------------------------------------------------
+def _rows(t, name, dtype, rows, device, cols=None):
+    """(pointer, row pitch) of a 2D tensor whose rows may lie further apart than they are wide."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor (the library has no CPU path)")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, QKV on {device}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
+    if t.dim() != 2 or t.shape[0] != rows or (cols is not None and t.shape[1] != cols):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, not ({rows}, {'...' if cols is None else cols})")
+    if t.shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    return t.data_ptr(), t.stride(0) if rows > 1 else max(t.stride(0), t.shape[1])
+
+
+def _vec(t, name, dtype, shape, device):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape):
+        raise (TypeError if t.dtype != dtype else ValueError)(f"{name} must be {dtype} of shape {tuple(shape)}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, QKV on {device}")
+    return _dev(t, name)
+
+
+def _attn_cfg(cfg: dict, T: int) -> tp_attn_config:
+    return tp_attn_config(T, cfg["b"], cfg.get("s") or 0, cfg["n_heads"], cfg["n_kv_heads"], cfg["d"], cfg["N"],
+                          int(bool(cfg["causal"])), float(cfg.get("scale") or 0.0))
+
+
+def _bias_cfg(bias: dict) -> tp_relbias_config:
+    return tp_relbias_config(bias["num_buckets"], bias["max_distance"], int(bool(bias["bidirectional"])))
+
+
+def _attn_common(QKV, cfg, C, lse, seq_starts):
+    """The arguments that every call of this family begins with, checked against the sizes."""
+    if not isinstance(QKV, torch.Tensor) or QKV.dim() != 2:
+        raise ValueError("QKV must be a 2D tensor")
+    T, dev = QKV.shape[0], QKV.device
+    if QKV.is_cuda and dev.index != torch.cuda.current_device():
+        raise ValueError(f"QKV is on {dev}, the current device is cuda:{torch.cuda.current_device()}")
+    H, KV, d = cfg["n_heads"], cfg["n_kv_heads"], cfg["d"]
+    q = _rows(QKV, "QKV", torch.bfloat16, T, dev, (H + 2 * KV) * d)
+    c = _rows(C, "C", torch.bfloat16, T, dev, H * d)
+    l = _vec(lse, "lse", torch.float32, (H, T), dev)
+    st = None if seq_starts is None else _vec(seq_starts, "seq_starts", torch.int64, (cfg["b"] + 1,), dev)
+    return _attn_cfg(cfg, T), q, c, l, st, T, dev
+
+
+def tp_attn_recompute_workspace_size(cfg: dict, T: int, bias: Optional[dict] = None) -> int:
+    """Bytes of the backward's workspace for T token rows (bias: if its table's gradient is asked for)."""
+    c = _attn_cfg(cfg, T)
+    b = None if bias is None else ctypes.byref(_bias_cfg(bias))
+    return int(lib().tp_attn_recompute_workspace_size(ctypes.byref(c), b))
+
+
+def tp_attn_recompute_fwd(QKV, cfg, C, lse, seq_starts=None, stream=None):
+    """C (T, n_heads d) bf16 and lse (n_heads, T) fp32 <- softmax attention of the shard-major
+    QKV (T, (n_heads + 2 n_kv_heads) d), no probabilities stored.
+
+    cfg: dict with b, n_heads, n_kv_heads, d, N, causal, optionally scale (0: 1 / sqrt(d)), and s (tokens of
+    every sequence) unless seq_starts (int64 CUDA tensor of b + 1 row numbers) is given.  Rows outside every
+    sequence are left as they are."""
+    c, q, o, l, st, _, _ = _attn_common(QKV, cfg, C, lse, seq_starts)
+    _check(lib().tp_attn_recompute_fwd(TP_BF16, ctypes.byref(c), st, q[0], q[1], o[0], o[1], l, _stream(stream)),
+           "tp_attn_recompute_fwd")
+
+
+def tp_attn_recompute_bwd(QKV, cfg, C, lse, dC, dQKV, workspace, seq_starts=None, stream=None):
+    """dQKV <- gradient of tp_attn_recompute_fwd given its C and lse and the context gradient dC."""
+    c, q, o, l, st, T, dev = _attn_common(QKV, cfg, C, lse, seq_starts)
+    do = _rows(dC, "dC", torch.bfloat16, T, dev, C.shape[1])
+    dq = _rows(dQKV, "dQKV", torch.bfloat16, T, dev, QKV.shape[1])
+    _check(lib().tp_attn_recompute_bwd(TP_BF16, ctypes.byref(c), st, q[0], q[1], o[0], o[1], l, do[0], do[1],
+                                       dq[0], dq[1], _dev(workspace, "workspace"), _ws_bytes(workspace),
+                                       _stream(stream)),
+           "tp_attn_recompute_bwd")
+
+
+def tp_attn_relbias_fwd(QKV, cfg, bias, table, C, lse, seq_starts=None, stream=None):
+    """tp_attn_recompute_fwd with table[bucket(key - query), head] added to the scores.
+
+    bias: dict with num_buckets, max_distance, bidirectional; table (num_buckets, n_heads) fp32."""
+    c, q, o, l, st, _, dev = _attn_common(QKV, cfg, C, lse, seq_starts)
+    t = _vec(table, "table", torch.float32, (bias["num_buckets"], cfg["n_heads"]), dev)
+    _check(lib().tp_attn_relbias_fwd(TP_BF16, ctypes.byref(c), ctypes.byref(_bias_cfg(bias)), t, st, q[0], q[1],
+                                     o[0], o[1], l, _stream(stream)),
+           "tp_attn_relbias_fwd")
+
+
+def tp_attn_relbias_bwd(QKV, cfg, bias, table, C, lse, dC, dQKV, dtable, workspace, accumulate=False,
+                        seq_starts=None, stream=None):
+    """dQKV and, unless it is None, dtable <- gradient of tp_attn_relbias_fwd."""
+    c, q, o, l, st, T, dev = _attn_common(QKV, cfg, C, lse, seq_starts)
+    shape = (bias["num_buckets"], cfg["n_heads"])
+    t = _vec(table, "table", torch.float32, shape, dev)
+    dt = None if dtable is None else _vec(dtable, "dtable", torch.float32, shape, dev)
+    do = _rows(dC, "dC", torch.bfloat16, T, dev, C.shape[1])
+    dq = _rows(dQKV, "dQKV", torch.bfloat16, T, dev, QKV.shape[1])
+    _check(lib().tp_attn_relbias_bwd(TP_BF16, ctypes.byref(c), ctypes.byref(_bias_cfg(bias)), t, st, q[0], q[1],
+                                     o[0], o[1], l, do[0], do[1], dq[0], dq[1], dt, int(bool(accumulate)),
+                                     _dev(workspace, "workspace"), _ws_bytes(workspace), _stream(stream)),
+           "tp_attn_relbias_bwd")
 
 
 def tp_position_embed_dropout(words, pos_table, positions, p, seed, stream_id, out, stream=None):

@@ -1206,6 +1206,250 @@ extern "C" tp_status tp_attn_core_dropout_bwd(tp_dtype dt, int64_t T, int64_t s,
 }
 
 // ===========================================================================
+// Attention without stored probabilities
+// ===========================================================================
+namespace {
+
+// One operand as a 4D map (d, token, head of the shard, shard) with a box of
+// 64 columns x 128 tokens of one head, 128-byte swizzle.  Columns past d and
+// tokens past T read as zeros.
+bool encode_map_heads(CUtensorMap* m, const void* ptr, int64_t d, int64_t T, int64_t ld, int heads, int shards,
+                      int64_t shard_w) {
+  cuuint64_t gdim[4] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(T), static_cast<cuuint64_t>(heads),
+                        static_cast<cuuint64_t>(shards)};
+  cuuint64_t gstride[3] = {static_cast<cuuint64_t>(ld) * 2, static_cast<cuuint64_t>(d) * 2,
+                           static_cast<cuuint64_t>(shard_w) * 2};
+  cuuint32_t box[4] = {64, 128, 1, 1};
+  cuuint32_t estr[4] = {1, 1, 1, 1};
+  return g_encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(ptr), gdim, gstride, box, estr,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Whether (n / E)^K >= (md / E)^j for whole numbers E <= n, E < md: exactly.
+// In doubles where the two logarithms are apart, else by multiplication of
+// whole numbers (n^K E^j against md^j E^K) in 32-bit limbs.
+bool rel_step_reached(int n, int E, int md, int K, int j) {
+  const double a = K * log(static_cast<double>(n) / E), b = j * log(static_cast<double>(md) / E);
+  if (fabs(a - b) > 1e-6 * (1.0 + fabs(b))) return a > b;
+  // at most 256 factors of 10 bits and 256 of 7: 4352 bits
+  struct Big {
+    uint32_t limb[144];
+    int n;
+  };
+  auto power = [](int x, int p, int y, int q) {
+    Big v;
+    v.limb[0] = 1u;
+    v.n = 1;
+    for (int i = 0; i < p + q; ++i) {
+      uint64_t carry = 0;
+      for (int l = 0; l < v.n; ++l) {
+        carry += static_cast<uint64_t>(v.limb[l]) * static_cast<uint32_t>(i < p ? x : y);
+        v.limb[l] = static_cast<uint32_t>(carry);
+        carry >>= 32;
+      }
+      if (carry) v.limb[v.n++] = static_cast<uint32_t>(carry);
+    }
+    return v;
+  };
+  const Big l = power(n, K, E, j), r = power(md, j, E, K);
+  if (l.n != r.n) return l.n > r.n;
+  for (int i = l.n; i-- > 0;)
+    if (l.limb[i] != r.limb[i]) return l.limb[i] > r.limb[i];
+  return true;
+}
+
+// Sizes and bias into P, without pointers.
+tp_status rc_sizes(const tp_attn_config* c, const tp_relbias_config* rb, bool dense, RcParams* P) {
+  if (c == nullptr) return TP_ERR_INVALID;
+  if (c->T < 0 || c->T > INT32_MAX || c->b < 0 || c->b > INT32_MAX || c->n_heads < 1 || c->n_kv_heads < 1 ||
+      c->N < 1 || c->N > 8 || c->n_heads % c->N != 0 || c->n_kv_heads % c->N != 0 ||
+      c->n_heads % c->n_kv_heads != 0 || c->d < 1 || c->d > 128)
+    return TP_ERR_INVALID;
+  if (!(c->scale >= 0.f) || !isfinite(c->scale)) return TP_ERR_INVALID;
+  if (c->T > 0 && c->b < 1) return TP_ERR_INVALID;
+  if (dense && c->T > 0 && (c->s < 1 || c->s > c->T || c->b > c->T || c->b * c->s != c->T)) return TP_ERR_INVALID;
+  // one CTA a head and run of 128 rows (each sequence adds at most one that is not full)
+  if ((c->T / 128 + c->b) * c->n_heads > INT32_MAX) return TP_ERR_INVALID;
+  if ((static_cast<int64_t>(c->n_heads) + 2 * static_cast<int64_t>(c->n_kv_heads)) * c->d > INT32_MAX)
+    return TP_ERR_INVALID;
+  P->bias.nb = 0;
+  if (rb != nullptr) {
+    const int nb = rb->num_buckets, both = rb->bidirectional != 0;
+    if (nb < 2 || nb > kMaxRelBuckets || (both && nb % 2 != 0)) return TP_ERR_INVALID;
+    const int B = both ? nb / 2 : nb, E = B / 2, md = rb->max_distance;
+    if (B < 2 || md <= E || md > kMaxRelDistance) return TP_ERR_INVALID;
+    P->bias.nb = nb;
+    P->bias.md = md;
+    P->bias.both = both;
+    P->bias.side = B;
+    for (int k = 0; k < E; ++k) P->bias.first[k] = k;
+    // Bucket E + j begins at the smallest n with (n / E)^(B-E) >= (max / E)^j.
+    const int K = B - E;
+    for (int j = 0, n = E; j < K; ++j) {
+      while (n < md && !rel_step_reached(n, E, md, K, j)) ++n;
+      P->bias.first[E + j] = n;
+    }
+  }
+  if (c->d % 8 != 0) return TP_ERR_ALIGN;
+  P->T = c->T;
+  P->b = static_cast<int>(c->b);
+  P->s = dense ? static_cast<int>(c->s) : 0;
+  P->H = c->n_heads;
+  P->KV = c->n_kv_heads;
+  P->d = c->d;
+  P->causal = c->causal != 0;
+  P->group = c->n_heads / c->n_kv_heads;
+  P->hq = c->n_heads / c->N;
+  P->hk = c->n_kv_heads / c->N;
+  P->shard_w = (P->hq + 2 * P->hk) * c->d;
+  P->scale = c->scale > 0.f ? c->scale : 1.f / sqrtf(static_cast<float>(c->d));
+  P->scale_log2 = P->scale * 1.4426950408889634f;
+  return TP_OK;
+}
+
+bool pitch_ok(int64_t ld, int64_t width) { return ld >= width && ld <= (int64_t{1} << 36); }
+
+// Everything both directions check and fill in.
+tp_status rc_args(tp_dtype dt, const tp_attn_config* c, const tp_relbias_config* rb, bool with_bias,
+                  const float* table, const int64_t* seq_starts, const void* QKV, int64_t ld_qkv, const void* C,
+                  int64_t ld_c, const float* lse, RcParams* P) {
+  if (!dtype_ok(dt)) return TP_ERR_UNSUPPORTED;
+  if (with_bias && rb == nullptr) return TP_ERR_INVALID;
+  tp_status st = rc_sizes(c, with_bias ? rb : nullptr, seq_starts == nullptr, P);
+  if (st == TP_ERR_INVALID) return st;
+  if (dt != TP_BF16) return TP_ERR_UNSUPPORTED;
+  if (st != TP_OK) return st;
+  if (c->T == 0) return TP_OK;
+  if (!QKV || !C || !lse || (with_bias && !table)) return TP_ERR_INVALID;
+  if (!pitch_ok(ld_qkv, static_cast<int64_t>(P->shard_w) * c->N) ||
+      !pitch_ok(ld_c, static_cast<int64_t>(P->H) * P->d))
+    return TP_ERR_INVALID;
+  if (!al16(QKV) || !al16(C) || ld_qkv % 8 != 0 || ld_c % 8 != 0 ||
+      (reinterpret_cast<uintptr_t>(lse) & 3u) != 0 || (reinterpret_cast<uintptr_t>(table) & 3u) != 0 ||
+      (reinterpret_cast<uintptr_t>(seq_starts) & 7u) != 0)
+    return TP_ERR_ALIGN;
+  P->seq_starts = seq_starts;
+  P->ld_c = ld_c;
+  P->C = const_cast<void*>(C);
+  P->lse = const_cast<float*>(lse);
+  P->table = table;
+  return TP_OK;
+}
+
+// Maps of Q, K and V, and the device's state: after every argument check.
+tp_status rc_device(RcParams* P, const void* QKV, int64_t ld_qkv, int N, DeviceState** dev) {
+  if (device_state(dev) != TP_OK || !get_encode()) return TP_ERR_CUDA;
+  const uint8_t* q = cb(QKV);
+  const uint8_t* k = q + static_cast<size_t>(P->hq) * P->d * 2;
+  const uint8_t* v = k + static_cast<size_t>(P->hk) * P->d * 2;
+  if (!encode_map_heads(&P->mapQ, q, P->d, P->T, ld_qkv, P->hq, N, P->shard_w) ||
+      !encode_map_heads(&P->mapK, k, P->d, P->T, ld_qkv, P->hk, N, P->shard_w) ||
+      !encode_map_heads(&P->mapV, v, P->d, P->T, ld_qkv, P->hk, N, P->shard_w))
+    return TP_ERR_CUDA;
+  P->err = (*dev)->err;
+  P->wait_limit_ns = g_wait_limit_ns;
+  P->fault_skip = g_fault_kind == 1;
+  g_fault_kind = 0;
+  return TP_OK;
+}
+
+tp_status rc_fwd_impl(const char* name, tp_dtype dt, const tp_attn_config* cfg, const tp_relbias_config* rb,
+                      bool with_bias, const float* table, const int64_t* seq_starts, const void* QKV,
+                      int64_t ld_qkv, void* C, int64_t ld_c, float* lse, void* stream) {
+  RcParams P;
+  memset(&P, 0, sizeof(P));
+  tp_status st = rc_args(dt, cfg, rb, with_bias, table, seq_starts, QKV, ld_qkv, C, ld_c, lse, &P);
+  if (st != TP_OK || cfg->T == 0) return st;
+  DeviceState* dev = nullptr;
+  if ((st = rc_device(&P, QKV, ld_qkv, cfg->N, &dev)) != TP_OK) return st;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const int sms = dev->num_sms;
+  return timed(name, s, [&] { return launch_rc_fwd(P, sms, s); }) == cudaSuccess ? TP_OK : TP_ERR_CUDA;
+}
+
+tp_status rc_bwd_impl(const char* name, tp_dtype dt, const tp_attn_config* cfg, const tp_relbias_config* rb,
+                      bool with_bias, const float* table, const int64_t* seq_starts, const void* QKV,
+                      int64_t ld_qkv, const void* C, int64_t ld_c, const float* lse, const void* dC, int64_t ld_dc,
+                      void* dQKV, int64_t ld_dqkv, float* dtable, int accumulate, void* workspace, size_t ws_bytes,
+                      void* stream) {
+  RcParams P;
+  memset(&P, 0, sizeof(P));
+  tp_status st = rc_args(dt, cfg, rb, with_bias, table, seq_starts, QKV, ld_qkv, C, ld_c, lse, &P);
+  if (st != TP_OK) return st;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (cfg->T == 0) {
+    // no pairs: the bias's gradient is zero
+    if (dtable == nullptr || accumulate) return TP_OK;
+    if ((reinterpret_cast<uintptr_t>(dtable) & 3u) != 0) return TP_ERR_ALIGN;
+    return cudaMemsetAsync(dtable, 0, static_cast<size_t>(P.bias.nb) * P.H * 4, s) == cudaSuccess ? TP_OK
+                                                                                                  : TP_ERR_CUDA;
+  }
+  if (!dC || !dQKV) return TP_ERR_INVALID;
+  if (!pitch_ok(ld_dc, static_cast<int64_t>(P.H) * P.d) || !pitch_ok(ld_dqkv, static_cast<int64_t>(P.shard_w) * cfg->N))
+    return TP_ERR_INVALID;
+  if (!al16(dC) || !al16(dQKV) || ld_dc % 8 != 0 || ld_dqkv % 8 != 0 ||
+      (reinterpret_cast<uintptr_t>(dtable) & 3u) != 0)
+    return TP_ERR_ALIGN;
+  const size_t dot = rc_dot_bytes(P.T, P.H);
+  if (workspace == nullptr || ws_bytes < dot + (dtable ? rc_partial_bytes(P) : 0)) return TP_ERR_WORKSPACE;
+  if (!al256(workspace)) return TP_ERR_ALIGN;
+  P.dC = dC;
+  P.ld_dc = ld_dc;
+  P.dQKV = dQKV;
+  P.ld_dqkv = ld_dqkv;
+  P.D = reinterpret_cast<float*>(workspace);
+  P.dtable = dtable;
+  P.accumulate = accumulate;
+  P.partial = dtable ? reinterpret_cast<float*>(bb(workspace) + dot) : nullptr;
+  DeviceState* dev = nullptr;
+  if ((st = rc_device(&P, QKV, ld_qkv, cfg->N, &dev)) != TP_OK) return st;
+  if (!encode_map_heads(&P.mapO, dC, P.d, P.T, ld_dc, P.hq, cfg->N, static_cast<int64_t>(P.hq) * P.d))
+    return TP_ERR_CUDA;
+  const int sms = dev->num_sms;
+  return timed(name, s, [&] { return launch_rc_bwd(P, sms, s); }) == cudaSuccess ? TP_OK : TP_ERR_CUDA;
+}
+
+}  // namespace
+
+extern "C" tp_status tp_attn_recompute_fwd(tp_dtype dt, const tp_attn_config* cfg, const int64_t* seq_starts,
+                                           const void* QKV, int64_t ld_qkv, void* C, int64_t ld_c, float* lse,
+                                           void* stream) {
+  return rc_fwd_impl("attn_recompute_fwd", dt, cfg, nullptr, false, nullptr, seq_starts, QKV, ld_qkv, C, ld_c, lse,
+                     stream);
+}
+
+extern "C" tp_status tp_attn_recompute_bwd(tp_dtype dt, const tp_attn_config* cfg, const int64_t* seq_starts,
+                                           const void* QKV, int64_t ld_qkv, const void* C, int64_t ld_c,
+                                           const float* lse, const void* dC, int64_t ld_dc, void* dQKV,
+                                           int64_t ld_dqkv, void* workspace, size_t ws_bytes, void* stream) {
+  return rc_bwd_impl("attn_recompute_bwd", dt, cfg, nullptr, false, nullptr, seq_starts, QKV, ld_qkv, C, ld_c, lse,
+                     dC, ld_dc, dQKV, ld_dqkv, nullptr, 0, workspace, ws_bytes, stream);
+}
+
+extern "C" tp_status tp_attn_relbias_fwd(tp_dtype dt, const tp_attn_config* cfg, const tp_relbias_config* bias,
+                                         const float* table, const int64_t* seq_starts, const void* QKV,
+                                         int64_t ld_qkv, void* C, int64_t ld_c, float* lse, void* stream) {
+  return rc_fwd_impl("attn_relbias_fwd", dt, cfg, bias, true, table, seq_starts, QKV, ld_qkv, C, ld_c, lse, stream);
+}
+
+extern "C" tp_status tp_attn_relbias_bwd(tp_dtype dt, const tp_attn_config* cfg, const tp_relbias_config* bias,
+                                         const float* table, const int64_t* seq_starts, const void* QKV,
+                                         int64_t ld_qkv, const void* C, int64_t ld_c, const float* lse,
+                                         const void* dC, int64_t ld_dc, void* dQKV, int64_t ld_dqkv, float* dtable,
+                                         int accumulate, void* workspace, size_t ws_bytes, void* stream) {
+  return rc_bwd_impl("attn_relbias_bwd", dt, cfg, bias, true, table, seq_starts, QKV, ld_qkv, C, ld_c, lse, dC,
+                     ld_dc, dQKV, ld_dqkv, dtable, accumulate, workspace, ws_bytes, stream);
+}
+
+extern "C" size_t tp_attn_recompute_workspace_size(const tp_attn_config* cfg, const tp_relbias_config* bias) {
+  RcParams P;
+  memset(&P, 0, sizeof(P));
+  if (rc_sizes(cfg, bias, false, &P) != TP_OK || cfg->T == 0) return 0;
+  return rc_dot_bytes(P.T, P.H) + (bias ? rc_partial_bytes(P) : 0);
+}
+
+// ===========================================================================
 // Vocab-parallel embedding, logits, tied gradient
 // ===========================================================================
 namespace {
@@ -1772,6 +2016,7 @@ extern "C" tp_status tp_get_status(void* stream) {
     const unsigned zero = 0;
     if (cudaMemcpyToSymbol(g_tp_error_word, &zero, sizeof(zero)) != cudaSuccess) return TP_ERR_CUDA;
     if (w & kErrTimeout) return TP_ERR_TIMEOUT;
+    if (w & kErrInvalid) return TP_ERR_INVALID;
   }
   return TP_OK;
 }

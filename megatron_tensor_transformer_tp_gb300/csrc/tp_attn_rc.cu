@@ -1,0 +1,1273 @@
+// Softmax attention that stores no probabilities, its gradient, and both with
+// a learned relative position bias, on the tcgen05 tensor cores.
+//
+// With x_ij = scale q_i . k_j (+ bias[bucket(j - i)]) over the keys that query
+// i sees (its own sequence; j <= i if causal):
+//   forward   lse_i = log sum_j exp(x_ij),  C_i = sum_j exp(x_ij - lse_i) v_j
+//   backward  P_ij = exp(x_ij - lse_i),  D_i = dC_i . C_i,  dP_ij = dC_i . v_j,
+//             dS_ij = P_ij (dP_ij - D_i),
+//             dV_j = sum_i P_ij dC_i,  dK_j = scale sum_i dS_ij q_i,
+//             dQ_i = scale sum_j dS_ij k_j,  dbias[u] = sum of dS_ij over bucket u.
+// Scores and probabilities live in TMEM and registers only: 128 x 128 tiles,
+// fp32 accumulators, exponentials as 2^(x log2 e).
+//
+// Three tensor-core kernels, each with eight compute warps (TMEM lane = row of
+// the score tile), one MMA warp and one TMA warp per CTA, one CTA per SM:
+//   rc_fwd_kernel   one or two 128-row query tiles of a head; the matrix
+//                   products of one tile run under the softmax of the other.
+//   rc_dkv_kernel   a 128-row key tile of a K/V head, over the query tiles of
+//                   every query head that shares it.  It computes the
+//                   transposed scores S^T = K Q^T and dP^T = V dC^T, so P^T
+//                   and dS^T are A operands straight from TMEM.
+//   rc_dq_kernel    a 128-row query tile of a head over its key tiles; it also
+//                   sums dS by relative distance for the bias.
+// The backward computes the scores and dP in both kernels (seven products a
+// tile instead of five): no output is summed by atomics, so results do not
+// depend on the order in which CTAs run, and dQ needs no fp32 buffer in memory.
+// Every wait is bounded, as in the GEMM engine.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <math.h>
+#include <stdint.h>
+
+#include "tp_device.cuh"
+#include "tp_internal.h"
+#include "tp_tcgen05.cuh"
+
+namespace tp {
+namespace {
+
+constexpr int kThreads = 320;        // 8 compute warps, MMA warp 8, TMA warp 9
+constexpr int kMmaWarp = 8, kTmaWarp = 9;
+constexpr int kPanel = 128 * 128;    // bytes of 128 rows x 64 bf16 columns (one swizzle width)
+constexpr int kBarBytes = 512;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+// The smem distance table covers [-(md + kPad), md + kPad], so that a tile that
+// holds any distance inside (-md, md) indexes it without clamping.
+constexpr int kPad = 255;
+__host__ __device__ constexpr int table_floats(int md) { return 2 * (md + kPad) + 1; }
+
+// ---------------------------------------------------------------------------
+// PTX wrappers of this file
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int c0, int c1,
+                                            int c2, int c3) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+      : "memory");
+}
+
+// D += A B with A (128 x 16 bf16, two per 32-bit column) in TMEM.
+__device__ __forceinline__ void mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t idesc,
+                                            uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b), "r"(idesc), "r"(accumulate));
+}
+
+// 32 columns of the warp's 32 lanes, without waiting for them.
+__device__ __forceinline__ void tmem_ld32_issue(uint32_t taddr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
+        "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
+        "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr));
+}
+// Waits for the loads issued so far.  The registers pass through the statement,
+// so no use of them can be moved in front of the wait.
+__device__ __forceinline__ void tmem_ld32_wait(uint32_t* r) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]),
+                 "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]),
+                 "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]),
+                 "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]),
+                 "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])::"memory");
+}
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31};" ::"r"(r[0]),
+      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]),
+      "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]),
+      "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+__device__ __forceinline__ void named_bar(int id, int threads) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+
+// wait_bounded by a whole warp, with one answer for all of its lanes.
+__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, const WaitCtx& w) {
+  return __all_sync(0xffffffffu, wait_bounded(bar, parity, w));
+}
+
+__device__ __forceinline__ float as_f(uint32_t u) { return __uint_as_float(u); }
+
+// ---------------------------------------------------------------------------
+// Work items
+// ---------------------------------------------------------------------------
+// Unit `unit` of the launch: a run of `rows` tokens of a sequence.  Called by
+// a whole warp; false if there is no such unit.  Sequences given by
+// seq_starts are clamped into [0, T]; starts that decrease or leave [0, T] are
+// reported in the error word by the first block.
+struct Unit {
+  int start, len, tile;  // first token and length of the sequence, tile inside it
+};
+__device__ __forceinline__ bool find_unit(const RcParams& p, int64_t unit, int rows, bool last_first, bool report,
+                                          int lane, Unit& u) {
+  if (p.seq_starts == nullptr) {
+    // the longest contractions first, across the sequences
+    const int per = (p.s + rows - 1) / rows;
+    const int rank = static_cast<int>(unit / p.b), seq = static_cast<int>(unit % p.b);
+    if (rank >= per) return false;
+    u.tile = last_first ? per - 1 - rank : rank;
+    u.start = seq * p.s;
+    u.len = p.s;
+    return true;
+  }
+  int64_t base = 0;
+  bool found = false, bad = false;
+  for (int i0 = 0; i0 < p.b; i0 += 32) {
+    const int i = i0 + lane;
+    int64_t a = 0, e = 0;
+    if (i < p.b) {
+      a = p.seq_starts[i];
+      e = p.seq_starts[i + 1];
+      bad |= a < 0 || e < a || e > p.T;
+      a = min(max(a, static_cast<int64_t>(0)), p.T);
+      e = min(max(e, a), p.T);
+    }
+    const int n = static_cast<int>((e - a + rows - 1) / rows);
+    int64_t incl = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += v;
+    }
+    const unsigned hit = __ballot_sync(0xffffffffu, base + incl > unit);
+    if (!found && hit) {
+      const int src = __ffs(hit) - 1;
+      u.start = static_cast<int>(__shfl_sync(0xffffffffu, a, src));
+      u.len = static_cast<int>(__shfl_sync(0xffffffffu, e - a, src));
+      const int tiles = __shfl_sync(0xffffffffu, n, src);
+      const int t = static_cast<int>(unit - __shfl_sync(0xffffffffu, base + incl - n, src));
+      u.tile = last_first ? tiles - 1 - t : t;
+      found = true;
+      if (!report) break;  // warp-uniform
+    }
+    base += __shfl_sync(0xffffffffu, incl, 31);
+  }
+  if (report && bad) atomicOr(p.err, kErrInvalid);
+  return found;
+}
+
+// ---------------------------------------------------------------------------
+// Relative position bias
+// ---------------------------------------------------------------------------
+// Bucket of the distance delta = key - query.
+__device__ __forceinline__ int bucket_of(const RcBias& b, int delta) {
+  int add = 0, n = -delta;
+  if (b.both) {
+    if (delta > 0) add = b.side;
+    n = delta > 0 ? delta : -delta;
+  }
+  n = max(n, 0);
+  int lo = 0, hi = b.side - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (b.first[mid] <= n) lo = mid;
+    else hi = mid - 1;
+  }
+  return add + lo;
+}
+// tab[delta + md + kPad] = bias of the clamped distance, times log2 e.
+__device__ __forceinline__ void fill_table(const RcParams& p, int head, float* tab) {
+  const int md = p.bias.md, n = table_floats(md);
+  for (int i = threadIdx.x; i < n; i += kThreads) {
+    const int delta = min(max(i - (md + kPad), -md), md);
+    tab[i] = __ldg(p.table + static_cast<int64_t>(bucket_of(p.bias, delta)) * p.H + head) * kLog2e;
+  }
+}
+// How a (query tile at r0, key tile at c0) pair of 128 x 128 sees the bias:
+// 0 distances differ, +-1 every distance is clamped to the same end.
+__device__ __forceinline__ int bias_side(int md, int r0, int c0) {
+  if (c0 + 127 - r0 <= -md) return -1;
+  if (c0 - r0 - 127 >= md) return 1;
+  return 0;
+}
+
+// ---------------------------------------------------------------------------
+// Pieces that the kernels share
+// ---------------------------------------------------------------------------
+struct HeadAt {
+  int shard, local;
+};
+__device__ __forceinline__ HeadAt head_at(int head, int per_shard) {
+  return HeadAt{head / per_shard, head % per_shard};
+}
+
+// 128 rows (from token) of one head as DP / 64 swizzled panels.
+template <int DP>
+__device__ __forceinline__ void load_tile(uint32_t dst, const CUtensorMap* map, uint32_t bar, int token, HeadAt h) {
+#pragma unroll
+  for (int c = 0; c < DP / 64; ++c) tma_load_4d(dst + c * kPanel, map, bar, 64 * c, token, h.local, h.shard);
+}
+// Rows [row, 128) of a tile become zeros (a whole warp); the tensor cores see
+// them after the caller's arrival on the tile's barrier.
+template <int DP>
+__device__ __forceinline__ void zero_rows(uint8_t* tile, int row, int lane) {
+#pragma unroll
+  for (int c = 0; c < DP / 64; ++c) {
+    uint4* q = reinterpret_cast<uint4*>(tile + c * kPanel);
+    for (int i = row * 8 + lane; i < 128 * 8; i += 32) q[i] = make_uint4(0, 0, 0, 0);
+  }
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  __syncwarp();
+}
+// Loads a tile whose rows from `valid` on belong to nobody: they hold another
+// sequence's values, or anything, and would reach the sums as 0 x NaN.  The
+// copy lands on the side barrier, the rows are cleared, then `bar` completes.
+template <int DP>
+__device__ __forceinline__ bool load_tail(uint8_t* smem_tile, const CUtensorMap* map, uint32_t bar,
+                                          uint32_t tail_bar, uint32_t& tail_phase, int token, HeadAt h, int valid,
+                                          int lane, const WaitCtx& w) {
+  if (lane == 0) {
+    mbar_arrive_expect_tx(tail_bar, DP / 64 * kPanel);
+    load_tile<DP>(smem_addr(smem_tile), map, tail_bar, token, h);
+  }
+  __syncwarp();
+  if (!wait_warp(tail_bar, tail_phase, w)) {
+    // aborted: the copy still has to land before the CTA may end
+    const unsigned long long t0 = global_ns();
+    while (!mbar_try_wait(tail_bar, tail_phase) && global_ns() - t0 <= w.limit_ns) {
+    }
+    __syncwarp();
+    return false;
+  }
+  tail_phase ^= 1u;
+  zero_rows<DP>(smem_tile, valid, lane);
+  if (lane == 0) mbar_arrive(bar);
+  return true;
+}
+
+// S = A B^T over the head width: both K-major in shared memory, 128 x 128.
+// A counted loop: unrolled with a condition around each issue, the compiled
+// code added the first product to what TMEM held before.
+template <int DP>
+__device__ __forceinline__ void mma_scores(uint32_t d_tmem, uint32_t a, uint32_t b, int ksteps) {
+  const uint64_t ad = sdesc(a, 16, 1024), bd = sdesc(b, 16, 1024);
+  const uint32_t idesc = idesc_bf16(0, 0, 128);
+  uint32_t acc = 0;
+#pragma unroll 1
+  for (int kk = 0; kk < ksteps; ++kk) {
+    const uint32_t off = static_cast<uint32_t>((kk >> 2) * kPanel + (kk & 3) * 32) >> 4;
+    mma_bf16(d_tmem, ad + off, bd + off, idesc, acc);
+    acc = 1;
+  }
+}
+// D (+)= A B: A 128 x 128 bf16 in TMEM, B = 128 rows of a tile as stored
+// (contraction over its rows).  a_half: TMEM columns between the two halves of
+// the contraction.
+__device__ __forceinline__ void mma_rows(uint32_t d_tmem, uint32_t a_tmem, int a_half, uint32_t b, uint32_t idesc,
+                                         bool accumulate) {
+  const uint64_t bd = sdesc(b, kPanel, 1024);
+#pragma unroll
+  for (int kk = 0; kk < 8; ++kk)
+    mma_bf16_ts(d_tmem, a_tmem + (kk >> 2) * a_half + (kk & 3) * 8, bd + kk * (2048 >> 4), idesc,
+                accumulate || kk > 0);
+}
+
+// One row of d fp32 TMEM columns, scaled, as bf16 to memory.
+__device__ __forceinline__ void store_row(uint32_t taddr, int d, float mul, __nv_bfloat16* out, bool ok) {
+  for (int c = 0; c < d; c += 32) {
+    uint32_t r[32];
+    tmem_ld32_issue(taddr + c, r);
+    tmem_ld32_wait(r);
+    if (ok) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        if (c + 8 * q < d) {
+          uint4 w;
+          w.x = pack_bf16x2(as_f(r[8 * q + 0]) * mul, as_f(r[8 * q + 1]) * mul);
+          w.y = pack_bf16x2(as_f(r[8 * q + 2]) * mul, as_f(r[8 * q + 3]) * mul);
+          w.z = pack_bf16x2(as_f(r[8 * q + 4]) * mul, as_f(r[8 * q + 5]) * mul);
+          w.w = pack_bf16x2(as_f(r[8 * q + 6]) * mul, as_f(r[8 * q + 7]) * mul);
+          *reinterpret_cast<uint4*>(out + c + 8 * q) = w;
+        }
+      }
+    }
+    __syncwarp();
+  }
+}
+
+// Copies in flight of the TMA warp: the barriers that one was issued on, and
+// the phase that it completes.  After an abort they are waited for.
+struct Flight {
+  uint32_t used = 0, phase = 0;
+  __device__ __forceinline__ void note(int i, uint32_t ph) {
+    used |= 1u << i;
+    phase = (phase & ~(1u << i)) | (ph << i);
+  }
+  __device__ __forceinline__ void drain(uint32_t bar0, unsigned long long limit_ns) const {
+    for (int i = 0; i < 32; ++i) {
+      if (!((used >> i) & 1u)) continue;
+      const unsigned long long t0 = global_ns();
+      while (!mbar_try_wait(bar0 + 8u * i, (phase >> i) & 1u))
+        if (global_ns() - t0 > limit_ns) break;
+    }
+  }
+};
+__device__ __forceinline__ void drain_mma(uint32_t bar, unsigned long long limit_ns) {
+  mma_commit(bar);
+  const unsigned long long t0 = global_ns();
+  while (!mbar_try_wait(bar, 0))
+    if (global_ns() - t0 > limit_ns) break;
+}
+
+__device__ __forceinline__ void tmem_alloc512(uint32_t slot) {
+  asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(slot), "r"(512)
+               : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_dealloc512(uint32_t base) {
+  asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(base), "r"(512) : "memory");
+}
+
+// Shared-memory head of every kernel here: barriers, the TMEM address, the
+// abort flag and the CTA's unit.
+struct Head {
+  uint64_t bar[40];
+  uint32_t tmem;
+  int abort_flag;
+  int found, start, len, tile;
+};
+static_assert(sizeof(Head) <= kBarBytes, "barrier area");
+
+__device__ __forceinline__ uint8_t* align1024(uint8_t* q) {
+  return reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(q) + 1023) & ~static_cast<uintptr_t>(1023));
+}
+
+// Common entry: barriers 0 .. nbars-1 with the given counts, TMEM, the unit.
+template <class Counts>
+__device__ __forceinline__ void enter(const RcParams& p, Head* hd, int nbars, Counts&& count, int64_t unit, int rows,
+                                      bool last_first) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < nbars; ++i) mbar_init(smem_addr(hd->bar + i), count(i));
+    hd->abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == kMmaWarp) tmem_alloc512(smem_addr(&hd->tmem));
+  if (warp == kTmaWarp) {
+    pdl_wait();
+    Unit u{0, 0, 0};
+    const bool f = find_unit(p, unit, rows, last_first, blockIdx.x == 0, lane, u);
+    if (lane == 0) {
+      hd->found = f;
+      hd->start = u.start;
+      hd->len = u.len;
+      hd->tile = u.tile;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  pdl_wait();
+  pdl_trigger();
+}
+__device__ __forceinline__ void leave(Head* hd) {
+  tc_fence_before();
+  __syncthreads();
+  if ((threadIdx.x >> 5) == kMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc512(hd->tmem);
+  }
+}
+
+// ===========================================================================
+// Forward
+// ===========================================================================
+template <int DP>
+struct FwdShape {
+  static constexpr int kTile = DP / 64 * kPanel;
+  static constexpr int kStages = DP == 128 ? 2 : 4;  // K tiles and V tiles held, each
+  static constexpr int kSmem = 2 * kTile + 2 * kStages * kTile + kBarBytes + 1024;
+  // barriers
+  static constexpr int qfull = 0, kfull = 2, vfull = kfull + kStages, tail = vfull + kStages, kempty = tail + 1,
+                       vempty = kempty + kStages, sfull = vempty + kStages, pfull = sfull + 2, odone = pfull + 2,
+                       drain = odone + 2, count = drain + 1;
+  static_assert(count <= 40 && kempty <= 32, "barriers");
+};
+
+template <int DP, bool BIAS>
+__global__ void __launch_bounds__(kThreads, 1) rc_fwd_kernel(const __grid_constant__ RcParams p) {
+  using L = FwdShape<DP>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = align1024(smem_raw);
+  uint8_t* sQ = smem;
+  uint8_t* sK = sQ + 2 * L::kTile;
+  uint8_t* sV = sK + L::kStages * L::kTile;
+  Head* hd = reinterpret_cast<Head*>(sV + L::kStages * L::kTile);
+  float* tab = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(hd) + kBarBytes);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int head = static_cast<int>(blockIdx.x % p.H);
+  const int nsub = p.sub;
+  enter(p, hd, L::count, [](int i) { return i >= L::pfull && i < L::pfull + 2 ? 4u : 1u; }, blockIdx.x / p.H,
+        128 * nsub, p.causal != 0);
+  if (BIAS && hd->found) fill_table(p, head, tab);
+  if (BIAS) __syncthreads();
+  const uint32_t bar0 = smem_addr(hd->bar);
+  auto bar = [&](int i) { return bar0 + 8u * i; };
+  const WaitCtx w{&hd->abort_flag, p.err, p.wait_limit_ns};
+  const uint32_t tmem = hd->tmem;
+  const int start = hd->start, len = hd->len, row0 = hd->tile * 128 * nsub;
+  const int nk_all = (len + 127) >> 7;
+  // key tiles of the CTA's query tile t (0: there is none)
+  auto tiles_of = [&](int t) {
+    const int r = row0 + 128 * t;
+    if (!hd->found || t >= nsub || r >= len) return 0;
+    return p.causal ? min(nk_all, (r >> 7) + 1) : nk_all;
+  };
+  const int n0 = tiles_of(0), n1 = tiles_of(1), nmax = max(n0, n1);
+
+  if (warp == kTmaWarp && nmax > 0) {
+    const HeadAt hq = head_at(head, p.hq), hk = head_at(head / p.group, p.hk);
+    Flight fl;
+    uint32_t tail_phase = 0;
+    bool ok = true, skip = p.fault_skip != 0;
+    auto load_q = [&](int t) {
+      mbar_arrive_expect_tx(bar(L::qfull + t), L::kTile);
+      fl.note(L::qfull + t, 0);
+      load_tile<DP>(smem_addr(sQ + t * L::kTile), &p.mapQ, bar(L::qfull + t), start + row0 + 128 * t, hq);
+    };
+    if (lane == 0) {
+      prefetch_tmap(&p.mapQ);
+      prefetch_tmap(&p.mapK);
+      prefetch_tmap(&p.mapV);
+      load_q(0);
+    }
+    for (int j = 0; ok && j < nmax; ++j) {
+      const int st = j % L::kStages;
+      const uint32_t ph = (j / L::kStages) & 1;
+      if (lane == 0) {
+        ok = wait_bounded(bar(L::kempty + st), ph ^ 1u, w);
+        if (ok && !skip) {
+          mbar_arrive_expect_tx(bar(L::kfull + st), L::kTile);
+          fl.note(L::kfull + st, ph);
+          load_tile<DP>(smem_addr(sK + st * L::kTile), &p.mapK, bar(L::kfull + st), start + 128 * j, hk);
+        }
+        skip = false;
+        if (ok && j == 0 && n1 > 0) load_q(1);
+        ok = ok && wait_bounded(bar(L::vempty + st), ph ^ 1u, w);
+      }
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+      if (!ok) break;
+      if (128 * j + 128 > len && start + len < p.T) {
+        ok = load_tail<DP>(sV + st * L::kTile, &p.mapV, bar(L::vfull + st), bar(L::tail), tail_phase,
+                           start + 128 * j, hk, len - 128 * j, lane, w);
+      } else if (lane == 0) {
+        mbar_arrive_expect_tx(bar(L::vfull + st), L::kTile);
+        fl.note(L::vfull + st, ph);
+        load_tile<DP>(smem_addr(sV + st * L::kTile), &p.mapV, bar(L::vfull + st), start + 128 * j, hk);
+      }
+    }
+    if (lane == 0 && *w.abort_flag) fl.drain(bar0, p.wait_limit_ns);
+    __syncwarp();
+  } else if (warp == kMmaWarp && lane == 0 && nmax > 0) {
+    const int ksteps = (p.d + 15) >> 4;
+    const uint32_t idesc_pv = idesc_bf16(0, 1, ksteps * 16);
+    const int last = n1 > 0 ? 1 : 0;  // the query tile that uses every key tile last
+    bool ok = true, issued = false;
+    auto scores = [&](int t, int j) {
+      mma_scores<DP>(tmem + 128 * t, smem_addr(sQ + t * L::kTile), smem_addr(sK + (j % L::kStages) * L::kTile),
+                     ksteps);
+      issued = true;
+      mma_commit(bar(L::sfull + t));
+      if (t == last) mma_commit(bar(L::kempty + j % L::kStages));
+    };
+    ok = wait_bounded(bar(L::kfull), 0, w);
+    for (int t = 0; ok && t <= last; ++t) {
+      ok = wait_bounded(bar(L::qfull + t), 0, w);
+      if (ok) {
+        tc_fence_after();
+        scores(t, 0);
+      }
+    }
+    for (int j = 0; ok && j < nmax; ++j) {
+      const int st = j % L::kStages;
+      const uint32_t ph = (j / L::kStages) & 1;
+      ok = wait_bounded(bar(L::vfull + st), ph, w);
+      for (int t = 0; ok && t <= last; ++t) {
+        const int nt = t ? n1 : n0;
+        if (j >= nt) continue;
+        if (!(ok = wait_bounded(bar(L::pfull + t), j & 1, w))) break;
+        tc_fence_after();
+        mma_rows(tmem + 256 + 128 * t, tmem + 128 * t, 32, smem_addr(sV + st * L::kTile), idesc_pv, j > 0);
+        issued = true;
+        if (t == last) mma_commit(bar(L::vempty + st));
+        if (j + 1 < nt) {
+          const int sn = (j + 1) % L::kStages;
+          if (!(ok = wait_bounded(bar(L::kfull + sn), ((j + 1) / L::kStages) & 1, w))) break;
+          scores(t, j + 1);
+        } else {
+          mma_commit(bar(L::odone + t));
+        }
+      }
+    }
+    if (*w.abort_flag && issued) drain_mma(bar(L::drain), p.wait_limit_ns);
+  } else if (warp < 8) {
+    const int t = warp >> 2;
+    const int nt = t ? n1 : n0;
+    const int row = row0 + 128 * t + (warp & 3) * 32 + lane;  // position in the sequence
+    const uint32_t lane_base = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+    const uint32_t tS = lane_base + 128 * t, tO = lane_base + 256 + 128 * t;
+    const float sl2 = p.scale_log2;
+    float m = 0.f, l = 0.f;  // the exponents' reference (log2) and the sum of 2^(x - m)
+    bool ok = true;
+    for (int j = 0; j < nt; ++j) {
+      if (!(ok = wait_warp(bar(L::sfull + t), j & 1, w))) break;
+      tc_fence_after();
+      uint32_t s[128];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) tmem_ld32_issue(tS + 32 * c, s + 32 * c);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) tmem_ld32_wait(s + 32 * c);
+      const int c0 = 128 * j, r0 = row0 + 128 * t;
+      float mul = sl2, add = 0.f;  // x = s mul + add
+      if (BIAS) {
+        const int side = bias_side(p.bias.md, r0, c0);
+        if (side != 0) {
+          add = tab[side < 0 ? 0 : table_floats(p.bias.md) - 1];
+        } else {
+          const float* tb = tab + (c0 - row + p.bias.md + kPad);
+#pragma unroll
+          for (int c = 0; c < 128; ++c) s[c] = __float_as_uint(fmaf(as_f(s[c]), sl2, tb[c]));
+          mul = 1.f;
+        }
+      }
+      if ((p.causal && c0 + 127 > r0) || c0 + 128 > len) {
+        const int seen = (p.causal ? min(len, row + 1) : len) - c0;  // columns this row sees
+#pragma unroll
+        for (int c = 0; c < 128; ++c) s[c] = c < seen ? s[c] : 0xff800000u;
+      }
+      float mx[4] = {as_f(s[0]), as_f(s[1]), as_f(s[2]), as_f(s[3])};
+#pragma unroll
+      for (int c = 4; c < 128; ++c) mx[c & 3] = fmaxf(mx[c & 3], as_f(s[c]));
+      const float mt = fmaf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), mul, add);
+      if (j == 0) {
+        m = mt;
+      } else if (__any_sync(0xffffffffu, mt > m + 8.f)) {
+        // The reference follows the maximum only when that is 2^8 above it: the
+        // exponentials stay below 2^8 (exact in fp32's and bf16's range), and
+        // the output is rescaled a few times a row instead of at every tile.
+        const float mn = mt > m + 8.f ? mt : m;
+        const float f = ex2_ftz(m - mn);
+        l *= f;
+        m = mn;
+        for (int c = 0; c < p.d; c += 32) {
+          uint32_t o[32];
+          tmem_ld32_issue(tO + c, o);
+          tmem_ld32_wait(o);
+#pragma unroll
+          for (int q = 0; q < 32; ++q) o[q] = __float_as_uint(as_f(o[q]) * f);
+          tmem_st32(tO + c, o);
+        }
+      }
+      const float off = add - m;
+      float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        uint32_t pk[32];
+#pragma unroll
+        for (int c = 0; c < 32; ++c) {
+          const float a = ex2_ftz(fmaf(as_f(s[64 * h + 2 * c]), mul, off));
+          const float b = ex2_ftz(fmaf(as_f(s[64 * h + 2 * c + 1]), mul, off));
+          sum[(2 * c) & 3] += a;
+          sum[(2 * c + 1) & 3] += b;
+          pk[c] = pack_bf16x2(a, b);
+        }
+        tmem_st32(tS + 32 * h, pk);
+      }
+      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(L::pfull + t));
+    }
+    if (nt > 0 && ok && wait_warp(bar(L::odone + t), 0, w)) {
+      tc_fence_after();
+      const bool mine = row < len;
+      const int64_t token = static_cast<int64_t>(start) + row;
+      store_row(tO, p.d, 1.f / l, static_cast<__nv_bfloat16*>(p.C) + token * p.ld_c + static_cast<int64_t>(head) * p.d,
+                mine);
+      if (mine) p.lse[static_cast<int64_t>(head) * p.T + token] = (m + log2f(l)) * kLn2;
+    }
+  }
+  leave(hd);
+}
+
+// ===========================================================================
+// Backward
+// ===========================================================================
+// D[h, t] = dC_t . C_t over head h's columns, in fp32.  One group of lanes a
+// (token, head), 16 bytes a lane and tensor.
+__global__ void __launch_bounds__(256) rc_dot_kernel(const __grid_constant__ RcParams p, int lanes_log2) {
+  pdl_wait();
+  pdl_trigger();
+  const int lg = lanes_log2, lanes = 1 << lg;
+  const int64_t n = p.T * p.H;
+  const int c = 8 * (threadIdx.x & (lanes - 1));
+  const int64_t step = (static_cast<int64_t>(gridDim.x) * 256) >> lg;
+  const int64_t i0 = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) >> lg;
+  const int64_t rounds = (n + step - 1) / step;
+  int64_t i = i0;
+  for (int64_t r = 0; r < rounds; ++r, i += step) {
+    float acc = 0.f;
+    const int64_t t = i / p.H;
+    const int h = static_cast<int>(i - t * p.H);
+    if (i < n && c < p.d) {
+      const uint4 a = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.C) + t * p.ld_c +
+                                                           static_cast<int64_t>(h) * p.d + c));
+      const uint4 b = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.dC) + t * p.ld_dc +
+                                                           static_cast<int64_t>(h) * p.d + c));
+      const uint32_t aa[4] = {a.x, a.y, a.z, a.w}, bb[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        float x0, x1, y0, y1;
+        unpack_bf16x2(aa[q], x0, x1);
+        unpack_bf16x2(bb[q], y0, y1);
+        acc = fmaf(x0, y0, acc);
+        acc = fmaf(x1, y1, acc);
+      }
+    }
+    for (int o = lanes >> 1; o > 0; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
+    if (i < n && c == 0) p.D[static_cast<int64_t>(h) * p.T + t] = acc;
+  }
+}
+
+template <int DP>
+struct DkvShape {
+  static constexpr int kTile = DP / 64 * kPanel;
+  static constexpr int kStages = DP == 128 ? 2 : 4;  // (Q, dC) tile pairs held
+  static constexpr int kVec = 2 * 128 * 8;           // (lse, D) of two query tiles
+  static constexpr int kSmem = 2 * kTile + 2 * kStages * kTile + kBarBytes + kVec + 1024;
+  static constexpr int kvfull = 0, qfull = 1, ofull = qfull + kStages, tail = ofull + kStages, empty = tail + 1,
+                       sfull = empty + kStages, dpfull = sfull + 1, pready = dpfull + 1, dsready = pready + 1,
+                       done = dsready + 1, drain = done + 1, count = drain + 1;
+  static_assert(count <= 40 && empty <= 32, "barriers");
+};
+
+template <int DP, bool BIAS>
+__global__ void __launch_bounds__(kThreads, 1) rc_dkv_kernel(const __grid_constant__ RcParams p) {
+  using L = DkvShape<DP>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = align1024(smem_raw);
+  uint8_t* sK = smem;
+  uint8_t* sV = sK + L::kTile;
+  uint8_t* sQ = sV + L::kTile;
+  uint8_t* sO = sQ + L::kStages * L::kTile;
+  Head* hd = reinterpret_cast<Head*>(sO + L::kStages * L::kTile);
+  float2* vec = reinterpret_cast<float2*>(reinterpret_cast<uint8_t*>(hd) + kBarBytes);
+  float* tab = reinterpret_cast<float*>(vec + 256);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int kvh = static_cast<int>(blockIdx.x % p.KV);
+  enter(p, hd, L::count, [](int i) { return i == L::pready || i == L::dsready ? 8u : 1u; }, blockIdx.x / p.KV, 128,
+        false);
+  const uint32_t bar0 = smem_addr(hd->bar);
+  auto bar = [&](int i) { return bar0 + 8u * i; };
+  const WaitCtx w{&hd->abort_flag, p.err, p.wait_limit_ns};
+  const uint32_t tmem = hd->tmem;
+  const uint32_t tS = tmem, tP = tmem + 128, tdV = tmem + 256, tdK = tmem + 256 + DP;
+  const int start = hd->start, len = hd->len, kt = hd->tile;
+  const int nq = (len + 127) >> 7;
+  const int i0 = p.causal ? kt : 0;
+  const int per = hd->found ? nq - i0 : 0;  // query tiles a head
+  const int total = per * p.group;
+
+  if (warp == kTmaWarp && total > 0) {
+    const HeadAt hk = head_at(kvh, p.hk);
+    Flight fl;
+    uint32_t tail_phase = 0;
+    bool ok = true, skip = p.fault_skip != 0;
+    if (lane == 0) {
+      prefetch_tmap(&p.mapQ);
+      prefetch_tmap(&p.mapO);
+      if (!skip) {
+        mbar_arrive_expect_tx(bar(L::kvfull), 2 * L::kTile);
+        fl.note(L::kvfull, 0);
+        load_tile<DP>(smem_addr(sK), &p.mapK, bar(L::kvfull), start + 128 * kt, hk);
+        load_tile<DP>(smem_addr(sV), &p.mapV, bar(L::kvfull), start + 128 * kt, hk);
+      }
+    }
+    for (int it = 0; ok && it < total; ++it) {
+      const int st = it % L::kStages;
+      const uint32_t ph = (it / L::kStages) & 1;
+      const HeadAt hq = head_at(kvh * p.group + it / per, p.hq);
+      const int i = i0 + it % per;
+      if (lane == 0) ok = wait_bounded(bar(L::empty + st), ph ^ 1u, w);
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+      if (!ok) break;
+      if (128 * i + 128 > len && start + len < p.T) {
+        ok = load_tail<DP>(sQ + st * L::kTile, &p.mapQ, bar(L::qfull + st), bar(L::tail), tail_phase,
+                           start + 128 * i, hq, len - 128 * i, lane, w);
+        ok = ok && load_tail<DP>(sO + st * L::kTile, &p.mapO, bar(L::ofull + st), bar(L::tail), tail_phase,
+                                 start + 128 * i, hq, len - 128 * i, lane, w);
+      } else if (lane == 0) {
+        mbar_arrive_expect_tx(bar(L::qfull + st), L::kTile);
+        fl.note(L::qfull + st, ph);
+        load_tile<DP>(smem_addr(sQ + st * L::kTile), &p.mapQ, bar(L::qfull + st), start + 128 * i, hq);
+        mbar_arrive_expect_tx(bar(L::ofull + st), L::kTile);
+        fl.note(L::ofull + st, ph);
+        load_tile<DP>(smem_addr(sO + st * L::kTile), &p.mapO, bar(L::ofull + st), start + 128 * i, hq);
+      }
+    }
+    if (lane == 0 && *w.abort_flag) fl.drain(bar0, p.wait_limit_ns);
+    __syncwarp();
+  } else if (warp == kMmaWarp && lane == 0 && total > 0) {
+    const int ksteps = (p.d + 15) >> 4;
+    const uint32_t idesc_out = idesc_bf16(0, 1, ksteps * 16);
+    bool ok = true, issued = false;
+    auto scores = [&](int it) {
+      mma_scores<DP>(tS, smem_addr(sK), smem_addr(sQ + (it % L::kStages) * L::kTile), ksteps);
+      issued = true;
+      mma_commit(bar(L::sfull));
+    };
+    auto dprobs = [&](int it) {
+      mma_scores<DP>(tP, smem_addr(sV), smem_addr(sO + (it % L::kStages) * L::kTile), ksteps);
+      mma_commit(bar(L::dpfull));
+    };
+    ok = wait_bounded(bar(L::kvfull), 0, w) && wait_bounded(bar(L::qfull), 0, w);
+    if (ok) {
+      tc_fence_after();
+      scores(0);
+      ok = wait_bounded(bar(L::ofull), 0, w);
+    }
+    if (ok) {
+      tc_fence_after();
+      dprobs(0);
+    }
+    for (int it = 0; ok && it < total; ++it) {
+      const int st = it % L::kStages, sn = (it + 1) % L::kStages;
+      const uint32_t pn = ((it + 1) / L::kStages) & 1;
+      const bool more = it + 1 < total;
+      if (!(ok = wait_bounded(bar(L::pready), it & 1, w))) break;
+      tc_fence_after();
+      mma_rows(tdV, tS, 64, smem_addr(sO + st * L::kTile), idesc_out, it > 0);
+      if (more) {
+        if (!(ok = wait_bounded(bar(L::qfull + sn), pn, w))) break;
+        tc_fence_after();
+        scores(it + 1);
+      }
+      if (!(ok = wait_bounded(bar(L::dsready), it & 1, w))) break;
+      tc_fence_after();
+      mma_rows(tdK, tP, 64, smem_addr(sQ + st * L::kTile), idesc_out, it > 0);
+      mma_commit(bar(L::empty + st));
+      if (more) {
+        if (!(ok = wait_bounded(bar(L::ofull + sn), pn, w))) break;
+        tc_fence_after();
+        dprobs(it + 1);
+      } else {
+        mma_commit(bar(L::done));
+      }
+    }
+    if (*w.abort_flag && issued) drain_mma(bar(L::drain), p.wait_limit_ns);
+  } else if (warp < 8 && total > 0) {
+    const int half = warp >> 2;              // the 64 query columns of this warp
+    const int wt = threadIdx.x & 127;        // thread of its warpgroup
+    const int key = (warp & 3) * 32 + lane;  // row of the transposed tile
+    const uint32_t lb = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const float sl2 = p.scale_log2;
+    // After a failed wait the loop runs on without waiting: the named barriers
+    // below need every warp, and nothing is stored at the end.
+    bool ok = true;
+    int table_head = -1;
+    // (lse log2 e, D) of a query: component wt / 64 of column wt % 64
+    auto fetch = [&](int it) {
+      const int pos = 128 * (i0 + it % per) + 64 * half + (wt & 63);
+      if (it >= total || pos >= len) return wt < 64 ? INFINITY : 0.f;  // 2^(x - inf) = 0
+      const int64_t at = static_cast<int64_t>(kvh * p.group + it / per) * p.T + start + pos;
+      return wt < 64 ? p.lse[at] * kLog2e : p.D[at];
+    };
+    float next = fetch(0);
+    for (int it = 0; it < total; ++it) {
+      const int i = i0 + it % per;
+      float* v = reinterpret_cast<float*>(vec + (it & 1) * 128 + half * 64);
+      v[2 * (wt & 63) + (wt >> 6)] = next;
+      if (BIAS && table_head != kvh * p.group + it / per) {
+        // the next query head's bias; both warpgroups share the table
+        table_head = kvh * p.group + it / per;
+        named_bar(3, 256);
+        const int md = p.bias.md, n = table_floats(md);
+        for (int x = threadIdx.x; x < n; x += 256) {
+          const int delta = min(max(x - (md + kPad), -md), md);
+          tab[x] = __ldg(p.table + static_cast<int64_t>(bucket_of(p.bias, delta)) * p.H + table_head) * kLog2e;
+        }
+        named_bar(3, 256);
+      }
+      named_bar(1 + half, 128);
+      next = fetch(it + 1);
+      const float4* v4 = reinterpret_cast<const float4*>(v);
+      ok = ok && wait_warp(bar(L::sfull), it & 1, w);
+      tc_fence_after();
+      uint32_t s[64];
+      tmem_ld32_issue(tS + lb + 64 * half, s);
+      tmem_ld32_issue(tS + lb + 64 * half + 32, s + 32);
+      tmem_ld32_wait(s);
+      tmem_ld32_wait(s + 32);
+      float add = 0.f;
+      bool near = false;
+      const float* tb = nullptr;
+      if (BIAS) {
+        const int side = bias_side(p.bias.md, 128 * i, 128 * kt);
+        near = side == 0;
+        if (!near) add = tab[side < 0 ? 0 : table_floats(p.bias.md) - 1];
+        // distance of column c: key - query = (128 kt + key) - (128 i + 64 half + c)
+        tb = tab + (128 * (kt - i) + key - 64 * half + p.bias.md + kPad);
+      }
+#pragma unroll
+      for (int c = 0; c < 64; c += 2) {
+        const float4 q = v4[c >> 1];  // (lse, D) of columns c and c + 1
+        float o0 = add - q.x, o1 = add - q.z;
+        if (BIAS && near) {
+          o0 = tb[-c] - q.x;
+          o1 = tb[-c - 1] - q.z;
+        }
+        s[c] = __float_as_uint(ex2_ftz(fmaf(as_f(s[c]), sl2, o0)));
+        s[c + 1] = __float_as_uint(ex2_ftz(fmaf(as_f(s[c + 1]), sl2, o1)));
+      }
+      if (p.causal && i == kt) {
+        const int first = key - 64 * half;  // the first query column that sees this key
+#pragma unroll
+        for (int c = 0; c < 64; ++c) s[c] = c >= first ? s[c] : 0u;
+      }
+      uint32_t pk[32];
+#pragma unroll
+      for (int c = 0; c < 32; ++c) pk[c] = pack_bf16x2(as_f(s[2 * c]), as_f(s[2 * c + 1]));
+      tmem_st32(tS + lb + 64 * half, pk);
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(L::pready));
+      ok = ok && wait_warp(bar(L::dpfull), it & 1, w);
+      tc_fence_after();
+      uint32_t g[64];
+      tmem_ld32_issue(tP + lb + 64 * half, g);
+      tmem_ld32_issue(tP + lb + 64 * half + 32, g + 32);
+      tmem_ld32_wait(g);
+      tmem_ld32_wait(g + 32);
+#pragma unroll
+      for (int c = 0; c < 64; c += 2) {
+        const float4 q = v4[c >> 1];
+        const float a = as_f(s[c]) * (as_f(g[c]) - q.y);
+        const float b = as_f(s[c + 1]) * (as_f(g[c + 1]) - q.w);
+        pk[c >> 1] = pack_bf16x2(a, b);
+      }
+      tmem_st32(tP + lb + 64 * half, pk);
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(L::dsready));
+    }
+    if (ok && wait_warp(bar(L::done), 0, w)) {
+      tc_fence_after();
+      // warps 0-3 store dV, warps 4-7 dK
+      const int pos = 128 * kt + key;
+      const HeadAt hk = head_at(kvh, p.hk);
+      const int64_t col = static_cast<int64_t>(hk.shard) * p.shard_w + static_cast<int64_t>(p.hq) * p.d +
+                          static_cast<int64_t>(hk.local + (half ? 0 : p.hk)) * p.d;
+      store_row((half ? tdK : tdV) + lb, p.d, half ? p.scale : 1.f,
+                static_cast<__nv_bfloat16*>(p.dQKV) + (static_cast<int64_t>(start) + pos) * p.ld_dqkv + col,
+                pos < len);
+    }
+  }
+  leave(hd);
+}
+
+template <int DP>
+struct DqShape {
+  static constexpr int kTile = DP / 64 * kPanel;
+  static constexpr int kStages = DP == 128 ? 2 : 4;  // K tiles and V tiles held, each
+  static constexpr int kSmem = 2 * kTile + 2 * kStages * kTile + kBarBytes + 1024;
+  static constexpr int qfull = 0, kfull = 1, vfull = kfull + kStages, tail = vfull + kStages, kempty = tail + 1,
+                       vempty = kempty + kStages, sfull = vempty + kStages, dpfull = sfull + 2, dsready = dpfull + 1,
+                       done = dsready + 1, drain = done + 1, count = drain + 1;
+  static_assert(count <= 40 && kempty <= 32, "barriers");
+};
+// The bias gradient's shared memory: per compute warp the sums of its 32 x 64
+// block by distance (95 of them), the CTA's sums by clamped distance, and the
+// threads' sums beyond the ends.
+constexpr int kDiag = 96;
+__host__ __device__ constexpr int grad_floats(int md) { return 8 * kDiag + 2 * md + 1 + 2 * 256; }
+
+template <int DP, bool BIAS>
+__global__ void __launch_bounds__(kThreads, 1) rc_dq_kernel(const __grid_constant__ RcParams p) {
+  using L = DqShape<DP>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = align1024(smem_raw);
+  uint8_t* sQ = smem;
+  uint8_t* sO = sQ + L::kTile;
+  uint8_t* sK = sO + L::kTile;
+  uint8_t* sV = sK + L::kStages * L::kTile;
+  Head* hd = reinterpret_cast<Head*>(sV + L::kStages * L::kTile);
+  float* tab = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(hd) + kBarBytes);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int head = static_cast<int>(blockIdx.x % p.H);
+  const int64_t unit = blockIdx.x / p.H;
+  enter(p, hd, L::count, [](int i) { return i == L::dsready ? 8u : 1u; }, unit, 128, p.causal != 0);
+  const bool grad = BIAS && p.partial != nullptr;
+  const int md = BIAS ? p.bias.md : 0;
+  float* diag = tab + (BIAS ? table_floats(md) : 0);  // [8][kDiag]
+  float* bins = diag + 8 * kDiag;                     // [2 md + 1]
+  float* ends = bins + 2 * md + 1;                    // [2][256]
+  if (BIAS) {
+    if (hd->found) fill_table(p, head, tab);
+    if (grad)
+      for (int i = threadIdx.x; i < 2 * md + 1; i += kThreads) bins[i] = 0.f;
+    __syncthreads();
+  }
+  const uint32_t bar0 = smem_addr(hd->bar);
+  auto bar = [&](int i) { return bar0 + 8u * i; };
+  const WaitCtx w{&hd->abort_flag, p.err, p.wait_limit_ns};
+  const uint32_t tmem = hd->tmem;
+  const uint32_t tP = tmem + 256, tdQ = tmem + 384;
+  const int start = hd->start, len = hd->len, r0 = 128 * hd->tile;
+  const int nk_all = (len + 127) >> 7;
+  const int nk = hd->found ? (p.causal ? min(nk_all, hd->tile + 1) : nk_all) : 0;
+
+  if (warp == kTmaWarp && nk > 0) {
+    const HeadAt hq = head_at(head, p.hq), hk = head_at(head / p.group, p.hk);
+    Flight fl;
+    uint32_t tail_phase = 0;
+    bool ok = true, skip = p.fault_skip != 0;
+    if (lane == 0) {
+      prefetch_tmap(&p.mapK);
+      prefetch_tmap(&p.mapV);
+      if (!skip) {
+        mbar_arrive_expect_tx(bar(L::qfull), 2 * L::kTile);
+        fl.note(L::qfull, 0);
+        load_tile<DP>(smem_addr(sQ), &p.mapQ, bar(L::qfull), start + r0, hq);
+        load_tile<DP>(smem_addr(sO), &p.mapO, bar(L::qfull), start + r0, hq);
+      }
+    }
+    for (int j = 0; ok && j < nk; ++j) {
+      const int st = j % L::kStages;
+      const uint32_t ph = (j / L::kStages) & 1;
+      if (lane == 0) ok = wait_bounded(bar(L::kempty + st), ph ^ 1u, w);
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+      if (!ok) break;
+      if (128 * j + 128 > len && start + len < p.T) {
+        ok = load_tail<DP>(sK + st * L::kTile, &p.mapK, bar(L::kfull + st), bar(L::tail), tail_phase,
+                           start + 128 * j, hk, len - 128 * j, lane, w);
+        if (!ok) break;
+      } else if (lane == 0) {
+        mbar_arrive_expect_tx(bar(L::kfull + st), L::kTile);
+        fl.note(L::kfull + st, ph);
+        load_tile<DP>(smem_addr(sK + st * L::kTile), &p.mapK, bar(L::kfull + st), start + 128 * j, hk);
+      }
+      if (lane == 0) {
+        ok = wait_bounded(bar(L::vempty + st), ph ^ 1u, w);
+        if (ok) {
+          mbar_arrive_expect_tx(bar(L::vfull + st), L::kTile);
+          fl.note(L::vfull + st, ph);
+          load_tile<DP>(smem_addr(sV + st * L::kTile), &p.mapV, bar(L::vfull + st), start + 128 * j, hk);
+        }
+      }
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+    }
+    if (lane == 0 && *w.abort_flag) fl.drain(bar0, p.wait_limit_ns);
+    __syncwarp();
+  } else if (warp == kMmaWarp && lane == 0 && nk > 0) {
+    const int ksteps = (p.d + 15) >> 4;
+    const uint32_t idesc_out = idesc_bf16(0, 1, ksteps * 16);
+    bool ok = true, issued = false;
+    auto scores = [&](int j) {
+      mma_scores<DP>(tmem + 128 * (j & 1), smem_addr(sQ), smem_addr(sK + (j % L::kStages) * L::kTile), ksteps);
+      issued = true;
+      mma_commit(bar(L::sfull + (j & 1)));
+    };
+    auto dprobs = [&](int j) {
+      mma_scores<DP>(tP, smem_addr(sO), smem_addr(sV + (j % L::kStages) * L::kTile), ksteps);
+      mma_commit(bar(L::dpfull));
+      mma_commit(bar(L::vempty + j % L::kStages));
+    };
+    ok = wait_bounded(bar(L::qfull), 0, w) && wait_bounded(bar(L::kfull), 0, w);
+    if (ok) {
+      tc_fence_after();
+      scores(0);
+      ok = wait_bounded(bar(L::vfull), 0, w);
+    }
+    if (ok) {
+      tc_fence_after();
+      dprobs(0);
+    }
+    for (int j = 0; ok && j < nk; ++j) {
+      const int st = j % L::kStages, sn = (j + 1) % L::kStages;
+      const uint32_t pn = ((j + 1) / L::kStages) & 1;
+      const bool more = j + 1 < nk;
+      if (more) {
+        // into the other score buffer: dS of tile j - 1 there has been read by
+        // its product, issued before
+        if (!(ok = wait_bounded(bar(L::kfull + sn), pn, w))) break;
+        tc_fence_after();
+        scores(j + 1);
+      }
+      if (!(ok = wait_bounded(bar(L::dsready), j & 1, w))) break;
+      tc_fence_after();
+      mma_rows(tdQ, tmem + 128 * (j & 1), 64, smem_addr(sK + st * L::kTile), idesc_out, j > 0);
+      mma_commit(bar(L::kempty + st));
+      if (more) {
+        if (!(ok = wait_bounded(bar(L::vfull + sn), pn, w))) break;
+        tc_fence_after();
+        dprobs(j + 1);
+      } else {
+        mma_commit(bar(L::done));
+      }
+    }
+    if (*w.abort_flag && issued) drain_mma(bar(L::drain), p.wait_limit_ns);
+  } else if (warp < 8) {
+    const int half = warp >> 2;
+    const int quarter = warp & 3;
+    const int row = r0 + quarter * 32 + lane;
+    const bool mine = row < len;
+    const int64_t token = static_cast<int64_t>(start) + row;
+    const uint32_t lb = static_cast<uint32_t>(quarter * 32) << 16;
+    const float sl2 = p.scale_log2;
+    float lse2 = 0.f, D = 0.f;
+    if (nk > 0 && mine) {
+      lse2 = p.lse[static_cast<int64_t>(head) * p.T + token] * kLog2e;
+      D = p.D[static_cast<int64_t>(head) * p.T + token];
+    }
+    float end_lo = 0.f, end_hi = 0.f;  // dS at distances <= -md and >= md
+    // After a failed wait the loop runs on without waiting: the named barriers
+    // below need every warp, and nothing of the gradient is stored.
+    bool ok = true;
+    for (int j = 0; j < nk; ++j) {
+      const uint32_t tS = tmem + 128 * (j & 1) + lb + 64 * half;
+      const int c0 = 128 * j + 64 * half;  // key position of this warp's first column
+      ok = ok && wait_warp(bar(L::sfull + (j & 1)), (j >> 1) & 1, w);
+      tc_fence_after();
+      uint32_t s[64];
+      tmem_ld32_issue(tS, s);
+      tmem_ld32_issue(tS + 32, s + 32);
+      tmem_ld32_wait(s);
+      tmem_ld32_wait(s + 32);
+      int side = 0;
+      float off = -lse2;
+      if (BIAS) {
+        side = bias_side(md, r0, 128 * j);
+        if (side != 0) {
+          off += tab[side < 0 ? 0 : table_floats(md) - 1];
+        } else {
+          const float* tb = tab + (c0 - row + md + kPad);
+#pragma unroll
+          for (int c = 0; c < 64; ++c) s[c] = __float_as_uint(ex2_ftz(fmaf(as_f(s[c]), sl2, tb[c] + off)));
+        }
+      }
+      if (!BIAS || side != 0) {
+#pragma unroll
+        for (int c = 0; c < 64; ++c) s[c] = __float_as_uint(ex2_ftz(fmaf(as_f(s[c]), sl2, off)));
+      }
+      const bool masked = (p.causal && 128 * j + 127 > r0) || 128 * j + 128 > len;
+      ok = ok && wait_warp(bar(L::dpfull), j & 1, w);
+      tc_fence_after();
+      uint32_t g[64];
+      tmem_ld32_issue(tP + lb + 64 * half, g);
+      tmem_ld32_issue(tP + lb + 64 * half + 32, g + 32);
+      tmem_ld32_wait(g);
+      tmem_ld32_wait(g + 32);
+#pragma unroll
+      for (int c = 0; c < 64; ++c) s[c] = __float_as_uint(as_f(s[c]) * (as_f(g[c]) - D));
+      if (masked) {
+        const int seen = (p.causal ? min(len, row + 1) : len) - c0;
+#pragma unroll
+        for (int c = 0; c < 64; ++c) s[c] = c < seen ? s[c] : 0u;
+      }
+      uint32_t pk[32];
+#pragma unroll
+      for (int c = 0; c < 32; ++c) pk[c] = pack_bf16x2(as_f(s[2 * c]), as_f(s[2 * c + 1]));
+      tmem_st32(tS, pk);
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(L::dsready));
+      if (BIAS && grad) {
+        if (side != 0) {
+          float a[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int c = 0; c < 64; ++c) a[c & 3] += as_f(s[c]);
+          const float sum = mine ? (a[0] + a[1]) + (a[2] + a[3]) : 0.f;
+          if (side < 0) end_lo += sum;
+          else end_hi += sum;
+        } else {
+          // Sums along the diagonals of the warp's 32 x 64 block: the running
+          // sum of a diagonal moves one lane up at every column; it is whole
+          // when it leaves lane 31.
+          float* dw = diag + warp * kDiag;
+          float acc = 0.f;
+#pragma unroll
+          for (int c = 0; c < 64; ++c) {
+            const float up = __shfl_up_sync(0xffffffffu, acc, 1);
+            acc = (lane == 0 ? 0.f : up) + (mine ? as_f(s[c]) : 0.f);
+            if (lane == 31) dw[c] = acc;  // distance (c - 31) + block offset
+          }
+          if (lane < 31) dw[94 - lane] = acc;
+          named_bar(1, 256);
+          // thread x sums distance x - 127 of the tile over the warps' blocks
+          if (threadIdx.x < 255) {
+            const int dt = static_cast<int>(threadIdx.x) - 127;
+            float sum = 0.f;
+#pragma unroll
+            for (int wv = 0; wv < 8; ++wv) {
+              const int at = dt - 64 * (wv >> 2) + 32 * (wv & 3) + 31;
+              if (at >= 0 && at < 95) sum += diag[wv * kDiag + at];
+            }
+            const int delta = 128 * j - r0 + dt;
+            if (delta <= -md) end_lo += sum;
+            else if (delta >= md) end_hi += sum;
+            else bins[delta + md] += sum;
+          }
+          named_bar(1, 256);
+        }
+      }
+    }
+    if (nk > 0 && ok && wait_warp(bar(L::done), 0, w)) {
+      tc_fence_after();
+      // each half of the warps stores half of the columns
+      const int cut = min(p.d, 32 * ((p.d + 63) / 64));
+      const int first = half ? cut : 0, n = half ? p.d - cut : cut;
+      const HeadAt hq = head_at(head, p.hq);
+      store_row(tdQ + lb + first, n, p.scale,
+                static_cast<__nv_bfloat16*>(p.dQKV) + token * p.ld_dqkv +
+                    static_cast<int64_t>(hq.shard) * p.shard_w + static_cast<int64_t>(hq.local) * p.d + first,
+                mine);
+    }
+    if (BIAS && grad) {
+      // the CTA's sums by bucket, in a fixed order
+      ends[threadIdx.x] = end_lo;
+      ends[256 + threadIdx.x] = end_hi;
+      named_bar(1, 256);
+      if (warp < 2) {
+        float a = 0.f;
+        for (int x = lane; x < 256; x += 32) a += ends[256 * warp + x];
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
+        if (lane == 0) bins[warp ? 2 * md : 0] = a;
+      }
+      named_bar(1, 256);
+      for (int u = threadIdx.x; u < p.bias.nb; u += 256) {
+        // bucket u holds the distances n with first[k] <= n < first[k + 1] on its side
+        const int k = u % p.bias.side;
+        const bool pos = p.bias.both && u >= p.bias.side;
+        const int lo = p.bias.first[k], hi = k + 1 < p.bias.side ? p.bias.first[k + 1] : md + 1;
+        float a = 0.f;
+        for (int n = max(lo, pos ? 1 : 0); n < min(hi, md + 1); ++n) a += bins[md + (pos ? n : -n)];
+        if (!p.bias.both && k == 0)
+          for (int n = 1; n <= md; ++n) a += bins[md + n];  // keys behind the query count as distance 0
+        p.partial[(unit * p.H + head) * p.bias.nb + u] = a;
+      }
+    }
+  }
+  leave(hd);
+}
+
+// dtable[u, h] (+)= the sum over the units' partial sums, in a fixed order: one
+// block a head and bucket.
+__global__ void __launch_bounds__(128) rc_bias_sum_kernel(const __grid_constant__ RcParams p, int64_t units) {
+  pdl_wait();
+  pdl_trigger();
+  const int h = blockIdx.x, u = blockIdx.y;
+  double a = 0.0;
+  for (int64_t i = threadIdx.x; i < units; i += 128) a += p.partial[(i * p.H + h) * p.bias.nb + u];
+  __shared__ double red[128];
+  red[threadIdx.x] = a;
+  __syncthreads();
+  for (int o = 64; o > 0; o >>= 1) {
+    if (threadIdx.x < o) red[threadIdx.x] += red[threadIdx.x + o];
+    __syncthreads();
+  }
+  if (threadIdx.x == 0) {
+    float* out = p.dtable + static_cast<int64_t>(u) * p.H + h;
+    *out = static_cast<float>(red[0] + (p.accumulate ? static_cast<double>(*out) : 0.0));
+  }
+}
+
+template <class K>
+cudaError_t launch_rc(K kernel, int64_t blocks, int smem, const RcParams& p, cudaStream_t st) {
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  launch_k(kernel, dim3(static_cast<unsigned>(blocks)), dim3(kThreads), smem, st, p);
+  count_launches(1);
+  return cudaGetLastError();
+}
+
+// Runs of `rows` tokens: exactly, or for sequences that only the device knows
+// an upper bound (each adds at most one run that is not full).
+int64_t units_of(const RcParams& p, int rows) {
+  if (p.seq_starts == nullptr) return static_cast<int64_t>(p.b) * ((p.s + rows - 1) / rows);
+  return p.T / rows + p.b;
+}
+
+template <int DP, bool BIAS>
+cudaError_t fwd_t(RcParams& p, int num_sms, cudaStream_t st) {
+  // Two query tiles a CTA where that still fills the SMs: their softmax and
+  // products overlap, and K/V tiles are read once for both.
+  p.sub = units_of(p, 256) * p.H >= num_sms ? 2 : 1;
+  const int smem = FwdShape<DP>::kSmem + (BIAS ? 4 * table_floats(p.bias.md) : 0);
+  return launch_rc(rc_fwd_kernel<DP, BIAS>, units_of(p, 128 * p.sub) * p.H, smem, p, st);
+}
+template <int DP, bool BIAS>
+cudaError_t bwd_t(RcParams& p, cudaStream_t st) {
+  const int64_t units = units_of(p, 128);
+  const int tab = BIAS ? 4 * table_floats(p.bias.md) : 0;
+  cudaError_t e = launch_rc(rc_dkv_kernel<DP, BIAS>, units * p.KV, DkvShape<DP>::kSmem + tab, p, st);
+  p.fault_skip = 0;
+  if (e != cudaSuccess) return e;
+  e = launch_rc(rc_dq_kernel<DP, BIAS>, units * p.H,
+                DqShape<DP>::kSmem + tab + (BIAS ? 4 * grad_floats(p.bias.md) : 0), p, st);
+  if (e != cudaSuccess || !BIAS || p.partial == nullptr) return e;
+  launch_k(rc_bias_sum_kernel, dim3(p.H, p.bias.nb), dim3(128), 0, st, p, units);
+  count_launches(1);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+size_t rc_dot_bytes(int64_t T, int H) { return (static_cast<size_t>(T) * H * 4 + 255) / 256 * 256; }
+size_t rc_partial_bytes(const RcParams& p) {
+  return static_cast<size_t>(p.T / 128 + p.b) * p.H * p.bias.nb * 4;  // units_of of any sequences
+}
+
+cudaError_t launch_rc_fwd(RcParams& p, int num_sms, cudaStream_t st) {
+  if (p.d <= 64) return p.bias.nb ? fwd_t<64, true>(p, num_sms, st) : fwd_t<64, false>(p, num_sms, st);
+  return p.bias.nb ? fwd_t<128, true>(p, num_sms, st) : fwd_t<128, false>(p, num_sms, st);
+}
+
+cudaError_t launch_rc_bwd(RcParams& p, int num_sms, cudaStream_t st) {
+  int lg = 0;
+  while (8 << lg < p.d) ++lg;
+  const int64_t blocks = (((p.T * p.H) << lg) + 255) / 256;
+  launch_k(rc_dot_kernel, dim3(static_cast<unsigned>(blocks < 16ll * num_sms ? blocks : 16ll * num_sms)), dim3(256), 0, st, p, lg);
+  count_launches(1);
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  if (p.d <= 64) return p.bias.nb ? bwd_t<64, true>(p, st) : bwd_t<64, false>(p, st);
+  return p.bias.nb ? bwd_t<128, true>(p, st) : bwd_t<128, false>(p, st);
+}
+
+}  // namespace tp

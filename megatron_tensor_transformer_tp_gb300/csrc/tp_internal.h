@@ -19,6 +19,7 @@ constexpr int kMaxRanges = 64;    // vocabulary ranges
 
 // Error bits of the device error word.
 constexpr unsigned kErrTimeout = 1u;
+constexpr unsigned kErrInvalid = 2u;  // sequence starts in device memory decrease or leave the buffer
 
 // Epilogue kinds of the GEMM engines.
 enum Epi : int {
@@ -183,6 +184,45 @@ cudaError_t launch_attn_norm(const void* part, int P, int64_t s, int64_t pairs, 
                              uint64_t stream0, int n_heads, int heads_per_shard, cudaStream_t st);
 cudaError_t launch_attn_rowdot(const void* C, const void* dC, int64_t h, int64_t s, int n_heads, int d,
                                int64_t pairs, float* D, cudaStream_t st);
+
+// Attention without stored probabilities (tp_attn_rc.cu).
+constexpr int kMaxRelBuckets = 256;
+constexpr int kMaxRelDistance = 1024;
+struct RcBias {
+  int nb;     // buckets, 0 = no bias
+  int md;     // distances of md and more share the last bucket
+  int both;   // keys behind and ahead of the query have buckets of their own
+  int side;   // buckets of one side: nb / 2 with `both`, else nb
+  int first[kMaxRelBuckets];  // smallest distance of a side's bucket k
+};
+struct RcParams {
+  CUtensorMap mapQ, mapK, mapV, mapO;  // 4D (d, token, head of the shard, shard); mapO: dC
+  const int64_t* seq_starts;           // device, b + 1 values, or null: b sequences of s tokens
+  int64_t T, ld_c, ld_dc, ld_dqkv;
+  int b, s, H, KV, d, causal;
+  int group;    // query heads a K/V head
+  int hq, hk;   // query and K/V heads a shard
+  int shard_w;  // columns of one shard in QKV
+  int sub;      // query tiles a CTA (forward; set by the launcher)
+  float scale, scale_log2;
+  void* C;          // forward out, backward in
+  float* lse;       // forward out, backward in; (H, T)
+  const void* dC;
+  float* D;         // (H, T) scratch
+  void* dQKV;
+  RcBias bias;
+  const float* table;  // (nb, H)
+  float* dtable;
+  float* partial;      // (units, H, nb) scratch, or null: no bias gradient
+  int accumulate;
+  int fault_skip;
+  unsigned* err;
+  unsigned long long wait_limit_ns;
+};
+size_t rc_dot_bytes(int64_t T, int H);
+size_t rc_partial_bytes(const RcParams& p);
+cudaError_t launch_rc_fwd(RcParams& p, int num_sms, cudaStream_t st);
+cudaError_t launch_rc_bwd(RcParams& p, int num_sms, cudaStream_t st);
 
 // Transformer-layer row kernels (LayerNorm, dropout + residual, attention
 // dropout bits).  Dropout keeps element e iff its 16-bit Philox4x32-10 field is >=

@@ -382,6 +382,127 @@ def attention_core_grad(QKV, P, dC, s, n_heads, N, p_attn=0.0, seed=0, layer=0):
     return dQKV
 
 
+# --------------------------------------------------------------------------
+# Attention from log-sum-exps, shared key/value heads, relative position bias
+# --------------------------------------------------------------------------
+def relative_bucket(rel, num_buckets, max_distance, bidirectional):
+    """Bucket of one distance rel = key - query, in whole numbers only: with B
+    buckets a side, E = B // 2 and distance n, n itself below E, else
+    min(B - 1, E + j) for the largest j with (n / E)^(B-E) >= (max_distance / E)^j.
+    Pinned by: the logarithm's formula in 60-digit decimals, a hand-made
+    table, monotony and the ends."""
+    B, add, n = num_buckets, 0, max(-rel, 0)
+    if bidirectional:
+        B //= 2
+        add, n = (B if rel > 0 else 0), abs(rel)
+    E = B // 2
+    if n < E:
+        return add + n
+    K, j = B - E, 0
+    while j + 1 < K and n ** K * E ** (j + 1) >= max_distance ** (j + 1) * E ** K:
+        j += 1
+    return add + E + j
+
+
+def relative_buckets(s, num_buckets, max_distance, bidirectional):
+    """(s, s) bucket of key j seen from query i.  Pinned through ``relative_bucket``."""
+    line = np.array([relative_bucket(r, num_buckets, max_distance, bidirectional) for r in range(-s + 1, s)])
+    i = np.arange(s)
+    return line[i[None, :] - i[:, None] + s - 1]
+
+
+def grouped_head_columns(d, n_heads, n_kv_heads, N, j):
+    """Columns of query head j and of its key/value head in the shard-major
+    QKV (shard i holds [Q_i K_i V_i], heads in order): (q, k, v).
+    Pinned by: ``attention_head_columns`` where every head has its own
+    key/value head, and a hand-made layout of two shards."""
+    hq, hk = n_heads // N, n_kv_heads // N
+    g = j // (n_heads // n_kv_heads)
+    base = lambda shard: shard * (hq + 2 * hk) * d  # noqa: E731
+    return (base(j // hq) + (j % hq) * d, base(g // hk) + (hq + g % hk) * d,
+            base(g // hk) + (hq + hk + g % hk) * d)
+
+
+def _masked_scores(q, k, scale, causal, bias):
+    S = scale * (q @ k.T)
+    if bias is not None:
+        S = S + bias
+    return np.where(np.tril(np.ones(S.shape, dtype=bool)), S, -np.inf) if causal else S
+
+
+def attention_lse(QKV, starts, cfg, bias=None, table=None):
+    """Attention of the sequences rows starts[i] .. starts[i+1] - 1 of the
+    shard-major QKV: x = scale q k^T (+ table[bucket, head]), lse the
+    log-sum-exp of a row over the keys it sees, C = exp(x - lse) v.  cfg: dict
+    with n_heads, n_kv_heads, d, N, causal, scale (0: 1 / sqrt(d)).
+    Returns (C (T, n_heads d), lse (n_heads, T), A (T, n_heads d)) with A = the
+    same sum over |v| (the scale of rounding errors); rows of no sequence are 0.
+    Pinned by: ``attention_core`` (own key/value heads, no bias), torch
+    scaled_dot_product_attention with an additive mask in float64."""
+    H, d = cfg["n_heads"], cfg["d"]
+    scale = cfg.get("scale") or 1.0 / math.sqrt(d)
+    T = QKV.shape[0]
+    C, A, lse = np.zeros((T, H * d)), np.zeros((T, H * d)), np.zeros((H, T))
+    for a, e in zip(starts[:-1], starts[1:]):
+        if e == a:
+            continue
+        bk = None if bias is None else relative_buckets(e - a, **bias)
+        for j in range(H):
+            qc, kc, vc = grouped_head_columns(d, H, cfg["n_kv_heads"], cfg["N"], j)
+            q, k, v = (QKV[a:e, c:c + d] for c in (qc, kc, vc))
+            S = _masked_scores(q, k, scale, cfg["causal"], None if bk is None else table[bk, j])
+            m = S.max(axis=1, keepdims=True)
+            E = np.exp(S - m)
+            z = E.sum(axis=1, keepdims=True)
+            lse[j, a:e] = (m + np.log(z))[:, 0]
+            C[a:e, j * d:(j + 1) * d] = (E / z) @ v
+            A[a:e, j * d:(j + 1) * d] = (E / z) @ np.abs(v)
+    return C, lse, A
+
+
+def attention_lse_grad(QKV, starts, cfg, C, lse, dC, bias=None, table=None, e_p=0.0, e_d=0.0):
+    """Gradient of ``attention_lse`` given its C and lse and the context
+    gradient: P = exp(x - lse), D = rowsum(dC C), dS = P (dC v^T - D),
+    dq = scale dS k, dk = scale dS^T q and dv = P^T dC summed over the query
+    heads of a key/value head, dtable[u, j] = sum of dS over bucket u.
+    Returns (dQKV, dtable or None, E_QKV, E_table): the E are first-order
+    bounds of what errors make of them, where P and dS are off by e_p of
+    themselves and dC v^T and D by e_d of their sums of magnitudes (the
+    table's sums see e_p through E_table's own factor, taken as given).
+    Pinned by: torch autograd in float64 through the same attention, and
+    ``attention_core_grad``."""
+    H, d = cfg["n_heads"], cfg["d"]
+    scale = cfg.get("scale") or 1.0 / math.sqrt(d)
+    dX, EX = np.zeros(QKV.shape), np.zeros(QKV.shape)
+    dT = ET = None
+    if bias is not None:
+        dT, ET = np.zeros(table.shape), np.zeros(table.shape)
+    for a, e in zip(starts[:-1], starts[1:]):
+        if e == a:
+            continue
+        bk = None if bias is None else relative_buckets(e - a, **bias)
+        for j in range(H):
+            qc, kc, vc = grouped_head_columns(d, H, cfg["n_kv_heads"], cfg["N"], j)
+            q, k, v = (QKV[a:e, c:c + d] for c in (qc, kc, vc))
+            g, o = dC[a:e, j * d:(j + 1) * d], C[a:e, j * d:(j + 1) * d]
+            S = _masked_scores(q, k, scale, cfg["causal"], None if bk is None else table[bk, j])
+            P = np.exp(S - lse[j, a:e, None])
+            dS = P * (g @ v.T - np.sum(g * o, axis=1, keepdims=True))
+            off = P * e_d * (np.abs(g) @ np.abs(v).T + np.sum(np.abs(g * o), axis=1, keepdims=True))
+            EdS = off + e_p * np.abs(dS)
+            dX[a:e, qc:qc + d] += scale * (dS @ k)
+            dX[a:e, kc:kc + d] += scale * (dS.T @ q)
+            dX[a:e, vc:vc + d] += P.T @ g
+            EX[a:e, qc:qc + d] += scale * (EdS @ np.abs(k))
+            EX[a:e, kc:kc + d] += scale * (EdS.T @ np.abs(q))
+            EX[a:e, vc:vc + d] += e_p * (P.T @ np.abs(g))
+            if bk is not None:
+                n = table.shape[0]
+                dT[:, j] += np.bincount(bk.ravel(), weights=dS.ravel(), minlength=n)
+                ET[:, j] += np.bincount(bk.ravel(), weights=(off + np.abs(dS) * e_d).ravel(), minlength=n)
+    return dX, dT, EX, ET
+
+
 def vocab_mask(ids, start, end):
     """Mask and shift of one vocabulary range.
 
