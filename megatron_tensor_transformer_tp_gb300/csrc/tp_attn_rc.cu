@@ -266,20 +266,39 @@ __device__ __forceinline__ bool load_tail(uint8_t* smem_tile, const CUtensorMap*
   return true;
 }
 
+// The MMA warp runs its loop as a whole warp and one elected lane issues: the
+// descriptors are then warp-uniform values.  Issued from a branch that only
+// lane 0 takes, each 128 x 128 x 16 product cost 75 to 160 cycles of issue for
+// its 64 cycles of work.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok));
+  return ok != 0;
+}
+__device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
+
 // S = A B^T over the head width: both K-major in shared memory, 128 x 128.
-// A counted loop: unrolled with a condition around each issue, the compiled
-// code added the first product to what TMEM held before.
+template <int KSTEPS>
+__device__ __forceinline__ void mma_scores_k(uint32_t d_tmem, uint64_t ad, uint64_t bd, uint32_t idesc) {
+#pragma unroll
+  for (int kk = 0; kk < KSTEPS; ++kk) {
+    const uint32_t off = ((kk >> 2) * kPanel + (kk & 3) * 32) >> 4;
+    mma_bf16(d_tmem, ad + off, bd + off, idesc, kk > 0);
+  }
+}
 template <int DP>
 __device__ __forceinline__ void mma_scores(uint32_t d_tmem, uint32_t a, uint32_t b, int ksteps) {
   const uint64_t ad = sdesc(a, 16, 1024), bd = sdesc(b, 16, 1024);
   const uint32_t idesc = idesc_bf16(0, 0, 128);
-  uint32_t acc = 0;
-#pragma unroll 1
-  for (int kk = 0; kk < ksteps; ++kk) {
-    const uint32_t off = static_cast<uint32_t>((kk >> 2) * kPanel + (kk & 3) * 32) >> 4;
-    mma_bf16(d_tmem, ad + off, bd + off, idesc, acc);
-    acc = 1;
-  }
+  constexpr int K0 = DP == 128 ? 4 : 0;
+  if (ksteps == K0 + 4) mma_scores_k<K0 + 4>(d_tmem, ad, bd, idesc);
+  else if (ksteps == K0 + 3) mma_scores_k<K0 + 3>(d_tmem, ad, bd, idesc);
+  else if (ksteps == K0 + 2) mma_scores_k<K0 + 2>(d_tmem, ad, bd, idesc);
+  else mma_scores_k<K0 + 1>(d_tmem, ad, bd, idesc);
 }
 // D (+)= A B: A 128 x 128 bf16 in TMEM, B = 128 rows of a tile as stored
 // (contraction over its rows).  a_half: TMEM columns between the two halves of
@@ -425,7 +444,7 @@ __global__ void __launch_bounds__(kThreads, 1) rc_fwd_kernel(const __grid_consta
   uint8_t* sV = sK + L::kStages * L::kTile;
   Head* hd = reinterpret_cast<Head*>(sV + L::kStages * L::kTile);
   float* tab = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(hd) + kBarBytes);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
   const int head = static_cast<int>(blockIdx.x % p.H);
   const int nsub = p.sub;
   enter(p, hd, L::count, [](int i) { return i >= L::pfull && i < L::pfull + 2 ? 4u : 1u; }, blockIdx.x / p.H,
@@ -435,13 +454,14 @@ __global__ void __launch_bounds__(kThreads, 1) rc_fwd_kernel(const __grid_consta
   const uint32_t bar0 = smem_addr(hd->bar);
   auto bar = [&](int i) { return bar0 + 8u * i; };
   const WaitCtx w{&hd->abort_flag, p.err, p.wait_limit_ns};
-  const uint32_t tmem = hd->tmem;
-  const int start = hd->start, len = hd->len, row0 = hd->tile * 128 * nsub;
+  const uint32_t tmem = uniform(hd->tmem);
+  const bool found = uniform(hd->found);
+  const int start = uniform(hd->start), len = uniform(hd->len), row0 = uniform(hd->tile) * 128 * nsub;
   const int nk_all = (len + 127) >> 7;
   // key tiles of the CTA's query tile t (0: there is none)
   auto tiles_of = [&](int t) {
     const int r = row0 + 128 * t;
-    if (!hd->found || t >= nsub || r >= len) return 0;
+    if (!found || t >= nsub || r >= len) return 0;
     return p.causal ? min(nk_all, (r >> 7) + 1) : nk_all;
   };
   const int n0 = tiles_of(0), n1 = tiles_of(1), nmax = max(n0, n1);
@@ -489,21 +509,24 @@ __global__ void __launch_bounds__(kThreads, 1) rc_fwd_kernel(const __grid_consta
     }
     if (lane == 0 && *w.abort_flag) fl.drain(bar0, p.wait_limit_ns);
     __syncwarp();
-  } else if (warp == kMmaWarp && lane == 0 && nmax > 0) {
+  } else if (warp == kMmaWarp && nmax > 0) {
     const int ksteps = (p.d + 15) >> 4;
     const uint32_t idesc_pv = idesc_bf16(0, 1, ksteps * 16);
     const int last = n1 > 0 ? 1 : 0;  // the query tile that uses every key tile last
     bool ok = true, issued = false;
     auto scores = [&](int t, int j) {
-      mma_scores<DP>(tmem + 128 * t, smem_addr(sQ + t * L::kTile), smem_addr(sK + (j % L::kStages) * L::kTile),
-                     ksteps);
       issued = true;
-      mma_commit(bar(L::sfull + t));
-      if (t == last) mma_commit(bar(L::kempty + j % L::kStages));
+      if (elect_one()) {
+        mma_scores<DP>(tmem + 128 * t, smem_addr(sQ + t * L::kTile), smem_addr(sK + (j % L::kStages) * L::kTile),
+                       ksteps);
+        mma_commit(bar(L::sfull + t));
+        if (t == last) mma_commit(bar(L::kempty + j % L::kStages));
+      }
+      __syncwarp();
     };
-    ok = wait_bounded(bar(L::kfull), 0, w);
+    ok = wait_warp(bar(L::kfull), 0, w);
     for (int t = 0; ok && t <= last; ++t) {
-      ok = wait_bounded(bar(L::qfull + t), 0, w);
+      ok = wait_warp(bar(L::qfull + t), 0, w);
       if (ok) {
         tc_fence_after();
         scores(t, 0);
@@ -512,25 +535,26 @@ __global__ void __launch_bounds__(kThreads, 1) rc_fwd_kernel(const __grid_consta
     for (int j = 0; ok && j < nmax; ++j) {
       const int st = j % L::kStages;
       const uint32_t ph = (j / L::kStages) & 1;
-      ok = wait_bounded(bar(L::vfull + st), ph, w);
+      ok = wait_warp(bar(L::vfull + st), ph, w);
       for (int t = 0; ok && t <= last; ++t) {
         const int nt = t ? n1 : n0;
         if (j >= nt) continue;
-        if (!(ok = wait_bounded(bar(L::pfull + t), j & 1, w))) break;
+        if (!(ok = wait_warp(bar(L::pfull + t), j & 1, w))) break;
         tc_fence_after();
-        mma_rows(tmem + 256 + 128 * t, tmem + 128 * t, 32, smem_addr(sV + st * L::kTile), idesc_pv, j > 0);
-        issued = true;
-        if (t == last) mma_commit(bar(L::vempty + st));
+        if (elect_one()) {
+          mma_rows(tmem + 256 + 128 * t, tmem + 128 * t, 32, smem_addr(sV + st * L::kTile), idesc_pv, j > 0);
+          if (t == last) mma_commit(bar(L::vempty + st));
+          if (j + 1 >= nt) mma_commit(bar(L::odone + t));
+        }
+        __syncwarp();
         if (j + 1 < nt) {
           const int sn = (j + 1) % L::kStages;
-          if (!(ok = wait_bounded(bar(L::kfull + sn), ((j + 1) / L::kStages) & 1, w))) break;
+          if (!(ok = wait_warp(bar(L::kfull + sn), ((j + 1) / L::kStages) & 1, w))) break;
           scores(t, j + 1);
-        } else {
-          mma_commit(bar(L::odone + t));
         }
       }
     }
-    if (*w.abort_flag && issued) drain_mma(bar(L::drain), p.wait_limit_ns);
+    if (*w.abort_flag && issued && elect_one()) drain_mma(bar(L::drain), p.wait_limit_ns);
   } else if (warp < 8) {
     const int t = warp >> 2;
     const int nt = t ? n1 : n0;
@@ -685,19 +709,19 @@ __global__ void __launch_bounds__(kThreads, 1) rc_dkv_kernel(const __grid_consta
   Head* hd = reinterpret_cast<Head*>(sO + L::kStages * L::kTile);
   float2* vec = reinterpret_cast<float2*>(reinterpret_cast<uint8_t*>(hd) + kBarBytes);
   float* tab = reinterpret_cast<float*>(vec + 256);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
   const int kvh = static_cast<int>(blockIdx.x % p.KV);
   enter(p, hd, L::count, [](int i) { return i == L::pready || i == L::dsready ? 8u : 1u; }, blockIdx.x / p.KV, 128,
         false);
   const uint32_t bar0 = smem_addr(hd->bar);
   auto bar = [&](int i) { return bar0 + 8u * i; };
   const WaitCtx w{&hd->abort_flag, p.err, p.wait_limit_ns};
-  const uint32_t tmem = hd->tmem;
+  const uint32_t tmem = uniform(hd->tmem);
   const uint32_t tS = tmem, tP = tmem + 128, tdV = tmem + 256, tdK = tmem + 256 + DP;
-  const int start = hd->start, len = hd->len, kt = hd->tile;
+  const int start = uniform(hd->start), len = uniform(hd->len), kt = uniform(hd->tile);
   const int nq = (len + 127) >> 7;
   const int i0 = p.causal ? kt : 0;
-  const int per = hd->found ? nq - i0 : 0;  // query tiles a head
+  const int per = uniform(hd->found) ? nq - i0 : 0;  // query tiles a head
   const int total = per * p.group;
 
   if (warp == kTmaWarp && total > 0) {
@@ -739,24 +763,30 @@ __global__ void __launch_bounds__(kThreads, 1) rc_dkv_kernel(const __grid_consta
     }
     if (lane == 0 && *w.abort_flag) fl.drain(bar0, p.wait_limit_ns);
     __syncwarp();
-  } else if (warp == kMmaWarp && lane == 0 && total > 0) {
+  } else if (warp == kMmaWarp && total > 0) {
     const int ksteps = (p.d + 15) >> 4;
     const uint32_t idesc_out = idesc_bf16(0, 1, ksteps * 16);
     bool ok = true, issued = false;
     auto scores = [&](int it) {
-      mma_scores<DP>(tS, smem_addr(sK), smem_addr(sQ + (it % L::kStages) * L::kTile), ksteps);
       issued = true;
-      mma_commit(bar(L::sfull));
+      if (elect_one()) {
+        mma_scores<DP>(tS, smem_addr(sK), smem_addr(sQ + (it % L::kStages) * L::kTile), ksteps);
+        mma_commit(bar(L::sfull));
+      }
+      __syncwarp();
     };
     auto dprobs = [&](int it) {
-      mma_scores<DP>(tP, smem_addr(sV), smem_addr(sO + (it % L::kStages) * L::kTile), ksteps);
-      mma_commit(bar(L::dpfull));
+      if (elect_one()) {
+        mma_scores<DP>(tP, smem_addr(sV), smem_addr(sO + (it % L::kStages) * L::kTile), ksteps);
+        mma_commit(bar(L::dpfull));
+      }
+      __syncwarp();
     };
-    ok = wait_bounded(bar(L::kvfull), 0, w) && wait_bounded(bar(L::qfull), 0, w);
+    ok = wait_warp(bar(L::kvfull), 0, w) && wait_warp(bar(L::qfull), 0, w);
     if (ok) {
       tc_fence_after();
       scores(0);
-      ok = wait_bounded(bar(L::ofull), 0, w);
+      ok = wait_warp(bar(L::ofull), 0, w);
     }
     if (ok) {
       tc_fence_after();
@@ -766,27 +796,30 @@ __global__ void __launch_bounds__(kThreads, 1) rc_dkv_kernel(const __grid_consta
       const int st = it % L::kStages, sn = (it + 1) % L::kStages;
       const uint32_t pn = ((it + 1) / L::kStages) & 1;
       const bool more = it + 1 < total;
-      if (!(ok = wait_bounded(bar(L::pready), it & 1, w))) break;
+      if (!(ok = wait_warp(bar(L::pready), it & 1, w))) break;
       tc_fence_after();
-      mma_rows(tdV, tS, 64, smem_addr(sO + st * L::kTile), idesc_out, it > 0);
+      if (elect_one()) mma_rows(tdV, tS, 64, smem_addr(sO + st * L::kTile), idesc_out, it > 0);
+      __syncwarp();
       if (more) {
-        if (!(ok = wait_bounded(bar(L::qfull + sn), pn, w))) break;
+        if (!(ok = wait_warp(bar(L::qfull + sn), pn, w))) break;
         tc_fence_after();
         scores(it + 1);
       }
-      if (!(ok = wait_bounded(bar(L::dsready), it & 1, w))) break;
+      if (!(ok = wait_warp(bar(L::dsready), it & 1, w))) break;
       tc_fence_after();
-      mma_rows(tdK, tP, 64, smem_addr(sQ + st * L::kTile), idesc_out, it > 0);
-      mma_commit(bar(L::empty + st));
+      if (elect_one()) {
+        mma_rows(tdK, tP, 64, smem_addr(sQ + st * L::kTile), idesc_out, it > 0);
+        mma_commit(bar(L::empty + st));
+        if (!more) mma_commit(bar(L::done));
+      }
+      __syncwarp();
       if (more) {
-        if (!(ok = wait_bounded(bar(L::ofull + sn), pn, w))) break;
+        if (!(ok = wait_warp(bar(L::ofull + sn), pn, w))) break;
         tc_fence_after();
         dprobs(it + 1);
-      } else {
-        mma_commit(bar(L::done));
       }
     }
-    if (*w.abort_flag && issued) drain_mma(bar(L::drain), p.wait_limit_ns);
+    if (*w.abort_flag && issued && elect_one()) drain_mma(bar(L::drain), p.wait_limit_ns);
   } else if (warp < 8 && total > 0) {
     const int half = warp >> 2;              // the 64 query columns of this warp
     const int wt = threadIdx.x & 127;        // thread of its warpgroup
@@ -926,7 +959,7 @@ __global__ void __launch_bounds__(kThreads, 1) rc_dq_kernel(const __grid_constan
   uint8_t* sV = sK + L::kStages * L::kTile;
   Head* hd = reinterpret_cast<Head*>(sV + L::kStages * L::kTile);
   float* tab = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(hd) + kBarBytes);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
   const int head = static_cast<int>(blockIdx.x % p.H);
   const int64_t unit = blockIdx.x / p.H;
   enter(p, hd, L::count, [](int i) { return i == L::dsready ? 8u : 1u; }, unit, 128, p.causal != 0);
@@ -944,11 +977,11 @@ __global__ void __launch_bounds__(kThreads, 1) rc_dq_kernel(const __grid_constan
   const uint32_t bar0 = smem_addr(hd->bar);
   auto bar = [&](int i) { return bar0 + 8u * i; };
   const WaitCtx w{&hd->abort_flag, p.err, p.wait_limit_ns};
-  const uint32_t tmem = hd->tmem;
+  const uint32_t tmem = uniform(hd->tmem);
   const uint32_t tP = tmem + 256, tdQ = tmem + 384;
-  const int start = hd->start, len = hd->len, r0 = 128 * hd->tile;
+  const int start = uniform(hd->start), len = uniform(hd->len), r0 = 128 * uniform(hd->tile);
   const int nk_all = (len + 127) >> 7;
-  const int nk = hd->found ? (p.causal ? min(nk_all, hd->tile + 1) : nk_all) : 0;
+  const int nk = uniform(hd->found) ? (p.causal ? min(nk_all, (r0 >> 7) + 1) : nk_all) : 0;
 
   if (warp == kTmaWarp && nk > 0) {
     const HeadAt hq = head_at(head, p.hq), hk = head_at(head / p.group, p.hk);
@@ -992,25 +1025,31 @@ __global__ void __launch_bounds__(kThreads, 1) rc_dq_kernel(const __grid_constan
     }
     if (lane == 0 && *w.abort_flag) fl.drain(bar0, p.wait_limit_ns);
     __syncwarp();
-  } else if (warp == kMmaWarp && lane == 0 && nk > 0) {
+  } else if (warp == kMmaWarp && nk > 0) {
     const int ksteps = (p.d + 15) >> 4;
     const uint32_t idesc_out = idesc_bf16(0, 1, ksteps * 16);
     bool ok = true, issued = false;
     auto scores = [&](int j) {
-      mma_scores<DP>(tmem + 128 * (j & 1), smem_addr(sQ), smem_addr(sK + (j % L::kStages) * L::kTile), ksteps);
       issued = true;
-      mma_commit(bar(L::sfull + (j & 1)));
+      if (elect_one()) {
+        mma_scores<DP>(tmem + 128 * (j & 1), smem_addr(sQ), smem_addr(sK + (j % L::kStages) * L::kTile), ksteps);
+        mma_commit(bar(L::sfull + (j & 1)));
+      }
+      __syncwarp();
     };
     auto dprobs = [&](int j) {
-      mma_scores<DP>(tP, smem_addr(sO), smem_addr(sV + (j % L::kStages) * L::kTile), ksteps);
-      mma_commit(bar(L::dpfull));
-      mma_commit(bar(L::vempty + j % L::kStages));
+      if (elect_one()) {
+        mma_scores<DP>(tP, smem_addr(sO), smem_addr(sV + (j % L::kStages) * L::kTile), ksteps);
+        mma_commit(bar(L::dpfull));
+        mma_commit(bar(L::vempty + j % L::kStages));
+      }
+      __syncwarp();
     };
-    ok = wait_bounded(bar(L::qfull), 0, w) && wait_bounded(bar(L::kfull), 0, w);
+    ok = wait_warp(bar(L::qfull), 0, w) && wait_warp(bar(L::kfull), 0, w);
     if (ok) {
       tc_fence_after();
       scores(0);
-      ok = wait_bounded(bar(L::vfull), 0, w);
+      ok = wait_warp(bar(L::vfull), 0, w);
     }
     if (ok) {
       tc_fence_after();
@@ -1023,23 +1062,25 @@ __global__ void __launch_bounds__(kThreads, 1) rc_dq_kernel(const __grid_constan
       if (more) {
         // into the other score buffer: dS of tile j - 1 there has been read by
         // its product, issued before
-        if (!(ok = wait_bounded(bar(L::kfull + sn), pn, w))) break;
+        if (!(ok = wait_warp(bar(L::kfull + sn), pn, w))) break;
         tc_fence_after();
         scores(j + 1);
       }
-      if (!(ok = wait_bounded(bar(L::dsready), j & 1, w))) break;
+      if (!(ok = wait_warp(bar(L::dsready), j & 1, w))) break;
       tc_fence_after();
-      mma_rows(tdQ, tmem + 128 * (j & 1), 64, smem_addr(sK + st * L::kTile), idesc_out, j > 0);
-      mma_commit(bar(L::kempty + st));
+      if (elect_one()) {
+        mma_rows(tdQ, tmem + 128 * (j & 1), 64, smem_addr(sK + st * L::kTile), idesc_out, j > 0);
+        mma_commit(bar(L::kempty + st));
+        if (!more) mma_commit(bar(L::done));
+      }
+      __syncwarp();
       if (more) {
-        if (!(ok = wait_bounded(bar(L::vfull + sn), pn, w))) break;
+        if (!(ok = wait_warp(bar(L::vfull + sn), pn, w))) break;
         tc_fence_after();
         dprobs(j + 1);
-      } else {
-        mma_commit(bar(L::done));
       }
     }
-    if (*w.abort_flag && issued) drain_mma(bar(L::drain), p.wait_limit_ns);
+    if (*w.abort_flag && issued && elect_one()) drain_mma(bar(L::drain), p.wait_limit_ns);
   } else if (warp < 8) {
     const int half = warp >> 2;
     const int quarter = warp & 3;
