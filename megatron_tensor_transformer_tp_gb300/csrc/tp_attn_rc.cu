@@ -38,8 +38,12 @@
 namespace tp {
 namespace {
 
-constexpr int kThreads = 320;        // 8 compute warps, MMA warp 8, TMA warp 9
-constexpr int kMmaWarp = 8, kTmaWarp = 9;
+// Compute warps first, then the MMA warps (forward: one a query tile) and last
+// the TMA warp.  The forward has
+// two compute warps on every 32 rows of a score tile (64 columns each), the
+// backward kernels as well.
+constexpr int kFwdWarps = 16, kBwdWarps = 8;
+constexpr int kFwdThreads = 32 * (kFwdWarps + 3), kBwdThreads = 32 * (kBwdWarps + 2);
 constexpr int kPanel = 128 * 128;    // bytes of 128 rows x 64 bf16 columns (one swizzle width)
 constexpr int kBarBytes = 512;
 constexpr float kLog2e = 1.4426950408889634f;
@@ -71,6 +75,8 @@ __device__ __forceinline__ void mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, ui
       "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
       "r"(a_tmem), "l"(b), "r"(idesc), "r"(accumulate));
 }
+
+__device__ __forceinline__ float as_f(uint32_t u) { return __uint_as_float(u); }
 
 // 32 columns of the warp's 32 lanes, without waiting for them.
 __device__ __forceinline__ void tmem_ld32_issue(uint32_t taddr, uint32_t* r) {
@@ -106,18 +112,93 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
       "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(taddr)
       : "memory");
 }
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15};" ::"r"(r[0]),
+      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(taddr)
+      : "memory");
+}
+// 8 columns times f, in place.
+__device__ __forceinline__ void tmem_scale8(uint32_t taddr, float f) {
+  uint32_t r[8];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+      : "r"(taddr)
+      : "memory");
+#pragma unroll
+  for (int q = 0; q < 8; ++q) r[q] = __float_as_uint(as_f(r[q]) * f);
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%8], {%0, %1, %2, %3, %4, %5, %6, %7};" ::"r"(r[0]),
+               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(taddr)
+               : "memory");
+}
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 __device__ __forceinline__ void named_bar(int id, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
 
-// wait_bounded by a whole warp, with one answer for all of its lanes.
+// wait_bounded by a whole warp, with one answer for all of its lanes; the clock
+// and the abort flag are looked at once in a while only.
 __device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, const WaitCtx& w) {
-  return __all_sync(0xffffffffu, wait_bounded(bar, parity, w));
+  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+  unsigned long long t0 = 0;
+  while (true) {
+#pragma unroll 1
+    for (int i = 0; i < 16; ++i)
+      if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+    const unsigned long long t = global_ns();
+    if (t0 == 0) t0 = t;
+    const bool late = t - t0 > w.limit_ns;
+    if (late) {
+      *w.abort_flag = 1;
+      atomicOr(w.err, kErrTimeout);
+    }
+    if (__any_sync(0xffffffffu, late || *w.abort_flag)) return false;
+  }
 }
 
-__device__ __forceinline__ float as_f(uint32_t u) { return __uint_as_float(u); }
+// Two fp32 values a register pair: one instruction for both.
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+// Barrier `id` of `threads` threads; whether any of them said yes.
+__device__ __forceinline__ bool named_bar_any(int id, int threads, bool yes) {
+  uint32_t any;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 q, %3, 0;\n\t"
+      "bar.red.or.pred p, %1, %2, q;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(any)
+      : "r"(id), "r"(threads), "r"(static_cast<uint32_t>(yes))
+      : "memory");
+  return any != 0;
+}
 
 // ---------------------------------------------------------------------------
 // Work items
@@ -197,9 +278,9 @@ __device__ __forceinline__ int bucket_of(const RcBias& b, int delta) {
   return add + lo;
 }
 // tab[delta + md + kPad] = bias of the clamped distance, times log2 e.
-__device__ __forceinline__ void fill_table(const RcParams& p, int head, float* tab) {
+__device__ __forceinline__ void fill_table(const RcParams& p, int head, float* tab, int threads) {
   const int md = p.bias.md, n = table_floats(md);
-  for (int i = threadIdx.x; i < n; i += kThreads) {
+  for (int i = threadIdx.x; i < n; i += threads) {
     const int delta = min(max(i - (md + kPad), -md), md);
     tab[i] = __ldg(p.table + static_cast<int64_t>(bucket_of(p.bias, delta)) * p.H + head) * kLog2e;
   }
@@ -301,15 +382,20 @@ __device__ __forceinline__ void mma_scores(uint32_t d_tmem, uint32_t a, uint32_t
   else mma_scores_k<K0 + 1>(d_tmem, ad, bd, idesc);
 }
 // D (+)= A B: A 128 x 128 bf16 in TMEM, B = 128 rows of a tile as stored
-// (contraction over its rows).  a_half: TMEM columns between the two halves of
-// the contraction.
-__device__ __forceinline__ void mma_rows(uint32_t d_tmem, uint32_t a_tmem, int a_half, uint32_t b, uint32_t idesc,
+// (contraction over its rows).  A's columns for rows 0-63 and 64-127 start 64
+// TMEM columns apart: each compute warp writes where it read its scores.
+// FIRST, COUNT: the 16-row steps of each half that are taken.
+template <int FIRST, int COUNT>
+__device__ __forceinline__ void mma_rows(uint32_t d_tmem, uint32_t a_tmem, uint32_t b, uint32_t idesc,
                                          bool accumulate) {
   const uint64_t bd = sdesc(b, kPanel, 1024);
 #pragma unroll
-  for (int kk = 0; kk < 8; ++kk)
-    mma_bf16_ts(d_tmem, a_tmem + (kk >> 2) * a_half + (kk & 3) * 8, bd + kk * (2048 >> 4), idesc,
-                accumulate || kk > 0);
+  for (int h = 0; h < 2; ++h) {
+#pragma unroll
+    for (int kk = FIRST; kk < FIRST + COUNT; ++kk)
+      mma_bf16_ts(d_tmem, a_tmem + 64 * h + 8 * kk, bd + (4 * h + kk) * (2048 >> 4), idesc,
+                  accumulate || h > 0 || kk > FIRST);
+  }
 }
 
 // One row of d fp32 TMEM columns, scaled, as bf16 to memory.
@@ -383,7 +469,7 @@ __device__ __forceinline__ uint8_t* align1024(uint8_t* q) {
 }
 
 // Common entry: barriers 0 .. nbars-1 with the given counts, TMEM, the unit.
-template <class Counts>
+template <int WARPS, int TMA_WARP, class Counts>
 __device__ __forceinline__ void enter(const RcParams& p, Head* hd, int nbars, Counts&& count, int64_t unit, int rows,
                                       bool last_first) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -392,8 +478,8 @@ __device__ __forceinline__ void enter(const RcParams& p, Head* hd, int nbars, Co
     hd->abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == kMmaWarp) tmem_alloc512(smem_addr(&hd->tmem));
-  if (warp == kTmaWarp) {
+  if (warp == WARPS) tmem_alloc512(smem_addr(&hd->tmem));
+  if (warp == TMA_WARP) {
     pdl_wait();
     Unit u{0, 0, 0};
     const bool f = find_unit(p, unit, rows, last_first, blockIdx.x == 0, lane, u);
@@ -410,10 +496,11 @@ __device__ __forceinline__ void enter(const RcParams& p, Head* hd, int nbars, Co
   pdl_wait();
   pdl_trigger();
 }
+template <int WARPS>
 __device__ __forceinline__ void leave(Head* hd) {
   tc_fence_before();
   __syncthreads();
-  if ((threadIdx.x >> 5) == kMmaWarp) {
+  if ((threadIdx.x >> 5) == WARPS) {
     tc_fence_after();
     tmem_dealloc512(hd->tmem);
   }
@@ -426,16 +513,17 @@ template <int DP>
 struct FwdShape {
   static constexpr int kTile = DP / 64 * kPanel;
   static constexpr int kStages = DP == 128 ? 2 : 4;  // K tiles and V tiles held, each
-  static constexpr int kSmem = 2 * kTile + 2 * kStages * kTile + kBarBytes + 1024;
+  static constexpr int kPart = 2 * 2 * 256 * 4;  // row maxima and row sums of the two column halves
+  static constexpr int kSmem = 2 * kTile + 2 * kStages * kTile + kBarBytes + kPart + 1024;
   // barriers
   static constexpr int qfull = 0, kfull = 2, vfull = kfull + kStages, tail = vfull + kStages, kempty = tail + 1,
-                       vempty = kempty + kStages, sfull = vempty + kStages, pfull = sfull + 2, odone = pfull + 2,
-                       drain = odone + 2, count = drain + 1;
+                       vempty = kempty + kStages, sfull = vempty + kStages, pfull = sfull + 2, odone = pfull + 4,
+                       drain = odone + 2, count = drain + 2;
   static_assert(count <= 40 && kempty <= 32, "barriers");
 };
 
 template <int DP, bool BIAS>
-__global__ void __launch_bounds__(kThreads, 1) rc_fwd_kernel(const __grid_constant__ RcParams p) {
+__global__ void __launch_bounds__(kFwdThreads, 1) rc_fwd_kernel(const __grid_constant__ RcParams p) {
   using L = FwdShape<DP>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = align1024(smem_raw);
@@ -443,13 +531,17 @@ __global__ void __launch_bounds__(kThreads, 1) rc_fwd_kernel(const __grid_consta
   uint8_t* sK = sQ + 2 * L::kTile;
   uint8_t* sV = sK + L::kStages * L::kTile;
   Head* hd = reinterpret_cast<Head*>(sV + L::kStages * L::kTile);
-  float* tab = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(hd) + kBarBytes);
+  float* part = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(hd) + kBarBytes);
+  float* tab = part + 1024;
   const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
   const int head = static_cast<int>(blockIdx.x % p.H);
   const int nsub = p.sub;
-  enter(p, hd, L::count, [](int i) { return i >= L::pfull && i < L::pfull + 2 ? 4u : 1u; }, blockIdx.x / p.H,
+  enter<kFwdWarps, kFwdWarps + 2>(p, hd, L::count, [](int i) {
+    if (i >= L::pfull && i < L::pfull + 4) return 8u;
+    return i >= L::kempty && i < L::sfull ? 2u : 1u;
+  }, blockIdx.x / p.H,
         128 * nsub, p.causal != 0);
-  if (BIAS && hd->found) fill_table(p, head, tab);
+  if (BIAS && hd->found) fill_table(p, head, tab, kFwdThreads);
   if (BIAS) __syncthreads();
   const uint32_t bar0 = smem_addr(hd->bar);
   auto bar = [&](int i) { return bar0 + 8u * i; };
@@ -466,7 +558,7 @@ __global__ void __launch_bounds__(kThreads, 1) rc_fwd_kernel(const __grid_consta
   };
   const int n0 = tiles_of(0), n1 = tiles_of(1), nmax = max(n0, n1);
 
-  if (warp == kTmaWarp && nmax > 0) {
+  if (warp == kFwdWarps + 2 && nmax > 0) {
     const HeadAt hq = head_at(head, p.hq), hk = head_at(head / p.group, p.hk);
     Flight fl;
     uint32_t tail_phase = 0;
@@ -509,141 +601,172 @@ __global__ void __launch_bounds__(kThreads, 1) rc_fwd_kernel(const __grid_consta
     }
     if (lane == 0 && *w.abort_flag) fl.drain(bar0, p.wait_limit_ns);
     __syncwarp();
-  } else if (warp == kMmaWarp && nmax > 0) {
+  } else if (warp >= kFwdWarps && warp < kFwdWarps + 2 && nmax > 0) {
+    // One MMA warp a query tile: while one waits, the other's products run.
+    // Both go through every key tile, and a K or V stage is free when both have
+    // passed it.
+    const int t = warp - kFwdWarps;
+    const int nt = t ? n1 : n0;
     const int ksteps = (p.d + 15) >> 4;
     const uint32_t idesc_pv = idesc_bf16(0, 1, ksteps * 16);
-    const int last = n1 > 0 ? 1 : 0;  // the query tile that uses every key tile last
-    bool ok = true, issued = false;
-    auto scores = [&](int t, int j) {
-      issued = true;
+    const uint32_t dO = tmem + 256 + 128 * t, tS = tmem + 128 * t;
+    auto scores = [&](int j) {
       if (elect_one()) {
-        mma_scores<DP>(tmem + 128 * t, smem_addr(sQ + t * L::kTile), smem_addr(sK + (j % L::kStages) * L::kTile),
-                       ksteps);
+        mma_scores<DP>(tS, smem_addr(sQ + t * L::kTile), smem_addr(sK + (j % L::kStages) * L::kTile), ksteps);
         mma_commit(bar(L::sfull + t));
-        if (t == last) mma_commit(bar(L::kempty + j % L::kStages));
+        mma_commit(bar(L::kempty + j % L::kStages));
       }
       __syncwarp();
     };
-    ok = wait_warp(bar(L::kfull), 0, w);
-    for (int t = 0; ok && t <= last; ++t) {
-      ok = wait_warp(bar(L::qfull + t), 0, w);
+    auto kfull = [&](int j) { return wait_warp(bar(L::kfull + j % L::kStages), (j / L::kStages) & 1, w); };
+    bool ok = true, issued = false;
+    if (nt > 0) {
+      ok = wait_warp(bar(L::qfull + t), 0, w) && kfull(0);
       if (ok) {
         tc_fence_after();
-        scores(t, 0);
+        issued = true;
+        scores(0);
       }
     }
-    for (int j = 0; ok && j < nmax; ++j) {
+    for (int j = 0; ok && j < nt; ++j) {
       const int st = j % L::kStages;
-      const uint32_t ph = (j / L::kStages) & 1;
-      ok = wait_warp(bar(L::vfull + st), ph, w);
-      for (int t = 0; ok && t <= last; ++t) {
-        const int nt = t ? n1 : n0;
-        if (j >= nt) continue;
-        if (!(ok = wait_warp(bar(L::pfull + t), j & 1, w))) break;
-        tc_fence_after();
-        if (elect_one()) {
-          mma_rows(tmem + 256 + 128 * t, tmem + 128 * t, 32, smem_addr(sV + st * L::kTile), idesc_pv, j > 0);
-          if (t == last) mma_commit(bar(L::vempty + st));
-          if (j + 1 >= nt) mma_commit(bar(L::odone + t));
-        }
-        __syncwarp();
-        if (j + 1 < nt) {
-          const int sn = (j + 1) % L::kStages;
-          if (!(ok = wait_warp(bar(L::kfull + sn), ((j + 1) / L::kStages) & 1, w))) break;
-          scores(t, j + 1);
-        }
+      const uint32_t b = smem_addr(sV + st * L::kTile);
+      // everything but the probabilities is waited for before they are, so the
+      // products are issued as one run
+      if (!(ok = wait_warp(bar(L::vfull + st), (j / L::kStages) & 1, w) && (j + 1 >= nt || kfull(j + 1)))) break;
+      if (!(ok = wait_warp(bar(L::pfull + 2 * t), j & 1, w))) break;
+      tc_fence_after();
+      if (elect_one()) mma_rows<0, 2>(dO, tS, b, idesc_pv, j > 0);
+      __syncwarp();
+      if (!(ok = wait_warp(bar(L::pfull + 2 * t + 1), j & 1, w))) break;
+      tc_fence_after();
+      if (elect_one()) {
+        mma_rows<2, 2>(dO, tS, b, idesc_pv, true);
+        mma_commit(bar(L::vempty + st));
+        if (j + 1 >= nt) mma_commit(bar(L::odone + t));
       }
+      __syncwarp();
+      if (j + 1 < nt) scores(j + 1);
     }
-    if (*w.abort_flag && issued && elect_one()) drain_mma(bar(L::drain), p.wait_limit_ns);
-  } else if (warp < 8) {
-    const int t = warp >> 2;
+    // key tiles that only the other query tile sees
+    for (int j = nt; ok && j < nmax; ++j) {
+      const int st = j % L::kStages;
+      if ((ok = kfull(j)) && lane == 0) mbar_arrive(bar(L::kempty + st));
+      if (ok && (ok = wait_warp(bar(L::vfull + st), (j / L::kStages) & 1, w)) && lane == 0)
+        mbar_arrive(bar(L::vempty + st));
+    }
+    if (*w.abort_flag && issued && elect_one()) drain_mma(bar(L::drain + t), p.wait_limit_ns);
+  } else if (warp < kFwdWarps) {
+    const int t = warp >> 3, half = (warp >> 2) & 1, quarter = warp & 3;
     const int nt = t ? n1 : n0;
-    const int row = row0 + 128 * t + (warp & 3) * 32 + lane;  // position in the sequence
-    const uint32_t lane_base = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+    const int row = row0 + 128 * t + quarter * 32 + lane;  // position in the sequence
+    const uint32_t lane_base = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
     const uint32_t tS = lane_base + 128 * t, tO = lane_base + 256 + 128 * t;
+    // the two warps of these rows meet at a barrier of their own
+    const int pair_bar = 1 + 4 * t + quarter;
+    float* mine_at = part + half * 256 + t * 128 + quarter * 32 + lane;
+    const float* other_at = part + (half ^ 1) * 256 + t * 128 + quarter * 32 + lane;
+    const int cut = min(p.d, 32 * ((p.d + 63) / 64));  // this warp's columns of the output
+    const int ofirst = half ? cut : 0, olast = half ? p.d : cut;
     const float sl2 = p.scale_log2;
-    float m = 0.f, l = 0.f;  // the exponents' reference (log2) and the sum of 2^(x - m)
+    float m = 0.f;            // the exponents' reference (log2)
+    float l0 = 0.f, l1 = 0.f; // sums of 2^(x - m) over this warp's columns
+    // After a failed wait the loop runs on without waiting: the pair's barrier
+    // needs both warps, and nothing is stored at the end.
     bool ok = true;
     for (int j = 0; j < nt; ++j) {
-      if (!(ok = wait_warp(bar(L::sfull + t), j & 1, w))) break;
+      ok = ok && wait_warp(bar(L::sfull + t), j & 1, w);
       tc_fence_after();
-      uint32_t s[128];
-#pragma unroll
-      for (int c = 0; c < 4; ++c) tmem_ld32_issue(tS + 32 * c, s + 32 * c);
-#pragma unroll
-      for (int c = 0; c < 4; ++c) tmem_ld32_wait(s + 32 * c);
-      const int c0 = 128 * j, r0 = row0 + 128 * t;
+      uint32_t s[64];
+      tmem_ld32_issue(tS + 64 * half, s);
+      tmem_ld32_issue(tS + 64 * half + 32, s + 32);
+      tmem_ld32_wait(s);
+      tmem_ld32_wait(s + 32);
+      const int c0 = 128 * j + 64 * half, r0 = row0 + 128 * t;
       float mul = sl2, add = 0.f;  // x = s mul + add
       if (BIAS) {
-        const int side = bias_side(p.bias.md, r0, c0);
+        const int side = bias_side(p.bias.md, r0, 128 * j);
         if (side != 0) {
           add = tab[side < 0 ? 0 : table_floats(p.bias.md) - 1];
         } else {
           const float* tb = tab + (c0 - row + p.bias.md + kPad);
 #pragma unroll
-          for (int c = 0; c < 128; ++c) s[c] = __float_as_uint(fmaf(as_f(s[c]), sl2, tb[c]));
+          for (int c = 0; c < 64; ++c) s[c] = __float_as_uint(fmaf(as_f(s[c]), sl2, tb[c]));
           mul = 1.f;
         }
       }
-      if ((p.causal && c0 + 127 > r0) || c0 + 128 > len) {
+      if ((p.causal && 128 * j + 127 > r0) || 128 * j + 128 > len) {
         const int seen = (p.causal ? min(len, row + 1) : len) - c0;  // columns this row sees
 #pragma unroll
-        for (int c = 0; c < 128; ++c) s[c] = c < seen ? s[c] : 0xff800000u;
+        for (int c = 0; c < 64; ++c) s[c] = c < seen ? s[c] : 0xff800000u;
       }
-      float mx[4] = {as_f(s[0]), as_f(s[1]), as_f(s[2]), as_f(s[3])};
+      float mx[4];
 #pragma unroll
-      for (int c = 4; c < 128; ++c) mx[c & 3] = fmaxf(mx[c & 3], as_f(s[c]));
-      const float mt = fmaf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), mul, add);
-      if (j == 0) {
-        m = mt;
-      } else if (__any_sync(0xffffffffu, mt > m + 8.f)) {
-        // The reference follows the maximum only when that is 2^8 above it: the
-        // exponentials stay below 2^8 (exact in fp32's and bf16's range), and
-        // the output is rescaled a few times a row instead of at every tile.
-        const float mn = mt > m + 8.f ? mt : m;
-        const float f = ex2_ftz(m - mn);
-        l *= f;
-        m = mn;
-        for (int c = 0; c < p.d; c += 32) {
-          uint32_t o[32];
-          tmem_ld32_issue(tO + c, o);
-          tmem_ld32_wait(o);
+      for (int q = 0; q < 4; ++q) {
+        mx[q] = fmaxf(as_f(s[q]), as_f(s[q + 4]));
 #pragma unroll
-          for (int q = 0; q < 32; ++q) o[q] = __float_as_uint(as_f(o[q]) * f);
-          tmem_st32(tO + c, o);
+        for (int c = 8 + q; c < 64; c += 8) mx[q] = fmaxf(fmaxf(mx[q], as_f(s[c])), as_f(s[c + 4]));
+      }
+      const float mh = fmaf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), mul, add);
+      // The exponents' reference is the first tile's maximum and follows the
+      // running one only when a row's is 2^16 above it: up to there the
+      // exponentials and their sums are as exact (fp32 and bf16 have the range),
+      // and neither the maxima are exchanged nor the output rescaled.
+      if (named_bar_any(pair_bar, 64, j == 0 || mh > m + 16.f)) {
+        mine_at[0] = mh;
+        named_bar(pair_bar, 64);
+        const float mt = fmaxf(mh, other_at[0]);
+        if (j == 0) {
+          m = mt;
+        } else {
+          const float mn = mt > m + 16.f ? mt : m;
+          const float f = ex2_ftz(m - mn);
+          l0 *= f;
+          l1 *= f;
+          m = mn;
+          for (int c = ofirst; c < olast; c += 8) tmem_scale8(tO + c, f);
         }
       }
       const float off = add - m;
-      float sum[4] = {0.f, 0.f, 0.f, 0.f};
+      const uint64_t scl2 = pack2(mul, mul), off2 = pack2(off, off);
+      uint64_t sum[2] = {pack2(l0, l1), 0ull};
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        uint32_t pk[32];
+        uint32_t pk[16];
 #pragma unroll
-        for (int c = 0; c < 32; ++c) {
-          const float a = ex2_ftz(fmaf(as_f(s[64 * h + 2 * c]), mul, off));
-          const float b = ex2_ftz(fmaf(as_f(s[64 * h + 2 * c + 1]), mul, off));
-          sum[(2 * c) & 3] += a;
-          sum[(2 * c + 1) & 3] += b;
+        for (int c = 0; c < 16; ++c) {
+          float a, b;
+          unpack2(fma2(pack2(as_f(s[32 * h + 2 * c]), as_f(s[32 * h + 2 * c + 1])), scl2, off2), a, b);
+          a = ex2_ftz(a);
+          b = ex2_ftz(b);
+          sum[c & 1] = add2(sum[c & 1], pack2(a, b));
           pk[c] = pack_bf16x2(a, b);
         }
-        tmem_st32(tS + 32 * h, pk);
+        tmem_st16(tS + 64 * half + 16 * h, pk);
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(L::pfull + 2 * t + h));
       }
-      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-      tmem_st_wait();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(L::pfull + t));
+      unpack2(add2(sum[0], sum[1]), l0, l1);
     }
-    if (nt > 0 && ok && wait_warp(bar(L::odone + t), 0, w)) {
-      tc_fence_after();
-      const bool mine = row < len;
-      const int64_t token = static_cast<int64_t>(start) + row;
-      store_row(tO, p.d, 1.f / l, static_cast<__nv_bfloat16*>(p.C) + token * p.ld_c + static_cast<int64_t>(head) * p.d,
-                mine);
-      if (mine) p.lse[static_cast<int64_t>(head) * p.T + token] = (m + log2f(l)) * kLn2;
+    if (nt > 0) {
+      const float lh = l0 + l1;
+      mine_at[512] = lh;
+      named_bar(pair_bar, 64);
+      const float lo = other_at[512];
+      const float l = half ? lo + lh : lh + lo;
+      if (ok && wait_warp(bar(L::odone + t), 0, w)) {
+        tc_fence_after();
+        const bool mine = row < len;
+        const int64_t token = static_cast<int64_t>(start) + row;
+        store_row(tO + ofirst, olast - ofirst, 1.f / l,
+                  static_cast<__nv_bfloat16*>(p.C) + token * p.ld_c + static_cast<int64_t>(head) * p.d + ofirst, mine);
+        if (mine && half == 0) p.lse[static_cast<int64_t>(head) * p.T + token] = (m + log2f(l)) * kLn2;
+      }
     }
   }
-  leave(hd);
+  leave<kFwdWarps>(hd);
 }
 
 // ===========================================================================
@@ -698,7 +821,7 @@ struct DkvShape {
 };
 
 template <int DP, bool BIAS>
-__global__ void __launch_bounds__(kThreads, 1) rc_dkv_kernel(const __grid_constant__ RcParams p) {
+__global__ void __launch_bounds__(kBwdThreads, 1) rc_dkv_kernel(const __grid_constant__ RcParams p) {
   using L = DkvShape<DP>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = align1024(smem_raw);
@@ -711,7 +834,7 @@ __global__ void __launch_bounds__(kThreads, 1) rc_dkv_kernel(const __grid_consta
   float* tab = reinterpret_cast<float*>(vec + 256);
   const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
   const int kvh = static_cast<int>(blockIdx.x % p.KV);
-  enter(p, hd, L::count, [](int i) { return i == L::pready || i == L::dsready ? 8u : 1u; }, blockIdx.x / p.KV, 128,
+  enter<kBwdWarps, kBwdWarps + 1>(p, hd, L::count, [](int i) { return i == L::pready || i == L::dsready ? 8u : 1u; }, blockIdx.x / p.KV, 128,
         false);
   const uint32_t bar0 = smem_addr(hd->bar);
   auto bar = [&](int i) { return bar0 + 8u * i; };
@@ -724,7 +847,7 @@ __global__ void __launch_bounds__(kThreads, 1) rc_dkv_kernel(const __grid_consta
   const int per = uniform(hd->found) ? nq - i0 : 0;  // query tiles a head
   const int total = per * p.group;
 
-  if (warp == kTmaWarp && total > 0) {
+  if (warp == kBwdWarps + 1 && total > 0) {
     const HeadAt hk = head_at(kvh, p.hk);
     Flight fl;
     uint32_t tail_phase = 0;
@@ -763,7 +886,7 @@ __global__ void __launch_bounds__(kThreads, 1) rc_dkv_kernel(const __grid_consta
     }
     if (lane == 0 && *w.abort_flag) fl.drain(bar0, p.wait_limit_ns);
     __syncwarp();
-  } else if (warp == kMmaWarp && total > 0) {
+  } else if (warp == kBwdWarps && total > 0) {
     const int ksteps = (p.d + 15) >> 4;
     const uint32_t idesc_out = idesc_bf16(0, 1, ksteps * 16);
     bool ok = true, issued = false;
@@ -798,7 +921,7 @@ __global__ void __launch_bounds__(kThreads, 1) rc_dkv_kernel(const __grid_consta
       const bool more = it + 1 < total;
       if (!(ok = wait_warp(bar(L::pready), it & 1, w))) break;
       tc_fence_after();
-      if (elect_one()) mma_rows(tdV, tS, 64, smem_addr(sO + st * L::kTile), idesc_out, it > 0);
+      if (elect_one()) mma_rows<0, 4>(tdV, tS, smem_addr(sO + st * L::kTile), idesc_out, it > 0);
       __syncwarp();
       if (more) {
         if (!(ok = wait_warp(bar(L::qfull + sn), pn, w))) break;
@@ -808,7 +931,7 @@ __global__ void __launch_bounds__(kThreads, 1) rc_dkv_kernel(const __grid_consta
       if (!(ok = wait_warp(bar(L::dsready), it & 1, w))) break;
       tc_fence_after();
       if (elect_one()) {
-        mma_rows(tdK, tP, 64, smem_addr(sQ + st * L::kTile), idesc_out, it > 0);
+        mma_rows<0, 4>(tdK, tP, smem_addr(sQ + st * L::kTile), idesc_out, it > 0);
         mma_commit(bar(L::empty + st));
         if (!more) mma_commit(bar(L::done));
       }
@@ -929,7 +1052,7 @@ __global__ void __launch_bounds__(kThreads, 1) rc_dkv_kernel(const __grid_consta
                 pos < len);
     }
   }
-  leave(hd);
+  leave<kBwdWarps>(hd);
 }
 
 template <int DP>
@@ -949,7 +1072,7 @@ constexpr int kDiag = 96;
 __host__ __device__ constexpr int grad_floats(int md) { return 8 * kDiag + 2 * md + 1 + 2 * 256; }
 
 template <int DP, bool BIAS>
-__global__ void __launch_bounds__(kThreads, 1) rc_dq_kernel(const __grid_constant__ RcParams p) {
+__global__ void __launch_bounds__(kBwdThreads, 1) rc_dq_kernel(const __grid_constant__ RcParams p) {
   using L = DqShape<DP>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = align1024(smem_raw);
@@ -962,16 +1085,16 @@ __global__ void __launch_bounds__(kThreads, 1) rc_dq_kernel(const __grid_constan
   const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
   const int head = static_cast<int>(blockIdx.x % p.H);
   const int64_t unit = blockIdx.x / p.H;
-  enter(p, hd, L::count, [](int i) { return i == L::dsready ? 8u : 1u; }, unit, 128, p.causal != 0);
+  enter<kBwdWarps, kBwdWarps + 1>(p, hd, L::count, [](int i) { return i == L::dsready ? 8u : 1u; }, unit, 128, p.causal != 0);
   const bool grad = BIAS && p.partial != nullptr;
   const int md = BIAS ? p.bias.md : 0;
   float* diag = tab + (BIAS ? table_floats(md) : 0);  // [8][kDiag]
   float* bins = diag + 8 * kDiag;                     // [2 md + 1]
   float* ends = bins + 2 * md + 1;                    // [2][256]
   if (BIAS) {
-    if (hd->found) fill_table(p, head, tab);
+    if (hd->found) fill_table(p, head, tab, kBwdThreads);
     if (grad)
-      for (int i = threadIdx.x; i < 2 * md + 1; i += kThreads) bins[i] = 0.f;
+      for (int i = threadIdx.x; i < 2 * md + 1; i += kBwdThreads) bins[i] = 0.f;
     __syncthreads();
   }
   const uint32_t bar0 = smem_addr(hd->bar);
@@ -983,7 +1106,7 @@ __global__ void __launch_bounds__(kThreads, 1) rc_dq_kernel(const __grid_constan
   const int nk_all = (len + 127) >> 7;
   const int nk = uniform(hd->found) ? (p.causal ? min(nk_all, (r0 >> 7) + 1) : nk_all) : 0;
 
-  if (warp == kTmaWarp && nk > 0) {
+  if (warp == kBwdWarps + 1 && nk > 0) {
     const HeadAt hq = head_at(head, p.hq), hk = head_at(head / p.group, p.hk);
     Flight fl;
     uint32_t tail_phase = 0;
@@ -1025,7 +1148,7 @@ __global__ void __launch_bounds__(kThreads, 1) rc_dq_kernel(const __grid_constan
     }
     if (lane == 0 && *w.abort_flag) fl.drain(bar0, p.wait_limit_ns);
     __syncwarp();
-  } else if (warp == kMmaWarp && nk > 0) {
+  } else if (warp == kBwdWarps && nk > 0) {
     const int ksteps = (p.d + 15) >> 4;
     const uint32_t idesc_out = idesc_bf16(0, 1, ksteps * 16);
     bool ok = true, issued = false;
@@ -1069,7 +1192,7 @@ __global__ void __launch_bounds__(kThreads, 1) rc_dq_kernel(const __grid_constan
       if (!(ok = wait_warp(bar(L::dsready), j & 1, w))) break;
       tc_fence_after();
       if (elect_one()) {
-        mma_rows(tdQ, tmem + 128 * (j & 1), 64, smem_addr(sK + st * L::kTile), idesc_out, j > 0);
+        mma_rows<0, 4>(tdQ, tmem + 128 * (j & 1), smem_addr(sK + st * L::kTile), idesc_out, j > 0);
         mma_commit(bar(L::kempty + st));
         if (!more) mma_commit(bar(L::done));
       }
@@ -1224,7 +1347,7 @@ __global__ void __launch_bounds__(kThreads, 1) rc_dq_kernel(const __grid_constan
       }
     }
   }
-  leave(hd);
+  leave<kBwdWarps>(hd);
 }
 
 // dtable[u, h] (+)= the sum over the units' partial sums, in a fixed order: one
@@ -1249,10 +1372,10 @@ __global__ void __launch_bounds__(128) rc_bias_sum_kernel(const __grid_constant_
 }
 
 template <class K>
-cudaError_t launch_rc(K kernel, int64_t blocks, int smem, const RcParams& p, cudaStream_t st) {
+cudaError_t launch_rc(K kernel, int64_t blocks, int threads, int smem, const RcParams& p, cudaStream_t st) {
   const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  launch_k(kernel, dim3(static_cast<unsigned>(blocks)), dim3(kThreads), smem, st, p);
+  launch_k(kernel, dim3(static_cast<unsigned>(blocks)), dim3(threads), smem, st, p);
   count_launches(1);
   return cudaGetLastError();
 }
@@ -1270,16 +1393,16 @@ cudaError_t fwd_t(RcParams& p, int num_sms, cudaStream_t st) {
   // products overlap, and K/V tiles are read once for both.
   p.sub = units_of(p, 256) * p.H >= num_sms ? 2 : 1;
   const int smem = FwdShape<DP>::kSmem + (BIAS ? 4 * table_floats(p.bias.md) : 0);
-  return launch_rc(rc_fwd_kernel<DP, BIAS>, units_of(p, 128 * p.sub) * p.H, smem, p, st);
+  return launch_rc(rc_fwd_kernel<DP, BIAS>, units_of(p, 128 * p.sub) * p.H, kFwdThreads, smem, p, st);
 }
 template <int DP, bool BIAS>
 cudaError_t bwd_t(RcParams& p, cudaStream_t st) {
   const int64_t units = units_of(p, 128);
   const int tab = BIAS ? 4 * table_floats(p.bias.md) : 0;
-  cudaError_t e = launch_rc(rc_dkv_kernel<DP, BIAS>, units * p.KV, DkvShape<DP>::kSmem + tab, p, st);
+  cudaError_t e = launch_rc(rc_dkv_kernel<DP, BIAS>, units * p.KV, kBwdThreads, DkvShape<DP>::kSmem + tab, p, st);
   p.fault_skip = 0;
   if (e != cudaSuccess) return e;
-  e = launch_rc(rc_dq_kernel<DP, BIAS>, units * p.H,
+  e = launch_rc(rc_dq_kernel<DP, BIAS>, units * p.H, kBwdThreads,
                 DqShape<DP>::kSmem + tab + (BIAS ? 4 * grad_floats(p.bias.md) : 0), p, st);
   if (e != cudaSuccess || !BIAS || p.partial == nullptr) return e;
   launch_k(rc_bias_sum_kernel, dim3(p.H, p.bias.nb), dim3(128), 0, st, p, units);
