@@ -1330,6 +1330,8 @@ tp_status rc_args(tp_dtype dt, const tp_attn_config* c, const tp_relbias_config*
       (reinterpret_cast<uintptr_t>(seq_starts) & 7u) != 0)
     return TP_ERR_ALIGN;
   P->seq_starts = seq_starts;
+  P->QKV = QKV;
+  P->ld_qkv = ld_qkv;
   P->ld_c = ld_c;
   P->C = const_cast<void*>(C);
   P->lse = const_cast<float*>(lse);

@@ -38,12 +38,12 @@
 namespace tp {
 namespace {
 
-// Compute warps first, then the MMA warps (forward: one a query tile) and last
-// the TMA warp.  The forward has
-// two compute warps on every 32 rows of a score tile (64 columns each), the
-// backward kernels as well.
-constexpr int kFwdWarps = 16, kBwdWarps = 8;
-constexpr int kFwdThreads = 32 * (kFwdWarps + 3), kBwdThreads = 32 * (kBwdWarps + 2);
+// Compute warps first, then two MMA warps, the TMA warp and (dK, dV) a warp that
+// stages the rows' lse and D.  The forward has two compute warps on every 32
+// rows of a score tile (64 columns each) and two tiles, the backward kernels
+// four (32 columns each).
+constexpr int kFwdWarps = 16, kBwdWarps = 16;
+constexpr int kFwdThreads = 32 * (kFwdWarps + 3), kDkvThreads = 32 * (kBwdWarps + 4), kDqThreads = 32 * (kBwdWarps + 2);
 constexpr int kPanel = 128 * 128;    // bytes of 128 rows x 64 bf16 columns (one swizzle width)
 constexpr int kBarBytes = 512;
 constexpr float kLog2e = 1.4426950408889634f;
@@ -381,22 +381,43 @@ __device__ __forceinline__ void mma_scores(uint32_t d_tmem, uint32_t a, uint32_t
   else if (ksteps == K0 + 2) mma_scores_k<K0 + 2>(d_tmem, ad, bd, idesc);
   else mma_scores_k<K0 + 1>(d_tmem, ad, bd, idesc);
 }
+// The same with A (128 x 16 KSTEPS) in TMEM.
+template <int KSTEPS>
+__device__ __forceinline__ void mma_scores_ts_k(uint32_t d_tmem, uint32_t a_tmem, uint64_t bd, uint32_t idesc) {
+#pragma unroll
+  for (int kk = 0; kk < KSTEPS; ++kk)
+    mma_bf16_ts(d_tmem, a_tmem + 8 * kk, bd + (((kk >> 2) * kPanel + (kk & 3) * 32) >> 4), idesc, kk > 0);
+}
+template <int DP>
+__device__ __forceinline__ void mma_scores_ts(uint32_t d_tmem, uint32_t a_tmem, uint32_t b, int ksteps) {
+  const uint64_t bd = sdesc(b, 16, 1024);
+  const uint32_t idesc = idesc_bf16(0, 0, 128);
+  constexpr int K0 = DP == 128 ? 4 : 0;
+  if (ksteps == K0 + 4) mma_scores_ts_k<K0 + 4>(d_tmem, a_tmem, bd, idesc);
+  else if (ksteps == K0 + 3) mma_scores_ts_k<K0 + 3>(d_tmem, a_tmem, bd, idesc);
+  else if (ksteps == K0 + 2) mma_scores_ts_k<K0 + 2>(d_tmem, a_tmem, bd, idesc);
+  else mma_scores_ts_k<K0 + 1>(d_tmem, a_tmem, bd, idesc);
+}
+
 // D (+)= A B: A 128 x 128 bf16 in TMEM, B = 128 rows of a tile as stored
-// (contraction over its rows).  A's columns for rows 0-63 and 64-127 start 64
-// TMEM columns apart: each compute warp writes where it read its scores.
-// FIRST, COUNT: the 16-row steps of each half that are taken.
-template <int FIRST, int COUNT>
+// (contraction over its rows).  Each compute warp writes its part of A where it
+// read its scores: with PARTS parts, part x's columns start at 128 x / PARTS.
+// FIRST, COUNT: the 16-row steps of each part that are taken.
+template <int PARTS, int FIRST = 0, int COUNT = 8 / PARTS>
 __device__ __forceinline__ void mma_rows(uint32_t d_tmem, uint32_t a_tmem, uint32_t b, uint32_t idesc,
                                          bool accumulate) {
   const uint64_t bd = sdesc(b, kPanel, 1024);
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
+  for (int h = 0; h < PARTS; ++h) {
 #pragma unroll
     for (int kk = FIRST; kk < FIRST + COUNT; ++kk)
-      mma_bf16_ts(d_tmem, a_tmem + 64 * h + 8 * kk, bd + (4 * h + kk) * (2048 >> 4), idesc,
+      mma_bf16_ts(d_tmem, a_tmem + 128 / PARTS * h + 8 * kk, bd + (8 / PARTS * h + kk) * (2048 >> 4), idesc,
                   accumulate || h > 0 || kk > FIRST);
   }
 }
+
+// A row's columns that the first of two warps takes, in 32s.
+__device__ __forceinline__ int first_columns(int d) { return min(d, 32 * ((d + 63) / 64)); }
 
 // One row of d fp32 TMEM columns, scaled, as bf16 to memory.
 __device__ __forceinline__ void store_row(uint32_t taddr, int d, float mul, __nv_bfloat16* out, bool ok) {
@@ -418,6 +439,23 @@ __device__ __forceinline__ void store_row(uint32_t taddr, int d, float mul, __nv
       }
     }
     __syncwarp();
+  }
+}
+
+// COLS bf16 columns of a row of memory as COLS / 2 TMEM columns; `n` of them
+// exist (a multiple of 8, <= 0: none), the others become zeros.
+template <int COLS>
+__device__ __forceinline__ void fill_tmem_rows(uint32_t taddr, const __nv_bfloat16* row, int n) {
+#pragma unroll
+  for (int c = 0; c < COLS; c += 16) {
+    uint4 v[2];
+#pragma unroll
+    for (int q = 0; q < 2; ++q)
+      v[q] = c + 8 * q < n ? __ldg(reinterpret_cast<const uint4*>(row + c + 8 * q)) : make_uint4(0, 0, 0, 0);
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%8], {%0, %1, %2, %3, %4, %5, %6, %7};" ::"r"(v[0].x),
+                 "r"(v[0].y), "r"(v[0].z), "r"(v[0].w), "r"(v[1].x), "r"(v[1].y), "r"(v[1].z), "r"(v[1].w),
+                 "r"(taddr + c / 2)
+                 : "memory");
   }
 }
 
@@ -636,12 +674,12 @@ __global__ void __launch_bounds__(kFwdThreads, 1) rc_fwd_kernel(const __grid_con
       if (!(ok = wait_warp(bar(L::vfull + st), (j / L::kStages) & 1, w) && (j + 1 >= nt || kfull(j + 1)))) break;
       if (!(ok = wait_warp(bar(L::pfull + 2 * t), j & 1, w))) break;
       tc_fence_after();
-      if (elect_one()) mma_rows<0, 2>(dO, tS, b, idesc_pv, j > 0);
+      if (elect_one()) mma_rows<2, 0, 2>(dO, tS, b, idesc_pv, j > 0);
       __syncwarp();
       if (!(ok = wait_warp(bar(L::pfull + 2 * t + 1), j & 1, w))) break;
       tc_fence_after();
       if (elect_one()) {
-        mma_rows<2, 2>(dO, tS, b, idesc_pv, true);
+        mma_rows<2, 2, 2>(dO, tS, b, idesc_pv, true);
         mma_commit(bar(L::vempty + st));
         if (j + 1 >= nt) mma_commit(bar(L::odone + t));
       }
@@ -666,7 +704,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) rc_fwd_kernel(const __grid_con
     const int pair_bar = 1 + 4 * t + quarter;
     float* mine_at = part + half * 256 + t * 128 + quarter * 32 + lane;
     const float* other_at = part + (half ^ 1) * 256 + t * 128 + quarter * 32 + lane;
-    const int cut = min(p.d, 32 * ((p.d + 63) / 64));  // this warp's columns of the output
+    const int cut = first_columns(p.d);  // this warp's columns of the output
     const int ofirst = half ? cut : 0, olast = half ? p.d : cut;
     const float sl2 = p.scale_log2;
     float m = 0.f;            // the exponents' reference (log2)
@@ -808,34 +846,56 @@ __global__ void __launch_bounds__(256) rc_dot_kernel(const __grid_constant__ RcP
   }
 }
 
-template <int DP>
+// A Q tile is held from the scores to dK, longer than a dC tile: three stages
+// of it for the wide heads, where they fit (the bias's table takes their place).
+// With two the loads were late by half an iteration.
+template <int DP, bool BIAS>
 struct DkvShape {
   static constexpr int kTile = DP / 64 * kPanel;
-  static constexpr int kStages = DP == 128 ? 2 : 4;  // (Q, dC) tile pairs held
-  static constexpr int kVec = 2 * 128 * 8;           // (lse, D) of two query tiles
-  static constexpr int kSmem = 2 * kTile + 2 * kStages * kTile + kBarBytes + kVec + 1024;
-  static constexpr int kvfull = 0, qfull = 1, ofull = qfull + kStages, tail = ofull + kStages, empty = tail + 1,
-                       sfull = empty + kStages, dpfull = sfull + 1, pready = dpfull + 1, dsready = pready + 1,
-                       done = dsready + 1, drain = done + 1, count = drain + 1;
-  static_assert(count <= 40 && empty <= 32, "barriers");
+  static constexpr int kQ = DP == 128 ? (BIAS ? 2 : 3) : 4, kO = DP == 128 ? 2 : 4;  // Q and dC tiles held
+  static constexpr int kVec = 2 * 2 * 128 * 4;  // (-lse log2 e, -D) of two query tiles
+  static constexpr int kSmem = (2 + kQ + kO) * kTile + kBarBytes + kVec;
+  static constexpr int kvfull = 0, qfull = 1, ofull = qfull + kQ, tail = ofull + kO, qempty = tail + 1,
+                       oempty = qempty + kQ, vecfull = oempty + kO, vecempty = vecfull + 2, sfull = vecempty + 2,
+                       dpfull = sfull + 1, pready = dpfull + 1, dsready = pready + 1, done = dsready + 1,
+                       drain = done + 1, count = drain + 2;
+  static_assert(count <= 40 && qempty <= 32, "barriers");
+  static uint32_t __device__ __forceinline__ arrivals(int i) {
+    if (i == pready || i == dsready || i == vecempty || i == vecempty + 1) return kBwdWarps;
+    return i == done || (i >= oempty && i < vecfull) ? 2u : 1u;
+  }
+};
+
+// The query tiles of a K/V head's key tile, head by head.
+struct QueryWalk {
+  int g, i, i0, nq;
+  __device__ __forceinline__ void next() {
+    if (++i == nq) {
+      i = i0;
+      ++g;
+    }
+  }
 };
 
 template <int DP, bool BIAS>
-__global__ void __launch_bounds__(kBwdThreads, 1) rc_dkv_kernel(const __grid_constant__ RcParams p) {
-  using L = DkvShape<DP>;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = align1024(smem_raw);
+__global__ void __launch_bounds__(kDkvThreads, 1) rc_dkv_kernel(const __grid_constant__ RcParams p) {
+  using L = DkvShape<DP, BIAS>;
+  extern __shared__ __align__(1024) uint8_t smem_wide[];
+  uint8_t* smem = smem_wide;
+  if (smem_addr(smem) & 1023u) {  // nothing of the launch is left for padding
+    if (threadIdx.x == 0) atomicOr(p.err, kErrTimeout);
+    return;
+  }
   uint8_t* sK = smem;
   uint8_t* sV = sK + L::kTile;
   uint8_t* sQ = sV + L::kTile;
-  uint8_t* sO = sQ + L::kStages * L::kTile;
-  Head* hd = reinterpret_cast<Head*>(sO + L::kStages * L::kTile);
-  float2* vec = reinterpret_cast<float2*>(reinterpret_cast<uint8_t*>(hd) + kBarBytes);
-  float* tab = reinterpret_cast<float*>(vec + 256);
+  uint8_t* sO = sQ + L::kQ * L::kTile;
+  Head* hd = reinterpret_cast<Head*>(sO + L::kO * L::kTile);
+  float* vec = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(hd) + kBarBytes);  // [2][2][128]
+  float* tab = vec + 512;
   const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
   const int kvh = static_cast<int>(blockIdx.x % p.KV);
-  enter<kBwdWarps, kBwdWarps + 1>(p, hd, L::count, [](int i) { return i == L::pready || i == L::dsready ? 8u : 1u; }, blockIdx.x / p.KV, 128,
-        false);
+  enter<kBwdWarps, kBwdWarps + 2>(p, hd, L::count, L::arrivals, blockIdx.x / p.KV, 128, false);
   const uint32_t bar0 = smem_addr(hd->bar);
   auto bar = [&](int i) { return bar0 + 8u * i; };
   const WaitCtx w{&hd->abort_flag, p.err, p.wait_limit_ns};
@@ -846,8 +906,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1) rc_dkv_kernel(const __grid_con
   const int i0 = p.causal ? kt : 0;
   const int per = uniform(hd->found) ? nq - i0 : 0;  // query tiles a head
   const int total = per * p.group;
+  QueryWalk q{kvh * p.group, i0, i0, nq};
 
-  if (warp == kBwdWarps + 1 && total > 0) {
+  if (warp == kBwdWarps + 2 && total > 0) {
     const HeadAt hk = head_at(kvh, p.hk);
     Flight fl;
     uint32_t tail_phase = 0;
@@ -862,192 +923,224 @@ __global__ void __launch_bounds__(kBwdThreads, 1) rc_dkv_kernel(const __grid_con
         load_tile<DP>(smem_addr(sV), &p.mapV, bar(L::kvfull), start + 128 * kt, hk);
       }
     }
-    for (int it = 0; ok && it < total; ++it) {
-      const int st = it % L::kStages;
-      const uint32_t ph = (it / L::kStages) & 1;
-      const HeadAt hq = head_at(kvh * p.group + it / per, p.hq);
-      const int i = i0 + it % per;
-      if (lane == 0) ok = wait_bounded(bar(L::empty + st), ph ^ 1u, w);
+    for (int it = 0; ok && it < total; ++it, q.next()) {
+      const int sq = it % L::kQ, so = it % L::kO;
+      const uint32_t pq = (it / L::kQ) & 1, po = (it / L::kO) & 1;
+      const HeadAt hq = head_at(q.g, p.hq);
+      const bool cut = 128 * q.i + 128 > len && start + len < p.T;  // rows of nobody in the tile
+      if (lane == 0) ok = wait_bounded(bar(L::qempty + sq), pq ^ 1u, w);
       ok = __shfl_sync(0xffffffffu, ok, 0);
       if (!ok) break;
-      if (128 * i + 128 > len && start + len < p.T) {
-        ok = load_tail<DP>(sQ + st * L::kTile, &p.mapQ, bar(L::qfull + st), bar(L::tail), tail_phase,
-                           start + 128 * i, hq, len - 128 * i, lane, w);
-        ok = ok && load_tail<DP>(sO + st * L::kTile, &p.mapO, bar(L::ofull + st), bar(L::tail), tail_phase,
-                                 start + 128 * i, hq, len - 128 * i, lane, w);
+      if (cut) {
+        ok = load_tail<DP>(sQ + sq * L::kTile, &p.mapQ, bar(L::qfull + sq), bar(L::tail), tail_phase,
+                           start + 128 * q.i, hq, len - 128 * q.i, lane, w);
+        if (!ok) break;
       } else if (lane == 0) {
-        mbar_arrive_expect_tx(bar(L::qfull + st), L::kTile);
-        fl.note(L::qfull + st, ph);
-        load_tile<DP>(smem_addr(sQ + st * L::kTile), &p.mapQ, bar(L::qfull + st), start + 128 * i, hq);
-        mbar_arrive_expect_tx(bar(L::ofull + st), L::kTile);
-        fl.note(L::ofull + st, ph);
-        load_tile<DP>(smem_addr(sO + st * L::kTile), &p.mapO, bar(L::ofull + st), start + 128 * i, hq);
+        mbar_arrive_expect_tx(bar(L::qfull + sq), L::kTile);
+        fl.note(L::qfull + sq, pq);
+        load_tile<DP>(smem_addr(sQ + sq * L::kTile), &p.mapQ, bar(L::qfull + sq), start + 128 * q.i, hq);
+      }
+      if (lane == 0) ok = wait_bounded(bar(L::oempty + so), po ^ 1u, w);
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+      if (!ok) break;
+      if (cut) {
+        ok = load_tail<DP>(sO + so * L::kTile, &p.mapO, bar(L::ofull + so), bar(L::tail), tail_phase,
+                           start + 128 * q.i, hq, len - 128 * q.i, lane, w);
+      } else if (lane == 0) {
+        mbar_arrive_expect_tx(bar(L::ofull + so), L::kTile);
+        fl.note(L::ofull + so, po);
+        load_tile<DP>(smem_addr(sO + so * L::kTile), &p.mapO, bar(L::ofull + so), start + 128 * q.i, hq);
       }
     }
     if (lane == 0 && *w.abort_flag) fl.drain(bar0, p.wait_limit_ns);
     __syncwarp();
+  } else if (warp == kBwdWarps + 3) {
+    // (-lse log2 e, -D) of the query tiles; a row past the sequence gets
+    // probability 2^(x - inf) = 0
+    bool ok = true;
+    for (int it = 0; ok && it < total; ++it, q.next()) {
+      const int buf = it & 1;
+      float nl[4], nd[4];
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        const int pos = 128 * q.i + 32 * x + lane;
+        const int64_t at = static_cast<int64_t>(q.g) * p.T + start + pos;
+        nl[x] = pos < len ? -p.lse[at] * kLog2e : -INFINITY;
+        nd[x] = pos < len ? -p.D[at] : 0.f;
+      }
+      if (!(ok = wait_warp(bar(L::vecempty + buf), ((it >> 1) & 1) ^ 1u, w))) break;
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        vec[256 * buf + 32 * x + lane] = nl[x];
+        vec[256 * buf + 128 + 32 * x + lane] = nd[x];
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(L::vecfull + buf));
+    }
   } else if (warp == kBwdWarps && total > 0) {
+    // products through the scores: S^T = K Q^T, then dV += P^T dC
     const int ksteps = (p.d + 15) >> 4;
     const uint32_t idesc_out = idesc_bf16(0, 1, ksteps * 16);
-    bool ok = true, issued = false;
-    auto scores = [&](int it) {
+    bool ok = wait_warp(bar(L::kvfull), 0, w), issued = false;
+    for (int it = -1; ok && it < total; ++it) {
+      const int sn = (it + 1) % L::kQ, so = it % L::kO;
+      if (it + 1 < total && !(ok = wait_warp(bar(L::qfull + sn), ((it + 1) / L::kQ) & 1, w))) break;
+      if (it >= 0) {
+        if (!(ok = wait_warp(bar(L::ofull + so), (it / L::kO) & 1, w))) break;
+        if (!(ok = wait_warp(bar(L::pready), it & 1, w))) break;
+      }
+      tc_fence_after();
       issued = true;
       if (elect_one()) {
-        mma_scores<DP>(tS, smem_addr(sK), smem_addr(sQ + (it % L::kStages) * L::kTile), ksteps);
-        mma_commit(bar(L::sfull));
+        if (it >= 0) {
+          mma_rows<4>(tdV, tS, smem_addr(sO + so * L::kTile), idesc_out, it > 0);
+          mma_commit(bar(L::oempty + so));
+        }
+        if (it + 1 < total) {
+          mma_scores<DP>(tS, smem_addr(sK), smem_addr(sQ + sn * L::kTile), ksteps);
+          mma_commit(bar(L::sfull));
+        } else {
+          mma_commit(bar(L::done));
+        }
       }
       __syncwarp();
-    };
-    auto dprobs = [&](int it) {
-      if (elect_one()) {
-        mma_scores<DP>(tP, smem_addr(sV), smem_addr(sO + (it % L::kStages) * L::kTile), ksteps);
-        mma_commit(bar(L::dpfull));
-      }
-      __syncwarp();
-    };
-    ok = wait_warp(bar(L::kvfull), 0, w) && wait_warp(bar(L::qfull), 0, w);
-    if (ok) {
-      tc_fence_after();
-      scores(0);
-      ok = wait_warp(bar(L::ofull), 0, w);
-    }
-    if (ok) {
-      tc_fence_after();
-      dprobs(0);
-    }
-    for (int it = 0; ok && it < total; ++it) {
-      const int st = it % L::kStages, sn = (it + 1) % L::kStages;
-      const uint32_t pn = ((it + 1) / L::kStages) & 1;
-      const bool more = it + 1 < total;
-      if (!(ok = wait_warp(bar(L::pready), it & 1, w))) break;
-      tc_fence_after();
-      if (elect_one()) mma_rows<0, 4>(tdV, tS, smem_addr(sO + st * L::kTile), idesc_out, it > 0);
-      __syncwarp();
-      if (more) {
-        if (!(ok = wait_warp(bar(L::qfull + sn), pn, w))) break;
-        tc_fence_after();
-        scores(it + 1);
-      }
-      if (!(ok = wait_warp(bar(L::dsready), it & 1, w))) break;
-      tc_fence_after();
-      if (elect_one()) {
-        mma_rows<0, 4>(tdK, tP, smem_addr(sQ + st * L::kTile), idesc_out, it > 0);
-        mma_commit(bar(L::empty + st));
-        if (!more) mma_commit(bar(L::done));
-      }
-      __syncwarp();
-      if (more) {
-        if (!(ok = wait_warp(bar(L::ofull + sn), pn, w))) break;
-        tc_fence_after();
-        dprobs(it + 1);
-      }
     }
     if (*w.abort_flag && issued && elect_one()) drain_mma(bar(L::drain), p.wait_limit_ns);
-  } else if (warp < 8 && total > 0) {
-    const int half = warp >> 2;              // the 64 query columns of this warp
-    const int wt = threadIdx.x & 127;        // thread of its warpgroup
+  } else if (warp == kBwdWarps + 1 && total > 0) {
+    // products through their gradient: dP^T = V dC^T, then dK += dS^T Q
+    const int ksteps = (p.d + 15) >> 4;
+    const uint32_t idesc_out = idesc_bf16(0, 1, ksteps * 16);
+    bool ok = wait_warp(bar(L::kvfull), 0, w), issued = false;
+    for (int it = -1; ok && it < total; ++it) {
+      const int sn = (it + 1) % L::kO, sq = it % L::kQ;
+      if (it + 1 < total && !(ok = wait_warp(bar(L::ofull + sn), ((it + 1) / L::kO) & 1, w))) break;
+      if (it >= 0) {
+        if (!(ok = wait_warp(bar(L::qfull + sq), (it / L::kQ) & 1, w))) break;
+        if (!(ok = wait_warp(bar(L::dsready), it & 1, w))) break;
+      }
+      tc_fence_after();
+      issued = true;
+      if (elect_one()) {
+        if (it >= 0) {
+          mma_rows<4>(tdK, tP, smem_addr(sQ + sq * L::kTile), idesc_out, it > 0);
+          mma_commit(bar(L::qempty + sq));
+        }
+        if (it + 1 < total) {
+          mma_scores<DP>(tP, smem_addr(sV), smem_addr(sO + sn * L::kTile), ksteps);
+          mma_commit(bar(L::dpfull));
+          mma_commit(bar(L::oempty + sn));
+        } else {
+          mma_commit(bar(L::done));
+        }
+      }
+      __syncwarp();
+    }
+    if (*w.abort_flag && issued && elect_one()) drain_mma(bar(L::drain + 1), p.wait_limit_ns);
+  } else if (warp < kBwdWarps && total > 0) {
+    const int part = warp >> 2;              // the 32 query columns of this warp
     const int key = (warp & 3) * 32 + lane;  // row of the transposed tile
     const uint32_t lb = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const float sl2 = p.scale_log2;
+    const uint32_t tSw = tS + lb + 32 * part, tPw = tP + lb + 32 * part;
+    const uint64_t scl2 = pack2(p.scale_log2, p.scale_log2);
     // After a failed wait the loop runs on without waiting: the named barriers
     // below need every warp, and nothing is stored at the end.
     bool ok = true;
     int table_head = -1;
-    // (lse log2 e, D) of a query: component wt / 64 of column wt % 64
-    auto fetch = [&](int it) {
-      const int pos = 128 * (i0 + it % per) + 64 * half + (wt & 63);
-      if (it >= total || pos >= len) return wt < 64 ? INFINITY : 0.f;  // 2^(x - inf) = 0
-      const int64_t at = static_cast<int64_t>(kvh * p.group + it / per) * p.T + start + pos;
-      return wt < 64 ? p.lse[at] * kLog2e : p.D[at];
-    };
-    float next = fetch(0);
-    for (int it = 0; it < total; ++it) {
-      const int i = i0 + it % per;
-      float* v = reinterpret_cast<float*>(vec + (it & 1) * 128 + half * 64);
-      v[2 * (wt & 63) + (wt >> 6)] = next;
-      if (BIAS && table_head != kvh * p.group + it / per) {
-        // the next query head's bias; both warpgroups share the table
-        table_head = kvh * p.group + it / per;
-        named_bar(3, 256);
-        const int md = p.bias.md, n = table_floats(md);
-        for (int x = threadIdx.x; x < n; x += 256) {
-          const int delta = min(max(x - (md + kPad), -md), md);
-          tab[x] = __ldg(p.table + static_cast<int64_t>(bucket_of(p.bias, delta)) * p.H + table_head) * kLog2e;
-        }
-        named_bar(3, 256);
+    for (int it = 0; it < total; ++it, q.next()) {
+      const int buf = it & 1;
+      if (BIAS && table_head != q.g) {
+        // the next query head's bias; every compute warp reads the table
+        table_head = q.g;
+        named_bar(1, 32 * kBwdWarps);
+        fill_table(p, q.g, tab, 32 * kBwdWarps);
+        named_bar(1, 32 * kBwdWarps);
       }
-      named_bar(1 + half, 128);
-      next = fetch(it + 1);
-      const float4* v4 = reinterpret_cast<const float4*>(v);
-      ok = ok && wait_warp(bar(L::sfull), it & 1, w);
-      tc_fence_after();
-      uint32_t s[64];
-      tmem_ld32_issue(tS + lb + 64 * half, s);
-      tmem_ld32_issue(tS + lb + 64 * half + 32, s + 32);
-      tmem_ld32_wait(s);
-      tmem_ld32_wait(s + 32);
       float add = 0.f;
       bool near = false;
       const float* tb = nullptr;
       if (BIAS) {
-        const int side = bias_side(p.bias.md, 128 * i, 128 * kt);
+        const int side = bias_side(p.bias.md, 128 * q.i, 128 * kt);
         near = side == 0;
         if (!near) add = tab[side < 0 ? 0 : table_floats(p.bias.md) - 1];
-        // distance of column c: key - query = (128 kt + key) - (128 i + 64 half + c)
-        tb = tab + (128 * (kt - i) + key - 64 * half + p.bias.md + kPad);
+        // distance of column c: key - query = (128 kt + key) - (128 i + 32 part + c)
+        tb = tab + (128 * (kt - q.i) + key - 32 * part + p.bias.md + kPad);
       }
+      ok = ok && wait_warp(bar(L::vecfull + buf), (it >> 1) & 1, w);
+      const float4* nl4 = reinterpret_cast<const float4*>(vec + 256 * buf + 32 * part);
+      const float4* nd4 = reinterpret_cast<const float4*>(vec + 256 * buf + 128 + 32 * part);
+      ok = ok && wait_warp(bar(L::sfull), it & 1, w);
+      tc_fence_after();
+      uint32_t s[32];
+      tmem_ld32_issue(tSw, s);
+      tmem_ld32_wait(s);
+      const uint64_t add2v = pack2(add, add);
 #pragma unroll
-      for (int c = 0; c < 64; c += 2) {
-        const float4 q = v4[c >> 1];  // (lse, D) of columns c and c + 1
-        float o0 = add - q.x, o1 = add - q.z;
-        if (BIAS && near) {
-          o0 = tb[-c] - q.x;
-          o1 = tb[-c - 1] - q.z;
+      for (int c = 0; c < 32; c += 4) {
+        const float4 n = nl4[c >> 2];
+        uint64_t o0 = pack2(n.x, n.y), o1 = pack2(n.z, n.w);
+        if (BIAS) {
+          if (near) {
+            o0 = add2(o0, pack2(tb[-c], tb[-c - 1]));
+            o1 = add2(o1, pack2(tb[-c - 2], tb[-c - 3]));
+          } else {
+            o0 = add2(o0, add2v);
+            o1 = add2(o1, add2v);
+          }
         }
-        s[c] = __float_as_uint(ex2_ftz(fmaf(as_f(s[c]), sl2, o0)));
-        s[c + 1] = __float_as_uint(ex2_ftz(fmaf(as_f(s[c + 1]), sl2, o1)));
+        float x0, x1, x2, x3;
+        unpack2(fma2(pack2(as_f(s[c]), as_f(s[c + 1])), scl2, o0), x0, x1);
+        unpack2(fma2(pack2(as_f(s[c + 2]), as_f(s[c + 3])), scl2, o1), x2, x3);
+        s[c] = __float_as_uint(ex2_ftz(x0));
+        s[c + 1] = __float_as_uint(ex2_ftz(x1));
+        s[c + 2] = __float_as_uint(ex2_ftz(x2));
+        s[c + 3] = __float_as_uint(ex2_ftz(x3));
       }
-      if (p.causal && i == kt) {
-        const int first = key - 64 * half;  // the first query column that sees this key
+      if (p.causal && q.i == kt) {
+        const int first = key - 32 * part;  // the first query column that sees this key
 #pragma unroll
-        for (int c = 0; c < 64; ++c) s[c] = c >= first ? s[c] : 0u;
+        for (int c = 0; c < 32; ++c) s[c] = c >= first ? s[c] : 0u;
       }
-      uint32_t pk[32];
+      uint32_t pk[16];
 #pragma unroll
-      for (int c = 0; c < 32; ++c) pk[c] = pack_bf16x2(as_f(s[2 * c]), as_f(s[2 * c + 1]));
-      tmem_st32(tS + lb + 64 * half, pk);
+      for (int c = 0; c < 16; ++c) pk[c] = pack_bf16x2(as_f(s[2 * c]), as_f(s[2 * c + 1]));
+      tmem_st16(tSw, pk);
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(L::pready));
       ok = ok && wait_warp(bar(L::dpfull), it & 1, w);
       tc_fence_after();
-      uint32_t g[64];
-      tmem_ld32_issue(tP + lb + 64 * half, g);
-      tmem_ld32_issue(tP + lb + 64 * half + 32, g + 32);
+      uint32_t g[32];
+      tmem_ld32_issue(tPw, g);
       tmem_ld32_wait(g);
-      tmem_ld32_wait(g + 32);
 #pragma unroll
-      for (int c = 0; c < 64; c += 2) {
-        const float4 q = v4[c >> 1];
-        const float a = as_f(s[c]) * (as_f(g[c]) - q.y);
-        const float b = as_f(s[c + 1]) * (as_f(g[c + 1]) - q.w);
+      for (int c = 0; c < 32; c += 4) {
+        const float4 n = nd4[c >> 2];
+        float a, b;
+        unpack2(mul2(pack2(as_f(s[c]), as_f(s[c + 1])), add2(pack2(as_f(g[c]), as_f(g[c + 1])), pack2(n.x, n.y))), a, b);
         pk[c >> 1] = pack_bf16x2(a, b);
+        unpack2(mul2(pack2(as_f(s[c + 2]), as_f(s[c + 3])), add2(pack2(as_f(g[c + 2]), as_f(g[c + 3])), pack2(n.z, n.w))), a, b);
+        pk[(c >> 1) + 1] = pack_bf16x2(a, b);
       }
-      tmem_st32(tP + lb + 64 * half, pk);
+      tmem_st16(tPw, pk);
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(bar(L::dsready));
+      if (lane == 0) {
+        mbar_arrive(bar(L::dsready));
+        mbar_arrive(bar(L::vecempty + buf));
+      }
     }
     if (ok && wait_warp(bar(L::done), 0, w)) {
       tc_fence_after();
-      // warps 0-3 store dV, warps 4-7 dK
+      // dV by the first half of the warps, dK by the second; two warps share a row
+      const int which = part >> 1, cut = first_columns(p.d);
+      const int first = part & 1 ? cut : 0, n = part & 1 ? p.d - cut : cut;
       const int pos = 128 * kt + key;
       const HeadAt hk = head_at(kvh, p.hk);
       const int64_t col = static_cast<int64_t>(hk.shard) * p.shard_w + static_cast<int64_t>(p.hq) * p.d +
-                          static_cast<int64_t>(hk.local + (half ? 0 : p.hk)) * p.d;
-      store_row((half ? tdK : tdV) + lb, p.d, half ? p.scale : 1.f,
+                          static_cast<int64_t>(hk.local + (which ? 0 : p.hk)) * p.d + first;
+      store_row((which ? tdK : tdV) + lb + first, n, which ? p.scale : 1.f,
                 static_cast<__nv_bfloat16*>(p.dQKV) + (static_cast<int64_t>(start) + pos) * p.ld_dqkv + col,
                 pos < len);
     }
@@ -1055,71 +1148,72 @@ __global__ void __launch_bounds__(kBwdThreads, 1) rc_dkv_kernel(const __grid_con
   leave<kBwdWarps>(hd);
 }
 
+// TMEM: scores [0, 128), dP and then dS [128, 256), dQ [256, 384), Q [384, 448)
+// and dC [448, 512).  Q and dC stay there for the whole row of key tiles: the
+// products read K and V from shared memory alone (both operands there would
+// take all of its bandwidth), and three tiles of each fit.
 template <int DP>
 struct DqShape {
   static constexpr int kTile = DP / 64 * kPanel;
-  static constexpr int kStages = DP == 128 ? 2 : 4;  // K tiles and V tiles held, each
-  static constexpr int kSmem = 2 * kTile + 2 * kStages * kTile + kBarBytes + 1024;
+  static constexpr int kStages = DP == 128 ? 3 : 4;  // K tiles and V tiles held, each
+  static constexpr int kSmem = 2 * kStages * kTile + kBarBytes + 1024;
   static constexpr int qfull = 0, kfull = 1, vfull = kfull + kStages, tail = vfull + kStages, kempty = tail + 1,
-                       vempty = kempty + kStages, sfull = vempty + kStages, dpfull = sfull + 2, dsready = dpfull + 1,
-                       done = dsready + 1, drain = done + 1, count = drain + 1;
+                       vempty = kempty + kStages, sfull = vempty + kStages, sread = sfull + 1, dpfull = sread + 1,
+                       dsready = dpfull + 1, done = dsready + 1, drain = done + 1, count = drain + 1;
   static_assert(count <= 40 && kempty <= 32, "barriers");
+  static uint32_t __device__ __forceinline__ arrivals(int i) {
+    return i == dsready || i == sread || i == qfull ? kBwdWarps : 1u;
+  }
 };
-// The bias gradient's shared memory: per compute warp the sums of its 32 x 64
-// block by distance (95 of them), the CTA's sums by clamped distance, and the
+// The bias gradient's shared memory: per compute warp the sums of its 32 x 32
+// block by distance (63 of them), the CTA's sums by clamped distance, and the
 // threads' sums beyond the ends.
-constexpr int kDiag = 96;
-__host__ __device__ constexpr int grad_floats(int md) { return 8 * kDiag + 2 * md + 1 + 2 * 256; }
+constexpr int kDiag = 64;
+__host__ __device__ constexpr int grad_floats(int md) {
+  return kBwdWarps * kDiag + 2 * md + 1 + 2 * 32 * kBwdWarps;
+}
 
 template <int DP, bool BIAS>
-__global__ void __launch_bounds__(kBwdThreads, 1) rc_dq_kernel(const __grid_constant__ RcParams p) {
+__global__ void __launch_bounds__(kDqThreads, 1) rc_dq_kernel(const __grid_constant__ RcParams p) {
   using L = DqShape<DP>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = align1024(smem_raw);
-  uint8_t* sQ = smem;
-  uint8_t* sO = sQ + L::kTile;
-  uint8_t* sK = sO + L::kTile;
+  uint8_t* sK = smem;
   uint8_t* sV = sK + L::kStages * L::kTile;
   Head* hd = reinterpret_cast<Head*>(sV + L::kStages * L::kTile);
   float* tab = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(hd) + kBarBytes);
   const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
   const int head = static_cast<int>(blockIdx.x % p.H);
   const int64_t unit = blockIdx.x / p.H;
-  enter<kBwdWarps, kBwdWarps + 1>(p, hd, L::count, [](int i) { return i == L::dsready ? 8u : 1u; }, unit, 128, p.causal != 0);
+  enter<kBwdWarps, kBwdWarps + 1>(p, hd, L::count, L::arrivals, unit, 128, p.causal != 0);
   const bool grad = BIAS && p.partial != nullptr;
   const int md = BIAS ? p.bias.md : 0;
-  float* diag = tab + (BIAS ? table_floats(md) : 0);  // [8][kDiag]
-  float* bins = diag + 8 * kDiag;                     // [2 md + 1]
-  float* ends = bins + 2 * md + 1;                    // [2][256]
+  float* diag = tab + (BIAS ? table_floats(md) : 0);  // [kBwdWarps][kDiag]
+  float* bins = diag + kBwdWarps * kDiag;             // [2 md + 1]
+  float* ends = bins + 2 * md + 1;                    // [2][32 kBwdWarps]
   if (BIAS) {
-    if (hd->found) fill_table(p, head, tab, kBwdThreads);
+    if (hd->found) fill_table(p, head, tab, kDqThreads);
     if (grad)
-      for (int i = threadIdx.x; i < 2 * md + 1; i += kBwdThreads) bins[i] = 0.f;
+      for (int i = threadIdx.x; i < 2 * md + 1; i += kDqThreads) bins[i] = 0.f;
     __syncthreads();
   }
   const uint32_t bar0 = smem_addr(hd->bar);
   auto bar = [&](int i) { return bar0 + 8u * i; };
   const WaitCtx w{&hd->abort_flag, p.err, p.wait_limit_ns};
   const uint32_t tmem = uniform(hd->tmem);
-  const uint32_t tP = tmem + 256, tdQ = tmem + 384;
+  const uint32_t tP = tmem + 128, tdQ = tmem + 256, tQ = tmem + 384, tO = tmem + 448;
   const int start = uniform(hd->start), len = uniform(hd->len), r0 = 128 * uniform(hd->tile);
   const int nk_all = (len + 127) >> 7;
   const int nk = uniform(hd->found) ? (p.causal ? min(nk_all, (r0 >> 7) + 1) : nk_all) : 0;
 
   if (warp == kBwdWarps + 1 && nk > 0) {
-    const HeadAt hq = head_at(head, p.hq), hk = head_at(head / p.group, p.hk);
+    const HeadAt hk = head_at(head / p.group, p.hk);
     Flight fl;
     uint32_t tail_phase = 0;
     bool ok = true, skip = p.fault_skip != 0;
     if (lane == 0) {
       prefetch_tmap(&p.mapK);
       prefetch_tmap(&p.mapV);
-      if (!skip) {
-        mbar_arrive_expect_tx(bar(L::qfull), 2 * L::kTile);
-        fl.note(L::qfull, 0);
-        load_tile<DP>(smem_addr(sQ), &p.mapQ, bar(L::qfull), start + r0, hq);
-        load_tile<DP>(smem_addr(sO), &p.mapO, bar(L::qfull), start + r0, hq);
-      }
     }
     for (int j = 0; ok && j < nk; ++j) {
       const int st = j % L::kStages;
@@ -1131,11 +1225,12 @@ __global__ void __launch_bounds__(kBwdThreads, 1) rc_dq_kernel(const __grid_cons
         ok = load_tail<DP>(sK + st * L::kTile, &p.mapK, bar(L::kfull + st), bar(L::tail), tail_phase,
                            start + 128 * j, hk, len - 128 * j, lane, w);
         if (!ok) break;
-      } else if (lane == 0) {
+      } else if (lane == 0 && !skip) {
         mbar_arrive_expect_tx(bar(L::kfull + st), L::kTile);
         fl.note(L::kfull + st, ph);
         load_tile<DP>(smem_addr(sK + st * L::kTile), &p.mapK, bar(L::kfull + st), start + 128 * j, hk);
       }
+      skip = false;
       if (lane == 0) {
         ok = wait_bounded(bar(L::vempty + st), ph ^ 1u, w);
         if (ok) {
@@ -1149,123 +1244,137 @@ __global__ void __launch_bounds__(kBwdThreads, 1) rc_dq_kernel(const __grid_cons
     if (lane == 0 && *w.abort_flag) fl.drain(bar0, p.wait_limit_ns);
     __syncwarp();
   } else if (warp == kBwdWarps && nk > 0) {
+    // After dS of a tile: dQ += dS K, dP = dC V^T of the next tile in dS's place,
+    // and last the scores S = Q K^T of the one after, which nobody waits for yet:
+    // they run while the compute warps make the next dS.
     const int ksteps = (p.d + 15) >> 4;
     const uint32_t idesc_out = idesc_bf16(0, 1, ksteps * 16);
-    bool ok = true, issued = false;
+    auto kwait = [&](int j) { return wait_warp(bar(L::kfull + j % L::kStages), (j / L::kStages) & 1, w); };
+    auto vwait = [&](int j) { return wait_warp(bar(L::vfull + j % L::kStages), (j / L::kStages) & 1, w); };
     auto scores = [&](int j) {
-      issued = true;
+      tc_fence_after();
       if (elect_one()) {
-        mma_scores<DP>(tmem + 128 * (j & 1), smem_addr(sQ), smem_addr(sK + (j % L::kStages) * L::kTile), ksteps);
-        mma_commit(bar(L::sfull + (j & 1)));
+        mma_scores_ts<DP>(tmem, tQ, smem_addr(sK + (j % L::kStages) * L::kTile), ksteps);
+        mma_commit(bar(L::sfull));
       }
       __syncwarp();
     };
-    auto dprobs = [&](int j) {
-      if (elect_one()) {
-        mma_scores<DP>(tP, smem_addr(sO), smem_addr(sV + (j % L::kStages) * L::kTile), ksteps);
-        mma_commit(bar(L::dpfull));
-        mma_commit(bar(L::vempty + j % L::kStages));
-      }
-      __syncwarp();
-    };
-    ok = wait_warp(bar(L::qfull), 0, w) && wait_warp(bar(L::kfull), 0, w);
-    if (ok) {
-      tc_fence_after();
-      scores(0);
-      ok = wait_warp(bar(L::vfull), 0, w);
-    }
-    if (ok) {
-      tc_fence_after();
-      dprobs(0);
-    }
-    for (int j = 0; ok && j < nk; ++j) {
+    bool ok = wait_warp(bar(L::qfull), 0, w) && kwait(0), issued = ok;
+    if (ok) scores(0);
+    for (int j = -1; ok && j < nk; ++j) {
       const int st = j % L::kStages, sn = (j + 1) % L::kStages;
-      const uint32_t pn = ((j + 1) / L::kStages) & 1;
-      const bool more = j + 1 < nk;
-      if (more) {
-        // into the other score buffer: dS of tile j - 1 there has been read by
-        // its product, issued before
-        if (!(ok = wait_warp(bar(L::kfull + sn), pn, w))) break;
-        tc_fence_after();
-        scores(j + 1);
-      }
-      if (!(ok = wait_warp(bar(L::dsready), j & 1, w))) break;
+      if (j + 1 < nk && !(ok = vwait(j + 1))) break;
+      if (j >= 0 && !(ok = wait_warp(bar(L::dsready), j & 1, w))) break;
       tc_fence_after();
       if (elect_one()) {
-        mma_rows<0, 4>(tdQ, tmem + 128 * (j & 1), smem_addr(sK + st * L::kTile), idesc_out, j > 0);
-        mma_commit(bar(L::kempty + st));
-        if (!more) mma_commit(bar(L::done));
+        if (j >= 0) {
+          mma_rows<4>(tdQ, tP, smem_addr(sK + st * L::kTile), idesc_out, j > 0);
+          mma_commit(bar(L::kempty + st));
+        }
+        if (j + 1 < nk) {
+          mma_scores_ts<DP>(tP, tO, smem_addr(sV + sn * L::kTile), ksteps);
+          mma_commit(bar(L::dpfull));
+          mma_commit(bar(L::vempty + sn));
+        } else {
+          mma_commit(bar(L::done));
+        }
       }
       __syncwarp();
-      if (more) {
-        if (!(ok = wait_warp(bar(L::vfull + sn), pn, w))) break;
-        tc_fence_after();
-        dprobs(j + 1);
+      if (j + 2 < nk) {
+        if (!(ok = kwait(j + 2) && wait_warp(bar(L::sread), (j + 1) & 1, w))) break;
+        scores(j + 2);
       }
     }
     if (*w.abort_flag && issued && elect_one()) drain_mma(bar(L::drain), p.wait_limit_ns);
-  } else if (warp < 8) {
-    const int half = warp >> 2;
+  } else if (warp < kBwdWarps) {
+    const int part = warp >> 2;  // the 32 key columns of this warp
     const int quarter = warp & 3;
     const int row = r0 + quarter * 32 + lane;
     const bool mine = row < len;
     const int64_t token = static_cast<int64_t>(start) + row;
     const uint32_t lb = static_cast<uint32_t>(quarter * 32) << 16;
-    const float sl2 = p.scale_log2;
-    float lse2 = 0.f, D = 0.f;
+    const uint64_t scl2 = pack2(p.scale_log2, p.scale_log2);
+    float nl = 0.f, nd = 0.f;
     if (nk > 0 && mine) {
-      lse2 = p.lse[static_cast<int64_t>(head) * p.T + token] * kLog2e;
-      D = p.D[static_cast<int64_t>(head) * p.T + token];
+      nl = -p.lse[static_cast<int64_t>(head) * p.T + token] * kLog2e;
+      nd = -p.D[static_cast<int64_t>(head) * p.T + token];
+    }
+    const uint64_t nd2 = pack2(nd, nd);
+    if (nk > 0) {
+      // this warp's quarter of the columns of Q and dC into TMEM (zeros past the
+      // head and the sequence)
+      const HeadAt hq = head_at(head, p.hq);
+      const int64_t qcol = static_cast<int64_t>(hq.shard) * p.shard_w + static_cast<int64_t>(hq.local) * p.d;
+      constexpr int kCols = DP / 4;
+      const int first = kCols * part;
+      fill_tmem_rows<kCols>(tQ + lb + first / 2,
+                            static_cast<const __nv_bfloat16*>(p.QKV) + token * p.ld_qkv + qcol + first,
+                            mine ? p.d - first : 0);
+      fill_tmem_rows<kCols>(tO + lb + first / 2,
+                            static_cast<const __nv_bfloat16*>(p.dC) + token * p.ld_dc +
+                                static_cast<int64_t>(head) * p.d + first,
+                            mine ? p.d - first : 0);
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(L::qfull));
     }
     float end_lo = 0.f, end_hi = 0.f;  // dS at distances <= -md and >= md
     // After a failed wait the loop runs on without waiting: the named barriers
     // below need every warp, and nothing of the gradient is stored.
     bool ok = true;
     for (int j = 0; j < nk; ++j) {
-      const uint32_t tS = tmem + 128 * (j & 1) + lb + 64 * half;
-      const int c0 = 128 * j + 64 * half;  // key position of this warp's first column
-      ok = ok && wait_warp(bar(L::sfull + (j & 1)), (j >> 1) & 1, w);
-      tc_fence_after();
-      uint32_t s[64];
-      tmem_ld32_issue(tS, s);
-      tmem_ld32_issue(tS + 32, s + 32);
-      tmem_ld32_wait(s);
-      tmem_ld32_wait(s + 32);
+      const int c0 = 128 * j + 32 * part;  // key position of this warp's first column
       int side = 0;
-      float off = -lse2;
+      float off = nl;
+      const float* tb = nullptr;
       if (BIAS) {
         side = bias_side(md, r0, 128 * j);
-        if (side != 0) {
-          off += tab[side < 0 ? 0 : table_floats(md) - 1];
-        } else {
-          const float* tb = tab + (c0 - row + md + kPad);
-#pragma unroll
-          for (int c = 0; c < 64; ++c) s[c] = __float_as_uint(ex2_ftz(fmaf(as_f(s[c]), sl2, tb[c] + off)));
-        }
+        if (side != 0) off += tab[side < 0 ? 0 : table_floats(md) - 1];
+        tb = tab + (c0 - row + md + kPad);
       }
-      if (!BIAS || side != 0) {
+      const uint64_t off2 = pack2(off, off);
+      ok = ok && wait_warp(bar(L::sfull), j & 1, w);
+      tc_fence_after();
+      uint32_t s[32];
+      tmem_ld32_issue(tmem + lb + 32 * part, s);
+      tmem_ld32_wait(s);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(L::sread));
 #pragma unroll
-        for (int c = 0; c < 64; ++c) s[c] = __float_as_uint(ex2_ftz(fmaf(as_f(s[c]), sl2, off)));
+      for (int c = 0; c < 32; c += 2) {
+        uint64_t o = off2;
+        if (BIAS) {
+          if (side == 0) o = add2(o, pack2(tb[c], tb[c + 1]));
+        }
+        float x0, x1;
+        unpack2(fma2(pack2(as_f(s[c]), as_f(s[c + 1])), scl2, o), x0, x1);
+        s[c] = __float_as_uint(ex2_ftz(x0));
+        s[c + 1] = __float_as_uint(ex2_ftz(x1));
       }
       const bool masked = (p.causal && 128 * j + 127 > r0) || 128 * j + 128 > len;
       ok = ok && wait_warp(bar(L::dpfull), j & 1, w);
       tc_fence_after();
-      uint32_t g[64];
-      tmem_ld32_issue(tP + lb + 64 * half, g);
-      tmem_ld32_issue(tP + lb + 64 * half + 32, g + 32);
+      uint32_t g[32];
+      tmem_ld32_issue(tP + lb + 32 * part, g);
       tmem_ld32_wait(g);
-      tmem_ld32_wait(g + 32);
 #pragma unroll
-      for (int c = 0; c < 64; ++c) s[c] = __float_as_uint(as_f(s[c]) * (as_f(g[c]) - D));
+      for (int c = 0; c < 32; c += 2) {
+        float a, b;
+        unpack2(mul2(pack2(as_f(s[c]), as_f(s[c + 1])), add2(pack2(as_f(g[c]), as_f(g[c + 1])), nd2)), a, b);
+        s[c] = __float_as_uint(a);
+        s[c + 1] = __float_as_uint(b);
+      }
       if (masked) {
         const int seen = (p.causal ? min(len, row + 1) : len) - c0;
 #pragma unroll
-        for (int c = 0; c < 64; ++c) s[c] = c < seen ? s[c] : 0u;
+        for (int c = 0; c < 32; ++c) s[c] = c < seen ? s[c] : 0u;
       }
-      uint32_t pk[32];
+      uint32_t pk[16];
 #pragma unroll
-      for (int c = 0; c < 32; ++c) pk[c] = pack_bf16x2(as_f(s[2 * c]), as_f(s[2 * c + 1]));
-      tmem_st32(tS, pk);
+      for (int c = 0; c < 16; ++c) pk[c] = pack_bf16x2(as_f(s[2 * c]), as_f(s[2 * c + 1]));
+      tmem_st16(tP + lb + 32 * part, pk);
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
@@ -1274,67 +1383,68 @@ __global__ void __launch_bounds__(kBwdThreads, 1) rc_dq_kernel(const __grid_cons
         if (side != 0) {
           float a[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-          for (int c = 0; c < 64; ++c) a[c & 3] += as_f(s[c]);
+          for (int c = 0; c < 32; ++c) a[c & 3] += as_f(s[c]);
           const float sum = mine ? (a[0] + a[1]) + (a[2] + a[3]) : 0.f;
           if (side < 0) end_lo += sum;
           else end_hi += sum;
         } else {
-          // Sums along the diagonals of the warp's 32 x 64 block: the running
+          // Sums along the diagonals of the warp's 32 x 32 block: the running
           // sum of a diagonal moves one lane up at every column; it is whole
           // when it leaves lane 31.
           float* dw = diag + warp * kDiag;
           float acc = 0.f;
 #pragma unroll
-          for (int c = 0; c < 64; ++c) {
+          for (int c = 0; c < 32; ++c) {
             const float up = __shfl_up_sync(0xffffffffu, acc, 1);
             acc = (lane == 0 ? 0.f : up) + (mine ? as_f(s[c]) : 0.f);
             if (lane == 31) dw[c] = acc;  // distance (c - 31) + block offset
           }
-          if (lane < 31) dw[94 - lane] = acc;
-          named_bar(1, 256);
+          if (lane < 31) dw[62 - lane] = acc;
+          named_bar(1, 32 * kBwdWarps);
           // thread x sums distance x - 127 of the tile over the warps' blocks
           if (threadIdx.x < 255) {
             const int dt = static_cast<int>(threadIdx.x) - 127;
             float sum = 0.f;
 #pragma unroll
-            for (int wv = 0; wv < 8; ++wv) {
-              const int at = dt - 64 * (wv >> 2) + 32 * (wv & 3) + 31;
-              if (at >= 0 && at < 95) sum += diag[wv * kDiag + at];
+            for (int wv = 0; wv < kBwdWarps; ++wv) {
+              const int at = dt - 32 * (wv >> 2) + 32 * (wv & 3) + 31;
+              if (at >= 0 && at < 63) sum += diag[wv * kDiag + at];
             }
             const int delta = 128 * j - r0 + dt;
             if (delta <= -md) end_lo += sum;
             else if (delta >= md) end_hi += sum;
             else bins[delta + md] += sum;
           }
-          named_bar(1, 256);
+          named_bar(1, 32 * kBwdWarps);
         }
       }
     }
     if (nk > 0 && ok && wait_warp(bar(L::done), 0, w)) {
       tc_fence_after();
-      // each half of the warps stores half of the columns
-      const int cut = min(p.d, 32 * ((p.d + 63) / 64));
-      const int first = half ? cut : 0, n = half ? p.d - cut : cut;
+      // the columns in 32s over the warps of a row
+      const int first = 32 * part, n = min(p.d - first, 32);
       const HeadAt hq = head_at(head, p.hq);
-      store_row(tdQ + lb + first, n, p.scale,
-                static_cast<__nv_bfloat16*>(p.dQKV) + token * p.ld_dqkv +
-                    static_cast<int64_t>(hq.shard) * p.shard_w + static_cast<int64_t>(hq.local) * p.d + first,
-                mine);
+      if (n > 0)
+        store_row(tdQ + lb + first, n, p.scale,
+                  static_cast<__nv_bfloat16*>(p.dQKV) + token * p.ld_dqkv +
+                      static_cast<int64_t>(hq.shard) * p.shard_w + static_cast<int64_t>(hq.local) * p.d + first,
+                  mine);
     }
     if (BIAS && grad) {
       // the CTA's sums by bucket, in a fixed order
+      constexpr int kN = 32 * kBwdWarps;
       ends[threadIdx.x] = end_lo;
-      ends[256 + threadIdx.x] = end_hi;
-      named_bar(1, 256);
+      ends[kN + threadIdx.x] = end_hi;
+      named_bar(1, kN);
       if (warp < 2) {
         float a = 0.f;
-        for (int x = lane; x < 256; x += 32) a += ends[256 * warp + x];
+        for (int x = lane; x < kN; x += 32) a += ends[kN * warp + x];
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
         if (lane == 0) bins[warp ? 2 * md : 0] = a;
       }
-      named_bar(1, 256);
-      for (int u = threadIdx.x; u < p.bias.nb; u += 256) {
+      named_bar(1, kN);
+      for (int u = threadIdx.x; u < p.bias.nb; u += kN) {
         // bucket u holds the distances n with first[k] <= n < first[k + 1] on its side
         const int k = u % p.bias.side;
         const bool pos = p.bias.both && u >= p.bias.side;
@@ -1399,10 +1509,10 @@ template <int DP, bool BIAS>
 cudaError_t bwd_t(RcParams& p, cudaStream_t st) {
   const int64_t units = units_of(p, 128);
   const int tab = BIAS ? 4 * table_floats(p.bias.md) : 0;
-  cudaError_t e = launch_rc(rc_dkv_kernel<DP, BIAS>, units * p.KV, kBwdThreads, DkvShape<DP>::kSmem + tab, p, st);
+  cudaError_t e = launch_rc(rc_dkv_kernel<DP, BIAS>, units * p.KV, kDkvThreads, (DkvShape<DP, BIAS>::kSmem) + tab, p, st);
   p.fault_skip = 0;
   if (e != cudaSuccess) return e;
-  e = launch_rc(rc_dq_kernel<DP, BIAS>, units * p.H, kBwdThreads,
+  e = launch_rc(rc_dq_kernel<DP, BIAS>, units * p.H, kDqThreads,
                 DqShape<DP>::kSmem + tab + (BIAS ? 4 * grad_floats(p.bias.md) : 0), p, st);
   if (e != cudaSuccess || !BIAS || p.partial == nullptr) return e;
   launch_k(rc_bias_sum_kernel, dim3(p.H, p.bias.nb), dim3(128), 0, st, p, units);

@@ -198,13 +198,14 @@ struct RcBias {
 struct RcParams {
   CUtensorMap mapQ, mapK, mapV, mapO;  // 4D (d, token, head of the shard, shard); mapO: dC
   const int64_t* seq_starts;           // device, b + 1 values, or null: b sequences of s tokens
-  int64_t T, ld_c, ld_dc, ld_dqkv;
+  int64_t T, ld_qkv, ld_c, ld_dc, ld_dqkv;
   int b, s, H, KV, d, causal;
   int group;    // query heads a K/V head
   int hq, hk;   // query and K/V heads a shard
   int shard_w;  // columns of one shard in QKV
   int sub;      // query tiles a CTA (forward; set by the launcher)
   float scale, scale_log2;
+  const void* QKV;
   void* C;          // forward out, backward in
   float* lse;       // forward out, backward in; (H, T)
   const void* dC;
