@@ -135,6 +135,12 @@ __device__ __forceinline__ void tmem_scale8(uint32_t taddr, float f) {
                "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(taddr)
                : "memory");
 }
+// The same registers as they are.
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t* r) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%8], {%0, %1, %2, %3, %4, %5, %6, %7};" ::"r"(r[0]),
+               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(taddr)
+               : "memory");
+}
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 __device__ __forceinline__ void named_bar(int id, int threads) {
@@ -857,11 +863,11 @@ struct DkvShape {
   static constexpr int kSmem = (2 + kQ + kO) * kTile + kBarBytes + kVec;
   static constexpr int kvfull = 0, qfull = 1, ofull = qfull + kQ, tail = ofull + kO, qempty = tail + 1,
                        oempty = qempty + kQ, vecfull = oempty + kO, vecempty = vecfull + 2, sfull = vecempty + 2,
-                       dpfull = sfull + 1, pready = dpfull + 1, dsready = pready + 1, done = dsready + 1,
+                       dpfull = sfull + 1, pready = dpfull + 1, dsready = pready + 2, done = dsready + 2,
                        drain = done + 1, count = drain + 2;
   static_assert(count <= 40 && qempty <= 32, "barriers");
   static uint32_t __device__ __forceinline__ arrivals(int i) {
-    if (i == pready || i == dsready || i == vecempty || i == vecempty + 1) return kBwdWarps;
+    if ((i >= pready && i < done) || i == vecempty || i == vecempty + 1) return kBwdWarps;
     return i == done || (i >= oempty && i < vecfull) ? 2u : 1u;
   }
 };
@@ -987,13 +993,18 @@ __global__ void __launch_bounds__(kDkvThreads, 1) rc_dkv_kernel(const __grid_con
       if (it + 1 < total && !(ok = wait_warp(bar(L::qfull + sn), ((it + 1) / L::kQ) & 1, w))) break;
       if (it >= 0) {
         if (!(ok = wait_warp(bar(L::ofull + so), (it / L::kO) & 1, w))) break;
+        // P comes in two halves of the contraction (16 of every 32 queries)
         if (!(ok = wait_warp(bar(L::pready), it & 1, w))) break;
+        tc_fence_after();
+        if (elect_one()) mma_rows<4, 0, 1>(tdV, tS, smem_addr(sO + so * L::kTile), idesc_out, it > 0);
+        __syncwarp();
+        if (!(ok = wait_warp(bar(L::pready + 1), it & 1, w))) break;
       }
       tc_fence_after();
       issued = true;
       if (elect_one()) {
         if (it >= 0) {
-          mma_rows<4>(tdV, tS, smem_addr(sO + so * L::kTile), idesc_out, it > 0);
+          mma_rows<4, 1, 1>(tdV, tS, smem_addr(sO + so * L::kTile), idesc_out, true);
           mma_commit(bar(L::oempty + so));
         }
         if (it + 1 < total) {
@@ -1017,12 +1028,16 @@ __global__ void __launch_bounds__(kDkvThreads, 1) rc_dkv_kernel(const __grid_con
       if (it >= 0) {
         if (!(ok = wait_warp(bar(L::qfull + sq), (it / L::kQ) & 1, w))) break;
         if (!(ok = wait_warp(bar(L::dsready), it & 1, w))) break;
+        tc_fence_after();
+        if (elect_one()) mma_rows<4, 0, 1>(tdK, tP, smem_addr(sQ + sq * L::kTile), idesc_out, it > 0);
+        __syncwarp();
+        if (!(ok = wait_warp(bar(L::dsready + 1), it & 1, w))) break;
       }
       tc_fence_after();
       issued = true;
       if (elect_one()) {
         if (it >= 0) {
-          mma_rows<4>(tdK, tP, smem_addr(sQ + sq * L::kTile), idesc_out, it > 0);
+          mma_rows<4, 1, 1>(tdK, tP, smem_addr(sQ + sq * L::kTile), idesc_out, true);
           mma_commit(bar(L::qempty + sq));
         }
         if (it + 1 < total) {
@@ -1074,62 +1089,66 @@ __global__ void __launch_bounds__(kDkvThreads, 1) rc_dkv_kernel(const __grid_con
       tmem_ld32_issue(tSw, s);
       tmem_ld32_wait(s);
       const uint64_t add2v = pack2(add, add);
+      const bool diagonal = p.causal && q.i == kt;
+      const int first = key - 32 * part;  // the first query column that sees this key, on the diagonal
 #pragma unroll
-      for (int c = 0; c < 32; c += 4) {
-        const float4 n = nl4[c >> 2];
-        uint64_t o0 = pack2(n.x, n.y), o1 = pack2(n.z, n.w);
-        if (BIAS) {
-          if (near) {
-            o0 = add2(o0, pack2(tb[-c], tb[-c - 1]));
-            o1 = add2(o1, pack2(tb[-c - 2], tb[-c - 3]));
-          } else {
-            o0 = add2(o0, add2v);
-            o1 = add2(o1, add2v);
+      for (int h = 0; h < 2; ++h) {
+        uint32_t pk[8];
+#pragma unroll
+        for (int c = 16 * h; c < 16 * h + 16; c += 4) {
+          const float4 n = nl4[c >> 2];
+          uint64_t o0 = pack2(n.x, n.y), o1 = pack2(n.z, n.w);
+          if (BIAS) {
+            if (near) {
+              o0 = add2(o0, pack2(tb[-c], tb[-c - 1]));
+              o1 = add2(o1, pack2(tb[-c - 2], tb[-c - 3]));
+            } else {
+              o0 = add2(o0, add2v);
+              o1 = add2(o1, add2v);
+            }
           }
+          float x[4];
+          unpack2(fma2(pack2(as_f(s[c]), as_f(s[c + 1])), scl2, o0), x[0], x[1]);
+          unpack2(fma2(pack2(as_f(s[c + 2]), as_f(s[c + 3])), scl2, o1), x[2], x[3]);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[c + e] = __float_as_uint(ex2_ftz(x[e]));
         }
-        float x0, x1, x2, x3;
-        unpack2(fma2(pack2(as_f(s[c]), as_f(s[c + 1])), scl2, o0), x0, x1);
-        unpack2(fma2(pack2(as_f(s[c + 2]), as_f(s[c + 3])), scl2, o1), x2, x3);
-        s[c] = __float_as_uint(ex2_ftz(x0));
-        s[c + 1] = __float_as_uint(ex2_ftz(x1));
-        s[c + 2] = __float_as_uint(ex2_ftz(x2));
-        s[c + 3] = __float_as_uint(ex2_ftz(x3));
-      }
-      if (p.causal && q.i == kt) {
-        const int first = key - 32 * part;  // the first query column that sees this key
+        if (diagonal) {
 #pragma unroll
-        for (int c = 0; c < 32; ++c) s[c] = c >= first ? s[c] : 0u;
-      }
-      uint32_t pk[16];
+          for (int c = 16 * h; c < 16 * h + 16; ++c) s[c] = c >= first ? s[c] : 0u;
+        }
 #pragma unroll
-      for (int c = 0; c < 16; ++c) pk[c] = pack_bf16x2(as_f(s[2 * c]), as_f(s[2 * c + 1]));
-      tmem_st16(tSw, pk);
-      tmem_st_wait();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(L::pready));
+        for (int c = 0; c < 8; ++c) pk[c] = pack_bf16x2(as_f(s[16 * h + 2 * c]), as_f(s[16 * h + 2 * c + 1]));
+        tmem_st8(tSw + 8 * h, pk);
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(L::pready + h));
+      }
       ok = ok && wait_warp(bar(L::dpfull), it & 1, w);
       tc_fence_after();
       uint32_t g[32];
       tmem_ld32_issue(tPw, g);
       tmem_ld32_wait(g);
 #pragma unroll
-      for (int c = 0; c < 32; c += 4) {
-        const float4 n = nd4[c >> 2];
-        float a, b;
-        unpack2(mul2(pack2(as_f(s[c]), as_f(s[c + 1])), add2(pack2(as_f(g[c]), as_f(g[c + 1])), pack2(n.x, n.y))), a, b);
-        pk[c >> 1] = pack_bf16x2(a, b);
-        unpack2(mul2(pack2(as_f(s[c + 2]), as_f(s[c + 3])), add2(pack2(as_f(g[c + 2]), as_f(g[c + 3])), pack2(n.z, n.w))), a, b);
-        pk[(c >> 1) + 1] = pack_bf16x2(a, b);
+      for (int h = 0; h < 2; ++h) {
+        uint32_t pk[8];
+#pragma unroll
+        for (int c = 16 * h; c < 16 * h + 16; c += 4) {
+          const float4 n = nd4[c >> 2];
+          float a, b;
+          unpack2(mul2(pack2(as_f(s[c]), as_f(s[c + 1])), add2(pack2(as_f(g[c]), as_f(g[c + 1])), pack2(n.x, n.y))), a, b);
+          pk[(c >> 1) & 7] = pack_bf16x2(a, b);
+          unpack2(mul2(pack2(as_f(s[c + 2]), as_f(s[c + 3])), add2(pack2(as_f(g[c + 2]), as_f(g[c + 3])), pack2(n.z, n.w))), a, b);
+          pk[((c >> 1) & 7) + 1] = pack_bf16x2(a, b);
+        }
+        tmem_st8(tPw + 8 * h, pk);
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(L::dsready + h));
       }
-      tmem_st16(tPw, pk);
-      tmem_st_wait();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(bar(L::dsready));
-        mbar_arrive(bar(L::vecempty + buf));
-      }
+      if (lane == 0) mbar_arrive(bar(L::vecempty + buf));
     }
     if (ok && wait_warp(bar(L::done), 0, w)) {
       tc_fence_after();
@@ -1159,10 +1178,10 @@ struct DqShape {
   static constexpr int kSmem = 2 * kStages * kTile + kBarBytes + 1024;
   static constexpr int qfull = 0, kfull = 1, vfull = kfull + kStages, tail = vfull + kStages, kempty = tail + 1,
                        vempty = kempty + kStages, sfull = vempty + kStages, sread = sfull + 1, dpfull = sread + 1,
-                       dsready = dpfull + 1, done = dsready + 1, drain = done + 1, count = drain + 1;
+                       dsready = dpfull + 1, done = dsready + 2, drain = done + 1, count = drain + 1;
   static_assert(count <= 40 && kempty <= 32, "barriers");
   static uint32_t __device__ __forceinline__ arrivals(int i) {
-    return i == dsready || i == sread || i == qfull ? kBwdWarps : 1u;
+    return i == dsready || i == dsready + 1 || i == sread || i == qfull ? kBwdWarps : 1u;
   }
 };
 // The bias gradient's shared memory: per compute warp the sums of its 32 x 32
@@ -1264,11 +1283,18 @@ __global__ void __launch_bounds__(kDqThreads, 1) rc_dq_kernel(const __grid_const
     for (int j = -1; ok && j < nk; ++j) {
       const int st = j % L::kStages, sn = (j + 1) % L::kStages;
       if (j + 1 < nk && !(ok = vwait(j + 1))) break;
-      if (j >= 0 && !(ok = wait_warp(bar(L::dsready), j & 1, w))) break;
+      if (j >= 0) {
+        // dS comes in two halves of the contraction (16 of every 32 keys)
+        if (!(ok = wait_warp(bar(L::dsready), j & 1, w))) break;
+        tc_fence_after();
+        if (elect_one()) mma_rows<4, 0, 1>(tdQ, tP, smem_addr(sK + st * L::kTile), idesc_out, j > 0);
+        __syncwarp();
+        if (!(ok = wait_warp(bar(L::dsready + 1), j & 1, w))) break;
+      }
       tc_fence_after();
       if (elect_one()) {
         if (j >= 0) {
-          mma_rows<4>(tdQ, tP, smem_addr(sK + st * L::kTile), idesc_out, j > 0);
+          mma_rows<4, 1, 1>(tdQ, tP, smem_addr(sK + st * L::kTile), idesc_out, true);
           mma_commit(bar(L::kempty + st));
         }
         if (j + 1 < nk) {
@@ -1359,26 +1385,29 @@ __global__ void __launch_bounds__(kDqThreads, 1) rc_dq_kernel(const __grid_const
       uint32_t g[32];
       tmem_ld32_issue(tP + lb + 32 * part, g);
       tmem_ld32_wait(g);
+      const int seen = (p.causal ? min(len, row + 1) : len) - c0;
 #pragma unroll
-      for (int c = 0; c < 32; c += 2) {
-        float a, b;
-        unpack2(mul2(pack2(as_f(s[c]), as_f(s[c + 1])), add2(pack2(as_f(g[c]), as_f(g[c + 1])), nd2)), a, b);
-        s[c] = __float_as_uint(a);
-        s[c + 1] = __float_as_uint(b);
+      for (int h = 0; h < 2; ++h) {
+        uint32_t pk[8];
+#pragma unroll
+        for (int c = 16 * h; c < 16 * h + 16; c += 2) {
+          float a, b;
+          unpack2(mul2(pack2(as_f(s[c]), as_f(s[c + 1])), add2(pack2(as_f(g[c]), as_f(g[c + 1])), nd2)), a, b);
+          s[c] = __float_as_uint(a);
+          s[c + 1] = __float_as_uint(b);
+        }
+        if (masked) {
+#pragma unroll
+          for (int c = 16 * h; c < 16 * h + 16; ++c) s[c] = c < seen ? s[c] : 0u;
+        }
+#pragma unroll
+        for (int c = 0; c < 8; ++c) pk[c] = pack_bf16x2(as_f(s[16 * h + 2 * c]), as_f(s[16 * h + 2 * c + 1]));
+        tmem_st8(tP + lb + 32 * part + 8 * h, pk);
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(L::dsready + h));
       }
-      if (masked) {
-        const int seen = (p.causal ? min(len, row + 1) : len) - c0;
-#pragma unroll
-        for (int c = 0; c < 32; ++c) s[c] = c < seen ? s[c] : 0u;
-      }
-      uint32_t pk[16];
-#pragma unroll
-      for (int c = 0; c < 16; ++c) pk[c] = pack_bf16x2(as_f(s[2 * c]), as_f(s[2 * c + 1]));
-      tmem_st16(tP + lb + 32 * part, pk);
-      tmem_st_wait();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(L::dsready));
       if (BIAS && grad) {
         if (side != 0) {
           float a[4] = {0.f, 0.f, 0.f, 0.f};
