@@ -31,6 +31,8 @@
 #include <math.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "tp_device.cuh"
 #include "tp_internal.h"
 #include "tp_tcgen05.cuh"
@@ -38,12 +40,12 @@
 namespace tp {
 namespace {
 
-// Compute warps first, then two MMA warps, the TMA warp and (dK, dV) a warp that
-// stages the rows' lse and D.  The forward has two compute warps on every 32
+// Compute warps first, then the MMA warps, the TMA warp and a warp for tables
+// (forward: the bias of a head; dK, dV: the rows' lse and D).  The forward has two compute warps on every 32
 // rows of a score tile (64 columns each) and two tiles, the backward kernels
 // four (32 columns each).
 constexpr int kFwdWarps = 16, kBwdWarps = 16;
-constexpr int kFwdThreads = 32 * (kFwdWarps + 3), kDkvThreads = 32 * (kBwdWarps + 4), kDqThreads = 32 * (kBwdWarps + 2);
+constexpr int kFwdThreads = 32 * (kFwdWarps + 4), kDkvThreads = 32 * (kBwdWarps + 4), kDqThreads = 32 * (kBwdWarps + 2);
 constexpr int kPanel = 128 * 128;    // bytes of 128 rows x 64 bf16 columns (one swizzle width)
 constexpr int kBarBytes = 512;
 constexpr float kLog2e = 1.4426950408889634f;
@@ -283,10 +285,11 @@ __device__ __forceinline__ int bucket_of(const RcBias& b, int delta) {
   }
   return add + lo;
 }
-// tab[delta + md + kPad] = bias of the clamped distance, times log2 e.
-__device__ __forceinline__ void fill_table(const RcParams& p, int head, float* tab, int threads) {
+// tab[delta + md + kPad] = bias of the clamped distance, times log2 e; by
+// `threads` threads.
+__device__ __forceinline__ void fill_table(const RcParams& p, int head, float* tab, int thread, int threads) {
   const int md = p.bias.md, n = table_floats(md);
-  for (int i = threadIdx.x; i < n; i += threads) {
+  for (int i = thread; i < n; i += threads) {
     const int delta = min(max(i - (md + kPad), -md), md);
     tab[i] = __ldg(p.table + static_cast<int64_t>(bucket_of(p.bias, delta)) * p.H + head) * kLog2e;
   }
@@ -425,27 +428,42 @@ __device__ __forceinline__ void mma_rows(uint32_t d_tmem, uint32_t a_tmem, uint3
 // A row's columns that the first of two warps takes, in 32s.
 __device__ __forceinline__ int first_columns(int d) { return min(d, 32 * ((d + 63) / 64)); }
 
-// One row of d fp32 TMEM columns, scaled, as bf16 to memory.
-__device__ __forceinline__ void store_row(uint32_t taddr, int d, float mul, __nv_bfloat16* out, bool ok) {
-  for (int c = 0; c < d; c += 32) {
-    uint32_t r[32];
-    tmem_ld32_issue(taddr + c, r);
-    tmem_ld32_wait(r);
-    if (ok) {
+// n of COLS fp32 values of a row, scaled, as bf16 to memory; `wide`: every row
+// start is 32-byte aligned and n a multiple of 16.
+template <int COLS>
+__device__ __forceinline__ void store_columns(const uint32_t* v, int n, float mul, __nv_bfloat16* out, bool wide) {
+  const uint64_t mul2v = pack2(mul, mul);
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        if (c + 8 * q < d) {
-          uint4 w;
-          w.x = pack_bf16x2(as_f(r[8 * q + 0]) * mul, as_f(r[8 * q + 1]) * mul);
-          w.y = pack_bf16x2(as_f(r[8 * q + 2]) * mul, as_f(r[8 * q + 3]) * mul);
-          w.z = pack_bf16x2(as_f(r[8 * q + 4]) * mul, as_f(r[8 * q + 5]) * mul);
-          w.w = pack_bf16x2(as_f(r[8 * q + 6]) * mul, as_f(r[8 * q + 7]) * mul);
-          *reinterpret_cast<uint4*>(out + c + 8 * q) = w;
-        }
-      }
+  for (int c = 0; c < COLS; c += 16) {
+    uint32_t q[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      float a, b;
+      unpack2(mul2(pack2(as_f(v[c + 2 * i]), as_f(v[c + 2 * i + 1])), mul2v), a, b);
+      q[i] = pack_bf16x2(a, b);
     }
-    __syncwarp();
+    if (wide) {
+      if (c < n)
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(out + c), "r"(q[0]), "r"(q[1]),
+                     "r"(q[2]), "r"(q[3]), "r"(q[4]), "r"(q[5]), "r"(q[6]), "r"(q[7])
+                     : "memory");
+    } else {
+      if (c < n) *reinterpret_cast<uint4*>(out + c) = make_uint4(q[0], q[1], q[2], q[3]);
+      if (c + 8 < n) *reinterpret_cast<uint4*>(out + c + 8) = make_uint4(q[4], q[5], q[6], q[7]);
+    }
   }
+}
+// n <= 32 CHUNKS fp32 TMEM columns of the warp's rows, scaled, as bf16 to
+// memory.  Called by the whole warp.
+template <int CHUNKS>
+__device__ __forceinline__ void store_row(uint32_t taddr, int n, float mul, __nv_bfloat16* out, bool ok, bool wide) {
+  uint32_t r[32 * CHUNKS];
+#pragma unroll
+  for (int c = 0; c < CHUNKS; ++c) tmem_ld32_issue(taddr + 32 * c, r + 32 * c);
+#pragma unroll
+  for (int c = 0; c < CHUNKS; ++c) tmem_ld32_wait(r + 32 * c);
+  if (ok) store_columns<32 * CHUNKS>(r, n, mul, out, wide);
+  __syncwarp();
 }
 
 // COLS bf16 columns of a row of memory as COLS / 2 TMEM columns; `n` of them
@@ -499,12 +517,14 @@ __device__ __forceinline__ void tmem_dealloc512(uint32_t base) {
 }
 
 // Shared-memory head of every kernel here: barriers, the TMEM address, the
-// abort flag and the CTA's unit.
+// abort flag and the CTA's items.
+constexpr int kMaxBars = 48;
 struct Head {
-  uint64_t bar[40];
+  uint64_t bar[kMaxBars];
   uint32_t tmem;
   int abort_flag;
   int found, start, len, tile;
+  int items[16];
 };
 static_assert(sizeof(Head) <= kBarBytes, "barrier area");
 
@@ -512,18 +532,56 @@ __device__ __forceinline__ uint8_t* align1024(uint8_t* q) {
   return reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(q) + 1023) & ~static_cast<uintptr_t>(1023));
 }
 
-// Common entry: barriers 0 .. nbars-1 with the given counts, TMEM, the unit.
-template <int WARPS, int TMA_WARP, class Counts>
-__device__ __forceinline__ void enter(const RcParams& p, Head* hd, int nbars, Counts&& count, int64_t unit, int rows,
-                                      bool last_first) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+// Items of a launch: unit u of head h is item u * heads + h.  A CTA begins with
+// item blockIdx.x and then takes the next one from a counter of the launch, so
+// long and short items balance whatever their order; the last CTA to leave
+// clears the counters for the next launch with this slot.
+constexpr int kRcSlots = 64;
+__device__ int g_rc_items[2 * kRcSlots];
+struct ItemWalk {
+  int64_t item;
+  int heads, index;  // index: head of the item
+  bool first;
+  __device__ __forceinline__ ItemWalk(const RcParams& p, int n) : item(blockIdx.x), heads(n), index(0), first(true) {}
+  // The next item that has rows, by a whole warp; false: there is none.
+  __device__ __forceinline__ bool next(const RcParams& p, int rows, bool last_first, int lane, Unit& u) {
+    while (true) {
+      if (!first) {
+        int v = 0;
+        if (lane == 0) v = atomicAdd(g_rc_items + 2 * p.slot, 1);
+        item = static_cast<int64_t>(gridDim.x) + __shfl_sync(0xffffffffu, v, 0);
+      }
+      if (item >= p.items) return false;
+      index = static_cast<int>(item % heads);
+      const bool found = find_unit(p, item / heads, rows, last_first, first && blockIdx.x == 0, lane, u);
+      first = false;
+      if (found) return true;
+    }
+  }
+};
+
+// Common entry: barriers 0 .. nbars-1 with the given counts, TMEM.
+template <int WARPS, class Counts>
+__device__ __forceinline__ void enter(Head* hd, int nbars, Counts&& count) {
+  const int warp = threadIdx.x >> 5;
   if (threadIdx.x == 0) {
     for (int i = 0; i < nbars; ++i) mbar_init(smem_addr(hd->bar + i), count(i));
     hd->abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == WARPS) tmem_alloc512(smem_addr(&hd->tmem));
-  if (warp == TMA_WARP) {
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  pdl_wait();
+  pdl_trigger();
+}
+// The same with one unit for the CTA.
+template <int WARPS, int TMA_WARP, class Counts>
+__device__ __forceinline__ void enter(const RcParams& p, Head* hd, int nbars, Counts&& count, int64_t unit, int rows,
+                                      bool last_first) {
+  if ((threadIdx.x >> 5) == TMA_WARP) {
+    const int lane = threadIdx.x & 31;
     pdl_wait();
     Unit u{0, 0, 0};
     const bool f = find_unit(p, unit, rows, last_first, blockIdx.x == 0, lane, u);
@@ -534,11 +592,7 @@ __device__ __forceinline__ void enter(const RcParams& p, Head* hd, int nbars, Co
       hd->tile = u.tile;
     }
   }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  pdl_wait();
-  pdl_trigger();
+  enter<WARPS>(hd, nbars, count);
 }
 template <int WARPS>
 __device__ __forceinline__ void leave(Head* hd) {
@@ -549,10 +603,29 @@ __device__ __forceinline__ void leave(Head* hd) {
     tmem_dealloc512(hd->tmem);
   }
 }
+template <int WARPS>
+__device__ __forceinline__ void leave(Head* hd, const RcParams& p) {
+  leave<WARPS>(hd);
+  if (threadIdx.x == 0) {
+    int* ctr = g_rc_items + 2 * p.slot;
+    __threadfence();
+    if (atomicAdd(ctr + 1, 1) == static_cast<int>(gridDim.x) - 1) {
+      atomicExch(ctr, 0);
+      atomicExch(ctr + 1, 0);
+    }
+  }
+}
 
 // ===========================================================================
 // Forward
 // ===========================================================================
+// What the TMA warp tells the other warps of an item: two slots, so that it
+// can be one item ahead.
+struct FwdItem {
+  int start, len, row0, head;  // row0: position of the first query row
+  int n[2];                    // key tiles of the query tiles (0: there is none)
+};
+
 template <int DP>
 struct FwdShape {
   static constexpr int kTile = DP / 64 * kPanel;
@@ -562,10 +635,21 @@ struct FwdShape {
   // barriers
   static constexpr int qfull = 0, kfull = 2, vfull = kfull + kStages, tail = vfull + kStages, kempty = tail + 1,
                        vempty = kempty + kStages, sfull = vempty + kStages, pfull = sfull + 2, odone = pfull + 4,
-                       drain = odone + 2, count = drain + 2;
-  static_assert(count <= 40 && kempty <= 32, "barriers");
+                       ofree = odone + 2, qempty = ofree + 2, info = qempty + 2, tabfull = info + 2,
+                       free_ = tabfull + 2, drain = free_ + 2, count = drain + 2;
+  static_assert(count <= kMaxBars && kempty <= 32, "barriers");
+  template <bool BIAS>
+  static uint32_t __device__ __forceinline__ arrivals(int i) {
+    if (i >= pfull && i < odone) return 8u;
+    if (i >= ofree && i < qempty) return 8u;
+    if (i >= free_ && i < drain) return kFwdWarps + 2 + (BIAS ? 1 : 0);
+    return i >= kempty && i < sfull ? 2u : 1u;
+  }
 };
 
+// Persistent: a CTA takes (query rows, head) items until there are none.  The
+// TMA warp runs ahead into the next item's loads, and its first scores are
+// computed while the last outputs are stored.
 template <int DP, bool BIAS>
 __global__ void __launch_bounds__(kFwdThreads, 1) rc_fwd_kernel(const __grid_constant__ RcParams p) {
   using L = FwdShape<DP>;
@@ -575,135 +659,178 @@ __global__ void __launch_bounds__(kFwdThreads, 1) rc_fwd_kernel(const __grid_con
   uint8_t* sK = sQ + 2 * L::kTile;
   uint8_t* sV = sK + L::kStages * L::kTile;
   Head* hd = reinterpret_cast<Head*>(sV + L::kStages * L::kTile);
+  volatile FwdItem* items = reinterpret_cast<volatile FwdItem*>(hd->items);
   float* part = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(hd) + kBarBytes);
-  float* tab = part + 1024;
+  float* tabs = part + 1024;  // a table for each slot
   const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
-  const int head = static_cast<int>(blockIdx.x % p.H);
-  const int nsub = p.sub;
-  enter<kFwdWarps, kFwdWarps + 2>(p, hd, L::count, [](int i) {
-    if (i >= L::pfull && i < L::pfull + 4) return 8u;
-    return i >= L::kempty && i < L::sfull ? 2u : 1u;
-  }, blockIdx.x / p.H,
-        128 * nsub, p.causal != 0);
-  if (BIAS && hd->found) fill_table(p, head, tab, kFwdThreads);
-  if (BIAS) __syncthreads();
+  enter<kFwdWarps>(hd, L::count, L::template arrivals<BIAS>);
   const uint32_t bar0 = smem_addr(hd->bar);
   auto bar = [&](int i) { return bar0 + 8u * i; };
   const WaitCtx w{&hd->abort_flag, p.err, p.wait_limit_ns};
   const uint32_t tmem = uniform(hd->tmem);
-  const bool found = uniform(hd->found);
-  const int start = uniform(hd->start), len = uniform(hd->len), row0 = uniform(hd->tile) * 128 * nsub;
-  const int nk_all = (len + 127) >> 7;
-  // key tiles of the CTA's query tile t (0: there is none)
-  auto tiles_of = [&](int t) {
-    const int r = row0 + 128 * t;
-    if (!found || t >= nsub || r >= len) return 0;
-    return p.causal ? min(nk_all, (r >> 7) + 1) : nk_all;
-  };
-  const int n0 = tiles_of(0), n1 = tiles_of(1), nmax = max(n0, n1);
 
-  if (warp == kFwdWarps + 2 && nmax > 0) {
-    const HeadAt hq = head_at(head, p.hq), hk = head_at(head / p.group, p.hk);
+  if (warp == kFwdWarps + 2) {
     Flight fl;
     uint32_t tail_phase = 0;
+    uint32_t nq[2] = {0, 0}, c = 0;  // Q tiles loaded, K/V tiles loaded
     bool ok = true, skip = p.fault_skip != 0;
-    auto load_q = [&](int t) {
-      mbar_arrive_expect_tx(bar(L::qfull + t), L::kTile);
-      fl.note(L::qfull + t, 0);
-      load_tile<DP>(smem_addr(sQ + t * L::kTile), &p.mapQ, bar(L::qfull + t), start + row0 + 128 * t, hq);
-    };
     if (lane == 0) {
       prefetch_tmap(&p.mapQ);
       prefetch_tmap(&p.mapK);
       prefetch_tmap(&p.mapV);
-      load_q(0);
     }
-    for (int j = 0; ok && j < nmax; ++j) {
-      const int st = j % L::kStages;
-      const uint32_t ph = (j / L::kStages) & 1;
+    ItemWalk walk(p, p.H);
+    for (uint32_t it = 0; ok; ++it) {
+      const int slot = it & 1;
+      Unit u{0, 0, 0};
+      const bool found = walk.next(p, 128 * p.sub, p.causal != 0, lane, u);
+      if (!(ok = wait_warp(bar(L::free_ + slot), ((it >> 1) & 1) ^ 1, w))) break;
+      const int row0 = u.tile * 128 * p.sub, head = walk.index, nk_all = (u.len + 127) >> 7;
+      int n[2];
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        const int r = row0 + 128 * t;
+        n[t] = !found || t >= p.sub || r >= u.len ? 0 : p.causal ? min(nk_all, (r >> 7) + 1) : nk_all;
+      }
       if (lane == 0) {
-        ok = wait_bounded(bar(L::kempty + st), ph ^ 1u, w);
-        if (ok && !skip) {
-          mbar_arrive_expect_tx(bar(L::kfull + st), L::kTile);
-          fl.note(L::kfull + st, ph);
-          load_tile<DP>(smem_addr(sK + st * L::kTile), &p.mapK, bar(L::kfull + st), start + 128 * j, hk);
+        items[slot].start = u.start;
+        items[slot].len = u.len;
+        items[slot].row0 = row0;
+        items[slot].head = found ? head : -1;
+        items[slot].n[0] = n[0];
+        items[slot].n[1] = n[1];
+        mbar_arrive(bar(L::info + slot));
+      }
+      if (!found) break;
+      const HeadAt hq = head_at(head, p.hq), hk = head_at(head / p.group, p.hk);
+      const int nmax = max(n[0], n[1]), start = u.start, len = u.len;
+      auto load_q = [&](int t) {  // lane 0
+        if (!wait_bounded(bar(L::qempty + t), (nq[t] & 1) ^ 1, w)) return false;
+        mbar_arrive_expect_tx(bar(L::qfull + t), L::kTile);
+        fl.note(L::qfull + t, nq[t] & 1);
+        load_tile<DP>(smem_addr(sQ + t * L::kTile), &p.mapQ, bar(L::qfull + t), start + row0 + 128 * t, hq);
+        return true;
+      };
+      if (lane == 0) ok = load_q(0);
+      for (int j = 0; j < nmax; ++j, ++c) {
+        const int st = c % L::kStages;
+        const uint32_t ph = (c / L::kStages) & 1;
+        if (lane == 0) {
+          ok = ok && wait_bounded(bar(L::kempty + st), ph ^ 1u, w);
+          if (ok && !skip) {
+            mbar_arrive_expect_tx(bar(L::kfull + st), L::kTile);
+            fl.note(L::kfull + st, ph);
+            load_tile<DP>(smem_addr(sK + st * L::kTile), &p.mapK, bar(L::kfull + st), start + 128 * j, hk);
+          }
+          skip = false;
+          if (ok && j == 0 && n[1] > 0) ok = load_q(1);
+          ok = ok && wait_bounded(bar(L::vempty + st), ph ^ 1u, w);
         }
-        skip = false;
-        if (ok && j == 0 && n1 > 0) load_q(1);
-        ok = ok && wait_bounded(bar(L::vempty + st), ph ^ 1u, w);
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+        if (!ok) break;
+        if (128 * j + 128 > len && start + len < p.T) {
+          ok = load_tail<DP>(sV + st * L::kTile, &p.mapV, bar(L::vfull + st), bar(L::tail), tail_phase,
+                             start + 128 * j, hk, len - 128 * j, lane, w);
+          if (!ok) break;
+        } else if (lane == 0) {
+          mbar_arrive_expect_tx(bar(L::vfull + st), L::kTile);
+          fl.note(L::vfull + st, ph);
+          load_tile<DP>(smem_addr(sV + st * L::kTile), &p.mapV, bar(L::vfull + st), start + 128 * j, hk);
+        }
       }
-      ok = __shfl_sync(0xffffffffu, ok, 0);
-      if (!ok) break;
-      if (128 * j + 128 > len && start + len < p.T) {
-        ok = load_tail<DP>(sV + st * L::kTile, &p.mapV, bar(L::vfull + st), bar(L::tail), tail_phase,
-                           start + 128 * j, hk, len - 128 * j, lane, w);
-      } else if (lane == 0) {
-        mbar_arrive_expect_tx(bar(L::vfull + st), L::kTile);
-        fl.note(L::vfull + st, ph);
-        load_tile<DP>(smem_addr(sV + st * L::kTile), &p.mapV, bar(L::vfull + st), start + 128 * j, hk);
-      }
+      nq[0] += n[0] > 0;
+      nq[1] += n[1] > 0;
     }
     if (lane == 0 && *w.abort_flag) fl.drain(bar0, p.wait_limit_ns);
     __syncwarp();
-  } else if (warp >= kFwdWarps && warp < kFwdWarps + 2 && nmax > 0) {
+  } else if (BIAS && warp == kFwdWarps + 3) {
+    // the bias of an item's head, into its slot's table
+    for (uint32_t it = 0;; ++it) {
+      const int slot = it & 1;
+      if (!wait_warp(bar(L::info + slot), (it >> 1) & 1, w)) break;
+      const int head = items[slot].head;
+      if (head < 0) break;
+      fill_table(p, head, tabs + slot * table_floats(p.bias.md), lane, 32);
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(bar(L::tabfull + slot));
+        mbar_arrive(bar(L::free_ + slot));
+      }
+    }
+  } else if (warp >= kFwdWarps && warp < kFwdWarps + 2) {
     // One MMA warp a query tile: while one waits, the other's products run.
     // Both go through every key tile, and a K or V stage is free when both have
     // passed it.
     const int t = warp - kFwdWarps;
-    const int nt = t ? n1 : n0;
     const int ksteps = (p.d + 15) >> 4;
     const uint32_t idesc_pv = idesc_bf16(0, 1, ksteps * 16);
     const uint32_t dO = tmem + 256 + 128 * t, tS = tmem + 128 * t;
-    auto scores = [&](int j) {
-      if (elect_one()) {
-        mma_scores<DP>(tS, smem_addr(sQ + t * L::kTile), smem_addr(sK + (j % L::kStages) * L::kTile), ksteps);
-        mma_commit(bar(L::sfull + t));
-        mma_commit(bar(L::kempty + j % L::kStages));
-      }
-      __syncwarp();
-    };
-    auto kfull = [&](int j) { return wait_warp(bar(L::kfull + j % L::kStages), (j / L::kStages) & 1, w); };
+    uint32_t c = 0, np = 0, nq = 0;  // K/V tiles, probability tiles and items of this query tile so far
     bool ok = true, issued = false;
-    if (nt > 0) {
-      ok = wait_warp(bar(L::qfull + t), 0, w) && kfull(0);
-      if (ok) {
+    for (uint32_t it = 0; ok; ++it) {
+      const int slot = it & 1;
+      if (!(ok = wait_warp(bar(L::info + slot), (it >> 1) & 1, w))) break;
+      const bool end = uniform(items[slot].head) < 0;
+      const int nt = uniform(items[slot].n[t]), nmax = max(nt, uniform(items[slot].n[t ^ 1]));
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(L::free_ + slot));
+      if (end) break;
+      auto kfull = [&](int j) {
+        return wait_warp(bar(L::kfull + (c + j) % L::kStages), ((c + j) / L::kStages) & 1, w);
+      };
+      auto vfull = [&](int j) {
+        return wait_warp(bar(L::vfull + (c + j) % L::kStages), ((c + j) / L::kStages) & 1, w);
+      };
+      auto scores = [&](int j) {
+        const int st = (c + j) % L::kStages;
+        if (elect_one()) {
+          mma_scores<DP>(tS, smem_addr(sQ + t * L::kTile), smem_addr(sK + st * L::kTile), ksteps);
+          mma_commit(bar(L::sfull + t));
+          mma_commit(bar(L::kempty + st));
+          if (j + 1 == nt) mma_commit(bar(L::qempty + t));
+        }
+        __syncwarp();
+      };
+      if (nt > 0) {
+        if (!(ok = wait_warp(bar(L::qfull + t), nq & 1, w) && kfull(0))) break;
         tc_fence_after();
         issued = true;
         scores(0);
       }
-    }
-    for (int j = 0; ok && j < nt; ++j) {
-      const int st = j % L::kStages;
-      const uint32_t b = smem_addr(sV + st * L::kTile);
-      // everything but the probabilities is waited for before they are, so the
-      // products are issued as one run
-      if (!(ok = wait_warp(bar(L::vfull + st), (j / L::kStages) & 1, w) && (j + 1 >= nt || kfull(j + 1)))) break;
-      if (!(ok = wait_warp(bar(L::pfull + 2 * t), j & 1, w))) break;
-      tc_fence_after();
-      if (elect_one()) mma_rows<2, 0, 2>(dO, tS, b, idesc_pv, j > 0);
-      __syncwarp();
-      if (!(ok = wait_warp(bar(L::pfull + 2 * t + 1), j & 1, w))) break;
-      tc_fence_after();
-      if (elect_one()) {
-        mma_rows<2, 2, 2>(dO, tS, b, idesc_pv, true);
-        mma_commit(bar(L::vempty + st));
-        if (j + 1 >= nt) mma_commit(bar(L::odone + t));
+      for (int j = 0; j < nt; ++j, ++np) {
+        const int st = (c + j) % L::kStages;
+        const uint32_t b = smem_addr(sV + st * L::kTile);
+        // everything but the probabilities is waited for before they are, so the
+        // products are issued as one run
+        if (!(ok = vfull(j) && (j + 1 >= nt || kfull(j + 1)))) break;
+        // the output of the item before has been read
+        if (j == 0 && !(ok = wait_warp(bar(L::ofree + t), (nq & 1) ^ 1, w))) break;
+        if (!(ok = wait_warp(bar(L::pfull + 2 * t), np & 1, w))) break;
+        tc_fence_after();
+        if (elect_one()) mma_rows<2, 0, 2>(dO, tS, b, idesc_pv, j > 0);
+        __syncwarp();
+        if (!(ok = wait_warp(bar(L::pfull + 2 * t + 1), np & 1, w))) break;
+        tc_fence_after();
+        if (elect_one()) {
+          mma_rows<2, 2, 2>(dO, tS, b, idesc_pv, true);
+          mma_commit(bar(L::vempty + st));
+          if (j + 1 >= nt) mma_commit(bar(L::odone + t));
+        }
+        __syncwarp();
+        if (j + 1 < nt) scores(j + 1);
       }
-      __syncwarp();
-      if (j + 1 < nt) scores(j + 1);
-    }
-    // key tiles that only the other query tile sees
-    for (int j = nt; ok && j < nmax; ++j) {
-      const int st = j % L::kStages;
-      if ((ok = kfull(j)) && lane == 0) mbar_arrive(bar(L::kempty + st));
-      if (ok && (ok = wait_warp(bar(L::vfull + st), (j / L::kStages) & 1, w)) && lane == 0)
-        mbar_arrive(bar(L::vempty + st));
+      // key tiles that only the other query tile sees
+      for (int j = nt; ok && j < nmax; ++j) {
+        const int st = (c + j) % L::kStages;
+        if ((ok = kfull(j)) && lane == 0) mbar_arrive(bar(L::kempty + st));
+        if (ok && (ok = vfull(j)) && lane == 0) mbar_arrive(bar(L::vempty + st));
+      }
+      c += nmax;
+      nq += nt > 0;
     }
     if (*w.abort_flag && issued && elect_one()) drain_mma(bar(L::drain + t), p.wait_limit_ns);
   } else if (warp < kFwdWarps) {
     const int t = warp >> 3, half = (warp >> 2) & 1, quarter = warp & 3;
-    const int nt = t ? n1 : n0;
-    const int row = row0 + 128 * t + quarter * 32 + lane;  // position in the sequence
     const uint32_t lane_base = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
     const uint32_t tS = lane_base + 128 * t, tO = lane_base + 256 + 128 * t;
     // the two warps of these rows meet at a barrier of their own
@@ -713,104 +840,130 @@ __global__ void __launch_bounds__(kFwdThreads, 1) rc_fwd_kernel(const __grid_con
     const int cut = first_columns(p.d);  // this warp's columns of the output
     const int ofirst = half ? cut : 0, olast = half ? p.d : cut;
     const float sl2 = p.scale_log2;
-    float m = 0.f;            // the exponents' reference (log2)
-    float l0 = 0.f, l1 = 0.f; // sums of 2^(x - m) over this warp's columns
-    // After a failed wait the loop runs on without waiting: the pair's barrier
-    // needs both warps, and nothing is stored at the end.
+    uint32_t np = 0, nq = 0;  // score tiles and items of this query tile so far
+    // After a failed wait an item runs on without waiting: the pair's barrier
+    // needs both warps, nothing is stored at its end, and both leave together.
     bool ok = true;
-    for (int j = 0; j < nt; ++j) {
-      ok = ok && wait_warp(bar(L::sfull + t), j & 1, w);
-      tc_fence_after();
-      uint32_t s[64];
-      tmem_ld32_issue(tS + 64 * half, s);
-      tmem_ld32_issue(tS + 64 * half + 32, s + 32);
-      tmem_ld32_wait(s);
-      tmem_ld32_wait(s + 32);
-      const int c0 = 128 * j + 64 * half, r0 = row0 + 128 * t;
-      float mul = sl2, add = 0.f;  // x = s mul + add
-      if (BIAS) {
-        const int side = bias_side(p.bias.md, r0, 128 * j);
-        if (side != 0) {
-          add = tab[side < 0 ? 0 : table_floats(p.bias.md) - 1];
-        } else {
-          const float* tb = tab + (c0 - row + p.bias.md + kPad);
+    for (uint32_t it = 0;; ++it) {
+      const int slot = it & 1;
+      ok = ok && wait_warp(bar(L::info + slot), (it >> 1) & 1, w);
+      if (named_bar_any(pair_bar, 64, !ok)) break;
+      const int head = uniform(items[slot].head);
+      if (head < 0) break;
+      if (BIAS) ok = wait_warp(bar(L::tabfull + slot), (it >> 1) & 1, w);
+      const int start = uniform(items[slot].start), len = uniform(items[slot].len);
+      const int row0 = uniform(items[slot].row0), nt = uniform(items[slot].n[t]);
+      const int row = row0 + 128 * t + quarter * 32 + lane;  // position in the sequence
+      const float* tab = tabs + (BIAS ? slot * table_floats(p.bias.md) : 0);
+      float m = 0.f;             // the exponents' reference (log2)
+      float l0 = 0.f, l1 = 0.f;  // sums of 2^(x - m) over this warp's columns
+      for (int j = 0; j < nt; ++j, ++np) {
+        ok = ok && wait_warp(bar(L::sfull + t), np & 1, w);
+        tc_fence_after();
+        uint32_t s[64];
+        tmem_ld32_issue(tS + 64 * half, s);
+        tmem_ld32_issue(tS + 64 * half + 32, s + 32);
+        tmem_ld32_wait(s);
+        tmem_ld32_wait(s + 32);
+        const int c0 = 128 * j + 64 * half, r0 = row0 + 128 * t;
+        float mul = sl2, add = 0.f;  // x = s mul + add
+        if (BIAS) {
+          const int side = bias_side(p.bias.md, r0, 128 * j);
+          if (side != 0) {
+            add = tab[side < 0 ? 0 : table_floats(p.bias.md) - 1];
+          } else {
+            const float* tb = tab + (c0 - row + p.bias.md + kPad);
 #pragma unroll
-          for (int c = 0; c < 64; ++c) s[c] = __float_as_uint(fmaf(as_f(s[c]), sl2, tb[c]));
-          mul = 1.f;
+            for (int c = 0; c < 64; ++c) s[c] = __float_as_uint(fmaf(as_f(s[c]), sl2, tb[c]));
+            mul = 1.f;
+          }
         }
-      }
-      if ((p.causal && 128 * j + 127 > r0) || 128 * j + 128 > len) {
-        const int seen = (p.causal ? min(len, row + 1) : len) - c0;  // columns this row sees
+        if ((p.causal && 128 * j + 127 > r0) || 128 * j + 128 > len) {
+          const int seen = (p.causal ? min(len, row + 1) : len) - c0;  // columns this row sees
 #pragma unroll
-        for (int c = 0; c < 64; ++c) s[c] = c < seen ? s[c] : 0xff800000u;
-      }
-      float mx[4];
+          for (int c = 0; c < 64; ++c) s[c] = c < seen ? s[c] : 0xff800000u;
+        }
+        float mx[4];
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        mx[q] = fmaxf(as_f(s[q]), as_f(s[q + 4]));
+        for (int q = 0; q < 4; ++q) {
+          mx[q] = fmaxf(as_f(s[q]), as_f(s[q + 4]));
 #pragma unroll
-        for (int c = 8 + q; c < 64; c += 8) mx[q] = fmaxf(fmaxf(mx[q], as_f(s[c])), as_f(s[c + 4]));
+          for (int c = 8 + q; c < 64; c += 8) mx[q] = fmaxf(fmaxf(mx[q], as_f(s[c])), as_f(s[c + 4]));
+        }
+        const float mh = fmaf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), mul, add);
+        // The exponents' reference is the first tile's maximum and follows the
+        // running one only when a row's is 2^16 above it: up to there the
+        // exponentials and their sums are as exact (fp32 and bf16 have the range),
+        // and neither the maxima are exchanged nor the output rescaled.
+        if (named_bar_any(pair_bar, 64, j == 0 || mh > m + 16.f)) {
+          mine_at[0] = mh;
+          named_bar(pair_bar, 64);
+          const float mt = fmaxf(mh, other_at[0]);
+          if (j == 0) {
+            m = mt;
+          } else {
+            const float mn = mt > m + 16.f ? mt : m;
+            const float f = ex2_ftz(m - mn);
+            l0 *= f;
+            l1 *= f;
+            m = mn;
+            for (int c = ofirst; c < olast; c += 8) tmem_scale8(tO + c, f);
+          }
+        }
+        const float off = add - m;
+        const uint64_t scl2 = pack2(mul, mul), off2 = pack2(off, off);
+        uint64_t sum[2] = {pack2(l0, l1), 0ull};
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int c = 0; c < 16; ++c) {
+            float a, b;
+            unpack2(fma2(pack2(as_f(s[32 * h + 2 * c]), as_f(s[32 * h + 2 * c + 1])), scl2, off2), a, b);
+            a = ex2_ftz(a);
+            b = ex2_ftz(b);
+            sum[c & 1] = add2(sum[c & 1], pack2(a, b));
+            pk[c] = pack_bf16x2(a, b);
+          }
+          tmem_st16(tS + 64 * half + 16 * h, pk);
+          tmem_st_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(L::pfull + 2 * t + h));
+        }
+        unpack2(add2(sum[0], sum[1]), l0, l1);
       }
-      const float mh = fmaf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), mul, add);
-      // The exponents' reference is the first tile's maximum and follows the
-      // running one only when a row's is 2^16 above it: up to there the
-      // exponentials and their sums are as exact (fp32 and bf16 have the range),
-      // and neither the maxima are exchanged nor the output rescaled.
-      if (named_bar_any(pair_bar, 64, j == 0 || mh > m + 16.f)) {
-        mine_at[0] = mh;
+      if (lane == 0) mbar_arrive(bar(L::free_ + slot));
+      if (nt > 0) {
+        const float lh = l0 + l1;
+        mine_at[512] = lh;
         named_bar(pair_bar, 64);
-        const float mt = fmaxf(mh, other_at[0]);
-        if (j == 0) {
-          m = mt;
-        } else {
-          const float mn = mt > m + 16.f ? mt : m;
-          const float f = ex2_ftz(m - mn);
-          l0 *= f;
-          l1 *= f;
-          m = mn;
-          for (int c = ofirst; c < olast; c += 8) tmem_scale8(tO + c, f);
-        }
-      }
-      const float off = add - m;
-      const uint64_t scl2 = pack2(mul, mul), off2 = pack2(off, off);
-      uint64_t sum[2] = {pack2(l0, l1), 0ull};
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        uint32_t pk[16];
-#pragma unroll
-        for (int c = 0; c < 16; ++c) {
-          float a, b;
-          unpack2(fma2(pack2(as_f(s[32 * h + 2 * c]), as_f(s[32 * h + 2 * c + 1])), scl2, off2), a, b);
-          a = ex2_ftz(a);
-          b = ex2_ftz(b);
-          sum[c & 1] = add2(sum[c & 1], pack2(a, b));
-          pk[c] = pack_bf16x2(a, b);
-        }
-        tmem_st16(tS + 64 * half + 16 * h, pk);
-        tmem_st_wait();
+        const float lo = other_at[512];
+        named_bar(pair_bar, 64);  // both have read before the next item writes
+        const float l = half ? lo + lh : lh + lo;
+        ok = ok && wait_warp(bar(L::odone + t), nq & 1, w);
+        tc_fence_after();
+        uint32_t o[64];
+        tmem_ld32_issue(tO + ofirst, o);
+        tmem_ld32_issue(tO + ofirst + (DP == 128 ? 32 : 0), o + 32);
+        tmem_ld32_wait(o);
+        tmem_ld32_wait(o + 32);
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar(L::pfull + 2 * t + h));
-      }
-      unpack2(add2(sum[0], sum[1]), l0, l1);
-    }
-    if (nt > 0) {
-      const float lh = l0 + l1;
-      mine_at[512] = lh;
-      named_bar(pair_bar, 64);
-      const float lo = other_at[512];
-      const float l = half ? lo + lh : lh + lo;
-      if (ok && wait_warp(bar(L::odone + t), 0, w)) {
-        tc_fence_after();
-        const bool mine = row < len;
-        const int64_t token = static_cast<int64_t>(start) + row;
-        store_row(tO + ofirst, olast - ofirst, 1.f / l,
-                  static_cast<__nv_bfloat16*>(p.C) + token * p.ld_c + static_cast<int64_t>(head) * p.d + ofirst, mine);
-        if (mine && half == 0) p.lse[static_cast<int64_t>(head) * p.T + token] = (m + log2f(l)) * kLn2;
+        if (lane == 0) mbar_arrive(bar(L::ofree + t));
+        if (ok && row < len) {
+          const int64_t token = static_cast<int64_t>(start) + row;
+          __nv_bfloat16* out =
+              static_cast<__nv_bfloat16*>(p.C) + token * p.ld_c + static_cast<int64_t>(head) * p.d + ofirst;
+          store_columns<DP / 2>(o, olast - ofirst, 1.f / l, out, p.wide);
+          if (half == 0) p.lse[static_cast<int64_t>(head) * p.T + token] = (m + log2f(l)) * kLn2;
+        }
+        __syncwarp();
+        ++nq;
       }
     }
   }
-  leave<kFwdWarps>(hd);
+  leave<kFwdWarps>(hd, p);
 }
 
 // ===========================================================================
@@ -865,7 +1018,7 @@ struct DkvShape {
                        oempty = qempty + kQ, vecfull = oempty + kO, vecempty = vecfull + 2, sfull = vecempty + 2,
                        dpfull = sfull + 1, pready = dpfull + 1, dsready = pready + 2, done = dsready + 2,
                        drain = done + 1, count = drain + 2;
-  static_assert(count <= 40 && qempty <= 32, "barriers");
+  static_assert(count <= kMaxBars && qempty <= 32, "barriers");
   static uint32_t __device__ __forceinline__ arrivals(int i) {
     if ((i >= pready && i < done) || i == vecempty || i == vecempty + 1) return kBwdWarps;
     return i == done || (i >= oempty && i < vecfull) ? 2u : 1u;
@@ -1067,7 +1220,7 @@ __global__ void __launch_bounds__(kDkvThreads, 1) rc_dkv_kernel(const __grid_con
         // the next query head's bias; every compute warp reads the table
         table_head = q.g;
         named_bar(1, 32 * kBwdWarps);
-        fill_table(p, q.g, tab, 32 * kBwdWarps);
+        fill_table(p, q.g, tab, threadIdx.x, 32 * kBwdWarps);
         named_bar(1, 32 * kBwdWarps);
       }
       float add = 0.f;
@@ -1159,9 +1312,9 @@ __global__ void __launch_bounds__(kDkvThreads, 1) rc_dkv_kernel(const __grid_con
       const HeadAt hk = head_at(kvh, p.hk);
       const int64_t col = static_cast<int64_t>(hk.shard) * p.shard_w + static_cast<int64_t>(p.hq) * p.d +
                           static_cast<int64_t>(hk.local + (which ? 0 : p.hk)) * p.d + first;
-      store_row((which ? tdK : tdV) + lb + first, n, which ? p.scale : 1.f,
-                static_cast<__nv_bfloat16*>(p.dQKV) + (static_cast<int64_t>(start) + pos) * p.ld_dqkv + col,
-                pos < len);
+      store_row<DP / 64>((which ? tdK : tdV) + lb + first, n, which ? p.scale : 1.f,
+                         static_cast<__nv_bfloat16*>(p.dQKV) + (static_cast<int64_t>(start) + pos) * p.ld_dqkv + col,
+                         pos < len, p.wide);
     }
   }
   leave<kBwdWarps>(hd);
@@ -1179,7 +1332,7 @@ struct DqShape {
   static constexpr int qfull = 0, kfull = 1, vfull = kfull + kStages, tail = vfull + kStages, kempty = tail + 1,
                        vempty = kempty + kStages, sfull = vempty + kStages, sread = sfull + 1, dpfull = sread + 1,
                        dsready = dpfull + 1, done = dsready + 2, drain = done + 1, count = drain + 1;
-  static_assert(count <= 40 && kempty <= 32, "barriers");
+  static_assert(count <= kMaxBars && kempty <= 32, "barriers");
   static uint32_t __device__ __forceinline__ arrivals(int i) {
     return i == dsready || i == dsready + 1 || i == sread || i == qfull ? kBwdWarps : 1u;
   }
@@ -1211,7 +1364,7 @@ __global__ void __launch_bounds__(kDqThreads, 1) rc_dq_kernel(const __grid_const
   float* bins = diag + kBwdWarps * kDiag;             // [2 md + 1]
   float* ends = bins + 2 * md + 1;                    // [2][32 kBwdWarps]
   if (BIAS) {
-    if (hd->found) fill_table(p, head, tab, kDqThreads);
+    if (hd->found) fill_table(p, head, tab, threadIdx.x, kDqThreads);
     if (grad)
       for (int i = threadIdx.x; i < 2 * md + 1; i += kDqThreads) bins[i] = 0.f;
     __syncthreads();
@@ -1454,10 +1607,10 @@ __global__ void __launch_bounds__(kDqThreads, 1) rc_dq_kernel(const __grid_const
       const int first = 32 * part, n = min(p.d - first, 32);
       const HeadAt hq = head_at(head, p.hq);
       if (n > 0)
-        store_row(tdQ + lb + first, n, p.scale,
-                  static_cast<__nv_bfloat16*>(p.dQKV) + token * p.ld_dqkv +
-                      static_cast<int64_t>(hq.shard) * p.shard_w + static_cast<int64_t>(hq.local) * p.d + first,
-                  mine);
+        store_row<1>(tdQ + lb + first, n, p.scale,
+                     static_cast<__nv_bfloat16*>(p.dQKV) + token * p.ld_dqkv +
+                         static_cast<int64_t>(hq.shard) * p.shard_w + static_cast<int64_t>(hq.local) * p.d + first,
+                     mine, p.wide);
     }
     if (BIAS && grad) {
       // the CTA's sums by bucket, in a fixed order
@@ -1510,6 +1663,11 @@ __global__ void __launch_bounds__(128) rc_bias_sum_kernel(const __grid_constant_
   }
 }
 
+// Whether every head's rows of `out` start on 32 bytes and are whole 32s long.
+int wide_rows(const RcParams& p, const void* out, int64_t ld, int shard_w) {
+  return (reinterpret_cast<uintptr_t>(out) & 31u) == 0 && ld % 16 == 0 && p.d % 16 == 0 && shard_w % 16 == 0;
+}
+
 template <class K>
 cudaError_t launch_rc(K kernel, int64_t blocks, int threads, int smem, const RcParams& p, cudaStream_t st) {
   const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
@@ -1526,17 +1684,23 @@ int64_t units_of(const RcParams& p, int rows) {
   return p.T / rows + p.b;
 }
 
+std::atomic<unsigned> g_rc_slot_seq{0};
+
 template <int DP, bool BIAS>
 cudaError_t fwd_t(RcParams& p, int num_sms, cudaStream_t st) {
   // Two query tiles a CTA where that still fills the SMs: their softmax and
   // products overlap, and K/V tiles are read once for both.
   p.sub = units_of(p, 256) * p.H >= num_sms ? 2 : 1;
-  const int smem = FwdShape<DP>::kSmem + (BIAS ? 4 * table_floats(p.bias.md) : 0);
-  return launch_rc(rc_fwd_kernel<DP, BIAS>, units_of(p, 128 * p.sub) * p.H, kFwdThreads, smem, p, st);
+  p.items = units_of(p, 128 * p.sub) * p.H;
+  p.slot = static_cast<int>(g_rc_slot_seq.fetch_add(1) % kRcSlots);
+  p.wide = wide_rows(p, p.C, p.ld_c, 0);
+  const int smem = FwdShape<DP>::kSmem + (BIAS ? 2 * 4 * table_floats(p.bias.md) : 0);
+  return launch_rc(rc_fwd_kernel<DP, BIAS>, p.items < num_sms ? p.items : num_sms, kFwdThreads, smem, p, st);
 }
 template <int DP, bool BIAS>
 cudaError_t bwd_t(RcParams& p, cudaStream_t st) {
   const int64_t units = units_of(p, 128);
+  p.wide = wide_rows(p, p.dQKV, p.ld_dqkv, p.shard_w);
   const int tab = BIAS ? 4 * table_floats(p.bias.md) : 0;
   cudaError_t e = launch_rc(rc_dkv_kernel<DP, BIAS>, units * p.KV, kDkvThreads, (DkvShape<DP, BIAS>::kSmem) + tab, p, st);
   p.fault_skip = 0;
