@@ -54,7 +54,8 @@ constexpr float kLn2 = 0.6931471805599453f;
 // The smem distance table covers [-(md + kPad), md + kPad], so that a tile that
 // holds any distance inside (-md, md) indexes it without clamping.
 constexpr int kPad = 255;
-__host__ __device__ constexpr int table_floats(int md) { return 2 * (md + kPad) + 1; }
+// (an even number of entries over: whole 16 bytes)
+__host__ __device__ constexpr int table_floats(int md) { return (2 * (md + kPad) + 1 + 3) & ~3; }
 
 // ---------------------------------------------------------------------------
 // PTX wrappers of this file
@@ -285,13 +286,31 @@ __device__ __forceinline__ int bucket_of(const RcBias& b, int delta) {
   }
   return add + lo;
 }
+// map[delta + md + kPad] = bucket of the clamped distance: of the arguments
+// alone, so a kernel makes it before it waits for the one in front of it.
+__device__ __forceinline__ void fill_map(const RcBias& b, uint8_t* map) {
+  for (int i = threadIdx.x; i < table_floats(b.md); i += blockDim.x)
+    map[i] = static_cast<uint8_t>(bucket_of(b, min(max(i - (b.md + kPad), -b.md), b.md)));
+}
 // tab[delta + md + kPad] = bias of the clamped distance, times log2 e; by
 // `threads` threads.
-__device__ __forceinline__ void fill_table(const RcParams& p, int head, float* tab, int thread, int threads) {
-  const int md = p.bias.md, n = table_floats(md);
-  for (int i = thread; i < n; i += threads) {
-    const int delta = min(max(i - (md + kPad), -md), md);
-    tab[i] = __ldg(p.table + static_cast<int64_t>(bucket_of(p.bias, delta)) * p.H + head) * kLog2e;
+__device__ __forceinline__ void fill_table(const RcParams& p, int head, const uint8_t* map, float* tab, int thread,
+                                           int threads) {
+  const int n = table_floats(p.bias.md);
+  for (int i = thread; i < n; i += threads)
+    tab[i] = __ldg(p.table + static_cast<int64_t>(map[i]) * p.H + head) * kLog2e;
+}
+// The same by one warp, through the head's column of the table in `vals`; the
+// map's and the table's rows are padded to fours.
+__device__ __forceinline__ void fill_table_warp(const RcParams& p, int head, const uint8_t* map, float* vals,
+                                                float* tab, int lane) {
+  for (int u = lane; u < p.bias.nb; u += 32) vals[u] = __ldg(p.table + static_cast<int64_t>(u) * p.H + head) * kLog2e;
+  __syncwarp();
+  const int n = table_floats(p.bias.md);
+#pragma unroll 2
+  for (int i = 4 * lane; i < n; i += 128) {
+    const uchar4 m = *reinterpret_cast<const uchar4*>(map + i);
+    *reinterpret_cast<float4*>(tab + i) = make_float4(vals[m.x], vals[m.y], vals[m.z], vals[m.w]);
   }
 }
 // How a (query tile at r0, key tile at c0) pair of 128 x 128 sees the bias:
@@ -547,6 +566,7 @@ struct ItemWalk {
   __device__ __forceinline__ bool next(const RcParams& p, int rows, bool last_first, int lane, Unit& u) {
     while (true) {
       if (!first) {
+        if (p.items <= gridDim.x) return false;  // an item each
         int v = 0;
         if (lane == 0) v = atomicAdd(g_rc_items + 2 * p.slot, 1);
         item = static_cast<int64_t>(gridDim.x) + __shfl_sync(0xffffffffu, v, 0);
@@ -606,7 +626,7 @@ __device__ __forceinline__ void leave(Head* hd) {
 template <int WARPS>
 __device__ __forceinline__ void leave(Head* hd, const RcParams& p) {
   leave<WARPS>(hd);
-  if (threadIdx.x == 0) {
+  if (threadIdx.x == 0 && p.items > gridDim.x) {
     int* ctr = g_rc_items + 2 * p.slot;
     __threadfence();
     if (atomicAdd(ctr + 1, 1) == static_cast<int>(gridDim.x) - 1) {
@@ -661,7 +681,11 @@ __global__ void __launch_bounds__(kFwdThreads, 1) rc_fwd_kernel(const __grid_con
   Head* hd = reinterpret_cast<Head*>(sV + L::kStages * L::kTile);
   volatile FwdItem* items = reinterpret_cast<volatile FwdItem*>(hd->items);
   float* part = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(hd) + kBarBytes);
-  float* tabs = part + 1024;  // a table for each slot
+  float* tabs = part + 1024;  // a table for each slot, the head's values, and the distances' buckets
+  const int tabn = BIAS ? table_floats(p.bias.md) : 0;
+  float* vals = tabs + 2 * tabn;
+  uint8_t* map = reinterpret_cast<uint8_t*>(vals + kMaxRelBuckets);
+  if (BIAS) fill_map(p.bias, map);
   const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
   enter<kFwdWarps>(hd, L::count, L::template arrivals<BIAS>);
   const uint32_t bar0 = smem_addr(hd->bar);
@@ -750,7 +774,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) rc_fwd_kernel(const __grid_con
       if (!wait_warp(bar(L::info + slot), (it >> 1) & 1, w)) break;
       const int head = items[slot].head;
       if (head < 0) break;
-      fill_table(p, head, tabs + slot * table_floats(p.bias.md), lane, 32);
+      fill_table_warp(p, head, map, vals, tabs + slot * tabn, lane);
       __syncwarp();
       if (lane == 0) {
         mbar_arrive(bar(L::tabfull + slot));
@@ -854,7 +878,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) rc_fwd_kernel(const __grid_con
       const int start = uniform(items[slot].start), len = uniform(items[slot].len);
       const int row0 = uniform(items[slot].row0), nt = uniform(items[slot].n[t]);
       const int row = row0 + 128 * t + quarter * 32 + lane;  // position in the sequence
-      const float* tab = tabs + (BIAS ? slot * table_floats(p.bias.md) : 0);
+      const float* tab = tabs + slot * tabn;
       float m = 0.f;             // the exponents' reference (log2)
       float l0 = 0.f, l1 = 0.f;  // sums of 2^(x - m) over this warp's columns
       for (int j = 0; j < nt; ++j, ++np) {
@@ -870,7 +894,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) rc_fwd_kernel(const __grid_con
         if (BIAS) {
           const int side = bias_side(p.bias.md, r0, 128 * j);
           if (side != 0) {
-            add = tab[side < 0 ? 0 : table_floats(p.bias.md) - 1];
+            add = tab[side < 0 ? 0 : 2 * (p.bias.md + kPad)];
           } else {
             const float* tb = tab + (c0 - row + p.bias.md + kPad);
 #pragma unroll
@@ -1052,6 +1076,8 @@ __global__ void __launch_bounds__(kDkvThreads, 1) rc_dkv_kernel(const __grid_con
   Head* hd = reinterpret_cast<Head*>(sO + L::kO * L::kTile);
   float* vec = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(hd) + kBarBytes);  // [2][2][128]
   float* tab = vec + 512;
+  uint8_t* map = reinterpret_cast<uint8_t*>(tab + (BIAS ? table_floats(p.bias.md) : 0));
+  if (BIAS) fill_map(p.bias, map);
   const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
   const int kvh = static_cast<int>(blockIdx.x % p.KV);
   enter<kBwdWarps, kBwdWarps + 2>(p, hd, L::count, L::arrivals, blockIdx.x / p.KV, 128, false);
@@ -1220,7 +1246,7 @@ __global__ void __launch_bounds__(kDkvThreads, 1) rc_dkv_kernel(const __grid_con
         // the next query head's bias; every compute warp reads the table
         table_head = q.g;
         named_bar(1, 32 * kBwdWarps);
-        fill_table(p, q.g, tab, threadIdx.x, 32 * kBwdWarps);
+        fill_table(p, q.g, map, tab, threadIdx.x, 32 * kBwdWarps);
         named_bar(1, 32 * kBwdWarps);
       }
       float add = 0.f;
@@ -1229,7 +1255,7 @@ __global__ void __launch_bounds__(kDkvThreads, 1) rc_dkv_kernel(const __grid_con
       if (BIAS) {
         const int side = bias_side(p.bias.md, 128 * q.i, 128 * kt);
         near = side == 0;
-        if (!near) add = tab[side < 0 ? 0 : table_floats(p.bias.md) - 1];
+        if (!near) add = tab[side < 0 ? 0 : 2 * (p.bias.md + kPad)];
         // distance of column c: key - query = (128 kt + key) - (128 i + 32 part + c)
         tb = tab + (128 * (kt - q.i) + key - 32 * part + p.bias.md + kPad);
       }
@@ -1354,17 +1380,19 @@ __global__ void __launch_bounds__(kDqThreads, 1) rc_dq_kernel(const __grid_const
   uint8_t* sV = sK + L::kStages * L::kTile;
   Head* hd = reinterpret_cast<Head*>(sV + L::kStages * L::kTile);
   float* tab = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(hd) + kBarBytes);
+  uint8_t* map = reinterpret_cast<uint8_t*>(tab + (BIAS ? table_floats(p.bias.md) : 0));
+  if (BIAS) fill_map(p.bias, map);
   const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
   const int head = static_cast<int>(blockIdx.x % p.H);
   const int64_t unit = blockIdx.x / p.H;
   enter<kBwdWarps, kBwdWarps + 1>(p, hd, L::count, L::arrivals, unit, 128, p.causal != 0);
   const bool grad = BIAS && p.partial != nullptr;
   const int md = BIAS ? p.bias.md : 0;
-  float* diag = tab + (BIAS ? table_floats(md) : 0);  // [kBwdWarps][kDiag]
+  float* diag = reinterpret_cast<float*>(map + (BIAS ? table_floats(md) : 0));  // [kBwdWarps][kDiag]
   float* bins = diag + kBwdWarps * kDiag;             // [2 md + 1]
   float* ends = bins + 2 * md + 1;                    // [2][32 kBwdWarps]
   if (BIAS) {
-    if (hd->found) fill_table(p, head, tab, threadIdx.x, kDqThreads);
+    if (hd->found) fill_table(p, head, map, tab, threadIdx.x, kDqThreads);
     if (grad)
       for (int i = threadIdx.x; i < 2 * md + 1; i += kDqThreads) bins[i] = 0.f;
     __syncthreads();
@@ -1509,7 +1537,7 @@ __global__ void __launch_bounds__(kDqThreads, 1) rc_dq_kernel(const __grid_const
       const float* tb = nullptr;
       if (BIAS) {
         side = bias_side(md, r0, 128 * j);
-        if (side != 0) off += tab[side < 0 ? 0 : table_floats(md) - 1];
+        if (side != 0) off += tab[side < 0 ? 0 : 2 * (md + kPad)];
         tb = tab + (c0 - row + md + kPad);
       }
       const uint64_t off2 = pack2(off, off);
@@ -1694,14 +1722,14 @@ cudaError_t fwd_t(RcParams& p, int num_sms, cudaStream_t st) {
   p.items = units_of(p, 128 * p.sub) * p.H;
   p.slot = static_cast<int>(g_rc_slot_seq.fetch_add(1) % kRcSlots);
   p.wide = wide_rows(p, p.C, p.ld_c, 0);
-  const int smem = FwdShape<DP>::kSmem + (BIAS ? 2 * 4 * table_floats(p.bias.md) : 0);
+  const int smem = FwdShape<DP>::kSmem + (BIAS ? 9 * table_floats(p.bias.md) + 4 * kMaxRelBuckets : 0);
   return launch_rc(rc_fwd_kernel<DP, BIAS>, p.items < num_sms ? p.items : num_sms, kFwdThreads, smem, p, st);
 }
 template <int DP, bool BIAS>
 cudaError_t bwd_t(RcParams& p, cudaStream_t st) {
   const int64_t units = units_of(p, 128);
   p.wide = wide_rows(p, p.dQKV, p.ld_dqkv, p.shard_w);
-  const int tab = BIAS ? 4 * table_floats(p.bias.md) : 0;
+  const int tab = BIAS ? 5 * table_floats(p.bias.md) : 0;  // the table, and a byte a distance
   cudaError_t e = launch_rc(rc_dkv_kernel<DP, BIAS>, units * p.KV, kDkvThreads, (DkvShape<DP, BIAS>::kSmem) + tab, p, st);
   p.fault_skip = 0;
   if (e != cudaSuccess) return e;
