@@ -45,7 +45,7 @@ namespace {
 // rows of a score tile (64 columns each) and two tiles, the backward kernels
 // four (32 columns each).
 constexpr int kFwdWarps = 16, kBwdWarps = 16;
-constexpr int kFwdThreads = 32 * (kFwdWarps + 4), kDkvThreads = 32 * (kBwdWarps + 4), kDqThreads = 32 * (kBwdWarps + 2);
+constexpr int kFwdThreads = 32 * (kFwdWarps + 4), kDkvThreads = 32 * (kBwdWarps + 4), kDqThreads = 32 * (kBwdWarps + 3);
 constexpr int kPanel = 128 * 128;    // bytes of 128 rows x 64 bf16 columns (one swizzle width)
 constexpr int kBarBytes = 512;
 constexpr float kLog2e = 1.4426950408889634f;
@@ -542,7 +542,6 @@ struct Head {
   uint64_t bar[kMaxBars];
   uint32_t tmem;
   int abort_flag;
-  int found, start, len, tile;
   int items[16];
 };
 static_assert(sizeof(Head) <= kBarBytes, "barrier area");
@@ -563,7 +562,9 @@ struct ItemWalk {
   bool first;
   __device__ __forceinline__ ItemWalk(const RcParams& p, int n) : item(blockIdx.x), heads(n), index(0), first(true) {}
   // The next item that has rows, by a whole warp; false: there is none.
-  __device__ __forceinline__ bool next(const RcParams& p, int rows, bool last_first, int lane, Unit& u) {
+  // `zero`: an item without rows leaves that many zeros there.
+  __device__ __forceinline__ bool next(const RcParams& p, int rows, bool last_first, int lane, Unit& u,
+                                       float* zero = nullptr, int nzero = 0) {
     while (true) {
       if (!first) {
         if (p.items <= gridDim.x) return false;  // an item each
@@ -576,6 +577,8 @@ struct ItemWalk {
       const bool found = find_unit(p, item / heads, rows, last_first, first && blockIdx.x == 0, lane, u);
       first = false;
       if (found) return true;
+      if (zero != nullptr)
+        for (int i = lane; i < nzero; i += 32) zero[item * nzero + i] = 0.f;
     }
   }
 };
@@ -595,24 +598,6 @@ __device__ __forceinline__ void enter(Head* hd, int nbars, Counts&& count) {
   tc_fence_after();
   pdl_wait();
   pdl_trigger();
-}
-// The same with one unit for the CTA.
-template <int WARPS, int TMA_WARP, class Counts>
-__device__ __forceinline__ void enter(const RcParams& p, Head* hd, int nbars, Counts&& count, int64_t unit, int rows,
-                                      bool last_first) {
-  if ((threadIdx.x >> 5) == TMA_WARP) {
-    const int lane = threadIdx.x & 31;
-    pdl_wait();
-    Unit u{0, 0, 0};
-    const bool f = find_unit(p, unit, rows, last_first, blockIdx.x == 0, lane, u);
-    if (lane == 0) {
-      hd->found = f;
-      hd->start = u.start;
-      hd->len = u.len;
-      hd->tile = u.tile;
-    }
-  }
-  enter<WARPS>(hd, nbars, count);
 }
 template <int WARPS>
 __device__ __forceinline__ void leave(Head* hd) {
@@ -1041,12 +1026,31 @@ struct DkvShape {
   static constexpr int kvfull = 0, qfull = 1, ofull = qfull + kQ, tail = ofull + kO, qempty = tail + 1,
                        oempty = qempty + kQ, vecfull = oempty + kO, vecempty = vecfull + 2, sfull = vecempty + 2,
                        dpfull = sfull + 1, pready = dpfull + 1, dsready = pready + 2, done = dsready + 2,
-                       drain = done + 1, count = drain + 2;
+                       dfree = done + 1, kvempty = dfree + 1, info = kvempty + 1, free_ = info + 2,
+                       drain = free_ + 2, count = drain + 2;
   static_assert(count <= kMaxBars && qempty <= 32, "barriers");
   static uint32_t __device__ __forceinline__ arrivals(int i) {
-    if ((i >= pready && i < done) || i == vecempty || i == vecempty + 1) return kBwdWarps;
-    return i == done || (i >= oempty && i < vecfull) ? 2u : 1u;
+    if ((i >= pready && i < done) || i == vecempty || i == vecempty + 1 || i == dfree) return kBwdWarps;
+    if (i >= free_ && i < drain) return kBwdWarps + 3;
+    return i == done || i == kvempty || (i >= oempty && i < vecfull) ? 2u : 1u;
   }
+};
+
+// Stage and phase of a ring of tiles.
+struct Ring {
+  int stage, stages;
+  uint32_t phase;
+  __device__ __forceinline__ void next() {
+    if (++stage == stages) {
+      stage = 0;
+      phase ^= 1u;
+    }
+  }
+};
+
+// What the TMA warp tells the other warps of an item (two slots).
+struct DkvItem {
+  int start, len, tile, head;  // head: the K/V head, -1: no more items
 };
 
 // The query tiles of a K/V head's key tile, head by head.
@@ -1079,62 +1083,99 @@ __global__ void __launch_bounds__(kDkvThreads, 1) rc_dkv_kernel(const __grid_con
   uint8_t* map = reinterpret_cast<uint8_t*>(tab + (BIAS ? table_floats(p.bias.md) : 0));
   if (BIAS) fill_map(p.bias, map);
   const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
-  const int kvh = static_cast<int>(blockIdx.x % p.KV);
-  enter<kBwdWarps, kBwdWarps + 2>(p, hd, L::count, L::arrivals, blockIdx.x / p.KV, 128, false);
+  volatile DkvItem* items = reinterpret_cast<volatile DkvItem*>(hd->items);
+  enter<kBwdWarps>(hd, L::count, L::arrivals);
   const uint32_t bar0 = smem_addr(hd->bar);
   auto bar = [&](int i) { return bar0 + 8u * i; };
   const WaitCtx w{&hd->abort_flag, p.err, p.wait_limit_ns};
   const uint32_t tmem = uniform(hd->tmem);
   const uint32_t tS = tmem, tP = tmem + 128, tdV = tmem + 256, tdK = tmem + 256 + DP;
-  const int start = uniform(hd->start), len = uniform(hd->len), kt = uniform(hd->tile);
-  const int nq = (len + 127) >> 7;
-  const int i0 = p.causal ? kt : 0;
-  const int per = uniform(hd->found) ? nq - i0 : 0;  // query tiles a head
-  const int total = per * p.group;
-  QueryWalk q{kvh * p.group, i0, i0, nq};
+  struct Work {
+    int start, len, kt, kvh, i0, nq, total;
+    __device__ __forceinline__ QueryWalk walk(const RcParams& p) const { return QueryWalk{kvh * p.group, i0, i0, nq}; }
+  };
+  auto work_of = [&](int start, int len, int tile, int head) {
+    Work k;
+    k.start = start;
+    k.len = len;
+    k.kt = tile;
+    k.kvh = head;
+    k.nq = (len + 127) >> 7;
+    k.i0 = p.causal ? tile : 0;
+    k.total = (k.nq - k.i0) * p.group;  // (query head, query tile) pairs
+    return k;
+  };
+  // the item in `slot`, once it is there
+  auto read_item = [&](int slot) {
+    return work_of(uniform(items[slot].start), uniform(items[slot].len), uniform(items[slot].tile),
+                   uniform(items[slot].head));
+  };
 
-  if (warp == kBwdWarps + 2 && total > 0) {
-    const HeadAt hk = head_at(kvh, p.hk);
+  if (warp == kBwdWarps + 2) {
     Flight fl;
-    uint32_t tail_phase = 0;
+    uint32_t tail_phase = 0, it = 0;  // it: (Q, dC) tiles loaded
     bool ok = true, skip = p.fault_skip != 0;
     if (lane == 0) {
       prefetch_tmap(&p.mapQ);
       prefetch_tmap(&p.mapO);
-      if (!skip) {
-        mbar_arrive_expect_tx(bar(L::kvfull), 2 * L::kTile);
-        fl.note(L::kvfull, 0);
-        load_tile<DP>(smem_addr(sK), &p.mapK, bar(L::kvfull), start + 128 * kt, hk);
-        load_tile<DP>(smem_addr(sV), &p.mapV, bar(L::kvfull), start + 128 * kt, hk);
-      }
     }
-    for (int it = 0; ok && it < total; ++it, q.next()) {
-      const int sq = it % L::kQ, so = it % L::kO;
-      const uint32_t pq = (it / L::kQ) & 1, po = (it / L::kO) & 1;
-      const HeadAt hq = head_at(q.g, p.hq);
-      const bool cut = 128 * q.i + 128 > len && start + len < p.T;  // rows of nobody in the tile
-      if (lane == 0) ok = wait_bounded(bar(L::qempty + sq), pq ^ 1u, w);
-      ok = __shfl_sync(0xffffffffu, ok, 0);
-      if (!ok) break;
-      if (cut) {
-        ok = load_tail<DP>(sQ + sq * L::kTile, &p.mapQ, bar(L::qfull + sq), bar(L::tail), tail_phase,
-                           start + 128 * q.i, hq, len - 128 * q.i, lane, w);
-        if (!ok) break;
-      } else if (lane == 0) {
-        mbar_arrive_expect_tx(bar(L::qfull + sq), L::kTile);
-        fl.note(L::qfull + sq, pq);
-        load_tile<DP>(smem_addr(sQ + sq * L::kTile), &p.mapQ, bar(L::qfull + sq), start + 128 * q.i, hq);
+    ItemWalk items_of(p, p.KV);
+    for (uint32_t n = 0; ok; ++n) {
+      const int slot = n & 1;
+      Unit u{0, 0, 0};
+      const bool found = items_of.next(p, 128, false, lane, u);
+      if (!(ok = wait_warp(bar(L::free_ + slot), ((n >> 1) & 1) ^ 1, w))) break;
+      if (lane == 0) {
+        items[slot].start = u.start;
+        items[slot].len = u.len;
+        items[slot].tile = u.tile;
+        items[slot].head = found ? items_of.index : -1;
+        mbar_arrive(bar(L::info + slot));
       }
-      if (lane == 0) ok = wait_bounded(bar(L::oempty + so), po ^ 1u, w);
-      ok = __shfl_sync(0xffffffffu, ok, 0);
-      if (!ok) break;
-      if (cut) {
-        ok = load_tail<DP>(sO + so * L::kTile, &p.mapO, bar(L::ofull + so), bar(L::tail), tail_phase,
-                           start + 128 * q.i, hq, len - 128 * q.i, lane, w);
-      } else if (lane == 0) {
-        mbar_arrive_expect_tx(bar(L::ofull + so), L::kTile);
-        fl.note(L::ofull + so, po);
-        load_tile<DP>(smem_addr(sO + so * L::kTile), &p.mapO, bar(L::ofull + so), start + 128 * q.i, hq);
+      if (!found) break;
+      const Work k = work_of(u.start, u.len, u.tile, items_of.index);
+      const HeadAt hk = head_at(k.kvh, p.hk);
+      QueryWalk q = k.walk(p);
+      const int start = k.start, len = k.len;
+      for (int i = 0; ok && i < k.total; ++i, ++it, q.next()) {
+        const int sq = it % L::kQ, so = it % L::kO;
+        const uint32_t pq = (it / L::kQ) & 1, po = (it / L::kO) & 1;
+        const HeadAt hq = head_at(q.g, p.hq);
+        const bool torn = 128 * q.i + 128 > len && start + len < p.T;  // rows of nobody in the tile
+        if (lane == 0) ok = wait_bounded(bar(L::qempty + sq), pq ^ 1u, w);
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+        if (!ok) break;
+        if (torn) {
+          ok = load_tail<DP>(sQ + sq * L::kTile, &p.mapQ, bar(L::qfull + sq), bar(L::tail), tail_phase,
+                             start + 128 * q.i, hq, len - 128 * q.i, lane, w);
+          if (!ok) break;
+        } else if (lane == 0) {
+          mbar_arrive_expect_tx(bar(L::qfull + sq), L::kTile);
+          fl.note(L::qfull + sq, pq);
+          load_tile<DP>(smem_addr(sQ + sq * L::kTile), &p.mapQ, bar(L::qfull + sq), start + 128 * q.i, hq);
+        }
+        if (i == 0 && lane == 0) {
+          // K and V of the item, once the last products of the one before have read theirs
+          ok = wait_bounded(bar(L::kvempty), (n & 1) ^ 1, w);
+          if (ok && !skip) {
+            mbar_arrive_expect_tx(bar(L::kvfull), 2 * L::kTile);
+            fl.note(L::kvfull, n & 1);
+            load_tile<DP>(smem_addr(sK), &p.mapK, bar(L::kvfull), start + 128 * k.kt, hk);
+            load_tile<DP>(smem_addr(sV), &p.mapV, bar(L::kvfull), start + 128 * k.kt, hk);
+          }
+          skip = false;
+        }
+        if (lane == 0) ok = ok && wait_bounded(bar(L::oempty + so), po ^ 1u, w);
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+        if (!ok) break;
+        if (torn) {
+          ok = load_tail<DP>(sO + so * L::kTile, &p.mapO, bar(L::ofull + so), bar(L::tail), tail_phase,
+                             start + 128 * q.i, hq, len - 128 * q.i, lane, w);
+        } else if (lane == 0) {
+          mbar_arrive_expect_tx(bar(L::ofull + so), L::kTile);
+          fl.note(L::ofull + so, po);
+          load_tile<DP>(smem_addr(sO + so * L::kTile), &p.mapO, bar(L::ofull + so), start + 128 * q.i, hq);
+        }
       }
     }
     if (lane == 0 && *w.abort_flag) fl.drain(bar0, p.wait_limit_ns);
@@ -1143,226 +1184,265 @@ __global__ void __launch_bounds__(kDkvThreads, 1) rc_dkv_kernel(const __grid_con
     // (-lse log2 e, -D) of the query tiles; a row past the sequence gets
     // probability 2^(x - inf) = 0
     bool ok = true;
-    for (int it = 0; ok && it < total; ++it, q.next()) {
-      const int buf = it & 1;
-      float nl[4], nd[4];
-#pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        const int pos = 128 * q.i + 32 * x + lane;
-        const int64_t at = static_cast<int64_t>(q.g) * p.T + start + pos;
-        nl[x] = pos < len ? -p.lse[at] * kLog2e : -INFINITY;
-        nd[x] = pos < len ? -p.D[at] : 0.f;
-      }
-      if (!(ok = wait_warp(bar(L::vecempty + buf), ((it >> 1) & 1) ^ 1u, w))) break;
-#pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        vec[256 * buf + 32 * x + lane] = nl[x];
-        vec[256 * buf + 128 + 32 * x + lane] = nd[x];
-      }
+    uint32_t it = 0;
+    for (uint32_t n = 0; ok; ++n) {
+      const int slot = n & 1;
+      if (!(ok = wait_warp(bar(L::info + slot), (n >> 1) & 1, w))) break;
+      const Work k = read_item(slot);
       __syncwarp();
-      if (lane == 0) mbar_arrive(bar(L::vecfull + buf));
+      if (lane == 0) mbar_arrive(bar(L::free_ + slot));
+      if (k.kvh < 0) break;
+      QueryWalk q = k.walk(p);
+      for (int i = 0; i < k.total; ++i, ++it, q.next()) {
+        const int buf = it & 1;
+        float nl[4], nd[4];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const int pos = 128 * q.i + 32 * x + lane;
+          const int64_t at = static_cast<int64_t>(q.g) * p.T + k.start + pos;
+          nl[x] = pos < k.len ? -p.lse[at] * kLog2e : -INFINITY;
+          nd[x] = pos < k.len ? -p.D[at] : 0.f;
+        }
+        if (!(ok = wait_warp(bar(L::vecempty + buf), ((it >> 1) & 1) ^ 1u, w))) break;
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          vec[256 * buf + 32 * x + lane] = nl[x];
+          vec[256 * buf + 128 + 32 * x + lane] = nd[x];
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(L::vecfull + buf));
+      }
     }
-  } else if (warp == kBwdWarps && total > 0) {
-    // products through the scores: S^T = K Q^T, then dV += P^T dC
+  } else if (warp == kBwdWarps || warp == kBwdWarps + 1) {
+    // Warp 0: products through the scores, S^T = K Q^T, then dV += P^T dC.
+    // Warp 1: through their gradient, dP^T = V dC^T, then dK += dS^T Q.
+    const bool grad = warp == kBwdWarps + 1;
     const int ksteps = (p.d + 15) >> 4;
     const uint32_t idesc_out = idesc_bf16(0, 1, ksteps * 16);
-    bool ok = wait_warp(bar(L::kvfull), 0, w), issued = false;
-    for (int it = -1; ok && it < total; ++it) {
-      const int sn = (it + 1) % L::kQ, so = it % L::kO;
-      if (it + 1 < total && !(ok = wait_warp(bar(L::qfull + sn), ((it + 1) / L::kQ) & 1, w))) break;
-      if (it >= 0) {
-        if (!(ok = wait_warp(bar(L::ofull + so), (it / L::kO) & 1, w))) break;
-        // P comes in two halves of the contraction (16 of every 32 queries)
-        if (!(ok = wait_warp(bar(L::pready), it & 1, w))) break;
-        tc_fence_after();
-        if (elect_one()) mma_rows<4, 0, 1>(tdV, tS, smem_addr(sO + so * L::kTile), idesc_out, it > 0);
-        __syncwarp();
-        if (!(ok = wait_warp(bar(L::pready + 1), it & 1, w))) break;
-      }
-      tc_fence_after();
-      issued = true;
-      if (elect_one()) {
-        if (it >= 0) {
-          mma_rows<4, 1, 1>(tdV, tS, smem_addr(sO + so * L::kTile), idesc_out, true);
-          mma_commit(bar(L::oempty + so));
-        }
-        if (it + 1 < total) {
-          mma_scores<DP>(tS, smem_addr(sK), smem_addr(sQ + sn * L::kTile), ksteps);
-          mma_commit(bar(L::sfull));
-        } else {
-          mma_commit(bar(L::done));
-        }
-      }
+    const uint32_t tX = grad ? tP : tS, tD = grad ? tdK : tdV;       // products, sums
+    const uint32_t a = smem_addr(grad ? sV : sK);                    // A of the products
+    Ring x{0, grad ? L::kO : L::kQ, 0u}, d{0, grad ? L::kQ : L::kO, 0u};  // of the next products, of the next sum
+    const uint32_t xtiles = smem_addr(grad ? sO : sQ), dtiles = smem_addr(grad ? sQ : sO);
+    const int xfull = grad ? L::ofull : L::qfull, dfull = grad ? L::qfull : L::ofull;
+    const int ready = grad ? L::dsready : L::pready, out = grad ? L::dpfull : L::sfull;
+    uint32_t it = 0;  // sums so far
+    bool ok = true, issued = false;
+    for (uint32_t n = 0; ok; ++n) {
+      const int slot = n & 1;
+      if (!(ok = wait_warp(bar(L::info + slot), (n >> 1) & 1, w))) break;
+      const Work k = read_item(slot);
       __syncwarp();
-    }
-    if (*w.abort_flag && issued && elect_one()) drain_mma(bar(L::drain), p.wait_limit_ns);
-  } else if (warp == kBwdWarps + 1 && total > 0) {
-    // products through their gradient: dP^T = V dC^T, then dK += dS^T Q
-    const int ksteps = (p.d + 15) >> 4;
-    const uint32_t idesc_out = idesc_bf16(0, 1, ksteps * 16);
-    bool ok = wait_warp(bar(L::kvfull), 0, w), issued = false;
-    for (int it = -1; ok && it < total; ++it) {
-      const int sn = (it + 1) % L::kO, sq = it % L::kQ;
-      if (it + 1 < total && !(ok = wait_warp(bar(L::ofull + sn), ((it + 1) / L::kO) & 1, w))) break;
-      if (it >= 0) {
-        if (!(ok = wait_warp(bar(L::qfull + sq), (it / L::kQ) & 1, w))) break;
-        if (!(ok = wait_warp(bar(L::dsready), it & 1, w))) break;
+      if (lane == 0) mbar_arrive(bar(L::free_ + slot));
+      if (k.kvh < 0) break;
+      if (!(ok = wait_warp(bar(L::kvfull), n & 1, w))) break;
+      for (int i = -1; i < k.total; ++i) {
+        const bool more = i + 1 < k.total;
+        if (more && !(ok = wait_warp(bar(xfull + x.stage), x.phase, w))) break;
+        if (i >= 0) {
+          if (!(ok = wait_warp(bar(dfull + d.stage), d.phase, w))) break;
+          // the sums of the item before have been read
+          if (i == 0 && !(ok = wait_warp(bar(L::dfree), (n & 1) ^ 1, w))) break;
+          // P or dS comes in two halves of the contraction (16 of every 32 queries)
+          if (!(ok = wait_warp(bar(ready), it & 1, w))) break;
+          tc_fence_after();
+          if (elect_one()) mma_rows<4, 0, 1>(tD, tX, dtiles + d.stage * L::kTile, idesc_out, i > 0);
+          __syncwarp();
+          if (!(ok = wait_warp(bar(ready + 1), it & 1, w))) break;
+        }
         tc_fence_after();
-        if (elect_one()) mma_rows<4, 0, 1>(tdK, tP, smem_addr(sQ + sq * L::kTile), idesc_out, it > 0);
+        issued = true;
+        if (elect_one()) {
+          if (i >= 0) {
+            mma_rows<4, 1, 1>(tD, tX, dtiles + d.stage * L::kTile, idesc_out, true);
+            mma_commit(bar((grad ? L::qempty : L::oempty) + d.stage));
+          }
+          if (more) {
+            mma_scores<DP>(tX, a, xtiles + x.stage * L::kTile, ksteps);
+            mma_commit(bar(out));
+            if (grad) mma_commit(bar(L::oempty + x.stage));
+            if (i + 2 == k.total) mma_commit(bar(L::kvempty));
+          } else {
+            mma_commit(bar(L::done));
+          }
+        }
         __syncwarp();
-        if (!(ok = wait_warp(bar(L::dsready + 1), it & 1, w))) break;
-      }
-      tc_fence_after();
-      issued = true;
-      if (elect_one()) {
-        if (it >= 0) {
-          mma_rows<4, 1, 1>(tdK, tP, smem_addr(sQ + sq * L::kTile), idesc_out, true);
-          mma_commit(bar(L::qempty + sq));
+        if (i >= 0) {
+          d.next();
+          ++it;
         }
-        if (it + 1 < total) {
-          mma_scores<DP>(tP, smem_addr(sV), smem_addr(sO + sn * L::kTile), ksteps);
-          mma_commit(bar(L::dpfull));
-          mma_commit(bar(L::oempty + sn));
-        } else {
-          mma_commit(bar(L::done));
-        }
+        if (more) x.next();
       }
-      __syncwarp();
     }
-    if (*w.abort_flag && issued && elect_one()) drain_mma(bar(L::drain + 1), p.wait_limit_ns);
-  } else if (warp < kBwdWarps && total > 0) {
+    if (*w.abort_flag && issued && elect_one()) drain_mma(bar(L::drain + grad), p.wait_limit_ns);
+  } else if (warp < kBwdWarps) {
     const int part = warp >> 2;              // the 32 query columns of this warp
     const int key = (warp & 3) * 32 + lane;  // row of the transposed tile
     const uint32_t lb = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t tSw = tS + lb + 32 * part, tPw = tP + lb + 32 * part;
     const uint64_t scl2 = pack2(p.scale_log2, p.scale_log2);
-    // After a failed wait the loop runs on without waiting: the named barriers
-    // below need every warp, and nothing is stored at the end.
+    // After a failed wait an item runs on without waiting: the named barriers
+    // need every warp, nothing is stored at its end, and all leave together.
     bool ok = true;
     int table_head = -1;
-    for (int it = 0; it < total; ++it, q.next()) {
-      const int buf = it & 1;
-      if (BIAS && table_head != q.g) {
-        // the next query head's bias; every compute warp reads the table
-        table_head = q.g;
-        named_bar(1, 32 * kBwdWarps);
-        fill_table(p, q.g, map, tab, threadIdx.x, 32 * kBwdWarps);
-        named_bar(1, 32 * kBwdWarps);
-      }
-      float add = 0.f;
-      bool near = false;
-      const float* tb = nullptr;
-      if (BIAS) {
-        const int side = bias_side(p.bias.md, 128 * q.i, 128 * kt);
-        near = side == 0;
-        if (!near) add = tab[side < 0 ? 0 : 2 * (p.bias.md + kPad)];
-        // distance of column c: key - query = (128 kt + key) - (128 i + 32 part + c)
-        tb = tab + (128 * (kt - q.i) + key - 32 * part + p.bias.md + kPad);
-      }
-      ok = ok && wait_warp(bar(L::vecfull + buf), (it >> 1) & 1, w);
-      const float4* nl4 = reinterpret_cast<const float4*>(vec + 256 * buf + 32 * part);
-      const float4* nd4 = reinterpret_cast<const float4*>(vec + 256 * buf + 128 + 32 * part);
-      ok = ok && wait_warp(bar(L::sfull), it & 1, w);
-      tc_fence_after();
-      uint32_t s[32];
-      tmem_ld32_issue(tSw, s);
-      tmem_ld32_wait(s);
-      const uint64_t add2v = pack2(add, add);
-      const bool diagonal = p.causal && q.i == kt;
-      const int first = key - 32 * part;  // the first query column that sees this key, on the diagonal
+    uint32_t it = 0;  // tiles so far
+    for (uint32_t n = 0;; ++n) {
+      const int slot = n & 1;
+      ok = ok && wait_warp(bar(L::info + slot), (n >> 1) & 1, w);
+      if (named_bar_any(2, 32 * kBwdWarps, !ok)) break;
+      const Work k = read_item(slot);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(L::free_ + slot));
+      if (k.kvh < 0) break;
+      QueryWalk q = k.walk(p);
+      const int kt = k.kt;
+      for (int i = 0; i < k.total; ++i, ++it, q.next()) {
+        const int buf = it & 1;
+        if (BIAS && table_head != q.g) {
+          // the next query head's bias; every compute warp reads the table
+          table_head = q.g;
+          named_bar(1, 32 * kBwdWarps);
+          fill_table(p, q.g, map, tab, threadIdx.x, 32 * kBwdWarps);
+          named_bar(1, 32 * kBwdWarps);
+        }
+        float add = 0.f;
+        bool near = false;
+        const float* tb = nullptr;
+        if (BIAS) {
+          const int side = bias_side(p.bias.md, 128 * q.i, 128 * kt);
+          near = side == 0;
+          if (!near) add = tab[side < 0 ? 0 : 2 * (p.bias.md + kPad)];
+          // distance of column c: key - query = (128 kt + key) - (128 i + 32 part + c)
+          tb = tab + (128 * (kt - q.i) + key - 32 * part + p.bias.md + kPad);
+        }
+        ok = ok && wait_warp(bar(L::vecfull + buf), (it >> 1) & 1, w);
+        const float4* nl4 = reinterpret_cast<const float4*>(vec + 256 * buf + 32 * part);
+        const float4* nd4 = reinterpret_cast<const float4*>(vec + 256 * buf + 128 + 32 * part);
+        ok = ok && wait_warp(bar(L::sfull), it & 1, w);
+        tc_fence_after();
+        uint32_t s[32];
+        tmem_ld32_issue(tSw, s);
+        tmem_ld32_wait(s);
+        const uint64_t add2v = pack2(add, add);
+        const bool diagonal = p.causal && q.i == kt;
+        const int first = key - 32 * part;  // the first query column that sees this key, on the diagonal
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        uint32_t pk[8];
+        for (int h = 0; h < 2; ++h) {
+          uint32_t pk[8];
 #pragma unroll
-        for (int c = 16 * h; c < 16 * h + 16; c += 4) {
-          const float4 n = nl4[c >> 2];
-          uint64_t o0 = pack2(n.x, n.y), o1 = pack2(n.z, n.w);
-          if (BIAS) {
-            if (near) {
-              o0 = add2(o0, pack2(tb[-c], tb[-c - 1]));
-              o1 = add2(o1, pack2(tb[-c - 2], tb[-c - 3]));
-            } else {
-              o0 = add2(o0, add2v);
-              o1 = add2(o1, add2v);
+          for (int c = 16 * h; c < 16 * h + 16; c += 4) {
+            const float4 n = nl4[c >> 2];
+            uint64_t o0 = pack2(n.x, n.y), o1 = pack2(n.z, n.w);
+            if (BIAS) {
+              if (near) {
+                o0 = add2(o0, pack2(tb[-c], tb[-c - 1]));
+                o1 = add2(o1, pack2(tb[-c - 2], tb[-c - 3]));
+              } else {
+                o0 = add2(o0, add2v);
+                o1 = add2(o1, add2v);
+              }
             }
+            float x[4];
+            unpack2(fma2(pack2(as_f(s[c]), as_f(s[c + 1])), scl2, o0), x[0], x[1]);
+            unpack2(fma2(pack2(as_f(s[c + 2]), as_f(s[c + 3])), scl2, o1), x[2], x[3]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[c + e] = __float_as_uint(ex2_ftz(x[e]));
           }
-          float x[4];
-          unpack2(fma2(pack2(as_f(s[c]), as_f(s[c + 1])), scl2, o0), x[0], x[1]);
-          unpack2(fma2(pack2(as_f(s[c + 2]), as_f(s[c + 3])), scl2, o1), x[2], x[3]);
+          if (diagonal) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) s[c + e] = __float_as_uint(ex2_ftz(x[e]));
+            for (int c = 16 * h; c < 16 * h + 16; ++c) s[c] = c >= first ? s[c] : 0u;
+          }
+#pragma unroll
+          for (int c = 0; c < 8; ++c) pk[c] = pack_bf16x2(as_f(s[16 * h + 2 * c]), as_f(s[16 * h + 2 * c + 1]));
+          tmem_st8(tSw + 8 * h, pk);
+          tmem_st_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(L::pready + h));
         }
-        if (diagonal) {
+        ok = ok && wait_warp(bar(L::dpfull), it & 1, w);
+        tc_fence_after();
+        uint32_t g[32];
+        tmem_ld32_issue(tPw, g);
+        tmem_ld32_wait(g);
 #pragma unroll
-          for (int c = 16 * h; c < 16 * h + 16; ++c) s[c] = c >= first ? s[c] : 0u;
+        for (int h = 0; h < 2; ++h) {
+          uint32_t pk[8];
+#pragma unroll
+          for (int c = 16 * h; c < 16 * h + 16; c += 4) {
+            const float4 n = nd4[c >> 2];
+            float a, b;
+            unpack2(mul2(pack2(as_f(s[c]), as_f(s[c + 1])), add2(pack2(as_f(g[c]), as_f(g[c + 1])), pack2(n.x, n.y))),
+                    a, b);
+            pk[(c >> 1) & 7] = pack_bf16x2(a, b);
+            unpack2(mul2(pack2(as_f(s[c + 2]), as_f(s[c + 3])),
+                         add2(pack2(as_f(g[c + 2]), as_f(g[c + 3])), pack2(n.z, n.w))),
+                    a, b);
+            pk[((c >> 1) & 7) + 1] = pack_bf16x2(a, b);
+          }
+          tmem_st8(tPw + 8 * h, pk);
+          tmem_st_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(L::dsready + h));
         }
-#pragma unroll
-        for (int c = 0; c < 8; ++c) pk[c] = pack_bf16x2(as_f(s[16 * h + 2 * c]), as_f(s[16 * h + 2 * c + 1]));
-        tmem_st8(tSw + 8 * h, pk);
-        tmem_st_wait();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(L::pready + h));
+        if (lane == 0) mbar_arrive(bar(L::vecempty + buf));
       }
-      ok = ok && wait_warp(bar(L::dpfull), it & 1, w);
-      tc_fence_after();
-      uint32_t g[32];
-      tmem_ld32_issue(tPw, g);
-      tmem_ld32_wait(g);
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        uint32_t pk[8];
-#pragma unroll
-        for (int c = 16 * h; c < 16 * h + 16; c += 4) {
-          const float4 n = nd4[c >> 2];
-          float a, b;
-          unpack2(mul2(pack2(as_f(s[c]), as_f(s[c + 1])), add2(pack2(as_f(g[c]), as_f(g[c + 1])), pack2(n.x, n.y))), a, b);
-          pk[(c >> 1) & 7] = pack_bf16x2(a, b);
-          unpack2(mul2(pack2(as_f(s[c + 2]), as_f(s[c + 3])), add2(pack2(as_f(g[c + 2]), as_f(g[c + 3])), pack2(n.z, n.w))), a, b);
-          pk[((c >> 1) & 7) + 1] = pack_bf16x2(a, b);
-        }
-        tmem_st8(tPw + 8 * h, pk);
-        tmem_st_wait();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(L::dsready + h));
-      }
-      if (lane == 0) mbar_arrive(bar(L::vecempty + buf));
-    }
-    if (ok && wait_warp(bar(L::done), 0, w)) {
-      tc_fence_after();
       // dV by the first half of the warps, dK by the second; two warps share a row
+      ok = ok && wait_warp(bar(L::done), n & 1, w);
+      tc_fence_after();
       const int which = part >> 1, cut = first_columns(p.d);
-      const int first = part & 1 ? cut : 0, n = part & 1 ? p.d - cut : cut;
+      const int first = part & 1 ? cut : 0, cols = part & 1 ? p.d - cut : cut;
+      uint32_t r[DP / 2];
+#pragma unroll
+      for (int c = 0; c < DP / 64; ++c) tmem_ld32_issue((which ? tdK : tdV) + lb + first + 32 * c, r + 32 * c);
+#pragma unroll
+      for (int c = 0; c < DP / 64; ++c) tmem_ld32_wait(r + 32 * c);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(L::dfree));
       const int pos = 128 * kt + key;
-      const HeadAt hk = head_at(kvh, p.hk);
-      const int64_t col = static_cast<int64_t>(hk.shard) * p.shard_w + static_cast<int64_t>(p.hq) * p.d +
-                          static_cast<int64_t>(hk.local + (which ? 0 : p.hk)) * p.d + first;
-      store_row<DP / 64>((which ? tdK : tdV) + lb + first, n, which ? p.scale : 1.f,
-                         static_cast<__nv_bfloat16*>(p.dQKV) + (static_cast<int64_t>(start) + pos) * p.ld_dqkv + col,
-                         pos < len, p.wide);
+      if (ok && pos < k.len) {
+        const HeadAt hk = head_at(k.kvh, p.hk);
+        const int64_t col = static_cast<int64_t>(hk.shard) * p.shard_w + static_cast<int64_t>(p.hq) * p.d +
+                            static_cast<int64_t>(hk.local + (which ? 0 : p.hk)) * p.d + first;
+        store_columns<DP / 2>(r, cols, which ? p.scale : 1.f,
+                              static_cast<__nv_bfloat16*>(p.dQKV) +
+                                  (static_cast<int64_t>(k.start) + pos) * p.ld_dqkv + col,
+                              p.wide);
+      }
+      __syncwarp();
     }
   }
-  leave<kBwdWarps>(hd);
+  leave<kBwdWarps>(hd, p);
 }
 
 // TMEM: scores [0, 128), dP and then dS [128, 256), dQ [256, 384), Q [384, 448)
 // and dC [448, 512).  Q and dC stay there for the whole row of key tiles: the
 // products read K and V from shared memory alone (both operands there would
 // take all of its bandwidth), and three tiles of each fit.
-template <int DP>
+template <int DP, bool WITH_BIAS>
 struct DqShape {
   static constexpr int kTile = DP / 64 * kPanel;
-  static constexpr int kStages = DP == 128 ? 3 : 4;  // K tiles and V tiles held, each
-  static constexpr int kSmem = 2 * kStages * kTile + kBarBytes + 1024;
-  static constexpr int qfull = 0, kfull = 1, vfull = kfull + kStages, tail = vfull + kStages, kempty = tail + 1,
-                       vempty = kempty + kStages, sfull = vempty + kStages, sread = sfull + 1, dpfull = sread + 1,
-                       dsready = dpfull + 1, done = dsready + 2, drain = done + 1, count = drain + 1;
+  // K and V tiles held (a V tile is read once and soon; the bias's tables take one's place)
+  static constexpr int kK = DP == 128 ? 3 : 4, kV = DP == 128 && WITH_BIAS ? 2 : kK;
+  static constexpr int kSmem = (kK + kV) * kTile + kBarBytes + 1024;
+  static constexpr int qfull = 0, kfull = 1, vfull = kfull + kK, tail = vfull + kV, kempty = tail + 1,
+                       vempty = kempty + kK, sfull = vempty + kV, sread = sfull + 1, dpfull = sread + 1,
+                       dsready = dpfull + 1, done = dsready + 2, info = done + 1, tabfull = info + 2,
+                       free_ = tabfull + 2, drain = free_ + 2, count = drain + 1;
   static_assert(count <= kMaxBars && kempty <= 32, "barriers");
+  template <bool BIAS>
   static uint32_t __device__ __forceinline__ arrivals(int i) {
+    if (i >= free_ && i < drain) return kBwdWarps + 1 + (BIAS ? 1 : 0);
     return i == dsready || i == dsready + 1 || i == sread || i == qfull ? kBwdWarps : 1u;
   }
 };
+// What the TMA warp tells the other warps of an item (two slots).
+struct DqItem {
+  int start, len, r0, head, nk;  // r0: position of the first query row; head -1: no more items
+  int64_t item;
+};
+
 // The bias gradient's shared memory: per compute warp the sums of its 32 x 32
 // block by distance (63 of them), the CTA's sums by clamped distance, and the
 // threads' sums beyond the ends.
@@ -1373,41 +1453,33 @@ __host__ __device__ constexpr int grad_floats(int md) {
 
 template <int DP, bool BIAS>
 __global__ void __launch_bounds__(kDqThreads, 1) rc_dq_kernel(const __grid_constant__ RcParams p) {
-  using L = DqShape<DP>;
+  using L = DqShape<DP, BIAS>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = align1024(smem_raw);
   uint8_t* sK = smem;
-  uint8_t* sV = sK + L::kStages * L::kTile;
-  Head* hd = reinterpret_cast<Head*>(sV + L::kStages * L::kTile);
-  float* tab = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(hd) + kBarBytes);
-  uint8_t* map = reinterpret_cast<uint8_t*>(tab + (BIAS ? table_floats(p.bias.md) : 0));
-  if (BIAS) fill_map(p.bias, map);
-  const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
-  const int head = static_cast<int>(blockIdx.x % p.H);
-  const int64_t unit = blockIdx.x / p.H;
-  enter<kBwdWarps, kBwdWarps + 1>(p, hd, L::count, L::arrivals, unit, 128, p.causal != 0);
+  uint8_t* sV = sK + L::kK * L::kTile;
+  Head* hd = reinterpret_cast<Head*>(sV + L::kV * L::kTile);
+  volatile DqItem* items = reinterpret_cast<volatile DqItem*>(hd->items);
+  const int md = BIAS ? p.bias.md : 0, tabn = BIAS ? table_floats(md) : 0;
+  float* tabs = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(hd) + kBarBytes);  // a table for each slot
+  float* vals = tabs + 2 * tabn;                                    // the head's values
+  uint8_t* map = reinterpret_cast<uint8_t*>(vals + (BIAS ? kMaxRelBuckets : 0));  // the distances' buckets
+  float* diag = reinterpret_cast<float*>(map + tabn);               // [kBwdWarps][kDiag]
+  float* bins = diag + kBwdWarps * kDiag;                           // [2 md + 1]
+  float* ends = bins + 2 * md + 1;                                  // [2][32 kBwdWarps]
   const bool grad = BIAS && p.partial != nullptr;
-  const int md = BIAS ? p.bias.md : 0;
-  float* diag = reinterpret_cast<float*>(map + (BIAS ? table_floats(md) : 0));  // [kBwdWarps][kDiag]
-  float* bins = diag + kBwdWarps * kDiag;             // [2 md + 1]
-  float* ends = bins + 2 * md + 1;                    // [2][32 kBwdWarps]
-  if (BIAS) {
-    if (hd->found) fill_table(p, head, map, tab, threadIdx.x, kDqThreads);
-    if (grad)
-      for (int i = threadIdx.x; i < 2 * md + 1; i += kDqThreads) bins[i] = 0.f;
-    __syncthreads();
-  }
+  if (BIAS) fill_map(p.bias, map);
+  if (grad)
+    for (int i = threadIdx.x; i < 2 * md + 1; i += kDqThreads) bins[i] = 0.f;
+  const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
+  enter<kBwdWarps>(hd, L::count, L::template arrivals<BIAS>);
   const uint32_t bar0 = smem_addr(hd->bar);
   auto bar = [&](int i) { return bar0 + 8u * i; };
   const WaitCtx w{&hd->abort_flag, p.err, p.wait_limit_ns};
   const uint32_t tmem = uniform(hd->tmem);
   const uint32_t tP = tmem + 128, tdQ = tmem + 256, tQ = tmem + 384, tO = tmem + 448;
-  const int start = uniform(hd->start), len = uniform(hd->len), r0 = 128 * uniform(hd->tile);
-  const int nk_all = (len + 127) >> 7;
-  const int nk = uniform(hd->found) ? (p.causal ? min(nk_all, (r0 >> 7) + 1) : nk_all) : 0;
 
-  if (warp == kBwdWarps + 1 && nk > 0) {
-    const HeadAt hk = head_at(head / p.group, p.hk);
+  if (warp == kBwdWarps + 1) {
     Flight fl;
     uint32_t tail_phase = 0;
     bool ok = true, skip = p.fault_skip != 0;
@@ -1415,259 +1487,327 @@ __global__ void __launch_bounds__(kDqThreads, 1) rc_dq_kernel(const __grid_const
       prefetch_tmap(&p.mapK);
       prefetch_tmap(&p.mapV);
     }
-    for (int j = 0; ok && j < nk; ++j) {
-      const int st = j % L::kStages;
-      const uint32_t ph = (j / L::kStages) & 1;
-      if (lane == 0) ok = wait_bounded(bar(L::kempty + st), ph ^ 1u, w);
-      ok = __shfl_sync(0xffffffffu, ok, 0);
-      if (!ok) break;
-      if (128 * j + 128 > len && start + len < p.T) {
-        ok = load_tail<DP>(sK + st * L::kTile, &p.mapK, bar(L::kfull + st), bar(L::tail), tail_phase,
-                           start + 128 * j, hk, len - 128 * j, lane, w);
-        if (!ok) break;
-      } else if (lane == 0 && !skip) {
-        mbar_arrive_expect_tx(bar(L::kfull + st), L::kTile);
-        fl.note(L::kfull + st, ph);
-        load_tile<DP>(smem_addr(sK + st * L::kTile), &p.mapK, bar(L::kfull + st), start + 128 * j, hk);
-      }
-      skip = false;
+    ItemWalk items_of(p, p.H);
+    Ring kr{0, L::kK, 0u}, vr{0, L::kV, 0u};
+    for (uint32_t n = 0; ok; ++n) {
+      const int slot = n & 1;
+      Unit u{0, 0, 0};
+      const bool found = items_of.next(p, 128, p.causal != 0, lane, u, grad ? p.partial : nullptr, p.bias.nb);
+      if (!(ok = wait_warp(bar(L::free_ + slot), ((n >> 1) & 1) ^ 1, w))) break;
+      const int nk_all = (u.len + 127) >> 7, nk = p.causal ? min(nk_all, u.tile + 1) : nk_all;
       if (lane == 0) {
-        ok = wait_bounded(bar(L::vempty + st), ph ^ 1u, w);
-        if (ok) {
-          mbar_arrive_expect_tx(bar(L::vfull + st), L::kTile);
-          fl.note(L::vfull + st, ph);
-          load_tile<DP>(smem_addr(sV + st * L::kTile), &p.mapV, bar(L::vfull + st), start + 128 * j, hk);
-        }
+        items[slot].start = u.start;
+        items[slot].len = u.len;
+        items[slot].r0 = 128 * u.tile;
+        items[slot].head = found ? items_of.index : -1;
+        items[slot].nk = nk;
+        items[slot].item = items_of.item;
+        mbar_arrive(bar(L::info + slot));
       }
-      ok = __shfl_sync(0xffffffffu, ok, 0);
+      if (!found) break;
+      const HeadAt hk = head_at(items_of.index / p.group, p.hk);
+      for (int j = 0; ok && j < nk; ++j, kr.next(), vr.next()) {
+        const int st = kr.stage, sv = vr.stage;
+        const uint32_t ph = kr.phase;
+        if (lane == 0) ok = wait_bounded(bar(L::kempty + st), ph ^ 1u, w);
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+        if (!ok) break;
+        if (128 * j + 128 > u.len && u.start + u.len < p.T) {
+          ok = load_tail<DP>(sK + st * L::kTile, &p.mapK, bar(L::kfull + st), bar(L::tail), tail_phase,
+                             u.start + 128 * j, hk, u.len - 128 * j, lane, w);
+          if (!ok) break;
+        } else if (lane == 0 && !skip) {
+          mbar_arrive_expect_tx(bar(L::kfull + st), L::kTile);
+          fl.note(L::kfull + st, ph);
+          load_tile<DP>(smem_addr(sK + st * L::kTile), &p.mapK, bar(L::kfull + st), u.start + 128 * j, hk);
+        }
+        skip = false;
+        if (lane == 0) {
+          ok = wait_bounded(bar(L::vempty + sv), vr.phase ^ 1u, w);
+          if (ok) {
+            mbar_arrive_expect_tx(bar(L::vfull + sv), L::kTile);
+            fl.note(L::vfull + sv, vr.phase);
+            load_tile<DP>(smem_addr(sV + sv * L::kTile), &p.mapV, bar(L::vfull + sv), u.start + 128 * j, hk);
+          }
+        }
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+      }
     }
     if (lane == 0 && *w.abort_flag) fl.drain(bar0, p.wait_limit_ns);
     __syncwarp();
-  } else if (warp == kBwdWarps && nk > 0) {
+  } else if (BIAS && warp == kBwdWarps + 2) {
+    // the bias of an item's head, into its slot's table
+    for (uint32_t n = 0;; ++n) {
+      const int slot = n & 1;
+      if (!wait_warp(bar(L::info + slot), (n >> 1) & 1, w)) break;
+      const int head = items[slot].head;
+      if (head < 0) break;
+      fill_table_warp(p, head, map, vals, tabs + slot * tabn, lane);
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(bar(L::tabfull + slot));
+        mbar_arrive(bar(L::free_ + slot));
+      }
+    }
+  } else if (warp == kBwdWarps) {
     // After dS of a tile: dQ += dS K, dP = dC V^T of the next tile in dS's place,
     // and last the scores S = Q K^T of the one after, which nobody waits for yet:
     // they run while the compute warps make the next dS.
     const int ksteps = (p.d + 15) >> 4;
     const uint32_t idesc_out = idesc_bf16(0, 1, ksteps * 16);
-    auto kwait = [&](int j) { return wait_warp(bar(L::kfull + j % L::kStages), (j / L::kStages) & 1, w); };
-    auto vwait = [&](int j) { return wait_warp(bar(L::vfull + j % L::kStages), (j / L::kStages) & 1, w); };
-    auto scores = [&](int j) {
+    Ring kr{0, L::kK, 0u}, vr{0, L::kV, 0u}, dr{0, L::kK, 0u};  // of scores, of dP, of dQ
+    uint32_t nd = 0, ns = 0;  // dS tiles and score tiles so far
+    bool ok = true, issued = false;
+    auto scores = [&]() {
       tc_fence_after();
       if (elect_one()) {
-        mma_scores_ts<DP>(tmem, tQ, smem_addr(sK + (j % L::kStages) * L::kTile), ksteps);
+        mma_scores_ts<DP>(tmem, tQ, smem_addr(sK + kr.stage * L::kTile), ksteps);
         mma_commit(bar(L::sfull));
       }
       __syncwarp();
+      kr.next();
+      ++ns;
     };
-    bool ok = wait_warp(bar(L::qfull), 0, w) && kwait(0), issued = ok;
-    if (ok) scores(0);
-    for (int j = -1; ok && j < nk; ++j) {
-      const int st = j % L::kStages, sn = (j + 1) % L::kStages;
-      if (j + 1 < nk && !(ok = vwait(j + 1))) break;
-      if (j >= 0) {
-        // dS comes in two halves of the contraction (16 of every 32 keys)
-        if (!(ok = wait_warp(bar(L::dsready), j & 1, w))) break;
-        tc_fence_after();
-        if (elect_one()) mma_rows<4, 0, 1>(tdQ, tP, smem_addr(sK + st * L::kTile), idesc_out, j > 0);
-        __syncwarp();
-        if (!(ok = wait_warp(bar(L::dsready + 1), j & 1, w))) break;
-      }
-      tc_fence_after();
-      if (elect_one()) {
-        if (j >= 0) {
-          mma_rows<4, 1, 1>(tdQ, tP, smem_addr(sK + st * L::kTile), idesc_out, true);
-          mma_commit(bar(L::kempty + st));
-        }
-        if (j + 1 < nk) {
-          mma_scores_ts<DP>(tP, tO, smem_addr(sV + sn * L::kTile), ksteps);
-          mma_commit(bar(L::dpfull));
-          mma_commit(bar(L::vempty + sn));
-        } else {
-          mma_commit(bar(L::done));
-        }
-      }
+    for (uint32_t n = 0; ok; ++n) {
+      const int slot = n & 1;
+      if (!(ok = wait_warp(bar(L::info + slot), (n >> 1) & 1, w))) break;
+      const int nk = uniform(items[slot].nk);
+      const bool end = uniform(items[slot].head) < 0;
       __syncwarp();
-      if (j + 2 < nk) {
-        if (!(ok = kwait(j + 2) && wait_warp(bar(L::sread), (j + 1) & 1, w))) break;
-        scores(j + 2);
+      if (lane == 0) mbar_arrive(bar(L::free_ + slot));
+      if (end) break;
+      if (!(ok = wait_warp(bar(L::qfull), n & 1, w) && wait_warp(bar(L::kfull + kr.stage), kr.phase, w))) break;
+      issued = true;
+      scores();
+      for (int j = -1; j < nk; ++j) {
+        const bool more = j + 1 < nk;
+        if (more && !(ok = wait_warp(bar(L::vfull + vr.stage), vr.phase, w))) break;
+        if (j >= 0) {
+          // dS comes in two halves of the contraction (16 of every 32 keys)
+          if (!(ok = wait_warp(bar(L::dsready), nd & 1, w))) break;
+          tc_fence_after();
+          if (elect_one()) mma_rows<4, 0, 1>(tdQ, tP, smem_addr(sK + dr.stage * L::kTile), idesc_out, j > 0);
+          __syncwarp();
+          if (!(ok = wait_warp(bar(L::dsready + 1), nd & 1, w))) break;
+        }
+        tc_fence_after();
+        if (elect_one()) {
+          if (j >= 0) {
+            mma_rows<4, 1, 1>(tdQ, tP, smem_addr(sK + dr.stage * L::kTile), idesc_out, true);
+            mma_commit(bar(L::kempty + dr.stage));
+          }
+          if (more) {
+            mma_scores_ts<DP>(tP, tO, smem_addr(sV + vr.stage * L::kTile), ksteps);
+            mma_commit(bar(L::dpfull));
+            mma_commit(bar(L::vempty + vr.stage));
+          } else {
+            mma_commit(bar(L::done));
+          }
+        }
+        __syncwarp();
+        if (j >= 0) {
+          dr.next();
+          ++nd;
+        }
+        if (more) vr.next();
+        if (j + 2 < nk) {
+          if (!(ok = wait_warp(bar(L::kfull + kr.stage), kr.phase, w) && wait_warp(bar(L::sread), (ns - 1) & 1, w)))
+            break;
+          scores();
+        }
       }
     }
     if (*w.abort_flag && issued && elect_one()) drain_mma(bar(L::drain), p.wait_limit_ns);
   } else if (warp < kBwdWarps) {
     const int part = warp >> 2;  // the 32 key columns of this warp
     const int quarter = warp & 3;
-    const int row = r0 + quarter * 32 + lane;
-    const bool mine = row < len;
-    const int64_t token = static_cast<int64_t>(start) + row;
     const uint32_t lb = static_cast<uint32_t>(quarter * 32) << 16;
     const uint64_t scl2 = pack2(p.scale_log2, p.scale_log2);
-    float nl = 0.f, nd = 0.f;
-    if (nk > 0 && mine) {
-      nl = -p.lse[static_cast<int64_t>(head) * p.T + token] * kLog2e;
-      nd = -p.D[static_cast<int64_t>(head) * p.T + token];
-    }
-    const uint64_t nd2 = pack2(nd, nd);
-    if (nk > 0) {
-      // this warp's quarter of the columns of Q and dC into TMEM (zeros past the
-      // head and the sequence)
+    uint32_t nt = 0;  // tiles so far
+    // After a failed wait an item runs on without waiting: the named barriers
+    // need every warp, nothing of the gradient is stored, and all leave together.
+    bool ok = true;
+    for (uint32_t n = 0;; ++n) {
+      const int slot = n & 1;
+      ok = ok && wait_warp(bar(L::info + slot), (n >> 1) & 1, w);
+      if (named_bar_any(2, 32 * kBwdWarps, !ok)) break;
+      const int head = uniform(items[slot].head);
+      if (head < 0) break;
+      const int start = uniform(items[slot].start), len = uniform(items[slot].len), r0 = uniform(items[slot].r0);
+      const int nk = uniform(items[slot].nk);
+      const int64_t item = items[slot].item;
+      const int row = r0 + quarter * 32 + lane;
+      const bool mine = row < len;
+      const int64_t token = static_cast<int64_t>(start) + row;
       const HeadAt hq = head_at(head, p.hq);
       const int64_t qcol = static_cast<int64_t>(hq.shard) * p.shard_w + static_cast<int64_t>(hq.local) * p.d;
-      constexpr int kCols = DP / 4;
-      const int first = kCols * part;
-      fill_tmem_rows<kCols>(tQ + lb + first / 2,
-                            static_cast<const __nv_bfloat16*>(p.QKV) + token * p.ld_qkv + qcol + first,
-                            mine ? p.d - first : 0);
-      fill_tmem_rows<kCols>(tO + lb + first / 2,
-                            static_cast<const __nv_bfloat16*>(p.dC) + token * p.ld_dc +
-                                static_cast<int64_t>(head) * p.d + first,
-                            mine ? p.d - first : 0);
-      tmem_st_wait();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(L::qfull));
-    }
-    float end_lo = 0.f, end_hi = 0.f;  // dS at distances <= -md and >= md
-    // After a failed wait the loop runs on without waiting: the named barriers
-    // below need every warp, and nothing of the gradient is stored.
-    bool ok = true;
-    for (int j = 0; j < nk; ++j) {
-      const int c0 = 128 * j + 32 * part;  // key position of this warp's first column
-      int side = 0;
-      float off = nl;
-      const float* tb = nullptr;
-      if (BIAS) {
-        side = bias_side(md, r0, 128 * j);
-        if (side != 0) off += tab[side < 0 ? 0 : 2 * (md + kPad)];
-        tb = tab + (c0 - row + md + kPad);
+      const float* tab = tabs + slot * tabn;
+      float nl = 0.f, nd = 0.f;
+      if (mine) {
+        nl = -p.lse[static_cast<int64_t>(head) * p.T + token] * kLog2e;
+        nd = -p.D[static_cast<int64_t>(head) * p.T + token];
       }
-      const uint64_t off2 = pack2(off, off);
-      ok = ok && wait_warp(bar(L::sfull), j & 1, w);
-      tc_fence_after();
-      uint32_t s[32];
-      tmem_ld32_issue(tmem + lb + 32 * part, s);
-      tmem_ld32_wait(s);
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(L::sread));
-#pragma unroll
-      for (int c = 0; c < 32; c += 2) {
-        uint64_t o = off2;
-        if (BIAS) {
-          if (side == 0) o = add2(o, pack2(tb[c], tb[c + 1]));
-        }
-        float x0, x1;
-        unpack2(fma2(pack2(as_f(s[c]), as_f(s[c + 1])), scl2, o), x0, x1);
-        s[c] = __float_as_uint(ex2_ftz(x0));
-        s[c + 1] = __float_as_uint(ex2_ftz(x1));
-      }
-      const bool masked = (p.causal && 128 * j + 127 > r0) || 128 * j + 128 > len;
-      ok = ok && wait_warp(bar(L::dpfull), j & 1, w);
-      tc_fence_after();
-      uint32_t g[32];
-      tmem_ld32_issue(tP + lb + 32 * part, g);
-      tmem_ld32_wait(g);
-      const int seen = (p.causal ? min(len, row + 1) : len) - c0;
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        uint32_t pk[8];
-#pragma unroll
-        for (int c = 16 * h; c < 16 * h + 16; c += 2) {
-          float a, b;
-          unpack2(mul2(pack2(as_f(s[c]), as_f(s[c + 1])), add2(pack2(as_f(g[c]), as_f(g[c + 1])), nd2)), a, b);
-          s[c] = __float_as_uint(a);
-          s[c + 1] = __float_as_uint(b);
-        }
-        if (masked) {
-#pragma unroll
-          for (int c = 16 * h; c < 16 * h + 16; ++c) s[c] = c < seen ? s[c] : 0u;
-        }
-#pragma unroll
-        for (int c = 0; c < 8; ++c) pk[c] = pack_bf16x2(as_f(s[16 * h + 2 * c]), as_f(s[16 * h + 2 * c + 1]));
-        tmem_st8(tP + lb + 32 * part + 8 * h, pk);
+      const uint64_t nd2 = pack2(nd, nd);
+      {
+        // this warp's quarter of the columns of Q and dC into TMEM (zeros past the
+        // head and the sequence); the item before has been through its products
+        constexpr int kCols = DP / 4;
+        const int first = kCols * part;
+        fill_tmem_rows<kCols>(tQ + lb + first / 2,
+                              static_cast<const __nv_bfloat16*>(p.QKV) + token * p.ld_qkv + qcol + first,
+                              mine ? p.d - first : 0);
+        fill_tmem_rows<kCols>(tO + lb + first / 2,
+                              static_cast<const __nv_bfloat16*>(p.dC) + token * p.ld_dc +
+                                  static_cast<int64_t>(head) * p.d + first,
+                              mine ? p.d - first : 0);
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar(L::dsready + h));
+        if (lane == 0) mbar_arrive(bar(L::qfull));
       }
-      if (BIAS && grad) {
-        if (side != 0) {
-          float a[4] = {0.f, 0.f, 0.f, 0.f};
+      if (BIAS) ok = ok && wait_warp(bar(L::tabfull + slot), (n >> 1) & 1, w);
+      float end_lo = 0.f, end_hi = 0.f;  // dS at distances <= -md and >= md
+      for (int j = 0; j < nk; ++j, ++nt) {
+        const int c0 = 128 * j + 32 * part;  // key position of this warp's first column
+        int side = 0;
+        float off = nl;
+        const float* tb = nullptr;
+        if (BIAS) {
+          side = bias_side(md, r0, 128 * j);
+          if (side != 0) off += tab[side < 0 ? 0 : 2 * (md + kPad)];
+          tb = tab + (c0 - row + md + kPad);
+        }
+        const uint64_t off2 = pack2(off, off);
+        ok = ok && wait_warp(bar(L::sfull), nt & 1, w);
+        tc_fence_after();
+        uint32_t s[32];
+        tmem_ld32_issue(tmem + lb + 32 * part, s);
+        tmem_ld32_wait(s);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(L::sread));
 #pragma unroll
-          for (int c = 0; c < 32; ++c) a[c & 3] += as_f(s[c]);
-          const float sum = mine ? (a[0] + a[1]) + (a[2] + a[3]) : 0.f;
-          if (side < 0) end_lo += sum;
-          else end_hi += sum;
-        } else {
-          // Sums along the diagonals of the warp's 32 x 32 block: the running
-          // sum of a diagonal moves one lane up at every column; it is whole
-          // when it leaves lane 31.
-          float* dw = diag + warp * kDiag;
-          float acc = 0.f;
-#pragma unroll
-          for (int c = 0; c < 32; ++c) {
-            const float up = __shfl_up_sync(0xffffffffu, acc, 1);
-            acc = (lane == 0 ? 0.f : up) + (mine ? as_f(s[c]) : 0.f);
-            if (lane == 31) dw[c] = acc;  // distance (c - 31) + block offset
+        for (int c = 0; c < 32; c += 2) {
+          uint64_t o = off2;
+          if (BIAS) {
+            if (side == 0) o = add2(o, pack2(tb[c], tb[c + 1]));
           }
-          if (lane < 31) dw[62 - lane] = acc;
-          named_bar(1, 32 * kBwdWarps);
-          // thread x sums distance x - 127 of the tile over the warps' blocks
-          if (threadIdx.x < 255) {
-            const int dt = static_cast<int>(threadIdx.x) - 127;
-            float sum = 0.f;
+          float x0, x1;
+          unpack2(fma2(pack2(as_f(s[c]), as_f(s[c + 1])), scl2, o), x0, x1);
+          s[c] = __float_as_uint(ex2_ftz(x0));
+          s[c + 1] = __float_as_uint(ex2_ftz(x1));
+        }
+        const bool masked = (p.causal && 128 * j + 127 > r0) || 128 * j + 128 > len;
+        ok = ok && wait_warp(bar(L::dpfull), nt & 1, w);
+        tc_fence_after();
+        uint32_t g[32];
+        tmem_ld32_issue(tP + lb + 32 * part, g);
+        tmem_ld32_wait(g);
+        const int seen = (p.causal ? min(len, row + 1) : len) - c0;
 #pragma unroll
-            for (int wv = 0; wv < kBwdWarps; ++wv) {
-              const int at = dt - 32 * (wv >> 2) + 32 * (wv & 3) + 31;
-              if (at >= 0 && at < 63) sum += diag[wv * kDiag + at];
+        for (int h = 0; h < 2; ++h) {
+          uint32_t pk[8];
+#pragma unroll
+          for (int c = 16 * h; c < 16 * h + 16; c += 2) {
+            float a, b;
+            unpack2(mul2(pack2(as_f(s[c]), as_f(s[c + 1])), add2(pack2(as_f(g[c]), as_f(g[c + 1])), nd2)), a, b);
+            s[c] = __float_as_uint(a);
+            s[c + 1] = __float_as_uint(b);
+          }
+          if (masked) {
+#pragma unroll
+            for (int c = 16 * h; c < 16 * h + 16; ++c) s[c] = c < seen ? s[c] : 0u;
+          }
+#pragma unroll
+          for (int c = 0; c < 8; ++c) pk[c] = pack_bf16x2(as_f(s[16 * h + 2 * c]), as_f(s[16 * h + 2 * c + 1]));
+          tmem_st8(tP + lb + 32 * part + 8 * h, pk);
+          tmem_st_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(L::dsready + h));
+        }
+        if (BIAS && grad) {
+          if (side != 0) {
+            float a[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int c = 0; c < 32; ++c) a[c & 3] += as_f(s[c]);
+            const float sum = mine ? (a[0] + a[1]) + (a[2] + a[3]) : 0.f;
+            if (side < 0) end_lo += sum;
+            else end_hi += sum;
+          } else {
+            // Sums along the diagonals of the warp's 32 x 32 block: the running
+            // sum of a diagonal moves one lane up at every column; it is whole
+            // when it leaves lane 31.
+            float* dw = diag + warp * kDiag;
+            float acc = 0.f;
+#pragma unroll
+            for (int c = 0; c < 32; ++c) {
+              const float up = __shfl_up_sync(0xffffffffu, acc, 1);
+              acc = (lane == 0 ? 0.f : up) + (mine ? as_f(s[c]) : 0.f);
+              if (lane == 31) dw[c] = acc;  // distance (c - 31) + block offset
             }
-            const int delta = 128 * j - r0 + dt;
-            if (delta <= -md) end_lo += sum;
-            else if (delta >= md) end_hi += sum;
-            else bins[delta + md] += sum;
+            if (lane < 31) dw[62 - lane] = acc;
+            named_bar(1, 32 * kBwdWarps);
+            // thread x sums distance x - 127 of the tile over the warps' blocks
+            if (threadIdx.x < 255) {
+              const int dt = static_cast<int>(threadIdx.x) - 127;
+              float sum = 0.f;
+#pragma unroll
+              for (int wv = 0; wv < kBwdWarps; ++wv) {
+                const int at = dt - 32 * (wv >> 2) + 32 * (wv & 3) + 31;
+                if (at >= 0 && at < 63) sum += diag[wv * kDiag + at];
+              }
+              const int delta = 128 * j - r0 + dt;
+              if (delta <= -md) end_lo += sum;
+              else if (delta >= md) end_hi += sum;
+              else bins[delta + md] += sum;
+            }
+            named_bar(1, 32 * kBwdWarps);
           }
-          named_bar(1, 32 * kBwdWarps);
         }
       }
-    }
-    if (nk > 0 && ok && wait_warp(bar(L::done), 0, w)) {
+      ok = ok && wait_warp(bar(L::done), n & 1, w);
       tc_fence_after();
-      // the columns in 32s over the warps of a row
-      const int first = 32 * part, n = min(p.d - first, 32);
-      const HeadAt hq = head_at(head, p.hq);
-      if (n > 0)
-        store_row<1>(tdQ + lb + first, n, p.scale,
-                     static_cast<__nv_bfloat16*>(p.dQKV) + token * p.ld_dqkv +
-                         static_cast<int64_t>(hq.shard) * p.shard_w + static_cast<int64_t>(hq.local) * p.d + first,
-                     mine, p.wide);
-    }
-    if (BIAS && grad) {
-      // the CTA's sums by bucket, in a fixed order
-      constexpr int kN = 32 * kBwdWarps;
-      ends[threadIdx.x] = end_lo;
-      ends[kN + threadIdx.x] = end_hi;
-      named_bar(1, kN);
-      if (warp < 2) {
-        float a = 0.f;
-        for (int x = lane; x < kN; x += 32) a += ends[kN * warp + x];
+      {
+        // the columns in 32s over the warps of a row
+        const int first = 32 * part, cols = min(p.d - first, 32);
+        if (cols > 0)
+          store_row<1>(tdQ + lb + first, cols, p.scale,
+                       static_cast<__nv_bfloat16*>(p.dQKV) + token * p.ld_dqkv + qcol + first, ok && mine, p.wide);
+        tc_fence_before();
+      }
+      if (BIAS && grad) {
+        // the item's sums by bucket, in a fixed order
+        constexpr int kN = 32 * kBwdWarps;
+        ends[threadIdx.x] = end_lo;
+        ends[kN + threadIdx.x] = end_hi;
+        named_bar(1, kN);
+        if (warp < 2) {
+          float a = 0.f;
+          for (int x = lane; x < kN; x += 32) a += ends[kN * warp + x];
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
-        if (lane == 0) bins[warp ? 2 * md : 0] = a;
+          for (int o = 16; o > 0; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
+          if (lane == 0) bins[warp ? 2 * md : 0] = a;
+        }
+        named_bar(1, kN);
+        for (int u = threadIdx.x; u < p.bias.nb; u += kN) {
+          // bucket u holds the distances x with first[k] <= x < first[k + 1] on its side
+          const int k = u % p.bias.side;
+          const bool pos = p.bias.both && u >= p.bias.side;
+          const int lo = p.bias.first[k], hi = k + 1 < p.bias.side ? p.bias.first[k + 1] : md + 1;
+          float a = 0.f;
+          for (int x = max(lo, pos ? 1 : 0); x < min(hi, md + 1); ++x) a += bins[md + (pos ? x : -x)];
+          if (!p.bias.both && k == 0)
+            for (int x = 1; x <= md; ++x) a += bins[md + x];  // keys behind the query count as distance 0
+          p.partial[item * p.bias.nb + u] = a;
+        }
+        named_bar(1, kN);
+        for (int i = threadIdx.x; i < 2 * md + 1; i += kN) bins[i] = 0.f;
       }
-      named_bar(1, kN);
-      for (int u = threadIdx.x; u < p.bias.nb; u += kN) {
-        // bucket u holds the distances n with first[k] <= n < first[k + 1] on its side
-        const int k = u % p.bias.side;
-        const bool pos = p.bias.both && u >= p.bias.side;
-        const int lo = p.bias.first[k], hi = k + 1 < p.bias.side ? p.bias.first[k + 1] : md + 1;
-        float a = 0.f;
-        for (int n = max(lo, pos ? 1 : 0); n < min(hi, md + 1); ++n) a += bins[md + (pos ? n : -n)];
-        if (!p.bias.both && k == 0)
-          for (int n = 1; n <= md; ++n) a += bins[md + n];  // keys behind the query count as distance 0
-        p.partial[(unit * p.H + head) * p.bias.nb + u] = a;
-      }
+      if (lane == 0) mbar_arrive(bar(L::free_ + slot));
     }
   }
-  leave<kBwdWarps>(hd);
+  leave<kBwdWarps>(hd, p);
 }
 
 // dtable[u, h] (+)= the sum over the units' partial sums, in a fixed order: one
@@ -1726,15 +1866,22 @@ cudaError_t fwd_t(RcParams& p, int num_sms, cudaStream_t st) {
   return launch_rc(rc_fwd_kernel<DP, BIAS>, p.items < num_sms ? p.items : num_sms, kFwdThreads, smem, p, st);
 }
 template <int DP, bool BIAS>
-cudaError_t bwd_t(RcParams& p, cudaStream_t st) {
+cudaError_t bwd_t(RcParams& p, int num_sms, cudaStream_t st) {
   const int64_t units = units_of(p, 128);
+  const int n = BIAS ? table_floats(p.bias.md) : 0;
   p.wide = wide_rows(p, p.dQKV, p.ld_dqkv, p.shard_w);
-  const int tab = BIAS ? 5 * table_floats(p.bias.md) : 0;  // the table, and a byte a distance
-  cudaError_t e = launch_rc(rc_dkv_kernel<DP, BIAS>, units * p.KV, kDkvThreads, (DkvShape<DP, BIAS>::kSmem) + tab, p, st);
+  p.items = units * p.KV;
+  p.slot = static_cast<int>(g_rc_slot_seq.fetch_add(1) % kRcSlots);
+  // (a table of floats and a byte a distance)
+  cudaError_t e = launch_rc(rc_dkv_kernel<DP, BIAS>, p.items < num_sms ? p.items : num_sms, kDkvThreads,
+                            (DkvShape<DP, BIAS>::kSmem) + 5 * n, p, st);
   p.fault_skip = 0;
   if (e != cudaSuccess) return e;
-  e = launch_rc(rc_dq_kernel<DP, BIAS>, units * p.H, kDqThreads,
-                DqShape<DP>::kSmem + tab + (BIAS ? 4 * grad_floats(p.bias.md) : 0), p, st);
+  p.items = units * p.H;
+  p.slot = static_cast<int>(g_rc_slot_seq.fetch_add(1) % kRcSlots);
+  // (two tables, a head's values, a byte a distance, the sums)
+  e = launch_rc(rc_dq_kernel<DP, BIAS>, p.items < num_sms ? p.items : num_sms, kDqThreads,
+                (DqShape<DP, BIAS>::kSmem) + 9 * n + (BIAS ? 4 * (kMaxRelBuckets + grad_floats(p.bias.md)) : 0), p, st);
   if (e != cudaSuccess || !BIAS || p.partial == nullptr) return e;
   launch_k(rc_bias_sum_kernel, dim3(p.H, p.bias.nb), dim3(128), 0, st, p, units);
   count_launches(1);
@@ -1757,12 +1904,13 @@ cudaError_t launch_rc_bwd(RcParams& p, int num_sms, cudaStream_t st) {
   int lg = 0;
   while (8 << lg < p.d) ++lg;
   const int64_t blocks = (((p.T * p.H) << lg) + 255) / 256;
-  launch_k(rc_dot_kernel, dim3(static_cast<unsigned>(blocks < 16ll * num_sms ? blocks : 16ll * num_sms)), dim3(256), 0, st, p, lg);
+  const int64_t most = 16 * static_cast<int64_t>(num_sms);
+  launch_k(rc_dot_kernel, dim3(static_cast<unsigned>(blocks < most ? blocks : most)), dim3(256), 0, st, p, lg);
   count_launches(1);
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  if (p.d <= 64) return p.bias.nb ? bwd_t<64, true>(p, st) : bwd_t<64, false>(p, st);
-  return p.bias.nb ? bwd_t<128, true>(p, st) : bwd_t<128, false>(p, st);
+  if (p.d <= 64) return p.bias.nb ? bwd_t<64, true>(p, num_sms, st) : bwd_t<64, false>(p, num_sms, st);
+  return p.bias.nb ? bwd_t<128, true>(p, num_sms, st) : bwd_t<128, false>(p, num_sms, st);
 }
 
 }  // namespace tp
