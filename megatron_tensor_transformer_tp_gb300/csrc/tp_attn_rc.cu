@@ -447,58 +447,57 @@ __device__ __forceinline__ void mma_rows(uint32_t d_tmem, uint32_t a_tmem, uint3
 // A row's columns that the first of two warps takes, in 32s.
 __device__ __forceinline__ int first_columns(int d) { return min(d, 32 * ((d + 63) / 64)); }
 
-// n of COLS fp32 values of a row, scaled, as bf16 to memory; `wide`: every row
-// start is 32-byte aligned and n a multiple of 16.
+// COLS fp32 values, scaled, as bf16 pairs.
 template <int COLS>
-__device__ __forceinline__ void store_columns(const uint32_t* v, int n, float mul, __nv_bfloat16* out, bool wide) {
+__device__ __forceinline__ void pack_columns(const uint32_t* v, float mul, uint32_t* q) {
   const uint64_t mul2v = pack2(mul, mul);
 #pragma unroll
-  for (int c = 0; c < COLS; c += 16) {
-    uint32_t q[8];
+  for (int i = 0; i < COLS / 2; ++i) {
+    float a, b;
+    unpack2(mul2(pack2(as_f(v[2 * i]), as_f(v[2 * i + 1])), mul2v), a, b);
+    q[i] = pack_bf16x2(a, b);
+  }
+}
+// n of COLS bf16 values of a row to memory; `wide`: every row start is 32-byte
+// aligned and n a multiple of 16.
+template <int COLS>
+__device__ __forceinline__ void put_columns(const uint32_t* q, int n, __nv_bfloat16* out, bool wide) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      float a, b;
-      unpack2(mul2(pack2(as_f(v[c + 2 * i]), as_f(v[c + 2 * i + 1])), mul2v), a, b);
-      q[i] = pack_bf16x2(a, b);
-    }
+  for (int c = 0; c < COLS; c += 16) {
+    const uint32_t* r = q + c / 2;
     if (wide) {
       if (c < n)
-        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(out + c), "r"(q[0]), "r"(q[1]),
-                     "r"(q[2]), "r"(q[3]), "r"(q[4]), "r"(q[5]), "r"(q[6]), "r"(q[7])
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(out + c), "r"(r[0]), "r"(r[1]),
+                     "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
                      : "memory");
     } else {
-      if (c < n) *reinterpret_cast<uint4*>(out + c) = make_uint4(q[0], q[1], q[2], q[3]);
-      if (c + 8 < n) *reinterpret_cast<uint4*>(out + c + 8) = make_uint4(q[4], q[5], q[6], q[7]);
+      if (c < n) *reinterpret_cast<uint4*>(out + c) = make_uint4(r[0], r[1], r[2], r[3]);
+      if (c + 8 < n) *reinterpret_cast<uint4*>(out + c + 8) = make_uint4(r[4], r[5], r[6], r[7]);
     }
   }
 }
-// n <= 32 CHUNKS fp32 TMEM columns of the warp's rows, scaled, as bf16 to
-// memory.  Called by the whole warp.
-template <int CHUNKS>
-__device__ __forceinline__ void store_row(uint32_t taddr, int n, float mul, __nv_bfloat16* out, bool ok, bool wide) {
-  uint32_t r[32 * CHUNKS];
-#pragma unroll
-  for (int c = 0; c < CHUNKS; ++c) tmem_ld32_issue(taddr + 32 * c, r + 32 * c);
-#pragma unroll
-  for (int c = 0; c < CHUNKS; ++c) tmem_ld32_wait(r + 32 * c);
-  if (ok) store_columns<32 * CHUNKS>(r, n, mul, out, wide);
-  __syncwarp();
+template <int COLS>
+__device__ __forceinline__ void store_columns(const uint32_t* v, int n, float mul, __nv_bfloat16* out, bool wide) {
+  uint32_t q[COLS / 2];
+  pack_columns<COLS>(v, mul, q);
+  put_columns<COLS>(q, n, out, wide);
 }
 
-// COLS bf16 columns of a row of memory as COLS / 2 TMEM columns; `n` of them
-// exist (a multiple of 8, <= 0: none), the others become zeros.
+// COLS bf16 columns from column `first` of the thread's row of a swizzled tile
+// as COLS / 2 TMEM columns.
 template <int COLS>
-__device__ __forceinline__ void fill_tmem_rows(uint32_t taddr, const __nv_bfloat16* row, int n) {
+__device__ __forceinline__ void tile_to_tmem(uint32_t taddr, const uint8_t* tile, int row, int first) {
 #pragma unroll
   for (int c = 0; c < COLS; c += 16) {
     uint4 v[2];
 #pragma unroll
-    for (int q = 0; q < 2; ++q)
-      v[q] = c + 8 * q < n ? __ldg(reinterpret_cast<const uint4*>(row + c + 8 * q)) : make_uint4(0, 0, 0, 0);
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%8], {%0, %1, %2, %3, %4, %5, %6, %7};" ::"r"(v[0].x),
-                 "r"(v[0].y), "r"(v[0].z), "r"(v[0].w), "r"(v[1].x), "r"(v[1].y), "r"(v[1].z), "r"(v[1].w),
-                 "r"(taddr + c / 2)
-                 : "memory");
+    for (int q = 0; q < 2; ++q) {
+      const int col = first + c + 8 * q;  // 16 bytes; chunk x of a row lies at x ^ (row mod 8)
+      v[q] = *reinterpret_cast<const uint4*>(tile + (col >> 6) * kPanel + row * 128 +
+                                             ((((col & 63) >> 3) ^ (row & 7)) << 4));
+    }
+    const uint32_t r[8] = {v[0].x, v[0].y, v[0].z, v[0].w, v[1].x, v[1].y, v[1].z, v[1].w};
+    tmem_st8(taddr + c / 2, r);
   }
 }
 
@@ -978,39 +977,54 @@ __global__ void __launch_bounds__(kFwdThreads, 1) rc_fwd_kernel(const __grid_con
 // ===========================================================================
 // Backward
 // ===========================================================================
-// D[h, t] = dC_t . C_t over head h's columns, in fp32.  One group of lanes a
-// (token, head), 16 bytes a lane and tensor.
-__global__ void __launch_bounds__(256) rc_dot_kernel(const __grid_constant__ RcParams p, int lanes_log2) {
+// D[h, t] = dC_t . C_t over head h's columns, in fp32.  A warp takes two tokens
+// and goes through their heads, 2^LG lanes a head and 16 bytes a lane and
+// tensor, with the loads of two steps in flight.
+template <int LG>
+__global__ void __launch_bounds__(256) rc_dot_kernel(const __grid_constant__ RcParams p) {
   pdl_wait();
   pdl_trigger();
-  const int lg = lanes_log2, lanes = 1 << lg;
-  const int64_t n = p.T * p.H;
-  const int c = 8 * (threadIdx.x & (lanes - 1));
-  const int64_t step = (static_cast<int64_t>(gridDim.x) * 256) >> lg;
-  const int64_t i0 = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) >> lg;
-  const int64_t rounds = (n + step - 1) / step;
-  int64_t i = i0;
-  for (int64_t r = 0; r < rounds; ++r, i += step) {
-    float acc = 0.f;
-    const int64_t t = i / p.H;
-    const int h = static_cast<int>(i - t * p.H);
-    if (i < n && c < p.d) {
-      const uint4 a = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.C) + t * p.ld_c +
-                                                           static_cast<int64_t>(h) * p.d + c));
-      const uint4 b = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.dC) + t * p.ld_dc +
-                                                           static_cast<int64_t>(h) * p.d + c));
-      const uint32_t aa[4] = {a.x, a.y, a.z, a.w}, bb[4] = {b.x, b.y, b.z, b.w};
+  constexpr int kLanes = 1 << LG, kHeads = 32 >> LG;  // lanes a head, heads a step
+  const int lane = threadIdx.x & 31, c = 8 * (lane & (kLanes - 1)), h0 = lane >> LG;
+  const int64_t t0 = 2 * (static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5));
+  for (int hb = 0; hb < p.H; hb += 2 * kHeads) {
+    uint4 a[2][2], b[2][2];  // [step][token]
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        float x0, x1, y0, y1;
-        unpack_bf16x2(aa[q], x0, x1);
-        unpack_bf16x2(bb[q], y0, y1);
-        acc = fmaf(x0, y0, acc);
-        acc = fmaf(x1, y1, acc);
+    for (int s = 0; s < 2; ++s) {
+      const int h = hb + s * kHeads + h0;
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        a[s][k] = b[s][k] = make_uint4(0, 0, 0, 0);
+        if (h < p.H && c < p.d && t0 + k < p.T) {
+          const int64_t col = static_cast<int64_t>(h) * p.d + c;
+          a[s][k] =
+              __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.C) + (t0 + k) * p.ld_c + col));
+          b[s][k] =
+              __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.dC) + (t0 + k) * p.ld_dc + col));
+        }
       }
     }
-    for (int o = lanes >> 1; o > 0; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
-    if (i < n && c == 0) p.D[static_cast<int64_t>(h) * p.T + t] = acc;
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      const int h = hb + s * kHeads + h0;
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const uint32_t aa[4] = {a[s][k].x, a[s][k].y, a[s][k].z, a[s][k].w};
+        const uint32_t bb[4] = {b[s][k].x, b[s][k].y, b[s][k].z, b[s][k].w};
+        float acc = 0.f;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          float x0, x1, y0, y1;
+          unpack_bf16x2(aa[q], x0, x1);
+          unpack_bf16x2(bb[q], y0, y1);
+          acc = fmaf(x0, y0, acc);
+          acc = fmaf(x1, y1, acc);
+        }
+#pragma unroll
+        for (int o = kLanes >> 1; o > 0; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
+        if (c == 0 && h < p.H && t0 + k < p.T) p.D[static_cast<int64_t>(h) * p.T + t0 + k] = acc;
+      }
+    }
   }
 }
 
@@ -1484,6 +1498,8 @@ __global__ void __launch_bounds__(kDqThreads, 1) rc_dq_kernel(const __grid_const
     uint32_t tail_phase = 0;
     bool ok = true, skip = p.fault_skip != 0;
     if (lane == 0) {
+      prefetch_tmap(&p.mapQ);
+      prefetch_tmap(&p.mapO);
       prefetch_tmap(&p.mapK);
       prefetch_tmap(&p.mapV);
     }
@@ -1505,7 +1521,27 @@ __global__ void __launch_bounds__(kDqThreads, 1) rc_dq_kernel(const __grid_const
         mbar_arrive(bar(L::info + slot));
       }
       if (!found) break;
-      const HeadAt hk = head_at(items_of.index / p.group, p.hk);
+      const HeadAt hq = head_at(items_of.index, p.hq), hk = head_at(items_of.index / p.group, p.hk);
+      // Q and dC pass through a K and a V stage on their way to TMEM
+      if (lane == 0) {
+        ok = wait_bounded(bar(L::kempty + kr.stage), kr.phase ^ 1u, w);
+        if (ok) {
+          mbar_arrive_expect_tx(bar(L::kfull + kr.stage), L::kTile);
+          fl.note(L::kfull + kr.stage, kr.phase);
+          load_tile<DP>(smem_addr(sK + kr.stage * L::kTile), &p.mapQ, bar(L::kfull + kr.stage), u.start + 128 * u.tile,
+                        hq);
+          ok = wait_bounded(bar(L::vempty + vr.stage), vr.phase ^ 1u, w);
+        }
+        if (ok) {
+          mbar_arrive_expect_tx(bar(L::vfull + vr.stage), L::kTile);
+          fl.note(L::vfull + vr.stage, vr.phase);
+          load_tile<DP>(smem_addr(sV + vr.stage * L::kTile), &p.mapO, bar(L::vfull + vr.stage), u.start + 128 * u.tile,
+                        hq);
+        }
+      }
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+      kr.next();
+      vr.next();
       for (int j = 0; ok && j < nk; ++j, kr.next(), vr.next()) {
         const int st = kr.stage, sv = vr.stage;
         const uint32_t ph = kr.phase;
@@ -1576,7 +1612,17 @@ __global__ void __launch_bounds__(kDqThreads, 1) rc_dq_kernel(const __grid_const
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(L::free_ + slot));
       if (end) break;
-      if (!(ok = wait_warp(bar(L::qfull), n & 1, w) && wait_warp(bar(L::kfull + kr.stage), kr.phase, w))) break;
+      // Q and dC are in TMEM: their stages are free again
+      if (!(ok = wait_warp(bar(L::qfull), n & 1, w))) break;
+      if (lane == 0) {
+        mbar_arrive(bar(L::kempty + kr.stage));
+        mbar_arrive(bar(L::vempty + vr.stage));
+      }
+      __syncwarp();
+      kr.next();
+      vr.next();
+      dr.next();
+      if (!(ok = wait_warp(bar(L::kfull + kr.stage), kr.phase, w))) break;
       issued = true;
       scores();
       for (int j = -1; j < nk; ++j) {
@@ -1624,6 +1670,16 @@ __global__ void __launch_bounds__(kDqThreads, 1) rc_dq_kernel(const __grid_const
     const uint32_t lb = static_cast<uint32_t>(quarter * 32) << 16;
     const uint64_t scl2 = pack2(p.scale_log2, p.scale_log2);
     uint32_t nt = 0;  // tiles so far
+    uint32_t kc = 0;  // ring tiles so far (K's and V's go together)
+    // the columns of the output in 32s over the warps of a row; an item's are
+    // stored when the next one's Q and dC are in place
+    const int ofirst = 32 * part, ocols = min(p.d - ofirst, 32);
+    uint32_t dq[16];
+    __nv_bfloat16* prev = nullptr;  // where dq goes, if anywhere
+    auto put = [&]() {
+      if (prev != nullptr) put_columns<32>(dq, ocols, prev, p.wide);
+      __syncwarp();
+    };
     // After a failed wait an item runs on without waiting: the named barriers
     // need every warp, nothing of the gradient is stored, and all leave together.
     bool ok = true;
@@ -1632,39 +1688,38 @@ __global__ void __launch_bounds__(kDqThreads, 1) rc_dq_kernel(const __grid_const
       ok = ok && wait_warp(bar(L::info + slot), (n >> 1) & 1, w);
       if (named_bar_any(2, 32 * kBwdWarps, !ok)) break;
       const int head = uniform(items[slot].head);
-      if (head < 0) break;
+      if (head < 0) {
+        put();
+        break;
+      }
       const int start = uniform(items[slot].start), len = uniform(items[slot].len), r0 = uniform(items[slot].r0);
       const int nk = uniform(items[slot].nk);
-      const int64_t item = items[slot].item;
       const int row = r0 + quarter * 32 + lane;
       const bool mine = row < len;
-      const int64_t token = static_cast<int64_t>(start) + row;
-      const HeadAt hq = head_at(head, p.hq);
-      const int64_t qcol = static_cast<int64_t>(hq.shard) * p.shard_w + static_cast<int64_t>(hq.local) * p.d;
       const float* tab = tabs + slot * tabn;
       float nl = 0.f, nd = 0.f;
       if (mine) {
-        nl = -p.lse[static_cast<int64_t>(head) * p.T + token] * kLog2e;
-        nd = -p.D[static_cast<int64_t>(head) * p.T + token];
+        const int64_t at = static_cast<int64_t>(head) * p.T + start + row;
+        nl = -p.lse[at] * kLog2e;
+        nd = -p.D[at];
       }
       const uint64_t nd2 = pack2(nd, nd);
+      // this warp's quarter of the columns of Q and dC into TMEM; the item before
+      // has been through its products
       {
-        // this warp's quarter of the columns of Q and dC into TMEM (zeros past the
-        // head and the sequence); the item before has been through its products
-        constexpr int kCols = DP / 4;
-        const int first = kCols * part;
-        fill_tmem_rows<kCols>(tQ + lb + first / 2,
-                              static_cast<const __nv_bfloat16*>(p.QKV) + token * p.ld_qkv + qcol + first,
-                              mine ? p.d - first : 0);
-        fill_tmem_rows<kCols>(tO + lb + first / 2,
-                              static_cast<const __nv_bfloat16*>(p.dC) + token * p.ld_dc +
-                                  static_cast<int64_t>(head) * p.d + first,
-                              mine ? p.d - first : 0);
-        tmem_st_wait();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(L::qfull));
+        const int sk = kc % L::kK, sv = kc % L::kV;
+        ok = ok && wait_warp(bar(L::kfull + sk), (kc / L::kK) & 1, w) &&
+             wait_warp(bar(L::vfull + sv), (kc / L::kV) & 1, w);
+        tile_to_tmem<DP / 4>(tQ + lb + DP / 8 * part, sK + sk * L::kTile, quarter * 32 + lane, DP / 4 * part);
+        tile_to_tmem<DP / 4>(tO + lb + DP / 8 * part, sV + sv * L::kTile, quarter * 32 + lane, DP / 4 * part);
       }
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(L::qfull));
+      kc += nk + 1;
+      // the item before's output, while the first products of this one run
+      put();
       if (BIAS) ok = ok && wait_warp(bar(L::tabfull + slot), (n >> 1) & 1, w);
       float end_lo = 0.f, end_hi = 0.f;  // dS at distances <= -md and >= md
       for (int j = 0; j < nk; ++j, ++nt) {
@@ -1769,13 +1824,16 @@ __global__ void __launch_bounds__(kDqThreads, 1) rc_dq_kernel(const __grid_const
       ok = ok && wait_warp(bar(L::done), n & 1, w);
       tc_fence_after();
       {
-        // the columns in 32s over the warps of a row
-        const int first = 32 * part, cols = min(p.d - first, 32);
-        if (cols > 0)
-          store_row<1>(tdQ + lb + first, cols, p.scale,
-                       static_cast<__nv_bfloat16*>(p.dQKV) + token * p.ld_dqkv + qcol + first, ok && mine, p.wide);
-        tc_fence_before();
+        uint32_t r[32];
+        tmem_ld32_issue(tdQ + lb + 32 * min(part, DP / 32 - 1), r);
+        tmem_ld32_wait(r);
+        pack_columns<32>(r, p.scale, dq);
       }
+      tc_fence_before();
+      const HeadAt hq = head_at(uniform(items[slot].head), p.hq);
+      prev = static_cast<__nv_bfloat16*>(p.dQKV) + (static_cast<int64_t>(items[slot].start) + row) * p.ld_dqkv +
+             static_cast<int64_t>(hq.shard) * p.shard_w + static_cast<int64_t>(hq.local) * p.d + ofirst;
+      if (!ok || !mine || ocols <= 0) prev = nullptr;
       if (BIAS && grad) {
         // the item's sums by bucket, in a fixed order
         constexpr int kN = 32 * kBwdWarps;
@@ -1799,7 +1857,7 @@ __global__ void __launch_bounds__(kDqThreads, 1) rc_dq_kernel(const __grid_const
           for (int x = max(lo, pos ? 1 : 0); x < min(hi, md + 1); ++x) a += bins[md + (pos ? x : -x)];
           if (!p.bias.both && k == 0)
             for (int x = 1; x <= md; ++x) a += bins[md + x];  // keys behind the query count as distance 0
-          p.partial[item * p.bias.nb + u] = a;
+  p.partial[items[slot].item * p.bias.nb + u] = a;
         }
         named_bar(1, kN);
         for (int i = threadIdx.x; i < 2 * md + 1; i += kN) bins[i] = 0.f;
@@ -1903,9 +1961,14 @@ cudaError_t launch_rc_fwd(RcParams& p, int num_sms, cudaStream_t st) {
 cudaError_t launch_rc_bwd(RcParams& p, int num_sms, cudaStream_t st) {
   int lg = 0;
   while (8 << lg < p.d) ++lg;
-  const int64_t blocks = (((p.T * p.H) << lg) + 255) / 256;
-  const int64_t most = 16 * static_cast<int64_t>(num_sms);
-  launch_k(rc_dot_kernel, dim3(static_cast<unsigned>(blocks < most ? blocks : most)), dim3(256), 0, st, p, lg);
+  const dim3 grid(static_cast<unsigned>((p.T + 15) / 16));
+  switch (lg) {
+    case 0: launch_k(rc_dot_kernel<0>, grid, dim3(256), 0, st, p); break;
+    case 1: launch_k(rc_dot_kernel<1>, grid, dim3(256), 0, st, p); break;
+    case 2: launch_k(rc_dot_kernel<2>, grid, dim3(256), 0, st, p); break;
+    case 3: launch_k(rc_dot_kernel<3>, grid, dim3(256), 0, st, p); break;
+    default: launch_k(rc_dot_kernel<4>, grid, dim3(256), 0, st, p); break;
+  }
   count_launches(1);
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
