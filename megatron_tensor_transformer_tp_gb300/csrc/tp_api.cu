@@ -1330,8 +1330,6 @@ tp_status rc_args(tp_dtype dt, const tp_attn_config* c, const tp_relbias_config*
       (reinterpret_cast<uintptr_t>(seq_starts) & 7u) != 0)
     return TP_ERR_ALIGN;
   P->seq_starts = seq_starts;
-  P->QKV = QKV;
-  P->ld_qkv = ld_qkv;
   P->ld_c = ld_c;
   P->C = const_cast<void*>(C);
   P->lse = const_cast<float*>(lse);
@@ -1396,8 +1394,6 @@ tp_status rc_bwd_impl(const char* name, tp_dtype dt, const tp_attn_config* cfg, 
   const size_t dot = rc_dot_bytes(P.T, P.H);
   if (workspace == nullptr || ws_bytes < dot + (dtable ? rc_partial_bytes(P) : 0)) return TP_ERR_WORKSPACE;
   if (!al256(workspace)) return TP_ERR_ALIGN;
-  P.dC = dC;
-  P.ld_dc = ld_dc;
   P.dQKV = dQKV;
   P.ld_dqkv = ld_dqkv;
   P.D = reinterpret_cast<float*>(workspace);
@@ -1406,7 +1402,9 @@ tp_status rc_bwd_impl(const char* name, tp_dtype dt, const tp_attn_config* cfg, 
   P.partial = dtable ? reinterpret_cast<float*>(bb(workspace) + dot) : nullptr;
   DeviceState* dev = nullptr;
   if ((st = rc_device(&P, QKV, ld_qkv, cfg->N, &dev)) != TP_OK) return st;
-  if (!encode_map_heads(&P.mapO, dC, P.d, P.T, ld_dc, P.hq, cfg->N, static_cast<int64_t>(P.hq) * P.d))
+  const int64_t width = static_cast<int64_t>(P.hq) * P.d;
+  if (!encode_map_heads(&P.mapO, dC, P.d, P.T, ld_dc, P.hq, cfg->N, width) ||
+      !encode_map_heads(&P.mapC, C, P.d, P.T, ld_c, P.hq, cfg->N, width))
     return TP_ERR_CUDA;
   const int sms = dev->num_sms;
   return timed(name, s, [&] { return launch_rc_bwd(P, sms, s); }) == cudaSuccess ? TP_OK : TP_ERR_CUDA;

@@ -501,6 +501,28 @@ __device__ __forceinline__ void tile_to_tmem(uint32_t taddr, const uint8_t* tile
   }
 }
 
+// The product of COLS columns from `first` of the thread's row of two tiles.
+template <int COLS>
+__device__ __forceinline__ float dot_tiles(const uint8_t* x, const uint8_t* y, int row, int first) {
+  float acc = 0.f;
+#pragma unroll
+  for (int c = 0; c < COLS; c += 8) {
+    const int col = first + c;
+    const int at = (col >> 6) * kPanel + row * 128 + ((((col & 63) >> 3) ^ (row & 7)) << 4);
+    const uint4 a = *reinterpret_cast<const uint4*>(x + at), b = *reinterpret_cast<const uint4*>(y + at);
+    const uint32_t aa[4] = {a.x, a.y, a.z, a.w}, bb[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      float x0, x1, y0, y1;
+      unpack_bf16x2(aa[q], x0, x1);
+      unpack_bf16x2(bb[q], y0, y1);
+      acc = fmaf(x0, y0, acc);
+      acc = fmaf(x1, y1, acc);
+    }
+  }
+  return acc;
+}
+
 // Copies in flight of the TMA warp: the barriers that one was issued on, and
 // the phase that it completes.  After an abort they are waited for.
 struct Flight {
@@ -977,57 +999,6 @@ __global__ void __launch_bounds__(kFwdThreads, 1) rc_fwd_kernel(const __grid_con
 // ===========================================================================
 // Backward
 // ===========================================================================
-// D[h, t] = dC_t . C_t over head h's columns, in fp32.  A warp takes two tokens
-// and goes through their heads, 2^LG lanes a head and 16 bytes a lane and
-// tensor, with the loads of two steps in flight.
-template <int LG>
-__global__ void __launch_bounds__(256) rc_dot_kernel(const __grid_constant__ RcParams p) {
-  pdl_wait();
-  pdl_trigger();
-  constexpr int kLanes = 1 << LG, kHeads = 32 >> LG;  // lanes a head, heads a step
-  const int lane = threadIdx.x & 31, c = 8 * (lane & (kLanes - 1)), h0 = lane >> LG;
-  const int64_t t0 = 2 * (static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5));
-  for (int hb = 0; hb < p.H; hb += 2 * kHeads) {
-    uint4 a[2][2], b[2][2];  // [step][token]
-#pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      const int h = hb + s * kHeads + h0;
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        a[s][k] = b[s][k] = make_uint4(0, 0, 0, 0);
-        if (h < p.H && c < p.d && t0 + k < p.T) {
-          const int64_t col = static_cast<int64_t>(h) * p.d + c;
-          a[s][k] =
-              __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.C) + (t0 + k) * p.ld_c + col));
-          b[s][k] =
-              __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.dC) + (t0 + k) * p.ld_dc + col));
-        }
-      }
-    }
-#pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      const int h = hb + s * kHeads + h0;
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const uint32_t aa[4] = {a[s][k].x, a[s][k].y, a[s][k].z, a[s][k].w};
-        const uint32_t bb[4] = {b[s][k].x, b[s][k].y, b[s][k].z, b[s][k].w};
-        float acc = 0.f;
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          float x0, x1, y0, y1;
-          unpack_bf16x2(aa[q], x0, x1);
-          unpack_bf16x2(bb[q], y0, y1);
-          acc = fmaf(x0, y0, acc);
-          acc = fmaf(x1, y1, acc);
-        }
-#pragma unroll
-        for (int o = kLanes >> 1; o > 0; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
-        if (c == 0 && h < p.H && t0 + k < p.T) p.D[static_cast<int64_t>(h) * p.T + t0 + k] = acc;
-      }
-    }
-  }
-}
-
 // A Q tile is held from the scores to dK, longer than a dC tile: three stages
 // of it for the wide heads, where they fit (the bias's table takes their place).
 // With two the loads were late by half an iteration.
@@ -1039,7 +1010,7 @@ struct DkvShape {
   static constexpr int kSmem = (2 + kQ + kO) * kTile + kBarBytes + kVec;
   static constexpr int kvfull = 0, qfull = 1, ofull = qfull + kQ, tail = ofull + kO, qempty = tail + 1,
                        oempty = qempty + kQ, vecfull = oempty + kO, vecempty = vecfull + 2, sfull = vecempty + 2,
-                       dpfull = sfull + 1, pready = dpfull + 1, dsready = pready + 2, done = dsready + 2,
+                       dpfull = sfull + 2, pready = dpfull + 1, dsready = pready + 4, done = dsready + 2,
                        dfree = done + 1, kvempty = dfree + 1, info = kvempty + 1, free_ = info + 2,
                        drain = free_ + 2, count = drain + 2;
   static_assert(count <= kMaxBars && qempty <= 32, "barriers");
@@ -1103,6 +1074,10 @@ __global__ void __launch_bounds__(kDkvThreads, 1) rc_dkv_kernel(const __grid_con
   auto bar = [&](int i) { return bar0 + 8u * i; };
   const WaitCtx w{&hd->abort_flag, p.err, p.wait_limit_ns};
   const uint32_t tmem = uniform(hd->tmem);
+  // Heads to 64 wide leave room for a second buffer of scores: they are computed
+  // a tile ahead.
+  constexpr bool kAhead = DP == 64;
+  constexpr uint32_t kOther = 384;  // columns from one score buffer to the other
   const uint32_t tS = tmem, tP = tmem + 128, tdV = tmem + 256, tdK = tmem + 256 + DP;
   struct Work {
     int start, len, kt, kvh, i0, nq, total;
@@ -1238,7 +1213,8 @@ __global__ void __launch_bounds__(kDkvThreads, 1) rc_dkv_kernel(const __grid_con
     Ring x{0, grad ? L::kO : L::kQ, 0u}, d{0, grad ? L::kQ : L::kO, 0u};  // of the next products, of the next sum
     const uint32_t xtiles = smem_addr(grad ? sO : sQ), dtiles = smem_addr(grad ? sQ : sO);
     const int xfull = grad ? L::ofull : L::qfull, dfull = grad ? L::qfull : L::ofull;
-    const int ready = grad ? L::dsready : L::pready, out = grad ? L::dpfull : L::sfull;
+    const int out = grad ? L::dpfull : L::sfull;
+    const bool ahead = kAhead && !grad;
     uint32_t it = 0;  // sums so far
     bool ok = true, issued = false;
     for (uint32_t n = 0; ok; ++n) {
@@ -1251,33 +1227,43 @@ __global__ void __launch_bounds__(kDkvThreads, 1) rc_dkv_kernel(const __grid_con
       if (!(ok = wait_warp(bar(L::kvfull), n & 1, w))) break;
       for (int i = -1; i < k.total; ++i) {
         const bool more = i + 1 < k.total;
+        const uint32_t tXi = tX + (ahead && (it & 1) ? kOther : 0);             // of this sum (after the first)
+        const uint32_t tXn = tX + (ahead && ((it + (i >= 0)) & 1) ? kOther : 0);  // of the next products
+        auto products = [&]() {  // by the elected lane
+          mma_scores<DP>(tXn, a, xtiles + x.stage * L::kTile, ksteps);
+          mma_commit(bar(grad ? out : out + ((it + (i >= 0)) & 1)));
+          if (grad) mma_commit(bar(L::oempty + x.stage));
+          if (i + 2 == k.total) mma_commit(bar(L::kvempty));
+        };
         if (more && !(ok = wait_warp(bar(xfull + x.stage), x.phase, w))) break;
+        issued = true;
+        if (ahead && more) {
+          tc_fence_after();
+          if (elect_one()) products();
+          __syncwarp();
+        }
         if (i >= 0) {
           if (!(ok = wait_warp(bar(dfull + d.stage), d.phase, w))) break;
           // the sums of the item before have been read
           if (i == 0 && !(ok = wait_warp(bar(L::dfree), (n & 1) ^ 1, w))) break;
           // P or dS comes in two halves of the contraction (16 of every 32 queries)
-          if (!(ok = wait_warp(bar(ready), it & 1, w))) break;
+          // (P's barriers alternate: with scores a tile ahead, two tiles may be ready)
+          const int ready = grad ? L::dsready : L::pready + 2 * (it & 1);
+          const uint32_t rphase = grad ? it & 1 : (it >> 1) & 1;
+          if (!(ok = wait_warp(bar(ready), rphase, w))) break;
           tc_fence_after();
-          if (elect_one()) mma_rows<4, 0, 1>(tD, tX, dtiles + d.stage * L::kTile, idesc_out, i > 0);
+          if (elect_one()) mma_rows<4, 0, 1>(tD, tXi, dtiles + d.stage * L::kTile, idesc_out, i > 0);
           __syncwarp();
-          if (!(ok = wait_warp(bar(ready + 1), it & 1, w))) break;
+          if (!(ok = wait_warp(bar(ready + 1), rphase, w))) break;
         }
         tc_fence_after();
-        issued = true;
         if (elect_one()) {
           if (i >= 0) {
-            mma_rows<4, 1, 1>(tD, tX, dtiles + d.stage * L::kTile, idesc_out, true);
+            mma_rows<4, 1, 1>(tD, tXi, dtiles + d.stage * L::kTile, idesc_out, true);
             mma_commit(bar((grad ? L::qempty : L::oempty) + d.stage));
           }
-          if (more) {
-            mma_scores<DP>(tX, a, xtiles + x.stage * L::kTile, ksteps);
-            mma_commit(bar(out));
-            if (grad) mma_commit(bar(L::oempty + x.stage));
-            if (i + 2 == k.total) mma_commit(bar(L::kvempty));
-          } else {
-            mma_commit(bar(L::done));
-          }
+          if (!ahead && more) products();
+          if (!more) mma_commit(bar(L::done));
         }
         __syncwarp();
         if (i >= 0) {
@@ -1292,7 +1278,7 @@ __global__ void __launch_bounds__(kDkvThreads, 1) rc_dkv_kernel(const __grid_con
     const int part = warp >> 2;              // the 32 query columns of this warp
     const int key = (warp & 3) * 32 + lane;  // row of the transposed tile
     const uint32_t lb = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const uint32_t tSw = tS + lb + 32 * part, tPw = tP + lb + 32 * part;
+    const uint32_t tPw = tP + lb + 32 * part;
     const uint64_t scl2 = pack2(p.scale_log2, p.scale_log2);
     // After a failed wait an item runs on without waiting: the named barriers
     // need every warp, nothing is stored at its end, and all leave together.
@@ -1311,6 +1297,7 @@ __global__ void __launch_bounds__(kDkvThreads, 1) rc_dkv_kernel(const __grid_con
       const int kt = k.kt;
       for (int i = 0; i < k.total; ++i, ++it, q.next()) {
         const int buf = it & 1;
+        const uint32_t tSw = tS + lb + 32 * part + (kAhead && buf ? kOther : 0);
         if (BIAS && table_head != q.g) {
           // the next query head's bias; every compute warp reads the table
           table_head = q.g;
@@ -1331,7 +1318,7 @@ __global__ void __launch_bounds__(kDkvThreads, 1) rc_dkv_kernel(const __grid_con
         ok = ok && wait_warp(bar(L::vecfull + buf), (it >> 1) & 1, w);
         const float4* nl4 = reinterpret_cast<const float4*>(vec + 256 * buf + 32 * part);
         const float4* nd4 = reinterpret_cast<const float4*>(vec + 256 * buf + 128 + 32 * part);
-        ok = ok && wait_warp(bar(L::sfull), it & 1, w);
+        ok = ok && wait_warp(bar(L::sfull + buf), (it >> 1) & 1, w);
         tc_fence_after();
         uint32_t s[32];
         tmem_ld32_issue(tSw, s);
@@ -1371,7 +1358,7 @@ __global__ void __launch_bounds__(kDkvThreads, 1) rc_dkv_kernel(const __grid_con
           tmem_st_wait();
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(bar(L::pready + h));
+          if (lane == 0) mbar_arrive(bar(L::pready + 2 * buf + h));
         }
         ok = ok && wait_warp(bar(L::dpfull), it & 1, w);
         tc_fence_after();
@@ -1431,7 +1418,8 @@ __global__ void __launch_bounds__(kDkvThreads, 1) rc_dkv_kernel(const __grid_con
 }
 
 // TMEM: scores [0, 128), dP and then dS [128, 256), dQ [256, 384), Q [384, 448)
-// and dC [448, 512).  Q and dC stay there for the whole row of key tiles: the
+// and dC [448, 512); heads to 64 wide: a second dP [256, 384), dQ [384, 448),
+// Q [448, 480), dC [480, 512), and dP is computed a tile ahead.  Q and dC stay there for the whole row of key tiles: the
 // products read K and V from shared memory alone (both operands there would
 // take all of its bandwidth), and three tiles of each fit.
 template <int DP, bool WITH_BIAS>
@@ -1439,16 +1427,17 @@ struct DqShape {
   static constexpr int kTile = DP / 64 * kPanel;
   // K and V tiles held (a V tile is read once and soon; the bias's tables take one's place)
   static constexpr int kK = DP == 128 ? 3 : 4, kV = DP == 128 && WITH_BIAS ? 2 : kK;
-  static constexpr int kSmem = (kK + kV) * kTile + kBarBytes + 1024;
+  static constexpr int kDot = 4 * 128 * 4;  // partial sums of D
+  static constexpr int kSmem = (kK + kV) * kTile + kBarBytes + kDot + 1024;
   static constexpr int qfull = 0, kfull = 1, vfull = kfull + kK, tail = vfull + kV, kempty = tail + 1,
                        vempty = kempty + kK, sfull = vempty + kV, sread = sfull + 1, dpfull = sread + 1,
-                       dsready = dpfull + 1, done = dsready + 2, info = done + 1, tabfull = info + 2,
+                       dsready = dpfull + 2, done = dsready + 4, info = done + 1, tabfull = info + 2,
                        free_ = tabfull + 2, drain = free_ + 2, count = drain + 1;
   static_assert(count <= kMaxBars && kempty <= 32, "barriers");
   template <bool BIAS>
   static uint32_t __device__ __forceinline__ arrivals(int i) {
     if (i >= free_ && i < drain) return kBwdWarps + 1 + (BIAS ? 1 : 0);
-    return i == dsready || i == dsready + 1 || i == sread || i == qfull ? kBwdWarps : 1u;
+    return (i >= dsready && i < done) || i == sread || i == qfull ? kBwdWarps : 1u;
   }
 };
 // What the TMA warp tells the other warps of an item (two slots).
@@ -1475,7 +1464,8 @@ __global__ void __launch_bounds__(kDqThreads, 1) rc_dq_kernel(const __grid_const
   Head* hd = reinterpret_cast<Head*>(sV + L::kV * L::kTile);
   volatile DqItem* items = reinterpret_cast<volatile DqItem*>(hd->items);
   const int md = BIAS ? p.bias.md : 0, tabn = BIAS ? table_floats(md) : 0;
-  float* tabs = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(hd) + kBarBytes);  // a table for each slot
+  float* dots = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(hd) + kBarBytes);  // [4][128]
+  float* tabs = dots + 512;                                         // a table for each slot
   float* vals = tabs + 2 * tabn;                                    // the head's values
   uint8_t* map = reinterpret_cast<uint8_t*>(vals + (BIAS ? kMaxRelBuckets : 0));  // the distances' buckets
   float* diag = reinterpret_cast<float*>(map + tabn);               // [kBwdWarps][kDiag]
@@ -1491,7 +1481,9 @@ __global__ void __launch_bounds__(kDqThreads, 1) rc_dq_kernel(const __grid_const
   auto bar = [&](int i) { return bar0 + 8u * i; };
   const WaitCtx w{&hd->abort_flag, p.err, p.wait_limit_ns};
   const uint32_t tmem = uniform(hd->tmem);
-  const uint32_t tP = tmem + 128, tdQ = tmem + 256, tQ = tmem + 384, tO = tmem + 448;
+  constexpr bool kAhead = DP == 64;  // dP in two buffers
+  const uint32_t tP = tmem + 128, tdQ = tmem + (kAhead ? 384 : 256), tQ = tmem + (kAhead ? 448 : 384),
+                 tO = tmem + (kAhead ? 480 : 448);
 
   if (warp == kBwdWarps + 1) {
     Flight fl;
@@ -1539,9 +1531,20 @@ __global__ void __launch_bounds__(kDqThreads, 1) rc_dq_kernel(const __grid_const
                         hq);
         }
       }
-      ok = __shfl_sync(0xffffffffu, ok, 0);
       kr.next();
       vr.next();
+      // C follows Q
+      if (lane == 0) {
+        ok = ok && wait_bounded(bar(L::kempty + kr.stage), kr.phase ^ 1u, w);
+        if (ok) {
+          mbar_arrive_expect_tx(bar(L::kfull + kr.stage), L::kTile);
+          fl.note(L::kfull + kr.stage, kr.phase);
+          load_tile<DP>(smem_addr(sK + kr.stage * L::kTile), &p.mapC, bar(L::kfull + kr.stage), u.start + 128 * u.tile,
+                        hq);
+        }
+      }
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+      kr.next();
       for (int j = 0; ok && j < nk; ++j, kr.next(), vr.next()) {
         const int st = kr.stage, sv = vr.stage;
         const uint32_t ph = kr.phase;
@@ -1604,6 +1607,12 @@ __global__ void __launch_bounds__(kDqThreads, 1) rc_dq_kernel(const __grid_const
       kr.next();
       ++ns;
     };
+    uint32_t np0 = 0;  // tiles of the items before
+    auto dprobs = [&](int j) {  // by the elected lane
+      mma_scores_ts<DP>(tP + (kAhead && ((np0 + j) & 1) ? 128 : 0), tO, smem_addr(sV + vr.stage * L::kTile), ksteps);
+      mma_commit(bar(L::dpfull + ((np0 + j) & 1)));
+      mma_commit(bar(L::vempty + vr.stage));
+    };
     for (uint32_t n = 0; ok; ++n) {
       const int slot = n & 1;
       if (!(ok = wait_warp(bar(L::info + slot), (n >> 1) & 1, w))) break;
@@ -1612,43 +1621,50 @@ __global__ void __launch_bounds__(kDqThreads, 1) rc_dq_kernel(const __grid_const
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(L::free_ + slot));
       if (end) break;
-      // Q and dC are in TMEM: their stages are free again
+      // Q and dC are in TMEM: Q's stage is free again
       if (!(ok = wait_warp(bar(L::qfull), n & 1, w))) break;
-      if (lane == 0) {
-        mbar_arrive(bar(L::kempty + kr.stage));
-        mbar_arrive(bar(L::vempty + vr.stage));
-      }
+      if (lane == 0) mbar_arrive(bar(L::kempty + kr.stage));
       __syncwarp();
       kr.next();
+      kr.next();  // C's; the compute warps release it and dC's
       vr.next();
+      dr.next();
       dr.next();
       if (!(ok = wait_warp(bar(L::kfull + kr.stage), kr.phase, w))) break;
       issued = true;
       scores();
+      if (kAhead) {
+        if (!(ok = wait_warp(bar(L::vfull + vr.stage), vr.phase, w))) break;
+        tc_fence_after();
+        if (elect_one()) dprobs(0);
+        __syncwarp();
+        vr.next();
+      }
       for (int j = -1; j < nk; ++j) {
-        const bool more = j + 1 < nk;
+        // the next dP: of tile j + 1 in place of tile j's dS, or (two buffers) of
+        // tile j + 2
+        const int jn = j + (kAhead ? 2 : 1);
+        const bool more = jn < nk;
+        const uint32_t tPj = tP + (kAhead && (nd & 1) ? 128 : 0);
         if (more && !(ok = wait_warp(bar(L::vfull + vr.stage), vr.phase, w))) break;
         if (j >= 0) {
-          // dS comes in two halves of the contraction (16 of every 32 keys)
-          if (!(ok = wait_warp(bar(L::dsready), nd & 1, w))) break;
+          // dS comes in two halves of the contraction (16 of every 32 keys); its
+          // barriers alternate: with dP a tile ahead, two tiles may be ready
+          const int ready = L::dsready + 2 * (nd & 1);
+          if (!(ok = wait_warp(bar(ready), (nd >> 1) & 1, w))) break;
           tc_fence_after();
-          if (elect_one()) mma_rows<4, 0, 1>(tdQ, tP, smem_addr(sK + dr.stage * L::kTile), idesc_out, j > 0);
+          if (elect_one()) mma_rows<4, 0, 1>(tdQ, tPj, smem_addr(sK + dr.stage * L::kTile), idesc_out, j > 0);
           __syncwarp();
-          if (!(ok = wait_warp(bar(L::dsready + 1), nd & 1, w))) break;
+          if (!(ok = wait_warp(bar(ready + 1), (nd >> 1) & 1, w))) break;
         }
         tc_fence_after();
         if (elect_one()) {
           if (j >= 0) {
-            mma_rows<4, 1, 1>(tdQ, tP, smem_addr(sK + dr.stage * L::kTile), idesc_out, true);
+            mma_rows<4, 1, 1>(tdQ, tPj, smem_addr(sK + dr.stage * L::kTile), idesc_out, true);
             mma_commit(bar(L::kempty + dr.stage));
           }
-          if (more) {
-            mma_scores_ts<DP>(tP, tO, smem_addr(sV + vr.stage * L::kTile), ksteps);
-            mma_commit(bar(L::dpfull));
-            mma_commit(bar(L::vempty + vr.stage));
-          } else {
-            mma_commit(bar(L::done));
-          }
+          if (more) dprobs(jn);
+          if (j + 1 >= nk) mma_commit(bar(L::done));
         }
         __syncwarp();
         if (j >= 0) {
@@ -1662,6 +1678,7 @@ __global__ void __launch_bounds__(kDqThreads, 1) rc_dq_kernel(const __grid_const
           scores();
         }
       }
+      np0 += nk;
     }
     if (*w.abort_flag && issued && elect_one()) drain_mma(bar(L::drain), p.wait_limit_ns);
   } else if (warp < kBwdWarps) {
@@ -1670,7 +1687,7 @@ __global__ void __launch_bounds__(kDqThreads, 1) rc_dq_kernel(const __grid_const
     const uint32_t lb = static_cast<uint32_t>(quarter * 32) << 16;
     const uint64_t scl2 = pack2(p.scale_log2, p.scale_log2);
     uint32_t nt = 0;  // tiles so far
-    uint32_t kc = 0;  // ring tiles so far (K's and V's go together)
+    uint32_t kc = 0, vc = 0;  // ring tiles so far
     // the columns of the output in 32s over the warps of a row; an item's are
     // stored when the next one's Q and dC are in place
     const int ofirst = 32 * part, ocols = min(p.d - ofirst, 32);
@@ -1701,15 +1718,13 @@ __global__ void __launch_bounds__(kDqThreads, 1) rc_dq_kernel(const __grid_const
       if (mine) {
         const int64_t at = static_cast<int64_t>(head) * p.T + start + row;
         nl = -p.lse[at] * kLog2e;
-        nd = -p.D[at];
       }
-      const uint64_t nd2 = pack2(nd, nd);
       // this warp's quarter of the columns of Q and dC into TMEM; the item before
       // has been through its products
       {
-        const int sk = kc % L::kK, sv = kc % L::kV;
+        const int sk = kc % L::kK, sv = vc % L::kV;
         ok = ok && wait_warp(bar(L::kfull + sk), (kc / L::kK) & 1, w) &&
-             wait_warp(bar(L::vfull + sv), (kc / L::kV) & 1, w);
+             wait_warp(bar(L::vfull + sv), (vc / L::kV) & 1, w);
         tile_to_tmem<DP / 4>(tQ + lb + DP / 8 * part, sK + sk * L::kTile, quarter * 32 + lane, DP / 4 * part);
         tile_to_tmem<DP / 4>(tO + lb + DP / 8 * part, sV + sv * L::kTile, quarter * 32 + lane, DP / 4 * part);
       }
@@ -1717,13 +1732,30 @@ __global__ void __launch_bounds__(kDqThreads, 1) rc_dq_kernel(const __grid_const
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(L::qfull));
-      kc += nk + 1;
+      // D of the rows: each warp its quarter of the columns, then the four sums
+      {
+        const int sc = (kc + 1) % L::kK, sv = vc % L::kV, r = quarter * 32 + lane;
+        ok = ok && wait_warp(bar(L::kfull + sc), ((kc + 1) / L::kK) & 1, w);
+        dots[128 * part + r] = dot_tiles<DP / 4>(sK + sc * L::kTile, sV + sv * L::kTile, r, DP / 4 * part);
+        named_bar(1, 32 * kBwdWarps);
+        if (threadIdx.x == 0) {
+          mbar_arrive(bar(L::kempty + sc));
+          mbar_arrive(bar(L::vempty + sv));
+        }
+        const float D = (dots[r] + dots[128 + r]) + (dots[256 + r] + dots[384 + r]);
+        if (part == 0 && mine) p.D[static_cast<int64_t>(head) * p.T + start + row] = D;
+        nd = -D;
+      }
+      const uint64_t nd2 = pack2(nd, nd);
+      kc += nk + 2;
+      vc += nk + 1;
       // the item before's output, while the first products of this one run
       put();
       if (BIAS) ok = ok && wait_warp(bar(L::tabfull + slot), (n >> 1) & 1, w);
       float end_lo = 0.f, end_hi = 0.f;  // dS at distances <= -md and >= md
       for (int j = 0; j < nk; ++j, ++nt) {
         const int c0 = 128 * j + 32 * part;  // key position of this warp's first column
+        const uint32_t tPj = tP + lb + 32 * part + (kAhead && (nt & 1) ? 128 : 0);
         int side = 0;
         float off = nl;
         const float* tb = nullptr;
@@ -1753,10 +1785,10 @@ __global__ void __launch_bounds__(kDqThreads, 1) rc_dq_kernel(const __grid_const
           s[c + 1] = __float_as_uint(ex2_ftz(x1));
         }
         const bool masked = (p.causal && 128 * j + 127 > r0) || 128 * j + 128 > len;
-        ok = ok && wait_warp(bar(L::dpfull), nt & 1, w);
+        ok = ok && wait_warp(bar(L::dpfull + (nt & 1)), (nt >> 1) & 1, w);
         tc_fence_after();
         uint32_t g[32];
-        tmem_ld32_issue(tP + lb + 32 * part, g);
+        tmem_ld32_issue(tPj, g);
         tmem_ld32_wait(g);
         const int seen = (p.causal ? min(len, row + 1) : len) - c0;
 #pragma unroll
@@ -1775,11 +1807,11 @@ __global__ void __launch_bounds__(kDqThreads, 1) rc_dq_kernel(const __grid_const
           }
 #pragma unroll
           for (int c = 0; c < 8; ++c) pk[c] = pack_bf16x2(as_f(s[16 * h + 2 * c]), as_f(s[16 * h + 2 * c + 1]));
-          tmem_st8(tP + lb + 32 * part + 8 * h, pk);
+          tmem_st8(tPj + 8 * h, pk);
           tmem_st_wait();
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(bar(L::dsready + h));
+          if (lane == 0) mbar_arrive(bar(L::dsready + 2 * (nt & 1) + h));
         }
         if (BIAS && grad) {
           if (side != 0) {
@@ -1928,18 +1960,20 @@ cudaError_t bwd_t(RcParams& p, int num_sms, cudaStream_t st) {
   const int64_t units = units_of(p, 128);
   const int n = BIAS ? table_floats(p.bias.md) : 0;
   p.wide = wide_rows(p, p.dQKV, p.ld_dqkv, p.shard_w);
+  // dQ first: it leaves D for dK and dV
+  p.items = units * p.H;
+  p.slot = static_cast<int>(g_rc_slot_seq.fetch_add(1) % kRcSlots);
+  // (two tables of floats, a head's values, a byte a distance, the sums)
+  cudaError_t e =
+      launch_rc(rc_dq_kernel<DP, BIAS>, p.items < num_sms ? p.items : num_sms, kDqThreads,
+                (DqShape<DP, BIAS>::kSmem) + 9 * n + (BIAS ? 4 * (kMaxRelBuckets + grad_floats(p.bias.md)) : 0), p, st);
+  p.fault_skip = 0;
+  if (e != cudaSuccess) return e;
   p.items = units * p.KV;
   p.slot = static_cast<int>(g_rc_slot_seq.fetch_add(1) % kRcSlots);
   // (a table of floats and a byte a distance)
-  cudaError_t e = launch_rc(rc_dkv_kernel<DP, BIAS>, p.items < num_sms ? p.items : num_sms, kDkvThreads,
-                            (DkvShape<DP, BIAS>::kSmem) + 5 * n, p, st);
-  p.fault_skip = 0;
-  if (e != cudaSuccess) return e;
-  p.items = units * p.H;
-  p.slot = static_cast<int>(g_rc_slot_seq.fetch_add(1) % kRcSlots);
-  // (two tables, a head's values, a byte a distance, the sums)
-  e = launch_rc(rc_dq_kernel<DP, BIAS>, p.items < num_sms ? p.items : num_sms, kDqThreads,
-                (DqShape<DP, BIAS>::kSmem) + 9 * n + (BIAS ? 4 * (kMaxRelBuckets + grad_floats(p.bias.md)) : 0), p, st);
+  e = launch_rc(rc_dkv_kernel<DP, BIAS>, p.items < num_sms ? p.items : num_sms, kDkvThreads,
+                (DkvShape<DP, BIAS>::kSmem) + 5 * n, p, st);
   if (e != cudaSuccess || !BIAS || p.partial == nullptr) return e;
   launch_k(rc_bias_sum_kernel, dim3(p.H, p.bias.nb), dim3(128), 0, st, p, units);
   count_launches(1);
@@ -1959,19 +1993,6 @@ cudaError_t launch_rc_fwd(RcParams& p, int num_sms, cudaStream_t st) {
 }
 
 cudaError_t launch_rc_bwd(RcParams& p, int num_sms, cudaStream_t st) {
-  int lg = 0;
-  while (8 << lg < p.d) ++lg;
-  const dim3 grid(static_cast<unsigned>((p.T + 15) / 16));
-  switch (lg) {
-    case 0: launch_k(rc_dot_kernel<0>, grid, dim3(256), 0, st, p); break;
-    case 1: launch_k(rc_dot_kernel<1>, grid, dim3(256), 0, st, p); break;
-    case 2: launch_k(rc_dot_kernel<2>, grid, dim3(256), 0, st, p); break;
-    case 3: launch_k(rc_dot_kernel<3>, grid, dim3(256), 0, st, p); break;
-    default: launch_k(rc_dot_kernel<4>, grid, dim3(256), 0, st, p); break;
-  }
-  count_launches(1);
-  const cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
   if (p.d <= 64) return p.bias.nb ? bwd_t<64, true>(p, num_sms, st) : bwd_t<64, false>(p, num_sms, st);
   return p.bias.nb ? bwd_t<128, true>(p, num_sms, st) : bwd_t<128, false>(p, num_sms, st);
 }

@@ -196,9 +196,9 @@ struct RcBias {
   int first[kMaxRelBuckets];  // smallest distance of a side's bucket k
 };
 struct RcParams {
-  CUtensorMap mapQ, mapK, mapV, mapO;  // 4D (d, token, head of the shard, shard); mapO: dC
+  CUtensorMap mapQ, mapK, mapV, mapO, mapC;  // 4D (d, token, head of the shard, shard); mapO: dC
   const int64_t* seq_starts;           // device, b + 1 values, or null: b sequences of s tokens
-  int64_t T, ld_qkv, ld_c, ld_dc, ld_dqkv;
+  int64_t T, ld_c, ld_dqkv;
   int b, s, H, KV, d, causal;
   int group;    // query heads a K/V head
   int hq, hk;   // query and K/V heads a shard
@@ -208,10 +208,8 @@ struct RcParams {
   int wide;     // output rows allow 32-byte stores (set by the launcher)
   int64_t items;  // of the launch, those without rows among them (set by the launcher)
   float scale, scale_log2;
-  const void* QKV;
   void* C;          // forward out, backward in
   float* lse;       // forward out, backward in; (H, T)
-  const void* dC;
   float* D;         // (H, T) scratch
   void* dQKV;
   RcBias bias;
