@@ -1329,24 +1329,35 @@ __global__ void __launch_bounds__(kDkvThreads, 1) rc_dkv_kernel(const __grid_con
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           uint32_t pk[8];
+          if (BIAS && near) {
 #pragma unroll
-          for (int c = 16 * h; c < 16 * h + 16; c += 4) {
-            const float4 n = nl4[c >> 2];
-            uint64_t o0 = pack2(n.x, n.y), o1 = pack2(n.z, n.w);
-            if (BIAS) {
-              if (near) {
-                o0 = add2(o0, pack2(tb[-c], tb[-c - 1]));
-                o1 = add2(o1, pack2(tb[-c - 2], tb[-c - 3]));
-              } else {
+            for (int c = 16 * h; c < 16 * h + 16; c += 4) {
+              const float4 n = nl4[c >> 2];
+              float x[4];
+              unpack2(fma2(pack2(as_f(s[c]), as_f(s[c + 1])), scl2,
+                           add2(pack2(n.x, n.y), pack2(tb[-c], tb[-c - 1]))),
+                      x[0], x[1]);
+              unpack2(fma2(pack2(as_f(s[c + 2]), as_f(s[c + 3])), scl2,
+                           add2(pack2(n.z, n.w), pack2(tb[-c - 2], tb[-c - 3]))),
+                      x[2], x[3]);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) s[c + e] = __float_as_uint(ex2_ftz(x[e]));
+            }
+          } else {
+#pragma unroll
+            for (int c = 16 * h; c < 16 * h + 16; c += 4) {
+              const float4 n = nl4[c >> 2];
+              uint64_t o0 = pack2(n.x, n.y), o1 = pack2(n.z, n.w);
+              if (BIAS) {
                 o0 = add2(o0, add2v);
                 o1 = add2(o1, add2v);
               }
-            }
-            float x[4];
-            unpack2(fma2(pack2(as_f(s[c]), as_f(s[c + 1])), scl2, o0), x[0], x[1]);
-            unpack2(fma2(pack2(as_f(s[c + 2]), as_f(s[c + 3])), scl2, o1), x[2], x[3]);
+              float x[4];
+              unpack2(fma2(pack2(as_f(s[c]), as_f(s[c + 1])), scl2, o0), x[0], x[1]);
+              unpack2(fma2(pack2(as_f(s[c + 2]), as_f(s[c + 3])), scl2, o1), x[2], x[3]);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) s[c + e] = __float_as_uint(ex2_ftz(x[e]));
+              for (int e = 0; e < 4; ++e) s[c + e] = __float_as_uint(ex2_ftz(x[e]));
+            }
           }
           if (diagonal) {
 #pragma unroll
@@ -1773,16 +1784,22 @@ __global__ void __launch_bounds__(kDqThreads, 1) rc_dq_kernel(const __grid_const
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(L::sread));
+        if (BIAS && side == 0) {
 #pragma unroll
-        for (int c = 0; c < 32; c += 2) {
-          uint64_t o = off2;
-          if (BIAS) {
-            if (side == 0) o = add2(o, pack2(tb[c], tb[c + 1]));
+          for (int c = 0; c < 32; c += 2) {
+            float x0, x1;
+            unpack2(fma2(pack2(as_f(s[c]), as_f(s[c + 1])), scl2, add2(off2, pack2(tb[c], tb[c + 1]))), x0, x1);
+            s[c] = __float_as_uint(ex2_ftz(x0));
+            s[c + 1] = __float_as_uint(ex2_ftz(x1));
           }
-          float x0, x1;
-          unpack2(fma2(pack2(as_f(s[c]), as_f(s[c + 1])), scl2, o), x0, x1);
-          s[c] = __float_as_uint(ex2_ftz(x0));
-          s[c + 1] = __float_as_uint(ex2_ftz(x1));
+        } else {
+#pragma unroll
+          for (int c = 0; c < 32; c += 2) {
+            float x0, x1;
+            unpack2(fma2(pack2(as_f(s[c]), as_f(s[c + 1])), scl2, off2), x0, x1);
+            s[c] = __float_as_uint(ex2_ftz(x0));
+            s[c + 1] = __float_as_uint(ex2_ftz(x1));
+          }
         }
         const bool masked = (p.causal && 128 * j + 127 > r0) || 128 * j + 128 > len;
         ok = ok && wait_warp(bar(L::dpfull + (nt & 1)), (nt >> 1) & 1, w);
