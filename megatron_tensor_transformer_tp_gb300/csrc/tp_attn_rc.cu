@@ -1009,7 +1009,7 @@ struct DkvShape {
   static constexpr int kVec = 2 * 2 * 128 * 4;  // (-lse log2 e, -D) of two query tiles
   static constexpr int kSmem = (2 + kQ + kO) * kTile + kBarBytes + kVec;
   static constexpr int kvfull = 0, qfull = 1, ofull = qfull + kQ, tail = ofull + kO, qempty = tail + 1,
-                       oempty = qempty + kQ, vecfull = oempty + kO, vecempty = vecfull + 2, sfull = vecempty + 2,
+                       oempty = qempty + kQ, vecempty = oempty + kO, sfull = vecempty + 2,
                        dpfull = sfull + 2, pready = dpfull + 1, dsready = pready + 4, done = dsready + 2,
                        dfree = done + 1, kvempty = dfree + 1, info = kvempty + 1, free_ = info + 2,
                        drain = free_ + 2, count = drain + 2;
@@ -1017,7 +1017,7 @@ struct DkvShape {
   static uint32_t __device__ __forceinline__ arrivals(int i) {
     if ((i >= pready && i < done) || i == vecempty || i == vecempty + 1 || i == dfree) return kBwdWarps;
     if (i >= free_ && i < drain) return kBwdWarps + 3;
-    return i == done || i == kvempty || (i >= oempty && i < vecfull) ? 2u : 1u;
+    return i == done || i == kvempty || (i >= oempty && i < vecempty) || i == sfull || i == sfull + 1 ? 2u : 1u;
   }
 };
 
@@ -1199,7 +1199,7 @@ __global__ void __launch_bounds__(kDkvThreads, 1) rc_dkv_kernel(const __grid_con
           vec[256 * buf + 128 + 32 * x + lane] = nd[x];
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar(L::vecfull + buf));
+        if (lane == 0) mbar_arrive(bar(L::sfull + buf));  // with the scores
       }
     }
   } else if (warp == kBwdWarps || warp == kBwdWarps + 1) {
@@ -1315,7 +1315,6 @@ __global__ void __launch_bounds__(kDkvThreads, 1) rc_dkv_kernel(const __grid_con
           // distance of column c: key - query = (128 kt + key) - (128 i + 32 part + c)
           tb = tab + (128 * (kt - q.i) + key - 32 * part + p.bias.md + kPad);
         }
-        ok = ok && wait_warp(bar(L::vecfull + buf), (it >> 1) & 1, w);
         const float4* nl4 = reinterpret_cast<const float4*>(vec + 256 * buf + 32 * part);
         const float4* nd4 = reinterpret_cast<const float4*>(vec + 256 * buf + 128 + 32 * part);
         ok = ok && wait_warp(bar(L::sfull + buf), (it >> 1) & 1, w);
@@ -1442,7 +1441,7 @@ struct DqShape {
   static constexpr int kSmem = (kK + kV) * kTile + kBarBytes + kDot + 1024;
   static constexpr int qfull = 0, kfull = 1, vfull = kfull + kK, tail = vfull + kV, kempty = tail + 1,
                        vempty = kempty + kK, sfull = vempty + kV, sread = sfull + 1, dpfull = sread + 1,
-                       dsready = dpfull + 2, done = dsready + 4, info = done + 1, tabfull = info + 2,
+                       dsready = dpfull + 1, done = dsready + 4, info = done + 1, tabfull = info + 2,
                        free_ = tabfull + 2, drain = free_ + 2, count = drain + 1;
   static_assert(count <= kMaxBars && kempty <= 32, "barriers");
   template <bool BIAS>
@@ -1621,7 +1620,8 @@ __global__ void __launch_bounds__(kDqThreads, 1) rc_dq_kernel(const __grid_const
     uint32_t np0 = 0;  // tiles of the items before
     auto dprobs = [&](int j) {  // by the elected lane
       mma_scores_ts<DP>(tP + (kAhead && ((np0 + j) & 1) ? 128 : 0), tO, smem_addr(sV + vr.stage * L::kTile), ksteps);
-      mma_commit(bar(L::dpfull + ((np0 + j) & 1)));
+      // (a tile ahead, dP is issued before the scores of its tile, whose commit covers it)
+      if (!kAhead) mma_commit(bar(L::dpfull));
       mma_commit(bar(L::vempty + vr.stage));
     };
     for (uint32_t n = 0; ok; ++n) {
@@ -1643,7 +1643,6 @@ __global__ void __launch_bounds__(kDqThreads, 1) rc_dq_kernel(const __grid_const
       dr.next();
       if (!(ok = wait_warp(bar(L::kfull + kr.stage), kr.phase, w))) break;
       issued = true;
-      scores();
       if (kAhead) {
         if (!(ok = wait_warp(bar(L::vfull + vr.stage), vr.phase, w))) break;
         tc_fence_after();
@@ -1651,6 +1650,7 @@ __global__ void __launch_bounds__(kDqThreads, 1) rc_dq_kernel(const __grid_const
         __syncwarp();
         vr.next();
       }
+      scores();
       for (int j = -1; j < nk; ++j) {
         // the next dP: of tile j + 1 in place of tile j's dS, or (two buffers) of
         // tile j + 2
@@ -1763,7 +1763,8 @@ __global__ void __launch_bounds__(kDqThreads, 1) rc_dq_kernel(const __grid_const
       // the item before's output, while the first products of this one run
       put();
       if (BIAS) ok = ok && wait_warp(bar(L::tabfull + slot), (n >> 1) & 1, w);
-      float end_lo = 0.f, end_hi = 0.f;  // dS at distances <= -md and >= md
+      float end_lo = 0.f, end_hi = 0.f;  // dS at distances <= -md and >= md, of the tile sums
+      uint64_t far_lo = 0, far_hi = 0;   // and of this row in tiles all beyond an end
       for (int j = 0; j < nk; ++j, ++nt) {
         const int c0 = 128 * j + 32 * part;  // key position of this warp's first column
         const uint32_t tPj = tP + lb + 32 * part + (kAhead && (nt & 1) ? 128 : 0);
@@ -1802,12 +1803,15 @@ __global__ void __launch_bounds__(kDqThreads, 1) rc_dq_kernel(const __grid_const
           }
         }
         const bool masked = (p.causal && 128 * j + 127 > r0) || 128 * j + 128 > len;
-        ok = ok && wait_warp(bar(L::dpfull + (nt & 1)), (nt >> 1) & 1, w);
-        tc_fence_after();
+        if (!kAhead) {
+          ok = ok && wait_warp(bar(L::dpfull), nt & 1, w);
+          tc_fence_after();
+        }
         uint32_t g[32];
         tmem_ld32_issue(tPj, g);
         tmem_ld32_wait(g);
         const int seen = (p.causal ? min(len, row + 1) : len) - c0;
+        uint64_t rowsum = 0;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           uint32_t pk[8];
@@ -1822,6 +1826,11 @@ __global__ void __launch_bounds__(kDqThreads, 1) rc_dq_kernel(const __grid_const
 #pragma unroll
             for (int c = 16 * h; c < 16 * h + 16; ++c) s[c] = c < seen ? s[c] : 0u;
           }
+          if (BIAS && side != 0) {
+#pragma unroll
+            for (int c = 16 * h; c < 16 * h + 16; c += 2)
+              rowsum = add2(rowsum, pack2(as_f(s[c]), as_f(s[c + 1])));
+          }
 #pragma unroll
           for (int c = 0; c < 8; ++c) pk[c] = pack_bf16x2(as_f(s[16 * h + 2 * c]), as_f(s[16 * h + 2 * c + 1]));
           tmem_st8(tPj + 8 * h, pk);
@@ -1831,13 +1840,10 @@ __global__ void __launch_bounds__(kDqThreads, 1) rc_dq_kernel(const __grid_const
           if (lane == 0) mbar_arrive(bar(L::dsready + 2 * (nt & 1) + h));
         }
         if (BIAS && grad) {
-          if (side != 0) {
-            float a[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int c = 0; c < 32; ++c) a[c & 3] += as_f(s[c]);
-            const float sum = mine ? (a[0] + a[1]) + (a[2] + a[3]) : 0.f;
-            if (side < 0) end_lo += sum;
-            else end_hi += sum;
+          if (side < 0) {
+            far_lo = add2(far_lo, rowsum);
+          } else if (side > 0) {
+            far_hi = add2(far_hi, rowsum);
           } else {
             // Sums along the diagonals of the warp's 32 x 32 block: the running
             // sum of a diagonal moves one lane up at every column; it is whole
@@ -1886,8 +1892,11 @@ __global__ void __launch_bounds__(kDqThreads, 1) rc_dq_kernel(const __grid_const
       if (BIAS && grad) {
         // the item's sums by bucket, in a fixed order
         constexpr int kN = 32 * kBwdWarps;
-        ends[threadIdx.x] = end_lo;
-        ends[kN + threadIdx.x] = end_hi;
+        float a0, a1, b0, b1;
+        unpack2(far_lo, a0, a1);
+        unpack2(far_hi, b0, b1);
+        ends[threadIdx.x] = end_lo + (mine ? a0 + a1 : 0.f);
+        ends[kN + threadIdx.x] = end_hi + (mine ? b0 + b1 : 0.f);
         named_bar(1, kN);
         if (warp < 2) {
           float a = 0.f;
