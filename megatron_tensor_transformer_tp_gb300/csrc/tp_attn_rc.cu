@@ -212,60 +212,122 @@ __device__ __forceinline__ bool named_bar_any(int id, int threads, bool yes) {
 // ---------------------------------------------------------------------------
 // Work items
 // ---------------------------------------------------------------------------
-// Unit `unit` of the launch: a run of `rows` tokens of a sequence.  Called by
-// a whole warp; false if there is no such unit.  Sequences given by
-// seq_starts are clamped into [0, T]; starts that decrease or leave [0, T] are
-// reported in the error word by the first block.
+// Unit `unit` of the launch: a run of `rows` tokens of a sequence.  Units are
+// taken so that long contractions come early: by rank, the first (or, where
+// `last_first`, the last) runs of all sequences, then their second ones and so
+// on.  Sequences given by seq_starts are clamped into [0, T]; starts that
+// decrease or leave [0, T] are reported in the error word by the first block.
+// Called by a whole warp.
 struct Unit {
   int start, len, tile;  // first token and length of the sequence, tile inside it
 };
-__device__ __forceinline__ bool find_unit(const RcParams& p, int64_t unit, int rows, bool last_first, bool report,
-                                          int lane, Unit& u) {
-  if (p.seq_starts == nullptr) {
-    // the longest contractions first, across the sequences
-    const int per = (p.s + rows - 1) / rows;
-    const int rank = static_cast<int>(unit / p.b), seq = static_cast<int>(unit % p.b);
-    if (rank >= per) return false;
-    u.tile = last_first ? per - 1 - rank : rank;
-    u.start = seq * p.s;
-    u.len = p.s;
-    return true;
+constexpr int kSeqRegs = 4;  // up to 32 kSeqRegs sequences are held by a warp, more go in their own order
+struct Units {
+  int start[kSeqRegs], len[kSeqRegs], n[kSeqRegs];  // of sequences lane + 32 k
+  int rows, top;                                    // the longest sequence's runs
+  bool held;
+
+  __device__ __forceinline__ static bool read(const RcParams& p, int i, int64_t& a, int64_t& e) {
+    a = e = 0;
+    if (i >= p.b) return true;
+    a = p.seq_starts[i];
+    e = p.seq_starts[i + 1];
+    const bool fine = a >= 0 && e >= a && e <= p.T;
+    a = min(max(a, static_cast<int64_t>(0)), p.T);
+    e = min(max(e, a), p.T);
+    return fine;
   }
-  int64_t base = 0;
-  bool found = false, bad = false;
-  for (int i0 = 0; i0 < p.b; i0 += 32) {
-    const int i = i0 + lane;
-    int64_t a = 0, e = 0;
-    if (i < p.b) {
-      a = p.seq_starts[i];
-      e = p.seq_starts[i + 1];
-      bad |= a < 0 || e < a || e > p.T;
-      a = min(max(a, static_cast<int64_t>(0)), p.T);
-      e = min(max(e, a), p.T);
-    }
-    const int n = static_cast<int>((e - a + rows - 1) / rows);
-    int64_t incl = n;
+  __device__ __forceinline__ Units(const RcParams& p, int rows_, int lane) : rows(rows_), top(0), held(false) {
+    if (p.seq_starts == nullptr) return;
+    bool fine = true;
+    held = p.b <= 32 * kSeqRegs;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += v;
+    for (int k = 0; k < kSeqRegs; ++k) {
+      int64_t a, e;
+      fine &= read(p, held ? lane + 32 * k : p.b, a, e);
+      start[k] = static_cast<int>(a);
+      len[k] = static_cast<int>(e - a);
+      n[k] = (len[k] + rows - 1) / rows;
+      top = max(top, n[k]);
     }
-    const unsigned hit = __ballot_sync(0xffffffffu, base + incl > unit);
-    if (!found && hit) {
-      const int src = __ffs(hit) - 1;
-      u.start = static_cast<int>(__shfl_sync(0xffffffffu, a, src));
-      u.len = static_cast<int>(__shfl_sync(0xffffffffu, e - a, src));
-      const int tiles = __shfl_sync(0xffffffffu, n, src);
-      const int t = static_cast<int>(unit - __shfl_sync(0xffffffffu, base + incl - n, src));
-      u.tile = last_first ? tiles - 1 - t : t;
-      found = true;
-      if (!report) break;  // warp-uniform
-    }
-    base += __shfl_sync(0xffffffffu, incl, 31);
+    top = __reduce_max_sync(0xffffffffu, top);
+    if (!held && blockIdx.x == 0)
+      for (int i = lane; i < p.b; i += 32) {
+        int64_t a, e;
+        fine &= read(p, i, a, e);
+      }
+    if (!fine && blockIdx.x == 0) atomicOr(p.err, kErrInvalid);
   }
-  if (report && bad) atomicOr(p.err, kErrInvalid);
-  return found;
-}
+  // Units of rank below r.
+  __device__ __forceinline__ int64_t below(int r) const {
+    int c = 0;
+#pragma unroll
+    for (int k = 0; k < kSeqRegs; ++k) c += min(n[k], r);
+    return __reduce_add_sync(0xffffffffu, c);
+  }
+  // false: there is no such unit
+  __device__ __forceinline__ bool find(const RcParams& p, int64_t unit, bool last_first, int lane, Unit& u) const {
+    if (p.seq_starts == nullptr) {
+      const int per = (p.s + rows - 1) / rows;
+      const int rank = static_cast<int>(unit / p.b), seq = static_cast<int>(unit % p.b);
+      if (rank >= per) return false;
+      u.tile = last_first ? per - 1 - rank : rank;
+      u.start = seq * p.s;
+      u.len = p.s;
+      return true;
+    }
+    if (held) {
+      if (unit >= below(top)) return false;
+      int lo = 0, hi = top - 1;  // the rank: the largest r with below(r) <= unit
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (below(mid) <= unit) lo = mid;
+        else hi = mid - 1;
+      }
+      int k = static_cast<int>(unit - below(lo));  // among the sequences that have this rank, in order
+      bool done = false;
+#pragma unroll
+      for (int g = 0; g < kSeqRegs; ++g) {
+        const unsigned has = __ballot_sync(0xffffffffu, n[g] > lo);
+        const int c = __popc(has);
+        if (!done && k < c) {
+          const int src = __fns(has, 0, k + 1);
+          u.start = __shfl_sync(0xffffffffu, start[g], src);
+          u.len = __shfl_sync(0xffffffffu, len[g], src);
+          const int runs = __shfl_sync(0xffffffffu, n[g], src);
+          u.tile = last_first ? runs - 1 - lo : lo;
+          done = true;
+        }
+        k -= c;
+      }
+      return true;
+    }
+    int64_t base = 0;
+    for (int i0 = 0; i0 < p.b; i0 += 32) {
+      int64_t a, e;
+      read(p, i0 + lane, a, e);
+      const int runs = static_cast<int>((e - a + rows - 1) / rows);
+      int64_t incl = runs;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += v;
+      }
+      const unsigned hit = __ballot_sync(0xffffffffu, base + incl > unit);
+      if (hit) {
+        const int src = __ffs(hit) - 1;
+        u.start = static_cast<int>(__shfl_sync(0xffffffffu, a, src));
+        u.len = static_cast<int>(__shfl_sync(0xffffffffu, e - a, src));
+        const int all = __shfl_sync(0xffffffffu, runs, src);
+        const int t = static_cast<int>(unit - __shfl_sync(0xffffffffu, base + incl - runs, src));
+        u.tile = last_first ? all - 1 - t : t;
+        return true;
+      }
+      base += __shfl_sync(0xffffffffu, incl, 31);
+    }
+    return false;
+  }
+};
 
 // ---------------------------------------------------------------------------
 // Relative position bias
@@ -578,14 +640,16 @@ __device__ __forceinline__ uint8_t* align1024(uint8_t* q) {
 constexpr int kRcSlots = 64;
 __device__ int g_rc_items[2 * kRcSlots];
 struct ItemWalk {
+  Units units;
   int64_t item;
   int heads, index;  // index: head of the item
   bool first;
-  __device__ __forceinline__ ItemWalk(const RcParams& p, int n) : item(blockIdx.x), heads(n), index(0), first(true) {}
+  __device__ __forceinline__ ItemWalk(const RcParams& p, int n, int rows, int lane)
+      : units(p, rows, lane), item(blockIdx.x), heads(n), index(0), first(true) {}
   // The next item that has rows, by a whole warp; false: there is none.
   // `zero`: an item without rows leaves that many zeros there.
-  __device__ __forceinline__ bool next(const RcParams& p, int rows, bool last_first, int lane, Unit& u,
-                                       float* zero = nullptr, int nzero = 0) {
+  __device__ __forceinline__ bool next(const RcParams& p, bool last_first, int lane, Unit& u, float* zero = nullptr,
+                                       int nzero = 0) {
     while (true) {
       if (!first) {
         if (p.items <= gridDim.x) return false;  // an item each
@@ -594,10 +658,9 @@ struct ItemWalk {
         item = static_cast<int64_t>(gridDim.x) + __shfl_sync(0xffffffffu, v, 0);
       }
       if (item >= p.items) return false;
-      index = static_cast<int>(item % heads);
-      const bool found = find_unit(p, item / heads, rows, last_first, first && blockIdx.x == 0, lane, u);
       first = false;
-      if (found) return true;
+      index = static_cast<int>(item % heads);
+      if (units.find(p, item / heads, last_first, lane, u)) return true;
       if (zero != nullptr)
         for (int i = lane; i < nzero; i += 32) zero[item * nzero + i] = 0.f;
     }
@@ -709,11 +772,11 @@ __global__ void __launch_bounds__(kFwdThreads, 1) rc_fwd_kernel(const __grid_con
       prefetch_tmap(&p.mapK);
       prefetch_tmap(&p.mapV);
     }
-    ItemWalk walk(p, p.H);
+    ItemWalk walk(p, p.H, 128 * p.sub, lane);
     for (uint32_t it = 0; ok; ++it) {
       const int slot = it & 1;
       Unit u{0, 0, 0};
-      const bool found = walk.next(p, 128 * p.sub, p.causal != 0, lane, u);
+      const bool found = walk.next(p, p.causal != 0, lane, u);
       if (!(ok = wait_warp(bar(L::free_ + slot), ((it >> 1) & 1) ^ 1, w))) break;
       const int row0 = u.tile * 128 * p.sub, head = walk.index, nk_all = (u.len + 127) >> 7;
       int n[2];
@@ -1108,11 +1171,11 @@ __global__ void __launch_bounds__(kDkvThreads, 1) rc_dkv_kernel(const __grid_con
       prefetch_tmap(&p.mapQ);
       prefetch_tmap(&p.mapO);
     }
-    ItemWalk items_of(p, p.KV);
+    ItemWalk items_of(p, p.KV, 128, lane);
     for (uint32_t n = 0; ok; ++n) {
       const int slot = n & 1;
       Unit u{0, 0, 0};
-      const bool found = items_of.next(p, 128, false, lane, u);
+      const bool found = items_of.next(p, false, lane, u);
       if (!(ok = wait_warp(bar(L::free_ + slot), ((n >> 1) & 1) ^ 1, w))) break;
       if (lane == 0) {
         items[slot].start = u.start;
@@ -1505,12 +1568,12 @@ __global__ void __launch_bounds__(kDqThreads, 1) rc_dq_kernel(const __grid_const
       prefetch_tmap(&p.mapK);
       prefetch_tmap(&p.mapV);
     }
-    ItemWalk items_of(p, p.H);
+    ItemWalk items_of(p, p.H, 128, lane);
     Ring kr{0, L::kK, 0u}, vr{0, L::kV, 0u};
     for (uint32_t n = 0; ok; ++n) {
       const int slot = n & 1;
       Unit u{0, 0, 0};
-      const bool found = items_of.next(p, 128, p.causal != 0, lane, u, grad ? p.partial : nullptr, p.bias.nb);
+      const bool found = items_of.next(p, p.causal != 0, lane, u, grad ? p.partial : nullptr, p.bias.nb);
       if (!(ok = wait_warp(bar(L::free_ + slot), ((n >> 1) & 1) ^ 1, w))) break;
       const int nk_all = (u.len + 127) >> 7, nk = p.causal ? min(nk_all, u.tile + 1) : nk_all;
       if (lane == 0) {
