@@ -1908,18 +1908,25 @@ __global__ void __launch_bounds__(kDqThreads, 1) rc_dq_kernel(const __grid_const
           } else if (side > 0) {
             far_hi = add2(far_hi, rowsum);
           } else {
-            // Sums along the diagonals of the warp's 32 x 32 block: the running
-            // sum of a diagonal moves one lane up at every column; it is whole
-            // when it leaves lane 31.
+            // Sums along the diagonals of the warp's 32 x 32 block: at column k lane
+            // l takes the value of row (l + k) mod 32, which lies at distance -l,
+            // or 32 - l past the last row.  (32 shuffles that do not wait for each
+            // other; handing one running sum from lane to lane took 2700 cycles a
+            // tile.)
             float* dw = diag + warp * kDiag;
-            float acc = 0.f;
+            if (!mine) {
+#pragma unroll
+              for (int c = 0; c < 32; ++c) s[c] = 0u;
+            }
+            float lo[2] = {0.f, 0.f}, hi[2] = {0.f, 0.f};
 #pragma unroll
             for (int c = 0; c < 32; ++c) {
-              const float up = __shfl_up_sync(0xffffffffu, acc, 1);
-              acc = (lane == 0 ? 0.f : up) + (mine ? as_f(s[c]) : 0.f);
-              if (lane == 31) dw[c] = acc;  // distance (c - 31) + block offset
+              const float v = as_f(__shfl_sync(0xffffffffu, s[c], (lane + c) & 31));
+              if (lane + c < 32) lo[c & 1] += v;
+              else hi[c & 1] += v;
             }
-            if (lane < 31) dw[62 - lane] = acc;
+            dw[31 - lane] = lo[0] + lo[1];  // distance (31 - lane) - 31 + block offset
+            if (lane > 0) dw[63 - lane] = hi[0] + hi[1];
             named_bar(1, 32 * kBwdWarps);
             // thread x sums distance x - 127 of the tile over the warps' blocks
             if (threadIdx.x < 255) {
