@@ -1140,6 +1140,7 @@ __global__ void __launch_bounds__(kDkvThreads, 1) rc_dkv_kernel(const __grid_con
   // Heads to 64 wide leave room for a second buffer of scores: they are computed
   // a tile ahead.
   constexpr bool kAhead = DP == 64;
+  constexpr int kHalves = kAhead ? 1 : 2;  // P and dS are handed over in (where the products wait for them)
   constexpr uint32_t kOther = 384;  // columns from one score buffer to the other
   const uint32_t tS = tmem, tP = tmem + 128, tdV = tmem + 256, tdK = tmem + 256 + DP;
   struct Work {
@@ -1315,14 +1316,17 @@ __global__ void __launch_bounds__(kDkvThreads, 1) rc_dkv_kernel(const __grid_con
           const uint32_t rphase = grad ? it & 1 : (it >> 1) & 1;
           if (!(ok = wait_warp(bar(ready), rphase, w))) break;
           tc_fence_after();
-          if (elect_one()) mma_rows<4, 0, 1>(tD, tXi, dtiles + d.stage * L::kTile, idesc_out, i > 0);
-          __syncwarp();
-          if (!(ok = wait_warp(bar(ready + 1), rphase, w))) break;
+          if (kHalves == 2) {
+            if (elect_one()) mma_rows<4, 0, 1>(tD, tXi, dtiles + d.stage * L::kTile, idesc_out, i > 0);
+            __syncwarp();
+            if (!(ok = wait_warp(bar(ready + 1), rphase, w))) break;
+          }
         }
         tc_fence_after();
         if (elect_one()) {
           if (i >= 0) {
-            mma_rows<4, 1, 1>(tD, tXi, dtiles + d.stage * L::kTile, idesc_out, true);
+            if (kHalves == 2) mma_rows<4, 1, 1>(tD, tXi, dtiles + d.stage * L::kTile, idesc_out, true);
+            else mma_rows<4>(tD, tXi, dtiles + d.stage * L::kTile, idesc_out, i > 0);
             mma_commit(bar((grad ? L::qempty : L::oempty) + d.stage));
           }
           if (!ahead && more) products();
@@ -1428,10 +1432,12 @@ __global__ void __launch_bounds__(kDkvThreads, 1) rc_dkv_kernel(const __grid_con
 #pragma unroll
           for (int c = 0; c < 8; ++c) pk[c] = pack_bf16x2(as_f(s[16 * h + 2 * c]), as_f(s[16 * h + 2 * c + 1]));
           tmem_st8(tSw + 8 * h, pk);
-          tmem_st_wait();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bar(L::pready + 2 * buf + h));
+          if (h + 1 == 2 || kHalves == 2) {
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(L::pready + 2 * buf + (kHalves == 2 ? h : 0)));
+          }
         }
         ok = ok && wait_warp(bar(L::dpfull), it & 1, w);
         tc_fence_after();
@@ -1454,10 +1460,12 @@ __global__ void __launch_bounds__(kDkvThreads, 1) rc_dkv_kernel(const __grid_con
             pk[((c >> 1) & 7) + 1] = pack_bf16x2(a, b);
           }
           tmem_st8(tPw + 8 * h, pk);
-          tmem_st_wait();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bar(L::dsready + h));
+          if (h + 1 == 2 || kHalves == 2) {
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(L::dsready + (kHalves == 2 ? h : 0)));
+          }
         }
         if (lane == 0) mbar_arrive(bar(L::vecempty + buf));
       }
@@ -1520,11 +1528,11 @@ struct DqItem {
 };
 
 // The bias gradient's shared memory: per compute warp the sums of its 32 x 32
-// block by distance (63 of them), the CTA's sums by clamped distance, and the
-// threads' sums beyond the ends.
+// block by distance (63 of them), for two tiles, the CTA's sums by distance,
+// the warps' sums beyond the ends, and the buckets' first distances.
 constexpr int kDiag = 64;
 __host__ __device__ constexpr int grad_floats(int md) {
-  return kBwdWarps * kDiag + 2 * md + 1 + 2 * 32 * kBwdWarps;
+  return 2 * kBwdWarps * kDiag + 2 * md + 1 + 2 * kBwdWarps + kMaxRelBuckets;
 }
 
 template <int DP, bool BIAS>
@@ -1541,13 +1549,16 @@ __global__ void __launch_bounds__(kDqThreads, 1) rc_dq_kernel(const __grid_const
   float* tabs = dots + 512;                                         // a table for each slot
   float* vals = tabs + 2 * tabn;                                    // the head's values
   uint8_t* map = reinterpret_cast<uint8_t*>(vals + (BIAS ? kMaxRelBuckets : 0));  // the distances' buckets
-  float* diag = reinterpret_cast<float*>(map + tabn);               // [kBwdWarps][kDiag]
-  float* bins = diag + kBwdWarps * kDiag;                           // [2 md + 1]
-  float* ends = bins + 2 * md + 1;                                  // [2][32 kBwdWarps]
+  float* diag = reinterpret_cast<float*>(map + tabn);               // [2][kBwdWarps][kDiag]
+  float* bins = diag + 2 * kBwdWarps * kDiag;                       // [2 md + 1]
+  float* ends = bins + 2 * md + 1;                                  // [2][kBwdWarps]
+  int* firsts = reinterpret_cast<int*>(ends + 2 * kBwdWarps);       // p.bias.first: indexed reads of it are slow
   const bool grad = BIAS && p.partial != nullptr;
   if (BIAS) fill_map(p.bias, map);
-  if (grad)
+  if (grad) {
     for (int i = threadIdx.x; i < 2 * md + 1; i += kDqThreads) bins[i] = 0.f;
+    for (int i = threadIdx.x; i < p.bias.side; i += kDqThreads) firsts[i] = p.bias.first[i];
+  }
   const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
   enter<kBwdWarps>(hd, L::count, L::template arrivals<BIAS>);
   const uint32_t bar0 = smem_addr(hd->bar);
@@ -1555,6 +1566,7 @@ __global__ void __launch_bounds__(kDqThreads, 1) rc_dq_kernel(const __grid_const
   const WaitCtx w{&hd->abort_flag, p.err, p.wait_limit_ns};
   const uint32_t tmem = uniform(hd->tmem);
   constexpr bool kAhead = DP == 64;  // dP in two buffers
+  constexpr int kHalves = kAhead ? 1 : 2;  // dS is handed over in (where the products wait for it)
   const uint32_t tP = tmem + 128, tdQ = tmem + (kAhead ? 384 : 256), tQ = tmem + (kAhead ? 448 : 384),
                  tO = tmem + (kAhead ? 480 : 448);
 
@@ -1727,14 +1739,17 @@ __global__ void __launch_bounds__(kDqThreads, 1) rc_dq_kernel(const __grid_const
           const int ready = L::dsready + 2 * (nd & 1);
           if (!(ok = wait_warp(bar(ready), (nd >> 1) & 1, w))) break;
           tc_fence_after();
-          if (elect_one()) mma_rows<4, 0, 1>(tdQ, tPj, smem_addr(sK + dr.stage * L::kTile), idesc_out, j > 0);
-          __syncwarp();
-          if (!(ok = wait_warp(bar(ready + 1), (nd >> 1) & 1, w))) break;
+          if (kHalves == 2) {
+            if (elect_one()) mma_rows<4, 0, 1>(tdQ, tPj, smem_addr(sK + dr.stage * L::kTile), idesc_out, j > 0);
+            __syncwarp();
+            if (!(ok = wait_warp(bar(ready + 1), (nd >> 1) & 1, w))) break;
+          }
         }
         tc_fence_after();
         if (elect_one()) {
           if (j >= 0) {
-            mma_rows<4, 1, 1>(tdQ, tPj, smem_addr(sK + dr.stage * L::kTile), idesc_out, true);
+            if (kHalves == 2) mma_rows<4, 1, 1>(tdQ, tPj, smem_addr(sK + dr.stage * L::kTile), idesc_out, true);
+            else mma_rows<4>(tdQ, tPj, smem_addr(sK + dr.stage * L::kTile), idesc_out, j > 0);
             mma_commit(bar(L::kempty + dr.stage));
           }
           if (more) dprobs(jn);
@@ -1897,10 +1912,12 @@ __global__ void __launch_bounds__(kDqThreads, 1) rc_dq_kernel(const __grid_const
 #pragma unroll
           for (int c = 0; c < 8; ++c) pk[c] = pack_bf16x2(as_f(s[16 * h + 2 * c]), as_f(s[16 * h + 2 * c + 1]));
           tmem_st8(tPj + 8 * h, pk);
-          tmem_st_wait();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bar(L::dsready + 2 * (nt & 1) + h));
+          if (h + 1 == 2 || kHalves == 2) {
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(L::dsready + 2 * (nt & 1) + (kHalves == 2 ? h : 0)));
+          }
         }
         if (BIAS && grad) {
           if (side < 0) {
@@ -1913,7 +1930,8 @@ __global__ void __launch_bounds__(kDqThreads, 1) rc_dq_kernel(const __grid_const
             // or 32 - l past the last row.  (32 shuffles that do not wait for each
             // other; handing one running sum from lane to lane took 2700 cycles a
             // tile.)
-            float* dw = diag + warp * kDiag;
+            float* dt_sums = diag + (nt & 1) * kBwdWarps * kDiag;
+            float* dw = dt_sums + warp * kDiag;
             if (!mine) {
 #pragma unroll
               for (int c = 0; c < 32; ++c) s[c] = 0u;
@@ -1927,22 +1945,25 @@ __global__ void __launch_bounds__(kDqThreads, 1) rc_dq_kernel(const __grid_const
             }
             dw[31 - lane] = lo[0] + lo[1];  // distance (31 - lane) - 31 + block offset
             if (lane > 0) dw[63 - lane] = hi[0] + hi[1];
+            // (the next near tile writes the other buffer, and the one after that
+            // comes behind the next one's barrier)
             named_bar(1, 32 * kBwdWarps);
-            // thread x sums distance x - 127 of the tile over the warps' blocks
+            // thread x sums distance x - 127 of the tile over the warps' blocks, whose
+            // offsets are 32 (part - quarter): two offsets hold the distance
             if (threadIdx.x < 255) {
               const int dt = static_cast<int>(threadIdx.x) - 127;
+              const int k = (dt + 31) >> 5, at = dt - 32 * k + 31;
               float sum = 0.f;
 #pragma unroll
-              for (int wv = 0; wv < kBwdWarps; ++wv) {
-                const int at = dt - 32 * (wv >> 2) + 32 * (wv & 3) + 31;
-                if (at >= 0 && at < 63) sum += diag[wv * kDiag + at];
+              for (int qu = 0; qu < 4; ++qu) {
+                if (qu + k >= 0 && qu + k < 4) sum += dt_sums[(4 * (qu + k) + qu) * kDiag + at];
+                if (qu + k >= 1 && qu + k < 5 && at < 31) sum += dt_sums[(4 * (qu + k - 1) + qu) * kDiag + at + 32];
               }
               const int delta = 128 * j - r0 + dt;
               if (delta <= -md) end_lo += sum;
               else if (delta >= md) end_hi += sum;
               else bins[delta + md] += sum;
             }
-            named_bar(1, 32 * kBwdWarps);
           }
         }
       }
@@ -1960,32 +1981,39 @@ __global__ void __launch_bounds__(kDqThreads, 1) rc_dq_kernel(const __grid_const
              static_cast<int64_t>(hq.shard) * p.shard_w + static_cast<int64_t>(hq.local) * p.d + ofirst;
       if (!ok || !mine || ocols <= 0) prev = nullptr;
       if (BIAS && grad) {
-        // the item's sums by bucket, in a fixed order
+        // the item's sums by bucket, in a fixed order: a warp a bucket
         constexpr int kN = 32 * kBwdWarps;
         float a0, a1, b0, b1;
         unpack2(far_lo, a0, a1);
         unpack2(far_hi, b0, b1);
-        ends[threadIdx.x] = end_lo + (mine ? a0 + a1 : 0.f);
-        ends[kN + threadIdx.x] = end_hi + (mine ? b0 + b1 : 0.f);
-        named_bar(1, kN);
-        if (warp < 2) {
-          float a = 0.f;
-          for (int x = lane; x < kN; x += 32) a += ends[kN * warp + x];
+        float lo = end_lo + (mine ? a0 + a1 : 0.f), hi = end_hi + (mine ? b0 + b1 : 0.f);
 #pragma unroll
-          for (int o = 16; o > 0; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
-          if (lane == 0) bins[warp ? 2 * md : 0] = a;
+        for (int o = 16; o > 0; o >>= 1) {
+          lo += __shfl_xor_sync(0xffffffffu, lo, o);
+          hi += __shfl_xor_sync(0xffffffffu, hi, o);
+        }
+        if (lane == 0) {
+          ends[warp] = lo;
+          ends[kBwdWarps + warp] = hi;
         }
         named_bar(1, kN);
-        for (int u = threadIdx.x; u < p.bias.nb; u += kN) {
-          // bucket u holds the distances x with first[k] <= x < first[k + 1] on its side
+        for (int u = warp; u < p.bias.nb; u += kBwdWarps) {
+          // bucket u holds the distances x with first[k] <= x < first[k + 1] on its
+          // side, the last one also those of md and more; without buckets of their
+          // own, keys behind the query count as distance 0
           const int k = u % p.bias.side;
-          const bool pos = p.bias.both && u >= p.bias.side;
-          const int lo = p.bias.first[k], hi = k + 1 < p.bias.side ? p.bias.first[k + 1] : md + 1;
+          const bool pos = p.bias.both && u >= p.bias.side, last = k + 1 == p.bias.side;
+          const int from = firsts[k], to = last ? md : firsts[k + 1];
           float a = 0.f;
-          for (int x = max(lo, pos ? 1 : 0); x < min(hi, md + 1); ++x) a += bins[md + (pos ? x : -x)];
-          if (!p.bias.both && k == 0)
-            for (int x = 1; x <= md; ++x) a += bins[md + x];  // keys behind the query count as distance 0
-  p.partial[items[slot].item * p.bias.nb + u] = a;
+          for (int x = max(from, pos ? 1 : 0) + lane; x < min(to, md); x += 32) a += bins[md + (pos ? x : -x)];
+          if (last && lane < kBwdWarps) a += ends[(pos ? kBwdWarps : 0) + lane];
+          if (!p.bias.both && k == 0 && !p.causal) {
+            for (int x = 1 + lane; x < md; x += 32) a += bins[md + x];
+            if (lane < kBwdWarps) a += ends[kBwdWarps + lane];
+          }
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
+          if (lane == 0) p.partial[items[slot].item * p.bias.nb + u] = a;
         }
         named_bar(1, kN);
         for (int i = threadIdx.x; i < 2 * md + 1; i += kN) bins[i] = 0.f;

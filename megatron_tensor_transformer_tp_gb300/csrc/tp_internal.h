@@ -212,7 +212,6 @@ struct RcParams {
   float* lse;       // forward out, backward in; (H, T)
   float* D;         // (H, T) scratch
   void* dQKV;
-  RcBias bias;
   const float* table;  // (nb, H)
   float* dtable;
   float* partial;      // (units, H, nb) scratch, or null: no bias gradient
@@ -220,6 +219,7 @@ struct RcParams {
   int fault_skip;
   unsigned* err;
   unsigned long long wait_limit_ns;
+  RcBias bias;
 };
 size_t rc_dot_bytes(int64_t T, int H);
 size_t rc_partial_bytes(const RcParams& p);
