@@ -510,55 +510,80 @@ def tp_attn_core_dropout_bwd(QKV, P, Pd, C, dC, s, n_heads, N, causal, p_attn, s
 # ----------------------------------------------------------------------------
 # Attention without stored probabilities, and the relative position bias
 # ----------------------------------------------------------------------------
-def _rows(t, name, dtype, rows, device, cols=None):
-    """(pointer, row pitch) of a 2D tensor whose rows may lie further apart than they are wide."""
+# These calls check in one expression what a right call passes at once, and look for the reason only if it fails:
+# on short sequences the checks took longer than the kernels.
+def _refuse(t, name, dtype, shape, index):
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor (the library has no CPU path)")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, QKV on {device}")
-    if t.dtype != dtype:
+    if t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, not on the current device cuda:{index}")
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
-    if t.dim() != 2 or t.shape[0] != rows or (cols is not None and t.shape[1] != cols):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, not ({rows}, {'...' if cols is None else cols})")
-    if t.shape[1] > 1 and t.stride(1) != 1:
-        raise ValueError(f"{name} must have contiguous rows")
-    return t.data_ptr(), t.stride(0) if rows > 1 else max(t.stride(0), t.shape[1])
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, not {tuple(shape)}")
+    raise ValueError(f"{name} must have contiguous rows" if len(shape) == 2 else f"{name} must be contiguous")
 
 
-def _vec(t, name, dtype, shape, device):
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape):
-        raise (TypeError if t.dtype != dtype else ValueError)(f"{name} must be {dtype} of shape {tuple(shape)}")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, QKV on {device}")
-    return _dev(t, name)
+def _rows(t, name, shape, index):
+    """(pointer, row pitch) of a bf16 matrix whose rows may lie further apart than they are wide."""
+    try:
+        if t.dtype is torch.bfloat16 and t.shape == shape and t.get_device() == index:
+            pitch, step = t.stride()
+            if step == 1 or shape[1] <= 1:
+                return t.data_ptr(), pitch if shape[0] > 1 else max(pitch, shape[1])
+    except AttributeError:
+        pass
+    _refuse(t, name, torch.bfloat16, shape, index)
+
+
+def _vec(t, name, dtype, shape, index):
+    """Pointer of a contiguous tensor."""
+    try:
+        if t.dtype is dtype and t.shape == shape and t.get_device() == index and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _refuse(t, name, dtype, shape, index)
 
 
 def _attn_cfg(cfg: dict, T: int) -> tp_attn_config:
     return tp_attn_config(T, cfg["b"], cfg.get("s") or 0, cfg["n_heads"], cfg["n_kv_heads"], cfg["d"], cfg["N"],
-                          int(bool(cfg["causal"])), float(cfg.get("scale") or 0.0))
+                          1 if cfg["causal"] else 0, cfg.get("scale") or 0.0)
 
 
 def _bias_cfg(bias: dict) -> tp_relbias_config:
-    return tp_relbias_config(bias["num_buckets"], bias["max_distance"], int(bool(bias["bidirectional"])))
+    return tp_relbias_config(bias["num_buckets"], bias["max_distance"], 1 if bias["bidirectional"] else 0)
 
 
 def _attn_common(QKV, cfg, C, lse, seq_starts):
     """The arguments that every call of this family begins with, checked against the sizes."""
     if not isinstance(QKV, torch.Tensor) or QKV.dim() != 2:
         raise ValueError("QKV must be a 2D tensor")
-    T, dev = QKV.shape[0], QKV.device
-    if QKV.is_cuda and dev.index != torch.cuda.current_device():
-        raise ValueError(f"QKV is on {dev}, the current device is cuda:{torch.cuda.current_device()}")
-    H, KV, d = cfg["n_heads"], cfg["n_kv_heads"], cfg["d"]
-    q = _rows(QKV, "QKV", torch.bfloat16, T, dev, (H + 2 * KV) * d)
-    c = _rows(C, "C", torch.bfloat16, T, dev, H * d)
-    l = _vec(lse, "lse", torch.float32, (H, T), dev)
-    st = None if seq_starts is None else _vec(seq_starts, "seq_starts", torch.int64, (cfg["b"] + 1,), dev)
-    return _attn_cfg(cfg, T), q, c, l, st, T, dev
+    T, H, d = QKV.shape[0], cfg["n_heads"], cfg["d"]
+    index = torch._C._cuda_getDevice() if QKV.is_cuda else -2
+    qshape, cshape = (T, (H + 2 * cfg["n_kv_heads"]) * d), (T, H * d)
+    q = _rows(QKV, "QKV", qshape, index)
+    c = _rows(C, "C", cshape, index)
+    l = _vec(lse, "lse", torch.float32, (H, T), index)
+    st = None if seq_starts is None else _vec(seq_starts, "seq_starts", torch.int64, (cfg["b"] + 1,), index)
+    return _attn_cfg(cfg, T), q, c, l, st, qshape, cshape, index
+
+
+def _attn_stream(stream, index) -> int:
+    return torch._C._cuda_getCurrentRawStream(index) if stream is None else _stream(stream)
+
+
+def _scratch(workspace, index):
+    """(pointer, bytes) of the workspace, any contiguous tensor on the device."""
+    if workspace is None:
+        return None, 0
+    if not isinstance(workspace, torch.Tensor):
+        raise TypeError("workspace must be a torch.Tensor")
+    if workspace.get_device() != index or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be contiguous and on cuda:{index}")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
 def tp_attn_recompute_workspace_size(cfg: dict, T: int, bias: Optional[dict] = None) -> int:
@@ -574,20 +599,21 @@ def tp_attn_recompute_fwd(QKV, cfg, C, lse, seq_starts=None, stream=None):
 
     cfg: dict with b, n_heads, n_kv_heads, d, N, causal, optionally scale (0: 1 / sqrt(d)), and s (tokens of
     every sequence) unless seq_starts (int64 CUDA tensor of b + 1 row numbers) is given.  Rows outside every
-    sequence are left as they are."""
-    c, q, o, l, st, _, _ = _attn_common(QKV, cfg, C, lse, seq_starts)
-    _check(lib().tp_attn_recompute_fwd(TP_BF16, ctypes.byref(c), st, q[0], q[1], o[0], o[1], l, _stream(stream)),
+    sequence are left as they are.  QKV, C and the backward's dC and dQKV may be column slices of wider buffers.
+    Every tensor lies on the current device."""
+    c, q, o, l, st, _, _, dev = _attn_common(QKV, cfg, C, lse, seq_starts)
+    _check(lib().tp_attn_recompute_fwd(TP_BF16, c, st, q[0], q[1], o[0], o[1], l, _attn_stream(stream, dev)),
            "tp_attn_recompute_fwd")
 
 
 def tp_attn_recompute_bwd(QKV, cfg, C, lse, dC, dQKV, workspace, seq_starts=None, stream=None):
-    """dQKV <- gradient of tp_attn_recompute_fwd given its C and lse and the context gradient dC."""
-    c, q, o, l, st, T, dev = _attn_common(QKV, cfg, C, lse, seq_starts)
-    do = _rows(dC, "dC", torch.bfloat16, T, dev, C.shape[1])
-    dq = _rows(dQKV, "dQKV", torch.bfloat16, T, dev, QKV.shape[1])
-    _check(lib().tp_attn_recompute_bwd(TP_BF16, ctypes.byref(c), st, q[0], q[1], o[0], o[1], l, do[0], do[1],
-                                       dq[0], dq[1], _dev(workspace, "workspace"), _ws_bytes(workspace),
-                                       _stream(stream)),
+    """dQKV <- gradient of tp_attn_recompute_fwd given its C and lse and the context gradient dC.
+
+    workspace: a CUDA tensor of tp_attn_recompute_workspace_size bytes."""
+    c, q, o, l, st, qshape, cshape, dev = _attn_common(QKV, cfg, C, lse, seq_starts)
+    do, dq, ws = _rows(dC, "dC", cshape, dev), _rows(dQKV, "dQKV", qshape, dev), _scratch(workspace, dev)
+    _check(lib().tp_attn_recompute_bwd(TP_BF16, c, st, q[0], q[1], o[0], o[1], l, do[0], do[1], dq[0], dq[1], ws[0],
+                                       ws[1], _attn_stream(stream, dev)),
            "tp_attn_recompute_bwd")
 
 
@@ -595,25 +621,24 @@ def tp_attn_relbias_fwd(QKV, cfg, bias, table, C, lse, seq_starts=None, stream=N
     """tp_attn_recompute_fwd with table[bucket(key - query), head] added to the scores.
 
     bias: dict with num_buckets, max_distance, bidirectional; table (num_buckets, n_heads) fp32."""
-    c, q, o, l, st, _, dev = _attn_common(QKV, cfg, C, lse, seq_starts)
+    c, q, o, l, st, _, _, dev = _attn_common(QKV, cfg, C, lse, seq_starts)
     t = _vec(table, "table", torch.float32, (bias["num_buckets"], cfg["n_heads"]), dev)
-    _check(lib().tp_attn_relbias_fwd(TP_BF16, ctypes.byref(c), ctypes.byref(_bias_cfg(bias)), t, st, q[0], q[1],
-                                     o[0], o[1], l, _stream(stream)),
+    _check(lib().tp_attn_relbias_fwd(TP_BF16, c, _bias_cfg(bias), t, st, q[0], q[1], o[0], o[1], l,
+                                     _attn_stream(stream, dev)),
            "tp_attn_relbias_fwd")
 
 
 def tp_attn_relbias_bwd(QKV, cfg, bias, table, C, lse, dC, dQKV, dtable, workspace, accumulate=False,
                         seq_starts=None, stream=None):
-    """dQKV and, unless it is None, dtable <- gradient of tp_attn_relbias_fwd."""
-    c, q, o, l, st, T, dev = _attn_common(QKV, cfg, C, lse, seq_starts)
+    """dQKV and, unless it is None, dtable <- gradient of tp_attn_relbias_fwd (accumulate: dtable is added to)."""
+    c, q, o, l, st, qshape, cshape, dev = _attn_common(QKV, cfg, C, lse, seq_starts)
     shape = (bias["num_buckets"], cfg["n_heads"])
     t = _vec(table, "table", torch.float32, shape, dev)
     dt = None if dtable is None else _vec(dtable, "dtable", torch.float32, shape, dev)
-    do = _rows(dC, "dC", torch.bfloat16, T, dev, C.shape[1])
-    dq = _rows(dQKV, "dQKV", torch.bfloat16, T, dev, QKV.shape[1])
-    _check(lib().tp_attn_relbias_bwd(TP_BF16, ctypes.byref(c), ctypes.byref(_bias_cfg(bias)), t, st, q[0], q[1],
-                                     o[0], o[1], l, do[0], do[1], dq[0], dq[1], dt, int(bool(accumulate)),
-                                     _dev(workspace, "workspace"), _ws_bytes(workspace), _stream(stream)),
+    do, dq, ws = _rows(dC, "dC", cshape, dev), _rows(dQKV, "dQKV", qshape, dev), _scratch(workspace, dev)
+    _check(lib().tp_attn_relbias_bwd(TP_BF16, c, _bias_cfg(bias), t, st, q[0], q[1], o[0], o[1], l, do[0], do[1],
+                                     dq[0], dq[1], dt, 1 if accumulate else 0, ws[0], ws[1],
+                                     _attn_stream(stream, dev)),
            "tp_attn_relbias_bwd")
 
 
