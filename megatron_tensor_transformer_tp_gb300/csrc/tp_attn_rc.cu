@@ -492,8 +492,9 @@ __device__ __forceinline__ void mma_scores_ts(uint32_t d_tmem, uint32_t a_tmem, 
 // D (+)= A B: A 128 x 128 bf16 in TMEM, B = 128 rows of a tile as stored
 // (contraction over its rows).  Each compute warp writes its part of A where it
 // read its scores: with PARTS parts, part x's columns start at 128 x / PARTS.
-// FIRST, COUNT: the 16-row steps of each part that are taken.
-template <int PARTS, int FIRST = 0, int COUNT = 8 / PARTS>
+// FIRST, COUNT: the 16-row steps of each part that are taken.  STRIDE: TMEM
+// columns from part to part, where not as above.
+template <int PARTS, int FIRST = 0, int COUNT = 8 / PARTS, int STRIDE = 128 / PARTS>
 __device__ __forceinline__ void mma_rows(uint32_t d_tmem, uint32_t a_tmem, uint32_t b, uint32_t idesc,
                                          bool accumulate) {
   const uint64_t bd = sdesc(b, kPanel, 1024);
@@ -501,7 +502,7 @@ __device__ __forceinline__ void mma_rows(uint32_t d_tmem, uint32_t a_tmem, uint3
   for (int h = 0; h < PARTS; ++h) {
 #pragma unroll
     for (int kk = FIRST; kk < FIRST + COUNT; ++kk)
-      mma_bf16_ts(d_tmem, a_tmem + 128 / PARTS * h + 8 * kk, bd + (8 / PARTS * h + kk) * (2048 >> 4), idesc,
+      mma_bf16_ts(d_tmem, a_tmem + STRIDE * h + 8 * kk, bd + (8 / PARTS * h + kk) * (2048 >> 4), idesc,
                   accumulate || h > 0 || kk > FIRST);
   }
 }
@@ -725,13 +726,14 @@ struct FwdShape {
   static constexpr int qfull = 0, kfull = 2, vfull = kfull + kStages, tail = vfull + kStages, kempty = tail + 1,
                        vempty = kempty + kStages, sfull = vempty + kStages, pfull = sfull + 2, odone = pfull + 4,
                        ofree = odone + 2, qempty = ofree + 2, info = qempty + 2, tabfull = info + 2,
-                       free_ = tabfull + 2, drain = free_ + 2, count = drain + 2;
+                       free_ = tabfull + 2, sread = free_ + 2, pvdone = sread + 2, drain = pvdone + 2, count = drain + 2;
   static_assert(count <= kMaxBars && kempty <= 32, "barriers");
   template <bool BIAS>
   static uint32_t __device__ __forceinline__ arrivals(int i) {
     if (i >= pfull && i < odone) return 8u;
     if (i >= ofree && i < qempty) return 8u;
-    if (i >= free_ && i < drain) return kFwdWarps + 2 + (BIAS ? 1 : 0);
+    if (i >= free_ && i < sread) return kFwdWarps + 2 + (BIAS ? 1 : 0);
+    if (i >= sread && i < pvdone) return 8u;
     return i >= kempty && i < sfull ? 2u : 1u;
   }
 };
@@ -761,6 +763,11 @@ __global__ void __launch_bounds__(kFwdThreads, 1) rc_fwd_kernel(const __grid_con
   auto bar = [&](int i) { return bar0 + 8u * i; };
   const WaitCtx w{&hd->abort_flag, p.err, p.wait_limit_ns};
   const uint32_t tmem = uniform(hd->tmem);
+  // TMEM: scores [0, 256), outputs from 256 and 384.  Heads to 64 wide leave 64
+  // columns behind each output, where the probabilities go instead of over the
+  // scores: the next scores then wait for the softmax to have read the last ones
+  // only, not for the product of its probabilities.
+  constexpr bool kApart = DP == 64;
 
   if (warp == kFwdWarps + 2) {
     Flight fl;
@@ -857,7 +864,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1) rc_fwd_kernel(const __grid_con
     const int t = warp - kFwdWarps;
     const int ksteps = (p.d + 15) >> 4;
     const uint32_t idesc_pv = idesc_bf16(0, 1, ksteps * 16);
-    const uint32_t dO = tmem + 256 + 128 * t, tS = tmem + 128 * t;
+    const uint32_t dO = tmem + 256 + 128 * t, tS = tmem + 128 * t, aP = kApart ? dO + 64 : tS;
+    constexpr int kStride = kApart ? 32 : 64;  // from the first key half's probabilities to the second's
     uint32_t c = 0, np = 0, nq = 0;  // K/V tiles, probability tiles and items of this query tile so far
     bool ok = true, issued = false;
     for (uint32_t it = 0; ok; ++it) {
@@ -898,19 +906,25 @@ __global__ void __launch_bounds__(kFwdThreads, 1) rc_fwd_kernel(const __grid_con
         if (!(ok = vfull(j) && (j + 1 >= nt || kfull(j + 1)))) break;
         // the output of the item before has been read
         if (j == 0 && !(ok = wait_warp(bar(L::ofree + t), (nq & 1) ^ 1, w))) break;
+        if (kApart) {
+          if (!(ok = wait_warp(bar(L::sread + t), np & 1, w))) break;
+          tc_fence_after();
+          if (j + 1 < nt) scores(j + 1);
+        }
         if (!(ok = wait_warp(bar(L::pfull + 2 * t), np & 1, w))) break;
         tc_fence_after();
-        if (elect_one()) mma_rows<2, 0, 2>(dO, tS, b, idesc_pv, j > 0);
+        if (elect_one()) mma_rows<2, 0, 2, kStride>(dO, aP, b, idesc_pv, j > 0);
         __syncwarp();
         if (!(ok = wait_warp(bar(L::pfull + 2 * t + 1), np & 1, w))) break;
         tc_fence_after();
         if (elect_one()) {
-          mma_rows<2, 2, 2>(dO, tS, b, idesc_pv, true);
+          mma_rows<2, 2, 2, kStride>(dO, aP, b, idesc_pv, true);
+          if (kApart) mma_commit(bar(L::pvdone + t));
           mma_commit(bar(L::vempty + st));
           if (j + 1 >= nt) mma_commit(bar(L::odone + t));
         }
         __syncwarp();
-        if (j + 1 < nt) scores(j + 1);
+        if (!kApart && j + 1 < nt) scores(j + 1);
       }
       // key tiles that only the other query tile sees
       for (int j = nt; ok && j < nmax; ++j) {
@@ -926,6 +940,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) rc_fwd_kernel(const __grid_con
     const int t = warp >> 3, half = (warp >> 2) & 1, quarter = warp & 3;
     const uint32_t lane_base = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
     const uint32_t tS = lane_base + 128 * t, tO = lane_base + 256 + 128 * t;
+    const uint32_t tP = kApart ? tO + 64 + 32 * half : tS + 64 * half;
     // the two warps of these rows meet at a barrier of their own
     const int pair_bar = 1 + 4 * t + quarter;
     float* mine_at = part + half * 256 + t * 128 + quarter * 32 + lane;
@@ -958,6 +973,11 @@ __global__ void __launch_bounds__(kFwdThreads, 1) rc_fwd_kernel(const __grid_con
         tmem_ld32_issue(tS + 64 * half + 32, s + 32);
         tmem_ld32_wait(s);
         tmem_ld32_wait(s + 32);
+        if (kApart) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(L::sread + t));
+        }
         const int c0 = 128 * j + 64 * half, r0 = row0 + 128 * t;
         float mul = sl2, add = 0.f;  // x = s mul + add
         if (BIAS) {
@@ -984,6 +1004,11 @@ __global__ void __launch_bounds__(kFwdThreads, 1) rc_fwd_kernel(const __grid_con
           for (int c = 8 + q; c < 64; c += 8) mx[q] = fmaxf(fmaxf(mx[q], as_f(s[c])), as_f(s[c + 4]));
         }
         const float mh = fmaf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), mul, add);
+        // the product of the tile before has read its probabilities and added to the output
+        if (kApart) {
+          ok = ok && wait_warp(bar(L::pvdone + t), (np & 1) ^ 1, w);
+          tc_fence_after();
+        }
         // The exponents' reference is the first tile's maximum and follows the
         // running one only when a row's is 2^16 above it: up to there the
         // exponentials and their sums are as exact (fp32 and bf16 have the range),
@@ -1018,7 +1043,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) rc_fwd_kernel(const __grid_con
             sum[c & 1] = add2(sum[c & 1], pack2(a, b));
             pk[c] = pack_bf16x2(a, b);
           }
-          tmem_st16(tS + 64 * half + 16 * h, pk);
+          tmem_st16(tP + 16 * h, pk);
           tmem_st_wait();
           tc_fence_before();
           __syncwarp();
