@@ -37,7 +37,8 @@
  *    optimizer's completion counters, a 16 x 64 block of ones) and it never
  *    frees caller memory.  Tensor-core GEMM launches and optimizer norm passes
  *    each rotate over 64 counter slots, so at most 64 launches of each may be
- *    in flight at the same time across all streams of a device.  A call captured into a
+ *    in flight at the same time across all streams of a device; the launches of
+ *    tp_attn_recompute_* and tp_attn_relbias_* rotate over 4096.  A call captured into a
  *    CUDA graph keeps the slot it was given at capture: replay such a graph
  *    on one stream at a time (replays in sequence reuse the slot safely, since
  *    every launch resets its counters as it ends).
@@ -341,7 +342,9 @@ TP_API tp_status tp_attn_recompute_bwd(tp_dtype dt, const tp_attn_config* cfg, c
  *           of bucket u in every sequence (fp32 dS, before its rounding; accumulate:
  *           added to the old value), or NULL: not computed
  * The bias is added inside the kernels and its gradient summed there, in a
- * fixed order.
+ * fixed order.  Entries are finite or -infinity; those below -2.3e38 count as
+ * -infinity, which hides the bucket's keys.  A row that sees no key has C = 0,
+ * lse = -infinity and no gradient.
  */
 TP_API tp_status tp_attn_relbias_fwd(tp_dtype dt, const tp_attn_config* cfg, const tp_relbias_config* bias,
                                      const float* table, const int64_t* seq_starts, const void* QKV,

@@ -1262,7 +1262,7 @@ bool rel_step_reached(int n, int E, int md, int K, int j) {
 // Sizes and bias into P, without pointers.
 tp_status rc_sizes(const tp_attn_config* c, const tp_relbias_config* rb, bool dense, RcParams* P) {
   if (c == nullptr) return TP_ERR_INVALID;
-  if (c->T < 0 || c->T > INT32_MAX || c->b < 0 || c->b > INT32_MAX || c->n_heads < 1 || c->n_kv_heads < 1 ||
+  if (c->T < 0 || c->T > INT32_MAX || c->b < 0 || c->b > (1 << 30) || c->n_heads < 1 || c->n_kv_heads < 1 ||
       c->N < 1 || c->N > 8 || c->n_heads % c->N != 0 || c->n_kv_heads % c->N != 0 ||
       c->n_heads % c->n_kv_heads != 0 || c->d < 1 || c->d > 128)
     return TP_ERR_INVALID;

@@ -222,10 +222,12 @@ struct Unit {
   int start, len, tile;  // first token and length of the sequence, tile inside it
 };
 // Up to 32 sequences are held by a warp, a lane each; more go in their own
-// order.  (Four a lane made the whole forward 4% slower.)
+// order, looked for from where the CTA's last unit was found.  (Four a lane made
+// the whole forward 4% slower.)
 struct Units {
   int start, len, n;  // of the lane's sequence
-  int rows, top;      // the longest sequence's runs
+  int rows, top;      // the longest sequence's runs; not held: the first sequence that is looked at next
+  int64_t base;       // not held: units of the sequences before that one
   bool held;
 
   __device__ __forceinline__ static bool read(const RcParams& p, int i, int64_t& a, int64_t& e) {
@@ -238,7 +240,7 @@ struct Units {
     e = min(max(e, a), p.T);
     return fine;
   }
-  __device__ __forceinline__ Units(const RcParams& p, int rows_, int lane) : rows(rows_), top(0), held(false) {
+  __device__ __forceinline__ Units(const RcParams& p, int rows_, int lane) : rows(rows_), top(0), base(0), held(false) {
     if (p.seq_starts == nullptr) return;
     held = p.b <= 32;
     int64_t a, e;
@@ -246,15 +248,15 @@ struct Units {
     start = static_cast<int>(a);
     len = static_cast<int>(e - a);
     n = (len + rows - 1) / rows;
-    top = __reduce_max_sync(0xffffffffu, n);
+    top = held ? __reduce_max_sync(0xffffffffu, n) : 0;
     if (!held && blockIdx.x == 0)
       for (int i = lane; i < p.b; i += 32) fine &= read(p, i, a, e);
     if (!fine && blockIdx.x == 0) atomicOr(p.err, kErrInvalid);
   }
   // Units of rank below r.
   __device__ __forceinline__ int64_t below(int r) const { return __reduce_add_sync(0xffffffffu, min(n, r)); }
-  // false: there is no such unit
-  __device__ __forceinline__ bool find(const RcParams& p, int64_t unit, bool last_first, int lane, Unit& u) const {
+  // false: there is no such unit.  The units of one Units object never decrease.
+  __device__ __forceinline__ bool find(const RcParams& p, int64_t unit, bool last_first, int lane, Unit& u) {
     if (p.seq_starts == nullptr) {
       const int per = (p.s + rows - 1) / rows;
       const int rank = static_cast<int>(unit / p.b), seq = static_cast<int>(unit % p.b);
@@ -281,10 +283,9 @@ struct Units {
       u.tile = last_first ? runs - 1 - lo : lo;
       return true;
     }
-    int64_t base = 0;
-    for (int i0 = 0; i0 < p.b; i0 += 32) {
+    for (; top < p.b; top += 32) {
       int64_t a, e;
-      read(p, i0 + lane, a, e);
+      read(p, top + lane, a, e);
       const int runs = static_cast<int>((e - a + rows - 1) / rows);
       int64_t incl = runs;
 #pragma unroll
@@ -543,6 +544,10 @@ __device__ __forceinline__ void tile_to_tmem(uint32_t taddr, const uint8_t* tile
   }
 }
 
+// What a row's log-sum-exp adds to its exponents; a row that saw no key has no
+// probabilities.
+__device__ __forceinline__ float row_shift(float lse) { return lse == -INFINITY ? -INFINITY : -lse * kLog2e; }
+
 // The product of COLS columns from `first` of the thread's row of two tiles.
 template <int COLS>
 __device__ __forceinline__ float dot_tiles(const uint8_t* x, const uint8_t* y, int row, int first) {
@@ -617,7 +622,7 @@ __device__ __forceinline__ uint8_t* align1024(uint8_t* q) {
 // item blockIdx.x and then takes the next one from a counter of the launch, so
 // long and short items balance whatever their order; the last CTA to leave
 // clears the counters for the next launch with this slot.
-constexpr int kRcSlots = 64;
+constexpr int kRcSlots = 4096;
 __device__ int g_rc_items[2 * kRcSlots];
 struct ItemWalk {
   Units units;
@@ -1000,14 +1005,15 @@ __global__ void __launch_bounds__(kFwdThreads, 1) rc_fwd_kernel(const __grid_con
             m = mt;
           } else {
             const float mn = mt > m + 16.f ? mt : m;
-            const float f = ex2_ftz(m - mn);
+            const float f = m == mn ? 1.f : ex2_ftz(m - mn);  // (-infinity stays)
             l0 *= f;
             l1 *= f;
             m = mn;
             for (int c = ofirst; c < olast; c += 8) tmem_scale8(tO + c, f);
           }
         }
-        const float off = add - m;
+        // (a row that has seen no key yet: its bias is -infinity everywhere)
+        const float off = add - (m == -INFINITY ? 0.f : m);
         const uint64_t scl2 = pack2(mul, mul), off2 = pack2(off, off);
         uint64_t sum[2] = {pack2(l0, l1), 0ull};
 #pragma unroll
@@ -1052,7 +1058,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) rc_fwd_kernel(const __grid_con
           const int64_t token = static_cast<int64_t>(start) + row;
           __nv_bfloat16* out =
               static_cast<__nv_bfloat16*>(p.C) + token * p.ld_c + static_cast<int64_t>(head) * p.d + ofirst;
-          store_columns<DP / 2>(o, olast - ofirst, 1.f / l, out, p.wide);
+          store_columns<DP / 2>(o, olast - ofirst, l > 0.f ? 1.f / l : 0.f, out, p.wide);
           if (half == 0) p.lse[static_cast<int64_t>(head) * p.T + token] = (m + log2f(l)) * kLn2;
         }
         __syncwarp();
@@ -1257,7 +1263,7 @@ __global__ void __launch_bounds__(kDkvThreads, 1) rc_dkv_kernel(const __grid_con
         for (int x = 0; x < 4; ++x) {
           const int pos = 128 * q.i + 32 * x + lane;
           const int64_t at = static_cast<int64_t>(q.g) * p.T + k.start + pos;
-          nl[x] = pos < k.len ? -p.lse[at] * kLog2e : -INFINITY;
+          nl[x] = pos < k.len ? row_shift(p.lse[at]) : -INFINITY;
           nd[x] = pos < k.len ? -p.D[at] : 0.f;
         }
         if (!(ok = wait_warp(bar(L::vecempty + buf), ((it >> 1) & 1) ^ 1u, w))) break;
@@ -1810,7 +1816,7 @@ __global__ void __launch_bounds__(kDqThreads, 1) rc_dq_kernel(const __grid_const
       float nl = 0.f, nd = 0.f;
       if (mine) {
         const int64_t at = static_cast<int64_t>(head) * p.T + start + row;
-        nl = -p.lse[at] * kLog2e;
+        nl = row_shift(p.lse[at]);
       }
       // this warp's quarter of the columns of Q and dC into TMEM; the item before
       // has been through its products

@@ -109,7 +109,7 @@ class Case:
                 q, k = X[a:e, qc:qc + self.d], X[a:e, kc:kc + self.d]
                 big = max(big, sc * np.max(np.abs(q) @ np.abs(k).T))
                 top = max(top, sc * np.max(np.abs(q @ k.T)))
-        top += 0.0 if table is None else np.max(np.abs(table))
+        top += 0.0 if table is None else np.max(np.abs(table[np.isfinite(table)]))
         e_x = (self.d + 16) * 2.0 ** -23 * big + 2.0 ** -21 * (np.max(np.abs(lse[:, u]), initial=0) + top + 4)
         assert e_x < 2.0 ** -9  # small against bf16's half step, else the bounds say little
         return e_x, BF + e_x, (self.d + 16) * 2.0 ** -23, C, lse, A
@@ -523,3 +523,61 @@ def test_binding_refuses():
         tp.tp_attn_recompute_bwd(Q, c.cfg, C, lse, C, torch.empty_like(Q), torch.empty(8, dtype=torch.uint8, device="cuda"))
     assert e.value.status == tp.TP_ERR_WORKSPACE
     assert tp.tp_get_status() == tp.TP_OK
+
+
+# ----------------------------------------------------------------------------
+# buckets that hide keys, many sequences
+# ----------------------------------------------------------------------------
+@pytest.mark.parametrize("low", [float("-inf"), torch.finfo(torch.float32).min])
+@pytest.mark.parametrize("d", [64, 128])
+def test_buckets_that_hide_keys(low, d):
+    """-infinity (or the lowest fp32) in the last bucket: a window of max_distance keys.  The first key tiles of a
+    late row are hidden altogether."""
+    bias = dict(num_buckets=4, max_distance=60, bidirectional=False)
+    c = Case([500, 30], 2, 1, d, 1, True, bias=bias, seed=81)
+    c.table[3] = low
+    C, lse = c.fwd()
+    g, t = c.bwd(C, lse)
+    c.table[3] = float("-inf")
+    check(c, C, lse, g, t)
+    assert (t[3] == 0).all()
+
+
+@pytest.mark.parametrize("causal", [True, False])
+def test_rows_that_see_no_key(causal):
+    """Every bucket of one head hidden: zeros, lse of -infinity, no gradient; the other head is not touched by it."""
+    bias = dict(num_buckets=8, max_distance=20, bidirectional=True)
+    c = Case([200, 77], 2, 2, 64, 1, causal, bias=bias, seed=82)
+    C0, lse0 = c.fwd()
+    g0, t0 = c.bwd(C0, lse0)
+    c.table[:, 1] = float("-inf")
+    C, lse = c.fwd()
+    g, t = c.bwd(C, lse)
+    assert (C[:, 64:] == 0).all() and (lse[1] == float("-inf")).all() and (t[:, 1] == 0).all()
+    cols = lambda j: [slice(x, x + 64) for x in O.grouped_head_columns(64, 2, 2, 1, j)]  # noqa: E731
+    for a, b in zip(cols(0), cols(1)):
+        assert (g[:, b] == 0).all() and torch.equal(g[:, a], g0[:, a])
+    assert torch.equal(C[:, :64], C0[:, :64]) and torch.equal(lse[0], lse0[0]) and torch.equal(t[:, 0], t0[:, 0])
+
+
+def test_many_sequences():
+    """More sequences than a warp holds and than there are SMs, each of its own length, some empty: every one as if
+    it were alone."""
+    rng = np.random.default_rng(3)
+    lens = [int(x) for x in rng.integers(0, 200, 300)]
+    c = Case(lens, 4, 2, 64, 1, True, tail=5, seed=83)
+    C, lse = c.fwd()
+    g, _ = c.bwd(C, lse)
+    check(c, C, lse, g)
+
+
+def test_growing_scores():
+    """Each key tile's scores lie far above the one before: the exponents' reference moves at every tile."""
+    c = Case([640], 1, 1, 64, 1, False, scale=1.0, seed=84)
+    X = c.QKV.float()
+    X[:, :64] = 1.0 / 64
+    X[:, 64:128] = (torch.arange(640) // 128 * 30.0)[:, None] + X[:, 64:128] * 0.5
+    c.QKV = X.to(torch.bfloat16)
+    C, lse = c.fwd()
+    g, _ = c.bwd(C, lse)
+    check(c, C, lse, g)
