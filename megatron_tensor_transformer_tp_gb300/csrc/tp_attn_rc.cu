@@ -630,14 +630,14 @@ struct ItemWalk {
   int heads, index;  // index: head of the item
   bool first;
   __device__ __forceinline__ ItemWalk(const RcParams& p, int n, int rows, int lane)
-      : units(p, rows, lane), item(blockIdx.x), heads(n), index(0), first(true) {}
+      : units(p, rows, lane), item(blockIdx.x / p.parts), heads(n), index(0), first(true) {}
   // The next item that has rows, by a whole warp; false: there is none.
   // `zero`: an item without rows leaves that many zeros there.
   __device__ __forceinline__ bool next(const RcParams& p, bool last_first, int lane, Unit& u, float* zero = nullptr,
                                        int nzero = 0) {
     while (true) {
       if (!first) {
-        if (p.items <= gridDim.x) return false;  // an item each
+        if (p.items * p.parts <= gridDim.x) return false;  // an item each
         int v = 0;
         if (lane == 0) v = atomicAdd(g_rc_items + 2 * p.slot, 1);
         item = static_cast<int64_t>(gridDim.x) + __shfl_sync(0xffffffffu, v, 0);
@@ -680,7 +680,7 @@ __device__ __forceinline__ void leave(Head* hd) {
 template <int WARPS>
 __device__ __forceinline__ void leave(Head* hd, const RcParams& p) {
   leave<WARPS>(hd);
-  if (threadIdx.x == 0 && p.items > gridDim.x) {
+  if (threadIdx.x == 0 && p.items * p.parts > gridDim.x) {
     int* ctr = g_rc_items + 2 * p.slot;
     __threadfence();
     if (atomicAdd(ctr + 1, 1) == static_cast<int>(gridDim.x) - 1) {
@@ -1111,18 +1111,52 @@ struct DkvItem {
   int start, len, tile, head;  // head: the K/V head, -1: no more items
 };
 
-// The query tiles of a K/V head's key tile, head by head.
+// The query tiles of a K/V head's key tile, head by head; every `step`-th.
 struct QueryWalk {
-  int g, i, i0, nq;
+  int g, i, i0, nq, step;
+  __device__ __forceinline__ void skip(int n) {
+    i += n;
+    while (i >= nq) {
+      i -= nq - i0;
+      ++g;
+    }
+  }
   __device__ __forceinline__ void next() {
-    if (++i == nq) {
+    if (step > 1) {
+      skip(step);
+    } else if (++i == nq) {
       i = i0;
       ++g;
     }
   }
 };
 
-template <int DP, bool BIAS>
+// Cluster of the CTAs that share an item.
+__device__ __forceinline__ int cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return static_cast<int>(r);
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// 16 bytes at the same shared-memory address of CTA `rank`.
+__device__ __forceinline__ float4 ld_cluster4(uint32_t addr, int rank) {
+  float4 v;
+  asm volatile(
+      "{\n\t.reg .b32 a;\n\t"
+      "mapa.shared::cluster.u32 a, %4, %5;\n\t"
+      "ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [a];\n\t}"
+      : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+      : "r"(addr), "r"(rank)
+      : "memory");
+  return v;
+}
+
+// SPLIT: the CTAs of a cluster share an item, each with every p.parts-th query
+// tile.  Their sums meet in shared memory, where each CTA adds up its part of
+// the rows, in the order of the ranks.  For launches with fewer items than SMs.
+template <int DP, bool BIAS, bool SPLIT>
 __global__ void __launch_bounds__(kDkvThreads, 1) rc_dkv_kernel(const __grid_constant__ RcParams p) {
   using L = DkvShape<DP, BIAS>;
   extern __shared__ __align__(1024) uint8_t smem_wide[];
@@ -1155,8 +1189,13 @@ __global__ void __launch_bounds__(kDkvThreads, 1) rc_dkv_kernel(const __grid_con
   const uint32_t tS = tmem, tP = tmem + 128, tdV = tmem + 256, tdK = tmem + 256 + DP;
   struct Work {
     int start, len, kt, kvh, i0, nq, total;
-    __device__ __forceinline__ QueryWalk walk(const RcParams& p) const { return QueryWalk{kvh * p.group, i0, i0, nq}; }
+    __device__ __forceinline__ QueryWalk walk(const RcParams& p, int rank) const {
+      QueryWalk q{kvh * p.group, i0, i0, nq, SPLIT ? p.parts : 1};
+      if (SPLIT && total > 0) q.skip(rank);
+      return q;
+    }
   };
+  const int rank = SPLIT ? cluster_rank() : 0;
   auto work_of = [&](int start, int len, int tile, int head) {
     Work k;
     k.start = start;
@@ -1166,6 +1205,7 @@ __global__ void __launch_bounds__(kDkvThreads, 1) rc_dkv_kernel(const __grid_con
     k.nq = (len + 127) >> 7;
     k.i0 = p.causal ? tile : 0;
     k.total = (k.nq - k.i0) * p.group;  // (query head, query tile) pairs
+    if (SPLIT) k.total = (k.total - rank + p.parts - 1) / p.parts;  // (may be none)
     return k;
   };
   // the item in `slot`, once it is there
@@ -1198,7 +1238,7 @@ __global__ void __launch_bounds__(kDkvThreads, 1) rc_dkv_kernel(const __grid_con
       if (!found) break;
       const Work k = work_of(u.start, u.len, u.tile, items_of.index);
       const HeadAt hk = head_at(k.kvh, p.hk);
-      QueryWalk q = k.walk(p);
+      QueryWalk q = k.walk(p, rank);
       const int start = k.start, len = k.len;
       for (int i = 0; ok && i < k.total; ++i, ++it, q.next()) {
         const int sq = it % L::kQ, so = it % L::kO;
@@ -1255,7 +1295,7 @@ __global__ void __launch_bounds__(kDkvThreads, 1) rc_dkv_kernel(const __grid_con
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(L::free_ + slot));
       if (k.kvh < 0) break;
-      QueryWalk q = k.walk(p);
+      QueryWalk q = k.walk(p, rank);
       for (int i = 0; i < k.total; ++i, ++it, q.next()) {
         const int buf = it & 1;
         float nl[4], nd[4];
@@ -1298,6 +1338,7 @@ __global__ void __launch_bounds__(kDkvThreads, 1) rc_dkv_kernel(const __grid_con
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(L::free_ + slot));
       if (k.kvh < 0) break;
+      if (SPLIT && k.total <= 0) continue;
       if (!(ok = wait_warp(bar(L::kvfull), n & 1, w))) break;
       for (int i = -1; i < k.total; ++i) {
         const bool more = i + 1 < k.total;
@@ -1370,7 +1411,7 @@ __global__ void __launch_bounds__(kDkvThreads, 1) rc_dkv_kernel(const __grid_con
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(L::free_ + slot));
       if (k.kvh < 0) break;
-      QueryWalk q = k.walk(p);
+      QueryWalk q = k.walk(p, rank);
       const int kt = k.kt;
       for (int i = 0; i < k.total; ++i, ++it, q.next()) {
         const int buf = it & 1;
@@ -1480,18 +1521,33 @@ __global__ void __launch_bounds__(kDkvThreads, 1) rc_dkv_kernel(const __grid_con
         if (lane == 0) mbar_arrive(bar(L::vecempty + buf));
       }
       // dV by the first half of the warps, dK by the second; two warps share a row
-      ok = ok && wait_warp(bar(L::done), n & 1, w);
-      tc_fence_after();
-      const int which = part >> 1, cut = first_columns(p.d);
+      const int which = part >> 1, cut = SPLIT ? DP / 2 : first_columns(p.d);
       const int first = part & 1 ? cut : 0, cols = part & 1 ? p.d - cut : cut;
       uint32_t r[DP / 2];
+      if (SPLIT && k.total <= 0) {
 #pragma unroll
-      for (int c = 0; c < DP / 64; ++c) tmem_ld32_issue((which ? tdK : tdV) + lb + first + 32 * c, r + 32 * c);
+        for (int c = 0; c < DP / 2; ++c) r[c] = 0u;
+      } else {
+        ok = ok && wait_warp(bar(L::done), n & 1, w);
+        tc_fence_after();
 #pragma unroll
-      for (int c = 0; c < DP / 64; ++c) tmem_ld32_wait(r + 32 * c);
-      tc_fence_before();
+        for (int c = 0; c < DP / 64; ++c) tmem_ld32_issue((which ? tdK : tdV) + lb + first + 32 * c, r + 32 * c);
+#pragma unroll
+        for (int c = 0; c < DP / 64; ++c) tmem_ld32_wait(r + 32 * c);
+        tc_fence_before();
+      }
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(L::dfree));
+      if (SPLIT) {
+        // the Q and dC stages are done with: fp32 rows there, 16 bytes at a time and
+        // swizzled by the row
+        float4* row4 = reinterpret_cast<float4*>(sQ) + (128 * which + key) * (DP / 4);
+#pragma unroll
+        for (int c = 0; c < DP / 2; c += 4)
+          row4[((first + c) / 4) ^ (key & (DP / 4 - 1))] =
+              make_float4(as_f(r[c]), as_f(r[c + 1]), as_f(r[c + 2]), as_f(r[c + 3]));
+        continue;
+      }
       const int pos = 128 * kt + key;
       if (ok && pos < k.len) {
         const HeadAt hk = head_at(k.kvh, p.hk);
@@ -1504,6 +1560,36 @@ __global__ void __launch_bounds__(kDkvThreads, 1) rc_dkv_kernel(const __grid_con
       }
       __syncwarp();
     }
+  }
+  if (SPLIT) {
+    __syncwarp();
+    cluster_sync();
+    const int kvh = items[0].head;
+    if (kvh >= 0) {
+      const int start = items[0].start, len = items[0].len, kt = items[0].tile, rows = 128 / p.parts;
+      const HeadAt hk = head_at(kvh, p.hk);
+      for (int x = threadIdx.x; x < 2 * rows * (DP / 4); x += kDkvThreads) {
+        const int chunk = x % (DP / 4), row = rank * rows + x / (DP / 4) % rows, which = x / (DP / 4) / rows;
+        const int pos = 128 * kt + row;
+        if (4 * chunk >= p.d || pos >= len) continue;
+        const uint32_t at =
+            smem_addr(reinterpret_cast<float4*>(sQ) + (128 * which + row) * (DP / 4) + (chunk ^ (row & (DP / 4 - 1))));
+        float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int c = 0; c < p.parts; ++c) {
+          const float4 b = ld_cluster4(at, c);
+          a.x += b.x;
+          a.y += b.y;
+          a.z += b.z;
+          a.w += b.w;
+        }
+        const float mul = which ? p.scale : 1.f;
+        const int64_t col = static_cast<int64_t>(hk.shard) * p.shard_w + static_cast<int64_t>(p.hq) * p.d +
+                            static_cast<int64_t>(hk.local + (which ? 0 : p.hk)) * p.d + 4 * chunk;
+        *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.dQKV) + (static_cast<int64_t>(start) + pos) * p.ld_dqkv +
+                                  col) = make_uint2(pack_bf16x2(a.x * mul, a.y * mul), pack_bf16x2(a.z * mul, a.w * mul));
+      }
+    }
+    cluster_sync();
   }
   leave<kBwdWarps>(hd, p);
 }
@@ -2060,13 +2146,38 @@ int wide_rows(const RcParams& p, const void* out, int64_t ld, int shard_w) {
   return (reinterpret_cast<uintptr_t>(out) & 31u) == 0 && ld % 16 == 0 && p.d % 16 == 0 && shard_w % 16 == 0;
 }
 
+// CTAs that share an item of `tiles` tiles: where there are fewer items than SMs,
+// as many as clusters find room for at once (pairs and fours leave 8 SMs over,
+// eights 24), with two tiles each at least.  One sequence of 4096, 4 query heads
+// and 1 K/V head of 128: backward 201 us with one, 87 us with four for dK and dV.
+int cluster_parts(int64_t items, int64_t tiles, int num_sms) {
+  int parts = 1;
+  while (parts < 8 && 2 * parts * items <= num_sms - (parts < 4 ? 8 : 24) && tiles >= 4 * parts) parts *= 2;
+  return parts;
+}
+
+// In clusters of p.parts CTAs.
 template <class K>
 cudaError_t launch_rc(K kernel, int64_t blocks, int threads, int smem, const RcParams& p, cudaStream_t st) {
   const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  launch_k(kernel, dim3(static_cast<unsigned>(blocks)), dim3(threads), smem, st, p);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(blocks));
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = pdl_on() ? 1 : 0;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(p.parts);
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = p.parts > 1 ? 2 : 1;
+  const cudaError_t l = cudaLaunchKernelEx(&cfg, kernel, p);
   count_launches(1);
-  return cudaGetLastError();
+  return l != cudaSuccess ? l : cudaGetLastError();
 }
 
 // Runs of `rows` tokens: exactly, or for sequences that only the device knows
@@ -2101,6 +2212,7 @@ int query_tiles(const RcParams& p, int num_sms) {
 template <int DP, bool BIAS>
 cudaError_t fwd_t(RcParams& p, int num_sms, cudaStream_t st) {
   p.sub = query_tiles(p, num_sms);
+  p.parts = 1;
   p.items = units_of(p, 128 * p.sub) * p.H;
   p.slot = static_cast<int>(g_rc_slot_seq.fetch_add(1) % kRcSlots);
   p.wide = wide_rows(p, p.C, p.ld_c, 0);
@@ -2109,6 +2221,7 @@ cudaError_t fwd_t(RcParams& p, int num_sms, cudaStream_t st) {
 }
 template <int DP, bool BIAS>
 cudaError_t bwd_t(RcParams& p, int num_sms, cudaStream_t st) {
+  p.parts = 1;
   const int64_t units = units_of(p, 128);
   const int n = BIAS ? table_floats(p.bias.md) : 0;
   p.wide = wide_rows(p, p.dQKV, p.ld_dqkv, p.shard_w);
@@ -2124,8 +2237,17 @@ cudaError_t bwd_t(RcParams& p, int num_sms, cudaStream_t st) {
   p.items = units * p.KV;
   p.slot = static_cast<int>(g_rc_slot_seq.fetch_add(1) % kRcSlots);
   // (a table of floats and a byte a distance)
-  e = launch_rc(rc_dkv_kernel<DP, BIAS>, p.items < num_sms ? p.items : num_sms, kDkvThreads,
-                (DkvShape<DP, BIAS>::kSmem) + 5 * n, p, st);
+  const int dkv_smem = (DkvShape<DP, BIAS>::kSmem) + 5 * n;
+  // (by bounds that hold for any sequences, so that equal rows are summed in the
+  // same order whether they come by seq_starts or by s)
+  const int64_t bound = p.T / 128 + p.b;
+  p.parts = cluster_parts(bound * p.KV, bound / p.b * p.group, num_sms);
+  if (p.parts > 1) {
+    e = launch_rc(rc_dkv_kernel<DP, BIAS, true>, p.items * p.parts, kDkvThreads, dkv_smem, p, st);
+  } else {
+    e = launch_rc(rc_dkv_kernel<DP, BIAS, false>, p.items < num_sms ? p.items : num_sms, kDkvThreads, dkv_smem, p, st);
+  }
+  p.parts = 1;
   if (e != cudaSuccess || !BIAS || p.partial == nullptr) return e;
   launch_k(rc_bias_sum_kernel, dim3(p.H, p.bias.nb), dim3(128), 0, st, p, units);
   count_launches(1);
