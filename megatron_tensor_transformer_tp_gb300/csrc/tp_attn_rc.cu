@@ -690,6 +690,28 @@ __device__ __forceinline__ void leave(Head* hd, const RcParams& p) {
   }
 }
 
+// Cluster of the CTAs that share an item.
+__device__ __forceinline__ int cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return static_cast<int>(r);
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// 16 bytes at the same shared-memory address of CTA `rank`.
+__device__ __forceinline__ float4 ld_cluster4(uint32_t addr, int rank) {
+  float4 v;
+  asm volatile(
+      "{\n\t.reg .b32 a;\n\t"
+      "mapa.shared::cluster.u32 a, %4, %5;\n\t"
+      "ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [a];\n\t}"
+      : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+      : "r"(addr), "r"(rank)
+      : "memory");
+  return v;
+}
+
 // ===========================================================================
 // Forward
 // ===========================================================================
@@ -725,7 +747,11 @@ struct FwdShape {
 // Persistent: a CTA takes (query rows, head) items until there are none.  The
 // TMA warp runs ahead into the next item's loads, and its first scores are
 // computed while the last outputs are stored.
-template <int DP, bool BIAS>
+// SPLIT (for launches with fewer items than SMs): the CTAs of a cluster share an
+// item of one query tile, each with every p.parts-th key tile.  Their outputs,
+// references and sums meet in shared memory, where each CTA joins its part of
+// the rows, in the order of the ranks.
+template <int DP, bool BIAS, bool SPLIT>
 __global__ void __launch_bounds__(kFwdThreads, 1) rc_fwd_kernel(const __grid_constant__ RcParams p) {
   using L = FwdShape<DP>;
   extern __shared__ uint8_t smem_raw[];
@@ -752,6 +778,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1) rc_fwd_kernel(const __grid_con
   // scores: the next scores then wait for the softmax to have read the last ones
   // only, not for the product of its probabilities.
   constexpr bool kApart = DP == 64;
+  const int rank = SPLIT ? cluster_rank() : 0;
+  auto key_tile = [&](int j) { return SPLIT ? rank + j * p.parts : j; };  // the CTA's j-th
 
   if (warp == kFwdWarps + 2) {
     Flight fl;
@@ -775,6 +803,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) rc_fwd_kernel(const __grid_con
       for (int t = 0; t < 2; ++t) {
         const int r = row0 + 128 * t;
         n[t] = !found || t >= p.sub || r >= u.len ? 0 : p.causal ? min(nk_all, (r >> 7) + 1) : nk_all;
+        if (SPLIT) n[t] = max(0, n[t] - rank + p.parts - 1) / p.parts;  // (may be none)
       }
       if (lane == 0) {
         items[slot].start = u.start;
@@ -795,16 +824,17 @@ __global__ void __launch_bounds__(kFwdThreads, 1) rc_fwd_kernel(const __grid_con
         load_tile<DP>(smem_addr(sQ + t * L::kTile), &p.mapQ, bar(L::qfull + t), start + row0 + 128 * t, hq);
         return true;
       };
-      if (lane == 0) ok = load_q(0);
-      for (int j = 0; j < nmax; ++j, ++c) {
-        const int st = c % L::kStages;
+      if (lane == 0 && n[0] > 0) ok = load_q(0);
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+      for (int j = 0; ok && j < nmax; ++j, ++c) {
+        const int st = c % L::kStages, jk = key_tile(j);
         const uint32_t ph = (c / L::kStages) & 1;
         if (lane == 0) {
           ok = ok && wait_bounded(bar(L::kempty + st), ph ^ 1u, w);
           if (ok && !skip) {
             mbar_arrive_expect_tx(bar(L::kfull + st), L::kTile);
             fl.note(L::kfull + st, ph);
-            load_tile<DP>(smem_addr(sK + st * L::kTile), &p.mapK, bar(L::kfull + st), start + 128 * j, hk);
+            load_tile<DP>(smem_addr(sK + st * L::kTile), &p.mapK, bar(L::kfull + st), start + 128 * jk, hk);
           }
           skip = false;
           if (ok && j == 0 && n[1] > 0) ok = load_q(1);
@@ -812,14 +842,14 @@ __global__ void __launch_bounds__(kFwdThreads, 1) rc_fwd_kernel(const __grid_con
         }
         ok = __shfl_sync(0xffffffffu, ok, 0);
         if (!ok) break;
-        if (128 * j + 128 > len && start + len < p.T) {
+        if (128 * jk + 128 > len && start + len < p.T) {
           ok = load_tail<DP>(sV + st * L::kTile, &p.mapV, bar(L::vfull + st), bar(L::tail), tail_phase,
-                             start + 128 * j, hk, len - 128 * j, lane, w);
+                             start + 128 * jk, hk, len - 128 * jk, lane, w);
           if (!ok) break;
         } else if (lane == 0) {
           mbar_arrive_expect_tx(bar(L::vfull + st), L::kTile);
           fl.note(L::vfull + st, ph);
-          load_tile<DP>(smem_addr(sV + st * L::kTile), &p.mapV, bar(L::vfull + st), start + 128 * j, hk);
+          load_tile<DP>(smem_addr(sV + st * L::kTile), &p.mapV, bar(L::vfull + st), start + 128 * jk, hk);
         }
       }
       nq[0] += n[0] > 0;
@@ -962,10 +992,10 @@ __global__ void __launch_bounds__(kFwdThreads, 1) rc_fwd_kernel(const __grid_con
           __syncwarp();
           if (lane == 0) mbar_arrive(bar(L::sread + t));
         }
-        const int c0 = 128 * j + 64 * half, r0 = row0 + 128 * t;
+        const int jk = key_tile(j), c0 = 128 * jk + 64 * half, r0 = row0 + 128 * t;
         float mul = sl2, add = 0.f;  // x = s mul + add
         if (BIAS) {
-          const int side = bias_side(p.bias.md, r0, 128 * j);
+          const int side = bias_side(p.bias.md, r0, 128 * jk);
           if (side != 0) {
             add = tab[side < 0 ? 0 : 2 * (p.bias.md + kPad)];
           } else {
@@ -975,7 +1005,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) rc_fwd_kernel(const __grid_con
             mul = 1.f;
           }
         }
-        if ((p.causal && 128 * j + 127 > r0) || 128 * j + 128 > len) {
+        if ((p.causal && 128 * jk + 127 > r0) || 128 * jk + 128 > len) {
           const int seen = (p.causal ? min(len, row + 1) : len) - c0;  // columns this row sees
 #pragma unroll
           for (int c = 0; c < 64; ++c) s[c] = c < seen ? s[c] : 0xff800000u;
@@ -1047,13 +1077,29 @@ __global__ void __launch_bounds__(kFwdThreads, 1) rc_fwd_kernel(const __grid_con
         ok = ok && wait_warp(bar(L::odone + t), nq & 1, w);
         tc_fence_after();
         uint32_t o[64];
-        tmem_ld32_issue(tO + ofirst, o);
-        tmem_ld32_issue(tO + ofirst + (DP == 128 ? 32 : 0), o + 32);
+        const int from = SPLIT ? DP / 2 * half : ofirst;
+        tmem_ld32_issue(tO + from, o);
+        tmem_ld32_issue(tO + from + (DP == 128 ? 32 : 0), o + 32);
         tmem_ld32_wait(o);
         tmem_ld32_wait(o + 32);
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(L::ofree + t));
+        if (SPLIT) {
+          // the Q, K and V stages are done with: fp32 rows there, 16 bytes at a time
+          // and swizzled by the row
+          const int r = quarter * 32 + lane;
+          float4* row4 = reinterpret_cast<float4*>(sQ) + r * (DP / 4);
+#pragma unroll
+          for (int c = 0; c < DP / 2; c += 4)
+            row4[((DP / 2 * half + c) / 4) ^ (r & (DP / 4 - 1))] =
+                make_float4(as_f(o[c]), as_f(o[c + 1]), as_f(o[c + 2]), as_f(o[c + 3]));
+          if (half == 0) {
+            part[2 * r] = m;
+            part[2 * r + 1] = l;
+          }
+          continue;
+        }
         if (ok && row < len) {
           const int64_t token = static_cast<int64_t>(start) + row;
           __nv_bfloat16* out =
@@ -1063,8 +1109,57 @@ __global__ void __launch_bounds__(kFwdThreads, 1) rc_fwd_kernel(const __grid_con
         }
         __syncwarp();
         ++nq;
+      } else if (SPLIT && t == 0) {
+        // no key tile for this CTA: nothing to add
+        const int r = quarter * 32 + lane;
+        float4* row4 = reinterpret_cast<float4*>(sQ) + r * (DP / 4);
+#pragma unroll
+        for (int c = 0; c < DP / 2; c += 4) row4[(DP / 2 * half + c) / 4] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (half == 0) {
+          part[2 * r] = -INFINITY;
+          part[2 * r + 1] = 0.f;
+        }
       }
     }
+  }
+  if (SPLIT) {
+    __syncwarp();
+    cluster_sync();
+    const int head = items[0].head;
+    if (head >= 0) {
+      const int start = items[0].start, len = items[0].len, row0 = items[0].row0, rows = 128 / p.parts;
+      for (int x = threadIdx.x; x < rows * (DP / 4); x += kFwdThreads) {
+        const int chunk = x % (DP / 4), r = rank * rows + x / (DP / 4), row = row0 + r;
+        if (4 * chunk >= p.d || row >= len) continue;
+        const uint32_t at =
+            smem_addr(reinterpret_cast<float4*>(sQ) + r * (DP / 4) + (chunk ^ (r & (DP / 4 - 1))));
+        const uint32_t ml = smem_addr(part + 4 * (r >> 1));  // (m, l) of rows r & ~1 and r | 1
+        float top = -INFINITY;
+        for (int c = 0; c < p.parts; ++c) {
+          const float4 v = ld_cluster4(ml, c);
+          top = fmaxf(top, r & 1 ? v.z : v.x);
+        }
+        float l = 0.f;
+        float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int c = 0; c < p.parts; ++c) {
+          const float4 v = ld_cluster4(ml, c), b = ld_cluster4(at, c);
+          const float mc = r & 1 ? v.z : v.x;
+          const float f = mc == top ? 1.f : ex2_ftz(mc - top);
+          l = fmaf(r & 1 ? v.w : v.y, f, l);
+          a.x = fmaf(b.x, f, a.x);
+          a.y = fmaf(b.y, f, a.y);
+          a.z = fmaf(b.z, f, a.z);
+          a.w = fmaf(b.w, f, a.w);
+        }
+        const float mul = l > 0.f ? 1.f / l : 0.f;
+        const int64_t token = static_cast<int64_t>(start) + row;
+        *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.C) + token * p.ld_c + static_cast<int64_t>(head) * p.d +
+                                  4 * chunk) =
+            make_uint2(pack_bf16x2(a.x * mul, a.y * mul), pack_bf16x2(a.z * mul, a.w * mul));
+        if (chunk == 0) p.lse[static_cast<int64_t>(head) * p.T + token] = (top + log2f(l)) * kLn2;
+      }
+    }
+    cluster_sync();
   }
   leave<kFwdWarps>(hd, p);
 }
@@ -1130,28 +1225,6 @@ struct QueryWalk {
     }
   }
 };
-
-// Cluster of the CTAs that share an item.
-__device__ __forceinline__ int cluster_rank() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return static_cast<int>(r);
-}
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-// 16 bytes at the same shared-memory address of CTA `rank`.
-__device__ __forceinline__ float4 ld_cluster4(uint32_t addr, int rank) {
-  float4 v;
-  asm volatile(
-      "{\n\t.reg .b32 a;\n\t"
-      "mapa.shared::cluster.u32 a, %4, %5;\n\t"
-      "ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [a];\n\t}"
-      : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-      : "r"(addr), "r"(rank)
-      : "memory");
-  return v;
-}
 
 // SPLIT: the CTAs of a cluster share an item, each with every p.parts-th query
 // tile.  Their sums meet in shared memory, where each CTA adds up its part of
@@ -2211,13 +2284,16 @@ int query_tiles(const RcParams& p, int num_sms) {
 
 template <int DP, bool BIAS>
 cudaError_t fwd_t(RcParams& p, int num_sms, cudaStream_t st) {
-  p.sub = query_tiles(p, num_sms);
-  p.parts = 1;
-  p.items = units_of(p, 128 * p.sub) * p.H;
-  p.slot = static_cast<int>(g_rc_slot_seq.fetch_add(1) % kRcSlots);
-  p.wide = wide_rows(p, p.C, p.ld_c, 0);
   const int smem = FwdShape<DP>::kSmem + (BIAS ? 9 * table_floats(p.bias.md) + 4 * kMaxRelBuckets : 0);
-  return launch_rc(rc_fwd_kernel<DP, BIAS>, p.items < num_sms ? p.items : num_sms, kFwdThreads, smem, p, st);
+  p.wide = wide_rows(p, p.C, p.ld_c, 0);
+  p.slot = static_cast<int>(g_rc_slot_seq.fetch_add(1) % kRcSlots);
+  // (by a bound that holds for any sequences, as for dK and dV)
+  const int64_t bound = p.T / 128 + p.b;
+  p.parts = cluster_parts(bound * p.H, bound / p.b, num_sms);
+  p.sub = p.parts > 1 ? 1 : query_tiles(p, num_sms);
+  p.items = units_of(p, 128 * p.sub) * p.H;
+  if (p.parts > 1) return launch_rc(rc_fwd_kernel<DP, BIAS, true>, p.items * p.parts, kFwdThreads, smem, p, st);
+  return launch_rc(rc_fwd_kernel<DP, BIAS, false>, p.items < num_sms ? p.items : num_sms, kFwdThreads, smem, p, st);
 }
 template <int DP, bool BIAS>
 cudaError_t bwd_t(RcParams& p, int num_sms, cudaStream_t st) {
