@@ -1704,7 +1704,9 @@ __host__ __device__ constexpr int grad_floats(int md) {
   return 2 * kBwdWarps * kDiag + 2 * md + 1 + 2 * kBwdWarps + kMaxRelBuckets;
 }
 
-template <int DP, bool BIAS>
+// SPLIT: as for dK and dV, with every p.parts-th key tile (not with a bias, whose
+// gradient's sums are an item's).
+template <int DP, bool BIAS, bool SPLIT>
 __global__ void __launch_bounds__(kDqThreads, 1) rc_dq_kernel(const __grid_constant__ RcParams p) {
   using L = DqShape<DP, BIAS>;
   extern __shared__ uint8_t smem_raw[];
@@ -1739,6 +1741,9 @@ __global__ void __launch_bounds__(kDqThreads, 1) rc_dq_kernel(const __grid_const
   const uint32_t tP = tmem + 128, tdQ = tmem + (kAhead ? 384 : 256), tQ = tmem + (kAhead ? 448 : 384),
                  tO = tmem + (kAhead ? 480 : 448);
 
+  const int rank = SPLIT ? cluster_rank() : 0;
+  auto key_tile = [&](int j) { return SPLIT ? rank + j * p.parts : j; };  // the CTA's j-th
+
   if (warp == kBwdWarps + 1) {
     Flight fl;
     uint32_t tail_phase = 0;
@@ -1756,7 +1761,9 @@ __global__ void __launch_bounds__(kDqThreads, 1) rc_dq_kernel(const __grid_const
       Unit u{0, 0, 0};
       const bool found = items_of.next(p, p.causal != 0, lane, u, grad ? p.partial : nullptr, p.bias.nb);
       if (!(ok = wait_warp(bar(L::free_ + slot), ((n >> 1) & 1) ^ 1, w))) break;
-      const int nk_all = (u.len + 127) >> 7, nk = p.causal ? min(nk_all, u.tile + 1) : nk_all;
+      const int nk_all = (u.len + 127) >> 7;
+      int nk = p.causal ? min(nk_all, u.tile + 1) : nk_all;
+      if (SPLIT) nk = max(0, nk - rank + p.parts - 1) / p.parts;  // (may be none)
       if (lane == 0) {
         items[slot].start = u.start;
         items[slot].len = u.len;
@@ -1767,6 +1774,7 @@ __global__ void __launch_bounds__(kDqThreads, 1) rc_dq_kernel(const __grid_const
         mbar_arrive(bar(L::info + slot));
       }
       if (!found) break;
+      if (SPLIT && nk == 0) continue;
       const HeadAt hq = head_at(items_of.index, p.hq), hk = head_at(items_of.index / p.group, p.hk);
       // Q and dC pass through a K and a V stage on their way to TMEM
       if (lane == 0) {
@@ -1800,19 +1808,19 @@ __global__ void __launch_bounds__(kDqThreads, 1) rc_dq_kernel(const __grid_const
       ok = __shfl_sync(0xffffffffu, ok, 0);
       kr.next();
       for (int j = 0; ok && j < nk; ++j, kr.next(), vr.next()) {
-        const int st = kr.stage, sv = vr.stage;
+        const int st = kr.stage, sv = vr.stage, jk = key_tile(j);
         const uint32_t ph = kr.phase;
         if (lane == 0) ok = wait_bounded(bar(L::kempty + st), ph ^ 1u, w);
         ok = __shfl_sync(0xffffffffu, ok, 0);
         if (!ok) break;
-        if (128 * j + 128 > u.len && u.start + u.len < p.T) {
+        if (128 * jk + 128 > u.len && u.start + u.len < p.T) {
           ok = load_tail<DP>(sK + st * L::kTile, &p.mapK, bar(L::kfull + st), bar(L::tail), tail_phase,
-                             u.start + 128 * j, hk, u.len - 128 * j, lane, w);
+                             u.start + 128 * jk, hk, u.len - 128 * jk, lane, w);
           if (!ok) break;
         } else if (lane == 0 && !skip) {
           mbar_arrive_expect_tx(bar(L::kfull + st), L::kTile);
           fl.note(L::kfull + st, ph);
-          load_tile<DP>(smem_addr(sK + st * L::kTile), &p.mapK, bar(L::kfull + st), u.start + 128 * j, hk);
+          load_tile<DP>(smem_addr(sK + st * L::kTile), &p.mapK, bar(L::kfull + st), u.start + 128 * jk, hk);
         }
         skip = false;
         if (lane == 0) {
@@ -1820,7 +1828,7 @@ __global__ void __launch_bounds__(kDqThreads, 1) rc_dq_kernel(const __grid_const
           if (ok) {
             mbar_arrive_expect_tx(bar(L::vfull + sv), L::kTile);
             fl.note(L::vfull + sv, vr.phase);
-            load_tile<DP>(smem_addr(sV + sv * L::kTile), &p.mapV, bar(L::vfull + sv), u.start + 128 * j, hk);
+            load_tile<DP>(smem_addr(sV + sv * L::kTile), &p.mapV, bar(L::vfull + sv), u.start + 128 * jk, hk);
           }
         }
         ok = __shfl_sync(0xffffffffu, ok, 0);
@@ -1876,6 +1884,7 @@ __global__ void __launch_bounds__(kDqThreads, 1) rc_dq_kernel(const __grid_const
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(L::free_ + slot));
       if (end) break;
+      if (SPLIT && nk == 0) continue;
       // Q and dC are in TMEM: Q's stage is free again
       if (!(ok = wait_warp(bar(L::qfull), n & 1, w))) break;
       if (lane == 0) mbar_arrive(bar(L::kempty + kr.stage));
@@ -1969,6 +1978,14 @@ __global__ void __launch_bounds__(kDqThreads, 1) rc_dq_kernel(const __grid_const
       }
       const int start = uniform(items[slot].start), len = uniform(items[slot].len), r0 = uniform(items[slot].r0);
       const int nk = uniform(items[slot].nk);
+      float4* row4 = reinterpret_cast<float4*>(sK) + (quarter * 32 + lane) * (DP / 4);  // SPLIT: the row's sums
+      if (SPLIT && nk == 0) {
+        // no key tile for this CTA: nothing to add
+#pragma unroll
+        for (int c = 0; c < DP / 16; ++c) row4[DP / 16 * part + c] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (lane == 0) mbar_arrive(bar(L::free_ + slot));
+        continue;
+      }
       const int row = r0 + quarter * 32 + lane;
       const bool mine = row < len;
       const float* tab = tabs + slot * tabn;
@@ -2001,7 +2018,7 @@ __global__ void __launch_bounds__(kDqThreads, 1) rc_dq_kernel(const __grid_const
           mbar_arrive(bar(L::vempty + sv));
         }
         const float D = (dots[r] + dots[128 + r]) + (dots[256 + r] + dots[384 + r]);
-        if (part == 0 && mine) p.D[static_cast<int64_t>(head) * p.T + start + row] = D;
+        if (part == 0 && mine && rank == 0) p.D[static_cast<int64_t>(head) * p.T + start + row] = D;
         nd = -D;
       }
       const uint64_t nd2 = pack2(nd, nd);
@@ -2013,13 +2030,13 @@ __global__ void __launch_bounds__(kDqThreads, 1) rc_dq_kernel(const __grid_const
       float end_lo = 0.f, end_hi = 0.f;  // dS at distances <= -md and >= md, of the tile sums
       uint64_t far_lo = 0, far_hi = 0;   // and of this row in tiles all beyond an end
       for (int j = 0; j < nk; ++j, ++nt) {
-        const int c0 = 128 * j + 32 * part;  // key position of this warp's first column
+        const int jk = key_tile(j), c0 = 128 * jk + 32 * part;  // key position of this warp's first column
         const uint32_t tPj = tP + lb + 32 * part + (kAhead && (nt & 1) ? 128 : 0);
         int side = 0;
         float off = nl;
         const float* tb = nullptr;
         if (BIAS) {
-          side = bias_side(md, r0, 128 * j);
+          side = bias_side(md, r0, 128 * jk);
           if (side != 0) off += tab[side < 0 ? 0 : 2 * (md + kPad)];
           tb = tab + (c0 - row + md + kPad);
         }
@@ -2049,7 +2066,7 @@ __global__ void __launch_bounds__(kDqThreads, 1) rc_dq_kernel(const __grid_const
             s[c + 1] = __float_as_uint(ex2_ftz(x1));
           }
         }
-        const bool masked = (p.causal && 128 * j + 127 > r0) || 128 * j + 128 > len;
+        const bool masked = (p.causal && 128 * jk + 127 > r0) || 128 * jk + 128 > len;
         if (!kAhead) {
           ok = ok && wait_warp(bar(L::dpfull), nt & 1, w);
           tc_fence_after();
@@ -2128,7 +2145,7 @@ __global__ void __launch_bounds__(kDqThreads, 1) rc_dq_kernel(const __grid_const
                 if (qu + k >= 0 && qu + k < 4) sum += dt_sums[(4 * (qu + k) + qu) * kDiag + at];
                 if (qu + k >= 1 && qu + k < 5 && at < 31) sum += dt_sums[(4 * (qu + k - 1) + qu) * kDiag + at + 32];
               }
-              const int delta = 128 * j - r0 + dt;
+              const int delta = 128 * jk - r0 + dt;
               if (delta <= -md) end_lo += sum;
               else if (delta >= md) end_hi += sum;
               else bins[delta + md] += sum;
@@ -2142,13 +2159,21 @@ __global__ void __launch_bounds__(kDqThreads, 1) rc_dq_kernel(const __grid_const
         uint32_t r[32];
         tmem_ld32_issue(tdQ + lb + 32 * min(part, DP / 32 - 1), r);
         tmem_ld32_wait(r);
-        pack_columns<32>(r, p.scale, dq);
+        if (SPLIT && part < DP / 32) {
+          // the K and V stages are done with: fp32 rows there, 16 bytes at a time and
+          // swizzled by the row
+#pragma unroll
+          for (int c = 0; c < 32; c += 4)
+            row4[(8 * part + c / 4) ^ (lane & (DP / 4 - 1))] =
+                make_float4(as_f(r[c]), as_f(r[c + 1]), as_f(r[c + 2]), as_f(r[c + 3]));
+        }
+        if (!SPLIT) pack_columns<32>(r, p.scale, dq);
       }
       tc_fence_before();
       const HeadAt hq = head_at(uniform(items[slot].head), p.hq);
       prev = static_cast<__nv_bfloat16*>(p.dQKV) + (static_cast<int64_t>(items[slot].start) + row) * p.ld_dqkv +
              static_cast<int64_t>(hq.shard) * p.shard_w + static_cast<int64_t>(hq.local) * p.d + ofirst;
-      if (!ok || !mine || ocols <= 0) prev = nullptr;
+      if (SPLIT || !ok || !mine || ocols <= 0) prev = nullptr;
       if (BIAS && grad) {
         // the item's sums by bucket, in a fixed order: a warp a bucket
         constexpr int kN = 32 * kBwdWarps;
@@ -2190,6 +2215,33 @@ __global__ void __launch_bounds__(kDqThreads, 1) rc_dq_kernel(const __grid_const
       if (lane == 0) mbar_arrive(bar(L::free_ + slot));
     }
   }
+  if (SPLIT) {
+    __syncwarp();
+    cluster_sync();
+    const int head = items[0].head;
+    if (head >= 0) {
+      const int start = items[0].start, len = items[0].len, r0 = items[0].r0, rows = 128 / p.parts;
+      const HeadAt hq = head_at(head, p.hq);
+      for (int x = threadIdx.x; x < rows * (DP / 4); x += kDqThreads) {
+        const int chunk = x % (DP / 4), r = rank * rows + x / (DP / 4), row = r0 + r;
+        if (4 * chunk >= p.d || row >= len) continue;
+        const uint32_t at = smem_addr(reinterpret_cast<float4*>(sK) + r * (DP / 4) + (chunk ^ (r & 31 & (DP / 4 - 1))));
+        float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int c = 0; c < p.parts; ++c) {
+          const float4 b = ld_cluster4(at, c);
+          a.x += b.x;
+          a.y += b.y;
+          a.z += b.z;
+          a.w += b.w;
+        }
+        const int64_t col = static_cast<int64_t>(hq.shard) * p.shard_w + static_cast<int64_t>(hq.local) * p.d + 4 * chunk;
+        *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.dQKV) + (static_cast<int64_t>(start) + row) * p.ld_dqkv +
+                                  col) =
+            make_uint2(pack_bf16x2(a.x * p.scale, a.y * p.scale), pack_bf16x2(a.z * p.scale, a.w * p.scale));
+      }
+    }
+    cluster_sync();
+  }
   leave<kBwdWarps>(hd, p);
 }
 
@@ -2221,11 +2273,13 @@ int wide_rows(const RcParams& p, const void* out, int64_t ld, int shard_w) {
 
 // CTAs that share an item of `tiles` tiles: where there are fewer items than SMs,
 // as many as clusters find room for at once (pairs and fours leave 8 SMs over,
-// eights 24), with two tiles each at least.  One sequence of 4096, 4 query heads
-// and 1 K/V head of 128: backward 201 us with one, 87 us with four for dK and dV.
-int cluster_parts(int64_t items, int64_t tiles, int num_sms) {
+// eights 24), with more than `least` tiles each.  One sequence of 4096, 4 query
+// heads and 1 K/V head of 128: backward 201 us with one, 87 us with four for dK
+// and dV; 2 heads of 128: forward 41 us with one, 27 us with two.  With 4 or 8
+// tiles an item in all, two take a microsecond longer than one in the forward.
+int cluster_parts(int64_t items, int64_t tiles, int least, int num_sms) {
   int parts = 1;
-  while (parts < 8 && 2 * parts * items <= num_sms - (parts < 4 ? 8 : 24) && tiles >= 4 * parts) parts *= 2;
+  while (parts < 8 && 2 * parts * items <= num_sms - (parts < 4 ? 8 : 24) && tiles > least * parts) parts *= 2;
   return parts;
 }
 
@@ -2289,7 +2343,7 @@ cudaError_t fwd_t(RcParams& p, int num_sms, cudaStream_t st) {
   p.slot = static_cast<int>(g_rc_slot_seq.fetch_add(1) % kRcSlots);
   // (by a bound that holds for any sequences, as for dK and dV)
   const int64_t bound = p.T / 128 + p.b;
-  p.parts = cluster_parts(bound * p.H, bound / p.b, num_sms);
+  p.parts = cluster_parts(bound * p.H, bound / p.b, 8, num_sms);
   p.sub = p.parts > 1 ? 1 : query_tiles(p, num_sms);
   p.items = units_of(p, 128 * p.sub) * p.H;
   if (p.parts > 1) return launch_rc(rc_fwd_kernel<DP, BIAS, true>, p.items * p.parts, kFwdThreads, smem, p, st);
@@ -2305,24 +2359,25 @@ cudaError_t bwd_t(RcParams& p, int num_sms, cudaStream_t st) {
   p.items = units * p.H;
   p.slot = static_cast<int>(g_rc_slot_seq.fetch_add(1) % kRcSlots);
   // (two tables of floats, a head's values, a byte a distance, the sums)
-  cudaError_t e =
-      launch_rc(rc_dq_kernel<DP, BIAS>, p.items < num_sms ? p.items : num_sms, kDqThreads,
-                (DqShape<DP, BIAS>::kSmem) + 9 * n + (BIAS ? 4 * (kMaxRelBuckets + grad_floats(p.bias.md)) : 0), p, st);
+  const int dq_smem =
+      (DqShape<DP, BIAS>::kSmem) + 9 * n + (BIAS ? 4 * (kMaxRelBuckets + grad_floats(p.bias.md)) : 0);
+  // (clusters by bounds that hold for any sequences, so that equal rows are summed
+  // in the same order whether they come by seq_starts or by s)
+  const int64_t bound = p.T / 128 + p.b;
+  if (!BIAS) p.parts = cluster_parts(bound * p.H, bound / p.b, 8, num_sms);
+  const auto dq = p.parts > 1 ? rc_dq_kernel<DP, BIAS, !BIAS> : rc_dq_kernel<DP, BIAS, false>;
+  cudaError_t e = launch_rc(dq, p.parts > 1 ? p.items * p.parts : p.items < num_sms ? p.items : num_sms, kDqThreads,
+                            dq_smem, p, st);
   p.fault_skip = 0;
   if (e != cudaSuccess) return e;
   p.items = units * p.KV;
   p.slot = static_cast<int>(g_rc_slot_seq.fetch_add(1) % kRcSlots);
   // (a table of floats and a byte a distance)
   const int dkv_smem = (DkvShape<DP, BIAS>::kSmem) + 5 * n;
-  // (by bounds that hold for any sequences, so that equal rows are summed in the
-  // same order whether they come by seq_starts or by s)
-  const int64_t bound = p.T / 128 + p.b;
-  p.parts = cluster_parts(bound * p.KV, bound / p.b * p.group, num_sms);
-  if (p.parts > 1) {
-    e = launch_rc(rc_dkv_kernel<DP, BIAS, true>, p.items * p.parts, kDkvThreads, dkv_smem, p, st);
-  } else {
-    e = launch_rc(rc_dkv_kernel<DP, BIAS, false>, p.items < num_sms ? p.items : num_sms, kDkvThreads, dkv_smem, p, st);
-  }
+  p.parts = cluster_parts(bound * p.KV, bound / p.b * p.group, 4, num_sms);
+  const auto dkv = p.parts > 1 ? rc_dkv_kernel<DP, BIAS, true> : rc_dkv_kernel<DP, BIAS, false>;
+  e = launch_rc(dkv, p.parts > 1 ? p.items * p.parts : p.items < num_sms ? p.items : num_sms, kDkvThreads, dkv_smem, p,
+                st);
   p.parts = 1;
   if (e != cudaSuccess || !BIAS || p.partial == nullptr) return e;
   launch_k(rc_bias_sum_kernel, dim3(p.H, p.bias.nb), dim3(128), 0, st, p, units);

@@ -581,3 +581,114 @@ def test_growing_scores():
     C, lse = c.fwd()
     g, _ = c.bwd(C, lse)
     check(c, C, lse, g)
+
+
+# ----------------------------------------------------------------------------
+# few heads and long sequences: clusters of CTAs share a tile's work.  (On 152 SMs
+# the forward, dQ, and dK with dV take as many CTAs an item as stands beside.)
+# ----------------------------------------------------------------------------
+FEW = [  # lens, query heads, key/value heads, d, shards, causal, tail
+    ([2100], 1, 1, 128, 1, True, 0),        # 4, 4, 4: the first rows' items have less tiles than CTAs
+    ([2100], 1, 1, 64, 1, False, 0),        # 4, 4, 4
+    ([600], 8, 1, 128, 1, True, 0),         # 1, 1, 8
+    ([600], 6, 1, 64, 1, False, 3),         # 1, 1, 8: 30 query tiles by 8 CTAs
+    ([1290], 3, 1, 96, 1, True, 0),         # 2, 2, 8
+    ([1700], 2, 2, 40, 2, True, 0),         # 2, 2, 4
+    ([2700, 0], 1, 1, 128, 1, False, 130),  # an empty one, rows behind: 2, 2, 4
+    ([1800, 900], 2, 1, 72, 1, True, 0),    # 2, 2, 4
+]
+
+
+@pytest.mark.parametrize("lens,H,KV,d,N,causal,tail", FEW)
+def test_few_heads(lens, H, KV, d, N, causal, tail):
+    run(Case(lens, H, KV, d, N, causal, tail=tail, seed=91 + d))
+
+
+@pytest.mark.parametrize("lens,H,KV,d,causal,nb,md,both", [
+    ([2100], 1, 1, 128, True, 32, 128, False),
+    ([2100], 1, 1, 64, False, 32, 128, True),
+    ([1290], 2, 1, 64, False, 64, 1024, True),
+    ([600], 8, 1, 96, True, 8, 20, True),
+])
+def test_few_heads_with_a_bias(lens, H, KV, d, causal, nb, md, both):
+    run(Case(lens, H, KV, d, 1, causal, 1.0, bias=dict(num_buckets=nb, max_distance=md, bidirectional=both), seed=92 + d))
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_few_heads_and_hidden_buckets(d):
+    """A window of 60 keys: of the CTAs that share a tile, some see no key of a row; and all of them, where every
+    bucket is hidden."""
+    bias = dict(num_buckets=4, max_distance=60, bidirectional=False)
+    c = Case([2000], 1, 1, d, 1, True, bias=bias, seed=93)
+    c.table[3] = float("-inf")
+    C, lse = c.fwd()
+    g, t = c.bwd(C, lse)
+    check(c, C, lse, g, t)
+    assert (t[3] == 0).all()
+    c.table[:] = float("-inf")
+    C, lse = c.fwd()
+    g, t = c.bwd(C, lse)
+    assert (C == 0).all() and (lse == float("-inf")).all() and (g == 0).all() and (t == 0).all()
+
+
+def test_few_heads_neighbours_bits_and_graph():
+    """Rows beside the sequences that are not numbers, equal calls, a table's gradient left out, another stream, and
+    a captured graph that is replayed: the same bits."""
+    tp = _tp()
+    for bias in (None, BIAS):
+        c = Case([1150, 1200], 2, 1, 128, 1, True, tail=60, head=20, bias=bias, seed=94)
+        C, lse = c.fwd()
+        g, t = c.bwd(C, lse)
+        for bad in (float("nan"), float("inf")):
+            Q, dC, C2, l2 = c.QKV.cuda(), c.dC.cuda(), C.clone(), lse.clone()
+            for x in (Q, dC, C2):
+                x[:20] = bad
+                x[2370:] = bad
+            l2[:, :20] = bad
+            l2[:, 2370:] = bad
+            fC, fl = c.fwd(Q)
+            g2, _ = c.bwd(C2, l2, Q, dC)
+            assert torch.equal(fC, C) and torch.equal(fl, lse) and torch.equal(g2, g)
+        if bias:
+            assert torch.equal(c.bwd(C, lse, dtable=None)[0], g)
+        st = torch.cuda.Stream()
+        torch.cuda.synchronize()
+        with torch.cuda.stream(st):
+            C2, lse2 = c.fwd()
+            g2, _ = c.bwd(C2, lse2)
+        st.synchronize()
+        assert torch.equal(C2, C) and torch.equal(lse2, lse) and torch.equal(g2, g)
+    c = Case([2100], 1, 1, 128, 1, True, seed=95)
+    C, lse = c.fwd()
+    g, _ = c.bwd(C, lse)
+    Q, dC, C2, lse2, dQ = c.QKV.cuda(), c.dC.cuda(), torch.zeros_like(C), torch.zeros_like(lse), torch.zeros_like(g)
+    ws = torch.empty(tp.tp_attn_recompute_workspace_size(c.cfg, c.T), dtype=torch.uint8, device="cuda")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        tp.tp_attn_recompute_fwd(Q, c.cfg, C2, lse2)
+        tp.tp_attn_recompute_bwd(Q, c.cfg, C2, lse2, dC, dQ, ws)
+    for _ in range(3):
+        C2.zero_(), lse2.zero_(), dQ.zero_()
+        graph.replay()
+        assert torch.equal(C2, C) and torch.equal(lse2, lse) and torch.equal(dQ, g)
+    assert tp.tp_get_status() == tp.TP_OK
+
+
+@pytest.mark.parametrize("which", ["fwd", "bwd"])
+def test_few_heads_a_wait_that_runs_out_returns(which):
+    tp = _tp()
+    c = Case([2100], 1, 1, 128, 1, True, seed=96)
+    C, lse = c.fwd()
+    torch.cuda.synchronize()
+    tp.tp_debug_set_wait_limit_ms(20)
+    try:
+        tp.tp_debug_inject_fault(1)
+        if which == "fwd":
+            c.fwd()
+        else:
+            c.bwd(C, lse)
+        assert tp.tp_get_status() == tp.TP_ERR_TIMEOUT
+    finally:
+        tp.tp_debug_inject_fault(0)
+        tp.tp_debug_set_wait_limit_ms(0)
+    run(c)
