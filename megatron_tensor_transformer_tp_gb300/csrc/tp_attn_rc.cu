@@ -233,8 +233,8 @@ struct Units {
   __device__ __forceinline__ static bool read(const RcParams& p, int i, int64_t& a, int64_t& e) {
     a = e = 0;
     if (i >= p.b) return true;
-    a = p.seq_starts[i];
-    e = p.seq_starts[i + 1];
+    a = __ldcg(p.seq_starts + i);
+    e = __ldcg(p.seq_starts + i + 1);
     const bool fine = a >= 0 && e >= a && e <= p.T;
     a = min(max(a, static_cast<int64_t>(0)), p.T);
     e = min(max(e, a), p.T);
@@ -340,7 +340,7 @@ __device__ __forceinline__ void fill_table(const RcParams& p, int head, const ui
                                            int threads) {
   const int n = table_floats(p.bias.md);
   for (int i = thread; i < n; i += threads)
-    tab[i] = __ldg(p.table + static_cast<int64_t>(map[i]) * p.H + head) * kLog2e;
+    tab[i] = __ldcg(p.table + static_cast<int64_t>(map[i]) * p.H + head) * kLog2e;
 }
 // The same by one warp, through the head's column of the table in `vals`; the
 // map's and the table's rows are padded to fours.
@@ -652,8 +652,9 @@ struct ItemWalk {
   }
 };
 
-// Common entry: barriers 0 .. nbars-1 with the given counts, TMEM.
-template <int WARPS, class Counts>
+// Common entry: barriers 0 .. nbars-1 with the given counts, TMEM.  WAIT: for the
+// kernels before.
+template <int WARPS, bool WAIT = true, class Counts>
 __device__ __forceinline__ void enter(Head* hd, int nbars, Counts&& count) {
   const int warp = threadIdx.x >> 5;
   if (threadIdx.x == 0) {
@@ -665,7 +666,7 @@ __device__ __forceinline__ void enter(Head* hd, int nbars, Counts&& count) {
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  pdl_wait();
+  if (WAIT) pdl_wait();
   pdl_trigger();
 }
 template <int WARPS>
@@ -1229,6 +1230,12 @@ struct QueryWalk {
 // SPLIT: the CTAs of a cluster share an item, each with every p.parts-th query
 // tile.  Their sums meet in shared memory, where each CTA adds up its part of
 // the rows, in the order of the ranks.  For launches with fewer items than SMs.
+//
+// Begins before the kernel before it has ended (dQ's, or the sums of the bias's
+// gradient, which follow it): that one waited for everything earlier, so Q, K, V,
+// dC, lse, seq_starts and the table may be read at once (past L1, which may hold
+// an earlier call's).  D is dQ's: it is waited for, unless the sums lie between.
+// The last thing is to wait for the kernel before, for those behind.
 template <int DP, bool BIAS, bool SPLIT>
 __global__ void __launch_bounds__(kDkvThreads, 1) rc_dkv_kernel(const __grid_constant__ RcParams p) {
   using L = DkvShape<DP, BIAS>;
@@ -1236,6 +1243,7 @@ __global__ void __launch_bounds__(kDkvThreads, 1) rc_dkv_kernel(const __grid_con
   uint8_t* smem = smem_wide;
   if (smem_addr(smem) & 1023u) {  // nothing of the launch is left for padding
     if (threadIdx.x == 0) atomicOr(p.err, kErrTimeout);
+    pdl_wait();
     return;
   }
   uint8_t* sK = smem;
@@ -1249,7 +1257,8 @@ __global__ void __launch_bounds__(kDkvThreads, 1) rc_dkv_kernel(const __grid_con
   if (BIAS) fill_map(p.bias, map);
   const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
   volatile DkvItem* items = reinterpret_cast<volatile DkvItem*>(hd->items);
-  enter<kBwdWarps>(hd, L::count, L::arrivals);
+  enter<kBwdWarps, false>(hd, L::count, L::arrivals);
+  const bool early = p.partial == nullptr;  // D may not be there yet
   const uint32_t bar0 = smem_addr(hd->bar);
   auto bar = [&](int i) { return bar0 + 8u * i; };
   const WaitCtx w{&hd->abort_flag, p.err, p.wait_limit_ns};
@@ -1318,6 +1327,7 @@ __global__ void __launch_bounds__(kDkvThreads, 1) rc_dkv_kernel(const __grid_con
         const uint32_t pq = (it / L::kQ) & 1, po = (it / L::kO) & 1;
         const HeadAt hq = head_at(q.g, p.hq);
         const bool torn = 128 * q.i + 128 > len && start + len < p.T;  // rows of nobody in the tile
+        if (early && it == 1) pdl_wait();  // (the limits of the waits run from here)
         if (lane == 0) ok = wait_bounded(bar(L::qempty + sq), pq ^ 1u, w);
         ok = __shfl_sync(0xffffffffu, ok, 0);
         if (!ok) break;
@@ -1361,6 +1371,7 @@ __global__ void __launch_bounds__(kDkvThreads, 1) rc_dkv_kernel(const __grid_con
     // probability 2^(x - inf) = 0
     bool ok = true;
     uint32_t it = 0;
+    if (early) pdl_wait();
     for (uint32_t n = 0; ok; ++n) {
       const int slot = n & 1;
       if (!(ok = wait_warp(bar(L::info + slot), (n >> 1) & 1, w))) break;
@@ -1376,8 +1387,8 @@ __global__ void __launch_bounds__(kDkvThreads, 1) rc_dkv_kernel(const __grid_con
         for (int x = 0; x < 4; ++x) {
           const int pos = 128 * q.i + 32 * x + lane;
           const int64_t at = static_cast<int64_t>(q.g) * p.T + k.start + pos;
-          nl[x] = pos < k.len ? row_shift(p.lse[at]) : -INFINITY;
-          nd[x] = pos < k.len ? -p.D[at] : 0.f;
+          nl[x] = pos < k.len ? row_shift(__ldcg(p.lse + at)) : -INFINITY;
+          nd[x] = pos < k.len ? -__ldcg(p.D + at) : 0.f;
         }
         if (!(ok = wait_warp(bar(L::vecempty + buf), ((it >> 1) & 1) ^ 1u, w))) break;
 #pragma unroll
@@ -1438,6 +1449,7 @@ __global__ void __launch_bounds__(kDkvThreads, 1) rc_dkv_kernel(const __grid_con
           // (P's barriers alternate: with scores a tile ahead, two tiles may be ready)
           const int ready = grad ? L::dsready : L::pready + 2 * (it & 1);
           const uint32_t rphase = grad ? it & 1 : (it >> 1) & 1;
+          if (early && it == 0) pdl_wait();
           if (!(ok = wait_warp(bar(ready), rphase, w))) break;
           tc_fence_after();
           if (kHalves == 2) {
@@ -1474,6 +1486,7 @@ __global__ void __launch_bounds__(kDkvThreads, 1) rc_dkv_kernel(const __grid_con
     // After a failed wait an item runs on without waiting: the named barriers
     // need every warp, nothing is stored at its end, and all leave together.
     bool ok = true;
+    if (early) pdl_wait();
     int table_head = -1;
     uint32_t it = 0;  // tiles so far
     for (uint32_t n = 0;; ++n) {
@@ -1664,6 +1677,7 @@ __global__ void __launch_bounds__(kDkvThreads, 1) rc_dkv_kernel(const __grid_con
     }
     cluster_sync();
   }
+  pdl_wait();
   leave<kBwdWarps>(hd, p);
 }
 
@@ -2370,6 +2384,11 @@ cudaError_t bwd_t(RcParams& p, int num_sms, cudaStream_t st) {
                             dq_smem, p, st);
   p.fault_skip = 0;
   if (e != cudaSuccess) return e;
+  if (BIAS && p.partial != nullptr) {
+    e = launch_k(rc_bias_sum_kernel, dim3(p.H, p.bias.nb), dim3(128), 0, st, p, units);
+    count_launches(1);
+    if (e != cudaSuccess) return e;
+  }
   p.items = units * p.KV;
   p.slot = static_cast<int>(g_rc_slot_seq.fetch_add(1) % kRcSlots);
   // (a table of floats and a byte a distance)
@@ -2379,10 +2398,7 @@ cudaError_t bwd_t(RcParams& p, int num_sms, cudaStream_t st) {
   e = launch_rc(dkv, p.parts > 1 ? p.items * p.parts : p.items < num_sms ? p.items : num_sms, kDkvThreads, dkv_smem, p,
                 st);
   p.parts = 1;
-  if (e != cudaSuccess || !BIAS || p.partial == nullptr) return e;
-  launch_k(rc_bias_sum_kernel, dim3(p.H, p.bias.nb), dim3(128), 0, st, p, units);
-  count_launches(1);
-  return cudaGetLastError();
+  return e;
 }
 
 }  // namespace
