@@ -2285,15 +2285,32 @@ int wide_rows(const RcParams& p, const void* out, int64_t ld, int shard_w) {
   return (reinterpret_cast<uintptr_t>(out) & 31u) == 0 && ld % 16 == 0 && p.d % 16 == 0 && shard_w % 16 == 0;
 }
 
-// CTAs that share an item of `tiles` tiles: where there are fewer items than SMs,
-// as many as clusters find room for at once (pairs and fours leave 8 SMs over,
-// eights 24), with more than `least` tiles each.  One sequence of 4096, 4 query
-// heads and 1 K/V head of 128: backward 201 us with one, 87 us with four for dK
-// and dV; 2 heads of 128: forward 41 us with one, 27 us with two.  With 4 or 8
-// tiles an item in all, two take a microsecond longer than one in the forward.
-int cluster_parts(int64_t items, int64_t tiles, int least, int num_sms) {
+// CTAs that share an item, by an estimate of the launch's time in tiles: the
+// longest item or the mean work of an SM (items of equal length: rounds of them),
+// and for each round what an item costs beside its tiles: 1.5, in pairs 5.5, in
+// fours 7.5, in eights 9.5 (2 more in each of several rounds, as only single CTAs
+// stay for the next item).  `once`: in one round only (a kernel whose items are better
+// without).  n: tiles of a sequence of mean length (no matter if the sequences
+// come by seq_starts or by s: equal rows are summed in the same order); mult:
+// tiles an item for each of them.  Pairs and fours of CTAs leave 8 SMs over,
+// eights 40.
+int cluster_parts(const RcParams& p, int heads, int mult, bool once, int num_sms) {
+  const int64_t n = (p.T + 128 * p.b - 1) / (128 * p.b), items = n * p.b * heads;
   int parts = 1;
-  while (parts < 8 && 2 * parts * items <= num_sms - (parts < 4 ? 8 : 24) && tiles > least * parts) parts *= 2;
+  double best = 0;
+  for (int c = 1; c <= 8; c *= 2) {
+    const int64_t slots = c == 1 ? num_sms : (num_sms - (c < 8 ? 8 : 40)) / c;
+    if (slots < 1) break;
+    const int64_t rounds = (items + slots - 1) / slots, longest = n * mult;
+    const double mean = 0.5 * (n + 1) * mult * items / (static_cast<double>(c) * slots);
+    double t = p.causal ? static_cast<double>(longest) / c : static_cast<double>(rounds * ((longest + c - 1) / c));
+    if (p.causal && mean > t) t = mean;
+    t += rounds * (c == 1 ? 1.5 : (c == 2 ? 5.5 : c == 4 ? 7.5 : 9.5) + (rounds > 1 ? 2 : 0));
+    if (c == 1 || (t < 0.95 * best && (!once || rounds == 1))) {
+      best = t;
+      parts = c;
+    }
+  }
   return parts;
 }
 
@@ -2355,9 +2372,7 @@ cudaError_t fwd_t(RcParams& p, int num_sms, cudaStream_t st) {
   const int smem = FwdShape<DP>::kSmem + (BIAS ? 9 * table_floats(p.bias.md) + 4 * kMaxRelBuckets : 0);
   p.wide = wide_rows(p, p.C, p.ld_c, 0);
   p.slot = static_cast<int>(g_rc_slot_seq.fetch_add(1) % kRcSlots);
-  // (by a bound that holds for any sequences, as for dK and dV)
-  const int64_t bound = p.T / 128 + p.b;
-  p.parts = cluster_parts(bound * p.H, bound / p.b, 8, num_sms);
+  p.parts = cluster_parts(p, p.H, 1, true, num_sms);
   p.sub = p.parts > 1 ? 1 : query_tiles(p, num_sms);
   p.items = units_of(p, 128 * p.sub) * p.H;
   if (p.parts > 1) return launch_rc(rc_fwd_kernel<DP, BIAS, true>, p.items * p.parts, kFwdThreads, smem, p, st);
@@ -2375,10 +2390,7 @@ cudaError_t bwd_t(RcParams& p, int num_sms, cudaStream_t st) {
   // (two tables of floats, a head's values, a byte a distance, the sums)
   const int dq_smem =
       (DqShape<DP, BIAS>::kSmem) + 9 * n + (BIAS ? 4 * (kMaxRelBuckets + grad_floats(p.bias.md)) : 0);
-  // (clusters by bounds that hold for any sequences, so that equal rows are summed
-  // in the same order whether they come by seq_starts or by s)
-  const int64_t bound = p.T / 128 + p.b;
-  if (!BIAS) p.parts = cluster_parts(bound * p.H, bound / p.b, 8, num_sms);
+  if (!BIAS) p.parts = cluster_parts(p, p.H, 1, false, num_sms);
   const auto dq = p.parts > 1 ? rc_dq_kernel<DP, BIAS, !BIAS> : rc_dq_kernel<DP, BIAS, false>;
   cudaError_t e = launch_rc(dq, p.parts > 1 ? p.items * p.parts : p.items < num_sms ? p.items : num_sms, kDqThreads,
                             dq_smem, p, st);
@@ -2393,7 +2405,7 @@ cudaError_t bwd_t(RcParams& p, int num_sms, cudaStream_t st) {
   p.slot = static_cast<int>(g_rc_slot_seq.fetch_add(1) % kRcSlots);
   // (a table of floats and a byte a distance)
   const int dkv_smem = (DkvShape<DP, BIAS>::kSmem) + 5 * n;
-  p.parts = cluster_parts(bound * p.KV, bound / p.b * p.group, 4, num_sms);
+  p.parts = cluster_parts(p, p.KV, p.group, false, num_sms);
   const auto dkv = p.parts > 1 ? rc_dkv_kernel<DP, BIAS, true> : rc_dkv_kernel<DP, BIAS, false>;
   e = launch_rc(dkv, p.parts > 1 ? p.items * p.parts : p.items < num_sms ? p.items : num_sms, kDkvThreads, dkv_smem, p,
                 st);

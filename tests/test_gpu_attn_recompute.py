@@ -592,10 +592,12 @@ FEW = [  # lens, query heads, key/value heads, d, shards, causal, tail
     ([2100], 1, 1, 64, 1, False, 0),        # 4, 4, 4
     ([600], 8, 1, 128, 1, True, 0),         # 1, 1, 8
     ([600], 6, 1, 64, 1, False, 3),         # 1, 1, 8: 30 query tiles by 8 CTAs
-    ([1290], 3, 1, 96, 1, True, 0),         # 2, 2, 8
-    ([1700], 2, 2, 40, 2, True, 0),         # 2, 2, 4
-    ([2700, 0], 1, 1, 128, 1, False, 130),  # an empty one, rows behind: 2, 2, 4
+    ([1290], 3, 1, 96, 1, True, 0),         # 4, 4, 8
+    ([1700], 2, 2, 40, 2, True, 0),         # 4, 4, 4
+    ([2700, 0], 1, 1, 128, 1, False, 130),  # an empty one, rows behind: 4, 4, 4
     ([1800, 900], 2, 1, 72, 1, True, 0),    # 2, 2, 4
+    ([2048], 8, 2, 64, 1, True, 0),         # 1, 1, 4
+    ([4000], 8, 1, 64, 1, False, 0),        # 1, 1, 4: in more than one round
 ]
 
 
