@@ -305,9 +305,9 @@ typedef struct {
  *   dv_j = sum_i P_ij dC_i   (dk, dv: over the query heads that share the head)
  * Arguments (bf16 only, TP_ERR_UNSUPPORTED for TP_F32):
  *   seq_starts  device int64[b + 1]: sequence i is the rows seq_starts[i] ..
- *               seq_starts[i + 1] - 1 (none, if they are equal); rows outside
- *               every sequence are neither used nor written.  Or NULL: b
- *               sequences of s rows each.
+ *               seq_starts[i + 1] - 1 (none, if they are equal; b <= 2^22);
+ *               rows outside every sequence are neither used nor written.  Or
+ *               NULL: b sequences of s rows each.
  *   QKV         (T, (n_heads + 2 n_kv_heads) d) with row pitch ld_qkv, shard-major:
  *               shard i holds [Q_i K_i V_i], its heads in order inside each.
  *   C, dC       (T, n_heads d), head j in columns [j d, (j + 1) d), pitches ld_c, ld_dc
@@ -319,8 +319,10 @@ typedef struct {
  * fixed order: equal calls give equal bits.
  * Rows of one sequence never depend on another sequence's values, whatever
  * they are.  Inside a sequence a non-finite value may reach every row.
+ * Outputs and workspace overlap no other buffer of the call (row pitches may
+ * interleave them): key/value tiles are read after the first dQ is written.
  * Errors: TP_ERR_INVALID for sizes outside the ranges above, pitches narrower
- * than a row, null pointers, T > 2^31 - 1; TP_ERR_ALIGN for a d or pitch that is
+ * than a row, null pointers, T > 2^31 - 512, an output at an input's address; TP_ERR_ALIGN for a d or pitch that is
  * no multiple of 8 or a QKV, C, dC, dQKV that is not 16-byte aligned (lse, table: 4-byte);
  * all before anything is launched.  Sequence starts are on the device: if they
  * decrease or leave [0, T], no access leaves the buffers, the results are

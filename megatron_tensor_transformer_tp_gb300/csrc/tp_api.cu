@@ -1262,7 +1262,8 @@ bool rel_step_reached(int n, int E, int md, int K, int j) {
 // Sizes and bias into P, without pointers.
 tp_status rc_sizes(const tp_attn_config* c, const tp_relbias_config* rb, bool dense, RcParams* P) {
   if (c == nullptr) return TP_ERR_INVALID;
-  if (c->T < 0 || c->T > INT32_MAX || c->b < 0 || c->b > (1 << 30) || c->n_heads < 1 || c->n_kv_heads < 1 ||
+  // (positions and rows are 32-bit numbers, up to two tiles past a sequence)
+  if (c->T < 0 || c->T > INT32_MAX - 511 || c->b < 0 || c->b > (1 << 30) || c->n_heads < 1 || c->n_kv_heads < 1 ||
       c->N < 1 || c->N > 8 || c->n_heads % c->N != 0 || c->n_kv_heads % c->N != 0 ||
       c->n_heads % c->n_kv_heads != 0 || c->d < 1 || c->d > 128)
     return TP_ERR_INVALID;
@@ -1318,6 +1319,8 @@ tp_status rc_args(tp_dtype dt, const tp_attn_config* c, const tp_relbias_config*
   if (with_bias && rb == nullptr) return TP_ERR_INVALID;
   tp_status st = rc_sizes(c, with_bias ? rb : nullptr, seq_starts == nullptr, P);
   if (st == TP_ERR_INVALID) return st;
+  // (a warp reads through the starts while others wait for it: 2^24 of them took 0.6 s)
+  if (seq_starts != nullptr && c->b > (1 << 22)) return TP_ERR_INVALID;
   if (dt != TP_BF16) return TP_ERR_UNSUPPORTED;
   if (st != TP_OK) return st;
   if (c->T == 0) return TP_OK;
@@ -1361,6 +1364,7 @@ tp_status rc_fwd_impl(const char* name, tp_dtype dt, const tp_attn_config* cfg, 
   memset(&P, 0, sizeof(P));
   tp_status st = rc_args(dt, cfg, rb, with_bias, table, seq_starts, QKV, ld_qkv, C, ld_c, lse, &P);
   if (st != TP_OK || cfg->T == 0) return st;
+  if (C == QKV) return TP_ERR_INVALID;
   DeviceState* dev = nullptr;
   if ((st = rc_device(&P, QKV, ld_qkv, cfg->N, &dev)) != TP_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -1394,6 +1398,7 @@ tp_status rc_bwd_impl(const char* name, tp_dtype dt, const tp_attn_config* cfg, 
   const size_t dot = rc_dot_bytes(P.T, P.H);
   if (workspace == nullptr || ws_bytes < dot + (dtable ? rc_partial_bytes(P) : 0)) return TP_ERR_WORKSPACE;
   if (!al256(workspace)) return TP_ERR_ALIGN;
+  if (dQKV == QKV || dQKV == C || dQKV == dC || (dtable != nullptr && dtable == table)) return TP_ERR_INVALID;
   P.dQKV = dQKV;
   P.ld_dqkv = ld_dqkv;
   P.D = reinterpret_cast<float*>(workspace);

@@ -646,8 +646,8 @@ struct ItemWalk {
       first = false;
       index = static_cast<int>(item % heads);
       if (units.find(p, item / heads, last_first, lane, u)) return true;
-      if (zero != nullptr)
-        for (int i = lane; i < nzero; i += 32) zero[item * nzero + i] = 0.f;
+      if (zero == nullptr) return false;  // nor do later items have rows
+      for (int i = lane; i < nzero; i += 32) zero[item * nzero + i] = 0.f;
     }
   }
 };
@@ -2295,7 +2295,7 @@ int wide_rows(const RcParams& p, const void* out, int64_t ld, int shard_w) {
 // tiles an item for each of them.  Pairs and fours of CTAs leave 8 SMs over,
 // eights 40.
 int cluster_parts(const RcParams& p, int heads, int mult, bool once, int num_sms) {
-  const int64_t n = (p.T + 128 * p.b - 1) / (128 * p.b), items = n * p.b * heads;
+  const int64_t seqs = p.b, n = (p.T + 128 * seqs - 1) / (128 * seqs), items = n * seqs * heads;
   int parts = 1;
   double best = 0;
   for (int c = 1; c <= 8; c *= 2) {

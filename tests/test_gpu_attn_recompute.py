@@ -571,6 +571,14 @@ def test_many_sequences():
     check(c, C, lse, g)
 
 
+@pytest.mark.parametrize("bias", [None, BIAS])
+def test_mostly_empty_sequences(bias):
+    """Far more sequences than rows."""
+    lens = [0] * 20000 + [77] + [0] * 9000 + [300, 1] + [0] * 5000
+    c = Case(lens, 2, 1, 64, 1, True, bias=bias, seed=85)
+    run(c)
+
+
 def test_growing_scores():
     """Each key tile's scores lie far above the one before: the exponents' reference moves at every tile."""
     c = Case([640], 1, 1, 64, 1, False, scale=1.0, seed=84)
