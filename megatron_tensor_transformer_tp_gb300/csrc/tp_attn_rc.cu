@@ -11,19 +11,34 @@
 // Scores and probabilities live in TMEM and registers only: 128 x 128 tiles,
 // fp32 accumulators, exponentials as 2^(x log2 e).
 //
-// Three tensor-core kernels, each with eight compute warps (TMEM lane = row of
-// the score tile), one MMA warp and one TMA warp per CTA, one CTA per SM:
-//   rc_fwd_kernel   one or two 128-row query tiles of a head; the matrix
-//                   products of one tile run under the softmax of the other.
+// Three tensor-core kernels, one CTA an SM, in which one warp loads tiles by TMA,
+// one or two issue products, 16 do the element-wise work (a TMEM lane is a row of
+// the score tile) and one prepares tables:
+//   rc_fwd_kernel   one or two 128-row query tiles of a head over its key tiles;
+//                   the products of one run under the softmax of the other.
+//   rc_dq_kernel    a 128-row query tile of a head over its key tiles.  It also
+//                   computes D, and sums dS by relative distance for the bias.
 //   rc_dkv_kernel   a 128-row key tile of a K/V head, over the query tiles of
 //                   every query head that shares it.  It computes the
 //                   transposed scores S^T = K Q^T and dP^T = V dC^T, so P^T
 //                   and dS^T are A operands straight from TMEM.
-//   rc_dq_kernel    a 128-row query tile of a head over its key tiles; it also
-//                   sums dS by relative distance for the bias.
-// The backward computes the scores and dP in both kernels (seven products a
-// tile instead of five): no output is summed by atomics, so results do not
+// The backward computes the scores and dP in both of its kernels (seven products
+// a tile instead of five): no output is summed by atomics, so results do not
 // depend on the order in which CTAs run, and dQ needs no fp32 buffer in memory.
+// CTAs are persistent and take items from a counter; where an item outlasts an
+// SM's share of the work, clusters share items (cluster_parts).
+//
+// All three are bound by arithmetic: a tile of 128 x 128 scores of width 128 takes
+// 512 cycles of tensor cores a product and reads 64 KB that other CTAs read too.
+// Measured on a GB300 (cuBLAS reaches 1.87 PFLOP/s in bf16 there), in matrix work
+// that the definition needs, four and ten flops a visible pair and column:
+//   causal, one sequence of 16384, 8 heads of 128, 2 K/V heads
+//     forward 341 us, 1.6 PFLOP/s; backward 1.20 ms, 1.15 PFLOP/s, which is 1.6
+//     with the two products that are computed twice
+//   causal, 2 x 2048, 32 heads of 128: 63 us, 1.10 PFLOP/s; 201 us, 0.86 PFLOP/s
+//   bias of both directions, 4 x 1024, 16 heads of 64: 30 us; 105 us, 0.41 PFLOP/s:
+//     at 64 columns a product takes 256 cycles and the element-wise work as long as
+//     before, which is then the bound.
 // Every wait is bounded, as in the GEMM engine.
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -41,9 +56,10 @@ namespace tp {
 namespace {
 
 // Compute warps first, then the MMA warps, the TMA warp and a warp for tables
-// (forward: the bias of a head; dK, dV: the rows' lse and D).  The forward has two compute warps on every 32
-// rows of a score tile (64 columns each) and two tiles, the backward kernels
-// four (32 columns each).
+// (forward and dQ: the bias of a head; dK, dV: the rows' lse and D).  The forward
+// has two compute warps on every 32 rows of a score tile (64 columns each) and two
+// tiles, the backward kernels four (32 columns each).  16 warps against 8, with a
+// product warp a query tile: forward of 16384, 8 heads of 128, 355 us and 447 us.
 constexpr int kFwdWarps = 16, kBwdWarps = 16;
 constexpr int kFwdThreads = 32 * (kFwdWarps + 4), kDkvThreads = 32 * (kBwdWarps + 4), kDqThreads = 32 * (kBwdWarps + 3);
 constexpr int kPanel = 128 * 128;    // bytes of 128 rows x 64 bf16 columns (one swizzle width)
@@ -733,7 +749,8 @@ struct FwdShape {
   static constexpr int qfull = 0, kfull = 2, vfull = kfull + kStages, tail = vfull + kStages, kempty = tail + 1,
                        vempty = kempty + kStages, sfull = vempty + kStages, pfull = sfull + 2, odone = pfull + 4,
                        ofree = odone + 2, qempty = ofree + 2, info = qempty + 2, tabfull = info + 2,
-                       free_ = tabfull + 2, sread = free_ + 2, pvdone = sread + 2, drain = pvdone + 2, count = drain + 2;
+                       free_ = tabfull + 2, sread = free_ + 2, pvdone = sread + 2, drain = pvdone + 2,
+                       count = drain + 2;
   static_assert(count <= kMaxBars && kempty <= 32, "barriers");
   template <bool BIAS>
   static uint32_t __device__ __forceinline__ arrivals(int i) {
@@ -745,10 +762,26 @@ struct FwdShape {
   }
 };
 
+// One pass over the keys with a running reference m and sum l a row,
+//   O = sum_j 2^(x_j - m) v_j,  l = sum_j 2^(x_j - m),  C = O / l,
+//   lse = (m + log2 l) ln 2  (x in units of log2 e),
+// where m follows the row's maximum only when that has grown past m by 16, so O is
+// rescaled rarely and no term exceeds 2^16.  Scores and probabilities stay in TMEM;
+// probabilities are rounded to bf16 as operands of the second product, while l sums
+// them in fp32.
+//
+// A tile of 128 x 128 x 128 is 1024 cycles of products and 16384 exponentials; a
+// pair of query tiles takes 2500 cycles against 2056 of products, since each waits
+// for the other's softmax at times.  16384, 8 heads of 128, causal: 341 us, 1.6
+// PFLOP/s (86% of cuBLAS), 2 x 2048, 32 heads: 63 us (59%: a sequence has 8.5 key
+// tiles a query tile, of which the diagonal's are half hidden, and an item costs
+// as much as 1.5 tiles beside them).  Two key and value tiles held, as much as fits
+// beside two query tiles.
+//
 // Persistent: a CTA takes (query rows, head) items until there are none.  The
 // TMA warp runs ahead into the next item's loads, and its first scores are
 // computed while the last outputs are stored.
-// SPLIT (for launches with fewer items than SMs): the CTAs of a cluster share an
+// SPLIT (where cluster_parts says so): the CTAs of a cluster share an
 // item of one query tile, each with every p.parts-th key tile.  Their outputs,
 // references and sums meet in shared memory, where each CTA joins its part of
 // the rows, in the order of the ranks.
@@ -1227,9 +1260,18 @@ struct QueryWalk {
   }
 };
 
+// dV = sum over the query tiles of P^T dC, dK = scale sum of dS^T Q, in TMEM for the
+// whole item.  One warp issues the two products through P, another the two through
+// dS, so that each waits while the other's run.  At width 128 the products bound it:
+// 2240 cycles a tile against 2048 of products (with P and dS handed over in one
+// piece 2780).  At width 64 the 16 warps' own work does: 2500 cycles against 1024,
+// with 11 instructions a score issued in 57% of the cycles.  P and dS in TMEM
+// columns of their own there, so that the products run a tile further ahead, was
+// 10% slower: two more waits a tile cost more than they hid.
+//
 // SPLIT: the CTAs of a cluster share an item, each with every p.parts-th query
 // tile.  Their sums meet in shared memory, where each CTA adds up its part of
-// the rows, in the order of the ranks.  For launches with fewer items than SMs.
+// the rows, in the order of the ranks.
 //
 // Begins before the kernel before it has ended (dQ's, or the sums of the bias's
 // gradient, which follow it): that one waited for everything earlier, so Q, K, V,
@@ -1671,8 +1713,9 @@ __global__ void __launch_bounds__(kDkvThreads, 1) rc_dkv_kernel(const __grid_con
         const float mul = which ? p.scale : 1.f;
         const int64_t col = static_cast<int64_t>(hk.shard) * p.shard_w + static_cast<int64_t>(p.hq) * p.d +
                             static_cast<int64_t>(hk.local + (which ? 0 : p.hk)) * p.d + 4 * chunk;
-        *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.dQKV) + (static_cast<int64_t>(start) + pos) * p.ld_dqkv +
-                                  col) = make_uint2(pack_bf16x2(a.x * mul, a.y * mul), pack_bf16x2(a.z * mul, a.w * mul));
+        __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.dQKV) + (static_cast<int64_t>(start) + pos) * p.ld_dqkv + col;
+        *reinterpret_cast<uint2*>(out) =
+            make_uint2(pack_bf16x2(a.x * mul, a.y * mul), pack_bf16x2(a.z * mul, a.w * mul));
       }
     }
     cluster_sync();
@@ -1683,9 +1726,10 @@ __global__ void __launch_bounds__(kDkvThreads, 1) rc_dkv_kernel(const __grid_con
 
 // TMEM: scores [0, 128), dP and then dS [128, 256), dQ [256, 384), Q [384, 448)
 // and dC [448, 512); heads to 64 wide: a second dP [256, 384), dQ [384, 448),
-// Q [448, 480), dC [480, 512), and dP is computed a tile ahead.  Q and dC stay there for the whole row of key tiles: the
-// products read K and V from shared memory alone (both operands there would
-// take all of its bandwidth), and three tiles of each fit.
+// Q [448, 480), dC [480, 512), and dP is computed a tile ahead.  Q and dC stay
+// there for the whole row of key tiles: the products read K and V from shared
+// memory alone (both operands there would take all of its bandwidth), and three
+// tiles of each fit.
 template <int DP, bool WITH_BIAS>
 struct DqShape {
   static constexpr int kTile = DP / 64 * kPanel;
@@ -1718,6 +1762,16 @@ __host__ __device__ constexpr int grad_floats(int md) {
   return 2 * kBwdWarps * kDiag + 2 * md + 1 + 2 * kBwdWarps + kMaxRelBuckets;
 }
 
+// dQ = scale sum over the key tiles of dS K, and D = dC . C of its rows.  At width
+// 128: 1955 cycles a tile against 1536 of its three products, which wait for dS; Q
+// and dC read from shared memory each time 3440.  At width 64 with the bias's
+// gradient 3300 cycles against 768: the 16 warps' work, 14 instructions a score.
+//
+// The bias's gradient: a tile within the largest distance sums its dS along the
+// diagonals by shuffles (1500 cycles, of which the shuffles are most; one running
+// sum handed from lane to lane took 2700), other tiles add to a sum a row.  Both go
+// to the item's sums by bucket in memory, and those to the table in fixed order.
+//
 // SPLIT: as for dK and dV, with every p.parts-th key tile (not with a bias, whose
 // gradient's sums are an item's).
 template <int DP, bool BIAS, bool SPLIT>
@@ -2248,9 +2302,9 @@ __global__ void __launch_bounds__(kDqThreads, 1) rc_dq_kernel(const __grid_const
           a.z += b.z;
           a.w += b.w;
         }
-        const int64_t col = static_cast<int64_t>(hq.shard) * p.shard_w + static_cast<int64_t>(hq.local) * p.d + 4 * chunk;
-        *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.dQKV) + (static_cast<int64_t>(start) + row) * p.ld_dqkv +
-                                  col) =
+        __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.dQKV) + (static_cast<int64_t>(start) + row) * p.ld_dqkv +
+                             static_cast<int64_t>(hq.shard) * p.shard_w + static_cast<int64_t>(hq.local) * p.d + 4 * chunk;
+        *reinterpret_cast<uint2*>(out) =
             make_uint2(pack_bf16x2(a.x * p.scale, a.y * p.scale), pack_bf16x2(a.z * p.scale, a.w * p.scale));
       }
     }
@@ -2289,11 +2343,19 @@ int wide_rows(const RcParams& p, const void* out, int64_t ld, int shard_w) {
 // longest item or the mean work of an SM (items of equal length: rounds of them),
 // and for each round what an item costs beside its tiles: 1.5, in pairs 5.5, in
 // fours 7.5, in eights 9.5 (2 more in each of several rounds, as only single CTAs
-// stay for the next item).  `once`: in one round only (a kernel whose items are better
-// without).  n: tiles of a sequence of mean length (no matter if the sequences
-// come by seq_starts or by s: equal rows are summed in the same order); mult:
-// tiles an item for each of them.  Pairs and fours of CTAs leave 8 SMs over,
-// eights 40.
+// stay for the next item).  `once`: in one round only (the forward, whose single
+// CTAs take pairs of query tiles).  n: tiles of a sequence of mean length (no matter
+// if the sequences come by seq_starts or by s: equal rows are summed in the same
+// order); mult: tiles an item for each of them.  Pairs and fours of CTAs leave 8
+// SMs over, eights 40.  Microseconds with 1, 2, 4 and 8, whole call, heads of 128:
+//   forward   2048, 2 heads, causal             23   18   14*  31
+//             4096, 2 heads                     41   28*  36   65
+//   dQ        2048, 2 heads, causal             36   31   28*  44
+//   dK, dV    512, 8 heads, 1 K/V head          54   38   28   24*
+//             2048, 16 heads, 2 K/V, causal    190  112   74*  82
+//             4096, 8 heads, 2 K/V             238  162* 173  226
+//             16384, 8 heads, 2 K/V, causal   1135 1079*1115 1344
+//             2048, 8 heads of 64, 8 K/V        38*  49   63  108   (* chosen)
 int cluster_parts(const RcParams& p, int heads, int mult, bool once, int num_sms) {
   const int64_t seqs = p.b, n = (p.T + 128 * seqs - 1) / (128 * seqs), items = n * seqs * heads;
   int parts = 1;
