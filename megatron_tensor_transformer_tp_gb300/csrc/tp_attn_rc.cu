@@ -517,29 +517,51 @@ __device__ __forceinline__ void pack_columns(const uint32_t* v, float mul, uint3
     q[i] = pack_bf16x2(a, b);
   }
 }
-// n of COLS bf16 values of a row to memory; `wide`: every row start is 32-byte
-// aligned and n a multiple of 16.
+__device__ __forceinline__ void st_global32(__nv_bfloat16* out, const uint32_t* r) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(out), "r"(r[0]), "r"(r[1]), "r"(r[2]),
+               "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+// n of COLS bf16 values of each lane's row to memory, rows in order over the lanes
+// and `ld` apart; `mine`: the row is stored.  By a whole warp.  `wide`: every row
+// start is 32-byte aligned and n a multiple of 16.  Two lanes then swap halves, so
+// that a store covers 64 bytes of a row: 64 KB by the 16 warps of all SMs at once
+// take 2100 cycles, with 32 bytes a row 3100.
 template <int COLS>
-__device__ __forceinline__ void put_columns(const uint32_t* q, int n, __nv_bfloat16* out, bool wide) {
+__device__ __forceinline__ void put_columns(const uint32_t* q, int n, bool mine, __nv_bfloat16* out, int64_t ld,
+                                            bool wide) {
+  if (wide) {
+    const bool odd = threadIdx.x & 1;
+    const bool other = __shfl_xor_sync(0xffffffffu, mine, 1);
+    const bool first = odd ? other : mine, second = odd ? mine : other;
+    __nv_bfloat16* row = (odd ? out - ld : out) + (odd ? 16 : 0);  // of the pair's first row
 #pragma unroll
-  for (int c = 0; c < COLS; c += 16) {
-    const uint32_t* r = q + c / 2;
-    if (wide) {
-      if (c < n)
-        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(out + c), "r"(r[0]), "r"(r[1]),
-                     "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
-                     : "memory");
-    } else {
-      if (c < n) *reinterpret_cast<uint4*>(out + c) = make_uint4(r[0], r[1], r[2], r[3]);
-      if (c + 8 < n) *reinterpret_cast<uint4*>(out + c + 8) = make_uint4(r[4], r[5], r[6], r[7]);
+    for (int c = 0; c < COLS; c += 32) {
+      const uint32_t* r = q + c / 2;
+      uint32_t x[8], y[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const uint32_t v = __shfl_xor_sync(0xffffffffu, odd ? r[i] : r[8 + i], 1);
+        x[i] = odd ? v : r[i];
+        y[i] = odd ? r[8 + i] : v;
+      }
+      if (c + (odd ? 16 : 0) < n) {
+        if (first) st_global32(row + c, x);
+        if (second) st_global32(row + ld + c, y);
+      }
     }
+  } else if (mine) {
+#pragma unroll
+    for (int c = 0; c < COLS; c += 8)
+      if (c < n) *reinterpret_cast<uint4*>(out + c) = make_uint4(q[c / 2], q[c / 2 + 1], q[c / 2 + 2], q[c / 2 + 3]);
   }
 }
 template <int COLS>
-__device__ __forceinline__ void store_columns(const uint32_t* v, int n, float mul, __nv_bfloat16* out, bool wide) {
+__device__ __forceinline__ void store_columns(const uint32_t* v, int n, float mul, bool mine, __nv_bfloat16* out,
+                                              int64_t ld, bool wide) {
   uint32_t q[COLS / 2];
   pack_columns<COLS>(v, mul, q);
-  put_columns<COLS>(q, n, out, wide);
+  put_columns<COLS>(q, n, mine, out, ld, wide);
 }
 
 // COLS bf16 columns from column `first` of the thread's row of a swizzled tile
@@ -1134,13 +1156,12 @@ __global__ void __launch_bounds__(kFwdThreads, 1) rc_fwd_kernel(const __grid_con
           }
           continue;
         }
-        if (ok && row < len) {
-          const int64_t token = static_cast<int64_t>(start) + row;
-          __nv_bfloat16* out =
-              static_cast<__nv_bfloat16*>(p.C) + token * p.ld_c + static_cast<int64_t>(head) * p.d + ofirst;
-          store_columns<DP / 2>(o, olast - ofirst, l > 0.f ? 1.f / l : 0.f, out, p.wide);
-          if (half == 0) p.lse[static_cast<int64_t>(head) * p.T + token] = (m + log2f(l)) * kLn2;
-        }
+        const int64_t token = static_cast<int64_t>(start) + row;
+        const bool mine = ok && row < len;
+        store_columns<DP / 2>(o, olast - ofirst, l > 0.f ? 1.f / l : 0.f, mine,
+                              static_cast<__nv_bfloat16*>(p.C) + token * p.ld_c + static_cast<int64_t>(head) * p.d + ofirst,
+                              p.ld_c, p.wide);
+        if (mine && half == 0) p.lse[static_cast<int64_t>(head) * p.T + token] = (m + log2f(l)) * kLn2;
         __syncwarp();
         ++nq;
       } else if (SPLIT && t == 0) {
@@ -1534,7 +1555,9 @@ __global__ void __launch_bounds__(kDkvThreads, 1) rc_dkv_kernel(const __grid_con
     for (uint32_t n = 0;; ++n) {
       const int slot = n & 1;
       ok = ok && wait_warp(bar(L::info + slot), (n >> 1) & 1, w);
-      if (named_bar_any(2, 32 * kBwdWarps, !ok)) break;
+      // (without a bias there are no named barriers to keep to: a warp goes on while
+      // others still store)
+      if (BIAS ? named_bar_any(2, 32 * kBwdWarps, !ok) : !ok) break;
       const Work k = read_item(slot);
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(L::free_ + slot));
@@ -1677,14 +1700,14 @@ __global__ void __launch_bounds__(kDkvThreads, 1) rc_dkv_kernel(const __grid_con
         continue;
       }
       const int pos = 128 * kt + key;
-      if (ok && pos < k.len) {
+      {
         const HeadAt hk = head_at(k.kvh, p.hk);
         const int64_t col = static_cast<int64_t>(hk.shard) * p.shard_w + static_cast<int64_t>(p.hq) * p.d +
                             static_cast<int64_t>(hk.local + (which ? 0 : p.hk)) * p.d + first;
-        store_columns<DP / 2>(r, cols, which ? p.scale : 1.f,
+        store_columns<DP / 2>(r, cols, which ? p.scale : 1.f, ok && pos < k.len,
                               static_cast<__nv_bfloat16*>(p.dQKV) +
                                   (static_cast<int64_t>(k.start) + pos) * p.ld_dqkv + col,
-                              p.wide);
+                              p.ld_dqkv, p.wide);
       }
       __syncwarp();
     }
@@ -2027,9 +2050,10 @@ __global__ void __launch_bounds__(kDqThreads, 1) rc_dq_kernel(const __grid_const
     // stored when the next one's Q and dC are in place
     const int ofirst = 32 * part, ocols = min(p.d - ofirst, 32);
     uint32_t dq[16];
-    __nv_bfloat16* prev = nullptr;  // where dq goes, if anywhere
+    __nv_bfloat16* prev = nullptr;  // where dq goes
+    bool stored = false;            // if anywhere
     auto put = [&]() {
-      if (prev != nullptr) put_columns<32>(dq, ocols, prev, p.wide);
+      if (prev != nullptr) put_columns<32>(dq, ocols, stored, prev, p.ld_dqkv, p.wide);
       __syncwarp();
     };
     // After a failed wait an item runs on without waiting: the named barriers
@@ -2241,7 +2265,8 @@ __global__ void __launch_bounds__(kDqThreads, 1) rc_dq_kernel(const __grid_const
       const HeadAt hq = head_at(uniform(items[slot].head), p.hq);
       prev = static_cast<__nv_bfloat16*>(p.dQKV) + (static_cast<int64_t>(items[slot].start) + row) * p.ld_dqkv +
              static_cast<int64_t>(hq.shard) * p.shard_w + static_cast<int64_t>(hq.local) * p.d + ofirst;
-      if (SPLIT || !ok || !mine || ocols <= 0) prev = nullptr;
+      if (SPLIT || ocols <= 0) prev = nullptr;  // (the whole warp)
+      stored = ok && mine;
       if (BIAS && grad) {
         // the item's sums by bucket, in a fixed order: a warp a bucket
         constexpr int kN = 32 * kBwdWarps;
