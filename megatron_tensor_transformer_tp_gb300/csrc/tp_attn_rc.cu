@@ -2081,11 +2081,8 @@ __global__ void __launch_bounds__(kDqThreads, 1) rc_dq_kernel(const __grid_const
       const int row = r0 + quarter * 32 + lane;
       const bool mine = row < len;
       const float* tab = tabs + slot * tabn;
-      float nl = 0.f, nd = 0.f;
-      if (mine) {
-        const int64_t at = static_cast<int64_t>(head) * p.T + start + row;
-        nl = row_shift(p.lse[at]);
-      }
+      float lse = 0.f, nd = 0.f;  // (lse is not looked at before the products have been asked for)
+      if (mine) lse = __ldcg(p.lse + static_cast<int64_t>(head) * p.T + start + row);
       // this warp's quarter of the columns of Q and dC into TMEM; the item before
       // has been through its products
       {
@@ -2118,6 +2115,7 @@ __global__ void __launch_bounds__(kDqThreads, 1) rc_dq_kernel(const __grid_const
       vc += nk + 1;
       // the item before's output, while the first products of this one run
       put();
+      const float nl = mine ? row_shift(lse) : 0.f;
       if (BIAS) ok = ok && wait_warp(bar(L::tabfull + slot), (n >> 1) & 1, w);
       float end_lo = 0.f, end_hi = 0.f;  // dS at distances <= -md and >= md, of the tile sums
       uint64_t far_lo = 0, far_hi = 0;   // and of this row in tiles all beyond an end
