@@ -1778,11 +1778,11 @@ struct DqItem {
 };
 
 // The bias gradient's shared memory: per compute warp the sums of its 32 x 32
-// block by distance (63 of them), for two tiles, the CTA's sums by distance,
-// the warps' sums beyond the ends, and the buckets' first distances.
+// block by distance (63 of them), for two tiles; of two items the CTA's sums by
+// distance and the warps' sums beyond the ends; and the buckets' first distances.
 constexpr int kDiag = 64;
 __host__ __device__ constexpr int grad_floats(int md) {
-  return 2 * kBwdWarps * kDiag + 2 * md + 1 + 2 * kBwdWarps + kMaxRelBuckets;
+  return 2 * kBwdWarps * kDiag + 2 * (2 * md + 1) + 4 * kBwdWarps + kMaxRelBuckets;
 }
 
 // dQ = scale sum over the key tiles of dS K, and D = dC . C of its rows.  At width
@@ -1812,13 +1812,14 @@ __global__ void __launch_bounds__(kDqThreads, 1) rc_dq_kernel(const __grid_const
   float* vals = tabs + 2 * tabn;                                    // the head's values
   uint8_t* map = reinterpret_cast<uint8_t*>(vals + (BIAS ? kMaxRelBuckets : 0));  // the distances' buckets
   float* diag = reinterpret_cast<float*>(map + tabn);               // [2][kBwdWarps][kDiag]
-  float* bins = diag + 2 * kBwdWarps * kDiag;                       // [2 md + 1]
-  float* ends = bins + 2 * md + 1;                                  // [2][kBwdWarps]
-  int* firsts = reinterpret_cast<int*>(ends + 2 * kBwdWarps);       // p.bias.first: indexed reads of it are slow
+  const int binn = 2 * md + 1;
+  float* all_bins = diag + 2 * kBwdWarps * kDiag;                   // [2][2 md + 1]
+  float* all_ends = all_bins + 2 * binn;                            // [2][2][kBwdWarps]
+  int* firsts = reinterpret_cast<int*>(all_ends + 4 * kBwdWarps);   // p.bias.first: indexed reads of it are slow
   const bool grad = BIAS && p.partial != nullptr;
   if (BIAS) fill_map(p.bias, map);
   if (grad) {
-    for (int i = threadIdx.x; i < 2 * md + 1; i += kDqThreads) bins[i] = 0.f;
+    for (int i = threadIdx.x; i < 2 * binn; i += kDqThreads) all_bins[i] = 0.f;
     for (int i = threadIdx.x; i < p.bias.side; i += kDqThreads) firsts[i] = p.bias.first[i];
   }
   const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
@@ -2117,6 +2118,7 @@ __global__ void __launch_bounds__(kDqThreads, 1) rc_dq_kernel(const __grid_const
       put();
       const float nl = mine ? row_shift(lse) : 0.f;
       if (BIAS) ok = ok && wait_warp(bar(L::tabfull + slot), (n >> 1) & 1, w);
+      float* bins = all_bins + slot * binn;
       float end_lo = 0.f, end_hi = 0.f;  // dS at distances <= -md and >= md, of the tile sums
       uint64_t far_lo = 0, far_hi = 0;   // and of this row in tiles all beyond an end
       for (int j = 0; j < nk; ++j, ++nt) {
@@ -2266,8 +2268,11 @@ __global__ void __launch_bounds__(kDqThreads, 1) rc_dq_kernel(const __grid_const
       if (SPLIT || ocols <= 0) prev = nullptr;  // (the whole warp)
       stored = ok && mine;
       if (BIAS && grad) {
-        // the item's sums by bucket, in a fixed order: a warp a bucket
+        // the item's sums by bucket, in a fixed order: 16 lanes a bucket.  The next item
+        // has bins and ends of its own; those of the one before are cleared here, which
+        // every warp has read.
         constexpr int kN = 32 * kBwdWarps;
+        float* ends = all_ends + 2 * kBwdWarps * slot;
         float a0, a1, b0, b1;
         unpack2(far_lo, a0, a1);
         unpack2(far_hi, b0, b1);
@@ -2282,26 +2287,31 @@ __global__ void __launch_bounds__(kDqThreads, 1) rc_dq_kernel(const __grid_const
           ends[kBwdWarps + warp] = hi;
         }
         named_bar(1, kN);
-        for (int u = warp; u < p.bias.nb; u += kBwdWarps) {
+        const int l = lane & 15;
+        static_assert(kBwdWarps == 16, "a lane an end's sum");
+        for (int u0 = 2 * warp; u0 < p.bias.nb; u0 += 2 * kBwdWarps) {
           // bucket u holds the distances x with first[k] <= x < first[k + 1] on its
           // side, the last one also those of md and more; without buckets of their
           // own, keys behind the query count as distance 0
-          const int k = u % p.bias.side;
-          const bool pos = p.bias.both && u >= p.bias.side, last = k + 1 == p.bias.side;
-          const int from = firsts[k], to = last ? md : firsts[k + 1];
+          const int u = u0 + (lane >> 4);
           float a = 0.f;
-          for (int x = max(from, pos ? 1 : 0) + lane; x < min(to, md); x += 32) a += bins[md + (pos ? x : -x)];
-          if (last && lane < kBwdWarps) a += ends[(pos ? kBwdWarps : 0) + lane];
-          if (!p.bias.both && k == 0 && !p.causal) {
-            for (int x = 1 + lane; x < md; x += 32) a += bins[md + x];
-            if (lane < kBwdWarps) a += ends[kBwdWarps + lane];
+          if (u < p.bias.nb) {
+            const bool pos = p.bias.both && u >= p.bias.side;
+            const int k = pos ? u - p.bias.side : u;
+            const bool last = k + 1 == p.bias.side;
+            const int from = firsts[k], to = last ? md : firsts[k + 1];
+            for (int x = max(from, pos ? 1 : 0) + l; x < min(to, md); x += 16) a += bins[md + (pos ? x : -x)];
+            if (last) a += ends[(pos ? kBwdWarps : 0) + l];
+            if (!p.bias.both && k == 0 && !p.causal) {
+              for (int x = 1 + l; x < md; x += 16) a += bins[md + x];
+              a += ends[kBwdWarps + l];
+            }
           }
 #pragma unroll
-          for (int o = 16; o > 0; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
-          if (lane == 0) p.partial[items[slot].item * p.bias.nb + u] = a;
+          for (int o = 8; o > 0; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
+          if (u < p.bias.nb && l == 0) p.partial[items[slot].item * p.bias.nb + u] = a;
         }
-        named_bar(1, kN);
-        for (int i = threadIdx.x; i < 2 * md + 1; i += kN) bins[i] = 0.f;
+        for (int i = threadIdx.x; i < binn; i += kN) all_bins[(slot ^ 1) * binn + i] = 0.f;
       }
       if (lane == 0) mbar_arrive(bar(L::free_ + slot));
     }
