@@ -120,17 +120,6 @@ __device__ __forceinline__ void tmem_ld32_wait(uint32_t* r) {
                  "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]),
                  "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])::"memory");
 }
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], "
-      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31};" ::"r"(r[0]),
-      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]),
-      "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]),
-      "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(taddr)
-      : "memory");
-}
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], "
@@ -350,19 +339,12 @@ __device__ __forceinline__ void fill_map(const RcBias& b, uint8_t* map) {
   for (int i = threadIdx.x; i < table_floats(b.md); i += blockDim.x)
     map[i] = static_cast<uint8_t>(bucket_of(b, min(max(i - (b.md + kPad), -b.md), b.md)));
 }
-// tab[delta + md + kPad] = bias of the clamped distance, times log2 e; by
-// `threads` threads.
-__device__ __forceinline__ void fill_table(const RcParams& p, int head, const uint8_t* map, float* tab, int thread,
-                                           int threads) {
-  const int n = table_floats(p.bias.md);
-  for (int i = thread; i < n; i += threads)
-    tab[i] = __ldcg(p.table + static_cast<int64_t>(map[i]) * p.H + head) * kLog2e;
-}
-// The same by one warp, through the head's column of the table in `vals`; the
-// map's and the table's rows are padded to fours.
+// tab[delta + md + kPad] = bias of the clamped distance, times log2 e; by one warp,
+// through the head's column of the table in `vals`; the map's and the table's rows
+// are padded to fours.
 __device__ __forceinline__ void fill_table_warp(const RcParams& p, int head, const uint8_t* map, float* vals,
                                                 float* tab, int lane) {
-  for (int u = lane; u < p.bias.nb; u += 32) vals[u] = __ldg(p.table + static_cast<int64_t>(u) * p.H + head) * kLog2e;
+  for (int u = lane; u < p.bias.nb; u += 32) vals[u] = __ldcg(p.table + static_cast<int64_t>(u) * p.H + head) * kLog2e;
   __syncwarp();
   const int n = table_floats(p.bias.md);
 #pragma unroll 2
@@ -1315,8 +1297,10 @@ __global__ void __launch_bounds__(kDkvThreads, 1) rc_dkv_kernel(const __grid_con
   uint8_t* sO = sQ + L::kQ * L::kTile;
   Head* hd = reinterpret_cast<Head*>(sO + L::kO * L::kTile);
   float* vec = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(hd) + kBarBytes);  // [2][2][128]
-  float* tab = vec + 512;
-  uint8_t* map = reinterpret_cast<uint8_t*>(tab + (BIAS ? table_floats(p.bias.md) : 0));
+  float* tabs = vec + 512;  // tables of two query heads, the head's values, and the distances' buckets
+  const int tabn = BIAS ? table_floats(p.bias.md) : 0;
+  float* vals = tabs + 2 * tabn;
+  uint8_t* map = reinterpret_cast<uint8_t*>(vals + kMaxRelBuckets);
   if (BIAS) fill_map(p.bias, map);
   const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
   volatile DkvItem* items = reinterpret_cast<volatile DkvItem*>(hd->items);
@@ -1430,11 +1414,12 @@ __global__ void __launch_bounds__(kDkvThreads, 1) rc_dkv_kernel(const __grid_con
     if (lane == 0 && *w.abort_flag) fl.drain(bar0, p.wait_limit_ns);
     __syncwarp();
   } else if (warp == kBwdWarps + 3) {
-    // (-lse log2 e, -D) of the query tiles; a row past the sequence gets
-    // probability 2^(x - inf) = 0
+    // (-lse log2 e, -D) of the query tiles, and a query head's bias where it changes;
+    // a row past the sequence gets probability 2^(x - inf) = 0
     bool ok = true;
     uint32_t it = 0;
     if (early) pdl_wait();
+    int tslot = 1;  // of the query head's table: the next one is taken where the head changes
     for (uint32_t n = 0; ok; ++n) {
       const int slot = n & 1;
       if (!(ok = wait_warp(bar(L::info + slot), (n >> 1) & 1, w))) break;
@@ -1443,6 +1428,7 @@ __global__ void __launch_bounds__(kDkvThreads, 1) rc_dkv_kernel(const __grid_con
       if (lane == 0) mbar_arrive(bar(L::free_ + slot));
       if (k.kvh < 0) break;
       QueryWalk q = k.walk(p, rank);
+      int table_head = -1;
       for (int i = 0; i < k.total; ++i, ++it, q.next()) {
         const int buf = it & 1;
         float nl[4], nd[4];
@@ -1454,6 +1440,12 @@ __global__ void __launch_bounds__(kDkvThreads, 1) rc_dkv_kernel(const __grid_con
           nd[x] = pos < k.len ? -__ldcg(p.D + at) : 0.f;
         }
         if (!(ok = wait_warp(bar(L::vecempty + buf), ((it >> 1) & 1) ^ 1u, w))) break;
+        if (BIAS && table_head != q.g) {
+          // (the tile before the last one has been through: that head's table is free)
+          table_head = q.g;
+          tslot ^= 1;
+          fill_table_warp(p, q.g, map, vals, tabs + tslot * tabn, lane);
+        }
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
           vec[256 * buf + 32 * x + lane] = nl[x];
@@ -1546,43 +1538,28 @@ __global__ void __launch_bounds__(kDkvThreads, 1) rc_dkv_kernel(const __grid_con
     const uint32_t lb = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t tPw = tP + lb + 32 * part;
     const uint64_t scl2 = pack2(p.scale_log2, p.scale_log2);
-    // After a failed wait an item runs on without waiting: the named barriers
-    // need every warp, nothing is stored at its end, and all leave together.
+    // After a failed wait an item runs on without waiting and stores nothing.
     bool ok = true;
     if (early) pdl_wait();
-    int table_head = -1;
+    int tslot = 1;
     uint32_t it = 0;  // tiles so far
     for (uint32_t n = 0;; ++n) {
       const int slot = n & 1;
       ok = ok && wait_warp(bar(L::info + slot), (n >> 1) & 1, w);
-      // (without a bias there are no named barriers to keep to: a warp goes on while
-      // others still store)
-      if (BIAS ? named_bar_any(2, 32 * kBwdWarps, !ok) : !ok) break;
+      if (!ok) break;
       const Work k = read_item(slot);
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(L::free_ + slot));
       if (k.kvh < 0) break;
       QueryWalk q = k.walk(p, rank);
       const int kt = k.kt;
+      int table_head = -1;
       for (int i = 0; i < k.total; ++i, ++it, q.next()) {
         const int buf = it & 1;
         const uint32_t tSw = tS + lb + 32 * part + (kAhead && buf ? kOther : 0);
         if (BIAS && table_head != q.g) {
-          // the next query head's bias; every compute warp reads the table
           table_head = q.g;
-          named_bar(1, 32 * kBwdWarps);
-          fill_table(p, q.g, map, tab, threadIdx.x, 32 * kBwdWarps);
-          named_bar(1, 32 * kBwdWarps);
-        }
-        float add = 0.f;
-        bool near = false;
-        const float* tb = nullptr;
-        if (BIAS) {
-          const int side = bias_side(p.bias.md, 128 * q.i, 128 * kt);
-          near = side == 0;
-          if (!near) add = tab[side < 0 ? 0 : 2 * (p.bias.md + kPad)];
-          // distance of column c: key - query = (128 kt + key) - (128 i + 32 part + c)
-          tb = tab + (128 * (kt - q.i) + key - 32 * part + p.bias.md + kPad);
+          tslot ^= 1;
         }
         const float4* nl4 = reinterpret_cast<const float4*>(vec + 256 * buf + 32 * part);
         const float4* nd4 = reinterpret_cast<const float4*>(vec + 256 * buf + 128 + 32 * part);
@@ -1590,6 +1567,17 @@ __global__ void __launch_bounds__(kDkvThreads, 1) rc_dkv_kernel(const __grid_con
         tc_fence_after();
         uint32_t s[32];
         tmem_ld32_issue(tSw, s);
+        float add = 0.f;
+        bool near = false;
+        const float* tb = nullptr;
+        if (BIAS) {
+          const float* tab = tabs + tslot * tabn;
+          const int side = bias_side(p.bias.md, 128 * q.i, 128 * kt);
+          near = side == 0;
+          if (!near) add = tab[side < 0 ? 0 : 2 * (p.bias.md + kPad)];
+          // distance of column c: key - query = (128 kt + key) - (128 i + 32 part + c)
+          tb = tab + (128 * (kt - q.i) + key - 32 * part + p.bias.md + kPad);
+        }
         tmem_ld32_wait(s);
         const uint64_t add2v = pack2(add, add);
         const bool diagonal = p.causal && q.i == kt;
@@ -2498,8 +2486,8 @@ cudaError_t bwd_t(RcParams& p, int num_sms, cudaStream_t st) {
   }
   p.items = units * p.KV;
   p.slot = static_cast<int>(g_rc_slot_seq.fetch_add(1) % kRcSlots);
-  // (a table of floats and a byte a distance)
-  const int dkv_smem = (DkvShape<DP, BIAS>::kSmem) + 5 * n;
+  // (two tables of floats, a head's values, a byte a distance)
+  const int dkv_smem = (DkvShape<DP, BIAS>::kSmem) + 9 * n + (BIAS ? 4 * kMaxRelBuckets : 0);
   p.parts = cluster_parts(p, p.KV, p.group, false, num_sms);
   const auto dkv = p.parts > 1 ? rc_dkv_kernel<DP, BIAS, true> : rc_dkv_kernel<DP, BIAS, false>;
   e = launch_rc(dkv, p.parts > 1 ? p.items * p.parts : p.items < num_sms ? p.items : num_sms, kDkvThreads, dkv_smem, p,
