@@ -33,10 +33,10 @@
 // Measured on a GB300 (cuBLAS reaches 1.87 PFLOP/s in bf16 there), in matrix work
 // that the definition needs, four and ten flops a visible pair and column:
 //   causal, one sequence of 16384, 8 heads of 128, 2 K/V heads
-//     forward 341 us, 1.6 PFLOP/s; backward 1.20 ms, 1.15 PFLOP/s, which is 1.6
+//     forward 342 us, 1.6 PFLOP/s; backward 1.17 ms, 1.17 PFLOP/s, which is 1.64
 //     with the two products that are computed twice
-//   causal, 2 x 2048, 32 heads of 128: 63 us, 1.10 PFLOP/s; 201 us, 0.86 PFLOP/s
-//   bias of both directions, 4 x 1024, 16 heads of 64: 30 us; 105 us, 0.41 PFLOP/s:
+//   causal, 2 x 2048, 32 heads of 128: 62 us, 1.11 PFLOP/s; 198 us, 0.87 PFLOP/s
+//   bias of both directions, 4 x 1024, 16 heads of 64: 30 us; 100 us, 0.43 PFLOP/s:
 //     at 64 columns a product takes 256 cycles and the element-wise work as long as
 //     before, which is then the bound.
 // Every wait is bounded, as in the GEMM engine.
@@ -776,10 +776,10 @@ struct FwdShape {
 //
 // A tile of 128 x 128 x 128 is 1024 cycles of products and 16384 exponentials; a
 // pair of query tiles takes 2500 cycles against 2056 of products, since each waits
-// for the other's softmax at times.  16384, 8 heads of 128, causal: 341 us, 1.6
-// PFLOP/s (86% of cuBLAS), 2 x 2048, 32 heads: 63 us (59%: a sequence has 8.5 key
-// tiles a query tile, of which the diagonal's are half hidden, and an item costs
-// as much as 1.5 tiles beside them).  Two key and value tiles held, as much as fits
+// for the other's softmax at times.  16384, 8 heads of 128, causal: 342 us, 1.6
+// PFLOP/s (86% of cuBLAS), 2 x 2048, 32 heads: 62 us (59%: a sequence has 8.5 key
+// tiles a query tile, of which the diagonal's are half hidden, and an item's output
+// and first scores take as long as one or two tiles more).  Two key and value tiles held, as much as fits
 // beside two query tiles.
 //
 // Persistent: a CTA takes (query rows, head) items until there are none.  The
@@ -1266,11 +1266,14 @@ struct QueryWalk {
 // dV = sum over the query tiles of P^T dC, dK = scale sum of dS^T Q, in TMEM for the
 // whole item.  One warp issues the two products through P, another the two through
 // dS, so that each waits while the other's run.  At width 128 the products bound it:
-// 2240 cycles a tile against 2048 of products (with P and dS handed over in one
-// piece 2780).  At width 64 the 16 warps' own work does: 2500 cycles against 1024,
-// with 11 instructions a score issued in 57% of the cycles.  P and dS in TMEM
-// columns of their own there, so that the products run a tile further ahead, was
-// 10% slower: two more waits a tile cost more than they hid.
+// 2240 to 2450 cycles a tile against 2048 of products (with P and dS handed over in
+// one piece 2780), and 5000 an item beside them: 3500 for 64 KB of dK and dV, which
+// an SM stores at 32 bytes a cycle at best.  (To store them under the next item's
+// first tile took as long: the 16 warps have no time to spare there.)  At width 64
+// the warps' own work bounds it: 1800 cycles a tile against 1024, with 11
+// instructions a score issued in 57% of the cycles, and 2900 an item.  P and dS in
+// TMEM columns of their own there, so that the products run a tile further ahead,
+// was 10% slower: two more waits a tile cost more than they hid.
 //
 // SPLIT: the CTAs of a cluster share an item, each with every p.parts-th query
 // tile.  Their sums meet in shared memory, where each CTA adds up its part of
@@ -1774,9 +1777,11 @@ __host__ __device__ constexpr int grad_floats(int md) {
 }
 
 // dQ = scale sum over the key tiles of dS K, and D = dC . C of its rows.  At width
-// 128: 1955 cycles a tile against 1536 of its three products, which wait for dS; Q
-// and dC read from shared memory each time 3440.  At width 64 with the bias's
-// gradient 3300 cycles against 768: the 16 warps' work, 14 instructions a score.
+// 128: 1800 cycles a tile against 1536 of its three products, which wait for dS (Q
+// and dC read from shared memory each time: 3440), and 6000 an item beside its
+// tiles: Q and dC to TMEM, D, the last item's output, the first scores.  At width 64
+// with the bias's gradient 2000 to 2300 cycles against 768, the 16 warps' work with
+// 14 instructions a score, and 6000 an item, of which 2000 for its sums by bucket.
 //
 // The bias's gradient: a tile within the largest distance sums its dS along the
 // diagonals by shuffles (1500 cycles, of which the shuffles are most; one running
