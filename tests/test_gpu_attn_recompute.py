@@ -396,6 +396,60 @@ def test_two_streams_at_once():
         assert torch.equal(ya, ga) and torch.equal(yb, gb)
 
 
+@pytest.mark.parametrize("few", [False, True])
+@pytest.mark.parametrize("bias", [None, BIAS])
+def test_calls_in_a_row_on_the_same_buffers(bias, few):
+    """Training steps: the same buffers with other values, sequences and tables, and no wait in between, give the
+    bits of calls apart from each other, each launch waiting for the one before."""
+    tp = _tp()
+    H, KV, d, T = (2, 1, 128, 1500) if few else (16, 4, 64, 700)
+    steps = []
+    for k in range(5):
+        cut = 100 + 130 * k
+        c = Case([cut, T - cut], H, KV, d, 1, True, bias=bias, seed=200 + k, packed=True)
+        steps.append(c)
+    ws = torch.empty(tp.tp_attn_recompute_workspace_size(steps[0].cfg, T, bias), dtype=torch.uint8, device="cuda")
+    dev = [(c.QKV.cuda(), c.dC.cuda(), torch.tensor(c.starts, device="cuda"), c.table.cuda() if bias else None)
+           for c in steps]
+    buf = [None if x is None else torch.zeros_like(x) for x in dev[0]]
+    bf = dict(dtype=torch.bfloat16, device="cuda")
+    C, lse, dQ = torch.zeros(T, H * d, **bf), torch.zeros(H, T, device="cuda"), torch.zeros_like(dev[0][0])
+    dt = torch.zeros(bias["num_buckets"], H, device="cuda") if bias else None
+
+    def step(k, keep):
+        for b, x in zip(buf, dev[k]):
+            if b is not None:
+                b.copy_(x)
+        Q, dC, starts, table = buf
+        cfg = dict(steps[k].cfg, s=None)
+        if bias:
+            tp.tp_attn_relbias_fwd(Q, cfg, bias, table, C, lse, seq_starts=starts)
+            tp.tp_attn_relbias_bwd(Q, cfg, bias, table, C, lse, dC, dQ, dt, ws, seq_starts=starts)
+        else:
+            tp.tp_attn_recompute_fwd(Q, cfg, C, lse, seq_starts=starts)
+            tp.tp_attn_recompute_bwd(Q, cfg, C, lse, dC, dQ, ws, seq_starts=starts)
+        for o, x in zip(keep, (C, lse, dQ, dt)):
+            if o is not None:
+                o.copy_(x)
+
+    outs = [[None if x is None else torch.zeros_like(x) for x in (C, lse, dQ, dt)] for _ in range(30)]
+    want = [[None if x is None else torch.zeros_like(x) for x in (C, lse, dQ, dt)] for _ in steps]
+    tp.tp_debug_set_pdl(0)
+    try:
+        for k in range(len(steps)):
+            step(k, want[k])
+            torch.cuda.synchronize()
+    finally:
+        tp.tp_debug_set_pdl(1)
+    for n, keep in enumerate(outs):
+        step(n % len(steps), keep)
+    torch.cuda.synchronize()
+    assert tp.tp_get_status() == tp.TP_OK
+    for n, keep in enumerate(outs):
+        for x, y in zip(keep, want[n % len(steps)]):
+            assert x is None or torch.equal(x, y)
+
+
 def test_attention_block_as_used():
     """QKV projection, attention without stored probabilities, output projection, and back, with shards: the
     gradients of the weights and of the input against the fp64 oracle's chain."""
