@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from typing import Optional, Sequence
 
 import torch
@@ -102,7 +103,7 @@ class tp_relbias_config(ctypes.Structure):
                 ("bidirectional", ctypes.c_int32)]
 
 
-_PCFG, _PBIAS = ctypes.POINTER(tp_attn_config), ctypes.POINTER(tp_relbias_config)
+_ATTN_CONFIG, _RELBIAS_CONFIG = struct.Struct("3q5if"), struct.Struct("3i")  # the same fields, as bytes
 
 _SIGNATURES = {
     "tp_mlp_fwd": (_int, [_int, _i64, _i64, _i64, _int, _c_void_p, _PP, _PP, _PP, _c_void_p,
@@ -159,16 +160,16 @@ _SIGNATURES = {
                                         ctypes.c_uint64, ctypes.c_uint64, _c_void_p, _c_void_p,
                                         _c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_void_p, _size_t,
                                         _c_void_p]),
-    "tp_attn_recompute_fwd": (_int, [_int, _PCFG, _c_void_p, _c_void_p, _i64, _c_void_p, _i64, _c_void_p,
+    "tp_attn_recompute_fwd": (_int, [_int, _c_void_p, _c_void_p, _c_void_p, _i64, _c_void_p, _i64, _c_void_p,
                                      _c_void_p]),
-    "tp_attn_recompute_bwd": (_int, [_int, _PCFG, _c_void_p, _c_void_p, _i64, _c_void_p, _i64, _c_void_p,
+    "tp_attn_recompute_bwd": (_int, [_int, _c_void_p, _c_void_p, _c_void_p, _i64, _c_void_p, _i64, _c_void_p,
                                      _c_void_p, _i64, _c_void_p, _i64, _c_void_p, _size_t, _c_void_p]),
-    "tp_attn_relbias_fwd": (_int, [_int, _PCFG, _PBIAS, _c_void_p, _c_void_p, _c_void_p, _i64, _c_void_p, _i64,
+    "tp_attn_relbias_fwd": (_int, [_int, _c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_void_p, _i64, _c_void_p, _i64,
                                    _c_void_p, _c_void_p]),
-    "tp_attn_relbias_bwd": (_int, [_int, _PCFG, _PBIAS, _c_void_p, _c_void_p, _c_void_p, _i64, _c_void_p, _i64,
+    "tp_attn_relbias_bwd": (_int, [_int, _c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_void_p, _i64, _c_void_p, _i64,
                                    _c_void_p, _c_void_p, _i64, _c_void_p, _i64, _c_void_p, _int, _c_void_p,
                                    _size_t, _c_void_p]),
-    "tp_attn_recompute_workspace_size": (_size_t, [_PCFG, _PBIAS]),
+    "tp_attn_recompute_workspace_size": (_size_t, [_c_void_p, _c_void_p]),
     "tp_position_embed_dropout": (_int, [_i64, _i64, _i64, _c_void_p, _c_void_p, _c_void_p,
                                          ctypes.c_float, ctypes.c_uint64, ctypes.c_uint64, _c_void_p,
                                          _c_void_p]),
@@ -548,13 +549,21 @@ def _vec(t, name, dtype, shape, index):
     _refuse(t, name, dtype, shape, index)
 
 
-def _attn_cfg(cfg: dict, T: int) -> tp_attn_config:
-    return tp_attn_config(T, cfg["b"], cfg.get("s") or 0, cfg["n_heads"], cfg["n_kv_heads"], cfg["d"], cfg["N"],
-                          1 if cfg["causal"] else 0, cfg.get("scale") or 0.0)
+def _attn_cfg(cfg: dict, T: int) -> bytes:
+    """The tp_attn_config of cfg, packed."""
+    try:
+        return _ATTN_CONFIG.pack(T, cfg["b"], cfg.get("s") or 0, cfg["n_heads"], cfg["n_kv_heads"], cfg["d"], cfg["N"],
+                                 1 if cfg["causal"] else 0, cfg.get("scale") or 0.0)
+    except struct.error as e:
+        raise ValueError(f"cfg: {e}") from None
 
 
-def _bias_cfg(bias: dict) -> tp_relbias_config:
-    return tp_relbias_config(bias["num_buckets"], bias["max_distance"], 1 if bias["bidirectional"] else 0)
+def _bias_cfg(bias: dict) -> bytes:
+    """The tp_relbias_config of bias, packed."""
+    try:
+        return _RELBIAS_CONFIG.pack(bias["num_buckets"], bias["max_distance"], 1 if bias["bidirectional"] else 0)
+    except struct.error as e:
+        raise ValueError(f"bias: {e}") from None
 
 
 def _attn_common(QKV, cfg, C, lse, seq_starts):
@@ -588,9 +597,7 @@ def _scratch(workspace, index):
 
 def tp_attn_recompute_workspace_size(cfg: dict, T: int, bias: Optional[dict] = None) -> int:
     """Bytes of the backward's workspace for T token rows (bias: if its table's gradient is asked for)."""
-    c = _attn_cfg(cfg, T)
-    b = None if bias is None else ctypes.byref(_bias_cfg(bias))
-    return int(lib().tp_attn_recompute_workspace_size(ctypes.byref(c), b))
+    return int(lib().tp_attn_recompute_workspace_size(_attn_cfg(cfg, T), None if bias is None else _bias_cfg(bias)))
 
 
 def tp_attn_recompute_fwd(QKV, cfg, C, lse, seq_starts=None, stream=None):

@@ -64,6 +64,7 @@ constexpr int kFwdWarps = 16, kBwdWarps = 16;
 constexpr int kFwdThreads = 32 * (kFwdWarps + 4), kDkvThreads = 32 * (kBwdWarps + 4), kDqThreads = 32 * (kBwdWarps + 3);
 constexpr int kPanel = 128 * 128;    // bytes of 128 rows x 64 bf16 columns (one swizzle width)
 constexpr int kBarBytes = 512;
+constexpr int kMaxSmem = 227 * 1024;  // of a CTA
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -2402,11 +2403,20 @@ int cluster_parts(const RcParams& p, int heads, int mult, bool once, int num_sms
   return parts;
 }
 
-// In clusters of p.parts CTAs.
-template <class K>
-cudaError_t launch_rc(K kernel, int64_t blocks, int threads, int smem, const RcParams& p, cudaStream_t st) {
-  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+// In clusters of p.parts CTAs.  The shared memory that a kernel may have is raised
+// once a device, to all there is.
+template <auto kernel>
+cudaError_t launch_rc(int64_t blocks, int threads, int smem, const RcParams& p, cudaStream_t st) {
+  constexpr int kDevices = 16;  // (on later ones it is set each time)
+  static std::atomic<int> granted[kDevices];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
+  if (dev >= kDevices || granted[dev].load(std::memory_order_acquire) == 0) {
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
+    if (e != cudaSuccess) return e;
+    if (dev < kDevices) granted[dev].store(1, std::memory_order_release);
+  }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(blocks));
   cfg.blockDim = dim3(static_cast<unsigned>(threads));
@@ -2463,8 +2473,8 @@ cudaError_t fwd_t(RcParams& p, int num_sms, cudaStream_t st) {
   p.parts = cluster_parts(p, p.H, 1, true, num_sms);
   p.sub = p.parts > 1 ? 1 : query_tiles(p, num_sms);
   p.items = units_of(p, 128 * p.sub) * p.H;
-  if (p.parts > 1) return launch_rc(rc_fwd_kernel<DP, BIAS, true>, p.items * p.parts, kFwdThreads, smem, p, st);
-  return launch_rc(rc_fwd_kernel<DP, BIAS, false>, p.items < num_sms ? p.items : num_sms, kFwdThreads, smem, p, st);
+  if (p.parts > 1) return launch_rc<rc_fwd_kernel<DP, BIAS, true>>(p.items * p.parts, kFwdThreads, smem, p, st);
+  return launch_rc<rc_fwd_kernel<DP, BIAS, false>>(p.items < num_sms ? p.items : num_sms, kFwdThreads, smem, p, st);
 }
 template <int DP, bool BIAS>
 cudaError_t bwd_t(RcParams& p, int num_sms, cudaStream_t st) {
@@ -2479,9 +2489,9 @@ cudaError_t bwd_t(RcParams& p, int num_sms, cudaStream_t st) {
   const int dq_smem =
       (DqShape<DP, BIAS>::kSmem) + 9 * n + (BIAS ? 4 * (kMaxRelBuckets + grad_floats(p.bias.md)) : 0);
   if (!BIAS) p.parts = cluster_parts(p, p.H, 1, false, num_sms);
-  const auto dq = p.parts > 1 ? rc_dq_kernel<DP, BIAS, !BIAS> : rc_dq_kernel<DP, BIAS, false>;
-  cudaError_t e = launch_rc(dq, p.parts > 1 ? p.items * p.parts : p.items < num_sms ? p.items : num_sms, kDqThreads,
-                            dq_smem, p, st);
+  cudaError_t e = p.parts > 1 ? launch_rc<rc_dq_kernel<DP, BIAS, !BIAS>>(p.items * p.parts, kDqThreads, dq_smem, p, st)
+                              : launch_rc<rc_dq_kernel<DP, BIAS, false>>(p.items < num_sms ? p.items : num_sms,
+                                                                         kDqThreads, dq_smem, p, st);
   p.fault_skip = 0;
   if (e != cudaSuccess) return e;
   if (BIAS && p.partial != nullptr) {
@@ -2494,9 +2504,9 @@ cudaError_t bwd_t(RcParams& p, int num_sms, cudaStream_t st) {
   // (two tables of floats, a head's values, a byte a distance)
   const int dkv_smem = (DkvShape<DP, BIAS>::kSmem) + 9 * n + (BIAS ? 4 * kMaxRelBuckets : 0);
   p.parts = cluster_parts(p, p.KV, p.group, false, num_sms);
-  const auto dkv = p.parts > 1 ? rc_dkv_kernel<DP, BIAS, true> : rc_dkv_kernel<DP, BIAS, false>;
-  e = launch_rc(dkv, p.parts > 1 ? p.items * p.parts : p.items < num_sms ? p.items : num_sms, kDkvThreads, dkv_smem, p,
-                st);
+  e = p.parts > 1 ? launch_rc<rc_dkv_kernel<DP, BIAS, true>>(p.items * p.parts, kDkvThreads, dkv_smem, p, st)
+                  : launch_rc<rc_dkv_kernel<DP, BIAS, false>>(p.items < num_sms ? p.items : num_sms, kDkvThreads,
+                                                              dkv_smem, p, st);
   p.parts = 1;
   return e;
 }

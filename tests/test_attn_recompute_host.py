@@ -183,6 +183,23 @@ def test_other_refusals_backward():
     assert bwd(T=0, b=0) == tp.TP_OK
 
 
+def test_packed_sizes():
+    """What the binding packs are the C structs; numbers that do not fit their fields are refused, not cut."""
+    c = dict(b=2, s=128, n_heads=4, n_kv_heads=2, d=64, N=2, causal=True, scale=0.25)
+    assert tp._attn_cfg(c, 256) == bytes(tp.tp_attn_config(256, 2, 128, 4, 2, 64, 2, 1, 0.25))
+    assert tp._attn_cfg(dict(c, s=None, scale=None, causal=False), 7) == \
+        bytes(tp.tp_attn_config(7, 2, 0, 4, 2, 64, 2, 0, 0.0))
+    assert tp._bias_cfg(dict(num_buckets=32, max_distance=128, bidirectional=True)) == \
+        bytes(tp.tp_relbias_config(32, 128, 1))
+    for bad in (dict(n_heads=(1 << 32) + 4), dict(b=1 << 63), dict(d=64.5)):
+        with pytest.raises(ValueError):
+            tp._attn_cfg(dict(c, **bad), 256)
+    # (beyond fp32 is infinite, which the library refuses)
+    assert L.tp_attn_recompute_workspace_size(tp._attn_cfg(dict(c, scale=1e300), 256), None) == 0
+    with pytest.raises(ValueError):
+        tp._bias_cfg(dict(num_buckets=(1 << 32) + 32, max_distance=128, bidirectional=0))
+
+
 @pytest.mark.parametrize("nb,md,both", [(1, 128, 0), (0, 128, 0), (257, 1000, 0), (33, 128, 1), (2, 128, 1), (32, 16, 0),
                                          (32, 8, 1), (32, 1025, 0), (-4, 128, 0), (32, -1, 1)])
 def test_bias_refused(nb, md, both):
