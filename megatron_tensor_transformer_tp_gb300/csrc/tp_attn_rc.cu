@@ -1766,15 +1766,16 @@ struct DqShape {
 // What the TMA warp tells the other warps of an item (two slots).
 struct DqItem {
   int start, len, r0, head, nk;  // r0: position of the first query row; head -1: no more items
+  int col;                       // the head's first column of Q
   int64_t item;
 };
 
 // The bias gradient's shared memory: per compute warp the sums of its 32 x 32
 // block by distance (63 of them), for two tiles; of two items the CTA's sums by
-// distance and the warps' sums beyond the ends; and the buckets' first distances.
+// distance and the warps' sums beyond the ends; and the buckets' ranges of distances.
 constexpr int kDiag = 64;
 __host__ __device__ constexpr int grad_floats(int md) {
-  return 2 * kBwdWarps * kDiag + 2 * (2 * md + 1) + 4 * kBwdWarps + kMaxRelBuckets;
+  return 2 * kBwdWarps * kDiag + 2 * (2 * md + 1) + 4 * kBwdWarps + 2 * kMaxRelBuckets;
 }
 
 // dQ = scale sum over the key tiles of dS K, and D = dC . C of its rows.  At width
@@ -1809,12 +1810,24 @@ __global__ void __launch_bounds__(kDqThreads, 1) rc_dq_kernel(const __grid_const
   const int binn = 2 * md + 1;
   float* all_bins = diag + 2 * kBwdWarps * kDiag;                   // [2][2 md + 1]
   float* all_ends = all_bins + 2 * binn;                            // [2][2][kBwdWarps]
-  int* firsts = reinterpret_cast<int*>(all_ends + 4 * kBwdWarps);   // p.bias.first: indexed reads of it are slow
+  int* from = reinterpret_cast<int*>(all_ends + 4 * kBwdWarps);     // the buckets' bins: from here
+  int* to = from + kMaxRelBuckets;                                  // to before here (and which ends: bits 16, 17)
   const bool grad = BIAS && p.partial != nullptr;
   if (BIAS) fill_map(p.bias, map);
   if (grad) {
     for (int i = threadIdx.x; i < 2 * binn; i += kDqThreads) all_bins[i] = 0.f;
-    for (int i = threadIdx.x; i < p.bias.side; i += kDqThreads) firsts[i] = p.bias.first[i];
+    // Bucket u holds the distances x with first[k] <= x < first[k + 1] on its side,
+    // the last one also those of md and more; without buckets of their own, keys
+    // behind the query count as distance 0.
+    for (int u = threadIdx.x; u < p.bias.nb; u += kDqThreads) {
+      const bool pos = p.bias.both && u >= p.bias.side;
+      const int k = pos ? u - p.bias.side : u;
+      const bool last = k + 1 == p.bias.side, all = !p.bias.both && k == 0;
+      const int x0 = min(max(p.bias.first[k], pos ? 1 : 0), md), x1 = last ? md : min(p.bias.first[k + 1], md);
+      from[u] = pos ? md + x0 : md - x1 + 1;
+      to[u] = (all ? 2 * md : pos ? md + x1 : md - x0 + 1) | (last && !pos ? 1 << 16 : 0) |
+              ((last && pos) || all ? 1 << 17 : 0);
+    }
   }
   const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
   enter<kBwdWarps>(hd, L::count, L::template arrivals<BIAS>);
@@ -1850,18 +1863,19 @@ __global__ void __launch_bounds__(kDqThreads, 1) rc_dq_kernel(const __grid_const
       const int nk_all = (u.len + 127) >> 7;
       int nk = p.causal ? min(nk_all, u.tile + 1) : nk_all;
       if (SPLIT) nk = max(0, nk - rank + p.parts - 1) / p.parts;  // (may be none)
+      const HeadAt hq = head_at(items_of.index, p.hq), hk = head_at(items_of.index / p.group, p.hk);
       if (lane == 0) {
         items[slot].start = u.start;
         items[slot].len = u.len;
         items[slot].r0 = 128 * u.tile;
         items[slot].head = found ? items_of.index : -1;
+        items[slot].col = hq.shard * p.shard_w + hq.local * p.d;
         items[slot].nk = nk;
         items[slot].item = items_of.item;
         mbar_arrive(bar(L::info + slot));
       }
       if (!found) break;
       if (SPLIT && nk == 0) continue;
-      const HeadAt hq = head_at(items_of.index, p.hq), hk = head_at(items_of.index / p.group, p.hk);
       // Q and dC pass through a K and a V stage on their way to TMEM
       if (lane == 0) {
         ok = wait_bounded(bar(L::kempty + kr.stage), kr.phase ^ 1u, w);
@@ -2256,9 +2270,8 @@ __global__ void __launch_bounds__(kDqThreads, 1) rc_dq_kernel(const __grid_const
         if (!SPLIT) pack_columns<32>(r, p.scale, dq);
       }
       tc_fence_before();
-      const HeadAt hq = head_at(uniform(items[slot].head), p.hq);
       prev = static_cast<__nv_bfloat16*>(p.dQKV) + (static_cast<int64_t>(items[slot].start) + row) * p.ld_dqkv +
-             static_cast<int64_t>(hq.shard) * p.shard_w + static_cast<int64_t>(hq.local) * p.d + ofirst;
+             items[slot].col + ofirst;
       if (SPLIT || ocols <= 0) prev = nullptr;  // (the whole warp)
       stored = ok && mine;
       if (BIAS && grad) {
@@ -2284,22 +2297,14 @@ __global__ void __launch_bounds__(kDqThreads, 1) rc_dq_kernel(const __grid_const
         const int l = lane & 15;
         static_assert(kBwdWarps == 16, "a lane an end's sum");
         for (int u0 = 2 * warp; u0 < p.bias.nb; u0 += 2 * kBwdWarps) {
-          // bucket u holds the distances x with first[k] <= x < first[k + 1] on its
-          // side, the last one also those of md and more; without buckets of their
-          // own, keys behind the query count as distance 0
           const int u = u0 + (lane >> 4);
           float a = 0.f;
           if (u < p.bias.nb) {
-            const bool pos = p.bias.both && u >= p.bias.side;
-            const int k = pos ? u - p.bias.side : u;
-            const bool last = k + 1 == p.bias.side;
-            const int from = firsts[k], to = last ? md : firsts[k + 1];
-            for (int x = max(from, pos ? 1 : 0) + l; x < min(to, md); x += 16) a += bins[md + (pos ? x : -x)];
-            if (last) a += ends[(pos ? kBwdWarps : 0) + l];
-            if (!p.bias.both && k == 0 && !p.causal) {
-              for (int x = 1 + l; x < md; x += 16) a += bins[md + x];
-              a += ends[kBwdWarps + l];
-            }
+            const int end = to[u];
+#pragma unroll 1
+            for (int x = from[u] + l; x < (end & 0xffff); x += 16) a += bins[x];
+            if (end & (1 << 16)) a += ends[l];
+            if (end & (1 << 17)) a += ends[kBwdWarps + l];
           }
 #pragma unroll
           for (int o = 8; o > 0; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
