@@ -1666,6 +1666,11 @@ __global__ void __launch_bounds__(kDkvThreads, 1) rc_dkv_kernel(const __grid_con
       // dV by the first half of the warps, dK by the second; two warps share a row
       const int which = part >> 1, cut = SPLIT ? DP / 2 : first_columns(p.d);
       const int first = part & 1 ? cut : 0, cols = part & 1 ? p.d - cut : cut;
+      const HeadAt hk = head_at(k.kvh, p.hk);
+      const int pos = 128 * kt + key;
+      __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.dQKV) + (static_cast<int64_t>(k.start) + pos) * p.ld_dqkv +
+                           static_cast<int64_t>(hk.shard) * p.shard_w + static_cast<int64_t>(p.hq) * p.d +
+                           static_cast<int64_t>(hk.local + (which ? 0 : p.hk)) * p.d + first;
       uint32_t r[DP / 2];
       if (SPLIT && k.total <= 0) {
 #pragma unroll
@@ -1691,16 +1696,7 @@ __global__ void __launch_bounds__(kDkvThreads, 1) rc_dkv_kernel(const __grid_con
               make_float4(as_f(r[c]), as_f(r[c + 1]), as_f(r[c + 2]), as_f(r[c + 3]));
         continue;
       }
-      const int pos = 128 * kt + key;
-      {
-        const HeadAt hk = head_at(k.kvh, p.hk);
-        const int64_t col = static_cast<int64_t>(hk.shard) * p.shard_w + static_cast<int64_t>(p.hq) * p.d +
-                            static_cast<int64_t>(hk.local + (which ? 0 : p.hk)) * p.d + first;
-        store_columns<DP / 2>(r, cols, which ? p.scale : 1.f, ok && pos < k.len,
-                              static_cast<__nv_bfloat16*>(p.dQKV) +
-                                  (static_cast<int64_t>(k.start) + pos) * p.ld_dqkv + col,
-                              p.ld_dqkv, p.wide);
-      }
+      store_columns<DP / 2>(r, cols, which ? p.scale : 1.f, ok && pos < k.len, out, p.ld_dqkv, p.wide);
       __syncwarp();
     }
   }
