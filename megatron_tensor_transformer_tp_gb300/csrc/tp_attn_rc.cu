@@ -33,10 +33,10 @@
 // Measured on a GB300 (cuBLAS reaches 1.87 PFLOP/s in bf16 there), in matrix work
 // that the definition needs, four and ten flops a visible pair and column:
 //   causal, one sequence of 16384, 8 heads of 128, 2 K/V heads
-//     forward 342 us, 1.6 PFLOP/s; backward 1.17 ms, 1.17 PFLOP/s, which is 1.64
+//     forward 342 us, 1.6 PFLOP/s; backward 1.16 ms, 1.18 PFLOP/s, which is 1.66
 //     with the two products that are computed twice
-//   causal, 2 x 2048, 32 heads of 128: 62 us, 1.11 PFLOP/s; 198 us, 0.87 PFLOP/s
-//   bias of both directions, 4 x 1024, 16 heads of 64: 30 us; 100 us, 0.43 PFLOP/s:
+//   causal, 2 x 2048, 32 heads of 128: 62 us, 1.11 PFLOP/s; 194 us, 0.89 PFLOP/s
+//   bias of both directions, 4 x 1024, 16 heads of 64: 30 us; 97 us, 0.44 PFLOP/s:
 //     at 64 columns a product takes 256 cycles and the element-wise work as long as
 //     before, which is then the bound.
 // Every wait is bounded, as in the GEMM engine.
@@ -1779,7 +1779,7 @@ __host__ __device__ constexpr int grad_floats(int md) {
 // and dC read from shared memory each time: 3440), and 6000 an item beside its
 // tiles: Q and dC to TMEM, D, the last item's output, the first scores.  At width 64
 // with the bias's gradient 2000 to 2300 cycles against 768, the 16 warps' work with
-// 14 instructions a score, and 6000 an item, of which 2000 for its sums by bucket.
+// 14 instructions a score, and 5000 an item, of which 1000 for its sums by bucket.
 //
 // The bias's gradient: a tile within the largest distance sums its dS along the
 // diagonals by shuffles (1500 cycles, of which the shuffles are most; one running
