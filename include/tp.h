@@ -314,7 +314,8 @@ typedef struct {
  *   lse         (n_heads, T) fp32
  *   dQKV        out, as QKV, pitch ld_dqkv; every column of a sequence's rows is written
  *   workspace   tp_attn_recompute_workspace_size bytes, 256-byte aligned (backward)
- * Scores, softmax and D are fp32; the probabilities and dS are rounded to bf16
+ * Scores, softmax and D are fp32 (scores of magnitude M leave probabilities off
+ * by about 2^-22 M of themselves); the probabilities and dS are rounded to bf16
  * as operands of their products.  No (s x s) matrix is stored.  Sums have a
  * fixed order: equal calls give equal bits.
  * Rows of one sequence never depend on another sequence's values, whatever
@@ -344,9 +345,12 @@ TP_API tp_status tp_attn_recompute_bwd(tp_dtype dt, const tp_attn_config* cfg, c
  *           of bucket u in every sequence (fp32 dS, before its rounding; accumulate:
  *           added to the old value), or NULL: not computed
  * The bias is added inside the kernels and its gradient summed there, in a
- * fixed order.  Entries are finite or -infinity; those below -2.3e38 count as
- * -infinity, which hides the bucket's keys.  A row that sees no key has C = 0,
- * lse = -infinity and no gradient.
+ * fixed order.  Entries are numbers of at most 131072; those below -131072 count as
+ * -infinity, which hides the bucket's keys: lse is fp32, and up to there the
+ * backward's probabilities are off by no more of themselves than their rounding
+ * to bf16.  A row that sees no key has C = 0, lse = -infinity and no gradient.
+ * With an entry above 131072 the results are unspecified and tp_get_status
+ * returns TP_ERR_INVALID.
  */
 TP_API tp_status tp_attn_relbias_fwd(tp_dtype dt, const tp_attn_config* cfg, const tp_relbias_config* bias,
                                      const float* table, const int64_t* seq_starts, const void* QKV,
@@ -713,7 +717,7 @@ TP_API size_t tp_adam_step_workspace_size(void);
 /* Synchronises `stream`, then reads and clears the device error word of the
  * current device: TP_OK, TP_ERR_TIMEOUT (a bounded wait expired),
  * TP_ERR_INVALID (sequence starts on the device that decrease or leave the
- * buffers), or TP_ERR_CUDA (a CUDA error, sticky or not). */
+ * buffers, a bias's table with an entry above its range), or TP_ERR_CUDA (a CUDA error, sticky or not). */
 TP_API tp_status tp_get_status(void* stream);
 
 /* Human-readable name of a status code (static string). */

@@ -627,7 +627,8 @@ def tp_attn_recompute_bwd(QKV, cfg, C, lse, dC, dQKV, workspace, seq_starts=None
 def tp_attn_relbias_fwd(QKV, cfg, bias, table, C, lse, seq_starts=None, stream=None):
     """tp_attn_recompute_fwd with table[bucket(key - query), head] added to the scores.
 
-    bias: dict with num_buckets, max_distance, bidirectional; table (num_buckets, n_heads) fp32."""
+    bias: dict with num_buckets, max_distance, bidirectional; table (num_buckets, n_heads) fp32, entries of at
+    most 131072 (others are reported by tp_get_status); those below -131072 hide their keys."""
     c, q, o, l, st, _, _, dev = _attn_common(QKV, cfg, C, lse, seq_starts)
     t = _vec(table, "table", torch.float32, (bias["num_buckets"], cfg["n_heads"]), dev)
     _check(lib().tp_attn_relbias_fwd(TP_BF16, c, _bias_cfg(bias), t, st, q[0], q[1], o[0], o[1], l,

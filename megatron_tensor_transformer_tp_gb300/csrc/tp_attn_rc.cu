@@ -67,6 +67,11 @@ constexpr int kBarBytes = 512;
 constexpr int kMaxSmem = 227 * 1024;  // of a CTA
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kLn2Rest = static_cast<float>(0.6931471805599453094 - static_cast<double>(kLn2));
+// Finite entries of the bias's table: half a step of an lse of this size is 2^-8,
+// which is what the backward's probabilities are then off by, as much as their
+// rounding to bf16.  Entries below count as -infinity, those above are reported.
+constexpr float kMaxEntry = 131072.f;
 
 // The smem distance table covers [-(md + kPad), md + kPad], so that a tile that
 // holds any distance inside (-md, md) indexes it without clamping.
@@ -340,12 +345,19 @@ __device__ __forceinline__ void fill_map(const RcBias& b, uint8_t* map) {
   for (int i = threadIdx.x; i < table_floats(b.md); i += blockDim.x)
     map[i] = static_cast<uint8_t>(bucket_of(b, min(max(i - (b.md + kPad), -b.md), b.md)));
 }
-// tab[delta + md + kPad] = bias of the clamped distance, times log2 e; by one warp,
-// through the head's column of the table in `vals`; the map's and the table's rows
-// are padded to fours.
+// tab[delta + md + kPad] = bias of the clamped distance; by one warp, through the
+// head's column of the table in `vals`; the map's and the table's rows are padded
+// to fours.  (Not times log2 e: the kernels take differences of entries and lse
+// first, which are exact where both are large and their probabilities are not 0.)
 __device__ __forceinline__ void fill_table_warp(const RcParams& p, int head, const uint8_t* map, float* vals,
                                                 float* tab, int lane) {
-  for (int u = lane; u < p.bias.nb; u += 32) vals[u] = __ldcg(p.table + static_cast<int64_t>(u) * p.H + head) * kLog2e;
+  bool high = false;
+  for (int u = lane; u < p.bias.nb; u += 32) {
+    const float v = __ldcg(p.table + static_cast<int64_t>(u) * p.H + head);
+    vals[u] = v < -kMaxEntry ? -INFINITY : v;
+    high |= v > kMaxEntry;
+  }
+  if (high) atomicOr(p.err, kErrInvalid);
   __syncwarp();
   const int n = table_floats(p.bias.md);
 #pragma unroll 2
@@ -565,9 +577,17 @@ __device__ __forceinline__ void tile_to_tmem(uint32_t taddr, const uint8_t* tile
   }
 }
 
-// What a row's log-sum-exp adds to its exponents; a row that saw no key has no
+// What a row's log-sum-exp adds to its scores; a row that saw no key has no
 // probabilities.
-__device__ __forceinline__ float row_shift(float lse) { return lse == -INFINITY ? -INFINITY : -lse * kLog2e; }
+__device__ __forceinline__ float row_shift(float lse) { return lse == -INFINITY ? -INFINITY : -lse; }
+// A row's log-sum-exp from its exponents' reference m (log2) and their sum l:
+// (m + log2 l) ln 2, where m ln 2 keeps what its rounding would lose, so that the
+// result is rounded once.
+__device__ __forceinline__ float row_lse(float m, float l) {
+  if (m == -INFINITY) return -INFINITY;
+  const float t = __fmul_rn(m, kLn2);  // (not to be joined with the sum below)
+  return t + fmaf(log2f(l), kLn2, fmaf(m, kLn2, -t) + m * kLn2Rest);
+}
 
 // The product of COLS columns from `first` of the thread's row of two tiles.
 template <int COLS>
@@ -768,8 +788,8 @@ struct FwdShape {
 };
 
 // One pass over the keys with a running reference m and sum l a row,
-//   O = sum_j 2^(x_j - m) v_j,  l = sum_j 2^(x_j - m),  C = O / l,
-//   lse = (m + log2 l) ln 2  (x in units of log2 e),
+//   O = sum_j 2^(x_j log2 e - m) v_j,  l = sum_j 2^(x_j log2 e - m),  C = O / l,
+//   lse = (m + log2 l) ln 2,
 // where m follows the row's maximum only when that has grown past m by 16, so O is
 // rescaled rarely and no term exceeds 2^16.  Scores and probabilities stay in TMEM;
 // probabilities are rounded to bf16 as operands of the second product, while l sums
@@ -1032,7 +1052,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) rc_fwd_kernel(const __grid_con
           if (lane == 0) mbar_arrive(bar(L::sread + t));
         }
         const int jk = key_tile(j), c0 = 128 * jk + 64 * half, r0 = row0 + 128 * t;
-        float mul = sl2, add = 0.f;  // x = s mul + add
+        float mul = sl2, add = 0.f;  // the exponents: s mul + add log2 e
         if (BIAS) {
           const int side = bias_side(p.bias.md, r0, 128 * jk);
           if (side != 0) {
@@ -1040,8 +1060,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1) rc_fwd_kernel(const __grid_con
           } else {
             const float* tb = tab + (c0 - row + p.bias.md + kPad);
 #pragma unroll
-            for (int c = 0; c < 64; ++c) s[c] = __float_as_uint(fmaf(as_f(s[c]), sl2, tb[c]));
-            mul = 1.f;
+            for (int c = 0; c < 64; ++c) s[c] = __float_as_uint(fmaf(as_f(s[c]), p.scale, tb[c]));
+            mul = kLog2e;
           }
         }
         if ((p.causal && 128 * jk + 127 > r0) || 128 * jk + 128 > len) {
@@ -1056,7 +1076,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) rc_fwd_kernel(const __grid_con
 #pragma unroll
           for (int c = 8 + q; c < 64; c += 8) mx[q] = fmaxf(fmaxf(mx[q], as_f(s[c])), as_f(s[c + 4]));
         }
-        const float mh = fmaf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), mul, add);
+        const float mh = fmaf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), mul, BIAS ? add * kLog2e : 0.f);
         // the product of the tile before has read its probabilities and added to the output
         if (kApart) {
           ok = ok && wait_warp(bar(L::pvdone + t), (np & 1) ^ 1, w);
@@ -1082,7 +1102,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1) rc_fwd_kernel(const __grid_con
           }
         }
         // (a row that has seen no key yet: its bias is -infinity everywhere)
-        const float off = add - (m == -INFINITY ? 0.f : m);
+        const float ref = m == -INFINITY ? 0.f : m;
+        const float off = BIAS ? fmaf(add, kLog2e, -ref) : -ref;
         const uint64_t scl2 = pack2(mul, mul), off2 = pack2(off, off);
         uint64_t sum[2] = {pack2(l0, l1), 0ull};
 #pragma unroll
@@ -1144,7 +1165,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) rc_fwd_kernel(const __grid_con
         store_columns<DP / 2>(o, olast - ofirst, l > 0.f ? 1.f / l : 0.f, mine,
                               static_cast<__nv_bfloat16*>(p.C) + token * p.ld_c + static_cast<int64_t>(head) * p.d + ofirst,
                               p.ld_c, p.wide);
-        if (mine && half == 0) p.lse[static_cast<int64_t>(head) * p.T + token] = (m + log2f(l)) * kLn2;
+        if (mine && half == 0) p.lse[static_cast<int64_t>(head) * p.T + token] = row_lse(m, l);
         __syncwarp();
         ++nq;
       } else if (SPLIT && t == 0) {
@@ -1194,7 +1215,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) rc_fwd_kernel(const __grid_con
         *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.C) + token * p.ld_c + static_cast<int64_t>(head) * p.d +
                                   4 * chunk) =
             make_uint2(pack_bf16x2(a.x * mul, a.y * mul), pack_bf16x2(a.z * mul, a.w * mul));
-        if (chunk == 0) p.lse[static_cast<int64_t>(head) * p.T + token] = (top + log2f(l)) * kLn2;
+        if (chunk == 0) p.lse[static_cast<int64_t>(head) * p.T + token] = row_lse(top, l);
       }
     }
     cluster_sync();
@@ -1212,7 +1233,7 @@ template <int DP, bool BIAS>
 struct DkvShape {
   static constexpr int kTile = DP / 64 * kPanel;
   static constexpr int kQ = DP == 128 ? (BIAS ? 2 : 3) : 4, kO = DP == 128 ? 2 : 4;  // Q and dC tiles held
-  static constexpr int kVec = 2 * 2 * 128 * 4;  // (-lse log2 e, -D) of two query tiles
+  static constexpr int kVec = 2 * 2 * 128 * 4;  // of two query tiles what is added to their exponents, and -D
   static constexpr int kSmem = (2 + kQ + kO) * kTile + kBarBytes + kVec;
   static constexpr int kvfull = 0, qfull = 1, ofull = qfull + kQ, tail = ofull + kO, qempty = tail + 1,
                        oempty = qempty + kQ, vecempty = oempty + kO, sfull = vecempty + 2,
@@ -1418,8 +1439,10 @@ __global__ void __launch_bounds__(kDkvThreads, 1) rc_dkv_kernel(const __grid_con
     if (lane == 0 && *w.abort_flag) fl.drain(bar0, p.wait_limit_ns);
     __syncwarp();
   } else if (warp == kBwdWarps + 3) {
-    // (-lse log2 e, -D) of the query tiles, and a query head's bias where it changes;
-    // a row past the sequence gets probability 2^(x - inf) = 0
+    // What is added to the exponents of the query tiles, and -D, and a query head's
+    // bias where it changes: -lse log2 e, in a tile of one distance with its bias,
+    // (bias - lse) log2 e; in other tiles with a bias -lse, for they take that difference
+    // for each key.  A row past the sequence gets probability 2^(x - inf) = 0.
     bool ok = true;
     uint32_t it = 0;
     if (early) pdl_wait();
@@ -1449,6 +1472,13 @@ __global__ void __launch_bounds__(kDkvThreads, 1) rc_dkv_kernel(const __grid_con
           table_head = q.g;
           tslot ^= 1;
           fill_table_warp(p, q.g, map, vals, tabs + tslot * tabn, lane);
+          __syncwarp();
+        }
+        const int side = BIAS ? bias_side(p.bias.md, 128 * q.i, 128 * k.kt) : 0;
+        if (!BIAS || side != 0) {
+          const float add = BIAS ? tabs[tslot * tabn + (side < 0 ? 0 : 2 * (p.bias.md + kPad))] : 0.f;
+#pragma unroll
+          for (int x = 0; x < 4; ++x) nl[x] = (BIAS ? nl[x] + add : nl[x]) * kLog2e;
         }
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
@@ -1541,7 +1571,7 @@ __global__ void __launch_bounds__(kDkvThreads, 1) rc_dkv_kernel(const __grid_con
     const int key = (warp & 3) * 32 + lane;  // row of the transposed tile
     const uint32_t lb = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t tPw = tP + lb + 32 * part;
-    const uint64_t scl2 = pack2(p.scale_log2, p.scale_log2);
+    const uint64_t scl2 = pack2(p.scale_log2, p.scale_log2), log2e2 = pack2(kLog2e, kLog2e);
     // After a failed wait an item runs on without waiting and stores nothing.
     bool ok = true;
     if (early) pdl_wait();
@@ -1571,19 +1601,14 @@ __global__ void __launch_bounds__(kDkvThreads, 1) rc_dkv_kernel(const __grid_con
         tc_fence_after();
         uint32_t s[32];
         tmem_ld32_issue(tSw, s);
-        float add = 0.f;
         bool near = false;
         const float* tb = nullptr;
         if (BIAS) {
-          const float* tab = tabs + tslot * tabn;
-          const int side = bias_side(p.bias.md, 128 * q.i, 128 * kt);
-          near = side == 0;
-          if (!near) add = tab[side < 0 ? 0 : 2 * (p.bias.md + kPad)];
+          near = bias_side(p.bias.md, 128 * q.i, 128 * kt) == 0;
           // distance of column c: key - query = (128 kt + key) - (128 i + 32 part + c)
-          tb = tab + (128 * (kt - q.i) + key - 32 * part + p.bias.md + kPad);
+          tb = tabs + tslot * tabn + (128 * (kt - q.i) + key - 32 * part + p.bias.md + kPad);
         }
         tmem_ld32_wait(s);
-        const uint64_t add2v = pack2(add, add);
         const bool diagonal = p.causal && q.i == kt;
         const int first = key - 32 * part;  // the first query column that sees this key, on the diagonal
 #pragma unroll
@@ -1595,10 +1620,10 @@ __global__ void __launch_bounds__(kDkvThreads, 1) rc_dkv_kernel(const __grid_con
               const float4 n = nl4[c >> 2];
               float x[4];
               unpack2(fma2(pack2(as_f(s[c]), as_f(s[c + 1])), scl2,
-                           add2(pack2(n.x, n.y), pack2(tb[-c], tb[-c - 1]))),
+                           mul2(add2(pack2(n.x, n.y), pack2(tb[-c], tb[-c - 1])), log2e2)),
                       x[0], x[1]);
               unpack2(fma2(pack2(as_f(s[c + 2]), as_f(s[c + 3])), scl2,
-                           add2(pack2(n.z, n.w), pack2(tb[-c - 2], tb[-c - 3]))),
+                           mul2(add2(pack2(n.z, n.w), pack2(tb[-c - 2], tb[-c - 3])), log2e2)),
                       x[2], x[3]);
 #pragma unroll
               for (int e = 0; e < 4; ++e) s[c + e] = __float_as_uint(ex2_ftz(x[e]));
@@ -1607,14 +1632,9 @@ __global__ void __launch_bounds__(kDkvThreads, 1) rc_dkv_kernel(const __grid_con
 #pragma unroll
             for (int c = 16 * h; c < 16 * h + 16; c += 4) {
               const float4 n = nl4[c >> 2];
-              uint64_t o0 = pack2(n.x, n.y), o1 = pack2(n.z, n.w);
-              if (BIAS) {
-                o0 = add2(o0, add2v);
-                o1 = add2(o1, add2v);
-              }
               float x[4];
-              unpack2(fma2(pack2(as_f(s[c]), as_f(s[c + 1])), scl2, o0), x[0], x[1]);
-              unpack2(fma2(pack2(as_f(s[c + 2]), as_f(s[c + 3])), scl2, o1), x[2], x[3]);
+              unpack2(fma2(pack2(as_f(s[c]), as_f(s[c + 1])), scl2, pack2(n.x, n.y)), x[0], x[1]);
+              unpack2(fma2(pack2(as_f(s[c + 2]), as_f(s[c + 3])), scl2, pack2(n.z, n.w)), x[2], x[3]);
 #pragma unroll
               for (int e = 0; e < 4; ++e) s[c + e] = __float_as_uint(ex2_ftz(x[e]));
             }
@@ -2048,7 +2068,7 @@ __global__ void __launch_bounds__(kDqThreads, 1) rc_dq_kernel(const __grid_const
     const int part = warp >> 2;  // the 32 key columns of this warp
     const int quarter = warp & 3;
     const uint32_t lb = static_cast<uint32_t>(quarter * 32) << 16;
-    const uint64_t scl2 = pack2(p.scale_log2, p.scale_log2);
+    const uint64_t scl2 = pack2(p.scale_log2, p.scale_log2), log2e2 = pack2(kLog2e, kLog2e);
     uint32_t nt = 0;  // tiles so far
     uint32_t kc = 0, vc = 0;  // ring tiles so far
     // the columns of the output in 32s over the warps of a row; an item's are
@@ -2129,13 +2149,14 @@ __global__ void __launch_bounds__(kDqThreads, 1) rc_dq_kernel(const __grid_const
         const int jk = key_tile(j), c0 = 128 * jk + 32 * part;  // key position of this warp's first column
         const uint32_t tPj = tP + lb + 32 * part + (kAhead && (nt & 1) ? 128 : 0);
         int side = 0;
-        float off = nl;
+        float off = nl;  // (differences with the bias come before the factor)
         const float* tb = nullptr;
         if (BIAS) {
           side = bias_side(md, r0, 128 * jk);
           if (side != 0) off += tab[side < 0 ? 0 : 2 * (md + kPad)];
           tb = tab + (c0 - row + md + kPad);
         }
+        if (!BIAS || side != 0) off *= kLog2e;
         const uint64_t off2 = pack2(off, off);
         ok = ok && wait_warp(bar(L::sfull), nt & 1, w);
         tc_fence_after();
@@ -2149,7 +2170,9 @@ __global__ void __launch_bounds__(kDqThreads, 1) rc_dq_kernel(const __grid_const
 #pragma unroll
           for (int c = 0; c < 32; c += 2) {
             float x0, x1;
-            unpack2(fma2(pack2(as_f(s[c]), as_f(s[c + 1])), scl2, add2(off2, pack2(tb[c], tb[c + 1]))), x0, x1);
+            unpack2(fma2(pack2(as_f(s[c]), as_f(s[c + 1])), scl2,
+                         mul2(add2(off2, pack2(tb[c], tb[c + 1])), log2e2)),
+                    x0, x1);
             s[c] = __float_as_uint(ex2_ftz(x0));
             s[c + 1] = __float_as_uint(ex2_ftz(x1));
           }
