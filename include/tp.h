@@ -41,7 +41,11 @@
  *    tp_attn_recompute_* and tp_attn_relbias_* rotate over 4096.  A call captured into a
  *    CUDA graph keeps the slot it was given at capture: replay such a graph
  *    on one stream at a time (replays in sequence reuse the slot safely, since
- *    every launch resets its counters as it ends).
+ *    every launch resets its counters as it ends).  A captured GEMM or norm
+ *    pass's slot comes round to others after 64 launches: let none of those run
+ *    beside the graph.  The captured launches of tp_attn_recompute_* and
+ *    tp_attn_relbias_* have slots of their own, 65536 in a process; those after
+ *    take their work in a fixed order, which needs none.
  *  - Execution: work is enqueued asynchronously on `stream` (a cudaStream_t
  *    passed as void*; NULL = legacy default stream).  Argument errors return
  *    synchronously before any launch.  Device-side errors (a bounded wait that

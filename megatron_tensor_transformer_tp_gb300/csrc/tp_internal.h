@@ -205,7 +205,7 @@ struct RcParams {
   int shard_w;  // columns of one shard in QKV
   int sub;      // query tiles an item (forward; set by the launcher)
   int parts;    // CTAs an item, a cluster (set by the launcher)
-  int slot;     // item counter of the launch (set by the launcher)
+  int slot;     // item counter of the launch, or -1 (set by the launcher)
   int wide;     // output rows allow 32-byte stores (set by the launcher)
   int64_t items;  // of the launch, those without rows among them (set by the launcher)
   float scale, scale_log2;
