@@ -39,7 +39,11 @@
 //   bias of both directions, 4 x 1024, 16 heads of 64: 30 us; 97 us, 0.44 PFLOP/s:
 //     at 64 columns a product takes 256 cycles and the element-wise work as long as
 //     before, which is then the bound.
-// Every wait is bounded, as in the GEMM engine.
+// Every wait on an mbarrier is bounded, as in the GEMM engine, and after one that
+// runs out the CTA's warps leave.  Without a limit are the barriers of a warp pair, of
+// the compute warps, of the CTA and of the cluster, which every warp reaches because
+// nothing before them waits without a limit, and the waits for the kernel before,
+// which ends for the same reason.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -1408,7 +1412,7 @@ __global__ void __launch_bounds__(kDkvThreads, 1) rc_dkv_kernel(const __grid_con
         const uint32_t pq = (it / L::kQ) & 1, po = (it / L::kO) & 1;
         const HeadAt hq = head_at(q.g, p.hq);
         const bool torn = 128 * q.i + 128 > len && start + len < p.T;  // rows of nobody in the tile
-        if (early && it == 1) pdl_wait();  // (the limits of the waits run from here)
+        if (early && it == 1) pdl_wait();  // (the limits of the waits for all but the first tile run from here)
         if (lane == 0) ok = wait_bounded(bar(L::qempty + sq), pq ^ 1u, w);
         ok = __shfl_sync(0xffffffffu, ok, 0);
         if (!ok) break;
@@ -1532,6 +1536,8 @@ __global__ void __launch_bounds__(kDkvThreads, 1) rc_dkv_kernel(const __grid_con
           if (grad) mma_commit(bar(L::oempty + x.stage));
           if (i + 2 == k.total) mma_commit(bar(L::kvempty));
         };
+        // the second tile is loaded when dQ has ended: its wait begins then
+        if (early && i == 0 && it == 0) pdl_wait();
         if (more && !(ok = wait_warp(bar(xfull + x.stage), x.phase, w))) break;
         issued = true;
         if (ahead && more) {
@@ -1547,7 +1553,6 @@ __global__ void __launch_bounds__(kDkvThreads, 1) rc_dkv_kernel(const __grid_con
           // (P's barriers alternate: with scores a tile ahead, two tiles may be ready)
           const int ready = grad ? L::dsready : L::pready + 2 * (it & 1);
           const uint32_t rphase = grad ? it & 1 : (it >> 1) & 1;
-          if (early && it == 0) pdl_wait();
           if (!(ok = wait_warp(bar(ready), rphase, w))) break;
           tc_fence_after();
           if (kHalves == 2) {

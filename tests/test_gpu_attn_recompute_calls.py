@@ -1,4 +1,5 @@
-"""Calls of attention without stored probabilities beside each other: captured and eager ones at the same time."""
+"""Calls of attention without stored probabilities beside each other: captured and eager ones at the same time,
+and the backward's two launches."""
 import pytest
 import torch
 
@@ -72,6 +73,31 @@ def test_captured_calls_share_no_counter_with_later_ones(which):
         for x, w in zip((a, b), want):
             assert all(torch.equal(y, z) for y, z in zip(x.outputs(), w))
     assert tp.tp_get_status() == tp.TP_OK
+
+
+def test_the_second_launch_may_wait_longer_than_the_limit():
+    """The kernel for dK and dV begins on SMs that dQ has left, 88 here, and waits for its last 64 items, 2 ms each:
+    no wait with a limit (1 ms here) covers that."""
+    tp = _tp()
+    T = 6144 * 128
+    cfg = dict(b=1, s=T, n_heads=1, n_kv_heads=1, d=64, N=1, causal=False)
+    bf = dict(dtype=torch.bfloat16, device="cuda")
+    gen = torch.Generator(device="cuda").manual_seed(420)
+    Q = torch.randn(T, 192, generator=gen, device="cuda").to(torch.bfloat16)
+    dC = torch.randn(T, 64, generator=gen, device="cuda").to(torch.bfloat16)
+    C, lse = torch.zeros(T, 64, **bf), torch.zeros(1, T, device="cuda")
+    ws = torch.empty(tp.tp_attn_recompute_workspace_size(cfg, T), dtype=torch.uint8, device="cuda")
+    tp.tp_attn_recompute_fwd(Q, cfg, C, lse)
+    a, b = torch.zeros_like(Q), torch.zeros_like(Q)
+    tp.tp_attn_recompute_bwd(Q, cfg, C, lse, dC, a, ws)
+    torch.cuda.synchronize()
+    tp.tp_debug_set_wait_limit_ms(1)
+    try:
+        tp.tp_attn_recompute_bwd(Q, cfg, C, lse, dC, b, ws)
+        assert tp.tp_get_status() == tp.TP_OK
+    finally:
+        tp.tp_debug_set_wait_limit_ms(0)
+    assert torch.equal(a, b)
 
 
 def test_captured_calls_beyond_the_counters():
