@@ -752,7 +752,9 @@ TP_API tp_status tp_gelu_eval(const float* z, float* y, float* dy, int64_t n, vo
 /* Fault injection for testing the bounded waits (host-controlled; never
  * faults the GPU).  kind 1: the TMA producer of the next tensor-core GEMM
  * or attention launch skips its first stage, so the consumer's bounded wait expires and
- * the kernel returns early with TP_ERR_TIMEOUT recorded.  kind 0: off.
+ * the kernel returns early with TP_ERR_TIMEOUT recorded.  kind 2: the same in
+ * the second kernel, of dK and dV, of the next tp_attn_recompute_bwd or
+ * tp_attn_relbias_bwd.  kind 0: off.
  * wait_limit_ms sets the bounded-wait limit (default 1000 ms). */
 TP_API void tp_debug_inject_fault(int kind);
 /* Selects the tensor-core GEMM kernel for bf16 work: 0 the one-SM kernel

@@ -597,7 +597,7 @@ tp_status launch_tc_groups(const Plan& pl, const bool* used, GemmGroup* groups, 
   p.err = dev->err;
   p.wait_limit_ns = g_wait_limit_ns;
   p.fault_skip = g_fault_kind == 1;
-  g_fault_kind = 0;
+  if (p.fault_skip) g_fault_kind = 0;
   (void)name;
   const cudaError_t e = launch_tc_gemm(p, dev->num_sms, s);
   return e == cudaSuccess ? TP_OK : TP_ERR_CUDA;
@@ -1353,7 +1353,8 @@ tp_status rc_device(RcParams* P, const void* QKV, int64_t ld_qkv, int N, DeviceS
   P->err = (*dev)->err;
   P->wait_limit_ns = g_wait_limit_ns;
   P->fault_skip = g_fault_kind == 1;
-  g_fault_kind = 0;
+  P->fault_second = P->dQKV != nullptr && g_fault_kind == 2;
+  if (P->fault_skip || P->fault_second) g_fault_kind = 0;
   return TP_OK;
 }
 

@@ -2545,7 +2545,7 @@ cudaError_t bwd_t(RcParams& p, int num_sms, cudaStream_t st) {
   if (!BIAS) p.parts = cluster_parts(p, p.H, 1, false, num_sms);
   cudaError_t e = p.parts > 1 ? launch_rc<rc_dq_kernel<DP, BIAS, !BIAS>>(num_sms, kDqThreads, dq_smem, p, st)
                               : launch_rc<rc_dq_kernel<DP, BIAS, false>>(num_sms, kDqThreads, dq_smem, p, st);
-  p.fault_skip = 0;
+  p.fault_skip = p.fault_second;
   if (e != cudaSuccess) return e;
   if (BIAS && p.partial != nullptr) {
     e = launch_k(rc_bias_sum_kernel, dim3(p.H, p.bias.nb), dim3(128), 0, st, p, units);

@@ -217,7 +217,8 @@ struct RcParams {
   float* dtable;
   float* partial;      // (units, H, nb) scratch, or null: no bias gradient
   int accumulate;
-  int fault_skip;
+  int fault_skip;    // a tile's copy is left out
+  int fault_second;  // and one in the backward's last launch
   unsigned* err;
   unsigned long long wait_limit_ns;
   RcBias bias;

@@ -100,6 +100,32 @@ def test_the_second_launch_may_wait_longer_than_the_limit():
     assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("bias", [None, dict(num_buckets=16, max_distance=40, bidirectional=False)])
+@pytest.mark.parametrize("lens,d", [([300], 64), ([300, 190], 128), ([2100], 64), ([2100], 128)])
+def test_a_wait_of_the_second_launch_runs_out(lens, d, bias):
+    """The kernel for dK and dV misses its keys and values, in single CTAs and in clusters: it ends, the call is
+    reported, and the next one is right.  Forward calls leave that fault for the backward."""
+    tp = _tp()
+    c = Case(lens, 1, 1, d, 1, True, bias=bias, seed=430)
+    C, lse = c.fwd()
+    g, t = c.bwd(C, lse)
+    torch.cuda.synchronize()
+    tp.tp_debug_set_wait_limit_ms(20)
+    try:
+        tp.tp_debug_inject_fault(2)
+        c.fwd()
+        assert tp.tp_get_status() == tp.TP_OK
+        g2, t2 = c.bwd(C, lse)
+        assert tp.tp_get_status() == tp.TP_ERR_TIMEOUT
+    finally:
+        tp.tp_debug_inject_fault(0)
+        tp.tp_debug_set_wait_limit_ms(0)
+    assert torch.equal(g2[:, :d], g[:, :d]) and (t is None or torch.equal(t2, t))  # dQ and the table came first
+    g2, t2 = c.bwd(C, lse)
+    assert tp.tp_get_status() == tp.TP_OK
+    assert torch.equal(g2, g) and (t is None or torch.equal(t2, t))
+
+
 def test_captured_calls_beyond_the_counters():
     """After 65536 captured launches the following ones have no counter and take their items in a fixed order: the
     same bits.  (This one uses the counters up, so it comes last.)"""
