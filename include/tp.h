@@ -323,7 +323,9 @@ typedef struct {
  * as operands of their products.  No (s x s) matrix is stored.  Sums have a
  * fixed order: equal calls give equal bits.
  * Rows of one sequence never depend on another sequence's values, whatever
- * they are.  Inside a sequence a non-finite value may reach every row.
+ * they are.  Inside a sequence a non-finite value may reach every row.  The
+ * forward's unscaled sums reach up to 2^16 times a row's sum of |v|: values of V
+ * above 2^80 may overflow them.
  * Outputs and workspace overlap no other buffer of the call (row pitches may
  * interleave them): key/value tiles are read after the first dQ is written.
  * Errors: TP_ERR_INVALID for sizes outside the ranges above, pitches narrower

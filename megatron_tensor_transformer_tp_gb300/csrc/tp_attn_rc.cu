@@ -33,12 +33,12 @@
 // Measured on a GB300 (cuBLAS reaches 1.87 PFLOP/s in bf16 there), in matrix work
 // that the definition needs, four and ten flops a visible pair and column:
 //   causal, one sequence of 16384, 8 heads of 128, 2 K/V heads
-//     forward 342 us, 1.6 PFLOP/s; backward 1.16 ms, 1.18 PFLOP/s, which is 1.66
+//     forward 343 us, 1.6 PFLOP/s; backward 1.18 ms, 1.17 PFLOP/s, which is 1.63
 //     with the two products that are computed twice
-//   causal, 2 x 2048, 32 heads of 128: 62 us, 1.11 PFLOP/s; 194 us, 0.89 PFLOP/s
-//   bias of both directions, 4 x 1024, 16 heads of 64: 30 us; 97 us, 0.44 PFLOP/s:
+//   causal, 2 x 2048, 32 heads of 128: 62 us, 1.11 PFLOP/s; 198 us, 0.87 PFLOP/s
+//   bias of both directions, 4 x 1024, 16 heads of 64: 30 us; 96 us, 0.45 PFLOP/s:
 //     at 64 columns a product takes 256 cycles and the element-wise work as long as
-//     before, which is then the bound.
+//     before, which with the waits between its steps is then the bound.
 // Every wait on an mbarrier is bounded, as in the GEMM engine, and after one that
 // runs out the CTA's warps leave.  Without a limit are the barriers of a warp pair, of
 // the compute warps, of the CTA and of the cluster, which every warp reaches because
@@ -1306,7 +1306,7 @@ struct QueryWalk {
 // an SM stores at 32 bytes a cycle at best.  (To store them under the next item's
 // first tile took as long: the 16 warps have no time to spare there.)  At width 64
 // the warps' own work bounds it: 1800 cycles a tile against 1024, with 11
-// instructions a score issued in 57% of the cycles, and 2900 an item.  P and dS in
+// instructions a score issued in 59% of the cycles, and 2900 an item.  P and dS in
 // TMEM columns of their own there, so that the products run a tile further ahead,
 // was 10% slower: two more waits a tile cost more than they hid.
 //
@@ -2411,7 +2411,9 @@ int wide_rows(const RcParams& p, const void* out, int64_t ld, int shard_w) {
 // stay for the next item).  `once`: in one round only (the forward, whose single
 // CTAs take pairs of query tiles).  n: tiles of a sequence of mean length (no matter
 // if the sequences come by seq_starts or by s: equal rows are summed in the same
-// order); mult: tiles an item for each of them.  Pairs and fours of CTAs leave 8
+// order); mult: tiles an item for each of them.  So one long sequence among many
+// short ones stays with single CTAs: 8192 tokens, 8 heads of 64, 1 K/V head, backward
+// 213 us alone and 551 us beside 31 sequences of 64.  Pairs and fours of CTAs leave 8
 // SMs over, eights 40.  Microseconds with 1, 2, 4 and 8, whole call, heads of 128:
 //   forward   2048, 2 heads, causal             23   18   14*  31
 //             4096, 2 heads                     41   28*  36   65
