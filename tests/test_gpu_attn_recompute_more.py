@@ -80,3 +80,60 @@ def test_calls_with_a_bias_on_two_streams_at_once():
         for a, b in zip(got, want):
             assert all(torch.equal(x, y) for x, y in zip(a, b))
     assert _tp().tp_get_status() == _tp().TP_OK
+
+
+@pytest.mark.parametrize("bias", [None, BIAS])
+def test_a_graph_replayed_on_other_lengths(bias):
+    """The starts are read when the graph runs: other lengths, empty ones and unused rows among them."""
+    tp = _tp()
+    T, H, KV, d = 900, 4, 2, 64
+    plans = [[900, 0, 0, 0], [1, 300, 299, 300], [128, 128, 128, 128], [0, 513, 0, 200], [0, 0, 0, 0]]
+    cases = [Case(lens, H, KV, d, 2, True, tail=T - sum(lens), bias=bias, seed=560 + i, packed=True)
+             for i, lens in enumerate(plans)]
+    bf = dict(dtype=torch.bfloat16, device="cuda")
+    Q, dC, starts = torch.zeros(T, (H + 2 * KV) * d, **bf), torch.zeros(T, H * d, **bf), torch.zeros(5, dtype=torch.int64, device="cuda")
+    C, lse, dQ = torch.zeros(T, H * d, **bf), torch.zeros(H, T, device="cuda"), torch.zeros(T, (H + 2 * KV) * d, **bf)
+    table = torch.zeros(bias["num_buckets"], H, device="cuda") if bias else None
+    dt = torch.zeros_like(table) if bias else None
+    cfg = dict(cases[0].cfg, s=None)
+    ws = torch.empty(tp.tp_attn_recompute_workspace_size(cfg, T, bias), dtype=torch.uint8, device="cuda")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        if bias:
+            tp.tp_attn_relbias_fwd(Q, cfg, bias, table, C, lse, seq_starts=starts)
+            tp.tp_attn_relbias_bwd(Q, cfg, bias, table, C, lse, dC, dQ, dt, ws, seq_starts=starts)
+        else:
+            tp.tp_attn_recompute_fwd(Q, cfg, C, lse, seq_starts=starts)
+            tp.tp_attn_recompute_bwd(Q, cfg, C, lse, dC, dQ, ws, seq_starts=starts)
+    for c in cases + cases[:2]:
+        Q.copy_(c.QKV), dC.copy_(c.dC), starts.copy_(torch.tensor(c.starts))
+        if bias:
+            table.copy_(c.table)
+        for x in (C, lse, dQ):
+            x.fill_(7.0)
+        ws.fill_(255)
+        graph.replay()
+        assert tp.tp_get_status() == tp.TP_OK
+        check(c, C, lse, dQ, dt)
+
+
+@pytest.mark.parametrize("lens,H,KV,d,bias", [([200, 100], 2, 1, 64, None), ([300], 1, 1, 128, BIAS), ([290], 2, 2, 40, None)])
+def test_rows_far_apart(lens, H, KV, d, bias):
+    """Row pitches of 2^24 elements: addresses beyond 2^32 in every matrix, and the bits of rows close together."""
+    c = Case(lens, H, KV, d, 1, True, bias=bias, seed=570)
+    C, lse = c.fwd()
+    g, t = c.bwd(C, lse)
+    pitch = 1 << 24
+
+    def far(x):
+        v = torch.empty((c.T - 1) * pitch + x.shape[1], dtype=torch.bfloat16, device="cuda").as_strided(x.shape, (pitch, 1))
+        v.copy_(x)
+        return v
+
+    Q, dC, C2, dQ = far(c.QKV), far(c.dC), far(torch.zeros_like(C)), far(torch.zeros_like(g))
+    lse2 = torch.zeros_like(lse)
+    c.fwd(Q, C2, lse2)
+    assert torch.equal(C2, C) and torch.equal(lse2, lse)
+    _, t2 = c.bwd(C2, lse2, Q, dC, dQ)
+    assert torch.equal(dQ, g) and (t is None or torch.equal(t2, t))
+    assert _tp().tp_get_status() == _tp().TP_OK
