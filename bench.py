@@ -120,7 +120,7 @@ def load_peaks():
 
 # The sources that define each kind of work's kernels and launches: a DRAM
 # traffic figure stays valid while these files are unchanged.
-_GEMM_SRC = ("tp_gemm_tc.cu", "tp_api.cu", "tp_internal.h", "tp_device.cuh", "tp_tcgen05.cuh")
+_GEMM_SRC = ("tp_gemm_tc.cu", "tp_api.cu", "tp_entry.h", "tp_internal.h", "tp_device.cuh", "tp_tcgen05.cuh")
 KERNEL_SOURCES = {"gemm": _GEMM_SRC, "embed": ("tp_embed.cu", "tp_internal.h", "tp_device.cuh"),
                   "ce_reduce": ("tp_embed.cu", "tp_internal.h", "tp_device.cuh"),
                   "attn_norm": ("tp_attn.cu", "tp_internal.h", "tp_philox.cuh"),

@@ -373,6 +373,130 @@ TP_API tp_status tp_attn_relbias_bwd(tp_dtype dt, const tp_attn_config* cfg, con
 TP_API size_t tp_attn_recompute_workspace_size(const tp_attn_config* cfg, const tp_relbias_config* bias);
 
 /* ------------------------------------------------------------------------ */
+/* Rotary positions, and norms of queries and keys                           */
+/* ------------------------------------------------------------------------ */
+
+/* Rotation of a head's leading n_rot columns by the token's position (host
+ * struct): n_rot / 2 pairs of columns, pair k turned by position * freq[k]. */
+typedef struct {
+  int32_t n_rot;       /* rotated columns of a head, even, at most d; 0 (norms alone): none */
+  int32_t interleaved; /* pair k is columns (2k, 2k + 1); else (k, k + n_rot / 2) */
+  const double* freq;  /* (host) radians a position, n_rot / 2 values in [0, 2^20] */
+  float amplitude;     /* factor of the rotated columns, finite and > 0; 0 = 1 */
+} tp_rotary_config;
+
+/* Norm of every query and key head (host struct): over its d columns,
+ *   TP_NORM_RMS    n = x / sqrt(mean(x^2) + eps)
+ *   TP_NORM_LAYER  the same with x less its mean first (biased variance) */
+enum { TP_NORM_RMS = 0, TP_NORM_LAYER = 1 };
+typedef struct {
+  int32_t kind;
+  float eps; /* finite and > 0 */
+} tp_qk_norm_config;
+
+/* Frequencies of tp_rotary_frequencies (host struct), f_k = base^(-2k / n_rot):
+ *   TP_ROTARY_PLAIN     f_k
+ *   TP_ROTARY_LINEAR    f_k / factor (positions interpolated)
+ *   TP_ROTARY_BASE      the base is base factor^(n_rot / (n_rot - 2)) (n_rot >= 4)
+ *   TP_ROTARY_BY_TURNS  u_k f_k + (1 - u_k) f_k / factor, where the share u_k that
+ *                       is kept goes by the turns r_k = trained f_k / 2 pi of
+ *                       the pair in the trained length: (r_k - low) / (high - low)
+ *   TP_ROTARY_BY_PAIR   the same with u_k = 1 - (k - A) / max(B - A, 0.001), a ramp over
+ *                       the pairs' numbers from A = max(floor(k(high)), 0) to
+ *                       B = min(ceil(k(low)), n_rot - 1), k(r) the (fractional) pair
+ *                       that turns r times: n_rot ln(trained / 2 pi r) / (2 ln base)
+ *   (u_k limited to [0, 1]).  The amplitude is 0.1 ln(factor) + 1 for BY_PAIR, else 1. */
+enum { TP_ROTARY_PLAIN = 0, TP_ROTARY_LINEAR = 1, TP_ROTARY_BASE = 2, TP_ROTARY_BY_TURNS = 3, TP_ROTARY_BY_PAIR = 4 };
+typedef struct {
+  int32_t n_rot; /* even, 2 <= n_rot <= 512 */
+  int32_t kind;
+  double base;      /* > 1, finite */
+  double factor;    /* >= 1, finite (unused by PLAIN) */
+  double trained;   /* BY_TURNS, BY_PAIR: length of the contexts trained on, >= 1 */
+  double low, high; /* BY_TURNS, BY_PAIR: 0 < low < high turns in that length */
+} tp_rotary_scaling;
+
+/* Host arithmetic: fills freq (n_rot / 2 values) and *amplitude for a
+ * tp_rotary_config.  TP_ERR_INVALID for null pointers and values outside the
+ * ranges above.  Frequencies of one's own serve as well. */
+TP_API tp_status tp_rotary_frequencies(const tp_rotary_scaling* scaling, double* freq, float* amplitude);
+
+/*
+ * tp_rotary_fwd / _bwd -- queries and keys rotated by their positions, between
+ * the QKV projection and the attention of each head ([Walkthrough]
+ * §ParallelSelfAttention; [TP notes] §Self-Attention层).  For every query and
+ * key head of a row at position t and every pair (x1, x2) of its columns, with
+ * a = t freq[k] and m the amplitude:
+ *   y1 = m (x1 cos a - x2 sin a),   y2 = m (x1 sin a + x2 cos a)
+ * and backward, with dy for x, the transposed matrix (the same with -sin a).
+ * Columns from n_rot on, and the value heads, are copied.
+ * Arguments (TP_BF16 or TP_F32; sizes T, b, s, n_heads, n_kv_heads, d, N of cfg, its
+ * causal and scale unused; here 8 <= d <= 512):
+ *   QKV, Out, dOut, dQKV  (T, (n_heads + 2 n_kv_heads) d), shard-major as in
+ *               tp_attn_recompute_fwd, pitches ld_*.  The output may be the input's
+ *               buffer (same pitch): the value heads are then not touched.
+ *   positions   device int64[T], any values, or NULL: a row's position is its
+ *               place in its sequence, from 0
+ *   seq_starts  device int64[b + 1] as in tp_attn_recompute_fwd: rows outside
+ *               every sequence are not written; or NULL: every row is used, and
+ *               without positions the sequences are b of s rows each (with
+ *               positions b and s are unused)
+ * Angles are exact to 2^-32 of a turn plus position * 2^-64 turns beside freq's own
+ * rounding; cosines and sines are fp32; results are rounded once to the dtype.
+ * Deterministic, no workspace.
+ * Errors, before anything is launched: TP_ERR_INVALID for sizes outside the
+ * ranges above, pitches narrower than a row, null pointers, frequencies or an
+ * amplitude outside their ranges, an output in place with another pitch;
+ * TP_ERR_ALIGN for a d that is no multiple of 8, matrices that are not 16-byte
+ * aligned or have a pitch that is no multiple of 16 bytes.  Buffers overlap in
+ * no other way.  Starts that decrease or leave [0, T]: no access leaves the
+ * buffers, results are unspecified and tp_get_status returns TP_ERR_INVALID.
+ */
+TP_API tp_status tp_rotary_fwd(tp_dtype dt, const tp_attn_config* cfg, const tp_rotary_config* rot,
+                               const int64_t* seq_starts, const int64_t* positions, const void* QKV, int64_t ld_qkv,
+                               void* Out, int64_t ld_out, void* stream);
+TP_API tp_status tp_rotary_bwd(tp_dtype dt, const tp_attn_config* cfg, const tp_rotary_config* rot,
+                               const int64_t* seq_starts, const int64_t* positions, const void* dOut,
+                               int64_t ld_dout, void* dQKV, int64_t ld_dqkv, void* stream);
+
+/*
+ * tp_qk_norm_rotary_fwd / _bwd -- the norm of every query and key head and its
+ * rotation in one pass:  y = R(n g), n as in tp_qk_norm_config, g the gain of
+ * the head's kind, R as in tp_rotary_fwd.  Backward, from QKV (the forward's
+ * input, so the forward is not in place where a gradient is wanted) and dOut:
+ *   dz = R^T dOut,  dg = sum over rows, shards and heads of dz n,
+ *   dx = (dz g - n mean(dz g n) [- mean(dz g), TP_NORM_LAYER]) / sqrt(mean(x^2) + eps)
+ * and the value heads' gradient copied.
+ * Arguments as tp_rotary_fwd, and
+ *   rot         NULL or n_rot = 0: norms alone
+ *   gq, gk      (d) fp32 gains of the query and key heads, one copy for all shards
+ *               and heads, or NULL: one
+ *   dQKV        out; may be dOut's buffer (same pitch: value heads not touched), not QKV's
+ *   dgq, dgk    (d) fp32 out, or NULL: not computed (accumulate: added to the old value)
+ *   workspace   tp_qk_norm_rotary_workspace_size bytes, 256-byte aligned; unused and
+ *               may be NULL if dgq and dgk are
+ * Norms, their sums and the gains' gradients are fp32: a head's sum of squares must
+ * stay below 2^127, as must the backward's products.  The gradients' sums have a
+ * fixed order for a given GPU model: equal calls give equal bits.
+ * Errors as tp_rotary_fwd's, and TP_ERR_INVALID for a kind or eps outside its range,
+ * dQKV at QKV's address, dgq or dgk at each other's or a gain's; TP_ERR_WORKSPACE.
+ */
+TP_API tp_status tp_qk_norm_rotary_fwd(tp_dtype dt, const tp_attn_config* cfg, const tp_qk_norm_config* norm,
+                                       const tp_rotary_config* rot, const float* gq, const float* gk,
+                                       const int64_t* seq_starts, const int64_t* positions, const void* QKV,
+                                       int64_t ld_qkv, void* Out, int64_t ld_out, void* stream);
+TP_API tp_status tp_qk_norm_rotary_bwd(tp_dtype dt, const tp_attn_config* cfg, const tp_qk_norm_config* norm,
+                                       const tp_rotary_config* rot, const float* gq, const float* gk,
+                                       const int64_t* seq_starts, const int64_t* positions, const void* QKV,
+                                       int64_t ld_qkv, const void* dOut, int64_t ld_dout, void* dQKV,
+                                       int64_t ld_dqkv, float* dgq, float* dgk, int accumulate, void* workspace,
+                                       size_t ws_bytes, void* stream);
+
+/* Workspace bytes of tp_qk_norm_rotary_bwd with gradients of the gains; 0 for
+ * invalid sizes or T = 0. */
+TP_API size_t tp_qk_norm_rotary_workspace_size(const tp_attn_config* cfg);
+
+/* ------------------------------------------------------------------------ */
 /* One tensor-parallel transformer layer                                     */
 /* ------------------------------------------------------------------------ */
 

@@ -34,6 +34,8 @@ __all__ = [
     "tp_transformer_layer_workspace_size", "tp_transformer_layer_fwd", "tp_transformer_layer_bwd",
     "tp_layer_config", "layer_stream", "tp_attn_config", "tp_relbias_config", "tp_attn_recompute_fwd",
     "tp_attn_recompute_bwd", "tp_attn_relbias_fwd", "tp_attn_relbias_bwd", "tp_attn_recompute_workspace_size",
+    "tp_rotary_config", "tp_qk_norm_config", "tp_rotary_scaling", "tp_rotary_frequencies", "tp_rotary_fwd",
+    "tp_rotary_bwd", "tp_qk_norm_rotary_fwd", "tp_qk_norm_rotary_bwd", "tp_qk_norm_rotary_workspace_size",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libtp.so")
@@ -103,6 +105,23 @@ class tp_relbias_config(ctypes.Structure):
                 ("bidirectional", ctypes.c_int32)]
 
 
+class tp_rotary_config(ctypes.Structure):
+    """Rotation of a head's columns (layout of the C struct)."""
+    _fields_ = [("n_rot", ctypes.c_int32), ("interleaved", ctypes.c_int32), ("freq", ctypes.c_void_p),
+                ("amplitude", ctypes.c_float)]
+
+
+class tp_qk_norm_config(ctypes.Structure):
+    _fields_ = [("kind", ctypes.c_int32), ("eps", ctypes.c_float)]
+
+
+class tp_rotary_scaling(ctypes.Structure):
+    _fields_ = [("n_rot", ctypes.c_int32), ("kind", ctypes.c_int32), ("base", ctypes.c_double),
+                ("factor", ctypes.c_double), ("trained", ctypes.c_double), ("low", ctypes.c_double),
+                ("high", ctypes.c_double)]
+
+
+_ROTARY_CONFIG, _QK_NORM_CONFIG = struct.Struct("2iPf4x"), struct.Struct("if")  # the same fields, as bytes
 _ATTN_CONFIG, _RELBIAS_CONFIG = struct.Struct("3q5if"), struct.Struct("3i")  # the same fields, as bytes
 
 _SIGNATURES = {
@@ -170,6 +189,18 @@ _SIGNATURES = {
                                    _c_void_p, _c_void_p, _i64, _c_void_p, _i64, _c_void_p, _int, _c_void_p,
                                    _size_t, _c_void_p]),
     "tp_attn_recompute_workspace_size": (_size_t, [_c_void_p, _c_void_p]),
+    "tp_rotary_frequencies": (_int, [ctypes.POINTER(tp_rotary_scaling), ctypes.POINTER(ctypes.c_double),
+                                     ctypes.POINTER(ctypes.c_float)]),
+    "tp_rotary_fwd": (_int, [_int, _c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_void_p, _i64, _c_void_p, _i64,
+                             _c_void_p]),
+    "tp_rotary_bwd": (_int, [_int, _c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_void_p, _i64, _c_void_p, _i64,
+                             _c_void_p]),
+    "tp_qk_norm_rotary_fwd": (_int, [_int, _c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_void_p,
+                                     _c_void_p, _i64, _c_void_p, _i64, _c_void_p]),
+    "tp_qk_norm_rotary_bwd": (_int, [_int, _c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_void_p,
+                                     _c_void_p, _i64, _c_void_p, _i64, _c_void_p, _i64, _c_void_p, _c_void_p, _int,
+                                     _c_void_p, _size_t, _c_void_p]),
+    "tp_qk_norm_rotary_workspace_size": (_size_t, [_c_void_p]),
     "tp_position_embed_dropout": (_int, [_i64, _i64, _i64, _c_void_p, _c_void_p, _c_void_p,
                                          ctypes.c_float, ctypes.c_uint64, ctypes.c_uint64, _c_void_p,
                                          _c_void_p]),
@@ -527,16 +558,16 @@ def _refuse(t, name, dtype, shape, index):
     raise ValueError(f"{name} must have contiguous rows" if len(shape) == 2 else f"{name} must be contiguous")
 
 
-def _rows(t, name, shape, index):
-    """(pointer, row pitch) of a bf16 matrix whose rows may lie further apart than they are wide."""
+def _rows(t, name, shape, index, dtype=torch.bfloat16):
+    """(pointer, row pitch) of a matrix whose rows may lie further apart than they are wide."""
     try:
-        if t.dtype is torch.bfloat16 and t.shape == shape and t.get_device() == index:
+        if t.dtype is dtype and t.shape == shape and t.get_device() == index:
             pitch, step = t.stride()
             if step == 1 or shape[1] <= 1:
                 return t.data_ptr(), pitch if shape[0] > 1 else max(pitch, shape[1])
     except AttributeError:
         pass
-    _refuse(t, name, torch.bfloat16, shape, index)
+    _refuse(t, name, dtype, shape, index)
 
 
 def _vec(t, name, dtype, shape, index):
@@ -648,6 +679,129 @@ def tp_attn_relbias_bwd(QKV, cfg, bias, table, C, lse, dC, dQKV, dtable, workspa
                                      dq[0], dq[1], dt, 1 if accumulate else 0, ws[0], ws[1],
                                      _attn_stream(stream, dev)),
            "tp_attn_relbias_bwd")
+
+
+# ----------------------------------------------------------------------------
+# Rotary positions, and norms of queries and keys
+# ----------------------------------------------------------------------------
+_ROTARY_KINDS = {"plain": 0, "linear": 1, "base": 2, "by_turns": 3, "by_pair": 4}
+_NORM_KINDS = {"rms": 0, "layer": 1}
+
+
+def tp_rotary_frequencies(n_rot, base=10000.0, kind="plain", factor=1.0, trained=0.0, low=1.0, high=32.0,
+                          interleaved=False) -> dict:
+    """The rot argument of the calls below: {n_rot, interleaved, freq, amplitude}, freq a float64 CPU tensor of
+    n_rot / 2 radians a position.  kind: plain, linear, base, by_turns or by_pair, as tp_rotary_scaling has them."""
+    if kind not in _ROTARY_KINDS:
+        raise ValueError(f"kind must be one of {', '.join(_ROTARY_KINDS)}, not {kind!r}")
+    sc = tp_rotary_scaling(n_rot, _ROTARY_KINDS[kind], base, factor, trained, low, high)
+    freq, amplitude = (ctypes.c_double * max(n_rot // 2, 1))(), ctypes.c_float()
+    _check(lib().tp_rotary_frequencies(ctypes.byref(sc), freq, ctypes.byref(amplitude)), "tp_rotary_frequencies")
+    return {"n_rot": n_rot, "interleaved": bool(interleaved), "freq": torch.tensor(list(freq), dtype=torch.float64),
+            "amplitude": amplitude.value}
+
+
+def _rotary_cfg(rot: Optional[dict]) -> Optional[bytes]:
+    """The tp_rotary_config of rot, packed."""
+    if rot is None:
+        return None
+    n, freq = rot["n_rot"], rot["freq"]
+    if n and not (isinstance(freq, torch.Tensor) and freq.dtype is torch.float64 and freq.shape == (n // 2,)
+                  and not freq.is_cuda and freq.is_contiguous()):
+        raise ValueError(f"rot: freq must be a contiguous float64 CPU tensor of n_rot / 2 = {n // 2} values")
+    try:
+        return _ROTARY_CONFIG.pack(n, 1 if rot.get("interleaved") else 0, freq.data_ptr() if n else 0,
+                                   rot.get("amplitude") or 0.0)
+    except (struct.error, OverflowError) as e:
+        raise ValueError(f"rot: {e}") from None
+
+
+def _norm_cfg(norm: dict) -> bytes:
+    """The tp_qk_norm_config of norm, packed."""
+    if norm["kind"] not in _NORM_KINDS:
+        raise ValueError(f"norm: kind must be rms or layer, not {norm['kind']!r}")
+    try:
+        return _QK_NORM_CONFIG.pack(_NORM_KINDS[norm["kind"]], norm["eps"])
+    except (struct.error, OverflowError) as e:
+        raise ValueError(f"norm: {e}") from None
+
+
+def _rotary_common(X, name, Y, yname, cfg, rot, seq_starts, positions):
+    """The arguments that every call of this family begins with, checked against the sizes."""
+    if not isinstance(X, torch.Tensor) or X.dim() != 2:
+        raise ValueError(f"{name} must be a 2D tensor")
+    T, dtype = X.shape[0], X.dtype
+    dt = _dtype(X)
+    index = torch._C._cuda_getDevice() if X.is_cuda else -2
+    shape = (T, (cfg["n_heads"] + 2 * cfg["n_kv_heads"]) * cfg["d"])
+    x, y = _rows(X, name, shape, index, dtype), _rows(Y, yname, shape, index, dtype)
+    st = None if seq_starts is None else _vec(seq_starts, "seq_starts", torch.int64, (cfg["b"] + 1,), index)
+    po = None if positions is None else _vec(positions, "positions", torch.int64, (T,), index)
+    return dt, _rotary_sizes(cfg, T), _rotary_cfg(rot), st, po, x, y, shape, index
+
+
+def _rotary_sizes(cfg: dict, T: int) -> bytes:
+    """The tp_attn_config of cfg, packed; b, s, causal and scale may be missing."""
+    try:
+        return _ATTN_CONFIG.pack(T, cfg.get("b") or 0, cfg.get("s") or 0, cfg["n_heads"], cfg["n_kv_heads"], cfg["d"],
+                                 cfg["N"], 0, 0.0)
+    except struct.error as e:
+        raise ValueError(f"cfg: {e}") from None
+
+
+def tp_rotary_fwd(QKV, cfg, rot, Out, seq_starts=None, positions=None, stream=None):
+    """Out <- the shard-major QKV (T, (n_heads + 2 n_kv_heads) d), bf16 or fp32, with its query and key heads rotated
+    by their rows' positions; Out may be QKV itself.
+
+    cfg: dict as for tp_attn_recompute_fwd (n_heads, n_kv_heads, d, N; b with seq_starts; b and s without positions
+    and seq_starts; the rest is not used).  rot: dict of tp_rotary_frequencies, or one's own.  positions: int64 CUDA
+    tensor of T values, else rows count from 0 in their sequence.  seq_starts: int64 CUDA tensor of b + 1 row numbers;
+    rows outside every sequence are left as they are.  Matrices may be column slices of wider buffers.  Every tensor
+    lies on the current device."""
+    dt, c, r, st, po, x, y, _, dev = _rotary_common(QKV, "QKV", Out, "Out", cfg, rot, seq_starts, positions)
+    _check(lib().tp_rotary_fwd(dt, c, r, st, po, x[0], x[1], y[0], y[1], _attn_stream(stream, dev)), "tp_rotary_fwd")
+
+
+def tp_rotary_bwd(dOut, cfg, rot, dQKV, seq_starts=None, positions=None, stream=None):
+    """dQKV <- gradient of tp_rotary_fwd given its output's; dQKV may be dOut itself."""
+    dt, c, r, st, po, x, y, _, dev = _rotary_common(dOut, "dOut", dQKV, "dQKV", cfg, rot, seq_starts, positions)
+    _check(lib().tp_rotary_bwd(dt, c, r, st, po, x[0], x[1], y[0], y[1], _attn_stream(stream, dev)), "tp_rotary_bwd")
+
+
+def tp_qk_norm_rotary_workspace_size(cfg: dict, T: int) -> int:
+    """Bytes of the workspace of tp_qk_norm_rotary_bwd for T token rows."""
+    return int(lib().tp_qk_norm_rotary_workspace_size(_rotary_sizes(cfg, T)))
+
+
+def _gain(t, name, d, index):
+    return None if t is None else _vec(t, name, torch.float32, (d,), index)
+
+
+def tp_qk_norm_rotary_fwd(QKV, cfg, norm, rot, gq, gk, Out, seq_starts=None, positions=None, stream=None):
+    """Out <- QKV with every query and key head normalised, times its gain (gq, gk: (d) fp32 or None), and rotated.
+
+    norm: dict with kind (rms or layer) and eps.  rot: as for tp_rotary_fwd, or None: norms alone.  The other
+    arguments as for tp_rotary_fwd."""
+    dt, c, r, st, po, x, y, _, dev = _rotary_common(QKV, "QKV", Out, "Out", cfg, rot, seq_starts, positions)
+    d = cfg["d"]
+    _check(lib().tp_qk_norm_rotary_fwd(dt, c, _norm_cfg(norm), r, _gain(gq, "gq", d, dev), _gain(gk, "gk", d, dev), st,
+                                       po, x[0], x[1], y[0], y[1], _attn_stream(stream, dev)),
+           "tp_qk_norm_rotary_fwd")
+
+
+def tp_qk_norm_rotary_bwd(QKV, cfg, norm, rot, gq, gk, dOut, dQKV, dgq, dgk, workspace=None, accumulate=False,
+                          seq_starts=None, positions=None, stream=None):
+    """dQKV and, unless they are None, dgq and dgk <- gradient of tp_qk_norm_rotary_fwd (accumulate: dgq and dgk are
+    added to).  dQKV may be dOut itself.
+
+    workspace: a CUDA tensor of tp_qk_norm_rotary_workspace_size bytes, or None without dgq and dgk."""
+    dt, c, r, st, po, x, y, shape, dev = _rotary_common(QKV, "QKV", dQKV, "dQKV", cfg, rot, seq_starts, positions)
+    do, ws, d = _rows(dOut, "dOut", shape, dev, QKV.dtype), _scratch(workspace, dev), cfg["d"]
+    _check(lib().tp_qk_norm_rotary_bwd(dt, c, _norm_cfg(norm), r, _gain(gq, "gq", d, dev), _gain(gk, "gk", d, dev), st,
+                                       po, x[0], x[1], do[0], do[1], y[0], y[1], _gain(dgq, "dgq", d, dev),
+                                       _gain(dgk, "dgk", d, dev), 1 if accumulate else 0, ws[0], ws[1],
+                                       _attn_stream(stream, dev)),
+           "tp_qk_norm_rotary_bwd")
 
 
 def tp_position_embed_dropout(words, pos_table, positions, p, seed, stream_id, out, stream=None):

@@ -13,6 +13,7 @@
 #include <vector>
 
 #include "tp.h"
+#include "tp_entry.h"
 #include "tp_internal.h"
 
 using namespace tp;
@@ -148,6 +149,18 @@ void prof_flush_locked() {
 
 void tp::count_launches(int n) { g_kernel_launches.fetch_add(n); }
 bool tp::pdl_on() { return g_pdl != 0; }
+
+tp_status tp::entry_device(int* num_sms, unsigned** err) {
+  DeviceState* dev = nullptr;
+  const tp_status st = device_state(&dev);
+  if (st != TP_OK) return st;
+  *num_sms = dev->num_sms;
+  *err = dev->err;
+  return TP_OK;
+}
+cudaError_t tp::entry_timed(const char* name, cudaStream_t s, cudaError_t (*work)(void*), void* arg) {
+  return timed(name, s, [&] { return work(arg); });
+}
 
 namespace {
 

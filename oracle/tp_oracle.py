@@ -976,6 +976,111 @@ def embed_position_dropout(words, pos_table, positions, keep, p):
 
 
 # --------------------------------------------------------------------------
+# Rotary positions, norms of queries and keys
+# --------------------------------------------------------------------------
+def rotary_frequencies(n_rot, base, kind="plain", factor=1.0, trained=0.0, low=1.0, high=32.0):
+    """(radians a position of every pair, amplitude), pair by pair from the
+    definitions (f_k = base^(-2k/n_rot) of rotary positions; linear
+    interpolation of positions; a larger base; frequencies kept or interpolated
+    by the turns of the pair in the trained length, or by its number).
+    Pinned by: hand-made values, limits of each scaling."""
+    freq, amp = [], 1.0
+    if kind == "base":
+        base = base * factor ** (n_rot / (n_rot - 2))
+    if kind == "by_pair":
+        amp = 0.1 * np.log(factor) + 1.0
+        turns_at = lambda r: n_rot / 2 * np.log(trained / (2 * np.pi * r)) / np.log(base)  # noqa: E731
+        A, B = max(np.floor(turns_at(high)), 0.0), min(np.ceil(turns_at(low)), n_rot - 1.0)
+    for k in range(n_rot // 2):
+        f = float(base) ** (-2.0 * k / n_rot)
+        if kind == "linear":
+            f /= factor
+        elif kind == "by_turns":
+            share = min(max((trained * f / (2 * np.pi) - low) / (high - low), 0.0), 1.0)
+            f = f * share + f / factor * (1 - share)
+        elif kind == "by_pair":
+            ramp = min(max((k - A) / max(B - A, 0.001), 0.0), 1.0)
+            f = f * (1 - ramp) + f / factor * ramp
+        freq.append(f)
+    return np.array(freq), amp
+
+
+def rotary_positions(T, starts=None, s=None):
+    """Position of every row in its sequence (-1 outside every sequence)."""
+    if starts is None:
+        return np.arange(T) % s
+    pos = np.full(T, -1, dtype=np.int64)
+    for a, e in zip(starts[:-1], starts[1:]):
+        pos[a:e] = np.arange(e - a)
+    return pos
+
+
+def rotate_heads(x, pos, rot, back=False):
+    """Rows x (T, d) of one head turned by their positions: pairs as complex
+    numbers times amplitude * exp(i pos freq) (`back`: the conjugate, the
+    gradient's map).  rot: dict n_rot, interleaved, freq, amplitude."""
+    y = np.array(x, dtype=np.float64)
+    n = rot["n_rot"]
+    if n == 0:
+        return y
+    i, j = (np.arange(0, n, 2), np.arange(1, n, 2)) if rot["interleaved"] else (np.arange(n // 2), np.arange(n // 2, n))
+    angle = np.outer(np.asarray(pos, dtype=np.float64), np.asarray(rot["freq"], dtype=np.float64))
+    z = (y[:, i] + 1j * y[:, j]) * rot["amplitude"] * np.exp((-1j if back else 1j) * angle)
+    y[:, i], y[:, j] = z.real, z.imag
+    return y
+
+
+def head_norm(x, kind, eps):
+    """(n, r): rows x normalised, r = 1 / sqrt(mean square + eps), of x less its
+    mean for kind "layer"."""
+    x = np.asarray(x, dtype=np.float64)
+    if kind == "layer":
+        x = x - x.mean(1, keepdims=True)
+    r = 1.0 / np.sqrt((x * x).mean(1, keepdims=True) + eps)
+    return x * r, r
+
+
+def qk_heads(cfg):
+    """(first column, "q" | "k") of every query and key head of the shard-major QKV."""
+    d, H, KV, N = cfg["d"], cfg["n_heads"], cfg["n_kv_heads"], cfg["N"]
+    w = (H + 2 * KV) // N
+    return [((i * w + j) * d, "q" if j < H // N else "k") for i in range(N) for j in range((H + KV) // N)]
+
+
+def qk_norm_rotary(X, pos, cfg, rot, norm=None, gains=None):
+    """QKV with every query and key head normalised (norm: dict kind, eps, or
+    None), times its gain (gains: dict q, k) and rotated, row t at position pos[t].
+    Pinned by: torch in float64 with an explicit 2 x 2 rotation of every pair."""
+    Y = np.array(X, dtype=np.float64)
+    d = cfg["d"]
+    for c, kind in qk_heads(cfg):
+        x = Y[:, c:c + d]
+        if norm is not None:
+            x = head_norm(x, norm["kind"], norm["eps"])[0] * gains[kind]
+        Y[:, c:c + d] = rotate_heads(x, pos, rot)
+    return Y
+
+
+def qk_norm_rotary_grad(X, dY, pos, cfg, rot, norm=None, gains=None):
+    """(dX, dict of the gains' gradients) of qk_norm_rotary.
+    Pinned by: autograd of the same in float64, differences."""
+    dX = np.array(dY, dtype=np.float64)
+    d = cfg["d"]
+    dg = {"q": np.zeros(d), "k": np.zeros(d)}
+    for c, kind in qk_heads(cfg):
+        dz = rotate_heads(dX[:, c:c + d], pos, rot, back=True)
+        if norm is not None:
+            n, r = head_norm(np.asarray(X)[:, c:c + d], norm["kind"], norm["eps"])
+            dg[kind] += (dz * n).sum(0)
+            e = dz * gains[kind]
+            dz = r * (e - n * (e * n).mean(1, keepdims=True))
+            if norm["kind"] == "layer":
+                dz -= r * e.mean(1, keepdims=True)
+        dX[:, c:c + d] = dz
+    return dX, dg
+
+
+# --------------------------------------------------------------------------
 # Closed forms the pages state
 # --------------------------------------------------------------------------
 def param_count(H, L, V):
