@@ -18,12 +18,13 @@
 // angle for sincospif.  A position costs one integer product a pair, and far
 // ones lose nothing to the range reduction.
 //
-// Every kernel streams: each value is read once and written once.  A block
-// takes a few rows; their cosines and sines are computed once into shared
-// memory and used by all heads.  A group of G lanes holds one head, 16 values
-// a lane: two vectors whose elements are partners (half layout: a distance of
-// n_rot / 2 apart), so that no value crosses lanes but in the norm's sums, and
-// a head may be written over itself.
+// One kernel form streams all of it: each value is read once and written once.
+// A group of G lanes holds one head, 16 values a lane: 8 pairs of partners, so
+// that no value crosses lanes but in the norm's sums, and a head may be
+// written over itself.  A block takes a chunk of heads, one a group, and walks
+// down its rows a tile at a time, so that a group's column, kind, gains and
+// gain sums never change.  The tile's cosines and sines are computed once, into
+// shared memory, while the tile before is worked on.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <math.h>
@@ -31,6 +32,7 @@
 #include <string.h>
 
 #include <algorithm>
+#include <mutex>
 
 #include "tp_device.cuh"
 #include "tp_entry.h"
@@ -41,11 +43,11 @@ namespace {
 
 constexpr int kRoThreads = 256;
 constexpr int kRoWarps = kRoThreads / 32;
-constexpr int kRoRows = 8;       // most rows a block takes at a time
+constexpr int kRoRows = 64;      // most rows of a tile
+constexpr int kRoTable = 16384;  // most bytes of its table
 constexpr int kRoMaxD = 512;     // head width
 constexpr int kRoPairs = kRoMaxD / 2;
 constexpr int kRoParts = 1024;   // most blocks of the backward with gains
-constexpr int kRoElems = 16;     // values of a head a lane holds
 
 enum RoMode : int { RO_ROTATE = 0, RO_NORM_FWD = 1, RO_NORM_BWD = 2 };
 
@@ -63,17 +65,23 @@ struct RoParams {
   int b, s;        // s: tokens of every sequence (no starts, no positions)
   int d, hq, hk;   // head width; query and key heads a shard
   int hs;          // heads a shard in memory: hq + 2 hk
-  int per;         // heads a shard that are visited: hs, or hq + hk where the values stay where they are
-  int items;       // visited heads a row
+  int items;       // query and key heads a row
+  int copied;      // values a row that are copied, 0 in place
   int pairs;       // rotated pairs a head
-  int G;           // lanes a head
-  int slots;       // pairs of vectors a head, the last one's second may be missing
-  int rot_slots;   // those with rotated elements
-  int width;       // cosines a row in shared memory
-  int rows;        // rows a block takes at a time
-  int back;        // the transposed rotation
+  int G, log_g;    // lanes a head
+  int slots;       // half layout: slots a head; interleaved: lanes a head that have values
+  int rot_slots;   // those with rotated pairs
+  int width;       // pairs of a row of the table
+  int row_floats;  // floats of a row
+  int fill_rows;   // rows that a block's threads fill at the same time
+  int chunks;      // parts that the heads are cut into, a block takes one
+  int chunk_heads; // heads of a chunk
+  int parts;       // rows a block works on at the same time
+  int steps;       // of a tile, a multiple of the stages
+  uint32_t apart;  // rows from one step to the next
   int centred;
   float eps, amp;
+  float amp_sin;   // negative for the transposed rotation
   unsigned* err;
   uint64_t turn[kRoPairs];  // turns a position, 64-bit fractions
 };
@@ -132,7 +140,10 @@ __device__ __forceinline__ void unpack(const uint32_t* w, float* f) {
     f[0] = __uint_as_float(w[0] << 16);
   } else {
 #pragma unroll
-    for (int i = 0; i < V / 2; ++i) unpack_bf16x2(w[i], f[2 * i], f[2 * i + 1]);
+    for (int i = 0; i < V / 2; ++i) {
+      f[2 * i] = __uint_as_float(w[i] << 16);
+      f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
   }
 }
 
@@ -150,455 +161,723 @@ __device__ __forceinline__ void pack(const float* f, uint32_t* w) {
   }
 }
 
-// Sum over the G lanes of a head (G a power of two); every lane of the warp
-// takes part.
-__device__ __forceinline__ float group_sum(float v, int G) {
-  for (int o = G >> 1; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return v;
+// Two fp32 operations an instruction (sm_100 and up): the kernels issue about
+// one instruction a value otherwise, more than the memory leaves time for.
+__device__ __forceinline__ void fma2(float* d, const float* a, const float* b, const float* c) {
+  asm("{.reg .b64 a, b, c;\n\t"
+      "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+      "fma.rn.f32x2 a, a, b, c;\n\tmov.b64 {%0, %1}, a;}"
+      : "=f"(d[0]), "=f"(d[1])
+      : "f"(a[0]), "f"(a[1]), "f"(b[0]), "f"(b[1]), "f"(c[0]), "f"(c[1]));
+}
+__device__ __forceinline__ void mul2(float* d, const float* a, const float* b) {
+  asm("{.reg .b64 a, b;\n\t"
+      "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "mul.rn.f32x2 a, a, b;\n\tmov.b64 {%0, %1}, a;}"
+      : "=f"(d[0]), "=f"(d[1])
+      : "f"(a[0]), "f"(a[1]), "f"(b[0]), "f"(b[1]));
 }
 
 // ---------------------------------------------------------------------------
 // Rows
 // ---------------------------------------------------------------------------
-// Start of the sequence that row t belongs to: the last start that is not
-// behind it.  32 starts a step; called by a whole warp.  Any contents of
-// `starts` end it in ceil(log32(b)) steps, inside the array.
-__device__ __forceinline__ int64_t start_of(const int64_t* starts, int b, int64_t t, int lane) {
-  int lo = 0, hi = b;
-  int64_t at = 0;
-  while (hi > lo) {
-    const int step = (hi - lo + 31) / 32;
-    const int i = lo + lane * step;
-    const int64_t v = i < hi ? __ldcg(starts + i) : INT64_MAX;
-    const unsigned below = __ballot_sync(0xffffffffu, v <= t);
-    const int last = below ? 31 - __clz(below) : 0;
-    at = __shfl_sync(0xffffffffu, v, last);
-    lo = lo + last * step;
-    hi = min(hi, lo + step);
-    if (step == 1) break;
+// The starts of the sequences as a warp holds them: up to 31 sequences a start a
+// lane, so that one load answers everything; more are looked for in memory.
+struct Starts {
+  const int64_t* from;  // null: every row is used
+  int b, lane;
+  int held;        // the lane's start, limited to [-1, 2^31 - 1]; behind the last one the largest
+  int first, end;  // rows of sequences
+
+  __device__ __forceinline__ static int limited(int64_t v) {
+    return static_cast<int>(min(max(v, static_cast<int64_t>(-1)), static_cast<int64_t>(INT32_MAX)));
   }
-  return at;
-}
-
-// Rows of sequences lie in [first, end); reports starts that decrease or leave
-// the buffer.
-__device__ __forceinline__ void used_rows(const RoParams& p, int64_t& first, int64_t& end) {
-  first = 0;
-  end = p.T;
-  if (p.starts == nullptr) return;
-  first = max(__ldcg(p.starts), static_cast<int64_t>(0));
-  end = min(__ldcg(p.starts + p.b), p.T);
-  bool fine = true;
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * kRoThreads + threadIdx.x; i < p.b;
-       i += static_cast<int64_t>(gridDim.x) * kRoThreads) {
-    const int64_t a = __ldcg(p.starts + i), e = __ldcg(p.starts + i + 1);
-    fine &= a >= 0 && e >= a && e <= p.T;
-  }
-  if (!fine) atomicOr(p.err, kErrInvalid);
-}
-
-// Positions of the tile's rows, 8 lanes a warp at most.
-__device__ __forceinline__ void fill_positions(const RoParams& p, int64_t row0, int n, int64_t first, int64_t end,
-                                               int64_t* pos) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  for (int r = warp; r < n; r += kRoWarps) {
-    const int64_t t = row0 + r;
-    int64_t at;
-    if (p.positions != nullptr) at = __ldcg(p.positions + t);
-    else if (p.starts != nullptr) at = t - start_of(p.starts, p.b, t, lane);
-    else at = t % p.s;
-    if (lane == 0) pos[r] = at;
-  }
-}
-
-// Where the cosine of pair k lies in its row.  Vectors of 8 are read as two
-// quads, each quad's lanes side by side.
-template <int V>
-__device__ __forceinline__ int place(int k, int rot_slots) {
-  if constexpr (V == 8) return (((k & 7) >> 2) * rot_slots + (k >> 3)) * 4 + (k & 3);
-  else return k;
-}
-
-// Cosines and sines of the tile's rows, times the amplitude.
-template <int V>
-__device__ __forceinline__ void fill_table(const RoParams& p, int n, const int64_t* pos, float* tab) {
-  const int w = p.width;
-  for (int i = threadIdx.x; i < n * w; i += kRoThreads) {
-    const int r = i / w, k = i - r * w;
-    float c = 1.f, s = 0.f;
-    if (k < p.pairs) {
-      const uint64_t turns = static_cast<uint64_t>(pos[r]) * p.turn[k];
-      const int32_t half_turns = static_cast<int32_t>((turns + (uint64_t{1} << 31)) >> 32);
-      sincospif(static_cast<float>(half_turns) * 0x1p-31f, &s, &c);
-      c *= p.amp;
-      s *= p.back ? -p.amp : p.amp;
+  // Reads them, and reports starts that decrease or leave the buffer.
+  __device__ __forceinline__ Starts(const RoParams& p) : from(p.starts), b(p.b), lane(threadIdx.x & 31), held(0) {
+    first = 0;
+    end = static_cast<int>(p.T);
+    if (from == nullptr) return;
+    bool fine = true;
+    if (b < 32) {
+      const int64_t v = lane <= b ? __ldcg(from + lane) : INT64_MAX;
+      const int64_t after = __shfl_down_sync(0xffffffffu, v, 1);
+      fine = lane > b || (v >= 0 && v <= p.T && (lane == b || after >= v));
+      held = limited(v);
+      first = max(__shfl_sync(0xffffffffu, held, 0), 0);
+      end = min(__shfl_sync(0xffffffffu, held, b), end);
+    } else {
+      first = max(limited(__ldcg(from)), 0);
+      end = min(limited(__ldcg(from + b)), end);
+      for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < b;
+           i += static_cast<int64_t>(gridDim.x) * blockDim.x) {
+        const int64_t a = __ldcg(from + i), e = __ldcg(from + i + 1);
+        fine &= a >= 0 && e >= a && e <= p.T;
+      }
     }
-    float* row = tab + static_cast<size_t>(r) * 2 * w + place<V>(k, p.rot_slots);
-    row[0] = c;
-    row[w] = s;
+    if (!fine) atomicOr(p.err, kErrInvalid);
+  }
+  // Start of the sequence that row t belongs to: the last one that is not behind
+  // it.  Called by a whole warp.  Any contents of memory end the search in
+  // ceil(log32(b)) steps, inside the array.
+  __device__ __forceinline__ int of(int t) const {
+    if (b < 32) {
+      const unsigned below = __ballot_sync(0xffffffffu, lane < b && held <= t);
+      return __shfl_sync(0xffffffffu, held, below ? 31 - __clz(below) : 0);
+    }
+    int lo = 0, hi = b, at = 0;
+    while (hi > lo) {
+      const int step = (hi - lo + 31) / 32;
+      const int i = lo + lane * step;
+      const int v = i < hi ? limited(__ldcg(from + i)) : INT32_MAX;
+      const unsigned below = __ballot_sync(0xffffffffu, v <= t);
+      const int last = below ? 31 - __clz(below) : 0;
+      at = __shfl_sync(0xffffffffu, v, last);
+      lo = lo + last * step;
+      hi = min(hi, lo + step);
+      if (step == 1) break;
+    }
+    return at;
+  }
+};
+
+// Positions of the rows of a tile: `steps` steps of p.parts rows, p.apart rows
+// apart.  Rows behind the buffer's have none.
+__device__ __forceinline__ void fill_positions(const RoParams& p, const Starts& starts, uint32_t row0, int steps,
+                                               int64_t* pos) {
+  const int n = steps * p.parts;
+  const uint32_t T = static_cast<uint32_t>(p.T);
+  auto row_of = [&](int r) {
+    const int step = p.parts == 1 ? r : r / p.parts;
+    return row0 + static_cast<uint32_t>(step) * p.apart + (r - step * p.parts);
+  };
+  if (p.positions == nullptr && starts.from != nullptr) {
+    for (int r = threadIdx.x >> 5; r < n; r += blockDim.x >> 5) {
+      const uint32_t t = row_of(r);
+      if (t >= T) continue;
+      const int at = starts.of(static_cast<int>(t));
+      if (starts.lane == 0) pos[r] = static_cast<int>(t) - at;
+    }
+  } else if (static_cast<int>(threadIdx.x) < n) {
+    const uint32_t t = row_of(threadIdx.x);
+    if (t < T) pos[threadIdx.x] = p.positions ? __ldcg(p.positions + t) : static_cast<int64_t>(t % p.s);
   }
 }
 
-template <int V>
-__device__ __forceinline__ void read_table(const float* row, int slot, int rot_slots, float* f) {
-  if constexpr (V == 8) {
-    const float4 a = reinterpret_cast<const float4*>(row)[slot];
-    const float4 b = reinterpret_cast<const float4*>(row)[rot_slots + slot];
-    f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
-    f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
-  } else if constexpr (V == 4) {
-    const float4 a = reinterpret_cast<const float4*>(row)[slot];
-    f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
+// A row of the table has, for every slot of kPairs pairs, their cosines, sines and
+// negated sines, times the amplitude, in kSlot floats: with 28 for 8 pairs the
+// 16-byte reads of eight lanes fall on different banks.
+template <int V, bool INTER>
+constexpr int kPairs = INTER ? 8 : V;
+template <int V, bool INTER>
+constexpr int kSlot = kPairs<V, INTER> == 8 ? 28 : 3 * V;
+
+// Where pair k's cosine lies in its row.  Interleaved: V / 2 pairs a vector,
+// vector v is number v / used of lane v % used.
+template <int V, bool INTER>
+__device__ __forceinline__ int place(const RoParams& p, int k) {
+  if constexpr (INTER) {
+    const int v = k / (V / 2), j = v / p.slots;
+    return (v - j * p.slots) * kSlot<V, INTER> + j * (V / 2) + k % (V / 2);
   } else {
-    f[0] = row[slot];
+    return k / V * kSlot<V, INTER> + k % V;
   }
+}
+
+// Angle of a position in half turns, in [-1, 1).
+__device__ __forceinline__ float half_turns(int64_t position, uint64_t turn) {
+  const uint64_t turns = static_cast<uint64_t>(position) * turn;
+  return static_cast<float>(static_cast<int32_t>((turns + (uint64_t{1} << 31)) >> 32)) * 0x1p-31f;
+}
+
+// The table of a tile's n rows.  A thread keeps its pair and goes from row to row.
+template <int V, bool INTER>
+__device__ __forceinline__ void fill_table(const RoParams& p, int n, const int64_t* pos, const uint64_t* turn, int r0,
+                                           int k0, float* tab) {
+  for (int k = k0; k < p.width; k += blockDim.x) {
+    const uint64_t t = turn[k];
+    float* to = tab + place<V, INTER>(p, k);
+    for (int r = r0; r < n; r += p.fill_rows) {
+      float c, s;
+      sincospif(half_turns(pos[r], t), &s, &c);
+      float* row = to + r * p.row_floats;
+      c *= p.amp;
+      s *= p.amp_sin;
+      row[0] = c;
+      row[kPairs<V, INTER>] = s;
+      row[2 * kPairs<V, INTER>] = -s;
+    }
+  }
+}
+
+template <int N>
+__device__ __forceinline__ void read_table(const float* from, float* f) {
+  if constexpr (N == 1) {
+    f[0] = from[0];
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; i += 4) {
+      const float4 a = *reinterpret_cast<const float4*>(from + i);
+      f[i] = a.x; f[i + 1] = a.y; f[i + 2] = a.z; f[i + 3] = a.w;
+    }
+  }
+}
+
+// One thread's copy of 8 or 16 bytes into shared memory, not waited for.
+template <int BYTES>
+__device__ __forceinline__ void copy_async(uint32_t to, const void* from) {
+  if constexpr (BYTES == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(to), "l"(from) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int LEFT>
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory");
 }
 
 // ---------------------------------------------------------------------------
 // A lane's part of a head
 // ---------------------------------------------------------------------------
-// Vectors of slot i: columns a and b of the head; a < 0: none, b < 0: only a.
-// Half layout: rotated slots first, their vectors n_rot / 2 apart, then
-// what is not rotated, vector after vector.  Interleaved (V = 8): vectors side by
-// side.
-template <int V, bool INTER>
-__device__ __forceinline__ void columns(const RoParams& p, int slot, int& a, int& b) {
-  if (slot >= p.slots) {
-    a = b = -1;
-    return;
-  }
-  if (INTER) {
-    a = 16 * slot;
-    b = a + 8;
-  } else if (slot < p.rot_slots) {
-    a = slot * V;
-    b = a + p.pairs;
-  } else {
-    a = 2 * p.pairs + 2 * (slot - p.rot_slots) * V;
-    b = a + V;
-  }
-  if (b >= p.d) b = -1;
-}
-
+// 16 / V vectors of V values, so that the lanes' vectors lie side by side in the
+// row.  Half layout: 8 / V slots of two vectors, a and b; the rotated ones first,
+// their vectors n_rot / 2 apart, pair e of a slot element e of both; then what is
+// not rotated.  Interleaved: pairs are elements 2e and 2e + 1 of a vector.  The
+// lane's values are held as f[0..7], the pairs' first elements, and f[8..15],
+// their second ones.
 template <class E, int V, bool INTER>
 struct Lane {
-  static constexpr int S = 8 / V;  // slots
+  static constexpr int S = 8 / V;
   static constexpr int N = Words<E, V>::N;
   static constexpr int kWords = 2 * S * N;
-  int a[S], b[S];
-  int first;  // the first slot; slot i is first + i G
+  int a[S], b[S];     // columns of a slot's vectors
+  bool ha[S], hb[S];  // and whether the head has them
+  int turned[2 * S];  // rotated pairs of the slot (half layout), of the vector (interleaved)
+  int first;          // the lane's number; slot i is number first + i G
+  // The lane's units of 8 or 16 bytes in a stage: those of one number lie side
+  // by side, lane after lane (no two lanes of a warp on one bank).  Single
+  // elements (V = 1) lie as in the row.
+  static constexpr int U = V * sizeof(E) < 16 ? V * sizeof(E) : 16;
+  uint32_t at0, apart;
 
-  __device__ __forceinline__ Lane(const RoParams& p, int lane) : first(lane & (p.G - 1)) {
-#pragma unroll
-    for (int i = 0; i < S; ++i) columns<V, INTER>(p, first + i * p.G, a[i], b[i]);
-  }
-  __device__ __forceinline__ void load(const E* head, uint32_t* w) const {
+  // home: the group's place in a stage
+  __device__ __forceinline__ Lane(const RoParams& p, int lane, uint32_t home) : first(lane & (p.G - 1)) {
+    at0 = V == 1 ? home : home + first * U;
+    apart = p.G * U;
 #pragma unroll
     for (int i = 0; i < S; ++i) {
-#pragma unroll
-      for (int k = 0; k < 2 * N; ++k) w[2 * N * i + k] = 0u;
-      if (a[i] >= 0) load_vec<E, V>(head + a[i], w + 2 * N * i);
-      if (b[i] >= 0) load_vec<E, V>(head + b[i], w + 2 * N * i + N);
+      if (INTER) {
+        a[i] = (first + 2 * i * p.slots) * V;
+        b[i] = a[i] + p.slots * V;
+        ha[i] = first < p.slots && a[i] < p.d;
+        hb[i] = first < p.slots && b[i] < p.d;
+        turned[2 * i] = ha[i] ? min(max(p.pairs - a[i] / 2, 0), V / 2) : 0;
+        turned[2 * i + 1] = hb[i] ? min(max(p.pairs - b[i] / 2, 0), V / 2) : 0;
+        continue;
+      }
+      const int slot = first + i * p.G, rest = p.slots - p.rot_slots;
+      if (slot < p.rot_slots) {
+        a[i] = slot * V;
+        b[i] = a[i] + p.pairs;
+      } else {
+        a[i] = 2 * p.pairs + (slot - p.rot_slots) * V;
+        b[i] = a[i] + rest * V;
+      }
+      ha[i] = slot < p.slots && a[i] < p.d;
+      hb[i] = slot < p.slots && b[i] < p.d;
+      turned[i] = slot < p.rot_slots ? V : 0;
     }
   }
-  __device__ __forceinline__ void store(E* head, const uint32_t* w) const {
+  // Zeros in place of what the head does not have: nothing is copied there.
+  __device__ __forceinline__ void clear(uint8_t* stage) const {
+    if constexpr (V > 1) {
 #pragma unroll
-    for (int i = 0; i < S; ++i) {
-      if (a[i] >= 0) store_words<E, V>(head + a[i], w + 2 * N * i);
-      if (b[i] >= 0) store_words<E, V>(head + b[i], w + 2 * N * i + N);
-    }
-  }
-  // f[2 V i ..]: slot i's vector a, then b
-  __device__ __forceinline__ void floats(const uint32_t* w, float* f) const {
+      for (int u = 0; u < 16 * static_cast<int>(sizeof(E)) / U; ++u) {
+        const int v = u * U / (V * static_cast<int>(sizeof(E)));
+        if (v % 2 ? hb[v / 2] : ha[v / 2]) continue;
 #pragma unroll
-    for (int i = 0; i < 2 * S; ++i) unpack<E, V>(w + N * i, f + V * i);
-  }
-  __device__ __forceinline__ void words(const float* f, uint32_t* w) const {
-#pragma unroll
-    for (int i = 0; i < 2 * S; ++i) pack<E, V>(f + V * i, w + N * i);
-  }
-  // Rotates the lane's pairs; what is not rotated is not touched.
-  __device__ __forceinline__ void turn(const RoParams& p, const float* row, float* f) const {
-#pragma unroll
-    for (int i = 0; i < S; ++i) {
-      const int slot = first + i * p.G;
-      if (slot >= p.rot_slots) continue;
-      float c[V], s[V];
-      read_table<V>(row, slot, p.rot_slots, c);
-      read_table<V>(row + p.width, slot, p.rot_slots, s);
-#pragma unroll
-      for (int e = 0; e < V; ++e) {
-        const int u = INTER ? 2 * e : 2 * V * i + e, v = INTER ? u + 1 : u + V;
-        if (INTER && slot * 8 + e >= p.pairs) continue;
-        const float x = f[u], y = f[v];
-        f[u] = x * c[e] - y * s[e];
-        f[v] = fmaf(x, s[e], y * c[e]);
+        for (int k = 0; k < U; k += 8) *reinterpret_cast<uint64_t*>(stage + at0 + u * apart + k) = 0;
       }
     }
   }
-  // f[j] <- fn(f[j], column) for the columns that the lane has
+  // Copies the lane's part of a head into its place of a stage.  With single
+  // elements every G-th 16 bytes of the head, which other lanes read.
+  __device__ __forceinline__ void fetch(const RoParams& p, const uint8_t* head, uint32_t stage) const {
+    if constexpr (V == 1) {
+      for (int c = first * 16; c < p.d * static_cast<int>(sizeof(E)); c += p.G * 16)
+        copy_async<16>(stage + at0 + c, head + c);
+    } else {
+      constexpr int B = V * sizeof(E);
+#pragma unroll
+      for (int i = 0; i < S; ++i) {
+        const uint8_t *pa = head + a[i] * sizeof(E), *pb = head + b[i] * sizeof(E);
+#pragma unroll
+        for (int k = 0; k < B / U; ++k) {
+          if (ha[i]) copy_async<U>(stage + at0 + (2 * i * (B / U) + k) * apart, pa + k * U);
+          if (hb[i]) copy_async<U>(stage + at0 + ((2 * i + 1) * (B / U) + k) * apart, pb + k * U);
+        }
+      }
+    }
+  }
+  // The lane's vectors from a stage.
+  __device__ __forceinline__ void read(const uint8_t* stage, uint32_t* w) const {
+    if constexpr (V == 1) {
+#pragma unroll
+      for (int i = 0; i < S; ++i) {
+        w[2 * i] = w[2 * i + 1] = 0u;
+        if (ha[i]) load_vec<E, V>(reinterpret_cast<const E*>(stage + at0) + a[i], w + 2 * i);
+        if (hb[i]) load_vec<E, V>(reinterpret_cast<const E*>(stage + at0) + b[i], w + 2 * i + 1);
+      }
+    } else {
+#pragma unroll
+      for (int u = 0; u < 16 * static_cast<int>(sizeof(E)) / U; ++u) {
+        const uint8_t* from = stage + at0 + u * apart;
+        if constexpr (U == 16) {
+          const uint4 q = *reinterpret_cast<const uint4*>(from);
+          w[4 * u] = q.x; w[4 * u + 1] = q.y; w[4 * u + 2] = q.z; w[4 * u + 3] = q.w;
+        } else {
+          const uint2 q = *reinterpret_cast<const uint2*>(from);
+          w[2 * u] = q.x; w[2 * u + 1] = q.y;
+        }
+      }
+    }
+  }
+  // Writes the lane's vectors; single elements go through shared memory.
+  __device__ __forceinline__ void store(const RoParams& p, uint8_t* stage, uint8_t* head, bool mine,
+                                        const uint32_t* w) const {
+    if constexpr (V == 1) {
+      __syncwarp();  // the others have read theirs
+      put(reinterpret_cast<E*>(stage + at0), w);
+      __syncwarp();
+      if (mine) {
+        for (int c = first * 16; c < p.d * static_cast<int>(sizeof(E)); c += p.G * 16)
+          *reinterpret_cast<uint4*>(head + c) = *reinterpret_cast<const uint4*>(stage + at0 + c);
+      }
+    } else if (mine) {
+      put(reinterpret_cast<E*>(head), w);
+    }
+  }
+  __device__ __forceinline__ void put(E* head, const uint32_t* w) const {
+#pragma unroll
+    for (int i = 0; i < S; ++i) {
+      if (ha[i]) store_words<E, V>(head + a[i], w + 2 * N * i);
+      if (hb[i]) store_words<E, V>(head + b[i], w + 2 * N * i + N);
+    }
+  }
+  __device__ __forceinline__ void floats(const uint32_t* w, float* f) const {
+    float v[16];
+#pragma unroll
+    for (int i = 0; i < 2 * S; ++i) unpack<E, V>(w + N * i, v + V * i);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) f[at(i)] = v[i];
+  }
+  __device__ __forceinline__ void words(const float* f, uint32_t* w) const {
+    float v[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = f[at(i)];
+#pragma unroll
+    for (int i = 0; i < 2 * S; ++i) pack<E, V>(v + V * i, w + N * i);
+  }
+  // Place in f of element i of the lane's vectors in a row.
+  __device__ __forceinline__ static constexpr int at(int i) {
+    return INTER ? (i & 1) * 8 + i / 2 : (i / V & 1) * 8 + i / (2 * V) * V + i % V;
+  }
+  // fn(place in f, column) for every value that the head has.
   template <class F>
   __device__ __forceinline__ void each(F&& fn) const {
 #pragma unroll
     for (int i = 0; i < S; ++i) {
 #pragma unroll
       for (int e = 0; e < V; ++e) {
-        if (a[i] >= 0) fn(2 * V * i + e, a[i] + e);
-        if (b[i] >= 0) fn(2 * V * i + V + e, b[i] + e);
+        if (ha[i]) fn(at(2 * V * i + e), a[i] + e);
+        if (hb[i]) fn(at(2 * V * i + V + e), b[i] + e);
+      }
+    }
+  }
+  // Rotates the lane's pairs; what is not rotated is not touched.
+  __device__ __forceinline__ void turn(const RoParams& p, const float* row, float* f) const {
+    if constexpr (INTER) {
+      if (turned[0] == 0) return;  // (the vectors' columns rise)
+      const float* from = row + first * kSlot<V, INTER>;
+      float c[8], s[8], z[8];
+      read_table<8>(from, c);
+      read_table<8>(from + 8, s);
+      read_table<8>(from + 16, z);
+#pragma unroll
+      for (int j = 0; j < 2 * S; ++j) {
+        constexpr int P = V / 2;
+        if (turned[j] == P) {
+          pairs<P>(f + j * P, f + 8 + j * P, c + j * P, s + j * P, z + j * P);
+        } else {
+          // the last vector of a part that does not fill it
+#pragma unroll
+          for (int e = 0; e < P; ++e)
+            if (e < turned[j]) pairs<1>(f + j * P + e, f + 8 + j * P + e, c + j * P + e, s + j * P + e, z + j * P + e);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < S; ++i) {
+        if (turned[i] == 0) continue;
+        const float* from = row + (first + i * p.G) * kSlot<V, INTER>;
+        float c[V], s[V], z[V];
+        read_table<V>(from, c);
+        read_table<V>(from + V, s);
+        read_table<V>(from + 2 * V, z);
+        pairs<V>(f + V * i, f + 8 + V * i, c, s, z);
+      }
+    }
+  }
+  // N pairs (x, y) <- (x c - y s, x s + y c), z = -s
+  template <int N>
+  __device__ __forceinline__ static void pairs(float* x, float* y, const float* c, const float* s, const float* z) {
+    if constexpr (N == 1) {
+      const float u = fmaf(x[0], c[0], y[0] * z[0]);
+      y[0] = fmaf(x[0], s[0], y[0] * c[0]);
+      x[0] = u;
+    } else {
+#pragma unroll
+      for (int e = 0; e < N; e += 2) {
+        float u[2], v[2];
+        mul2(u, y + e, z + e);
+        mul2(v, y + e, c + e);
+        fma2(y + e, x + e, s + e, v);
+        fma2(x + e, x + e, c + e, u);
       }
     }
   }
 };
 
-// A group's walk over the tile's (row, head) pairs.
-struct Walk {
-  int r, h, dr, dh, items;
-  __device__ __forceinline__ Walk(int group, int groups, int items_) : items(items_) {
-    r = group / items;
-    h = group - r * items;
-    dr = groups / items;
-    dh = groups - dr * items;
+// Sums of N values each over the G lanes of a head (a power of two); every
+// lane of the warp takes part.  One branch for the usual widths, not one a step.
+template <int N, int FROM>
+__device__ __forceinline__ void lane_sums(float* v) {
+#pragma unroll
+  for (int o = FROM; o > 0; o >>= 1) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
   }
-  __device__ __forceinline__ void step() {
-    r += dr;
-    h += dh;
-    if (h >= items) {
-      h -= items;
-      ++r;
-    }
-  }
-};
-
-// Column of visited head h, and what it is: 0 query, 1 key, 2 value.
-__device__ __forceinline__ int head_column(const RoParams& p, int h, int& kind) {
-  const int shard = h / p.per, at = h - shard * p.per;
-  kind = at < p.hq ? 0 : at < p.hq + p.hk ? 1 : 2;
-  return (shard * p.hs + at) * p.d;
 }
-
-__device__ __forceinline__ void fill_gains(const RoParams& p, float* gains) {
-  for (int i = threadIdx.x; i < 2 * p.d; i += kRoThreads) {
-    const float* g = i < p.d ? p.gq : p.gk;
-    gains[i] = g == nullptr ? 1.f : __ldg(g + (i < p.d ? i : i - p.d));
+template <int N>
+__device__ __forceinline__ void group_sums(float* v, int G) {
+  if (G == 8) return lane_sums<N, 4>(v);
+  if (G == 4) return lane_sums<N, 2>(v);
+  if (G >= 16) {
+    if (G == 32) lane_sums<N, 16>(v);
+    else lane_sums<N, 8>(v);
+  } else if (G == 2) {
+    lane_sums<N, 1>(v);
   }
 }
 
-// Mean (0 unless centred) and 1 / sqrt(mean square + eps) of the lane's head;
-// x loses the mean.  Sums are fp32.
-template <class L>
-__device__ __forceinline__ float norm_of(const RoParams& p, const L& lane, float* x) {
-  const float inv_d = 1.f / static_cast<float>(p.d);
-  if (p.centred) {
-    float m = 0.f;
+// sum over f[i] g[i]: two chains of 8
+__device__ __forceinline__ float dot16(const float* f, const float* g) {
+  float t[2] = {0.f, 0.f};
 #pragma unroll
-    for (int i = 0; i < kRoElems; ++i) m += x[i];
-    m = group_sum(m, p.G) * inv_d;
-    lane.each([&](int i, int) { x[i] -= m; });
-  }
-  float q = 0.f;
-#pragma unroll
-  for (int i = 0; i < kRoElems; ++i) q = fmaf(x[i], x[i], q);
-  return rsqrtf(group_sum(q, p.G) * inv_d + p.eps);
+  for (int i = 0; i < 16; i += 2) fma2(t, f + i, g + i, t);
+  return t[0] + t[1];
 }
 
 // ---------------------------------------------------------------------------
-// Rotation, and the norm's forward
+// The kernel
 // ---------------------------------------------------------------------------
-template <class E, int V, bool INTER, bool NORM>
-__global__ void __launch_bounds__(kRoThreads) rotary_kernel(const __grid_constant__ RoParams p) {
-  extern __shared__ __align__(16) float smem[];
-  __shared__ int64_t pos[kRoRows];
-  float* tab = smem;
-  float* gains = smem + static_cast<size_t>(p.rows) * 2 * p.width;
-  const int64_t row0 = static_cast<int64_t>(blockIdx.x) * p.rows;
-  const int n = static_cast<int>(min(static_cast<int64_t>(p.rows), p.T - row0));
-  int64_t first, end;
-  pdl_wait();
-  pdl_trigger();
-  used_rows(p, first, end);
-  const Lane<E, V, INTER> L(p, threadIdx.x & 31);
-  const E* x = static_cast<const E*>(p.x);
-  E* out = static_cast<E*>(p.out);
-  const int groups = kRoThreads / p.G;
-  Walk at(threadIdx.x / p.G, groups, p.items);
-  uint32_t next[Lane<E, V, INTER>::kWords];
-  int kind = 2, col = 0;
-  if (at.r < n) {
-    col = head_column(p, at.h, kind);
-    L.load(x + (row0 + at.r) * p.ld_x + col, next);
-  }
-  fill_positions(p, row0, n, first, end, pos);
-  if (NORM) fill_gains(p, gains);
-  __syncthreads();
-  fill_table<V>(p, n, pos, tab);
-  __syncthreads();
-  const int steps = (n * p.items + groups - 1) / groups;
-  for (int i = 0; i < steps; ++i) {
-    uint32_t w[Lane<E, V, INTER>::kWords];
-#pragma unroll
-    for (int k = 0; k < Lane<E, V, INTER>::kWords; ++k) w[k] = next[k];
-    const int r = at.r, what = kind;
-    const bool mine = r < n;
-    const int64_t row = row0 + r;
-    E* to = out + row * p.ld_out + col;
-    at.step();
-    if (at.r < n) {
-      col = head_column(p, at.h, kind);
-      L.load(x + (row0 + at.r) * p.ld_x + col, next);
-    }
-    float f[kRoElems];
-    L.floats(w, f);
-    if (NORM) {
-      float v[kRoElems];
-#pragma unroll
-      for (int k = 0; k < kRoElems; ++k) v[k] = mine ? f[k] : 0.f;
-      const float inv = norm_of(p, L, v);
-      if (what != 2) {
-        const float* g = gains + (what == 1 ? p.d : 0);
-        L.each([&](int k, int c) { f[k] = v[k] * inv * g[c]; });
-      }
-    }
-    if (mine && row >= first && row < end) {
-      if (what != 2) {
-        L.turn(p, tab + static_cast<size_t>(r) * 2 * p.width, f);
-        L.words(f, w);
-      }
-      L.store(to, w);
-    }
-  }
+// Head of a group of the chunk.
+__device__ __forceinline__ int block_head(const RoParams& p, int chunk, int slot) {
+  const int log_unit = 5 - p.log_g, in_unit = slot & ((1 << log_unit) - 1);
+  return p.chunks == 1 ? slot : (((slot >> log_unit) * p.chunks + chunk) << log_unit) + in_unit;
 }
 
-// ---------------------------------------------------------------------------
-// The norm's backward
-// ---------------------------------------------------------------------------
-// Blocks take tiles in turn; every lane sums its columns' part of the gains'
-// gradients over all heads it sees, then the block sums its warps' in order.
-template <class E, int V, bool INTER>
-__global__ void __launch_bounds__(kRoThreads) qk_norm_bwd_kernel(const __grid_constant__ RoParams p) {
-  extern __shared__ __align__(16) float smem[];
-  __shared__ int64_t pos[kRoRows];
+// Rows on their way to a group.
+template <class E, int MODE>
+constexpr int kDepth = sizeof(E) == 4 ? 2 : MODE == RO_NORM_BWD ? 3 : 4;
+// A stage: the groups' heads and, behind those of x, the values that are copied.  Constants for
+// blocks of up to NT threads: with a size known at the launch the addresses took registers that the kernels lack
+// (norm's forward 39 us instead of 33).
+template <class E, int NT>
+constexpr uint32_t kStageY = NT * 16 * sizeof(E);
+template <class E, int NT>
+constexpr uint32_t kStageX = kStageY<E, NT> + NT * 8 * sizeof(E);
+
+// Blocks on an SM at the same time, by their registers: the backward holds 64 values a lane.
+constexpr int kRoFew = 160;  // threads of the smaller blocks
+template <int MODE, int NT>
+constexpr int kBlocks = MODE == RO_NORM_BWD ? (NT == kRoFew ? 3 : 2) : (NT == kRoFew ? 5 : 3);
+
+template <class E, int V, bool INTER, int MODE, int NT>
+__global__ void __launch_bounds__(NT, kBlocks<MODE, NT>)
+    rotary_kernel(const __grid_constant__ RoParams p) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  __shared__ int64_t pos[2][kRoRows];
   using LaneT = Lane<E, V, INTER>;
-  float* gains = smem;
-  float* tab = smem + 2 * p.d;
+  constexpr bool kBwd = MODE == RO_NORM_BWD;
+  constexpr int D = kDepth<E, MODE>;
+  constexpr uint32_t stage = kStageX<E, NT>, stage_y = kStageY<E, NT>;
+  constexpr uint32_t ys = D * stage;  // the stages of dy lie behind those of x
+  uint64_t* turn = reinterpret_cast<uint64_t*>(smem + ys + (kBwd ? D * stage_y : 0));
+  float* tab = reinterpret_cast<float*>(turn + ((p.width + 1) & ~1));
+  // the group's head: the chunks take turns by runs of a warp's heads
+  const int group = threadIdx.x >> p.log_g;
+  const LaneT L(p, threadIdx.x & 31, group * p.G * 16 * sizeof(E));
+  const int block = blockIdx.x / p.chunks, chunk = blockIdx.x - block * p.chunks;
+  const int part = group / p.chunk_heads, slot = group - part * p.chunk_heads;
+  const int head = block_head(p, chunk, slot);
+  const bool active = part < p.parts && head < p.items;
+  const int in_shard = p.hq + p.hk, shard = head / in_shard, place_in = head - shard * in_shard;
+  const bool key = place_in >= p.hq;
+  // eight of the value heads' columns, numbered through the shards: half as many as the lane's own at most, so one
+  // such run a lane is enough
+  const int v_at = (head * p.G + L.first) * 8, v_width = p.hk * p.d, v_shard = v_at / v_width;
+  const bool copies = active && v_at < p.copied;
+  // the block's rows: p.parts at a time, p.apart apart
+  const uint32_t base = block * p.parts, T = static_cast<uint32_t>(p.T);
+  const int total = (T - base + p.apart - 1) / p.apart;  // steps
+  const int fill_r = threadIdx.x / max(p.width, 1), fill_k = p.width > blockDim.x ? threadIdx.x : threadIdx.x - fill_r * p.width;
+  const int r0 = p.width > blockDim.x ? 0 : fill_r < p.fill_rows ? fill_r : INT32_MAX;
+
+  for (int i = threadIdx.x; i < p.width; i += blockDim.x) turn[i] = i < p.pairs ? p.turn[i] : 0;
+#pragma unroll
+  for (int i = 0; i < D; ++i) {
+    L.clear(smem + i * stage);
+    if (kBwd) L.clear(smem + ys + i * stage_y);
+  }
+  // column of the head's rows
+  const int64_t col = static_cast<int64_t>(shard * p.hs + place_in) * p.d;
+  uint32_t row = base + part;
+  const uint8_t* fx = static_cast<const uint8_t*>(p.x) + (row * p.ld_x + col) * sizeof(E);
+  const uint8_t* fy = static_cast<const uint8_t*>(p.dy) + (row * p.ld_dy + col) * sizeof(E);
+  uint8_t* to = static_cast<uint8_t*>(p.out) + (row * p.ld_out + col) * sizeof(E);
+  // from there to the value columns
+  const int64_t to_v = (static_cast<int64_t>(v_shard * p.hs + in_shard) * p.d + v_at - v_shard * v_width - col) *
+                       static_cast<int64_t>(sizeof(E));
+  const uint32_t v_home = stage_y + threadIdx.x * 8 * sizeof(E);
+  const int64_t step_x = p.apart * p.ld_x * sizeof(E), step_dy = p.apart * p.ld_dy * sizeof(E);
+  const int64_t step_out = p.apart * p.ld_out * sizeof(E);
   pdl_wait();
   pdl_trigger();
-  int64_t first, end;
-  used_rows(p, first, end);
-  fill_gains(p, gains);
-  const LaneT L(p, threadIdx.x & 31);
-  const E* x = static_cast<const E*>(p.x);
-  const E* dy = static_cast<const E*>(p.dy);
-  E* out = static_cast<E*>(p.out);
-  const int groups = kRoThreads / p.G;
+  // fetches a row into stage `into`; unused rows too, so that nothing waits for the starts
+  const uint32_t smem_at = static_cast<uint32_t>(__cvta_generic_to_shared(smem));
+  uint32_t f_row = row;
+  int f_left = active ? total : 0;
+  auto fetch = [&](int into) {
+    if (f_left > 0 && f_row < T) {
+      L.fetch(p, fx, smem_at + into * stage);
+      if (kBwd) L.fetch(p, fy, smem_at + ys + into * stage_y);
+      if (copies) {
+#pragma unroll
+        for (uint32_t k = 0; k < 8 * sizeof(E); k += 16)
+          copy_async<16>(smem_at + into * stage + v_home + k, (kBwd ? fy : fx) + to_v + k);
+      }
+    }
+    copies_commit();
+    --f_left;
+    f_row += p.apart;
+    fx += step_x;
+    if (kBwd) fy += step_dy;
+  };
+#pragma unroll
+  for (int i = 0; i < D - 1; ++i) fetch(i);
+  const Starts starts(p);
+  const uint32_t first = starts.first;
+  const uint32_t used = active && starts.end > starts.first ? starts.end - starts.first : 0;  // (starts may decrease)
+  fill_positions(p, starts, base, min(p.steps, total), pos[0]);
+  if (total > p.steps) fill_positions(p, starts, base + p.steps * p.apart, min(p.steps, total - p.steps), pos[1]);
+  float g[MODE != RO_ROTATE ? 16 : 1], sum[kBwd ? 16 : 1];
+  if (MODE != RO_ROTATE) {
+    const float* gain = key ? p.gk : p.gq;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) g[i] = 0.f;
+    L.each([&](int i, int c) { g[i] = gain == nullptr ? 1.f : __ldg(gain + c); });
+  }
+  if (kBwd) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) sum[i] = 0.f;
+  }
+  __syncthreads();
+  fill_table<V, INTER>(p, min(p.steps, total) * p.parts, pos[0], turn, r0, fill_k, tab);
   const float inv_d = 1.f / static_cast<float>(p.d);
-  float sum[2][kRoElems];
+  const int tab_floats = p.steps * p.parts * p.row_floats;
+
+  // a row: stage `from` holds it, and the row D - 1 steps ahead goes into the stage before
+  auto work = [&](int from, const float* angles) {
+    const bool mine = row - first < used;
+    if (V == 1) __syncwarp();  // the stage that is filled now is read
+    fetch((from + D - 1) % D);
+    copies_wait<D - 1>();
+    if (V == 1) __syncwarp();
+    uint8_t* sx = smem + from * stage;
+    uint8_t* sy = smem + ys + from * stage_y;
+    uint32_t wx[LaneT::kWords];
+    if (!kBwd) L.read(sx, wx);
+      if (!kBwd) {
+        float f[16];
+        L.floats(wx, f);
+        if (MODE == RO_NORM_FWD) {
+          if (p.centred) {
+            float m = 0.f;
 #pragma unroll
-  for (int i = 0; i < kRoElems; ++i) sum[0][i] = sum[1][i] = 0.f;
-  for (int64_t row0 = static_cast<int64_t>(blockIdx.x) * p.rows; row0 < p.T;
-       row0 += static_cast<int64_t>(gridDim.x) * p.rows) {
-    const int n = static_cast<int>(min(static_cast<int64_t>(p.rows), p.T - row0));
-    Walk at(threadIdx.x / p.G, groups, p.items);
-    uint32_t nx[LaneT::kWords], ny[LaneT::kWords];
-    int kind = 2, col = 0;
-    auto fetch = [&] {
-      if (at.r >= n) return;
-      col = head_column(p, at.h, kind);
-      if (kind != 2) L.load(x + (row0 + at.r) * p.ld_x + col, nx);
-      L.load(dy + (row0 + at.r) * p.ld_dy + col, ny);
-    };
-    fetch();
-    __syncthreads();  // the last tile's table and positions are read
-    fill_positions(p, row0, n, first, end, pos);
-    __syncthreads();
-    fill_table<V>(p, n, pos, tab);
-    __syncthreads();
-    const int steps = (n * p.items + groups - 1) / groups;
-    for (int i = 0; i < steps; ++i) {
-      uint32_t wx[LaneT::kWords], wy[LaneT::kWords];
+            for (int i = 0; i < 16; ++i) m += f[i];
+            group_sums<1>(&m, p.G);
+            m *= -inv_d;
+            L.each([&](int i, int) { f[i] += m; });
+          }
+          float q = dot16(f, f);
+          group_sums<1>(&q, p.G);
+          const float inv = rsqrtf(fmaf(q, inv_d, p.eps)), both[2] = {inv, inv};
 #pragma unroll
-      for (int k = 0; k < LaneT::kWords; ++k) wx[k] = nx[k], wy[k] = ny[k];
-      const int r = at.r, what = kind;
-      const int64_t row = row0 + r;
-      const bool mine = r < n && row >= first && row < end;
-      const bool turned = mine && what != 2;
-      E* to = out + row * p.ld_out + col;
-      at.step();
-      fetch();
-      float v[kRoElems], e[kRoElems];
+          for (int i = 0; i < 16; i += 4) {
+            for (int j = 0; j < 4; j += 2) {
+            mul2(f + i + j, f + i + j, both);
+            mul2(f + i + j, f + i + j, g + i + j); }
+          }
+        }
+        if (mine) {
+          L.turn(p, angles, f);
+          L.words(f, wx);
+        }
+        L.store(p, sx, to, mine, wx);
+      } else {
+        uint32_t wy[LaneT::kWords];
+        float f[16], e[16];
+        L.read(sy, wy);
+        L.floats(wy, e);
+        if (mine) L.turn(p, angles, e);
+        L.read(sx, wx);
+        L.floats(wx, f);
+        float mean = 0.f;
+        if (p.centred) {
+          float m[2] = {0.f, 0.f};
 #pragma unroll
-      for (int k = 0; k < LaneT::kWords; ++k) {
-        if (!turned) wx[k] = 0u;
+          for (int i = 0; i < 16; i += 4) {
+            for (int j = 0; j < 4; ++j) {
+            m[0] += f[i + j];
+            m[1] = fmaf(e[i + j], g[i + j], m[1]); }
+          }
+          group_sums<2>(m, p.G);
+          const float less = m[0] * -inv_d;
+          L.each([&](int i, int) { f[i] += less; });
+          mean = m[1] * inv_d;
+        }
+        // q = |x|^2 and the sum of e g x
+        float q[2];
+        q[0] = dot16(f, f);
+        float along[2] = {0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < 16; i += 4) {
+          for (int j = 0; j < 4; j += 2) {
+          float t[2];
+          mul2(t, e + i + j, f + i + j);
+          fma2(along, t, g + i + j, along); }
+        }
+        q[1] = along[0] + along[1];
+        group_sums<2>(q, p.G);
+        const float inv = rsqrtf(fmaf(q[0], inv_d, p.eps));
+        // dx = inv e g - x inv (inv (inv q1 / d)): in this order nothing is larger than the result's parts
+        const float k = -inv * (inv * (inv * (q[1] * inv_d)));
+        const float invs[2] = {inv, inv}, ks[2] = {k, k};
+        if (mine) {
+          const float shift[2] = {-inv * mean, -inv * mean};
+#pragma unroll
+          for (int i = 0; i < 16; i += 4) {
+            for (int j = 0; j < 4; j += 2) {
+            float t[2];
+            mul2(e + i + j, e + i + j, invs);
+            fma2(sum + i + j, e + i + j, f + i + j, sum + i + j);
+            if (p.centred) fma2(t, f + i + j, ks, shift);
+            else mul2(t, f + i + j, ks);
+            fma2(e + i + j, e + i + j, g + i + j, t); }
+          }
+          L.words(e, wy);
+        }
+        L.store(p, sy, to, mine, wy);
       }
-      L.floats(wx, v);
-      L.floats(wy, e);
-      const float inv = norm_of(p, L, v);
-      float along = 0.f, mean = 0.f;
-      if (turned) {
-        L.turn(p, tab + static_cast<size_t>(r) * 2 * p.width, e);
-        const float* g = gains + (what == 1 ? p.d : 0);
-        L.each([&](int k, int c) {
-          v[k] *= inv;
-          const float t = e[k] * v[k];
-          sum[0][k] += what == 0 ? t : 0.f;
-          sum[1][k] += what == 1 ? t : 0.f;
-          e[k] *= g[c];
-          along = fmaf(e[k], v[k], along);
-          mean += e[k];
-        });
-      }
-      along = group_sum(along, p.G) * inv_d;
-      mean = p.centred ? group_sum(mean, p.G) * inv_d : 0.f;
-      if (turned) {
+    if (mine && copies) {
 #pragma unroll
-        for (int k = 0; k < kRoElems; ++k) e[k] = inv * (fmaf(-v[k], along, e[k]) - mean);
-        L.words(e, wy);
+      for (uint32_t k = 0; k < 8 * sizeof(E); k += 16)
+        *reinterpret_cast<uint4*>(to + to_v + k) = *reinterpret_cast<const uint4*>(sx + v_home + k);
+    }
+    row += p.apart;
+    to += step_out;
+  };
+  int left = total;
+  uint32_t ahead = base + 2 * p.steps * p.apart;  // first row of the tile after the next
+  for (int even = 0; left > 0; left -= p.steps, ahead += p.steps * p.apart, even ^= 1) {
+    __syncthreads();  // this tile's table and the next one's positions are there; the last tile's are read
+    if (left > p.steps)
+      fill_table<V, INTER>(p, min(p.steps, left - p.steps) * p.parts, pos[even ^ 1], turn, r0, fill_k,
+                    tab + (even ^ 1) * tab_floats);
+    if (left > 2 * p.steps) fill_positions(p, starts, ahead, min(p.steps, left - 2 * p.steps), pos[even]);
+    const float* angles = tab + even * tab_floats + part * p.row_floats;
+    const int n = min(p.steps, left);
+    // (steps is a multiple of D: a tile begins at stage 0)
+    for (int i = 0; i < n; i += D) {
+#pragma unroll
+      for (int j = 0; j < D; ++j) {
+        if (i + j >= n) break;
+        work(j, angles);
+        angles += p.parts * p.row_floats;
       }
-      if (mine) L.store(to, wy);
     }
   }
-  if (p.partial == nullptr) return;
-  // groups of a warp, then warps
-  for (int o = p.G; o < 32; o <<= 1) {
+  copies_wait<0>();
+  if constexpr (kBwd) {
+    if (p.partial == nullptr) return;
+    // the block's groups of each kind, in their order
+    __syncthreads();
+    const int d = p.d;
+    float* red = reinterpret_cast<float*>(smem);
+    for (int what = 0; what < 2; ++what) {
+      // a warp's groups first: values of the other kind count as zero
+      float t[16];
 #pragma unroll
-    for (int k = 0; k < kRoElems; ++k) {
-      sum[0][k] += __shfl_xor_sync(0xffffffffu, sum[0][k], o);
-      sum[1][k] += __shfl_xor_sync(0xffffffffu, sum[1][k], o);
+      for (int i = 0; i < 16; ++i) t[i] = active && key == (what == 1) ? sum[i] : 0.f;
+      for (int o = p.G; o < 32; o <<= 1) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) t[i] += __shfl_xor_sync(0xffffffffu, t[i], o);
+      }
+      if ((static_cast<int>(threadIdx.x) & 31) < p.G) {
+        float* to = red + (static_cast<size_t>(threadIdx.x >> 5) * 2 + what) * d;
+        L.each([&](int i, int c) { to[c] = t[i]; });
+      }
     }
-  }
-  __syncthreads();
-  if ((threadIdx.x & 31) < p.G) {
-    float* mine = smem + static_cast<size_t>(threadIdx.x >> 5) * 2 * p.d;
-    L.each([&](int k, int c) {
-      mine[c] = sum[0][k];
-      mine[p.d + c] = sum[1][k];
-    });
-  }
-  __syncthreads();
-  for (int c = threadIdx.x; c < 2 * p.d; c += kRoThreads) {
-    float t = 0.f;
-#pragma unroll
-    for (int w = 0; w < kRoWarps; ++w) t += smem[static_cast<size_t>(w) * 2 * p.d + c];
-    p.partial[static_cast<size_t>(blockIdx.x) * 2 * p.d + c] = t;
+    __syncthreads();
+    const int warps = blockDim.x >> 5;
+    for (int c = threadIdx.x; c < 2 * d; c += blockDim.x) {
+      float t = 0.f;
+      for (int w = 0; w < warps; ++w) t += red[static_cast<size_t>(w) * 2 * d + c];
+      p.partial[static_cast<size_t>(blockIdx.x) * 2 * d + c] = t;
+    }
   }
 }
 
-// The blocks' sums in their order: 32 columns a block, 32 rows at a time.
-__global__ void __launch_bounds__(1024) qk_gain_sum_kernel(const float* __restrict__ partial, int parts, int d,
-                                                           float* dgq, float* dgk, int accumulate) {
+// The blocks' sums: eight columns a block, 32 rows at a time in their order,
+// then a tree.
+constexpr int kGainColumns = 8;
+__global__ void __launch_bounds__(32 * kGainColumns) qk_gain_sum_kernel(const float* __restrict__ partial, int parts,
+                                                                       int d, float* dgq, float* dgk,
+                                                                       int accumulate) {
+  __shared__ float red[kGainColumns][33];
+  const int c = threadIdx.x % kGainColumns, r = threadIdx.x / kGainColumns;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int col = blockIdx.x * kGainColumns + warp;
+  float* to = col < d ? dgq : dgk;
   pdl_wait();
   pdl_trigger();
-  __shared__ float red[32][33];
-  const int c = blockIdx.x * 32 + threadIdx.x % 32, r = threadIdx.x / 32;
+  const float* from = partial + blockIdx.x * kGainColumns + c;
   float t = 0.f;
-  if (c < 2 * d)
-    for (int i = r; i < parts; i += 32) t += __ldcg(partial + static_cast<size_t>(i) * 2 * d + c);
-  red[r][threadIdx.x % 32] = t;
+  for (int i = r; i < parts; i += 32 * 8) {
+    float v[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] = i + 32 * k < parts ? __ldcg(from + static_cast<size_t>(i + 32 * k) * 2 * d) : 0.f;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) t += v[k];
+  }
+  red[c][r] = t;
   __syncthreads();
-  if (r != 0 || c >= 2 * d) return;
-  for (int i = 1; i < 32; ++i) t += red[i][threadIdx.x];
-  float* to = c < d ? dgq : dgk;
-  if (to == nullptr) return;
-  to += c < d ? c : c - d;
+  t = red[warp][lane];
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+  if (lane != 0 || to == nullptr) return;
+  to += col < d ? col : col - d;
   *to = accumulate ? *to + t : t;
 }
 
@@ -614,37 +893,87 @@ struct RoCall {
   cudaStream_t stream;
 };
 
+// Warps of a block, chunks of heads and rows at the same time: as few idle
+// groups as possible, then as few chunks (each computes its own table), then the largest block.
+void lay_out(RoParams* p, int max_parts, int* threads) {
+  const int unit = 32 / p->G, units = (p->items + unit - 1) / unit;
+  double best = 0.0;
+  for (int warps = kRoWarps; warps >= 4; --warps) {
+    const int groups = warps * unit, room = warps * 32 > kRoFew ? kRoWarps : kRoFew / 32;  // warps that the block's stages are made for
+    for (int chunks = (units + warps - 1) / warps, tries = 0; tries < 3; ++chunks, ++tries) {
+      const int heads = chunks == 1 ? p->items : (units + chunks - 1) / chunks * unit;
+      const int parts = std::min(groups / heads, max_parts);
+      const double busy = static_cast<double>(p->items) * parts / (static_cast<double>(room) * unit * chunks);
+      const double worth = busy * (1.0 - 0.01 * (chunks - 1)) * (warps * 32 > kRoFew ? 1.0 : 0.98);
+      if (worth > best + 1e-9) {
+        best = worth;
+        p->chunks = chunks;
+        p->chunk_heads = heads;
+        p->parts = parts;
+        *threads = warps * 32;
+      }
+    }
+  }
+}
+
+template <class E, int V, bool INTER, int MODE, int NT>
+cudaError_t launch_block(const RoCall& c, RoParams& p, int threads, int max_rows) {
+  constexpr int D = kDepth<E, MODE>;
+  constexpr auto kernel = rotary_kernel<E, V, INTER, MODE, NT>;
+  p.steps = std::max(1, std::min(8, max_rows / p.parts) / D) * D;
+  p.fill_rows = p.width ? std::max(1, threads / p.width) : 1;
+  const int64_t rows = (p.T + p.parts - 1) / p.parts;  // steps of all blocks of a chunk
+  // the backward: one wave, every block leaves a row of sums; else waves of blocks of 8 steps, so that the next
+  // kernel's blocks find room while the last ones end
+  int64_t blocks;
+  if (MODE == RO_NORM_BWD) blocks = std::min(kRoParts, kBlocks<MODE, NT> * c.num_sms) / p.chunks;
+  else blocks = std::max<int64_t>(2 * kBlocks<MODE, NT> * c.num_sms / p.chunks, rows / 8);
+  blocks = std::max<int64_t>(blocks, 1);
+  blocks = std::min(blocks, rows);
+  p.apart = static_cast<uint32_t>(blocks * p.parts);
+  const int64_t grid = blocks * p.chunks;
+  size_t smem = (kStageX<E, NT> + (MODE == RO_NORM_BWD ? kStageY<E, NT> : 0)) * D + ((p.width + 1) & ~1) * 8 +
+                static_cast<size_t>(2) * p.steps * p.parts * p.row_floats * 4;
+  if (MODE == RO_NORM_BWD && p.partial) smem = std::max(smem, static_cast<size_t>(threads / 32) * 8 * p.d);
+  static std::once_flag once[64];
+  int dev = 0;
+  cudaGetDevice(&dev);
+  std::call_once(once[dev & 63], [] {
+    cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 200 * 1024);
+  });
+  count_launches(1);
+  cudaError_t e = launch_k(kernel, static_cast<unsigned>(grid), threads, smem, c.stream, p);
+  if (e != cudaSuccess || MODE != RO_NORM_BWD || p.partial == nullptr) return e;
+  count_launches(1);
+  return launch_k(qk_gain_sum_kernel, 2 * p.d / kGainColumns, 32 * kGainColumns, 0, c.stream, static_cast<const float*>(p.partial),
+                  static_cast<int>(grid), p.d, c.dgq, c.dgk, c.accumulate);
+}
+
+template <class E, int V, bool INTER, int MODE>
+cudaError_t launch_mode(const RoCall& c) {
+  RoParams p = c.p;
+  int threads = kRoThreads;
+  p.row_floats = p.rot_slots * kSlot<V, INTER>;
+  const int max_rows = p.width ? std::max(1, std::min(kRoRows, kRoTable / (4 * p.row_floats))) : kRoRows;
+  lay_out(&p, std::max(1, max_rows / kDepth<E, MODE>), &threads);
+  return threads <= kRoFew ? launch_block<E, V, INTER, MODE, kRoFew>(c, p, threads, max_rows)
+                           : launch_block<E, V, INTER, MODE, kRoThreads>(c, p, threads, max_rows);
+}
+
 template <class E, int V, bool INTER>
 cudaError_t launch_as(const RoCall& c) {
-  RoParams p = c.p;
-  const size_t row_bytes = static_cast<size_t>(2) * p.width * 4;
-  if (c.mode != RO_NORM_BWD) {
-    p.rows = static_cast<int>(std::min<int64_t>(kRoRows, std::max<int64_t>(1, p.T / (8 * c.num_sms))));
-    const unsigned grid = static_cast<unsigned>((p.T + p.rows - 1) / p.rows);
-    const size_t smem = p.rows * row_bytes + (c.mode == RO_NORM_FWD ? 8 * p.d : 0);
-    count_launches(1);
-    return c.mode == RO_NORM_FWD ? launch_k(rotary_kernel<E, V, INTER, true>, grid, kRoThreads, smem, c.stream, p)
-                                 : launch_k(rotary_kernel<E, V, INTER, false>, grid, kRoThreads, smem, c.stream, p);
-  }
-  p.rows = static_cast<int>(std::min<int64_t>(4, std::max<int64_t>(1, p.T / (8 * c.num_sms))));
-  const unsigned grid = static_cast<unsigned>(
-      std::min<int64_t>((p.T + p.rows - 1) / p.rows, std::min(kRoParts, 4 * c.num_sms)));
-  const size_t smem = std::max(8 * static_cast<size_t>(p.d) + p.rows * row_bytes,
-                               p.partial ? static_cast<size_t>(kRoWarps) * 8 * p.d : 0);
-  count_launches(1);
-  cudaError_t e = launch_k(qk_norm_bwd_kernel<E, V, INTER>, grid, kRoThreads, smem, c.stream, p);
-  if (e != cudaSuccess || p.partial == nullptr) return e;
-  count_launches(1);
-  return launch_k(qk_gain_sum_kernel, (2 * p.d + 31) / 32, 1024, 0, c.stream, static_cast<const float*>(p.partial),
-                  static_cast<int>(grid), p.d, c.dgq, c.dgk, c.accumulate);
+  if (c.mode == RO_ROTATE) return launch_mode<E, V, INTER, RO_ROTATE>(c);
+  if (c.mode == RO_NORM_FWD) return launch_mode<E, V, INTER, RO_NORM_FWD>(c);
+  return launch_mode<E, V, INTER, RO_NORM_BWD>(c);
 }
 
 template <class E>
 cudaError_t launch_typed(const RoCall& c) {
-  if (c.inter) return launch_as<E, 8, true>(c);
-  if (c.vec == 8) return launch_as<E, 8, false>(c);
-  if (c.vec == 4) return launch_as<E, 4, false>(c);
-  return launch_as<E, 1, false>(c);
+  constexpr int kWide = 16 / sizeof(E);
+  if (c.inter) return launch_as<E, kWide, true>(c);
+  if (c.vec == 1) return launch_as<E, 1, false>(c);
+  if (c.vec == kWide) return launch_as<E, kWide, false>(c);
+  return launch_as<E, 4, false>(c);
 }
 
 cudaError_t launch_call(void* call) {
@@ -665,13 +994,13 @@ uint64_t turn_fraction(double freq) {
 
 // Sizes and the rotation into c, without pointers.
 tp_status ro_sizes(const tp_attn_config* cfg, const tp_rotary_config* rot, bool norm, const int64_t* seq_starts,
-                   const int64_t* positions, RoCall* c) {
+                   const int64_t* positions, bool f32, RoCall* c) {
   if (cfg == nullptr || (rot == nullptr && !norm)) return TP_ERR_INVALID;
   if (cfg->T < 0 || cfg->T > INT32_MAX - 511 || cfg->n_heads < 1 || cfg->n_kv_heads < 1 || cfg->N < 1 || cfg->N > 8 ||
       cfg->n_heads % cfg->N != 0 || cfg->n_kv_heads % cfg->N != 0 || cfg->n_heads % cfg->n_kv_heads != 0 ||
       cfg->d < 1 || cfg->d > kRoMaxD)
     return TP_ERR_INVALID;
-  if ((static_cast<int64_t>(cfg->n_heads) + 2 * static_cast<int64_t>(cfg->n_kv_heads)) * cfg->d > INT32_MAX / kRoRows)
+  if ((static_cast<int64_t>(cfg->n_heads) + 2 * static_cast<int64_t>(cfg->n_kv_heads)) * cfg->d > INT32_MAX / 8)
     return TP_ERR_INVALID;
   if (cfg->T > 0) {
     if (seq_starts != nullptr) {
@@ -701,17 +1030,25 @@ tp_status ro_sizes(const tp_attn_config* cfg, const tp_rotary_config* rot, bool 
   p.hs = p.hq + 2 * p.hk;
   p.pairs = n_rot / 2;
   p.amp = n_rot > 0 && rot->amplitude > 0.f ? rot->amplitude : 1.f;
+  p.amp_sin = p.amp;
   c->inter = n_rot > 0 && rot->interleaved != 0;
-  // Partners in the half layout lie n_rot / 2 apart: the widest vectors that
-  // keep both ends of a pair aligned.
-  c->vec = c->inter || p.pairs % 8 == 0 ? 8 : p.pairs % 4 == 0 ? 4 : 1;
+  // Vectors of 16 bytes.  Partners in the half layout lie n_rot / 2 apart: the
+  // widest that keep both ends of a pair aligned.
+  const int widest = f32 ? 4 : 8;
+  c->vec = c->inter || p.pairs % widest == 0 ? widest : p.pairs % 4 == 0 ? 4 : 1;
   const int v = c->vec;
-  p.rot_slots = (p.pairs + v - 1) / v;
-  p.slots = c->inter ? (p.d + 15) / 16 : p.rot_slots + ((p.d - n_rot) / v + 1) / 2;
-  p.width = p.rot_slots * v;
-  const int lanes = (p.slots + 8 / v - 1) / (8 / v);
+  int lanes;
+  if (c->inter) {
+    lanes = p.slots = (p.d + 15) / 16;
+    p.rot_slots = std::min(p.slots, (2 * p.pairs + v - 1) / v);
+  } else {
+    p.rot_slots = p.pairs / v;
+    p.slots = p.rot_slots + ((p.d - n_rot) / v + 1) / 2;
+    lanes = (p.slots + 8 / v - 1) / (8 / v);
+  }
+  p.width = p.pairs;
   p.G = 1;
-  while (p.G < lanes) p.G <<= 1;
+  while (p.G < lanes) p.G <<= 1, ++p.log_g;
   return TP_OK;
 }
 
@@ -722,7 +1059,7 @@ tp_status ro_args(tp_dtype dt, RoMode mode, const tp_attn_config* cfg, const tp_
   if (dt != TP_F32 && dt != TP_BF16) return TP_ERR_UNSUPPORTED;
   const bool with_norm = mode != RO_ROTATE;
   if (with_norm && norm == nullptr) return TP_ERR_INVALID;
-  tp_status st = ro_sizes(cfg, rot, with_norm, seq_starts, positions, c);
+  tp_status st = ro_sizes(cfg, rot, with_norm, seq_starts, positions, dt == TP_F32, c);
   if (st == TP_ERR_INVALID) return st;
   if (with_norm && ((norm->kind != TP_NORM_RMS && norm->kind != TP_NORM_LAYER) || !(norm->eps > 0.f) ||
                     !isfinite(norm->eps)))
@@ -749,8 +1086,8 @@ tp_status ro_args(tp_dtype dt, RoMode mode, const tp_attn_config* cfg, const tp_
   p.ld_out = ld_out;
   p.starts = seq_starts;
   p.positions = positions;
-  p.per = out == src ? p.hq + p.hk : p.hs;
-  p.items = p.per * cfg->N;
+  p.items = (p.hq + p.hk) * cfg->N;
+  p.copied = out == src ? 0 : p.hk * cfg->N * p.d;
   p.centred = with_norm && norm->kind == TP_NORM_LAYER;
   p.eps = with_norm ? norm->eps : 0.f;
   c->mode = mode;
@@ -829,7 +1166,7 @@ extern "C" tp_status tp_rotary_bwd(tp_dtype dt, const tp_attn_config* cfg, const
   const tp_status st = ro_args(dt, RO_ROTATE, cfg, rot, nullptr, seq_starts, positions, dOut, ld_dout, nullptr, 0,
                                dQKV, ld_dqkv, &c);
   if (st != TP_OK || cfg->T == 0) return st;
-  c.p.back = 1;
+  c.p.amp_sin = -c.p.amp;
   return ro_run("rotary_bwd", &c, stream);
 }
 
@@ -879,7 +1216,7 @@ extern "C" tp_status tp_qk_norm_rotary_bwd(tp_dtype dt, const tp_attn_config* cf
   }
   c.p.gq = gq;
   c.p.gk = gk;
-  c.p.back = 1;
+  c.p.amp_sin = -c.p.amp;
   c.dgq = dgq;
   c.dgk = dgk;
   c.accumulate = accumulate;
