@@ -431,7 +431,7 @@ TP_API tp_status tp_rotary_frequencies(const tp_rotary_scaling* scaling, double*
  * and backward, with dy for x, the transposed matrix (the same with -sin a).
  * Columns from n_rot on, and the value heads, are copied.
  * Arguments (TP_BF16 or TP_F32; sizes T, b, s, n_heads, n_kv_heads, d, N of cfg, its
- * causal and scale unused; here 8 <= d <= 512):
+ * causal and scale unused; here 8 <= d <= 512 and n_heads + n_kv_heads <= 4096):
  *   QKV, Out, dOut, dQKV  (T, (n_heads + 2 n_kv_heads) d), shard-major as in
  *               tp_attn_recompute_fwd, pitches ld_*.  The output may be the input's
  *               buffer (same pitch): the value heads are then not touched.

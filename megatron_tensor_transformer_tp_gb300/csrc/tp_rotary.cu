@@ -28,6 +28,7 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <math.h>
+#include <stddef.h>
 #include <stdint.h>
 #include <string.h>
 
@@ -41,13 +42,15 @@
 namespace tp {
 namespace {
 
-constexpr int kRoThreads = 256;
-constexpr int kRoWarps = kRoThreads / 32;
-constexpr int kRoRows = 64;      // most rows of a tile
-constexpr int kRoTable = 16384;  // most bytes of its table
-constexpr int kRoMaxD = 512;     // head width
+constexpr int kRoMaxD = 512;       // head width
 constexpr int kRoPairs = kRoMaxD / 2;
-constexpr int kRoParts = 1024;   // most blocks of the backward with gains
+constexpr int kRoMaxHeads = 4096;  // query and key heads
+constexpr int kRoThreads = 256;    // of a block
+constexpr int kRoFew = 160;        // of a smaller one
+constexpr int kRoRows = 64;        // most rows of a tile
+constexpr int kRoTable = 16384;    // bytes that its table should not exceed
+constexpr int kRoParts = 1024;     // most blocks of the backward with gains
+constexpr int64_t kRoCached = 112 << 20;  // bytes of a call that the L2 (129 MB) holds for the next one
 
 enum RoMode : int { RO_ROTATE = 0, RO_NORM_FWD = 1, RO_NORM_BWD = 2 };
 
@@ -61,6 +64,8 @@ struct RoParams {
   const float* gq;
   const float* gk;           // gains, or null: one
   float* partial;            // (blocks, 2, d) sums of the gains' gradients, or null
+  float *dgq, *dgk;          // the gains' gradients
+  int accumulate;
   int64_t T;
   int b, s;        // s: tokens of every sequence (no starts, no positions)
   int d, hq, hk;   // head width; query and key heads a shard
@@ -71,8 +76,7 @@ struct RoParams {
   int G, log_g;    // lanes a head
   int slots;       // half layout: slots a head; interleaved: lanes a head that have values
   int rot_slots;   // those with rotated pairs
-  int width;       // pairs of a row of the table
-  int row_floats;  // floats of a row
+  int row_floats;  // floats of a row of the table
   int fill_rows;   // rows that a block's threads fill at the same time
   int chunks;      // parts that the heads are cut into, a block takes one
   int chunk_heads; // heads of a chunk
@@ -293,7 +297,7 @@ __device__ __forceinline__ float half_turns(int64_t position, uint64_t turn) {
 template <int V, bool INTER>
 __device__ __forceinline__ void fill_table(const RoParams& p, int n, const int64_t* pos, const uint64_t* turn, int r0,
                                            int k0, float* tab) {
-  for (int k = k0; k < p.width; k += blockDim.x) {
+  for (int k = k0; k < p.pairs; k += blockDim.x) {
     const uint64_t t = turn[k];
     float* to = tab + place<V, INTER>(p, k);
     for (int r = r0; r < n; r += p.fill_rows) {
@@ -587,21 +591,21 @@ __device__ __forceinline__ int block_head(const RoParams& p, int chunk, int slot
   return p.chunks == 1 ? slot : (((slot >> log_unit) * p.chunks + chunk) << log_unit) + in_unit;
 }
 
-// Rows on their way to a group.
+// Rows on their way to a group, the one that is worked on among them.  (The backward, 65536 rows of 8 + 2 heads: 92 us;
+// with 4, 123: one block less an SM.)
 template <class E, int MODE>
 constexpr int kDepth = sizeof(E) == 4 ? 2 : MODE == RO_NORM_BWD ? 3 : 4;
-// A stage: the groups' heads and, behind those of x, the values that are copied.  Constants for
-// blocks of up to NT threads: with a size known at the launch the addresses took registers that the kernels lack
-// (norm's forward 39 us instead of 33).
+// A stage: the groups' heads and, behind those of x, the values that are copied (of dy in the backward).  Constants for
+// blocks of up to NT threads: with a size known at the launch, addresses took registers that the kernels lack (two
+// sequences of 2048, 32 heads of 128, norm's forward: 39 us, 33 so).
 template <class E, int NT>
 constexpr uint32_t kStageY = NT * 16 * sizeof(E);
 template <class E, int NT>
 constexpr uint32_t kStageX = kStageY<E, NT> + NT * 8 * sizeof(E);
-
-// Blocks on an SM at the same time, by their registers: the backward holds 64 values a lane.
-constexpr int kRoFew = 160;  // threads of the smaller blocks
+// Blocks on an SM, by their registers: the backward holds 64 values a lane.  (Forward, 4 of the smaller blocks with 96
+// registers: 12000 rows of 16 + 4 heads of 96 26 us; 5 with 72: 30.)
 template <int MODE, int NT>
-constexpr int kBlocks = MODE == RO_NORM_BWD ? (NT == kRoFew ? 3 : 2) : (NT == kRoFew ? 5 : 3);
+constexpr int kBlocks = MODE == RO_NORM_BWD ? (NT == kRoFew ? 3 : 2) : (NT == kRoFew ? 4 : 3);
 
 template <class E, int V, bool INTER, int MODE, int NT>
 __global__ void __launch_bounds__(NT, kBlocks<MODE, NT>)
@@ -614,7 +618,7 @@ __global__ void __launch_bounds__(NT, kBlocks<MODE, NT>)
   constexpr uint32_t stage = kStageX<E, NT>, stage_y = kStageY<E, NT>;
   constexpr uint32_t ys = D * stage;  // the stages of dy lie behind those of x
   uint64_t* turn = reinterpret_cast<uint64_t*>(smem + ys + (kBwd ? D * stage_y : 0));
-  float* tab = reinterpret_cast<float*>(turn + ((p.width + 1) & ~1));
+  float* tab = reinterpret_cast<float*>(turn + ((p.pairs + 1) & ~1));
   // the group's head: the chunks take turns by runs of a warp's heads
   const int group = threadIdx.x >> p.log_g;
   const LaneT L(p, threadIdx.x & 31, group * p.G * 16 * sizeof(E));
@@ -631,10 +635,14 @@ __global__ void __launch_bounds__(NT, kBlocks<MODE, NT>)
   // the block's rows: p.parts at a time, p.apart apart
   const uint32_t base = block * p.parts, T = static_cast<uint32_t>(p.T);
   const int total = (T - base + p.apart - 1) / p.apart;  // steps
-  const int fill_r = threadIdx.x / max(p.width, 1), fill_k = p.width > blockDim.x ? threadIdx.x : threadIdx.x - fill_r * p.width;
-  const int r0 = p.width > blockDim.x ? 0 : fill_r < p.fill_rows ? fill_r : INT32_MAX;
+  // the thread's first row and pair of a table: whole rows of pairs side by side, or, of more pairs than threads, parts
+  // of one
+  const bool wide = p.pairs > static_cast<int>(blockDim.x);
+  const int fill_r = wide ? 0 : threadIdx.x / max(p.pairs, 1);
+  const int fill_k = wide ? threadIdx.x : threadIdx.x - fill_r * p.pairs;
+  const int r0 = fill_r < p.fill_rows ? fill_r : INT32_MAX;
 
-  for (int i = threadIdx.x; i < p.width; i += blockDim.x) turn[i] = i < p.pairs ? p.turn[i] : 0;
+  for (int i = threadIdx.x; i < p.pairs; i += blockDim.x) turn[i] = p.turn[i];
 #pragma unroll
   for (int i = 0; i < D; ++i) {
     L.clear(smem + i * stage);
@@ -706,90 +714,82 @@ __global__ void __launch_bounds__(NT, kBlocks<MODE, NT>)
     if (V == 1) __syncwarp();
     uint8_t* sx = smem + from * stage;
     uint8_t* sy = smem + ys + from * stage_y;
-    uint32_t wx[LaneT::kWords];
-    if (!kBwd) L.read(sx, wx);
-      if (!kBwd) {
-        float f[16];
-        L.floats(wx, f);
-        if (MODE == RO_NORM_FWD) {
-          if (p.centred) {
-            float m = 0.f;
-#pragma unroll
-            for (int i = 0; i < 16; ++i) m += f[i];
-            group_sums<1>(&m, p.G);
-            m *= -inv_d;
-            L.each([&](int i, int) { f[i] += m; });
-          }
-          float q = dot16(f, f);
-          group_sums<1>(&q, p.G);
-          const float inv = rsqrtf(fmaf(q, inv_d, p.eps)), both[2] = {inv, inv};
-#pragma unroll
-          for (int i = 0; i < 16; i += 4) {
-            for (int j = 0; j < 4; j += 2) {
-            mul2(f + i + j, f + i + j, both);
-            mul2(f + i + j, f + i + j, g + i + j); }
-          }
-        }
-        if (mine) {
-          L.turn(p, angles, f);
-          L.words(f, wx);
-        }
-        L.store(p, sx, to, mine, wx);
-      } else {
-        uint32_t wy[LaneT::kWords];
-        float f[16], e[16];
-        L.read(sy, wy);
-        L.floats(wy, e);
-        if (mine) L.turn(p, angles, e);
-        L.read(sx, wx);
-        L.floats(wx, f);
-        float mean = 0.f;
+    uint32_t w[LaneT::kWords];
+    float f[16];
+    if (!kBwd) {
+      L.read(sx, w);
+      L.floats(w, f);
+      if (MODE == RO_NORM_FWD) {
         if (p.centred) {
-          float m[2] = {0.f, 0.f};
+          float m = 0.f;
 #pragma unroll
-          for (int i = 0; i < 16; i += 4) {
-            for (int j = 0; j < 4; ++j) {
-            m[0] += f[i + j];
-            m[1] = fmaf(e[i + j], g[i + j], m[1]); }
-          }
-          group_sums<2>(m, p.G);
-          const float less = m[0] * -inv_d;
-          L.each([&](int i, int) { f[i] += less; });
-          mean = m[1] * inv_d;
+          for (int i = 0; i < 16; ++i) m += f[i];
+          group_sums<1>(&m, p.G);
+          m *= -inv_d;
+          L.each([&](int i, int) { f[i] += m; });
         }
-        // q = |x|^2 and the sum of e g x
-        float q[2];
-        q[0] = dot16(f, f);
-        float along[2] = {0.f, 0.f};
+        float q = dot16(f, f);
+        group_sums<1>(&q, p.G);
+        const float inv = rsqrtf(fmaf(q, inv_d, p.eps)), invs[2] = {inv, inv};
 #pragma unroll
-        for (int i = 0; i < 16; i += 4) {
-          for (int j = 0; j < 4; j += 2) {
-          float t[2];
-          mul2(t, e + i + j, f + i + j);
-          fma2(along, t, g + i + j, along); }
+        for (int i = 0; i < 16; i += 2) {
+          mul2(f + i, f + i, invs);
+          mul2(f + i, f + i, g + i);
         }
-        q[1] = along[0] + along[1];
-        group_sums<2>(q, p.G);
-        const float inv = rsqrtf(fmaf(q[0], inv_d, p.eps));
-        // dx = inv e g - x inv (inv (inv q1 / d)): in this order nothing is larger than the result's parts
-        const float k = -inv * (inv * (inv * (q[1] * inv_d)));
-        const float invs[2] = {inv, inv}, ks[2] = {k, k};
-        if (mine) {
-          const float shift[2] = {-inv * mean, -inv * mean};
-#pragma unroll
-          for (int i = 0; i < 16; i += 4) {
-            for (int j = 0; j < 4; j += 2) {
-            float t[2];
-            mul2(e + i + j, e + i + j, invs);
-            fma2(sum + i + j, e + i + j, f + i + j, sum + i + j);
-            if (p.centred) fma2(t, f + i + j, ks, shift);
-            else mul2(t, f + i + j, ks);
-            fma2(e + i + j, e + i + j, g + i + j, t); }
-          }
-          L.words(e, wy);
-        }
-        L.store(p, sy, to, mine, wy);
       }
+      if (mine) {
+        L.turn(p, angles, f);
+        L.words(f, w);
+      }
+      L.store(p, sx, to, mine, w);
+    } else {
+      float e[16];
+      L.read(sy, w);
+      L.floats(w, e);
+      if (mine) L.turn(p, angles, e);
+      L.read(sx, w);
+      L.floats(w, f);
+      float mean = 0.f;
+      if (p.centred) {
+        float m[2] = {0.f, 0.f};  // sums of x and of e g
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          m[0] += f[i];
+          m[1] = fmaf(e[i], g[i], m[1]);
+        }
+        group_sums<2>(m, p.G);
+        const float less = m[0] * -inv_d;
+        L.each([&](int i, int) { f[i] += less; });
+        mean = m[1] * inv_d;
+      }
+      float q[2], along[2] = {0.f, 0.f};  // sums of x^2 and of e g x
+      q[0] = dot16(f, f);
+#pragma unroll
+      for (int i = 0; i < 16; i += 2) {
+        float t[2];
+        mul2(t, e + i, f + i);
+        fma2(along, t, g + i, along);
+      }
+      q[1] = along[0] + along[1];
+      group_sums<2>(q, p.G);
+      const float inv = rsqrtf(fmaf(q[0], inv_d, p.eps));
+      // dx = inv e g - x inv (inv (inv q1 / d)): in this order nothing is larger than the result's parts
+      const float k = -inv * (inv * (inv * (q[1] * inv_d)));
+      if (mine) {
+        const float invs[2] = {inv, inv}, ks[2] = {k, k}, shift[2] = {-inv * mean, -inv * mean};
+#pragma unroll
+        for (int i = 0; i < 16; i += 2) {
+          float t[2];
+          mul2(e + i, e + i, invs);
+          fma2(sum + i, e + i, f + i, sum + i);
+          if (p.centred) fma2(t, f + i, ks, shift);
+          else mul2(t, f + i, ks);
+          fma2(e + i, e + i, g + i, t);
+        }
+        L.words(e, w);
+      }
+      L.store(p, sy, to, mine, w);
+    }
     if (mine && copies) {
 #pragma unroll
       for (uint32_t k = 0; k < 8 * sizeof(E); k += 16)
@@ -804,7 +804,7 @@ __global__ void __launch_bounds__(NT, kBlocks<MODE, NT>)
     __syncthreads();  // this tile's table and the next one's positions are there; the last tile's are read
     if (left > p.steps)
       fill_table<V, INTER>(p, min(p.steps, left - p.steps) * p.parts, pos[even ^ 1], turn, r0, fill_k,
-                    tab + (even ^ 1) * tab_floats);
+                           tab + (even ^ 1) * tab_floats);
     if (left > 2 * p.steps) fill_positions(p, starts, ahead, min(p.steps, left - 2 * p.steps), pos[even]);
     const float* angles = tab + even * tab_floats + part * p.row_floats;
     const int n = min(p.steps, left);
@@ -885,100 +885,129 @@ __global__ void __launch_bounds__(32 * kGainColumns) qk_gain_sum_kernel(const fl
 // Launches
 // ---------------------------------------------------------------------------
 struct RoCall {
-  RoParams p;
   RoMode mode;
   bool f32, inter;
-  int vec, num_sms, accumulate;
-  float *dgq, *dgk;
+  int vec, num_sms;
   cudaStream_t stream;
+  RoParams p;  // last, its frequencies at its end: those are not cleared
 };
 
-// Warps of a block, chunks of heads and rows at the same time: as few idle
-// groups as possible, then as few chunks (each computes its own table), then the largest block.
-void lay_out(RoParams* p, int max_parts, int* threads) {
+// Warps of a block, chunks of heads and rows at the same time: as few idle groups as possible (of the threads that the
+// block's stages are made for), and among equals few chunks, as each computes tables of its own.
+int lay_out(RoParams* p, int max_parts) {
   const int unit = 32 / p->G, units = (p->items + unit - 1) / unit;
+  int threads = 0;
   double best = 0.0;
-  for (int warps = kRoWarps; warps >= 4; --warps) {
-    const int groups = warps * unit, room = warps * 32 > kRoFew ? kRoWarps : kRoFew / 32;  // warps that the block's stages are made for
-    for (int chunks = (units + warps - 1) / warps, tries = 0; tries < 3; ++chunks, ++tries) {
+  for (int warps = kRoThreads / 32; warps >= 4; --warps) {
+    const bool few = warps * 32 <= kRoFew;
+    const int groups = warps * unit, room = (few ? kRoFew : kRoThreads) / 32 * unit;
+    for (int chunks = (units + warps - 1) / warps, tries = 0; tries < 3 && chunks <= kRoParts; ++chunks, ++tries) {
       const int heads = chunks == 1 ? p->items : (units + chunks - 1) / chunks * unit;
       const int parts = std::min(groups / heads, max_parts);
-      const double busy = static_cast<double>(p->items) * parts / (static_cast<double>(room) * unit * chunks);
-      const double worth = busy * (1.0 - 0.01 * (chunks - 1)) * (warps * 32 > kRoFew ? 1.0 : 0.98);
+      const double busy = static_cast<double>(p->items) * parts / (static_cast<double>(room) * chunks);
+      const double worth = busy / (1.0 + 0.01 * (chunks - 1)) * (few ? 0.98 : 1.0);
       if (worth > best + 1e-9) {
         best = worth;
         p->chunks = chunks;
         p->chunk_heads = heads;
         p->parts = parts;
-        *threads = warps * 32;
+        threads = warps * 32;
       }
     }
   }
+  return threads;
 }
 
 template <class E, int V, bool INTER, int MODE, int NT>
-cudaError_t launch_block(const RoCall& c, RoParams& p, int threads, int max_rows) {
+cudaError_t launch_block(RoCall& c, int threads, int max_rows) {
   constexpr int D = kDepth<E, MODE>;
-  constexpr auto kernel = rotary_kernel<E, V, INTER, MODE, NT>;
+  constexpr bool kBwd = MODE == RO_NORM_BWD;
+  RoParams& p = c.p;
   p.steps = std::max(1, std::min(8, max_rows / p.parts) / D) * D;
-  p.fill_rows = p.width ? std::max(1, threads / p.width) : 1;
+  p.fill_rows = std::max(1, threads / std::max(1, p.pairs));
   const int64_t rows = (p.T + p.parts - 1) / p.parts;  // steps of all blocks of a chunk
-  // the backward: one wave, every block leaves a row of sums; else waves of blocks of 8 steps, so that the next
-  // kernel's blocks find room while the last ones end
-  int64_t blocks;
-  if (MODE == RO_NORM_BWD) blocks = std::min(kRoParts, kBlocks<MODE, NT> * c.num_sms) / p.chunks;
-  else blocks = std::max<int64_t>(2 * kBlocks<MODE, NT> * c.num_sms / p.chunks, rows / 8);
-  blocks = std::max<int64_t>(blocks, 1);
+  // Waves of blocks.  Where HBM bounds the call, several: the next kernel's blocks find room while the last ones end,
+  // and set-up hides behind the others' copies.  In the L2's reach set-up counts: one.  (us by waves 1 / 2 / 3 / 5:
+  // two sequences of 2048, 32 heads of 128, norm's forward: 35.4 33.9 32.6 34.4; 12000 rows of 16 + 4 heads of 96,
+  // 110 MB: 22.0 23.9 25.8 30.3; 12000 rows of 32 + 8 heads of 128, rotation: 51.3 49.3 48.7 47.6.)  The backward: one,
+  // as every block leaves sums of the gains' gradients (two: 48.7 -> 52.7).
+  const int64_t wave = std::max(1, std::min(kBlocks<MODE, NT> * c.num_sms, kRoParts) / p.chunks);
+  const int64_t bytes = 2 * p.T * (static_cast<int64_t>(p.items) * p.d + p.copied) * static_cast<int64_t>(sizeof(E));
+  int64_t blocks = wave;
+  if (!kBwd && bytes > kRoCached) blocks *= (rows + 8 * wave - 1) / (8 * wave);
   blocks = std::min(blocks, rows);
   p.apart = static_cast<uint32_t>(blocks * p.parts);
-  const int64_t grid = blocks * p.chunks;
-  size_t smem = (kStageX<E, NT> + (MODE == RO_NORM_BWD ? kStageY<E, NT> : 0)) * D + ((p.width + 1) & ~1) * 8 +
+  const unsigned grid = static_cast<unsigned>(blocks * p.chunks);
+  size_t smem = (kStageX<E, NT> + (kBwd ? kStageY<E, NT> : 0)) * D + ((p.pairs + 1) & ~1) * 8 +
                 static_cast<size_t>(2) * p.steps * p.parts * p.row_floats * 4;
-  if (MODE == RO_NORM_BWD && p.partial) smem = std::max(smem, static_cast<size_t>(threads / 32) * 8 * p.d);
-  static std::once_flag once[64];
-  int dev = 0;
-  cudaGetDevice(&dev);
-  std::call_once(once[dev & 63], [] {
-    cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 200 * 1024);
-  });
+  if (kBwd) smem = std::max(smem, static_cast<size_t>(threads / 32) * 8 * p.d);
   count_launches(1);
-  cudaError_t e = launch_k(kernel, static_cast<unsigned>(grid), threads, smem, c.stream, p);
-  if (e != cudaSuccess || MODE != RO_NORM_BWD || p.partial == nullptr) return e;
+  const cudaError_t e = launch_k(rotary_kernel<E, V, INTER, MODE, NT>, grid, threads, smem, c.stream, p);
+  if (e != cudaSuccess || !kBwd || p.partial == nullptr) return e;
   count_launches(1);
-  return launch_k(qk_gain_sum_kernel, 2 * p.d / kGainColumns, 32 * kGainColumns, 0, c.stream, static_cast<const float*>(p.partial),
-                  static_cast<int>(grid), p.d, c.dgq, c.dgk, c.accumulate);
+  return launch_k(qk_gain_sum_kernel, 2 * p.d / kGainColumns, 32 * kGainColumns, 0, c.stream,
+                  static_cast<const float*>(p.partial), static_cast<int>(grid), p.d, p.dgq, p.dgk, p.accumulate);
 }
 
+// The call with its kernel, or (c null) the kernels' shared memory limits of the current device.
 template <class E, int V, bool INTER, int MODE>
-cudaError_t launch_mode(const RoCall& c) {
-  RoParams p = c.p;
-  int threads = kRoThreads;
+cudaError_t launch_mode(RoCall* c) {
+  if (c == nullptr) {
+    constexpr int kMost = 160 * 1024;
+    const cudaError_t e = cudaFuncSetAttribute(rotary_kernel<E, V, INTER, MODE, kRoThreads>,
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
+    return e != cudaSuccess ? e : cudaFuncSetAttribute(rotary_kernel<E, V, INTER, MODE, kRoFew>,
+                                                       cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
+  }
+  RoParams& p = c->p;
   p.row_floats = p.rot_slots * kSlot<V, INTER>;
-  const int max_rows = p.width ? std::max(1, std::min(kRoRows, kRoTable / (4 * p.row_floats))) : kRoRows;
-  lay_out(&p, std::max(1, max_rows / kDepth<E, MODE>), &threads);
-  return threads <= kRoFew ? launch_block<E, V, INTER, MODE, kRoFew>(c, p, threads, max_rows)
-                           : launch_block<E, V, INTER, MODE, kRoThreads>(c, p, threads, max_rows);
+  const int max_rows = p.pairs ? std::max(1, std::min(kRoRows, kRoTable / (4 * p.row_floats))) : kRoRows;
+  const int threads = lay_out(&p, std::max(1, max_rows / kDepth<E, MODE>));
+  return threads <= kRoFew ? launch_block<E, V, INTER, MODE, kRoFew>(*c, threads, max_rows)
+                           : launch_block<E, V, INTER, MODE, kRoThreads>(*c, threads, max_rows);
 }
 
 template <class E, int V, bool INTER>
-cudaError_t launch_as(const RoCall& c) {
-  if (c.mode == RO_ROTATE) return launch_mode<E, V, INTER, RO_ROTATE>(c);
-  if (c.mode == RO_NORM_FWD) return launch_mode<E, V, INTER, RO_NORM_FWD>(c);
+cudaError_t launch_as(RoCall* c) {
+  if (c == nullptr) {
+    cudaError_t e = launch_mode<E, V, INTER, RO_ROTATE>(nullptr);
+    if (e == cudaSuccess) e = launch_mode<E, V, INTER, RO_NORM_FWD>(nullptr);
+    return e != cudaSuccess ? e : launch_mode<E, V, INTER, RO_NORM_BWD>(nullptr);
+  }
+  if (c->mode == RO_ROTATE) return launch_mode<E, V, INTER, RO_ROTATE>(c);
+  if (c->mode == RO_NORM_FWD) return launch_mode<E, V, INTER, RO_NORM_FWD>(c);
   return launch_mode<E, V, INTER, RO_NORM_BWD>(c);
 }
 
-template <class E>
-cudaError_t launch_typed(const RoCall& c) {
-  constexpr int kWide = 16 / sizeof(E);
-  if (c.inter) return launch_as<E, kWide, true>(c);
-  if (c.vec == 1) return launch_as<E, 1, false>(c);
-  if (c.vec == kWide) return launch_as<E, kWide, false>(c);
-  return launch_as<E, 4, false>(c);
+cudaError_t launch_call(void* call) {
+  RoCall* c = static_cast<RoCall*>(call);
+  if (c->f32) {
+    if (c->inter) return launch_as<float, 4, true>(c);
+    return c->vec == 4 ? launch_as<float, 4, false>(c) : launch_as<float, 1, false>(c);
+  }
+  if (c->inter) return launch_as<__nv_bfloat16, 8, true>(c);
+  if (c->vec == 8) return launch_as<__nv_bfloat16, 8, false>(c);
+  return c->vec == 4 ? launch_as<__nv_bfloat16, 4, false>(c) : launch_as<__nv_bfloat16, 1, false>(c);
 }
 
-cudaError_t launch_call(void* call) {
-  const RoCall& c = *static_cast<const RoCall*>(call);
-  return c.f32 ? launch_typed<float>(c) : launch_typed<__nv_bfloat16>(c);
+// Once a device, at the first call with it current.
+cudaError_t set_up() {
+  static std::mutex mu;
+  static bool done[64];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess || dev < 0 || dev >= 64) return e != cudaSuccess ? e : cudaErrorInvalidDevice;
+  std::lock_guard<std::mutex> lk(mu);
+  if (done[dev]) return cudaSuccess;
+  if ((e = launch_as<float, 4, true>(nullptr)) != cudaSuccess || (e = launch_as<float, 4, false>(nullptr)) != cudaSuccess ||
+      (e = launch_as<float, 1, false>(nullptr)) != cudaSuccess ||
+      (e = launch_as<__nv_bfloat16, 8, true>(nullptr)) != cudaSuccess ||
+      (e = launch_as<__nv_bfloat16, 8, false>(nullptr)) != cudaSuccess ||
+      (e = launch_as<__nv_bfloat16, 4, false>(nullptr)) != cudaSuccess ||
+      (e = launch_as<__nv_bfloat16, 1, false>(nullptr)) != cudaSuccess)
+    return e;
+  done[dev] = true;
+  return cudaSuccess;
 }
 
 // ---------------------------------------------------------------------------
@@ -1000,8 +1029,7 @@ tp_status ro_sizes(const tp_attn_config* cfg, const tp_rotary_config* rot, bool 
       cfg->n_heads % cfg->N != 0 || cfg->n_kv_heads % cfg->N != 0 || cfg->n_heads % cfg->n_kv_heads != 0 ||
       cfg->d < 1 || cfg->d > kRoMaxD)
     return TP_ERR_INVALID;
-  if ((static_cast<int64_t>(cfg->n_heads) + 2 * static_cast<int64_t>(cfg->n_kv_heads)) * cfg->d > INT32_MAX / 8)
-    return TP_ERR_INVALID;
+  if (cfg->n_heads > kRoMaxHeads - cfg->n_kv_heads) return TP_ERR_INVALID;
   if (cfg->T > 0) {
     if (seq_starts != nullptr) {
       if (cfg->b < 1 || cfg->b > (1 << 22)) return TP_ERR_INVALID;
@@ -1046,11 +1074,12 @@ tp_status ro_sizes(const tp_attn_config* cfg, const tp_rotary_config* rot, bool 
     p.slots = p.rot_slots + ((p.d - n_rot) / v + 1) / 2;
     lanes = (p.slots + 8 / v - 1) / (8 / v);
   }
-  p.width = p.pairs;
   p.G = 1;
   while (p.G < lanes) p.G <<= 1, ++p.log_g;
   return TP_OK;
 }
+
+void clear(RoCall* c) { memset(static_cast<void*>(c), 0, offsetof(RoCall, p) + offsetof(RoParams, turn)); }
 
 // What every call checks and fills in.
 tp_status ro_args(tp_dtype dt, RoMode mode, const tp_attn_config* cfg, const tp_rotary_config* rot,
@@ -1098,6 +1127,7 @@ tp_status ro_args(tp_dtype dt, RoMode mode, const tp_attn_config* cfg, const tp_
 tp_status ro_run(const char* name, RoCall* c, void* stream) {
   const tp_status st = entry_device(&c->num_sms, &c->p.err);
   if (st != TP_OK) return st;
+  if (set_up() != cudaSuccess) return TP_ERR_CUDA;
   c->stream = static_cast<cudaStream_t>(stream);
   return entry_timed(name, c->stream, launch_call, c) == cudaSuccess ? TP_OK : TP_ERR_CUDA;
 }
@@ -1151,7 +1181,7 @@ extern "C" tp_status tp_rotary_fwd(tp_dtype dt, const tp_attn_config* cfg, const
                                    const int64_t* seq_starts, const int64_t* positions, const void* QKV,
                                    int64_t ld_qkv, void* Out, int64_t ld_out, void* stream) {
   RoCall c;
-  memset(&c, 0, sizeof(c));
+  clear(&c);
   const tp_status st = ro_args(dt, RO_ROTATE, cfg, rot, nullptr, seq_starts, positions, QKV, ld_qkv, nullptr, 0, Out,
                                ld_out, &c);
   if (st != TP_OK || cfg->T == 0) return st;
@@ -1162,7 +1192,7 @@ extern "C" tp_status tp_rotary_bwd(tp_dtype dt, const tp_attn_config* cfg, const
                                    const int64_t* seq_starts, const int64_t* positions, const void* dOut,
                                    int64_t ld_dout, void* dQKV, int64_t ld_dqkv, void* stream) {
   RoCall c;
-  memset(&c, 0, sizeof(c));
+  clear(&c);
   const tp_status st = ro_args(dt, RO_ROTATE, cfg, rot, nullptr, seq_starts, positions, dOut, ld_dout, nullptr, 0,
                                dQKV, ld_dqkv, &c);
   if (st != TP_OK || cfg->T == 0) return st;
@@ -1175,7 +1205,7 @@ extern "C" tp_status tp_qk_norm_rotary_fwd(tp_dtype dt, const tp_attn_config* cf
                                            const int64_t* seq_starts, const int64_t* positions, const void* QKV,
                                            int64_t ld_qkv, void* Out, int64_t ld_out, void* stream) {
   RoCall c;
-  memset(&c, 0, sizeof(c));
+  clear(&c);
   const tp_status st = ro_args(dt, RO_NORM_FWD, cfg, rot, norm, seq_starts, positions, QKV, ld_qkv, nullptr, 0, Out,
                                ld_out, &c);
   if (st != TP_OK || cfg->T == 0) return st;
@@ -1192,7 +1222,7 @@ extern "C" tp_status tp_qk_norm_rotary_bwd(tp_dtype dt, const tp_attn_config* cf
                                            int64_t ld_dqkv, float* dgq, float* dgk, int accumulate, void* workspace,
                                            size_t ws_bytes, void* stream) {
   RoCall c;
-  memset(&c, 0, sizeof(c));
+  clear(&c);
   const tp_status st = ro_args(dt, RO_NORM_BWD, cfg, rot, norm, seq_starts, positions, QKV, ld_qkv, dOut, ld_dout,
                                dQKV, ld_dqkv, &c);
   if (st != TP_OK) return st;
@@ -1217,9 +1247,9 @@ extern "C" tp_status tp_qk_norm_rotary_bwd(tp_dtype dt, const tp_attn_config* cf
   c.p.gq = gq;
   c.p.gk = gk;
   c.p.amp_sin = -c.p.amp;
-  c.dgq = dgq;
-  c.dgk = dgk;
-  c.accumulate = accumulate;
+  c.p.dgq = dgq;
+  c.p.dgk = dgk;
+  c.p.accumulate = accumulate;
   return ro_run("qk_norm_rotary_bwd", &c, stream);
 }
 

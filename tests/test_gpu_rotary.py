@@ -203,6 +203,14 @@ def test_heads(H, KV, N, norm):
 
 
 @pytest.mark.parametrize("norm", NORMS)
+@pytest.mark.parametrize("H,KV,N,d", [(2048, 2048, 8, 8), (4088, 8, 8, 16), (4094, 2, 2, 512), (301, 301, 1, 64),
+                                      (90, 45, 5, 128)])
+def test_many_heads(H, KV, N, d, norm):
+    """More heads than a block takes, up to the most, and numbers that do not fill the last block."""
+    Case([3], H, KV, d, N, norm=norm, seed=19).check()
+
+
+@pytest.mark.parametrize("norm", NORMS)
 @pytest.mark.parametrize("lens,head,tail", [([1], 0, 0), ([1], 3, 2), ([2048], 0, 0), ([700, 1, 333, 64], 0, 40),
                                             ([0, 5, 0, 0, 4, 0], 2, 3), ([1] * 200, 0, 1), ([4000, 97, 5000], 0, 0),
                                             ([0], 4, 4), ([3] * 1500, 0, 7)])

@@ -203,6 +203,7 @@ CALLS = (turn, fwd, bwd)
 @pytest.mark.parametrize("bad", [dict(T=-1), dict(T=2 ** 31), dict(n_heads=0), dict(n_kv_heads=0), dict(n_kv_heads=3),
                                  dict(n_heads=6, n_kv_heads=4), dict(N=0), dict(N=9), dict(N=3), dict(d=0),
                                  dict(d=520), dict(b=0), dict(s=0), dict(s=100), dict(b=3), dict(n_heads=1 << 20, n_kv_heads=1 << 20),
+                                 dict(n_heads=2050, n_kv_heads=2050, d=8), dict(n_heads=2 ** 31 - 2, n_kv_heads=2),
                                  dict(b=1 << 62, s=4)])
 def test_sizes_refused(bad):
     for f in CALLS:
