@@ -585,6 +585,14 @@ __device__ __forceinline__ float dot16(const float* f, const float* g) {
 // ---------------------------------------------------------------------------
 // The kernel
 // ---------------------------------------------------------------------------
+// A sum of the gains' gradients, column c of (2, d).
+__device__ __forceinline__ void add_gain(float* dgq, float* dgk, int d, int c, float t, int accumulate) {
+  float* to = c < d ? dgq : dgk;
+  if (to == nullptr) return;
+  to += c < d ? c : c - d;
+  *to = accumulate ? *to + t : t;
+}
+
 // Head of a group of the chunk.
 __device__ __forceinline__ int block_head(const RoParams& p, int chunk, int slot) {
   const int log_unit = 5 - p.log_g, in_unit = slot & ((1 << log_unit) - 1);
@@ -841,10 +849,11 @@ __global__ void __launch_bounds__(NT, kBlocks<MODE, NT>)
     }
     __syncthreads();
     const int warps = blockDim.x >> 5;
+    float* sums = p.partial + static_cast<size_t>(blockIdx.x) * 2 * d;
     for (int c = threadIdx.x; c < 2 * d; c += blockDim.x) {
       float t = 0.f;
       for (int w = 0; w < warps; ++w) t += red[static_cast<size_t>(w) * 2 * d + c];
-      p.partial[static_cast<size_t>(blockIdx.x) * 2 * d + c] = t;
+      sums[c] = t;
     }
   }
 }
@@ -858,8 +867,6 @@ __global__ void __launch_bounds__(32 * kGainColumns) qk_gain_sum_kernel(const fl
   __shared__ float red[kGainColumns][33];
   const int c = threadIdx.x % kGainColumns, r = threadIdx.x / kGainColumns;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const int col = blockIdx.x * kGainColumns + warp;
-  float* to = col < d ? dgq : dgk;
   pdl_wait();
   pdl_trigger();
   const float* from = partial + blockIdx.x * kGainColumns + c;
@@ -876,9 +883,7 @@ __global__ void __launch_bounds__(32 * kGainColumns) qk_gain_sum_kernel(const fl
   t = red[warp][lane];
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
-  if (lane != 0 || to == nullptr) return;
-  to += col < d ? col : col - d;
-  *to = accumulate ? *to + t : t;
+  if (lane == 0) add_gain(dgq, dgk, d, blockIdx.x * kGainColumns + warp, t, accumulate);
 }
 
 // ---------------------------------------------------------------------------
