@@ -610,10 +610,11 @@ template <class E, int NT>
 constexpr uint32_t kStageY = NT * 16 * sizeof(E);
 template <class E, int NT>
 constexpr uint32_t kStageX = kStageY<E, NT> + NT * 8 * sizeof(E);
-// Blocks on an SM, by their registers: the backward holds 64 values a lane.  (Forward, 4 of the smaller blocks with 96
-// registers: 12000 rows of 16 + 4 heads of 96 26 us; 5 with 72: 30.)
+// Blocks on an SM, by their registers: 128 a thread, or 96 for the smaller blocks' forward.  More blocks with fewer
+// registers were slower (norm's forward, 3 blocks of 256 threads: two sequences of 2048, 32 heads of 128, interleaved,
+// 38 us instead of 32; 5 blocks of 160: 12000 rows of 16 + 4 heads of 96 30 instead of 26).
 template <int MODE, int NT>
-constexpr int kBlocks = MODE == RO_NORM_BWD ? (NT == kRoFew ? 3 : 2) : (NT == kRoFew ? 4 : 3);
+constexpr int kBlocks = NT != kRoFew ? 2 : MODE == RO_NORM_BWD ? 3 : 4;
 
 template <class E, int V, bool INTER, int MODE, int NT>
 __global__ void __launch_bounds__(NT, kBlocks<MODE, NT>)
