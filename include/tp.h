@@ -441,8 +441,9 @@ TP_API tp_status tp_rotary_frequencies(const tp_rotary_scaling* scaling, double*
  *               every sequence are not written; or NULL: every row is used, and
  *               without positions the sequences are b of s rows each (with
  *               positions b and s are unused)
- * Angles are exact to 2^-32 of a turn plus position * 2^-64 turns beside freq's own
- * rounding; cosines and sines are fp32; results are rounded once to the dtype.
+ * freq / 2 pi is kept to 2^-53 of itself; times the position it loses its whole turns
+ * exactly, is cut to 2^-32 of a turn, and its cosine and sine are good to 2^-23.
+ * Results are rounded once to the dtype.
  * Deterministic, no workspace.
  * Errors, before anything is launched: TP_ERR_INVALID for sizes outside the
  * ranges above, pitches narrower than a row, null pointers, frequencies or an

@@ -705,13 +705,14 @@ def _rotary_cfg(rot: Optional[dict]) -> Optional[bytes]:
     """The tp_rotary_config of rot, packed."""
     if rot is None:
         return None
-    n, freq = rot["n_rot"], rot["freq"]
-    if n and not (isinstance(freq, torch.Tensor) and freq.dtype is torch.float64 and freq.shape == (n // 2,)
-                  and not freq.is_cuda and freq.is_contiguous()):
-        raise ValueError(f"rot: freq must be a contiguous float64 CPU tensor of n_rot / 2 = {n // 2} values")
+    n, freq, at = rot["n_rot"], rot["freq"], 0
+    if n:
+        if not (isinstance(freq, torch.Tensor) and freq.dtype is torch.float64 and freq.numel() == n // 2
+                and not freq.is_cuda and freq.is_contiguous()):
+            raise ValueError(f"rot: freq must be a contiguous float64 CPU tensor of n_rot / 2 = {n // 2} values")
+        at = freq.data_ptr()
     try:
-        return _ROTARY_CONFIG.pack(n, 1 if rot.get("interleaved") else 0, freq.data_ptr() if n else 0,
-                                   rot.get("amplitude") or 0.0)
+        return _ROTARY_CONFIG.pack(n, 1 if rot.get("interleaved") else 0, at, rot.get("amplitude") or 0.0)
     except (struct.error, OverflowError) as e:
         raise ValueError(f"rot: {e}") from None
 
@@ -730,14 +731,26 @@ def _rotary_common(X, name, Y, yname, cfg, rot, seq_starts, positions):
     """The arguments that every call of this family begins with, checked against the sizes."""
     if not isinstance(X, torch.Tensor) or X.dim() != 2:
         raise ValueError(f"{name} must be a 2D tensor")
-    T, dtype = X.shape[0], X.dtype
+    shape, dtype, index = X.shape, X.dtype, torch._C._cuda_getDevice() if X.is_cuda else -2
+    T, width = shape
     dt = _dtype(X)
-    index = torch._C._cuda_getDevice() if X.is_cuda else -2
-    shape = (T, (cfg["n_heads"] + 2 * cfg["n_kv_heads"]) * cfg["d"])
-    x, y = _rows(X, name, shape, index, dtype), _rows(Y, yname, shape, index, dtype)
+    want = (cfg["n_heads"] + 2 * cfg["n_kv_heads"]) * cfg["d"]
+    try:
+        x, xstep = X.stride()
+        y, ystep = Y.stride()
+        fine = (xstep == 1 and ystep == 1 and T > 1 and width == want and Y.dtype is dtype and Y.shape == shape
+                and X.get_device() == index and Y.get_device() == index)
+    except (AttributeError, ValueError, TypeError):
+        fine = False
+    if fine:
+        xp, yp = X.data_ptr(), Y.data_ptr()
+    else:
+        shape = (T, want)
+        xp, x = _rows(X, name, shape, index, dtype)
+        yp, y = _rows(Y, yname, shape, index, dtype)
     st = None if seq_starts is None else _vec(seq_starts, "seq_starts", torch.int64, (cfg["b"] + 1,), index)
     po = None if positions is None else _vec(positions, "positions", torch.int64, (T,), index)
-    return dt, _rotary_sizes(cfg, T), _rotary_cfg(rot), st, po, x, y, shape, index
+    return dt, _rotary_sizes(cfg, T), _rotary_cfg(rot), st, po, xp, x, yp, y, shape, index
 
 
 def _rotary_sizes(cfg: dict, T: int) -> bytes:
@@ -758,14 +771,14 @@ def tp_rotary_fwd(QKV, cfg, rot, Out, seq_starts=None, positions=None, stream=No
     tensor of T values, else rows count from 0 in their sequence.  seq_starts: int64 CUDA tensor of b + 1 row numbers;
     rows outside every sequence are left as they are.  Matrices may be column slices of wider buffers.  Every tensor
     lies on the current device."""
-    dt, c, r, st, po, x, y, _, dev = _rotary_common(QKV, "QKV", Out, "Out", cfg, rot, seq_starts, positions)
-    _check(lib().tp_rotary_fwd(dt, c, r, st, po, x[0], x[1], y[0], y[1], _attn_stream(stream, dev)), "tp_rotary_fwd")
+    dt, c, r, st, po, xp, x, yp, y, _, dev = _rotary_common(QKV, "QKV", Out, "Out", cfg, rot, seq_starts, positions)
+    _check(lib().tp_rotary_fwd(dt, c, r, st, po, xp, x, yp, y, _attn_stream(stream, dev)), "tp_rotary_fwd")
 
 
 def tp_rotary_bwd(dOut, cfg, rot, dQKV, seq_starts=None, positions=None, stream=None):
     """dQKV <- gradient of tp_rotary_fwd given its output's; dQKV may be dOut itself."""
-    dt, c, r, st, po, x, y, _, dev = _rotary_common(dOut, "dOut", dQKV, "dQKV", cfg, rot, seq_starts, positions)
-    _check(lib().tp_rotary_bwd(dt, c, r, st, po, x[0], x[1], y[0], y[1], _attn_stream(stream, dev)), "tp_rotary_bwd")
+    dt, c, r, st, po, xp, x, yp, y, _, dev = _rotary_common(dOut, "dOut", dQKV, "dQKV", cfg, rot, seq_starts, positions)
+    _check(lib().tp_rotary_bwd(dt, c, r, st, po, xp, x, yp, y, _attn_stream(stream, dev)), "tp_rotary_bwd")
 
 
 def tp_qk_norm_rotary_workspace_size(cfg: dict, T: int) -> int:
@@ -782,10 +795,10 @@ def tp_qk_norm_rotary_fwd(QKV, cfg, norm, rot, gq, gk, Out, seq_starts=None, pos
 
     norm: dict with kind (rms or layer) and eps.  rot: as for tp_rotary_fwd, or None: norms alone.  The other
     arguments as for tp_rotary_fwd."""
-    dt, c, r, st, po, x, y, _, dev = _rotary_common(QKV, "QKV", Out, "Out", cfg, rot, seq_starts, positions)
+    dt, c, r, st, po, xp, x, yp, y, _, dev = _rotary_common(QKV, "QKV", Out, "Out", cfg, rot, seq_starts, positions)
     d = cfg["d"]
     _check(lib().tp_qk_norm_rotary_fwd(dt, c, _norm_cfg(norm), r, _gain(gq, "gq", d, dev), _gain(gk, "gk", d, dev), st,
-                                       po, x[0], x[1], y[0], y[1], _attn_stream(stream, dev)),
+                                       po, xp, x, yp, y, _attn_stream(stream, dev)),
            "tp_qk_norm_rotary_fwd")
 
 
@@ -795,10 +808,11 @@ def tp_qk_norm_rotary_bwd(QKV, cfg, norm, rot, gq, gk, dOut, dQKV, dgq, dgk, wor
     added to).  dQKV may be dOut itself.
 
     workspace: a CUDA tensor of tp_qk_norm_rotary_workspace_size bytes, or None without dgq and dgk."""
-    dt, c, r, st, po, x, y, shape, dev = _rotary_common(QKV, "QKV", dQKV, "dQKV", cfg, rot, seq_starts, positions)
+    dt, c, r, st, po, xp, x, yp, y, shape, dev = _rotary_common(QKV, "QKV", dQKV, "dQKV", cfg, rot, seq_starts,
+                                                                positions)
     do, ws, d = _rows(dOut, "dOut", shape, dev, QKV.dtype), _scratch(workspace, dev), cfg["d"]
     _check(lib().tp_qk_norm_rotary_bwd(dt, c, _norm_cfg(norm), r, _gain(gq, "gq", d, dev), _gain(gk, "gk", d, dev), st,
-                                       po, x[0], x[1], do[0], do[1], y[0], y[1], _gain(dgq, "dgq", d, dev),
+                                       po, xp, x, do[0], do[1], yp, y, _gain(dgq, "dgq", d, dev),
                                        _gain(dgk, "dgk", d, dev), 1 if accumulate else 0, ws[0], ws[1],
                                        _attn_stream(stream, dev)),
            "tp_qk_norm_rotary_bwd")

@@ -14,9 +14,9 @@
 //
 // Angles without 64-bit floating point: f_k / 2 pi, the turns a position, comes
 // as a 64-bit fraction of a turn; its product with the position modulo 2^64 is
-// exact and drops the whole turns by itself, and its upper 32 bits are the
-// angle for sincospif.  A position costs one integer product a pair, and far
-// ones lose nothing to the range reduction.
+// exact and drops the whole turns by itself; its upper 32 bits are the angle.  A
+// position costs one integer product a pair, and far ones lose nothing to the
+// range reduction.
 //
 // One kernel form streams all of it: each value is read once and written once.
 // A group of G lanes holds one head, 16 values a lane: 8 pairs of partners, so
@@ -101,8 +101,8 @@ struct Words {
 template <class E, int V>
 __device__ __forceinline__ void load_vec(const E* p, uint32_t* w) {
   constexpr int N = Words<E, V>::N;
-  if constexpr (V == 1) {
-    if constexpr (sizeof(E) == 2) w[0] = *reinterpret_cast<const uint16_t*>(p);
+  if constexpr (N == 1) {
+    if constexpr (V * sizeof(E) == 2) w[0] = *reinterpret_cast<const uint16_t*>(p);
     else w[0] = *reinterpret_cast<const uint32_t*>(p);
   } else if constexpr (N == 2) {
     const uint2 q = *reinterpret_cast<const uint2*>(p);
@@ -123,8 +123,8 @@ __device__ __forceinline__ void load_vec(const E* p, uint32_t* w) {
 template <class E, int V>
 __device__ __forceinline__ void store_words(E* p, const uint32_t* w) {
   constexpr int N = Words<E, V>::N;
-  if constexpr (V == 1) {
-    if constexpr (sizeof(E) == 2) *reinterpret_cast<uint16_t*>(p) = static_cast<uint16_t>(w[0]);
+  if constexpr (N == 1) {
+    if constexpr (V * sizeof(E) == 2) *reinterpret_cast<uint16_t*>(p) = static_cast<uint16_t>(w[0]);
     else *reinterpret_cast<uint32_t*>(p) = w[0];
   } else if constexpr (N == 2) {
     *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
@@ -287,10 +287,26 @@ __device__ __forceinline__ int place(const RoParams& p, int k) {
   }
 }
 
-// Angle of a position in half turns, in [-1, 1).
-__device__ __forceinline__ float half_turns(int64_t position, uint64_t turn) {
-  const uint64_t turns = static_cast<uint64_t>(position) * turn;
-  return static_cast<float>(static_cast<int32_t>((turns + (uint64_t{1} << 31)) >> 32)) * 0x1p-31f;
+// Cosine and sine of the angle of a position, whose turns are a whole number of
+// 2^-32nds.  The nearest quarter turn is taken off in whole numbers, which leaves
+// x in [-pi/4, pi/4]; there Taylor's series to x^9 and x^8 leave out less than
+// 2.6e-8, below half a step of 1.
+__device__ __forceinline__ void cos_sin(int64_t position, uint64_t turn, float* c, float* s) {
+  const uint32_t u = static_cast<uint32_t>((static_cast<uint64_t>(position) * turn) >> 32);
+  const uint32_t quarter = (u + (1u << 29)) >> 30;
+  const float x = static_cast<float>(static_cast<int32_t>(u << 2)) * 3.6572951981e-10f;  // pi / 2 2^-32
+  const float y = x * x;
+  float p = fmaf(y, 2.7557319224e-6f, -1.9841269841e-4f);  // 1 / 9!, -1 / 7!
+  p = fmaf(y, p, 8.3333333333e-3f);
+  p = fmaf(y, p, -1.6666666667e-1f);
+  p = fmaf(x * y, p, x);
+  float q = fmaf(y, 2.4801587302e-5f, -1.3888888889e-3f);  // 1 / 8!, -1 / 6!
+  q = fmaf(y, q, 4.1666666667e-2f);
+  q = fmaf(y, q, -0.5f);
+  q = fmaf(y, q, 1.f);
+  const bool odd = quarter & 1;
+  *s = __uint_as_float(__float_as_uint(odd ? q : p) ^ (quarter & 2) << 30);
+  *c = __uint_as_float(__float_as_uint(odd ? p : q) ^ ((quarter + 1) & 2) << 30);
 }
 
 // The table of a tile's n rows.  A thread keeps its pair and goes from row to row.
@@ -302,7 +318,7 @@ __device__ __forceinline__ void fill_table(const RoParams& p, int n, const int64
     float* to = tab + place<V, INTER>(p, k);
     for (int r = r0; r < n; r += p.fill_rows) {
       float c, s;
-      sincospif(half_turns(pos[r], t), &s, &c);
+      cos_sin(pos[r], t, &c, &s);
       float* row = to + r * p.row_floats;
       c *= p.amp;
       s *= p.amp_sin;
@@ -317,6 +333,9 @@ template <int N>
 __device__ __forceinline__ void read_table(const float* from, float* f) {
   if constexpr (N == 1) {
     f[0] = from[0];
+  } else if constexpr (N == 2) {
+    const float2 a = *reinterpret_cast<const float2*>(from);
+    f[0] = a.x; f[1] = a.y;
   } else {
 #pragma unroll
     for (int i = 0; i < N; i += 4) {
@@ -326,13 +345,13 @@ __device__ __forceinline__ void read_table(const float* from, float* f) {
   }
 }
 
-// One thread's copy of 8 or 16 bytes into shared memory, not waited for.
+// One thread's copy of 4, 8 or 16 bytes into shared memory, not waited for.
 template <int BYTES>
 __device__ __forceinline__ void copy_async(uint32_t to, const void* from) {
   if constexpr (BYTES == 16)
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
   else
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(to), "l"(from) : "memory");
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(to), "l"(from), "n"(BYTES) : "memory");
 }
 __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int LEFT>
@@ -358,7 +377,7 @@ struct Lane {
   bool ha[S], hb[S];  // and whether the head has them
   int turned[2 * S];  // rotated pairs of the slot (half layout), of the vector (interleaved)
   int first;          // the lane's number; slot i is number first + i G
-  // The lane's units of 8 or 16 bytes in a stage: those of one number lie side
+  // The lane's units of 4, 8 or 16 bytes in a stage: those of one number lie side
   // by side, lane after lane (no two lanes of a warp on one bank).  Single
   // elements (V = 1) lie as in the row.
   static constexpr int U = V * sizeof(E) < 16 ? V * sizeof(E) : 16;
@@ -400,7 +419,7 @@ struct Lane {
         const int v = u * U / (V * static_cast<int>(sizeof(E)));
         if (v % 2 ? hb[v / 2] : ha[v / 2]) continue;
 #pragma unroll
-        for (int k = 0; k < U; k += 8) *reinterpret_cast<uint64_t*>(stage + at0 + u * apart + k) = 0;
+        for (int k = 0; k < U; k += 4) *reinterpret_cast<uint32_t*>(stage + at0 + u * apart + k) = 0u;
       }
     }
   }
@@ -439,9 +458,11 @@ struct Lane {
         if constexpr (U == 16) {
           const uint4 q = *reinterpret_cast<const uint4*>(from);
           w[4 * u] = q.x; w[4 * u + 1] = q.y; w[4 * u + 2] = q.z; w[4 * u + 3] = q.w;
-        } else {
+        } else if constexpr (U == 8) {
           const uint2 q = *reinterpret_cast<const uint2*>(from);
           w[2 * u] = q.x; w[2 * u + 1] = q.y;
+        } else {
+          w[u] = *reinterpret_cast<const uint32_t*>(from);
         }
       }
     }
@@ -989,11 +1010,13 @@ cudaError_t launch_call(void* call) {
   RoCall* c = static_cast<RoCall*>(call);
   if (c->f32) {
     if (c->inter) return launch_as<float, 4, true>(c);
-    return c->vec == 4 ? launch_as<float, 4, false>(c) : launch_as<float, 1, false>(c);
+    if (c->vec == 4) return launch_as<float, 4, false>(c);
+    return c->vec == 2 ? launch_as<float, 2, false>(c) : launch_as<float, 1, false>(c);
   }
   if (c->inter) return launch_as<__nv_bfloat16, 8, true>(c);
   if (c->vec == 8) return launch_as<__nv_bfloat16, 8, false>(c);
-  return c->vec == 4 ? launch_as<__nv_bfloat16, 4, false>(c) : launch_as<__nv_bfloat16, 1, false>(c);
+  if (c->vec == 4) return launch_as<__nv_bfloat16, 4, false>(c);
+  return c->vec == 2 ? launch_as<__nv_bfloat16, 2, false>(c) : launch_as<__nv_bfloat16, 1, false>(c);
 }
 
 // Once a device, at the first call with it current.
@@ -1005,13 +1028,12 @@ cudaError_t set_up() {
   if (e != cudaSuccess || dev < 0 || dev >= 64) return e != cudaSuccess ? e : cudaErrorInvalidDevice;
   std::lock_guard<std::mutex> lk(mu);
   if (done[dev]) return cudaSuccess;
-  if ((e = launch_as<float, 4, true>(nullptr)) != cudaSuccess || (e = launch_as<float, 4, false>(nullptr)) != cudaSuccess ||
-      (e = launch_as<float, 1, false>(nullptr)) != cudaSuccess ||
-      (e = launch_as<__nv_bfloat16, 8, true>(nullptr)) != cudaSuccess ||
-      (e = launch_as<__nv_bfloat16, 8, false>(nullptr)) != cudaSuccess ||
-      (e = launch_as<__nv_bfloat16, 4, false>(nullptr)) != cudaSuccess ||
-      (e = launch_as<__nv_bfloat16, 1, false>(nullptr)) != cudaSuccess)
-    return e;
+  constexpr cudaError_t (*kAll[])(RoCall*) = {
+      launch_as<float, 4, true>,          launch_as<float, 4, false>,         launch_as<float, 2, false>,
+      launch_as<float, 1, false>,         launch_as<__nv_bfloat16, 8, true>,  launch_as<__nv_bfloat16, 8, false>,
+      launch_as<__nv_bfloat16, 4, false>, launch_as<__nv_bfloat16, 2, false>, launch_as<__nv_bfloat16, 1, false>};
+  for (auto kernels : kAll)
+    if ((e = kernels(nullptr)) != cudaSuccess) return e;
   done[dev] = true;
   return cudaSuccess;
 }
@@ -1067,9 +1089,10 @@ tp_status ro_sizes(const tp_attn_config* cfg, const tp_rotary_config* rot, bool 
   p.amp_sin = p.amp;
   c->inter = n_rot > 0 && rot->interleaved != 0;
   // Vectors of 16 bytes.  Partners in the half layout lie n_rot / 2 apart: the
-  // widest that keep both ends of a pair aligned.
+  // widest that keep both ends of a pair aligned (8192 rows of 16 + 16 heads of 64
+  // with n_rot = 20, rotation: 28 us by twos, 39 by single elements).
   const int widest = f32 ? 4 : 8;
-  c->vec = c->inter || p.pairs % widest == 0 ? widest : p.pairs % 4 == 0 ? 4 : 1;
+  c->vec = c->inter || p.pairs % widest == 0 ? widest : p.pairs % 4 == 0 ? 4 : p.pairs % 2 == 0 ? 2 : 1;
   const int v = c->vec;
   int lanes;
   if (c->inter) {
