@@ -733,15 +733,15 @@ def _rotary_common(X, name, Y, yname, cfg, rot, seq_starts, positions):
         raise ValueError(f"{name} must be a 2D tensor")
     shape, dtype, index = X.shape, X.dtype, torch._C._cuda_getDevice() if X.is_cuda else -2
     T, width = shape
-    dt = _dtype(X)
     want = (cfg["n_heads"] + 2 * cfg["n_kv_heads"]) * cfg["d"]
     try:
         x, xstep = X.stride()
         y, ystep = Y.stride()
-        fine = (xstep == 1 and ystep == 1 and T > 1 and width == want and Y.dtype is dtype and Y.shape == shape
-                and X.get_device() == index and Y.get_device() == index)
+        fine = (xstep == 1 == ystep and T > 1 and width == want and Y.dtype is dtype and Y.shape == shape
+                and X.get_device() == index == Y.get_device())
     except (AttributeError, ValueError, TypeError):
         fine = False
+    dt = _dtype(X)
     if fine:
         xp, yp = X.data_ptr(), Y.data_ptr()
     else:

@@ -33,6 +33,7 @@
 #include <string.h>
 
 #include <algorithm>
+#include <atomic>
 #include <mutex>
 
 #include "tp_device.cuh"
@@ -49,6 +50,7 @@ constexpr int kRoThreads = 256;    // of a block
 constexpr int kRoFew = 160;        // of a smaller one
 constexpr int kRoRows = 64;        // most rows of a tile
 constexpr int kRoTable = 16384;    // bytes that its table should not exceed
+constexpr int kRoCluster = 8;      // blocks of a cluster
 constexpr int kRoParts = 1024;     // most blocks of the backward with gains
 constexpr int64_t kRoCached = 112 << 20;  // bytes of a call that the L2 (129 MB) holds for the next one
 
@@ -66,6 +68,7 @@ struct RoParams {
   float* partial;            // (blocks, 2, d) sums of the gains' gradients, or null
   float *dgq, *dgk;          // the gains' gradients
   int accumulate;
+  int cluster;               // blocks of the launch, a cluster that adds its sums by itself; 0: each block leaves its own
   int64_t T;
   int b, s;        // s: tokens of every sequence (no starts, no positions)
   int d, hq, hk;   // head width; query and key heads a shard
@@ -614,6 +617,19 @@ __device__ __forceinline__ void add_gain(float* dgq, float* dgk, int d, int c, f
   *to = accumulate ? *to + t : t;
 }
 
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// The value at the same shared-memory address of the cluster's block `rank`.
+__device__ __forceinline__ float read_cluster(const float* at, int rank) {
+  float v;
+  asm volatile("{.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %1, %2;\n\tld.shared::cluster.f32 %0, [a];}"
+               : "=f"(v)
+               : "r"(static_cast<uint32_t>(__cvta_generic_to_shared(at))), "r"(rank)
+               : "memory");
+  return v;
+}
+
 // Head of a group of the chunk.
 __device__ __forceinline__ int block_head(const RoParams& p, int chunk, int slot) {
   const int log_unit = 5 - p.log_g, in_unit = slot & ((1 << log_unit) - 1);
@@ -871,12 +887,20 @@ __global__ void __launch_bounds__(NT, kBlocks<MODE, NT>)
     }
     __syncthreads();
     const int warps = blockDim.x >> 5;
-    float* sums = p.partial + static_cast<size_t>(blockIdx.x) * 2 * d;
+    float* sums = p.cluster ? red + warps * 2 * d : p.partial + static_cast<size_t>(blockIdx.x) * 2 * d;
     for (int c = threadIdx.x; c < 2 * d; c += blockDim.x) {
       float t = 0.f;
       for (int w = 0; w < warps; ++w) t += red[static_cast<size_t>(w) * 2 * d + c];
       sums[c] = t;
     }
+    if (p.cluster == 0) return;
+    cluster_sync();
+    for (int c = blockIdx.x * blockDim.x + threadIdx.x; c < 2 * d; c += p.cluster * blockDim.x) {
+      float t = 0.f;
+      for (int k = 0; k < p.cluster; ++k) t += read_cluster(sums + c, k);
+      add_gain(p.dgq, p.dgk, d, c, t, p.accumulate);
+    }
+    cluster_sync();  // the others have read this block's
   }
 }
 
@@ -945,6 +969,26 @@ int lay_out(RoParams* p, int max_parts) {
   return threads;
 }
 
+// launch_k, the grid one cluster.
+cudaError_t launch_cluster(void (*kernel)(RoParams), unsigned grid, int threads, size_t smem, cudaStream_t st,
+                           const RoParams& p) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = pdl_on() ? 1 : 0;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = grid;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+
 template <class E, int V, bool INTER, int MODE, int NT>
 cudaError_t launch_block(RoCall& c, int threads, int max_rows) {
   constexpr int D = kDepth<E, MODE>;
@@ -963,12 +1007,20 @@ cudaError_t launch_block(RoCall& c, int threads, int max_rows) {
   int64_t blocks = wave;
   if (!kBwd && bytes > kRoCached) blocks *= (rows + 8 * wave - 1) / (8 * wave);
   blocks = std::min(blocks, rows);
+  // Up to 32 steps of the backward run as one cluster, which adds the gains' gradients by itself: one launch on the host
+  // instead of two, fewer blocks on the GPU (96 rows of 8 + 8 heads of 64: 11.1 us a call instead of 13.4, 6.8 us on the
+  // GPU instead of 5.6).
+  if (kBwd && p.partial && p.chunks <= kRoCluster && rows * p.chunks <= 4 * kRoCluster) {
+    blocks = std::min<int64_t>(rows, kRoCluster / p.chunks);
+    p.cluster = static_cast<int>(blocks * p.chunks);
+  }
   p.apart = static_cast<uint32_t>(blocks * p.parts);
   const unsigned grid = static_cast<unsigned>(blocks * p.chunks);
   size_t smem = (kStageX<E, NT> + (kBwd ? kStageY<E, NT> : 0)) * D + ((p.pairs + 1) & ~1) * 8 +
                 static_cast<size_t>(2) * p.steps * p.parts * p.row_floats * 4;
-  if (kBwd) smem = std::max(smem, static_cast<size_t>(threads / 32) * 8 * p.d);
+  if (kBwd) smem = std::max(smem, static_cast<size_t>(threads / 32 + 1) * 8 * p.d);
   count_launches(1);
+  if (p.cluster) return launch_cluster(rotary_kernel<E, V, INTER, MODE, NT>, grid, threads, smem, c.stream, p);
   const cudaError_t e = launch_k(rotary_kernel<E, V, INTER, MODE, NT>, grid, threads, smem, c.stream, p);
   if (e != cudaSuccess || !kBwd || p.partial == nullptr) return e;
   count_launches(1);
@@ -1022,19 +1074,20 @@ cudaError_t launch_call(void* call) {
 // Once a device, at the first call with it current.
 cudaError_t set_up() {
   static std::mutex mu;
-  static bool done[64];
+  static std::atomic<bool> done[64];
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess || dev < 0 || dev >= 64) return e != cudaSuccess ? e : cudaErrorInvalidDevice;
+  if (done[dev].load(std::memory_order_acquire)) return cudaSuccess;
   std::lock_guard<std::mutex> lk(mu);
-  if (done[dev]) return cudaSuccess;
+  if (done[dev].load(std::memory_order_relaxed)) return cudaSuccess;
   constexpr cudaError_t (*kAll[])(RoCall*) = {
       launch_as<float, 4, true>,          launch_as<float, 4, false>,         launch_as<float, 2, false>,
       launch_as<float, 1, false>,         launch_as<__nv_bfloat16, 8, true>,  launch_as<__nv_bfloat16, 8, false>,
       launch_as<__nv_bfloat16, 4, false>, launch_as<__nv_bfloat16, 2, false>, launch_as<__nv_bfloat16, 1, false>};
   for (auto kernels : kAll)
     if ((e = kernels(nullptr)) != cudaSuccess) return e;
-  done[dev] = true;
+  done[dev].store(true, std::memory_order_release);
   return cudaSuccess;
 }
 
@@ -1045,8 +1098,9 @@ inline bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintp
 
 // Turns a position as a 64-bit fraction.
 uint64_t turn_fraction(double freq) {
-  const double turns = fmod(freq * 0.15915494309189533577, 1.0);  // 1 / 2 pi
-  return static_cast<uint64_t>(turns * 0x1p64);                   // 0 <= turns < 1
+  double turns = freq * 0.15915494309189533577;  // 1 / 2 pi
+  if (turns >= 1.0) turns -= floor(turns);       // exact
+  return static_cast<uint64_t>(turns * 0x1p64);  // 0 <= turns < 1
 }
 
 // Sizes and the rotation into c, without pointers.
