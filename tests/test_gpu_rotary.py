@@ -9,7 +9,7 @@ Bounds, element by element, from the arithmetic; u = 2^-24 is half a step of fp3
     (the last term: freq / 2 pi in a double);
   * a sum of squares adds 16 terms a lane and at most 5 levels of lanes: 21 u of itself, half of that after the root,
     rsqrtf 4 u, the mean and eps 2 u: r is off by e_r = 17 u of itself; a mean is off by 22 u of the mean magnitude;
-  * the backward's sums over d likewise by 22 u of their magnitudes; the gains' gradients are sums of at most 300 terms in a
+  * the backward's sums over d likewise by 22 u of their magnitudes; the gains' gradients are sums of at most 310 terms in a
     row, then of at most 64: 400 u of the magnitudes;
   * results are rounded once: 2^-8 (bf16), 2^-24 (fp32) of the value.
 """
@@ -237,6 +237,15 @@ def test_many_sequences():
     Case(lens, 1, 1, 8, 1, norm="rms", head=5, tail=5, seed=5).check()
 
 
+@pytest.mark.parametrize("b", [1, 2, 30, 31, 32, 33, 1023, 1024, 1025])
+def test_numbers_of_sequences(b):
+    """Around what a warp holds at once, and what it finds in one, two and three steps."""
+    rng = np.random.default_rng(b)
+    lens = [int(x) for x in rng.integers(0, 9, b)]
+    lens[-1] += 1
+    Case(lens, 2, 2, 16, 2, norm="rms", head=3, tail=2, packed=True, seed=20).check()
+
+
 @pytest.mark.parametrize("T", [1, 2, 31, 500])
 @pytest.mark.parametrize("norm", NORMS)
 def test_given_positions(T, norm):
@@ -303,9 +312,10 @@ def test_in_place(norm, dtype):
 
 
 @pytest.mark.parametrize("norm", NORMS)
-def test_slices_of_wider_buffers(norm):
-    """Row pitches of their own; what lies between the rows stays."""
-    c = Case([30, 11], 4, 2, 40, 2, norm=norm, tail=1, seed=10)
+@pytest.mark.parametrize("dtype,u,n_rot", [("bf16", 8, 40), ("f32", 4, 40), ("bf16", 8, 22)])
+def test_slices_of_wider_buffers(dtype, u, n_rot, norm):
+    """Row pitches of their own, multiples of 16 bytes (u elements); what lies between the rows stays."""
+    c = Case([30, 11], 4, 2, 40, 2, n_rot, norm=norm, dtype=dtype, tail=1, seed=10)
     Y, (dX, dg) = c.fwd(), c.bwd()
     T, W = c.X.shape
 
@@ -314,14 +324,14 @@ def test_slices_of_wider_buffers(norm):
         big[:, left:left + W] = t
         return big, big[:, left:left + W]
 
-    _, X = wide(c.X.cuda(), 8, 24)
-    _, D = wide(c.dY.cuda(), 16, 0)
-    bigY, Y2 = wide(torch.full_like(Y, 7.0), 8, 40)
-    bigG, dX2 = wide(torch.full_like(dX, 7.0), 0, 8)
+    _, X = wide(c.X.cuda(), u, 3 * u)
+    _, D = wide(c.dY.cuda(), 2 * u, 0)
+    bigY, Y2 = wide(torch.full_like(Y, 7.0), u, 5 * u)
+    bigG, dX2 = wide(torch.full_like(dX, 7.0), 0, u)
     c.fwd(X, Y2)
     _, dg2 = c.bwd(X, D, dX2)
     assert torch.equal(Y, Y2) and torch.equal(dX, dX2)
-    assert (bigY[:, :8] == 5).all() and (bigY[:, 8 + W:] == 5).all() and (bigG[:, W:] == 5).all()
+    assert (bigY[:, :u] == 5).all() and (bigY[:, u + W:] == 5).all() and (bigG[:, W:] == 5).all()
     if norm:
         assert all(torch.equal(a, b) for a, b in zip(dg, dg2))
 
@@ -431,6 +441,24 @@ def test_many_rows():
     """More tiles than blocks in the backward, and rows that do not fill the last tile."""
     Case([40003], 1, 1, 16, 1, norm="rms", seed=16).check()
     Case([30001, 20000], 1, 1, 8, 1, 6, norm="layer", dtype="f32", tail=13, seed=17).check()
+    Case([1500000], 1, 1, 8, 1, norm="rms", seed=21).check()
+    Case([700001, 3], 2, 1, 8, 1, 4, True, tail=1, seed=22).check()
+
+
+def test_amplitude_and_frequencies_at_their_ends():
+    """An amplitude of 0 counts as 1; frequencies of 0, of whole turns and beyond a turn a position."""
+    import math
+    tp = _tp()
+    c = Case([40], 2, 1, 16, 1, amp=1.0, seed=23)
+    Y = c.fwd()
+    c.rot["amplitude"] = 0.0
+    assert torch.equal(c.fwd(), Y)
+    c.rot = dict(c.rot, amplitude=None)
+    assert torch.equal(c.fwd(), Y)
+    c.rot = dict(c.rot, amplitude=0.25, freq=torch.tensor([0.0, 6.5, 2 * math.pi, 100.0, 1e-300, 1048576.0, 1e-5, math.pi],
+                                                          dtype=torch.float64))
+    c.check()
+    assert tp.tp_get_status() == tp.TP_OK
 
 
 def test_rows_far_apart():
