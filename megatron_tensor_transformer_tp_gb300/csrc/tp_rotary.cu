@@ -1310,6 +1310,10 @@ extern "C" tp_status tp_qk_norm_rotary_bwd(tp_dtype dt, const tp_attn_config* cf
                                dQKV, ld_dqkv, &c);
   if (st != TP_OK) return st;
   if (!aligned(gq, 4) || !aligned(gk, 4) || !aligned(dgq, 4) || !aligned(dgk, 4)) return TP_ERR_ALIGN;
+  // (null gradients and null gains are equal, and allowed)
+  for (const float* g : {dgq, dgk})
+    if (g != nullptr && (g == gq || g == gk)) return TP_ERR_INVALID;
+  if (dgq != nullptr && dgq == dgk) return TP_ERR_INVALID;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (cfg->T == 0) {
     // no rows: the gains' gradients are zero
@@ -1319,10 +1323,6 @@ extern "C" tp_status tp_qk_norm_rotary_bwd(tp_dtype dt, const tp_attn_config* cf
     return TP_OK;
   }
   if (dgq != nullptr || dgk != nullptr) {
-    // (null gradients and null gains are equal, and allowed)
-    for (const float* g : {dgq, dgk})
-      if (g != nullptr && (g == gq || g == gk)) return TP_ERR_INVALID;
-    if (dgq == dgk) return TP_ERR_INVALID;
     if (workspace == nullptr || ws_bytes < gain_bytes(cfg->d)) return TP_ERR_WORKSPACE;
     if (!aligned(workspace, 256)) return TP_ERR_ALIGN;
     c.p.partial = static_cast<float*>(workspace);
