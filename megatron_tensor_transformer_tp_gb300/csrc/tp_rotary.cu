@@ -1103,15 +1103,19 @@ uint64_t turn_fraction(double freq) {
   return static_cast<uint64_t>(turns * 0x1p64);  // 0 <= turns < 1
 }
 
+// Numbers of rows and heads, and the head width but for its multiple.
+bool head_sizes(const tp_attn_config* cfg) {
+  return cfg->T >= 0 && cfg->T <= INT32_MAX - 511 && cfg->n_heads >= 1 && cfg->n_kv_heads >= 1 && cfg->N >= 1 &&
+         cfg->N <= 8 && cfg->n_heads % cfg->N == 0 && cfg->n_kv_heads % cfg->N == 0 &&
+         cfg->n_heads % cfg->n_kv_heads == 0 && cfg->d >= 1 && cfg->d <= kRoMaxD &&
+         cfg->n_heads <= kRoMaxHeads - cfg->n_kv_heads;
+}
+
 // Sizes and the rotation into c, without pointers.
 tp_status ro_sizes(const tp_attn_config* cfg, const tp_rotary_config* rot, bool norm, const int64_t* seq_starts,
                    const int64_t* positions, bool f32, RoCall* c) {
   if (cfg == nullptr || (rot == nullptr && !norm)) return TP_ERR_INVALID;
-  if (cfg->T < 0 || cfg->T > INT32_MAX - 511 || cfg->n_heads < 1 || cfg->n_kv_heads < 1 || cfg->N < 1 || cfg->N > 8 ||
-      cfg->n_heads % cfg->N != 0 || cfg->n_kv_heads % cfg->N != 0 || cfg->n_heads % cfg->n_kv_heads != 0 ||
-      cfg->d < 1 || cfg->d > kRoMaxD)
-    return TP_ERR_INVALID;
-  if (cfg->n_heads > kRoMaxHeads - cfg->n_kv_heads) return TP_ERR_INVALID;
+  if (!head_sizes(cfg)) return TP_ERR_INVALID;
   if (cfg->T > 0) {
     if (seq_starts != nullptr) {
       if (cfg->b < 1 || cfg->b > (1 << 22)) return TP_ERR_INVALID;
@@ -1337,6 +1341,6 @@ extern "C" tp_status tp_qk_norm_rotary_bwd(tp_dtype dt, const tp_attn_config* cf
 }
 
 extern "C" size_t tp_qk_norm_rotary_workspace_size(const tp_attn_config* cfg) {
-  if (cfg == nullptr || cfg->T < 1 || cfg->d < 8 || cfg->d > kRoMaxD || cfg->d % 8 != 0) return 0;
+  if (cfg == nullptr || !head_sizes(cfg) || cfg->T == 0 || cfg->d % 8 != 0) return 0;
   return gain_bytes(cfg->d);
 }
