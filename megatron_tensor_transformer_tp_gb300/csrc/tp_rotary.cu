@@ -50,6 +50,7 @@ constexpr int kRoThreads = 256;    // of a block
 constexpr int kRoFew = 160;        // of a smaller one
 constexpr int kRoRows = 64;        // most rows of a tile
 constexpr int kRoTable = 16384;    // bytes that its table should not exceed
+constexpr int kRoShared = 228 << 10;  // shared memory of an SM; a block takes 1 KB besides its own
 constexpr int kRoCluster = 8;      // blocks of a cluster
 constexpr int kRoParts = 1024;     // most blocks of the backward with gains
 constexpr int64_t kRoCached = 112 << 20;  // bytes of a call that the L2 (129 MB) holds for the next one
@@ -656,9 +657,10 @@ template <class E, int NT>
 constexpr uint32_t kStageY = NT * 16 * sizeof(E);
 template <class E, int NT>
 constexpr uint32_t kStageX = kStageY<E, NT> + NT * 8 * sizeof(E);
-// Blocks on an SM, by their registers: 128 a thread, or 96 for the smaller blocks' forward.  More blocks with fewer
-// registers were slower (norm's forward, 3 blocks of 256 threads: two sequences of 2048, 32 heads of 128, interleaved,
-// 38 us instead of 32; 5 blocks of 160: 12000 rows of 16 + 4 heads of 96 30 instead of 26).
+// Most blocks on an SM, by their registers: 128 a thread, or 96 for the smaller blocks' forward.  (Stages and table may
+// leave room for fewer.)  More blocks with fewer registers were slower (norm's forward, 3 blocks of 256 threads: two
+// sequences of 2048, 32 heads of 128, interleaved, 38 us instead of 32; 5 blocks of 160: 12000 rows of 16 + 4 heads of 96
+// 30 instead of 26).
 template <int MODE, int NT>
 constexpr int kBlocks = NT != kRoFew ? 2 : MODE == RO_NORM_BWD ? 3 : 4;
 
@@ -1005,13 +1007,20 @@ cudaError_t launch_block(RoCall& c, int threads, int max_rows) {
   RoParams& p = c.p;
   p.steps = std::max(1, std::min(8, max_rows / p.parts) / D) * D;
   p.fill_rows = std::max(1, threads / std::max(1, p.pairs));
+  size_t smem = (kStageX<E, NT> + (kBwd ? kStageY<E, NT> : 0)) * D + ((p.pairs + 1) & ~1) * 8 +
+                static_cast<size_t>(2) * p.steps * p.parts * p.row_floats * 4;
+  if (kBwd) smem = std::max(smem, static_cast<size_t>(threads / 32 + 1) * 8 * p.d);
+  // Blocks that an SM holds at once: rows are dealt out evenly, so blocks beyond those would be a nearly empty second
+  // wave.  (By the registers' limit alone / so: 16384 rows of 8 + 2 heads of 128, rotation 20.4 / 18.8 us, norm's forward
+  // 24.0 / 20.4; 8192 in fp32, norm's backward 31.5 / 27.1.)
+  const int fit = std::min(kBlocks<MODE, NT>, static_cast<int>(kRoShared / (smem + sizeof(int64_t[2][kRoRows]) + 1024)));
   const int64_t rows = (p.T + p.parts - 1) / p.parts;  // steps of all blocks of a chunk
   // Waves of blocks.  Where HBM bounds the call, several: the next kernel's blocks find room while the last ones end,
   // and set-up hides behind the others' copies.  In the L2's reach set-up counts: one.  (us by waves 1 / 2 / 3 / 5:
   // two sequences of 2048, 32 heads of 128, norm's forward: 35.4 33.9 32.6 34.4; 12000 rows of 16 + 4 heads of 96,
   // 110 MB: 22.0 23.9 25.8 30.3; 12000 rows of 32 + 8 heads of 128, rotation: 51.3 49.3 48.7 47.6.)  The backward: one,
   // as every block leaves sums of the gains' gradients (two: 48.7 -> 52.7).
-  const int64_t wave = std::max(1, std::min(kBlocks<MODE, NT> * c.num_sms, kRoParts) / p.chunks);
+  const int64_t wave = std::max(1, std::min(fit * c.num_sms, kRoParts) / p.chunks);
   const int64_t bytes = 2 * p.T * (static_cast<int64_t>(p.items) * p.d + p.copied) * static_cast<int64_t>(sizeof(E));
   int64_t blocks = wave;
   if (!kBwd && bytes > kRoCached) blocks *= (rows + 8 * wave - 1) / (8 * wave);
@@ -1025,9 +1034,6 @@ cudaError_t launch_block(RoCall& c, int threads, int max_rows) {
   }
   p.apart = static_cast<uint32_t>(blocks * p.parts);
   const unsigned grid = static_cast<unsigned>(blocks * p.chunks);
-  size_t smem = (kStageX<E, NT> + (kBwd ? kStageY<E, NT> : 0)) * D + ((p.pairs + 1) & ~1) * 8 +
-                static_cast<size_t>(2) * p.steps * p.parts * p.row_floats * 4;
-  if (kBwd) smem = std::max(smem, static_cast<size_t>(threads / 32 + 1) * 8 * p.d);
   count_launches(1);
   if (p.cluster) return launch_cluster(rotary_kernel<E, V, INTER, MODE, NT>, grid, threads, smem, c.stream, p);
   const cudaError_t e = launch_k(rotary_kernel<E, V, INTER, MODE, NT>, grid, threads, smem, c.stream, p);

@@ -4,7 +4,7 @@ import pytest
 import torch
 
 import synthetic_inputs as SI
-from tests.test_gpu_rotary import Case, _tp
+from tests.test_gpu_rotary import NORMS, Case, _tp
 
 pytestmark = pytest.mark.gpu
 
@@ -50,3 +50,15 @@ def test_gains_written_by_the_call_before(lens, d, norm):
         got = chain(False)
         assert all(torch.equal(a, b) for a, b in zip(got, want))
     assert tp.tp_get_status() == tp.TP_OK
+
+
+# ----------------------------------------------------------------------------
+# blocks whose number an SM's shared memory limits, not their registers
+# ----------------------------------------------------------------------------
+@pytest.mark.parametrize("norm", NORMS)
+@pytest.mark.parametrize("lens,H,KV,d,inter,dtype", [([9000, 77], 8, 2, 128, False, "bf16"), ([6000], 8, 2, 128, False, "f32"),
+                                                     ([5000], 8, 2, 64, False, "f32"), ([4845], 1, 1, 512, True, "bf16"),
+                                                     ([6007], 1, 1, 128, True, "f32")])
+def test_fewer_blocks_an_sm(lens, H, KV, d, inter, dtype, norm):
+    """Wide tables and stages of fp32: fewer blocks on an SM than their registers allow, many steps a block."""
+    Case(lens, H, KV, d, 1, None, inter, norm=norm, dtype=dtype, seed=62).check()
