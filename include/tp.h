@@ -441,8 +441,10 @@ TP_API tp_status tp_rotary_frequencies(const tp_rotary_scaling* scaling, double*
  *               every sequence are not written; or NULL: every row is used, and
  *               without positions the sequences are b of s rows each (with
  *               positions b and s are unused)
- * freq / 2 pi is kept to 2^-53 of itself; times the position it loses its whole turns
- * exactly, is cut to 2^-32 of a turn, and its cosine and sine are good to 2^-23.
+ * freq / 2 pi, the turns a position, is kept to 2^-52 of itself plus 2^-64 of a turn.
+ * Times the position it loses its whole turns exactly and is cut to 2^-32 of a turn, so
+ * the angle is off by |position| times that error and the cut at most; the angle's
+ * cosine and sine are good to 2^-23.
  * Results are rounded once to the dtype.
  * Deterministic, no workspace.
  * Errors, before anything is launched: TP_ERR_INVALID for sizes outside the

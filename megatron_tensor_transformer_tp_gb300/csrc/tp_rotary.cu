@@ -15,8 +15,9 @@
 // Angles without 64-bit floating point: f_k / 2 pi, the turns a position, comes
 // as a 64-bit fraction of a turn; its product with the position modulo 2^64 is
 // exact and drops the whole turns by itself; its upper 32 bits are the angle.  A
-// position costs one integer product a pair, and far ones lose nothing to the
-// range reduction.
+// position costs one integer product a pair, and the range reduction loses
+// nothing at far ones: the fraction's own error, 2^-52 of itself and 2^-64 of a
+// turn, times the position is all there is.
 //
 // One kernel form streams all of it: each value is read once and written once.
 // A group of G lanes holds one head, 16 values a lane: 8 pairs of partners, so
@@ -1111,7 +1112,8 @@ cudaError_t set_up() {
 // ---------------------------------------------------------------------------
 inline bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
-// Turns a position as a 64-bit fraction.
+// Turns a position as a 64-bit fraction.  The constant and the product are rounded, 2^-52 of the turns together; what
+// is behind the fraction's 64 bits is cut off.
 uint64_t turn_fraction(double freq) {
   double turns = freq * 0.15915494309189533577;  // 1 / 2 pi
   if (turns >= 1.0) turns -= floor(turns);       // exact

@@ -1,5 +1,9 @@
 """More of the rotation of queries and keys and of their norms: what the call just before has written, positions and
 frequencies at their ends."""
+import math
+import random
+from fractions import Fraction
+
 import pytest
 import torch
 
@@ -62,3 +66,57 @@ def test_gains_written_by_the_call_before(lens, d, norm):
 def test_fewer_blocks_an_sm(lens, H, KV, d, inter, dtype, norm):
     """Wide tables and stages of fp32: fewer blocks on an SM than their registers allow, many steps a block."""
     Case(lens, H, KV, d, 1, None, inter, norm=norm, dtype=dtype, seed=62).check()
+
+
+# ----------------------------------------------------------------------------
+# angles
+# ----------------------------------------------------------------------------
+def _pi():
+    """pi to 2^-400: 16 arctan(1/5) - 4 arctan(1/239) (Machin) in whole numbers."""
+    one = 1 << 420
+
+    def arctan(n):
+        total, power, k = 0, one // n, 0
+        while power:
+            total += (-1) ** k * (power // (2 * k + 1))
+            power //= n * n
+            k += 1
+        return total
+
+    return Fraction(16 * arctan(5) - 4 * arctan(239), one)
+
+
+@pytest.mark.parametrize("inter", [False, True])
+def test_angles_within_their_bound(inter):
+    """Frequencies of 2^-70 to 2^20 radians and positions to the ends of int64.  A pair (1, 0) becomes the cosine and the
+    sine of its angle, which the header bounds: freq / 2 pi is off by 2^-52 of itself and 2^-64 of a turn, the position
+    multiplies that, 2^-32 of a turn is cut off, and cosine and sine are good to 2^-23.  Against the angle in whole
+    numbers; pairs that may be off by a radian and more are only finite."""
+    tp = _tp()
+    rng = random.Random(7)
+    two_pi = 2 * _pi()
+    freq = [0.0, 2.0 ** 20, math.pi, 2.0 ** -70] + [2.0 ** rng.uniform(-70, 20) for _ in range(252)]
+    pos = [0, 1, -1, (1 << 63) - 1, -(1 << 63)] + [rng.choice((-1, 1)) * int(2 ** rng.uniform(0, 62)) for _ in range(59)]
+    T, n = len(pos), 2 * len(freq)
+    first = slice(0, n, 2) if inter else slice(0, n // 2)
+    second = slice(1, n, 2) if inter else slice(n // 2, n)
+    X = torch.zeros(T, 3 * n)
+    X[:, first] = 1
+    Y = torch.empty(T, 3 * n, device="cuda")
+    tp.tp_rotary_fwd(X.cuda(), dict(n_heads=1, n_kv_heads=1, d=n, N=1),
+                     dict(n_rot=n, interleaved=inter, freq=torch.tensor(freq, dtype=torch.float64)), Y,
+                     positions=torch.tensor(pos).cuda())
+    Y = Y.double().cpu()
+    assert torch.isfinite(Y).all()
+    compared = 0
+    for t, at in enumerate(pos):
+        c, s = Y[t, :n][first].tolist(), Y[t, :n][second].tolist()
+        for k, f in enumerate(freq):
+            turns = at * Fraction(f) / two_pi
+            allowed = 2 * math.pi * (abs(at) * (f / (2 * math.pi) * 2.0 ** -52 + 2.0 ** -64) + 2.0 ** -32) + 2.0 ** -23
+            if allowed >= 1:
+                continue
+            compared += 1
+            a = float(turns % 1 * two_pi)  # (fp64 adds less than 2^-50)
+            assert abs(c[k] - math.cos(a)) <= allowed and abs(s[k] - math.sin(a)) <= allowed, (at, f)
+    assert compared > T * len(freq) // 2
