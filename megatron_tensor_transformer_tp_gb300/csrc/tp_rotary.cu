@@ -54,7 +54,7 @@ constexpr int kRoTable = 16384;    // bytes that its table should not exceed
 constexpr int kRoShared = 228 << 10;  // shared memory of an SM; a block takes 1 KB besides its own
 constexpr int kRoCluster = 8;      // blocks of a cluster
 constexpr int kRoParts = 1024;     // most blocks of the backward with gains
-constexpr int64_t kRoCached = 112 << 20;  // bytes of a call that the L2 (129 MB) holds for the next one
+constexpr int64_t kRoOneWave = 112 << 20;  // most bytes of a forward call that runs in one wave of blocks
 
 enum RoMode : int { RO_ROTATE = 0, RO_NORM_FWD = 1, RO_NORM_BWD = 2 };
 
@@ -1016,19 +1016,22 @@ cudaError_t launch_block(RoCall& c, int threads, int max_rows) {
   // 24.0 / 20.4; 8192 in fp32, norm's backward 31.5 / 27.1.)
   const int fit = std::min(kBlocks<MODE, NT>, static_cast<int>(kRoShared / (smem + sizeof(int64_t[2][kRoRows]) + 1024)));
   const int64_t rows = (p.T + p.parts - 1) / p.parts;  // steps of all blocks of a chunk
-  // Waves of blocks.  Where HBM bounds the call, several: the next kernel's blocks find room while the last ones end,
-  // and set-up hides behind the others' copies.  In the L2's reach set-up counts: one.  (us by waves 1 / 2 / 3 / 5:
-  // two sequences of 2048, 32 heads of 128, norm's forward: 35.4 33.9 32.6 34.4; 12000 rows of 16 + 4 heads of 96,
-  // 110 MB: 22.0 23.9 25.8 30.3; 12000 rows of 32 + 8 heads of 128, rotation: 51.3 49.3 48.7 47.6.)  The backward: one,
-  // as every block leaves sums of the gains' gradients (two: 48.7 -> 52.7).
+  // Waves of blocks of the forward.  Several where the call is long: the next kernel's blocks find room while the last
+  // ones end, and set-up hides behind the others' copies; one where set-up counts.  The size at which that changes
+  // differs with the heads, so the limit is a compromise.  us by waves 1 / 2 / 3 / 5, calls on three sets of buffers:
+  //   norm's forward, 16 + 4 heads of 96, 101 MB 20.0 21.2 21.8 25.2, 118 MB 22.6 23.6 24.2 27.6 (the rule takes 3),
+  //     221 MB 38.8 40.6 40.4 41.3 (5); 32 + 32 heads of 128, 201 MB 33.9 32.1 31.9 32.5 (4: 32.0)
+  //   rotation, 8 + 2 heads of 128, 61 MB 11.9 11.2 12.0 14.7 (1), 101 MB 18.7 17.7 17.2 19.2 (1), 123 MB 22.0 21.0 20.4 21.8
+  //     (3), 403 MB 68.5 65.3 62.7 62.1 (18: 60.9); 32 + 8 heads of 128, 295 MB 49.9 47.2 45.0 44.3 (5)
+  // The backward: one, as every block leaves sums of the gains' gradients (two: 48.7 -> 52.7).
   const int64_t wave = std::max(1, std::min(fit * c.num_sms, kRoParts) / p.chunks);
   const int64_t bytes = 2 * p.T * (static_cast<int64_t>(p.items) * p.d + p.copied) * static_cast<int64_t>(sizeof(E));
   int64_t blocks = wave;
-  if (!kBwd && bytes > kRoCached) blocks *= (rows + 8 * wave - 1) / (8 * wave);
+  if (!kBwd && bytes > kRoOneWave) blocks *= (rows + 8 * wave - 1) / (8 * wave);
   blocks = std::min(blocks, rows);
   // Up to 32 steps of the backward run as one cluster, which adds the gains' gradients by itself: one launch on the host
-  // instead of two, fewer blocks on the GPU (96 rows of 8 + 8 heads of 64: 11.1 us a call instead of 13.4, 6.8 us on the
-  // GPU instead of 5.6).
+  // instead of two, but fewer blocks on the GPU.  (96 rows of 8 + 8 heads of 64, 24 steps: 11.1 us a call instead of 13.4;
+  // 6.8 us on the GPU instead of 5.6, which is what a replayed graph pays.)
   if (kBwd && p.partial && p.chunks <= kRoCluster && rows * p.chunks <= 4 * kRoCluster) {
     blocks = std::min<int64_t>(rows, kRoCluster / p.chunks);
     p.cluster = static_cast<int>(blocks * p.chunks);
